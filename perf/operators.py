@@ -278,9 +278,10 @@ def _ce(s):
     return r
 
 
-# 8-bit moments.  A block of 256 values has a scale 2^(e-127), e the largest
-# exponent field in it (253 at most).  A magnitude y < 2, relative to it, is a
-# float with four bits of fraction: m has a sign and three bits of exponent
+# 8-bit moments.  A block of 256 values has a scale 2^(e-127), e the exponent
+# field of its largest magnitude plus one code step (253 at most), so that the
+# largest too can round up.  A magnitude y < 31/16, relative to it, is a float
+# with four bits of fraction: m has a sign and three bits of exponent
 # (least normal 2^-6), sqrt(v) has four (least normal 2^-14); below the least
 # normal the codes are evenly spaced.  Rounding is stochastic, its 16 random
 # bits hashed from the seed, the step and the value's place in the list.
@@ -321,7 +322,7 @@ def _power(e):
 
 
 def _block_scale(x):
-    return (_blocks(x).view(torch.int32).max(1).values >> 23).clamp(max=253)
+    return ((_blocks(x).view(torch.int32).max(1).values + (1 << 19)) >> 23).clamp(max=253)
 
 
 def _adamw_one(f, a, n, decay, h, bits):
@@ -473,7 +474,7 @@ def _stored64(x, rnd, deep, most, floor=False):
     """What x >= 0 is stored as: the next code below, or above with the chance of its distance, in blocks of 256."""
     b = x.view(-1, 256)
     top = b.max(1, keepdim=True).values
-    unit = torch.exp2(torch.floor(torch.log2(top.clamp(min=2.0 ** -126))))
+    unit = torch.exp2(torch.floor(torch.log2(top.clamp(min=2.0 ** -126) * (32 / 31))))
     y = b / unit
     gap = torch.exp2(torch.floor(torch.log2(y.clamp(min=2.0 ** -deep)))) / 16
     y = (torch.floor(y / gap + rnd.view(-1, 256)) * gap).clamp(max=most)
