@@ -518,6 +518,146 @@ zero_status_t zero_pa_partition(const zero_pa_plan_t* plan, const void* const* r
 zero_status_t zero_pa_gather(const zero_pa_plan_t* plan, const void* const* shards, void* const* dst, int32_t n_dst,
                              void* stream);
 
+/* ---- layer norm -----------------------------------------------------------
+ * The norm in front of a transformer block or the vocabulary projection, and
+ * its gradient, on rows of `dim` values:
+ *   y  = (x - mean) * rstd * weight + bias,  rstd = 1/sqrt(var + eps)
+ *   dx = rstd * (g - avg(g) - xhat * avg(g * xhat)),  g = dy * weight,
+ *        xhat = (x - mean) * rstd,  avg over the row
+ *   dweight = sum over rows of dy * xhat,  dbias = sum over rows of dy
+ * Every sum is a binary32 sum in an order fixed by the plan; each output is
+ * rounded once to its type.  All of x, weight, bias, y, dy, dx, dweight,
+ * dbias have the plan's dtype; mean and rstd are binary32, one per row.
+ * Rows may lie further apart than dim (strides, in values); what is between
+ * them is neither read nor written.  Pointers need the alignment of their
+ * type only: rows that start on 16-byte boundaries take 16-byte accesses,
+ * others single-value ones.  72 bytes. */
+typedef struct zero_ln_plan {
+    int64_t rows, dim;
+    int64_t x_stride;            /* values between rows of x and dx */
+    int64_t y_stride;            /* values between rows of y and dy */
+    int64_t workspace_bytes;     /* zero_ln_backward's workspace */
+    int64_t hbm_bytes_forward;   /* algorithmic HBM bytes (each array access once) */
+    int64_t hbm_bytes_backward;
+    int32_t dtype;               /* zero_dtype_t */
+    int32_t blocks;              /* backward: row groups summed apart */
+    int64_t reserved;
+} zero_ln_plan_t;
+
+/* Host only.  strides 0: dim.  rows >= 0, 1 <= dim <= 2^20, strides >= dim.
+ * Errors: ZERO_EINVAL, ZERO_EUNSUPPORTED (rows or dim too large). */
+zero_status_t zero_ln_plan(int64_t rows, int64_t dim, int32_t dtype, int64_t x_stride, int64_t y_stride,
+                           zero_ln_plan_t* out);
+/* weight NULL: ones; bias NULL: zeros; mean, rstd NULL: not written.
+ * Asynchronous on `stream`.  Errors: ZERO_EINVAL (plan not made by
+ * zero_ln_plan, eps < 0 or NaN), ZERO_ENOMEM (x or y NULL), ZERO_EALIGN,
+ * ZERO_ECUDA. */
+zero_status_t zero_ln_forward(const zero_ln_plan_t* plan, const void* x, const void* weight, const void* bias,
+                              float eps, void* y, float* mean, float* rstd, void* stream);
+/* mean and rstd as the forward pass wrote them.  dx, dweight, dbias NULL:
+ * not computed; dx must not overlap dy or x.  dweight and dbias are
+ * overwritten, with zeros when there are no rows.  workspace:
+ * plan->workspace_bytes, 16-byte aligned (may be NULL when neither dweight
+ * nor dbias is wanted). */
+zero_status_t zero_ln_backward(const zero_ln_plan_t* plan, const void* dy, const void* x, const void* weight,
+                               const float* mean, const float* rstd, void* dx, void* dweight, void* dbias,
+                               void* workspace, void* stream);
+
+/* ---- AdamW over a list of tensors -------------------------------------------
+ * One optimizer step of every tensor of a list in one kernel launch, for
+ * parameters that are not laid out as one flat partitioned vector (a head or
+ * an adapter beside the sharded model).  Adam as in the sharded step
+ * (Kingma & Ba, Algorithm 1) with decoupled weight decay (Loshchilov &
+ * Hutter, "Decoupled Weight Decay Regularization"), g = grad * grad_scale:
+ *   w = w * (1 - lr * weight_decay)
+ *   m = b1*m + (1-b1)*g;  v = b2*v + (1-b2)*(g*g)
+ *   w = w - lr * (m/bc1) / (sqrt(v/bc2) + eps),  bc = 1 - b^t
+ * state_bits 32: m, v binary32, one IEEE rounding per operation in the
+ * sharded step's order (weight_decay 0 gives its results bit for bit, where
+ * the bias corrections agree).
+ * state_bits 8: m and r = sqrt(v) are kept in one byte per value, in blocks
+ * of 256 values of a tensor with one scale byte each:
+ *   scale byte e: the block's values are stored relative to 2^(e-127), e the
+ *     exponent field of the largest one plus 2^-4 of its binade (at most 253;
+ *     0: the block is zero), so relative magnitudes lie below 31/16, the
+ *     largest code, and the largest too can be rounded up;
+ *   m: sign bit 7, exponent E = bits 6..4, fraction f = bits 3..0: (16+f)/16 *
+ *     2^(E-7), or f/16 * 2^-6 when E = 0;
+ *   r: exponent E = bits 7..4, fraction f: (16+f)/16 * 2^(E-15), or f/16 *
+ *     2^-14 when E = 0.
+ *   A value is rounded down or up to a code at random, up with the chance of
+ *   its distance from the lower one (an EMA with b2 = 0.999 moves by 0.1 % a
+ *   step, far below a code's spacing, and rounding to nearest would hold it
+ *   still.)  A nonzero r is never stored as 0, so no later step divides by
+ *   eps alone.  The 16 random bits of value i (its place in the plan's flat
+ *   order) come from i, t and seed alone: h = (lo32(i/2) * 0x9E3779B1 +
+ *   (i/2 >> 32) * 0x6A09E667 + seed + t * 0x510E527F), h = (h ^ h>>15) *
+ *   0xBB67AE85, h = (h ^ h>>15) * 0xA54FF53B, h ^= h>>16 (all mod 2^32); even
+ *   i takes the low half, odd i the high half.
+ *   The update uses m and r before they are rounded:
+ *     r = sqrt(b2*(r*r) + (1-b2)*(g*g));
+ *     w = w - (m * (lr/bc1)) / (r * (1/sqrt(bc2)) + eps)
+ * master is the binary32 weight; param (may be NULL) receives its cast to
+ * the plan's dtype, the type of grad.  Non-finite gradients poison the
+ * values they meet: see zero_adamw_check.  72 bytes. */
+typedef struct zero_adamw_tensor {
+    const void* grad;
+    void* param;                 /* NULL: not written */
+    float* master;
+    void* m;                     /* float, or one byte per value */
+    void* v;
+    uint8_t* m_scale;            /* 8-bit states: ceil(numel / 256) bytes (else NULL) */
+    uint8_t* v_scale;
+    int64_t numel;               /* >= 0 */
+    float weight_decay;
+    int32_t reserved;            /* 0 */
+} zero_adamw_tensor_t;
+
+/* 64 bytes. */
+typedef struct zero_adamw_plan {
+    int64_t n_tensors;
+    int64_t numel;               /* values in all tensors */
+    int64_t flat_elems;          /* the flat order: tensor after tensor, each from a multiple of 256 */
+    int64_t n_chunks;
+    int64_t table_bytes;         /* device memory of the list */
+    int64_t hbm_bytes;           /* algorithmic HBM bytes of one step */
+    int32_t dtype, state_bits;   /* zero_dtype_t; 8 or 32 */
+    int64_t reserved;
+} zero_adamw_plan_t;
+
+/* Hyper-parameters of one step.  32 bytes. */
+typedef struct zero_adamw {
+    int64_t t;                   /* the step's number, from 1 */
+    float lr, beta1, beta2, eps;
+    float grad_scale;            /* multiplies every gradient: 1/(S*N) */
+    uint32_t seed;               /* 8-bit states: of the random rounding */
+} zero_adamw_t;
+
+/* Host only.  Errors: ZERO_EINVAL (bad field), ZERO_EUNSUPPORTED (state_bits
+ * neither 8 nor 32, over 2^20 tensors or 2^40 values). */
+zero_status_t zero_adamw_plan(const zero_adamw_tensor_t* tensors, int64_t n_tensors, int32_t dtype,
+                              int32_t state_bits, zero_adamw_plan_t* out);
+/* Write the list into `table` (plan->table_bytes of device memory, 16-byte
+ * aligned, kept by the caller); synchronises `stream`.  The pointers are
+ * taken as they are now: a list whose gradients move needs its table written
+ * again.  Pointers need the alignment of their type; tensors whose buffers
+ * all start on 16-byte boundaries take 16-byte accesses, others single-value
+ * ones.  Tensors must not overlap.  Errors: ZERO_EINVAL, ZERO_ENOMEM (a NULL
+ * buffer), ZERO_EALIGN, ZERO_ECUDA. */
+zero_status_t zero_adamw_table_init(const zero_adamw_plan_t* plan, const zero_adamw_tensor_t* tensors, void* table,
+                                    void* stream);
+/* *flag = 1 if any gradient is inf or NaN, else 0 (device memory, 4-byte aligned). */
+zero_status_t zero_adamw_check(const zero_adamw_plan_t* plan, const void* table, uint32_t* flag, void* stream);
+/* One step; asynchronous.  skip: NULL, or a device flag -- nothing changes
+ * when it is nonzero. */
+zero_status_t zero_adamw_step(const zero_adamw_plan_t* plan, const void* table, const zero_adamw_t* hp,
+                              const uint32_t* skip, void* stream);
+/* 8-bit states: the stored m and r = sqrt(v) as bfloat16 values, exact, in
+ * the plan's flat order (flat_elems each, 16-byte aligned; the gaps between
+ * tensors are not written): for a checkpoint. */
+zero_status_t zero_adamw_states(const zero_adamw_plan_t* plan, const void* table, void* m, void* root_v,
+                                void* stream);
+
 /* Profiling: for the step calls made afterwards on this thread, record
  * start_event (a cudaEvent_t) on the step's stream right after the workspace
  * clear, before the first kernel, and end_event after the step's last kernel,

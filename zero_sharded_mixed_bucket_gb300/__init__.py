@@ -29,6 +29,9 @@ __all__ = [
     "zero_pa_plan_t", "zero_pa_plan", "zero_pa_partition", "zero_pa_gather",
     "zero_step_begin", "zero_step_bucket", "zero_step_end", "zero_gather_layer", "zero_last_error",
     "zero_step_buckets", "zero_step_buckets_async",
+    "zero_ln_plan_t", "zero_ln_plan", "zero_ln_forward", "zero_ln_backward",
+    "zero_adamw_tensor_t", "zero_adamw_plan_t", "zero_adamw_t", "adamw_tensor", "zero_adamw_plan",
+    "zero_adamw_table_init", "zero_adamw_check", "zero_adamw_step", "zero_adamw_states",
     "zero_version", "zero_set_profile_events", "zero_fetch_schedule", "Fetcher", "DeviceBuffers", "ptr_array",
 ]
 
@@ -82,6 +85,27 @@ class zero_pa_plan_t(ctypes.Structure):
                 ("gather_bytes", c_i64), ("reserved", c_i64 * 2)]
 
 
+class zero_ln_plan_t(ctypes.Structure):
+    _fields_ = [(n, c_i64) for n in ("rows", "dim", "x_stride", "y_stride", "workspace_bytes", "hbm_bytes_forward",
+                                      "hbm_bytes_backward")] + \
+               [("dtype", c_i32), ("blocks", c_i32), ("reserved", c_i64)]
+
+
+class zero_adamw_tensor_t(ctypes.Structure):
+    _fields_ = [(n, c_vp) for n in ("grad", "param", "master", "m", "v", "m_scale", "v_scale")] + \
+               [("numel", c_i64), ("weight_decay", c_f), ("reserved", c_i32)]
+
+
+class zero_adamw_plan_t(ctypes.Structure):
+    _fields_ = [(n, c_i64) for n in ("n_tensors", "numel", "flat_elems", "n_chunks", "table_bytes", "hbm_bytes")] + \
+               [("dtype", c_i32), ("state_bits", c_i32), ("reserved", c_i64)]
+
+
+class zero_adamw_t(ctypes.Structure):
+    _fields_ = [("t", c_i64), ("lr", c_f), ("beta1", c_f), ("beta2", c_f), ("eps", c_f), ("grad_scale", c_f),
+                ("seed", c_u32)]
+
+
 class ZeroError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__("zero status %d: %s" % (status, message))
@@ -129,6 +153,14 @@ def lib():
             "zero_pa_plan": [c_i64, c_i32, c_i32, c_i64, P(zero_pa_plan_t)],
             "zero_pa_partition": [P(zero_pa_plan_t), P(c_vp), P(c_vp), c_vp],
             "zero_pa_gather": [P(zero_pa_plan_t), P(c_vp), P(c_vp), c_i32, c_vp],
+            "zero_ln_plan": [c_i64, c_i64, c_i32, c_i64, c_i64, P(zero_ln_plan_t)],
+            "zero_ln_forward": [P(zero_ln_plan_t), c_vp, c_vp, c_vp, c_f, c_vp, c_vp, c_vp, c_vp],
+            "zero_ln_backward": [P(zero_ln_plan_t)] + [c_vp] * 10,
+            "zero_adamw_plan": [P(zero_adamw_tensor_t), c_i64, c_i32, c_i32, P(zero_adamw_plan_t)],
+            "zero_adamw_table_init": [P(zero_adamw_plan_t), P(zero_adamw_tensor_t), c_vp, c_vp],
+            "zero_adamw_check": [P(zero_adamw_plan_t), c_vp, c_vp, c_vp],
+            "zero_adamw_step": [P(zero_adamw_plan_t), c_vp, P(zero_adamw_t), c_vp, c_vp],
+            "zero_adamw_states": [P(zero_adamw_plan_t), c_vp, c_vp, c_vp, c_vp],
             "zero_step_begin": [cfg, plan, bufs, adam, state, c_vp],
             "zero_step_bucket": [cfg, plan, bufs, adam, state, c_i64, P(c_vp), c_vp],
             "zero_step_end": [cfg, plan, bufs, adam, state, c_vp, res],
@@ -339,6 +371,71 @@ def zero_pa_gather(plan: zero_pa_plan_t, shards, dst, stream=None):
     """All-gather: the checkpoint rebuilt from the slices into every dst."""
     _check(lib().zero_pa_gather(ctypes.byref(plan), _ptr_array([_dptr(x) for x in shards]),
                                 _ptr_array([_dptr(x) for x in dst]), len(dst), _stream(stream)))
+
+
+def _optr(x):
+    """A device pointer that may be absent: None, an int or a tensor."""
+    return None if x is None else _dptr(x)
+
+
+def zero_ln_plan(rows: int, dim: int, dtype: int = ZERO_FP16, x_stride: int = 0, y_stride: int = 0) -> zero_ln_plan_t:
+    """Layer norm of `rows` rows of `dim` values; strides in values between rows (0: dim)."""
+    p = zero_ln_plan_t()
+    _check(lib().zero_ln_plan(rows, dim, dtype, x_stride, y_stride, ctypes.byref(p)))
+    return p
+
+
+def zero_ln_forward(plan: zero_ln_plan_t, x, weight, bias, eps: float, y, mean=None, rstd=None, stream=None):
+    """y = layer norm of x's rows (pointers or tensors; weight, bias, mean, rstd may be None)."""
+    _check(lib().zero_ln_forward(ctypes.byref(plan), _optr(x), _optr(weight), _optr(bias), eps, _optr(y), _optr(mean),
+                                 _optr(rstd), _stream(stream)))
+
+
+def zero_ln_backward(plan: zero_ln_plan_t, dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=None,
+                     workspace=None, stream=None):
+    """Gradients of zero_ln_forward; those passed as None are not computed."""
+    _check(lib().zero_ln_backward(ctypes.byref(plan), _optr(dy), _optr(x), _optr(weight), _optr(mean), _optr(rstd),
+                                  _optr(dx), _optr(dweight), _optr(dbias), _optr(workspace), _stream(stream)))
+
+
+def adamw_tensor(grad, master, m, v, numel: int, param=None, m_scale=None, v_scale=None,
+                 weight_decay: float = 0.0) -> zero_adamw_tensor_t:
+    """One tensor of a zero_adamw list (pointers or tensors, kept alive by the caller)."""
+    return zero_adamw_tensor_t(grad=_optr(grad), param=_optr(param), master=_optr(master), m=_optr(m), v=_optr(v),
+                               m_scale=_optr(m_scale), v_scale=_optr(v_scale), numel=numel, weight_decay=weight_decay)
+
+
+def _tensor_array(tensors):
+    return tensors if isinstance(tensors, ctypes.Array) else (zero_adamw_tensor_t * len(tensors))(*tensors)
+
+
+def zero_adamw_plan(tensors, dtype: int = ZERO_FP16, state_bits: int = 32) -> zero_adamw_plan_t:
+    """Plan of one AdamW step over a list of tensors (adamw_tensor records)."""
+    p = zero_adamw_plan_t()
+    _check(lib().zero_adamw_plan(_tensor_array(tensors), len(tensors), dtype, state_bits, ctypes.byref(p)))
+    return p
+
+
+def zero_adamw_table_init(plan: zero_adamw_plan_t, tensors, table, stream=None):
+    """Write the list into `table` (plan.table_bytes of device memory); synchronises the stream."""
+    if len(tensors) != plan.n_tensors:
+        raise ZeroError(ZERO_EINVAL, "zero_adamw_table_init: %d tensors, the plan has %d" % (len(tensors), plan.n_tensors))
+    _check(lib().zero_adamw_table_init(ctypes.byref(plan), _tensor_array(tensors), _optr(table), _stream(stream)))
+
+
+def zero_adamw_check(plan: zero_adamw_plan_t, table, flag, stream=None):
+    """*flag (a device uint32) = 1 if any gradient of the list is inf or NaN, else 0."""
+    _check(lib().zero_adamw_check(ctypes.byref(plan), _optr(table), _optr(flag), _stream(stream)))
+
+
+def zero_adamw_step(plan: zero_adamw_plan_t, table, hp: zero_adamw_t, skip=None, stream=None):
+    """One AdamW step of the whole list; skip: None, or a device flag that stops it when nonzero."""
+    _check(lib().zero_adamw_step(ctypes.byref(plan), _optr(table), ctypes.byref(hp), _optr(skip), _stream(stream)))
+
+
+def zero_adamw_states(plan: zero_adamw_plan_t, table, m, root_v, stream=None):
+    """The list's 8-bit moments as bfloat16 values: m and sqrt(v), plan.flat_elems each."""
+    _check(lib().zero_adamw_states(ctypes.byref(plan), _optr(table), _optr(m), _optr(root_v), _stream(stream)))
 
 
 def zero_step_begin(cfg, plan, bufs, adam, state, stream=None):

@@ -1,0 +1,519 @@
+// AdamW over a list of tensors: the plan, the list's table in device memory,
+// and the step with binary32 or 8-bit moments.
+#include <cmath>
+#include <cstdio>
+#include <cstring>
+
+#include "dev_common.cuh"
+#include "nvtx_ranges.h"
+
+namespace zg {
+namespace {
+
+constexpr int kQBlock = 256;         // values per scale byte
+constexpr int kChunk = 4096;         // values per block of threads: one tensor's, from a multiple of kChunk
+constexpr int kAdThreads = 128;
+
+// One tensor in the table.
+struct AdRec {
+    zero_adamw_tensor_t t;
+    int64_t start;                   // place in the flat order
+    int64_t first_chunk;
+    int64_t aligned;                 // every buffer starts on a 16-byte boundary
+    int64_t pad;
+};
+static_assert(sizeof(AdRec) == 104, "the plan sizes the table");
+
+struct AdTable {
+    const AdRec* rec;
+    const int32_t* chunk_tensor;
+};
+
+int64_t chunk_map_offset(int64_t n) { return (n * (int64_t)sizeof(AdRec) + 15) / 16 * 16; }
+
+__host__ __device__ inline AdTable table_of(const void* table, int64_t n)
+{
+    const unsigned char* b = static_cast<const unsigned char*>(table);
+    return AdTable{reinterpret_cast<const AdRec*>(b),
+                   reinterpret_cast<const int32_t*>(b + (n * (int64_t)sizeof(AdRec) + 15) / 16 * 16)};
+}
+
+// Step scalars, rounded once to binary32 on the host.
+struct AdHP {
+    AdamHP a;                        // lr, b1, 1-b1, b2, 1-b2, eps, bc1, bc2
+    float gs;
+    float step8;                     // lr / bc1
+    float root8;                     // 1 / sqrt(bc2)
+    uint32_t mix;                    // seed + t * constant
+};
+
+// The 16 random bits of values i and i+1 (i even), low and high half.
+__device__ __forceinline__ uint32_t hash_pair(uint64_t i, uint32_t mix)
+{
+    const uint64_t j = i >> 1;
+    uint32_t h = (uint32_t)j * 0x9E3779B1u + (uint32_t)(j >> 32) * 0x6A09E667u + mix;
+    h = (h ^ (h >> 15)) * 0xBB67AE85u;
+    h = (h ^ (h >> 15)) * 0xA54FF53Bu;
+    return h ^ (h >> 16);
+}
+
+// Codes of a block: magnitudes relative to its scale are binary32 numbers cut
+// to 4 fraction bits, so a code is the top of the number's bit pattern, less
+// the pattern of the least normal (exponent field `least`), plus 16.  Below
+// the least normal, adding it first lines the bits up with the even spacing
+// there.
+template <int LEAST>
+__device__ __forceinline__ float decode8(uint32_t c)
+{
+    const bool low = c < 16u;
+    const float y = __uint_as_float((c + LEAST * 16u - (low ? 0u : 16u)) << 19);
+    return low ? __fsub_rn(y, __uint_as_float((uint32_t)LEAST << 23)) : y;
+}
+
+template <int LEAST, uint32_t MOST>
+__device__ __forceinline__ uint32_t encode8(float y, uint32_t rnd16)
+{
+    const float base = __uint_as_float((uint32_t)LEAST << 23);
+    const bool low = y < base;
+    const uint32_t b = __float_as_uint(low ? __fadd_rn(y, base) : y) + (rnd16 << 3);
+    return min((b >> 19) - LEAST * 16u + (low ? 0u : 16u), MOST);
+}
+
+// A block's scale byte, from the bit pattern of its largest magnitude: the
+// exponent field one code step (1/16 of the binade) above it, so that the
+// largest value too can round up.  Scaled by its own exponent alone, a value
+// within one step of the binade's end could only be cut to the largest code:
+// an average that moves by less than a step would stop there for good.
+__device__ __forceinline__ uint32_t scale_field(uint32_t most) { return min((most + (1u << 19)) >> 23, 253u); }
+
+constexpr int kLeastM = 121, kLeastR = 113;   // 2^-6, 2^-14
+
+__device__ __forceinline__ float pow2_field(uint32_t e) { return __uint_as_float(e << 23); }
+
+template <int V, typename T>
+__device__ __forceinline__ void ld_any(const T* p, int cnt, bool vec, T x[V])
+{
+    static_assert(sizeof(T) * V >= 8, "");
+    if (vec && cnt == V) {
+        if constexpr (sizeof(T) * V == 8) {
+            *reinterpret_cast<uint2*>(x) = __ldcs(reinterpret_cast<const uint2*>(p));
+        } else {
+#pragma unroll
+            for (int k = 0; k < (int)(sizeof(T) * V / 16); k++)
+                reinterpret_cast<uint4*>(x)[k] = __ldcs(reinterpret_cast<const uint4*>(p) + k);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; j++)
+            x[j] = j < cnt ? p[j] : T(0);
+    }
+}
+
+template <int V, typename T>
+__device__ __forceinline__ void st_any(T* p, int cnt, bool vec, const T x[V])
+{
+    if (vec && cnt == V) {
+        if constexpr (sizeof(T) * V == 8) {
+            __stcs(reinterpret_cast<uint2*>(p), *reinterpret_cast<const uint2*>(x));
+        } else {
+#pragma unroll
+            for (int k = 0; k < (int)(sizeof(T) * V / 16); k++)
+                __stcs(reinterpret_cast<uint4*>(p) + k, reinterpret_cast<const uint4*>(x)[k]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; j++)
+            if (j < cnt) p[j] = x[j];
+    }
+}
+
+template <int DT>
+using Bits = typename std::conditional<DT == kF32, uint32_t, uint16_t>::type;
+
+// Binary32 moments: groups of 4 values, one 16-byte access per binary32 array.
+template <int DT>
+__global__ void __launch_bounds__(kAdThreads) k_adamw32(const AdTable tab, const __grid_constant__ AdHP hp,
+                                                        const uint32_t* skip)
+{
+    if (skip && *skip) return;
+    constexpr int V = 4;
+    const AdRec& r = tab.rec[tab.chunk_tensor[blockIdx.x]];
+    const int64_t lo = ((int64_t)blockIdx.x - r.first_chunk) * kChunk;
+    const int64_t hi = min(lo + kChunk, r.t.numel);
+    const bool vec = r.aligned;
+    const float keep = __fmaf_rn(-hp.a.lr, r.t.weight_decay, 1.0f);
+    const Bits<DT>* grad = static_cast<const Bits<DT>*>(r.t.grad);
+    Bits<DT>* param = static_cast<Bits<DT>*>(r.t.param);
+    float* mp = static_cast<float*>(r.t.m);
+    float* vp = static_cast<float*>(r.t.v);
+    for (int64_t i = lo + threadIdx.x * V; i < hi; i += kAdThreads * V) {
+        const int cnt = (int)min((int64_t)V, hi - i);
+        alignas(16) Bits<DT> g[V], p[V];
+        alignas(16) float w[V], m[V], v[V];
+        ld_any<V>(grad + i, cnt, vec, g);
+        ld_any<V>(r.t.master + i, cnt, vec, w);
+        ld_any<V>(mp + i, cnt, vec, m);
+        ld_any<V>(vp + i, cnt, vec, v);
+#pragma unroll
+        for (int j = 0; j < V; j++) {
+            w[j] = __fmul_rn(w[j], keep);
+            adam1(__fmul_rn(to_f32<DT>(g[j]), hp.gs), w[j], m[j], v[j], hp.a);
+            p[j] = (Bits<DT>)from_f32<DT>(w[j]);
+        }
+        st_any<V>(r.t.master + i, cnt, vec, w);
+        st_any<V>(mp + i, cnt, vec, m);
+        st_any<V>(vp + i, cnt, vec, v);
+        if (param) st_any<V>(param + i, cnt, vec, p);
+    }
+}
+
+// 8-bit moments: a warp takes a block of 256 values, 8 per lane, so the
+// block's largest magnitudes are one warp-wide maximum each.
+template <int DT>
+__global__ void __launch_bounds__(kAdThreads) k_adamw8(const AdTable tab, const __grid_constant__ AdHP hp,
+                                                       const uint32_t* skip)
+{
+    if (skip && *skip) return;
+    constexpr int V = 8;
+    const AdRec& r = tab.rec[tab.chunk_tensor[blockIdx.x]];
+    const int64_t lo = ((int64_t)blockIdx.x - r.first_chunk) * kChunk;
+    const int64_t hi = min(lo + kChunk, r.t.numel);
+    const bool vec = r.aligned;
+    const float keep = __fmaf_rn(-hp.a.lr, r.t.weight_decay, 1.0f);
+    const Bits<DT>* grad = static_cast<const Bits<DT>*>(r.t.grad);
+    Bits<DT>* param = static_cast<Bits<DT>*>(r.t.param);
+    uint8_t* mp = static_cast<uint8_t*>(r.t.m);
+    uint8_t* vp = static_cast<uint8_t*>(r.t.v);
+    const int lane = threadIdx.x & 31;
+    for (int64_t b = lo + (threadIdx.x >> 5) * kQBlock; b < hi; b += kAdThreads / 32 * kQBlock) {
+        const int64_t i = b + lane * V;
+        const int cnt = i < hi ? (int)min((int64_t)V, hi - i) : 0;
+        alignas(16) Bits<DT> g[V], p[V];
+        alignas(16) float w[V];
+        alignas(16) uint8_t cm[V], cr[V];
+        ld_any<V>(grad + i, cnt, vec, g);
+        ld_any<V>(r.t.master + i, cnt, vec, w);
+        ld_any<V>(mp + i, cnt, vec, cm);
+        ld_any<V>(vp + i, cnt, vec, cr);
+        const float sm = pow2_field(r.t.m_scale[b / kQBlock]), sr = pow2_field(r.t.v_scale[b / kQBlock]);
+        float m[V], q[V];
+        uint32_t most_m = 0, most_r = 0;
+#pragma unroll
+        for (int j = 0; j < V; j++) {
+            const float gj = __fmul_rn(to_f32<DT>(g[j]), hp.gs);
+            const float a = __fmul_rn(decode8<kLeastM>(cm[j] & 127u), sm);
+            const float m0 = cm[j] > 127u ? -a : a;
+            const float r0 = __fmul_rn(decode8<kLeastR>(cr[j]), sr);
+            m[j] = __fadd_rn(__fmul_rn(m0, hp.a.b1), __fmul_rn(gj, hp.a.omb1));
+            q[j] = __fsqrt_rn(__fadd_rn(__fmul_rn(__fmul_rn(r0, r0), hp.a.b2), __fmul_rn(__fmul_rn(gj, gj), hp.a.omb2)));
+            const float d = __fadd_rn(__fmul_rn(q[j], hp.root8), hp.a.eps);
+            w[j] = __fsub_rn(__fmul_rn(w[j], keep), __fdiv_rn(__fmul_rn(m[j], hp.step8), d));
+            p[j] = (Bits<DT>)from_f32<DT>(w[j]);
+            if (j < cnt) {
+                most_m = max(most_m, __float_as_uint(m[j]) & 0x7fffffffu);
+                most_r = max(most_r, __float_as_uint(q[j]) & 0x7fffffffu);
+            }
+        }
+        const uint32_t em = scale_field(__reduce_max_sync(0xffffffffu, most_m));
+        const uint32_t er = scale_field(__reduce_max_sync(0xffffffffu, most_r));
+        const float im = pow2_field(254u - em), ir = pow2_field(254u - er);
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+            const uint32_t h = hash_pair((uint64_t)(r.start + i + j), hp.mix);
+#pragma unroll
+            for (int k = j; k < j + 2; k++) {
+                const uint32_t rnd = k == j ? h & 0xffffu : h >> 16;
+                const uint32_t c = encode8<kLeastM, 127u>(__fmul_rn(fabsf(m[k]), im), rnd);
+                cm[k] = (uint8_t)(c | (m[k] < 0.0f && c ? 128u : 0u));
+                cr[k] = (uint8_t)max(encode8<kLeastR, 255u>(__fmul_rn(q[k], ir), rnd), q[k] > 0.0f ? 1u : 0u);
+            }
+        }
+        st_any<V>(r.t.master + i, cnt, vec, w);
+        st_any<V>(mp + i, cnt, vec, cm);
+        st_any<V>(vp + i, cnt, vec, cr);
+        if (param) st_any<V>(param + i, cnt, vec, p);
+        if (lane == 0) {
+            r.t.m_scale[b / kQBlock] = (uint8_t)em;
+            r.t.v_scale[b / kQBlock] = (uint8_t)er;
+        }
+    }
+}
+
+// Stored 8-bit moments as bfloat16 values (5 significant bits: exact).
+__global__ void __launch_bounds__(kAdThreads) k_adamw_states(const AdTable tab, uint16_t* m_out, uint16_t* r_out)
+{
+    constexpr int V = 8;
+    const AdRec& r = tab.rec[tab.chunk_tensor[blockIdx.x]];
+    const int64_t lo = ((int64_t)blockIdx.x - r.first_chunk) * kChunk;
+    const int64_t hi = min(lo + kChunk, r.t.numel);
+    const bool vec = r.aligned;
+    for (int64_t i = lo + threadIdx.x * V; i < hi; i += kAdThreads * V) {
+        const int cnt = (int)min((int64_t)V, hi - i);
+        alignas(16) uint8_t cm[V], cr[V];
+        alignas(16) uint16_t m[V], q[V];
+        ld_any<V>(static_cast<const uint8_t*>(r.t.m) + i, cnt, vec, cm);
+        ld_any<V>(static_cast<const uint8_t*>(r.t.v) + i, cnt, vec, cr);
+        const float sm = pow2_field(r.t.m_scale[i / kQBlock]), sr = pow2_field(r.t.v_scale[i / kQBlock]);
+#pragma unroll
+        for (int j = 0; j < V; j++) {
+            const float a = __fmul_rn(decode8<kLeastM>(cm[j] & 127u), sm);
+            m[j] = (uint16_t)from_f32<kBF16>(cm[j] > 127u ? -a : a);
+            q[j] = (uint16_t)from_f32<kBF16>(__fmul_rn(decode8<kLeastR>(cr[j]), sr));
+        }
+        st_any<V>(m_out + r.start + i, cnt, true, m);
+        st_any<V>(r_out + r.start + i, cnt, true, q);
+    }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kAdThreads) k_adamw_check(const AdTable tab, uint32_t* flag)
+{
+    constexpr int V = 8;
+    const AdRec& r = tab.rec[tab.chunk_tensor[blockIdx.x]];
+    const int64_t lo = ((int64_t)blockIdx.x - r.first_chunk) * kChunk;
+    const int64_t hi = min(lo + kChunk, r.t.numel);
+    const Bits<DT>* grad = static_cast<const Bits<DT>*>(r.t.grad);
+    uint32_t bad = 0;
+    for (int64_t i = lo + threadIdx.x * V; i < hi; i += kAdThreads * V) {
+        const int cnt = (int)min((int64_t)V, hi - i);
+        alignas(16) Bits<DT> g[V];
+        ld_any<V>(grad + i, cnt, r.aligned, g);
+#pragma unroll
+        for (int j = 0; j < V; j++)
+            bad |= nonfinite32(__float_as_uint(to_f32<DT>(g[j])));
+    }
+    if (__syncthreads_or((int)bad) && threadIdx.x == 0) *flag = 1u;
+}
+
+// One warp: the tensors' places in the flat order and in the chunk order.
+__global__ void __launch_bounds__(32) k_adamw_places(AdRec* rec, int64_t n)
+{
+    int64_t start = 0, chunk = 0;
+    const int lane = threadIdx.x;
+    for (int64_t k0 = 0; k0 < n; k0 += 32) {
+        const int64_t k = k0 + lane;
+        const int64_t num = k < n ? rec[k].t.numel : 0;
+        const int64_t len = (num + kQBlock - 1) / kQBlock * kQBlock, chunks = (num + kChunk - 1) / kChunk;
+        int64_t ls = len, cs = chunks;               // inclusive sums over the lanes
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t l = __shfl_up_sync(0xffffffffu, ls, o), c = __shfl_up_sync(0xffffffffu, cs, o);
+            if (lane >= o) {
+                ls += l;
+                cs += c;
+            }
+        }
+        if (k < n) {
+            const zero_adamw_tensor_t& t = rec[k].t;
+            const uintptr_t any = (uintptr_t)t.grad | (uintptr_t)t.param | (uintptr_t)t.master | (uintptr_t)t.m |
+                                  (uintptr_t)t.v;
+            rec[k].start = start + ls - len;
+            rec[k].first_chunk = chunk + cs - chunks;
+            rec[k].aligned = (any & 15u) == 0;
+        }
+        start += __shfl_sync(0xffffffffu, ls, 31);
+        chunk += __shfl_sync(0xffffffffu, cs, 31);
+    }
+}
+
+__global__ void k_adamw_chunks(const AdRec* rec, int64_t n, int32_t* chunk_tensor)
+{
+    for (int64_t k = blockIdx.x; k < n; k += gridDim.x) {
+        const int64_t c = (rec[k].t.numel + kChunk - 1) / kChunk;
+        for (int64_t j = threadIdx.x; j < c; j += blockDim.x)
+            chunk_tensor[rec[k].first_chunk + j] = (int32_t)k;
+    }
+}
+
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+zero_status_t cuda_failed(cudaError_t e, const char* what)
+{
+    char msg[200];
+    std::snprintf(msg, sizeof msg, "%s: %s", what, cudaGetErrorString(e));
+    return set_error(ZERO_ECUDA, msg);
+}
+
+zero_status_t check_adamw_plan(const zero_adamw_plan_t* p, const void* table)
+{
+    if (!p) return set_error(ZERO_EINVAL, "AdamW plan is NULL");
+    const int64_t e = p->dtype == ZERO_FP32 ? 4 : 2;
+    if ((p->state_bits != 8 && p->state_bits != 32) ||
+        (p->dtype != ZERO_FP16 && p->dtype != ZERO_BF16 && p->dtype != ZERO_FP32) || p->n_tensors < 0 ||
+        p->n_tensors > (int64_t(1) << 20) || p->numel < 0 || p->n_chunks < 0 || p->n_chunks > INT32_MAX ||
+        p->table_bytes != chunk_map_offset(p->n_tensors) + p->n_chunks * 4 || p->flat_elems < p->numel ||
+        p->flat_elems % kQBlock || p->hbm_bytes != p->numel * (2 * e + (p->state_bits == 32 ? 24 : 12)))
+        return set_error(ZERO_EINVAL, "AdamW plan was not made by zero_adamw_plan");
+    if (p->n_chunks && !table) return set_error(ZERO_ENOMEM, "AdamW table is NULL");
+    if (!aligned_to(table, 16)) return set_error(ZERO_EALIGN, "AdamW table is not 16-byte aligned");
+    return ZERO_OK;
+}
+
+}  // namespace
+}  // namespace zg
+
+using namespace zg;
+
+extern "C" {
+
+zero_status_t zero_adamw_plan(const zero_adamw_tensor_t* tensors, int64_t n_tensors, int32_t dtype,
+                              int32_t state_bits, zero_adamw_plan_t* out)
+{
+    if (!out) return set_error(ZERO_EINVAL, "zero_adamw_plan: out is NULL");
+    if (dtype != ZERO_FP16 && dtype != ZERO_BF16 && dtype != ZERO_FP32)
+        return set_error(ZERO_EINVAL, "zero_adamw_plan: dtype unknown");
+    if (state_bits != 8 && state_bits != 32)
+        return set_error(ZERO_EUNSUPPORTED, "zero_adamw_plan: state_bits must be 8 or 32");
+    if (n_tensors < 0 || (n_tensors && !tensors)) return set_error(ZERO_EINVAL, "zero_adamw_plan: no tensors given");
+    if (n_tensors > (int64_t(1) << 20)) return set_error(ZERO_EUNSUPPORTED, "zero_adamw_plan: over 2^20 tensors");
+    std::memset(out, 0, sizeof *out);
+    int64_t numel = 0, flat = 0, chunks = 0;
+    for (int64_t k = 0; k < n_tensors; k++) {
+        const int64_t n = tensors[k].numel;
+        if (n < 0) return set_error(ZERO_EINVAL, "zero_adamw_plan: a tensor has a negative numel");
+        if (n > (int64_t(1) << 40) || numel + n > (int64_t(1) << 40))
+            return set_error(ZERO_EUNSUPPORTED, "zero_adamw_plan: over 2^40 values");
+        if (!std::isfinite(tensors[k].weight_decay))
+            return set_error(ZERO_EINVAL, "zero_adamw_plan: a weight_decay is not finite");
+        numel += n;
+        flat += (n + kQBlock - 1) / kQBlock * kQBlock;
+        chunks += (n + kChunk - 1) / kChunk;
+    }
+    out->n_tensors = n_tensors;
+    out->numel = numel;
+    out->flat_elems = flat;
+    out->n_chunks = chunks;
+    out->table_bytes = chunk_map_offset(n_tensors) + chunks * 4;
+    out->dtype = dtype;
+    out->state_bits = state_bits;
+    out->hbm_bytes = numel * (2 * (dtype == ZERO_FP32 ? 4 : 2) + (state_bits == 32 ? 24 : 12));
+    return ZERO_OK;
+}
+
+zero_status_t zero_adamw_table_init(const zero_adamw_plan_t* plan, const zero_adamw_tensor_t* tensors, void* table,
+                                    void* stream)
+{
+    NvtxRange range("zero_adamw_table_init");
+    zero_status_t st = check_adamw_plan(plan, table);
+    if (st != ZERO_OK) return st;
+    zero_adamw_plan_t fresh;
+    st = zero_adamw_plan(tensors, plan->n_tensors, plan->dtype, plan->state_bits, &fresh);
+    if (st != ZERO_OK) return st;
+    if (std::memcmp(&fresh, plan, sizeof fresh) != 0)
+        return set_error(ZERO_EINVAL, "zero_adamw_table_init: the plan was made for other tensors");
+    const size_t e = plan->dtype == ZERO_FP32 ? 4 : 2, se = plan->state_bits / 8;
+    for (int64_t k = 0; k < plan->n_tensors; k++) {
+        const zero_adamw_tensor_t& t = tensors[k];
+        if (t.numel == 0) continue;
+        if (!t.grad || !t.master || !t.m || !t.v || (plan->state_bits == 8 && (!t.m_scale || !t.v_scale)))
+            return set_error(ZERO_ENOMEM, "zero_adamw_table_init: a tensor's buffer is NULL");
+        if (!aligned_to(t.grad, e) || !aligned_to(t.param, e) || !aligned_to(t.master, 4) || !aligned_to(t.m, se) ||
+            !aligned_to(t.v, se))
+            return set_error(ZERO_EALIGN, "zero_adamw_table_init: a tensor's buffer is not aligned to its type");
+    }
+    if (plan->n_chunks == 0) return ZERO_OK;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    AdRec* rec = static_cast<AdRec*>(table);
+    // the records' tensor parts, a strided copy; the rest is filled in on the device
+    cudaError_t err = cudaMemcpy2DAsync(rec, sizeof(AdRec), tensors, sizeof(zero_adamw_tensor_t),
+                                        sizeof(zero_adamw_tensor_t), (size_t)plan->n_tensors, cudaMemcpyHostToDevice, s);
+    if (err == cudaSuccess) {
+        k_adamw_places<<<1, 32, 0, s>>>(rec, plan->n_tensors);
+        const unsigned grid = (unsigned)(plan->n_tensors < 1024 ? plan->n_tensors : 1024);
+        k_adamw_chunks<<<grid, 256, 0, s>>>(rec, plan->n_tensors,
+                                            const_cast<int32_t*>(table_of(table, plan->n_tensors).chunk_tensor));
+        err = cudaGetLastError();
+    }
+    if (err == cudaSuccess) err = cudaStreamSynchronize(s);
+    return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_adamw_table_init");
+}
+
+zero_status_t zero_adamw_check(const zero_adamw_plan_t* plan, const void* table, uint32_t* flag, void* stream)
+{
+    NvtxRange range("zero_adamw_check");
+    const zero_status_t st = check_adamw_plan(plan, table);
+    if (st != ZERO_OK) return st;
+    if (!flag) return set_error(ZERO_ENOMEM, "zero_adamw_check: flag is NULL");
+    if (!aligned_to(flag, 4)) return set_error(ZERO_EALIGN, "zero_adamw_check: flag is not 4-byte aligned");
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t err = cudaMemsetAsync(flag, 0, 4, s);
+    if (err == cudaSuccess && plan->n_chunks) {
+        const AdTable tab = table_of(table, plan->n_tensors);
+        const unsigned grid = (unsigned)plan->n_chunks;
+        if (plan->dtype == ZERO_FP32)
+            k_adamw_check<kF32><<<grid, kAdThreads, 0, s>>>(tab, flag);
+        else if (plan->dtype == ZERO_BF16)
+            k_adamw_check<kBF16><<<grid, kAdThreads, 0, s>>>(tab, flag);
+        else
+            k_adamw_check<kF16><<<grid, kAdThreads, 0, s>>>(tab, flag);
+        err = cudaGetLastError();
+    }
+    return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_adamw_check");
+}
+
+zero_status_t zero_adamw_step(const zero_adamw_plan_t* plan, const void* table, const zero_adamw_t* hp,
+                              const uint32_t* skip, void* stream)
+{
+    NvtxRange range("zero_adamw_step");
+    const zero_status_t st = check_adamw_plan(plan, table);
+    if (st != ZERO_OK) return st;
+    if (!hp) return set_error(ZERO_EINVAL, "zero_adamw_step: hyper-parameters are NULL");
+    if (hp->t < 1) return set_error(ZERO_EINVAL, "zero_adamw_step: t must be at least 1");
+    if (!(hp->beta1 >= 0.0f && hp->beta1 < 1.0f) || !(hp->beta2 >= 0.0f && hp->beta2 < 1.0f))
+        return set_error(ZERO_EINVAL, "zero_adamw_step: betas must be in [0, 1)");
+    if (!(hp->eps >= 0.0f) || !std::isfinite(hp->lr) || !std::isfinite(hp->grad_scale))
+        return set_error(ZERO_EINVAL, "zero_adamw_step: eps must be >= 0, lr and grad_scale finite");
+    if (!aligned_to(skip, 4)) return set_error(ZERO_EALIGN, "zero_adamw_step: skip is not 4-byte aligned");
+    if (plan->n_chunks == 0) return ZERO_OK;
+    AdHP h;
+    std::memset(&h, 0, sizeof h);
+    const double bc1 = 1.0 - std::pow((double)hp->beta1, (double)hp->t);
+    const double bc2 = 1.0 - std::pow((double)hp->beta2, (double)hp->t);
+    h.a.lr = hp->lr;
+    h.a.b1 = hp->beta1;
+    h.a.omb1 = 1.0f - hp->beta1;
+    h.a.b2 = hp->beta2;
+    h.a.omb2 = 1.0f - hp->beta2;
+    h.a.eps = hp->eps;
+    h.a.bc1 = (float)bc1;
+    h.a.bc2 = (float)bc2;
+    h.gs = hp->grad_scale;
+    h.step8 = (float)((double)hp->lr / bc1);
+    h.root8 = (float)(1.0 / std::sqrt(bc2));
+    h.mix = hp->seed + (uint32_t)hp->t * 0x510E527Fu;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const AdTable tab = table_of(table, plan->n_tensors);
+    const unsigned grid = (unsigned)plan->n_chunks;
+    const int dt = plan->dtype;
+    if (plan->state_bits == 32) {
+        if (dt == ZERO_FP32) k_adamw32<kF32><<<grid, kAdThreads, 0, s>>>(tab, h, skip);
+        else if (dt == ZERO_BF16) k_adamw32<kBF16><<<grid, kAdThreads, 0, s>>>(tab, h, skip);
+        else k_adamw32<kF16><<<grid, kAdThreads, 0, s>>>(tab, h, skip);
+    } else {
+        if (dt == ZERO_FP32) k_adamw8<kF32><<<grid, kAdThreads, 0, s>>>(tab, h, skip);
+        else if (dt == ZERO_BF16) k_adamw8<kBF16><<<grid, kAdThreads, 0, s>>>(tab, h, skip);
+        else k_adamw8<kF16><<<grid, kAdThreads, 0, s>>>(tab, h, skip);
+    }
+    const cudaError_t err = cudaGetLastError();
+    return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_adamw_step");
+}
+
+zero_status_t zero_adamw_states(const zero_adamw_plan_t* plan, const void* table, void* m, void* root_v, void* stream)
+{
+    NvtxRange range("zero_adamw_states");
+    const zero_status_t st = check_adamw_plan(plan, table);
+    if (st != ZERO_OK) return st;
+    if (plan->state_bits != 8) return set_error(ZERO_EINVAL, "zero_adamw_states: the list's moments are binary32");
+    if (plan->n_chunks == 0) return ZERO_OK;
+    if (!m || !root_v) return set_error(ZERO_ENOMEM, "zero_adamw_states: an output is NULL");
+    if (!aligned_to(m, 16) || !aligned_to(root_v, 16))
+        return set_error(ZERO_EALIGN, "zero_adamw_states: an output is not 16-byte aligned");
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    k_adamw_states<<<(unsigned)plan->n_chunks, kAdThreads, 0, s>>>(table_of(table, plan->n_tensors),
+                                                                   static_cast<uint16_t*>(m),
+                                                                   static_cast<uint16_t*>(root_v));
+    const cudaError_t err = cudaGetLastError();
+    return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_adamw_states");
+}
+
+}  // extern "C"
