@@ -563,6 +563,61 @@ zero_status_t zero_ln_backward(const zero_ln_plan_t* plan, const void* dy, const
                                const float* mean, const float* rstd, void* dx, void* dweight, void* dbias,
                                void* workspace, void* stream);
 
+/* ---- softmax cross entropy over a large vocabulary ---------------------------
+ * The loss of tokens' last hidden states x [tokens, hidden] against a weight
+ * w [vocab, hidden] (a vocabulary projection, or a tied embedding), without
+ * the [tokens, vocab] logits in memory:
+ *   z = x w^T;  lse_i = log sum_v exp z_iv;  loss_i = lse_i - z_i,t(i)
+ *   G_iv = s_i (exp(z_iv - lse_i) - [v = t(i)]);  dx = G w;  dw = G^T x
+ * The forward pass keeps one running maximum and sum per token and strip of
+ * 256 vocabulary entries.  The backward pass computes z again, a piece of the
+ * vocabulary at a time, and holds G of one piece in 16 bits.
+ * x, w, dx and dw have the plan's dtype (ZERO_FP16 or ZERO_BF16; ZERO_FP32 is
+ * ZERO_EUNSUPPORTED); products are accumulated in binary32, softmax
+ * statistics and loss are binary32, dx and dw are rounded once, and G is
+ * rounded once, to the dtype (the operand type of the products that use it),
+ * scaled so that its largest row factor is 1 (binary16: 2^14).
+ * A token whose target is outside 0..vocab-1 (such as -100) has no loss: its
+ * loss is 0 and its row of dx is 0.  Rows may lie further apart than hidden (strides in
+ * values, multiples of 8).  All pointers 16-byte aligned but targets, loss,
+ * lse, total and dloss (alignment of their type).  Results do not depend on
+ * timing: equal calls give equal bits.  96 bytes. */
+typedef struct zero_ce_plan {
+    int64_t tokens, vocab, hidden;
+    int64_t x_stride, w_stride;  /* values between rows of x and dx, of w and dw */
+    int64_t piece;               /* vocabulary entries per piece of the backward pass, a multiple of 256 */
+    int64_t workspace_bytes;
+    int64_t flops_forward;       /* 2 tokens vocab hidden */
+    int64_t flops_backward;      /* 6 tokens vocab hidden: z again, dx, dw */
+    int32_t dtype;
+    int32_t splits;              /* parts of the vocabulary that dx's product sums apart */
+    int64_t reserved[2];
+} zero_ce_plan_t;
+
+/* Host only.  strides 0: hidden (then a multiple of 8); piece 0: chosen so
+ * that G takes about 256 MiB, else rounded up to a multiple of 256.  tokens
+ * >= 0, vocab >= 1, hidden >= 1.  Errors: ZERO_EINVAL, ZERO_EALIGN (a stride
+ * that is not a multiple of 8), ZERO_EUNSUPPORTED. */
+zero_status_t zero_ce_plan(int64_t tokens, int64_t vocab, int64_t hidden, int32_t dtype, int64_t x_stride,
+                           int64_t w_stride, int64_t piece, zero_ce_plan_t* out);
+/* loss, lse: binary32, one per token.  total (may be NULL): {mean loss of the
+ * tokens that have one (0 when none has), their number}.  workspace:
+ * plan->workspace_bytes, contents scratch.  Asynchronous. */
+zero_status_t zero_ce_forward(const zero_ce_plan_t* plan, const void* x, const void* w, const int64_t* targets,
+                              float* loss, float* lse, float* total, void* workspace, void* stream);
+/* lse as the forward pass wrote it.  s_i = dloss[i] * grad_scale, or with
+ * dloss NULL grad_scale / (number of tokens that have a loss): the gradient
+ * of the mean, times grad_scale (the loss scale).  dx, dw NULL: not
+ * computed; they are overwritten otherwise (with zeros where there are no
+ * tokens). */
+zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const void* w, const int64_t* targets,
+                               const float* lse, const float* dloss, float grad_scale, void* dx, void* dw,
+                               void* workspace, void* stream);
+/* Synchronises `stream`; ZERO_ETIMEOUT if a bounded wait inside the last
+ * forward or backward call with this workspace ran out (its outputs are then
+ * NaN or incomplete). */
+zero_status_t zero_ce_status(const zero_ce_plan_t* plan, const void* workspace, void* stream);
+
 /* ---- AdamW over a list of tensors -------------------------------------------
  * One optimizer step of every tensor of a list in one kernel launch, for
  * parameters that are not laid out as one flat partitioned vector (a head or

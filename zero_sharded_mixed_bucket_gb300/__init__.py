@@ -30,6 +30,7 @@ __all__ = [
     "zero_step_begin", "zero_step_bucket", "zero_step_end", "zero_gather_layer", "zero_last_error",
     "zero_step_buckets", "zero_step_buckets_async",
     "zero_ln_plan_t", "zero_ln_plan", "zero_ln_forward", "zero_ln_backward",
+    "zero_ce_plan_t", "zero_ce_plan", "zero_ce_forward", "zero_ce_backward", "zero_ce_status",
     "zero_adamw_tensor_t", "zero_adamw_plan_t", "zero_adamw_t", "adamw_tensor", "zero_adamw_plan",
     "zero_adamw_table_init", "zero_adamw_check", "zero_adamw_step", "zero_adamw_states",
     "zero_version", "zero_set_profile_events", "zero_fetch_schedule", "Fetcher", "DeviceBuffers", "ptr_array",
@@ -89,6 +90,12 @@ class zero_ln_plan_t(ctypes.Structure):
     _fields_ = [(n, c_i64) for n in ("rows", "dim", "x_stride", "y_stride", "workspace_bytes", "hbm_bytes_forward",
                                       "hbm_bytes_backward")] + \
                [("dtype", c_i32), ("blocks", c_i32), ("reserved", c_i64)]
+
+
+class zero_ce_plan_t(ctypes.Structure):
+    _fields_ = [(n, c_i64) for n in ("tokens", "vocab", "hidden", "x_stride", "w_stride", "piece", "workspace_bytes",
+                                      "flops_forward", "flops_backward")] + \
+               [("dtype", c_i32), ("splits", c_i32), ("reserved", c_i64 * 2)]
 
 
 class zero_adamw_tensor_t(ctypes.Structure):
@@ -156,6 +163,10 @@ def lib():
             "zero_ln_plan": [c_i64, c_i64, c_i32, c_i64, c_i64, P(zero_ln_plan_t)],
             "zero_ln_forward": [P(zero_ln_plan_t), c_vp, c_vp, c_vp, c_f, c_vp, c_vp, c_vp, c_vp],
             "zero_ln_backward": [P(zero_ln_plan_t)] + [c_vp] * 10,
+            "zero_ce_plan": [c_i64, c_i64, c_i64, c_i32, c_i64, c_i64, c_i64, P(zero_ce_plan_t)],
+            "zero_ce_forward": [P(zero_ce_plan_t)] + [c_vp] * 8,
+            "zero_ce_backward": [P(zero_ce_plan_t)] + [c_vp] * 5 + [c_f] + [c_vp] * 4,
+            "zero_ce_status": [P(zero_ce_plan_t), c_vp, c_vp],
             "zero_adamw_plan": [P(zero_adamw_tensor_t), c_i64, c_i32, c_i32, P(zero_adamw_plan_t)],
             "zero_adamw_table_init": [P(zero_adamw_plan_t), P(zero_adamw_tensor_t), c_vp, c_vp],
             "zero_adamw_check": [P(zero_adamw_plan_t), c_vp, c_vp, c_vp],
@@ -396,6 +407,32 @@ def zero_ln_backward(plan: zero_ln_plan_t, dy, x, weight, mean, rstd, dx=None, d
     """Gradients of zero_ln_forward; those passed as None are not computed."""
     _check(lib().zero_ln_backward(ctypes.byref(plan), _optr(dy), _optr(x), _optr(weight), _optr(mean), _optr(rstd),
                                   _optr(dx), _optr(dweight), _optr(dbias), _optr(workspace), _stream(stream)))
+
+
+def zero_ce_plan(tokens: int, vocab: int, hidden: int, dtype: int = ZERO_FP16, x_stride: int = 0, w_stride: int = 0,
+                 piece: int = 0) -> zero_ce_plan_t:
+    """Cross entropy of `tokens` hidden states against a [vocab, hidden] weight; strides in values between rows."""
+    p = zero_ce_plan_t()
+    _check(lib().zero_ce_plan(tokens, vocab, hidden, dtype, x_stride, w_stride, piece, ctypes.byref(p)))
+    return p
+
+
+def zero_ce_forward(plan: zero_ce_plan_t, x, w, targets, loss, lse, total, workspace, stream=None):
+    """loss and lse per token; total: None, or {mean, count} (pointers or tensors; targets int64)."""
+    _check(lib().zero_ce_forward(ctypes.byref(plan), _optr(x), _optr(w), _optr(targets), _optr(loss), _optr(lse),
+                                 _optr(total), _optr(workspace), _stream(stream)))
+
+
+def zero_ce_backward(plan: zero_ce_plan_t, x, w, targets, lse, dloss, grad_scale: float, dx, dw, workspace,
+                     stream=None):
+    """dx and dw (None: not computed) of sum(dloss * loss) * grad_scale, or with dloss None of the mean loss."""
+    _check(lib().zero_ce_backward(ctypes.byref(plan), _optr(x), _optr(w), _optr(targets), _optr(lse), _optr(dloss),
+                                  grad_scale, _optr(dx), _optr(dw), _optr(workspace), _stream(stream)))
+
+
+def zero_ce_status(plan: zero_ce_plan_t, workspace, stream=None):
+    """Synchronise; raises ZeroError (ZERO_ETIMEOUT) if a wait inside the last call ran out."""
+    _check(lib().zero_ce_status(ctypes.byref(plan), _optr(workspace), _stream(stream)))
 
 
 def adamw_tensor(grad, master, m, v, numel: int, param=None, m_scale=None, v_scale=None,

@@ -1,0 +1,654 @@
+// Softmax cross entropy over a large vocabulary without stored logits: the
+// plan, the three products (logits with a softmax epilogue, dx, dw) on the
+// tensor cores, and the small kernels around them.
+#include <cmath>
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+
+#include "dev_common.cuh"
+#include "dev_tc.cuh"
+#include "nvtx_ranges.h"
+
+namespace zg {
+namespace {
+
+constexpr int kBM = 128, kBN = 256, kBK = 64;         // tile of one block's product, K-values per stage
+constexpr int kStages = 4;
+constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2;
+constexpr int kCeThreads = 192;                       // producer warp, issuing warp, four epilogue warps
+constexpr int kCeSmem = kStages * (kABytes + kBBytes) + 1024;
+constexpr float kLog2e = 1.4426950408889634f;
+
+enum { kEpiLse, kEpiGrad, kEpiAcc };
+
+// Workspace head.
+struct CeHead {
+    uint32_t err;                // a bounded wait ran out
+    float alpha;                 // gradients are alpha times the products with G
+    uint32_t pad[62];
+};
+
+struct GemmArgs {
+    CUtensorMap a, b;
+    int64_t m, n;                // rows, columns of the product that exist
+    int m_tiles, n_tiles;
+    int k_blocks;                // K-blocks in all
+    int splits;                  // parts of the K-blocks, one output each (kEpiAcc)
+    int b_y0;                    // logits: first vocabulary entry of the piece
+    CeHead* head;
+    const int64_t* targets;
+    int64_t vocab;
+    // kEpiLse
+    float2* part;                // [n_tiles][m]: a strip's maximum and sum
+    float* target_logit;         // [m]
+    // kEpiGrad
+    const float* lse;
+    const float* coef;           // row factors of G, 0: no loss
+    uint16_t* g;
+    int64_t g_stride;
+    // kEpiAcc
+    float* acc;                  // binary32 output [splits][m][n], or
+    int accumulate;              //   added to it
+    uint16_t* out;               // rounded output, times alpha
+    int64_t out_stride;
+    int withhold;                // test hook: the first copy is announced but not made, so the waits run out
+};
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <int EPI, int DT, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(kCeThreads, 1) k_ce_gemm(const __grid_constant__ GemmArgs g)
+{
+    extern __shared__ unsigned char sm_raw[];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 1];
+    __shared__ uint32_t s_tmem, s_fail;
+    const uint32_t sm = (tc::smem_addr(sm_raw) + 1023u) & ~1023u;
+    const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kStages, done = full + 16 * kStages;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; s++) {
+            tc::mbar_init(full + 8 * s, 1);
+            tc::mbar_init(empty + 8 * s, 1);
+        }
+        tc::mbar_init(done, 1);
+        s_fail = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tc::tmem_alloc(tc::smem_addr(&s_tmem), kBN);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = s_tmem;
+
+    int t = blockIdx.x;
+    const int mt = t % g.m_tiles;
+    t /= g.m_tiles;
+    const int nt = t % g.n_tiles, split = t / g.n_tiles;
+    const int kb0 = (int)((int64_t)g.k_blocks * split / g.splits);
+    const int kb1 = (int)((int64_t)g.k_blocks * (split + 1) / g.splits);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            bool ok = true;
+            int it = 0;
+            for (int kb = kb0; kb < kb1; kb++, it++) {
+                const int s = it % kStages;
+                if (!tc::mbar_wait(empty + 8 * s, ((it / kStages) & 1) ^ 1)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t bar = full + 8 * s, sa = sm + s * (kABytes + kBBytes), sb = sa + kABytes;
+                tc::mbar_arrive_expect_tx(bar, kABytes + kBBytes);
+                if (g.withhold && blockIdx.x == 0 && it == 0) continue;
+                if (A_MN) {
+                    for (int j = 0; j < kBM / 64; j++)
+                        tc::tma_load(sa + j * tc::kBoxBytes, &g.a, mt * kBM + 64 * j, kb * kBK, bar);
+                } else {
+                    tc::tma_load(sa, &g.a, kb * kBK, mt * kBM, bar);
+                }
+                if (B_MN) {
+                    for (int j = 0; j < kBN / 64; j++)
+                        tc::tma_load(sb + j * tc::kBoxBytes, &g.b, nt * kBN + 64 * j, g.b_y0 + kb * kBK, bar);
+                } else {
+                    tc::tma_load(sb, &g.b, kb * kBK, g.b_y0 + nt * kBN, bar);
+                }
+            }
+            // the last fill of every stage has landed before the block exits
+            for (int j = it - kStages < 0 ? 0 : it - kStages; j < it; j++)
+                ok &= tc::mbar_wait(full + 8 * (j % kStages), (j / kStages) & 1);
+            if (!ok) {
+                atomicOr(&g.head->err, 1u);
+                s_fail = 1;
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = tc::instr_desc<DT == kBF16, A_MN, B_MN>(kBM, kBN);
+            int it = 0;
+            for (int kb = kb0; kb < kb1; kb++, it++) {
+                const int s = it % kStages;
+                if (!tc::mbar_wait(full + 8 * s, (it / kStages) & 1)) {
+                    atomicOr(&g.head->err, 1u);
+                    s_fail = 1;
+                    break;
+                }
+                tc::fence_after_sync();
+                const uint32_t sa = sm + s * (kABytes + kBBytes), sb = sa + kABytes;
+                const uint64_t da = tc::operand_desc<A_MN>(sa), db = tc::operand_desc<B_MN>(sb);
+#pragma unroll
+                for (int k = 0; k < kBK / 16; k++)
+                    tc::mma(tmem, da + k * tc::kStep16<A_MN>, db + k * tc::kStep16<B_MN>, idesc, it > 0 || k > 0);
+                tc::mma_commit(empty + 8 * s);
+            }
+            tc::mma_commit(done);
+        }
+    } else {
+        const bool ok = tc::mbar_wait(done, 0) && *(volatile uint32_t*)&s_fail == 0;
+        if (!ok && lane == 0) atomicOr(&g.head->err, 1u);
+        tc::fence_after_sync();
+        const int band = warp & 3;                    // the warp's 32 lanes of tensor memory
+        const int64_t row = (int64_t)mt * kBM + band * 32 + lane;
+        const bool live = ok && row < g.m;
+        const uint32_t src = tmem + ((uint32_t)(band * 32) << 16);
+        const int64_t col0 = (int64_t)nt * kBN;
+        uint32_t r[32];
+        if constexpr (EPI == kEpiLse) {
+            const int64_t tgt = live ? g.targets[row] : -1;
+            float mx = -INFINITY, sum = 0.0f;
+            for (int c = 0; c < kBN; c += 32) {
+                tc::tmem_ld32(src + c, r);
+                tc::tmem_ld_wait();
+                float top = mx;
+#pragma unroll
+                for (int k = 0; k < 32; k++) {
+                    if (col0 + c + k >= g.n) r[k] = 0xff800000u;        // -inf
+                    top = fmaxf(top, __uint_as_float(r[k]));
+                    if (col0 + c + k == tgt) g.target_logit[row] = __uint_as_float(r[k]);
+                }
+                const float base = top == -INFINITY ? 0.0f : top * kLog2e;
+                sum *= exp2_fast(fmaf(mx, kLog2e, -base));
+#pragma unroll
+                for (int k = 0; k < 32; k++)
+                    sum += exp2_fast(fmaf(__uint_as_float(r[k]), kLog2e, -base));
+                mx = top;
+            }
+            if (live) g.part[(int64_t)nt * g.m + row] = make_float2(mx, sum);
+        } else if constexpr (EPI == kEpiGrad) {
+            const float cf = live ? g.coef[row] : 0.0f;
+            const int64_t tgt = live && cf != 0.0f ? g.targets[row] - g.b_y0 : -1;
+            const float base = live ? g.lse[row] * kLog2e : 0.0f;
+            for (int c = 0; c < kBN; c += 32) {
+                tc::tmem_ld32(src + c, r);
+                tc::tmem_ld_wait();
+                uint32_t h[16];
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                    float p[2];
+#pragma unroll
+                    for (int q = 0; q < 2; q++) {
+                        p[q] = exp2_fast(fmaf(__uint_as_float(r[k + q]), kLog2e, -base));
+                        if (col0 + c + k + q == tgt) p[q] -= 1.0f;
+                        p[q] = cf != 0.0f && col0 + c + k + q < g.n ? p[q] * cf : 0.0f;
+                    }
+                    h[k / 2] = from_f32x2<DT>(p[0], p[1]);
+                }
+                if (live) {
+                    uint4* dst = reinterpret_cast<uint4*>(g.g + row * g.g_stride + col0 + c);
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        dst[k] = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
+                }
+            }
+        } else {
+            const float alpha = g.head->alpha;
+            for (int c = 0; c < kBN && col0 + c < g.n; c += 32) {
+                tc::tmem_ld32(src + c, r);
+                tc::tmem_ld_wait();
+                const int cols = (int)min((int64_t)32, g.n - col0 - c);
+                if (!live) continue;
+                if (g.acc) {
+                    float* dst = g.acc + ((int64_t)split * g.m + row) * g.n + col0 + c;
+#pragma unroll
+                    for (int k = 0; k < 32; k++)
+                        if (k < cols) dst[k] = __uint_as_float(kb1 > kb0 ? r[k] : 0u) + (g.accumulate ? dst[k] : 0.0f);
+                } else {
+                    uint16_t* dst = g.out + row * g.out_stride + col0 + c;
+#pragma unroll
+                    for (int k = 0; k < 32; k++)
+                        if (k < cols) dst[k] = (uint16_t)from_f32<DT>(__uint_as_float(kb1 > kb0 ? r[k] : 0u) * alpha);
+                }
+            }
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 1) tc::tmem_free(tmem, kBN);
+}
+
+// Per token: the strips' maxima and sums joined, in strip order; the loss.
+__global__ void __launch_bounds__(128) k_ce_join(const CeHead* head, const float2* part, int strips, int64_t n,
+                                                 const int64_t* targets, int64_t vocab, const float* target_logit,
+                                                 float* loss, float* lse)
+{
+    const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    if (i >= n) return;
+    float mx = -INFINITY;
+    for (int s = 0; s < strips; s++)
+        mx = fmaxf(mx, part[(int64_t)s * n + i].x);
+    float sum = 0.0f;
+    const float ref = mx == -INFINITY ? 0.0f : mx;
+    for (int s = 0; s < strips; s++) {
+        const float2 p = part[(int64_t)s * n + i];
+        sum = fmaf(p.y, exp2f((p.x - ref) * kLog2e), sum);
+    }
+    float l = ref + logf(sum);
+    if (head->err) l = NAN;
+    lse[i] = l;
+    const int64_t t = targets[i];
+    loss[i] = t >= 0 && t < vocab ? l - target_logit[i] : 0.0f;
+}
+
+// One block: mean loss over the tokens that have one, and their number.
+__global__ void __launch_bounds__(1024) k_ce_total(const float* loss, const int64_t* targets, int64_t n, int64_t vocab,
+                                                   float* total)
+{
+    __shared__ float ss[1024];
+    __shared__ int64_t sc[1024];
+    float s = 0.0f;
+    int64_t c = 0;
+    for (int64_t i = threadIdx.x; i < n; i += 1024) {
+        const int64_t t = targets[i];
+        if (t >= 0 && t < vocab) {
+            s += loss[i];
+            c++;
+        }
+    }
+    ss[threadIdx.x] = s;
+    sc[threadIdx.x] = c;
+    __syncthreads();
+    for (int o = 512; o > 0; o >>= 1) {
+        if (threadIdx.x < o) {
+            ss[threadIdx.x] += ss[threadIdx.x + o];
+            sc[threadIdx.x] += sc[threadIdx.x + o];
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        total[0] = sc[0] ? ss[0] / (float)sc[0] : 0.0f;
+        total[1] = (float)sc[0];
+    }
+}
+
+// One block: the row factors of G and what the products are multiplied by.
+// Row factor = s_i / max |s| (times 2^14 in binary16, which keeps small
+// probabilities out of its subnormals), so that equal factors are exactly 1.
+__global__ void __launch_bounds__(1024) k_ce_factors(CeHead* head, const int64_t* targets, int64_t n, int64_t vocab,
+                                                     const float* dloss, float scale, float up, float* coef)
+{
+    __shared__ float sm[1024];
+    __shared__ int64_t sc[1024];
+    float most = 0.0f;
+    int64_t c = 0;
+    for (int64_t i = threadIdx.x; i < n; i += 1024) {
+        const int64_t t = targets[i];
+        if (t >= 0 && t < vocab) {
+            c++;
+            const float d = dloss ? fabsf(dloss[i]) : 1.0f;
+            most = !(d <= most) ? d : most;                  // NaN stays
+        }
+    }
+    sm[threadIdx.x] = most;
+    sc[threadIdx.x] = c;
+    __syncthreads();
+    for (int o = 512; o > 0; o >>= 1) {
+        if (threadIdx.x < o) {
+            const float x = sm[threadIdx.x], y = sm[threadIdx.x + o];
+            sm[threadIdx.x] = !(y <= x) ? y : x;
+            sc[threadIdx.x] += sc[threadIdx.x + o];
+        }
+        __syncthreads();
+    }
+    most = sm[0];
+    const float inv = most > 0.0f ? 1.0f / most : (most == 0.0f ? 0.0f : most);
+    if (threadIdx.x == 0) {
+        head->err = 0;
+        head->alpha = (dloss ? scale * most : (sc[0] ? scale / (float)sc[0] : 0.0f)) / up;
+    }
+    for (int64_t i = threadIdx.x; i < n; i += 1024) {
+        const int64_t t = targets[i];
+        coef[i] = t >= 0 && t < vocab ? (dloss ? dloss[i] * inv * up : up) : 0.0f;
+    }
+}
+
+// dx = alpha times the sum of the splits, rounded.
+template <int DT>
+__global__ void __launch_bounds__(256) k_ce_dx(const CeHead* head, const float* acc, int splits, int64_t m, int64_t n,
+                                               uint16_t* dx, int64_t stride)
+{
+    const float alpha = head->err ? NAN : head->alpha;
+    const int64_t total = m * n;
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
+        float s = 0.0f;
+        for (int k = 0; k < splits; k++)
+            s += acc[(int64_t)k * total + e];
+        dx[e / n * stride + e % n] = (uint16_t)from_f32<DT>(s * alpha);
+    }
+}
+
+__global__ void __launch_bounds__(256) k_ce_zero(uint16_t* p, int64_t rows, int64_t cols, int64_t stride)
+{
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < rows * cols; e += (int64_t)gridDim.x * 256)
+        p[e / cols * stride + e % cols] = 0;
+}
+
+// ---- host -------------------------------------------------------------------------
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t up256(int64_t a) { return (a + 255) / 256 * 256; }
+
+zero_status_t cuda_failed(cudaError_t e, const char* what)
+{
+    char msg[200];
+    std::snprintf(msg, sizeof msg, "%s: %s", what, cudaGetErrorString(e));
+    return set_error(ZERO_ECUDA, msg);
+}
+
+// Byte offsets in the workspace.
+struct CeLayout {
+    int64_t coef, target_logit, part, g, acc, end;
+};
+
+CeLayout layout_of(const zero_ce_plan_t& p)
+{
+    CeLayout l;
+    l.coef = sizeof(CeHead);
+    l.target_logit = l.coef + up256(p.tokens * 4);
+    l.part = l.target_logit + up256(p.tokens * 4);
+    l.g = l.part;                                     // the two passes do not meet
+    l.acc = l.g + up256(p.tokens * p.piece * 2);
+    const int64_t fwd = l.part + ceil_div(p.vocab, kBN) * p.tokens * 8;
+    const int64_t bwd = l.acc + (int64_t)p.splits * p.tokens * p.hidden * 4;
+    l.end = up256(fwd > bwd ? fwd : bwd);
+    return l;
+}
+
+zero_status_t check_ce_plan(const zero_ce_plan_t* p)
+{
+    if (!p) return set_error(ZERO_EINVAL, "cross entropy plan is NULL");
+    zero_ce_plan_t fresh;
+    const zero_status_t st = zero_ce_plan(p->tokens, p->vocab, p->hidden, p->dtype, p->x_stride, p->w_stride, p->piece,
+                                          &fresh);
+    if (st != ZERO_OK) return st;
+    if (std::memcmp(&fresh, p, sizeof fresh) != 0)
+        return set_error(ZERO_EINVAL, "cross entropy plan was not made by zero_ce_plan");
+    return ZERO_OK;
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn()
+{
+    static const EncodeFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+
+// rows x cols 16-bit values, `stride` values between rows; boxes of 64
+// columns x box_rows rows, 128-byte swizzle; zeros outside.
+bool make_map(CUtensorMap* map, int dtype, const void* base, int64_t rows, int64_t cols, int64_t stride, int box_rows)
+{
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    return encode_fn()(map, dtype == ZERO_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                       const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int EPI, int DT, bool A_MN, bool B_MN>
+cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t s)
+{
+    const void* k = (const void*)k_ce_gemm<EPI, DT, A_MN, B_MN>;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kCeSmem);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = (unsigned)((int64_t)g.m_tiles * g.n_tiles * g.splits);
+    k_ce_gemm<EPI, DT, A_MN, B_MN><<<grid, kCeThreads, kCeSmem, s>>>(g);
+    return cudaGetLastError();
+}
+
+template <int EPI, bool A_MN, bool B_MN>
+cudaError_t gemm(int dtype, const GemmArgs& g, cudaStream_t s)
+{
+    return dtype == ZERO_BF16 ? launch_gemm<EPI, kBF16, A_MN, B_MN>(g, s) : launch_gemm<EPI, kF16, A_MN, B_MN>(g, s);
+}
+
+}  // namespace
+}  // namespace zg
+
+using namespace zg;
+
+extern "C" {
+
+zero_status_t zero_ce_plan(int64_t tokens, int64_t vocab, int64_t hidden, int32_t dtype, int64_t x_stride,
+                           int64_t w_stride, int64_t piece, zero_ce_plan_t* out)
+{
+    if (!out) return set_error(ZERO_EINVAL, "zero_ce_plan: out is NULL");
+    if (dtype == ZERO_FP32) return set_error(ZERO_EUNSUPPORTED, "zero_ce_plan: 16-bit types only");
+    if (dtype != ZERO_FP16 && dtype != ZERO_BF16) return set_error(ZERO_EINVAL, "zero_ce_plan: dtype unknown");
+    if (tokens < 0 || vocab < 1 || hidden < 1)
+        return set_error(ZERO_EINVAL, "zero_ce_plan: tokens must be >= 0, vocab and hidden >= 1");
+    if (tokens > (int64_t(1) << 24) || vocab > (int64_t(1) << 24) || hidden > (int64_t(1) << 20))
+        return set_error(ZERO_EUNSUPPORTED, "zero_ce_plan: tokens or vocab exceed 2^24, or hidden 2^20");
+    const int64_t xs = x_stride ? x_stride : hidden, ws = w_stride ? w_stride : hidden;
+    if (xs < hidden || ws < hidden || piece < 0)
+        return set_error(ZERO_EINVAL, "zero_ce_plan: a stride is below hidden, or piece below 0");
+    if (xs % 8 || ws % 8) return set_error(ZERO_EALIGN, "zero_ce_plan: row strides must be multiples of 8 values");
+    if (xs >= (int64_t(1) << 38) || ws >= (int64_t(1) << 38))
+        return set_error(ZERO_EUNSUPPORTED, "zero_ce_plan: a stride is 2^38 or more");
+    std::memset(out, 0, sizeof *out);
+    out->tokens = tokens;
+    out->vocab = vocab;
+    out->hidden = hidden;
+    out->x_stride = xs;
+    out->w_stride = ws;
+    out->dtype = dtype;
+    const int64_t all = up256(vocab);
+    if (piece) {
+        out->piece = up256(piece) < all ? up256(piece) : all;
+    } else {
+        // about 256 MiB of G, in pieces of about the same size
+        const int64_t most = tokens ? (int64_t(1) << 27) / tokens / 256 * 256 : all;
+        const int64_t fit = most < 256 ? 256 : (most < all ? most : all);
+        out->piece = up256(ceil_div(vocab, ceil_div(all, fit)));
+    }
+    // dx has few tiles when there are few tokens: its K (the piece) is then
+    // summed in parts, each at least 8 K-blocks, until the tiles fill the GPU
+    const int64_t tiles = ceil_div(tokens, kBM) * ceil_div(hidden, kBN), blocks = ceil_div(out->piece, kBK);
+    int64_t best = 1;
+    double cost = 1e30;
+    for (int64_t s = 1; s <= 32 && s * 8 <= blocks; s++) {
+        const double c = (double)ceil_div(tiles * s, 152) / (double)s * (1.0 + 0.01 * (double)s);
+        if (c < cost * 0.97) {
+            cost = c;
+            best = s;
+        }
+    }
+    out->splits = (int32_t)best;
+    out->workspace_bytes = layout_of(*out).end;
+    out->flops_forward = 2 * tokens * vocab * hidden;
+    out->flops_backward = 3 * out->flops_forward;
+    return ZERO_OK;
+}
+
+zero_status_t zero_ce_forward(const zero_ce_plan_t* plan, const void* x, const void* w, const int64_t* targets,
+                              float* loss, float* lse, float* total, void* workspace, void* stream)
+{
+    NvtxRange range("zero_ce_forward");
+    const zero_status_t st = check_ce_plan(plan);
+    if (st != ZERO_OK) return st;
+    const zero_ce_plan_t& p = *plan;
+    if (!workspace) return set_error(ZERO_ENOMEM, "zero_ce_forward: workspace is NULL");
+    if (p.tokens && (!x || !w || !targets || !loss || !lse))
+        return set_error(ZERO_ENOMEM, "zero_ce_forward: a buffer is NULL");
+    if (!aligned_to(x, 16) || !aligned_to(w, 16) || !aligned_to(workspace, 16) || !aligned_to(targets, 8) ||
+        !aligned_to(loss, 4) || !aligned_to(lse, 4) || !aligned_to(total, 4))
+        return set_error(ZERO_EALIGN, "zero_ce_forward: x, w and workspace must be 16-byte aligned, the others to their type");
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(CeHead), s);
+    if (e != cudaSuccess) return cuda_failed(e, "zero_ce_forward");
+    if (p.tokens) {
+        if (!encode_fn()) return set_error(ZERO_ECUDA, "zero_ce_forward: the driver has no cuTensorMapEncodeTiled");
+        const CeLayout l = layout_of(p);
+        GemmArgs g;
+        std::memset(&g, 0, sizeof g);
+        if (!make_map(&g.a, p.dtype, x, p.tokens, p.hidden, p.x_stride, kBM) ||
+            !make_map(&g.b, p.dtype, w, p.vocab, p.hidden, p.w_stride, kBN))
+            return set_error(ZERO_ECUDA, "zero_ce_forward: cuTensorMapEncodeTiled refused a buffer");
+        g.m = p.tokens;
+        g.n = p.vocab;
+        g.m_tiles = (int)ceil_div(p.tokens, kBM);
+        g.n_tiles = (int)ceil_div(p.vocab, kBN);
+        g.k_blocks = (int)ceil_div(p.hidden, kBK);
+        g.splits = 1;
+        g.head = reinterpret_cast<CeHead*>(ws);
+        g.targets = targets;
+        g.vocab = p.vocab;
+        g.part = reinterpret_cast<float2*>(ws + l.part);
+        g.target_logit = reinterpret_cast<float*>(ws + l.target_logit);
+        g.withhold = std::getenv("ZERO_TEST_WITHHOLD_TILE") != nullptr;
+        e = gemm<kEpiLse, false, false>(p.dtype, g, s);
+        if (e == cudaSuccess) {
+            k_ce_join<<<(unsigned)ceil_div(p.tokens, 128), 128, 0, s>>>(g.head, g.part, g.n_tiles, p.tokens, targets,
+                                                                        p.vocab, g.target_logit, loss, lse);
+            e = cudaGetLastError();
+        }
+    }
+    if (e == cudaSuccess && total) {
+        k_ce_total<<<1, 1024, 0, s>>>(loss, targets, p.tokens, p.vocab, total);
+        e = cudaGetLastError();
+    }
+    return e == cudaSuccess ? ZERO_OK : cuda_failed(e, "zero_ce_forward");
+}
+
+zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const void* w, const int64_t* targets,
+                               const float* lse, const float* dloss, float grad_scale, void* dx, void* dw,
+                               void* workspace, void* stream)
+{
+    NvtxRange range("zero_ce_backward");
+    const zero_status_t st = check_ce_plan(plan);
+    if (st != ZERO_OK) return st;
+    const zero_ce_plan_t& p = *plan;
+    if (!std::isfinite(grad_scale)) return set_error(ZERO_EINVAL, "zero_ce_backward: grad_scale is not finite");
+    if (!workspace) return set_error(ZERO_ENOMEM, "zero_ce_backward: workspace is NULL");
+    if (p.tokens && (!x || !w || !targets || !lse)) return set_error(ZERO_ENOMEM, "zero_ce_backward: a buffer is NULL");
+    if (!aligned_to(x, 16) || !aligned_to(w, 16) || !aligned_to(dx, 16) || !aligned_to(dw, 16) ||
+        !aligned_to(workspace, 16) || !aligned_to(targets, 8) || !aligned_to(lse, 4) || !aligned_to(dloss, 4))
+        return set_error(ZERO_EALIGN, "zero_ce_backward: x, w, dx, dw and workspace must be 16-byte aligned, the others to their type");
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!p.tokens) {
+        if (dw) k_ce_zero<<<1024, 256, 0, s>>>(static_cast<uint16_t*>(dw), p.vocab, p.hidden, p.w_stride);
+        const cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(CeHead), s);
+        return e == cudaSuccess ? ZERO_OK : cuda_failed(e, "zero_ce_backward");
+    }
+    if (!dx && !dw) return ZERO_OK;
+    if (!encode_fn()) return set_error(ZERO_ECUDA, "zero_ce_backward: the driver has no cuTensorMapEncodeTiled");
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    const CeLayout l = layout_of(p);
+    CeHead* head = reinterpret_cast<CeHead*>(ws);
+    float* coef = reinterpret_cast<float*>(ws + l.coef);
+    uint16_t* G = reinterpret_cast<uint16_t*>(ws + l.g);
+    float* acc = reinterpret_cast<float*>(ws + l.acc);
+    const float up = p.dtype == ZERO_FP16 ? 16384.0f : 1.0f;
+    k_ce_factors<<<1, 1024, 0, s>>>(head, targets, p.tokens, p.vocab, dloss, grad_scale, up, coef);
+    cudaError_t e = cudaGetLastError();
+    for (int64_t v0 = 0; v0 < p.vocab && e == cudaSuccess; v0 += p.piece) {
+        const int64_t nv = p.vocab - v0 < p.piece ? p.vocab - v0 : p.piece;
+        GemmArgs g;
+        std::memset(&g, 0, sizeof g);
+        bool ok = make_map(&g.a, p.dtype, x, p.tokens, p.hidden, p.x_stride, kBM) &&
+                  make_map(&g.b, p.dtype, w, p.vocab, p.hidden, p.w_stride, kBN);
+        g.m = p.tokens;
+        g.n = nv;
+        g.m_tiles = (int)ceil_div(p.tokens, kBM);
+        g.n_tiles = (int)ceil_div(nv, kBN);
+        g.k_blocks = (int)ceil_div(p.hidden, kBK);
+        g.splits = 1;
+        g.b_y0 = (int)v0;
+        g.head = head;
+        g.targets = targets;
+        g.vocab = p.vocab;
+        g.lse = lse;
+        g.coef = coef;
+        g.g = G;
+        g.g_stride = p.piece;
+        if (ok) e = gemm<kEpiGrad, false, false>(p.dtype, g, s);
+        if (ok && dx && e == cudaSuccess) {          // dx += G w
+            ok = make_map(&g.a, p.dtype, G, p.tokens, p.piece, p.piece, kBM) &&
+                 make_map(&g.b, p.dtype, w, p.vocab, p.hidden, p.w_stride, 64);
+            g.n = p.hidden;
+            g.n_tiles = (int)ceil_div(p.hidden, kBN);
+            g.k_blocks = (int)ceil_div(nv, kBK);
+            g.splits = p.splits;
+            g.acc = acc;
+            g.accumulate = v0 > 0;
+            if (ok) e = gemm<kEpiAcc, false, true>(p.dtype, g, s);
+        }
+        if (ok && dw && e == cudaSuccess) {          // dw = G^T x
+            ok = make_map(&g.a, p.dtype, G, p.tokens, p.piece, p.piece, 64) &&
+                 make_map(&g.b, p.dtype, x, p.tokens, p.hidden, p.x_stride, 64);
+            g.b_y0 = 0;
+            g.m = nv;
+            g.n = p.hidden;
+            g.m_tiles = (int)ceil_div(nv, kBM);
+            g.n_tiles = (int)ceil_div(p.hidden, kBN);
+            g.k_blocks = (int)ceil_div(p.tokens, kBK);
+            g.splits = 1;
+            g.acc = nullptr;
+            g.out = static_cast<uint16_t*>(dw) + v0 * p.w_stride;
+            g.out_stride = p.w_stride;
+            if (ok) e = gemm<kEpiAcc, true, true>(p.dtype, g, s);
+        }
+        if (!ok) return set_error(ZERO_ECUDA, "zero_ce_backward: cuTensorMapEncodeTiled refused a buffer");
+    }
+    if (dx && e == cudaSuccess) {
+        if (p.dtype == ZERO_BF16)
+            k_ce_dx<kBF16><<<152 * 8, 256, 0, s>>>(head, acc, p.splits, p.tokens, p.hidden, static_cast<uint16_t*>(dx), p.x_stride);
+        else
+            k_ce_dx<kF16><<<152 * 8, 256, 0, s>>>(head, acc, p.splits, p.tokens, p.hidden, static_cast<uint16_t*>(dx), p.x_stride);
+        e = cudaGetLastError();
+    }
+    return e == cudaSuccess ? ZERO_OK : cuda_failed(e, "zero_ce_backward");
+}
+
+zero_status_t zero_ce_status(const zero_ce_plan_t* plan, const void* workspace, void* stream)
+{
+    const zero_status_t st = check_ce_plan(plan);
+    if (st != ZERO_OK) return st;
+    if (!workspace) return set_error(ZERO_ENOMEM, "zero_ce_status: workspace is NULL");
+    if (!aligned_to(workspace, 16)) return set_error(ZERO_EALIGN, "zero_ce_status: workspace is not 16-byte aligned");
+    uint32_t err = 0;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMemcpyAsync(&err, workspace, 4, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return cuda_failed(e, "zero_ce_status");
+    return err ? set_error(ZERO_ETIMEOUT, "a bounded wait inside the cross entropy kernels ran out") : ZERO_OK;
+}
+
+}  // extern "C"
