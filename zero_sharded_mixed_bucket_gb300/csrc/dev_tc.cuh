@@ -37,13 +37,14 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t byt
 }
 
 // Wait for the completion of the barrier's phase with parity `parity`; false
-// once kWaitNs have passed without it.
+// once kWaitNs have passed without it.  Acquires at cluster scope: some of
+// the barriers are arrived on from the pair's other CTA.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity)
 {
     uint64_t t0 = 0;
     for (uint32_t k = 0;; k++) {
         uint32_t done;
-        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
                      "selp.u32 %0, 1, 0, p;\n\t}"
                      : "=r"(done) : "r"(bar), "r"(parity) : "memory");
         if (done) return true;
@@ -55,11 +56,37 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity)
     }
 }
 
-// Tiled bulk copy of a box at element coordinates (x, y); x starts a 16-byte
-// unit (the callers' x are multiples of 64 values).
+// ---- pairs of CTAs (a cluster of two) ------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Arrive on the barrier at this offset in the pair's first CTA.
+__device__ __forceinline__ void mbar_arrive_leader(uint32_t bar)
+{
+    asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
+                 "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" :: "r"(bar) : "memory");
+}
+
+// The address, in the pair's first CTA, of what lies at this address here
+// (shared::cluster addresses of a pair differ in bit 24).
+__device__ __forceinline__ uint32_t in_leader(uint32_t addr) { return addr & 0xfeffffffu; }
+
+// Tiled bulk copy of a box at element coordinates (x, y) into this CTA's
+// shared memory, completing on a barrier of either CTA of the pair; x starts
+// a 16-byte unit (the callers' x are multiples of 64 values).
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
 {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3}], [%4];"
                  :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
 }
 
@@ -68,16 +95,17 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map)
     asm volatile("prefetch.tensormap [%0];" :: "l"(map) : "memory");
 }
 
-// ---- tensor memory ----------------------------------------------------------------
+// ---- tensor memory (of both CTAs of a pair at once) ------------------------------------
+// One whole warp in each CTA.
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_out, uint32_t cols)
 {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_out), "r"(cols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_out), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols)
 {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(addr), "r"(cols) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(addr), "r"(cols) : "memory");
 }
 
 __device__ __forceinline__ void fence_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -127,17 +155,22 @@ __host__ __device__ constexpr uint32_t instr_desc(uint32_t m, uint32_t n)
            ((B_MN ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
+// D (+)= A B: rows 0..127 in the first CTA's tensor memory, 128..255 in the
+// second's; A's halves of rows and B's halves of columns lie in the two CTAs'
+// shared memory at the same offsets.
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
 {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
                  :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate) : "memory");
 }
 
-// Arrive on `bar` when every product issued so far by this thread is done.
+// Arrive on `bar`, in both CTAs, when every product issued so far by this
+// thread is done.
 __device__ __forceinline__ void mma_commit(uint32_t bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 :: "r"(bar), "h"((uint16_t)3) : "memory");
 }
 
 }  // namespace tc

@@ -13,11 +13,15 @@
 namespace zg {
 namespace {
 
-constexpr int kBM = 128, kBN = 256, kBK = 64;         // tile of one block's product, K-values per stage
-constexpr int kStages = 4;
-constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2;
-constexpr int kCeThreads = 192;                       // producer warp, issuing warp, four epilogue warps
+constexpr int kBM = 256, kBN = 256, kBK = 64;         // a pair's tile, K-values per stage
+constexpr int kStages = 6;
+constexpr int kABytes = kBM / 2 * kBK * 2, kBBytes = kBN / 2 * kBK * 2;   // one CTA's part of a stage
+constexpr int kEpiWarps = 8;
+constexpr int kCeThreads = 64 + 32 * kEpiWarps;       // copying warp, issuing warp, epilogue warps
 constexpr int kCeSmem = kStages * (kABytes + kBBytes) + 1024;
+constexpr int kStrip = kBN / 2;                       // vocabulary entries per (maximum, sum)
+constexpr int kChunk = 16;                            // loss: K-blocks the tensor cores add up by themselves
+constexpr int kGroup = 8;                             // row tiles that share the column tiles in L2
 constexpr float kLog2e = 1.4426950408889634f;
 
 enum { kEpiLse, kEpiGrad, kEpiAcc };
@@ -40,7 +44,7 @@ struct GemmArgs {
     const int64_t* targets;
     int64_t vocab;
     // kEpiLse
-    float2* part;                // [n_tiles][m]: a strip's maximum and sum
+    float2* part;                // [strips][m]: a strip's maximum and sum
     float* target_logit;         // [m]
     // kEpiGrad
     const float* lse;
@@ -62,174 +66,304 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
+struct Tile {
+    int split, mt, nt, kb0, kb1;
+};
+
+// Tile of a place in the order: splits outermost, then groups of kGroup row
+// tiles, then column tiles, so that the tiles running at one time share rows
+// of A and of B in L2.
+__device__ __forceinline__ Tile tile_at(const GemmArgs& g, int64_t t)
+{
+    const int64_t per = (int64_t)g.m_tiles * g.n_tiles;
+    Tile r;
+    r.split = (int)(t / per);
+    t %= per;
+    const int group = (int)(t / ((int64_t)kGroup * g.n_tiles));
+    const int in = (int)(t - (int64_t)group * kGroup * g.n_tiles);
+    const int rows = min(kGroup, g.m_tiles - group * kGroup);
+    r.nt = in / rows;
+    r.mt = group * kGroup + in % rows;
+    r.kb0 = (int)((int64_t)g.k_blocks * r.split / g.splits);
+    r.kb1 = (int)((int64_t)g.k_blocks * (r.split + 1) / g.splits);
+    return r;
+}
+
+// C = A B^T for 256 x 256 tiles, a pair of CTAs per tile, each pair striding
+// over the tiles.  One thread per CTA copies the CTA's half of A's rows and of
+// B's through a ring of kStages stages; one thread of the pair issues the
+// products, which accumulate in one of two halves of tensor memory while the
+// epilogue warps read the other.  Every wait is bounded; one that runs out
+// sets head->err and ends its role, and the others run out in turn.
+// A chunk is the K-range that is accumulated in tensor memory at one go: the
+// tensor cores cut their binary32 sums toward zero, 256 times along K = 4096,
+// which is off by 1e-6 of the loss; the loss adds chunks of kChunk K-blocks in
+// registers, rounding to nearest.  The other products are rounded to 16 bits.
 template <int EPI, int DT, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(kCeThreads, 1) k_ce_gemm(const __grid_constant__ GemmArgs g)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_gemm(const __grid_constant__ GemmArgs g)
 {
     extern __shared__ unsigned char sm_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * kStages + 1];
-    __shared__ uint32_t s_tmem, s_fail;
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 4];
+    __shared__ uint32_t s_tmem;
     const uint32_t sm = (tc::smem_addr(sm_raw) + 1023u) & ~1023u;
-    const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kStages, done = full + 16 * kStages;
+    const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kStages;
+    const uint32_t acc_full = full + 16 * kStages, acc_empty = acc_full + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = tc::cluster_rank();
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; s++) {
             tc::mbar_init(full + 8 * s, 1);
             tc::mbar_init(empty + 8 * s, 1);
         }
-        tc::mbar_init(done, 1);
-        s_fail = 0;
+        for (int s = 0; s < 2; s++) {
+            tc::mbar_init(acc_full + 8 * s, 1);
+            tc::mbar_init(acc_empty + 8 * s, 2 * kEpiWarps);
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 1) tc::tmem_alloc(tc::smem_addr(&s_tmem), kBN);
+    if (warp == 1) tc::tmem_alloc(tc::smem_addr(&s_tmem), 2 * kBN);
     tc::fence_before_sync();
     __syncthreads();
+    tc::cluster_sync();
     tc::fence_after_sync();
     const uint32_t tmem = s_tmem;
-
-    int t = blockIdx.x;
-    const int mt = t % g.m_tiles;
-    t /= g.m_tiles;
-    const int nt = t % g.n_tiles, split = t / g.n_tiles;
-    const int kb0 = (int)((int64_t)g.k_blocks * split / g.splits);
-    const int kb1 = (int)((int64_t)g.k_blocks * (split + 1) / g.splits);
+    const int64_t tiles = (int64_t)g.m_tiles * g.n_tiles * g.splits;
+    const int64_t first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+    constexpr int kChunkBlocks = EPI == kEpiLse ? kChunk : 1 << 30;
 
     if (warp == 0) {
         if (lane == 0) {
             bool ok = true;
             int it = 0;
-            for (int kb = kb0; kb < kb1; kb++, it++) {
-                const int s = it % kStages;
-                if (!tc::mbar_wait(empty + 8 * s, ((it / kStages) & 1) ^ 1)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t bar = full + 8 * s, sa = sm + s * (kABytes + kBBytes), sb = sa + kABytes;
-                tc::mbar_arrive_expect_tx(bar, kABytes + kBBytes);
-                if (g.withhold && blockIdx.x == 0 && it == 0) continue;
-                if (A_MN) {
-                    for (int j = 0; j < kBM / 64; j++)
-                        tc::tma_load(sa + j * tc::kBoxBytes, &g.a, mt * kBM + 64 * j, kb * kBK, bar);
-                } else {
-                    tc::tma_load(sa, &g.a, kb * kBK, mt * kBM, bar);
-                }
-                if (B_MN) {
-                    for (int j = 0; j < kBN / 64; j++)
-                        tc::tma_load(sb + j * tc::kBoxBytes, &g.b, nt * kBN + 64 * j, g.b_y0 + kb * kBK, bar);
-                } else {
-                    tc::tma_load(sb, &g.b, kb * kBK, g.b_y0 + nt * kBN, bar);
+            for (int64_t t = first; t < tiles && ok; t += stride) {
+                const Tile w = tile_at(g, t);
+                const int m0 = w.mt * kBM + (int)rank * (kBM / 2), n0 = w.nt * kBN + (int)rank * (kBN / 2);
+                for (int kb = w.kb0; kb < w.kb1; kb++, it++) {
+                    const int s = it % kStages;
+                    if (!tc::mbar_wait(empty + 8 * s, ((it / kStages) & 1) ^ 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = tc::in_leader(full + 8 * s);
+                    const uint32_t sa = sm + s * (kABytes + kBBytes), sb = sa + kABytes;
+                    if (rank == 0) {
+                        tc::mbar_arrive_expect_tx(full + 8 * s, 2 * (kABytes + kBBytes));
+                        if (g.withhold && blockIdx.x == 0 && it == 0) continue;
+                    }
+                    if (A_MN) {
+#pragma unroll
+                        for (int j = 0; j < kBM / 128; j++)
+                            tc::tma_load(sa + j * tc::kBoxBytes, &g.a, m0 + 64 * j, kb * kBK, bar);
+                    } else {
+                        tc::tma_load(sa, &g.a, kb * kBK, m0, bar);
+                    }
+                    if (B_MN) {
+#pragma unroll
+                        for (int j = 0; j < kBN / 128; j++)
+                            tc::tma_load(sb + j * tc::kBoxBytes, &g.b, n0 + 64 * j, g.b_y0 + kb * kBK, bar);
+                    } else {
+                        tc::tma_load(sb, &g.b, kb * kBK, g.b_y0 + n0, bar);
+                    }
                 }
             }
-            // the last fill of every stage has landed before the block exits
-            for (int j = it - kStages < 0 ? 0 : it - kStages; j < it; j++)
-                ok &= tc::mbar_wait(full + 8 * (j % kStages), (j / kStages) & 1);
             if (!ok) {
+                // the copies in flight have landed before the pair exits (when
+                // all went well the epilogue has seen every product done)
                 atomicOr(&g.head->err, 1u);
-                s_fail = 1;
+                if (rank == 0)
+                    for (int j = it - kStages < 0 ? 0 : it - kStages; j < it; j++)
+                        tc::mbar_wait(full + 8 * (j % kStages), (j / kStages) & 1);
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (lane == 0 && rank == 0) {
             constexpr uint32_t idesc = tc::instr_desc<DT == kBF16, A_MN, B_MN>(kBM, kBN);
-            int it = 0;
-            for (int kb = kb0; kb < kb1; kb++, it++) {
-                const int s = it % kStages;
-                if (!tc::mbar_wait(full + 8 * s, (it / kStages) & 1)) {
-                    atomicOr(&g.head->err, 1u);
-                    s_fail = 1;
-                    break;
-                }
-                tc::fence_after_sync();
-                const uint32_t sa = sm + s * (kABytes + kBBytes), sb = sa + kABytes;
-                const uint64_t da = tc::operand_desc<A_MN>(sa), db = tc::operand_desc<B_MN>(sb);
+            int it = 0, unit = 0;
+            bool ok = true;
+            for (int64_t t = first; t < tiles && ok; t += stride) {
+                const Tile w = tile_at(g, t);
+                for (int c0 = w.kb0; c0 < w.kb1 && ok; c0 += kChunkBlocks, unit++) {
+                    const int buf = unit & 1;
+                    if (!tc::mbar_wait(acc_empty + 8 * buf, ((unit >> 1) & 1) ^ 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after_sync();
+                    const int c1 = min(w.kb1, (EPI == kEpiLse ? c0 + kChunkBlocks : w.kb1));
+                    for (int kb = c0; kb < c1; kb++, it++) {
+                        const int s = it % kStages;
+                        if (!tc::mbar_wait(full + 8 * s, (it / kStages) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after_sync();
+                        const uint32_t sa = sm + s * (kABytes + kBBytes), sb = sa + kABytes;
+                        const uint64_t da = tc::operand_desc<A_MN>(sa), db = tc::operand_desc<B_MN>(sb);
 #pragma unroll
-                for (int k = 0; k < kBK / 16; k++)
-                    tc::mma(tmem, da + k * tc::kStep16<A_MN>, db + k * tc::kStep16<B_MN>, idesc, it > 0 || k > 0);
-                tc::mma_commit(empty + 8 * s);
+                        for (int k = 0; k < kBK / 16; k++)
+                            tc::mma(tmem + buf * kBN, da + k * tc::kStep16<A_MN>, db + k * tc::kStep16<B_MN>, idesc,
+                                    kb > c0 || k > 0);
+                        tc::mma_commit(empty + 8 * s);
+                    }
+                    if (ok) tc::mma_commit(acc_full + 8 * buf);
+                    if (EPI != kEpiLse) {
+                        unit++;
+                        break;
+                    }
+                }
             }
-            tc::mma_commit(done);
+            if (!ok) atomicOr(&g.head->err, 1u);
         }
     } else {
-        const bool ok = tc::mbar_wait(done, 0) && *(volatile uint32_t*)&s_fail == 0;
-        if (!ok && lane == 0) atomicOr(&g.head->err, 1u);
-        tc::fence_after_sync();
         const int band = warp & 3;                    // the warp's 32 lanes of tensor memory
-        const int64_t row = (int64_t)mt * kBM + band * 32 + lane;
-        const bool live = ok && row < g.m;
-        const uint32_t src = tmem + ((uint32_t)(band * 32) << 16);
-        const int64_t col0 = (int64_t)nt * kBN;
-        uint32_t r[32];
-        if constexpr (EPI == kEpiLse) {
-            const int64_t tgt = live ? g.targets[row] : -1;
-            float mx = -INFINITY, sum = 0.0f;
-            for (int c = 0; c < kBN; c += 32) {
-                tc::tmem_ld32(src + c, r);
-                tc::tmem_ld_wait();
-                float top = mx;
+        const int half = (warp - 2) >> 2;             // and its 128 columns
+        const uint32_t src = tmem + ((uint32_t)(band * 32) << 16) + half * kStrip;
+        int unit = 0;
+        bool ok = true;
+        for (int64_t t = first; t < tiles && ok; t += stride) {
+            const Tile w = tile_at(g, t);
+            const int64_t row = (int64_t)w.mt * kBM + rank * (kBM / 2) + band * 32 + lane;
+            const bool live = row < g.m;
+            const int64_t col0 = (int64_t)w.nt * kBN + half * kStrip;
+            if constexpr (EPI == kEpiLse) {
+                float z[kStrip];
+                for (int c0 = w.kb0; c0 < w.kb1; c0 += kChunkBlocks, unit++) {
+                    const int buf = unit & 1;
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(acc_full + 8 * buf, (unit >> 1) & 1));
+                    if (!ok) break;
+                    tc::fence_after_sync();
 #pragma unroll
-                for (int k = 0; k < 32; k++) {
-                    if (col0 + c + k >= g.n) r[k] = 0xff800000u;        // -inf
-                    top = fmaxf(top, __uint_as_float(r[k]));
-                    if (col0 + c + k == tgt) g.target_logit[row] = __uint_as_float(r[k]);
-                }
-                const float base = top == -INFINITY ? 0.0f : top * kLog2e;
-                sum *= exp2_fast(fmaf(mx, kLog2e, -base));
+                    for (int q = 0; q < kStrip / 32; q++) {
+                        uint32_t r[32];
+                        tc::tmem_ld32(src + buf * kBN + 32 * q, r);
+                        tc::tmem_ld_wait();
+                        if (c0 == w.kb0) {
 #pragma unroll
-                for (int k = 0; k < 32; k++)
-                    sum += exp2_fast(fmaf(__uint_as_float(r[k]), kLog2e, -base));
-                mx = top;
-            }
-            if (live) g.part[(int64_t)nt * g.m + row] = make_float2(mx, sum);
-        } else if constexpr (EPI == kEpiGrad) {
-            const float cf = live ? g.coef[row] : 0.0f;
-            const int64_t tgt = live && cf != 0.0f ? g.targets[row] - g.b_y0 : -1;
-            const float base = live ? g.lse[row] * kLog2e : 0.0f;
-            for (int c = 0; c < kBN; c += 32) {
-                tc::tmem_ld32(src + c, r);
-                tc::tmem_ld_wait();
-                uint32_t h[16];
+                            for (int k = 0; k < 32; k++)
+                                z[32 * q + k] = __uint_as_float(r[k]);
+                        } else {
 #pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                    float p[2];
-#pragma unroll
-                    for (int q = 0; q < 2; q++) {
-                        p[q] = exp2_fast(fmaf(__uint_as_float(r[k + q]), kLog2e, -base));
-                        if (col0 + c + k + q == tgt) p[q] -= 1.0f;
-                        p[q] = cf != 0.0f && col0 + c + k + q < g.n ? p[q] * cf : 0.0f;
+                            for (int k = 0; k < 32; k++)
+                                z[32 * q + k] += __uint_as_float(r[k]);
+                        }
                     }
-                    h[k / 2] = from_f32x2<DT>(p[0], p[1]);
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_leader(acc_empty + 8 * buf);
                 }
-                if (live) {
-                    uint4* dst = reinterpret_cast<uint4*>(g.g + row * g.g_stride + col0 + c);
+                if (!ok) break;
+                // the strip's maximum and its sum
+                const int64_t left = g.n - col0;
+                if (left < kStrip) {
 #pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        dst[k] = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
+                    for (int k = 0; k < kStrip; k++)
+                        if (k >= left) z[k] = -INFINITY;
                 }
-            }
-        } else {
-            const float alpha = g.head->alpha;
-            for (int c = 0; c < kBN && col0 + c < g.n; c += 32) {
-                tc::tmem_ld32(src + c, r);
-                tc::tmem_ld_wait();
-                const int cols = (int)min((int64_t)32, g.n - col0 - c);
-                if (!live) continue;
-                if (g.acc) {
-                    float* dst = g.acc + ((int64_t)split * g.m + row) * g.n + col0 + c;
+                const int64_t tgt = (live ? g.targets[row] : -1) - col0;
+                const bool here = tgt >= 0 && tgt < kStrip && tgt < left;
+                if (__any_sync(0xffffffffu, here)) {
+                    float zt = 0.0f;
 #pragma unroll
-                    for (int k = 0; k < 32; k++)
-                        if (k < cols) dst[k] = __uint_as_float(kb1 > kb0 ? r[k] : 0u) + (g.accumulate ? dst[k] : 0.0f);
+                    for (int k = 0; k < kStrip; k++)
+                        if (k == tgt) zt = z[k];
+                    if (here) g.target_logit[row] = zt;
+                }
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int k = 0; k < kStrip; k++)
+                    m4[k & 3] = fmaxf(m4[k & 3], z[k]);
+                const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                // (z - top) first: the largest term is exactly 1
+                const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+                for (int k = 0; k < kStrip; k++)
+                    s4[k & 3] += exp2_fast((z[k] - ref) * kLog2e);
+                if (live)
+                    g.part[((int64_t)w.nt * 2 + half) * g.m + row] = make_float2(top, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+            } else {
+                const int buf = unit & 1;
+                const bool some = w.kb1 > w.kb0;      // else nothing was accumulated, and nothing is waited for
+                if (some) {
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(acc_full + 8 * buf, (unit >> 1) & 1));
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    unit++;
+                }
+                float cf = 0.0f, base = 0.0f, alpha = 0.0f;
+                int64_t tgt = -1;
+                if constexpr (EPI == kEpiGrad) {
+                    if (live) {
+                        cf = g.coef[row];
+                        base = g.lse[row] * kLog2e;
+                        if (cf != 0.0f) tgt = g.targets[row] - g.b_y0 - col0;
+                    }
                 } else {
-                    uint16_t* dst = g.out + row * g.out_stride + col0 + c;
+                    alpha = g.head->alpha;
+                }
+#pragma unroll 1
+                for (int c = 0; c < kStrip; c += 32) {
+                    uint32_t r[32];
+                    if (some) {
+                        tc::tmem_ld32(src + buf * kBN + c, r);
+                        tc::tmem_ld_wait();
+                    } else {
 #pragma unroll
-                    for (int k = 0; k < 32; k++)
-                        if (k < cols) dst[k] = (uint16_t)from_f32<DT>(__uint_as_float(kb1 > kb0 ? r[k] : 0u) * alpha);
+                        for (int k = 0; k < 32; k++)
+                            r[k] = 0;
+                    }
+                    const int64_t left = g.n - col0 - c;          // columns that exist from here on
+                    if constexpr (EPI == kEpiGrad) {
+                        float p[32];
+#pragma unroll
+                        for (int k = 0; k < 32; k++)
+                            p[k] = exp2_fast(fmaf(__uint_as_float(r[k]), kLog2e, -base));
+                        if (__any_sync(0xffffffffu, tgt >= c && tgt < c + 32)) {
+#pragma unroll
+                            for (int k = 0; k < 32; k++)
+                                if (tgt == c + k) p[k] -= 1.0f;
+                        }
+                        uint32_t h[16];
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            const float a = cf != 0.0f && k < left ? p[k] * cf : 0.0f;
+                            const float b = cf != 0.0f && k + 1 < left ? p[k + 1] * cf : 0.0f;
+                            h[k / 2] = from_f32x2<DT>(a, b);
+                        }
+                        if (live) {
+                            uint4* dst = reinterpret_cast<uint4*>(g.g + row * g.g_stride + col0 + c);
+#pragma unroll
+                            for (int k = 0; k < 4; k++)
+                                dst[k] = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
+                        }
+                    } else if (live && left > 0) {
+                        if (g.acc) {
+                            float* dst = g.acc + ((int64_t)w.split * g.m + row) * g.n + col0 + c;
+#pragma unroll
+                            for (int k = 0; k < 32; k++)
+                                if (k < left) dst[k] = __uint_as_float(r[k]) + (g.accumulate ? dst[k] : 0.0f);
+                        } else {
+                            uint16_t* dst = g.out + row * g.out_stride + col0 + c;
+#pragma unroll
+                            for (int k = 0; k < 32; k++)
+                                if (k < left) dst[k] = (uint16_t)from_f32<DT>(__uint_as_float(r[k]) * alpha);
+                        }
+                    }
+                }
+                if (some) {
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_leader(acc_empty + 8 * buf);
                 }
             }
         }
+        if (!ok && lane == 0) atomicOr(&g.head->err, 1u);
     }
+    __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
+    tc::cluster_sync();
     tc::fence_after_sync();
-    if (warp == 1) tc::tmem_free(tmem, kBN);
+    if (warp == 1) tc::tmem_free(tmem, 2 * kBN);
 }
 
 // Per token: the strips' maxima and sums joined, in strip order; the loss.
@@ -373,7 +507,7 @@ CeLayout layout_of(const zero_ce_plan_t& p)
     l.part = l.target_logit + up256(p.tokens * 4);
     l.g = l.part;                                     // the two passes do not meet
     l.acc = l.g + up256(p.tokens * p.piece * 2);
-    const int64_t fwd = l.part + ceil_div(p.vocab, kBN) * p.tokens * 8;
+    const int64_t fwd = l.part + ceil_div(p.vocab, kBN) * 2 * p.tokens * 8;
     const int64_t bwd = l.acc + (int64_t)p.splits * p.tokens * p.hidden * 4;
     l.end = up256(fwd > bwd ? fwd : bwd);
     return l;
@@ -421,14 +555,23 @@ bool make_map(CUtensorMap* map, int dtype, const void* base, int64_t rows, int64
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+int sm_count()
+{
+    int dev = 0, n = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n > 1 ? n : 152;
+}
+
 template <int EPI, int DT, bool A_MN, bool B_MN>
 cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t s)
 {
     const void* k = (const void*)k_ce_gemm<EPI, DT, A_MN, B_MN>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kCeSmem);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)((int64_t)g.m_tiles * g.n_tiles * g.splits);
-    k_ce_gemm<EPI, DT, A_MN, B_MN><<<grid, kCeThreads, kCeSmem, s>>>(g);
+    const int64_t tiles = (int64_t)g.m_tiles * g.n_tiles * g.splits;
+    const int64_t pairs = sm_count() / 2;
+    k_ce_gemm<EPI, DT, A_MN, B_MN><<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), kCeThreads, kCeSmem, s>>>(g);
     return cudaGetLastError();
 }
 
@@ -483,7 +626,7 @@ zero_status_t zero_ce_plan(int64_t tokens, int64_t vocab, int64_t hidden, int32_
     int64_t best = 1;
     double cost = 1e30;
     for (int64_t s = 1; s <= 32 && s * 8 <= blocks; s++) {
-        const double c = (double)ceil_div(tiles * s, 152) / (double)s * (1.0 + 0.01 * (double)s);
+        const double c = (double)ceil_div(tiles * s, 76) / (double)s * (1.0 + 0.01 * (double)s);
         if (c < cost * 0.97) {
             cost = c;
             best = s;
@@ -518,8 +661,8 @@ zero_status_t zero_ce_forward(const zero_ce_plan_t* plan, const void* x, const v
         const CeLayout l = layout_of(p);
         GemmArgs g;
         std::memset(&g, 0, sizeof g);
-        if (!make_map(&g.a, p.dtype, x, p.tokens, p.hidden, p.x_stride, kBM) ||
-            !make_map(&g.b, p.dtype, w, p.vocab, p.hidden, p.w_stride, kBN))
+        if (!make_map(&g.a, p.dtype, x, p.tokens, p.hidden, p.x_stride, kBM / 2) ||
+            !make_map(&g.b, p.dtype, w, p.vocab, p.hidden, p.w_stride, kBN / 2))
             return set_error(ZERO_ECUDA, "zero_ce_forward: cuTensorMapEncodeTiled refused a buffer");
         g.m = p.tokens;
         g.n = p.vocab;
@@ -535,7 +678,7 @@ zero_status_t zero_ce_forward(const zero_ce_plan_t* plan, const void* x, const v
         g.withhold = std::getenv("ZERO_TEST_WITHHOLD_TILE") != nullptr;
         e = gemm<kEpiLse, false, false>(p.dtype, g, s);
         if (e == cudaSuccess) {
-            k_ce_join<<<(unsigned)ceil_div(p.tokens, 128), 128, 0, s>>>(g.head, g.part, g.n_tiles, p.tokens, targets,
+            k_ce_join<<<(unsigned)ceil_div(p.tokens, 128), 128, 0, s>>>(g.head, g.part, 2 * g.n_tiles, p.tokens, targets,
                                                                         p.vocab, g.target_logit, loss, lse);
             e = cudaGetLastError();
         }
@@ -582,8 +725,8 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
         const int64_t nv = p.vocab - v0 < p.piece ? p.vocab - v0 : p.piece;
         GemmArgs g;
         std::memset(&g, 0, sizeof g);
-        bool ok = make_map(&g.a, p.dtype, x, p.tokens, p.hidden, p.x_stride, kBM) &&
-                  make_map(&g.b, p.dtype, w, p.vocab, p.hidden, p.w_stride, kBN);
+        bool ok = make_map(&g.a, p.dtype, x, p.tokens, p.hidden, p.x_stride, kBM / 2) &&
+                  make_map(&g.b, p.dtype, w, p.vocab, p.hidden, p.w_stride, kBN / 2);
         g.m = p.tokens;
         g.n = nv;
         g.m_tiles = (int)ceil_div(p.tokens, kBM);
@@ -600,7 +743,7 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
         g.g_stride = p.piece;
         if (ok) e = gemm<kEpiGrad, false, false>(p.dtype, g, s);
         if (ok && dx && e == cudaSuccess) {          // dx += G w
-            ok = make_map(&g.a, p.dtype, G, p.tokens, p.piece, p.piece, kBM) &&
+            ok = make_map(&g.a, p.dtype, G, p.tokens, p.piece, p.piece, kBM / 2) &&
                  make_map(&g.b, p.dtype, w, p.vocab, p.hidden, p.w_stride, 64);
             g.n = p.hidden;
             g.n_tiles = (int)ceil_div(p.hidden, kBN);
