@@ -18,45 +18,43 @@ constexpr int kStages = 6;
 constexpr int kABytes = kBM / 2 * kBK * 2, kBBytes = kBN / 2 * kBK * 2;   // one CTA's part of a stage
 constexpr int kEpiWarps = 8;
 constexpr int kCeThreads = 64 + 32 * kEpiWarps;       // copying warp, issuing warp, epilogue warps
-constexpr int kCeSmem = kStages * (kABytes + kBBytes) + 1024;
+constexpr int kOutBytes = 4096;                       // an epilogue warp's box of results: 32 rows of 128 bytes
+constexpr int kCeSmem = kStages * (kABytes + kBBytes) + kEpiWarps * kOutBytes + 1024;
 constexpr int kStrip = kBN / 2;                       // vocabulary entries per (maximum, sum)
 constexpr int kChunk = 16;                            // loss: K-blocks the tensor cores add up by themselves
 constexpr int kGroup = 8;                             // row tiles that share the column tiles in L2
 constexpr float kLog2e = 1.4426950408889634f;
 
-enum { kEpiLse, kEpiGrad, kEpiAcc };
+// Epilogues: softmax statistics; G; binary32 sums; 16-bit results times alpha.
+enum { kEpiLse, kEpiGrad, kEpiAcc, kEpiOut };
 
 // Workspace head.
 struct CeHead {
     uint32_t err;                // a bounded wait ran out
     float alpha;                 // gradients are alpha times the products with G
-    uint32_t pad[62];
+    uint32_t joined;             // blocks of k_ce_join that are done
+    uint32_t pad[61];
 };
 
 struct GemmArgs {
     CUtensorMap a, b;
+    CUtensorMap c;               // results: G, binary32 sums or rounded gradients
     int64_t m, n;                // rows, columns of the product that exist
     int m_tiles, n_tiles;
     int k_blocks;                // K-blocks in all
-    int splits;                  // parts of the K-blocks, one output each (kEpiAcc)
-    int b_y0;                    // logits: first vocabulary entry of the piece
+    int splits;                  // parts of the K-blocks, one result each (kEpiAcc), m_tiles * kBM rows apart
+    int b_y0;                    // first vocabulary entry of the piece
+    int accumulate;              // kEpiAcc: added to what is there
+    int withhold;                // test hook: the first copy is announced but not made, so the waits run out
     CeHead* head;
     const int64_t* targets;
-    int64_t vocab;
-    // kEpiLse
-    float2* part;                // [strips][m]: a strip's maximum and sum
-    float* target_logit;         // [m]
-    // kEpiGrad
-    const float* lse;
-    const float* coef;           // row factors of G, 0: no loss
-    uint16_t* g;
-    int64_t g_stride;
-    // kEpiAcc
-    float* acc;                  // binary32 output [splits][m][n], or
-    int accumulate;              //   added to it
-    uint16_t* out;               // rounded output, times alpha
+    float2* part;                // kEpiLse: [strips][m], a strip's maximum and sum
+    float* target_logit;         //   [m]
+    const float* lse;            // kEpiGrad
+    const float* coef;           //   row factors of G, 0: no loss
+    int64_t c_cols;              //   columns of G in memory
+    uint16_t* out;               // kEpiOut: stored from registers, when a row's end is not on 16 bytes (else NULL)
     int64_t out_stride;
-    int withhold;                // test hook: the first copy is announced but not made, so the waits run out
 };
 
 __device__ __forceinline__ float exp2_fast(float x)
@@ -218,6 +216,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
         const int band = warp & 3;                    // the warp's 32 lanes of tensor memory
         const int half = (warp - 2) >> 2;             // and its 128 columns
         const uint32_t src = tmem + ((uint32_t)(band * 32) << 16) + half * kStrip;
+        const uint32_t box = sm + kStages * (kABytes + kBBytes) + (warp - 2) * kOutBytes;
         int unit = 0;
         bool ok = true;
         for (int64_t t = first; t < tiles && ok; t += stride) {
@@ -297,65 +296,96 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
                         base = g.lse[row] * kLog2e;
                         if (cf != 0.0f) tgt = g.targets[row] - g.b_y0 - col0;
                     }
-                } else {
+                } else if constexpr (EPI == kEpiOut) {
                     alpha = g.head->alpha;
                 }
-#pragma unroll 1
-                for (int c = 0; c < kStrip; c += 32) {
-                    uint32_t r[32];
+                // all of the warp's columns into registers, and tensor memory is free again
+                float z[kStrip];
+#pragma unroll
+                for (int q = 0; q < kStrip / 32; q++) {
+                    uint32_t* r = reinterpret_cast<uint32_t*>(z) + 32 * q;
                     if (some) {
-                        tc::tmem_ld32(src + buf * kBN + c, r);
-                        tc::tmem_ld_wait();
+                        tc::tmem_ld32(src + buf * kBN + 32 * q, r);
                     } else {
 #pragma unroll
                         for (int k = 0; k < 32; k++)
                             r[k] = 0;
                     }
-                    const int64_t left = g.n - col0 - c;          // columns that exist from here on
-                    if constexpr (EPI == kEpiGrad) {
-                        float p[32];
-#pragma unroll
-                        for (int k = 0; k < 32; k++)
-                            p[k] = exp2_fast(fmaf(__uint_as_float(r[k]), kLog2e, -base));
-                        if (__any_sync(0xffffffffu, tgt >= c && tgt < c + 32)) {
-#pragma unroll
-                            for (int k = 0; k < 32; k++)
-                                if (tgt == c + k) p[k] -= 1.0f;
-                        }
-                        uint32_t h[16];
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2) {
-                            const float a = cf != 0.0f && k < left ? p[k] * cf : 0.0f;
-                            const float b = cf != 0.0f && k + 1 < left ? p[k + 1] * cf : 0.0f;
-                            h[k / 2] = from_f32x2<DT>(a, b);
-                        }
-                        if (live) {
-                            uint4* dst = reinterpret_cast<uint4*>(g.g + row * g.g_stride + col0 + c);
-#pragma unroll
-                            for (int k = 0; k < 4; k++)
-                                dst[k] = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
-                        }
-                    } else if (live && left > 0) {
-                        if (g.acc) {
-                            float* dst = g.acc + ((int64_t)w.split * g.m + row) * g.n + col0 + c;
-#pragma unroll
-                            for (int k = 0; k < 32; k++)
-                                if (k < left) dst[k] = __uint_as_float(r[k]) + (g.accumulate ? dst[k] : 0.0f);
-                        } else {
-                            uint16_t* dst = g.out + row * g.out_stride + col0 + c;
-#pragma unroll
-                            for (int k = 0; k < 32; k++)
-                                if (k < left) dst[k] = (uint16_t)from_f32<DT>(__uint_as_float(r[k]) * alpha);
-                        }
-                    }
                 }
                 if (some) {
+                    tc::tmem_ld_wait();
                     tc::fence_before_sync();
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive_leader(acc_empty + 8 * buf);
                 }
+                if constexpr (EPI == kEpiGrad) {
+#pragma unroll
+                    for (int k = 0; k < kStrip; k++)
+                        z[k] = exp2_fast(fmaf(z[k], kLog2e, -base));
+                    if (__any_sync(0xffffffffu, tgt >= 0 && tgt < kStrip)) {
+#pragma unroll
+                        for (int k = 0; k < kStrip; k++)
+                            if (k == tgt) z[k] -= 1.0f;
+                    }
+                    const int64_t left = g.n - col0;  // columns that exist
+                    if (left < kStrip) {
+#pragma unroll
+                        for (int k = 0; k < kStrip; k++)
+                            if (k >= left) z[k] = 0.0f;
+                    }
+#pragma unroll
+                    for (int k = 0; k < kStrip; k++)
+                        z[k] *= cf;
+                } else if constexpr (EPI == kEpiOut) {
+#pragma unroll
+                    for (int k = 0; k < kStrip; k++)
+                        z[k] *= alpha;
+                }
+                const uint32_t keep = EPI == kEpiGrad && cf == 0.0f ? 0u : 0xffffffffu;   // 0 whatever the logit
+                const int row0 = w.mt * kBM + (int)rank * (kBM / 2) + band * 32;
+                if (EPI == kEpiOut && g.out) {
+                    // rows that do not end on a 16-byte unit, which is what a tiled copy writes
+                    if (live)
+#pragma unroll
+                        for (int k = 0; k < kStrip; k++)
+                            if (col0 + k < g.n) g.out[row * g.out_stride + col0 + k] = (uint16_t)from_f32<DT>(z[k]);
+                    continue;
+                }
+                // the warp's box: 32 rows of 128 bytes with the copy's swizzle (16-byte
+                // unit j of row i at j ^ (i & 7): no bank conflicts); one copy out per box
+                const int y = row0 + (EPI == kEpiAcc ? w.split * g.m_tiles * kBM : 0);
+                constexpr int kCols = EPI == kEpiAcc ? 32 : 64;       // columns of a box
+#pragma unroll
+                for (int c = 0; c < kStrip; c += kCols) {
+                    if (lane == 0) tc::bulk_wait_read();
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 8; k++) {
+                        const uint32_t at = box + lane * 128 + ((k ^ (lane & 7)) << 4);
+                        if constexpr (EPI == kEpiAcc) {
+                            const float* p = z + c + 4 * k;
+                            tc::st_shared16(at, __float_as_uint(p[0]), __float_as_uint(p[1]), __float_as_uint(p[2]),
+                                            __float_as_uint(p[3]));
+                        } else {
+                            const float* p = z + c + 8 * k;
+                            tc::st_shared16(at, from_f32x2<DT>(p[0], p[1]) & keep, from_f32x2<DT>(p[2], p[3]) & keep,
+                                            from_f32x2<DT>(p[4], p[5]) & keep, from_f32x2<DT>(p[6], p[7]) & keep);
+                        }
+                    }
+                    tc::fence_async_shared();
+                    __syncwarp();
+                    const int64_t x = col0 + c;
+                    if (lane == 0 && row0 < g.m && x < (EPI == kEpiGrad ? g.c_cols : g.n)) {
+                        if (EPI == kEpiAcc && g.accumulate)
+                            tc::tma_add(&g.c, (int)x, y, box);
+                        else
+                            tc::tma_store(&g.c, (int)x, y, box);
+                        tc::bulk_commit();
+                    }
+                }
             }
         }
+        if (lane == 0) tc::bulk_wait_all();
         if (!ok && lane == 0) atomicOr(&g.head->err, 1u);
     }
     __syncwarp();
@@ -366,57 +396,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
     if (warp == 1) tc::tmem_free(tmem, 2 * kBN);
 }
 
-// Per token: the strips' maxima and sums joined, in strip order; the loss.
-__global__ void __launch_bounds__(128) k_ce_join(const CeHead* head, const float2* part, int strips, int64_t n,
-                                                 const int64_t* targets, int64_t vocab, const float* target_logit,
-                                                 float* loss, float* lse)
+// Per token: the strips' maxima and sums joined, in a fixed order (32 parts of
+// the strips, then the parts); the loss.  The last block to finish adds the
+// blocks' losses and counts, in block order.
+__global__ void __launch_bounds__(1024) k_ce_join(CeHead* head, const float2* part, int strips, int64_t n,
+                                                  const int64_t* targets, int64_t vocab, const float* target_logit,
+                                                  float* loss, float* lse, float2* block_total, float* total)
 {
-    const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
-    if (i >= n) return;
-    float mx = -INFINITY;
-    for (int s = 0; s < strips; s++)
-        mx = fmaxf(mx, part[(int64_t)s * n + i].x);
-    float sum = 0.0f;
-    const float ref = mx == -INFINITY ? 0.0f : mx;
-    for (int s = 0; s < strips; s++) {
-        const float2 p = part[(int64_t)s * n + i];
-        sum = fmaf(p.y, exp2f((p.x - ref) * kLog2e), sum);
-    }
-    float l = ref + logf(sum);
-    if (head->err) l = NAN;
-    lse[i] = l;
-    const int64_t t = targets[i];
-    loss[i] = t >= 0 && t < vocab ? l - target_logit[i] : 0.0f;
-}
-
-// One block: mean loss over the tokens that have one, and their number.
-__global__ void __launch_bounds__(1024) k_ce_total(const float* loss, const int64_t* targets, int64_t n, int64_t vocab,
-                                                   float* total)
-{
-    __shared__ float ss[1024];
-    __shared__ int64_t sc[1024];
-    float s = 0.0f;
-    int64_t c = 0;
-    for (int64_t i = threadIdx.x; i < n; i += 1024) {
-        const int64_t t = targets[i];
-        if (t >= 0 && t < vocab) {
-            s += loss[i];
-            c++;
+    __shared__ float2 sh[32][33];
+    __shared__ uint32_t last;
+    const int tok = threadIdx.x & 31, p = threadIdx.x >> 5;
+    const int64_t i = (int64_t)blockIdx.x * 32 + tok;
+    float mx = -INFINITY, sum = 0.0f;
+    if (i < n)
+        for (int s = p; s < strips; s += 32) {
+            const float2 q = part[(int64_t)s * n + i];
+            const float top = fmaxf(mx, q.x), ref = top == -INFINITY ? 0.0f : top;
+            sum = fmaf(sum, exp2f((mx - ref) * kLog2e), q.y * exp2f((q.x - ref) * kLog2e));
+            mx = top;
         }
-    }
-    ss[threadIdx.x] = s;
-    sc[threadIdx.x] = c;
+    sh[p][tok] = make_float2(mx, sum);
     __syncthreads();
-    for (int o = 512; o > 0; o >>= 1) {
-        if (threadIdx.x < o) {
-            ss[threadIdx.x] += ss[threadIdx.x + o];
-            sc[threadIdx.x] += sc[threadIdx.x + o];
+    if (p == 0) {
+        for (int s = 1; s < 32; s++)
+            mx = fmaxf(mx, sh[s][tok].x);
+        const float ref = mx == -INFINITY ? 0.0f : mx;
+        sum = 0.0f;
+        for (int s = 0; s < 32; s++)
+            sum = fmaf(sh[s][tok].y, exp2f((sh[s][tok].x - ref) * kLog2e), sum);
+        float l = ref + logf(sum), li = 0.0f, ci = 0.0f;
+        if (head->err) l = NAN;
+        if (i < n) {
+            lse[i] = l;
+            const int64_t t = targets[i];
+            if (t >= 0 && t < vocab) {
+                li = l - target_logit[i];
+                ci = 1.0f;
+            }
+            loss[i] = li;
         }
-        __syncthreads();
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            li += __shfl_down_sync(0xffffffffu, li, o);
+            ci += __shfl_down_sync(0xffffffffu, ci, o);
+        }
+        if (tok == 0) {
+            block_total[blockIdx.x] = make_float2(li, ci);
+            __threadfence();
+            last = atomicAdd(&head->joined, 1u) == gridDim.x - 1;
+        }
     }
+    __syncthreads();
+    if (!last || !total) return;
+    __threadfence();
+    float s = 0.0f, c = 0.0f;
+    for (unsigned k = threadIdx.x; k < gridDim.x; k += 1024) {
+        const float2 q = __ldcg(block_total + k);
+        s += q.x;
+        c += q.y;                                     // at most 2^24 tokens: exact
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        s += __shfl_down_sync(0xffffffffu, s, o);
+        c += __shfl_down_sync(0xffffffffu, c, o);
+    }
+    if (tok == 0) sh[0][p] = make_float2(s, c);
+    __syncthreads();
     if (threadIdx.x == 0) {
-        total[0] = sc[0] ? ss[0] / (float)sc[0] : 0.0f;
-        total[1] = (float)sc[0];
+        for (int k = 1; k < 32; k++) {
+            s += sh[0][k].x;
+            c += sh[0][k].y;
+        }
+        total[0] = c > 0.0f ? s / c : 0.0f;
+        total[1] = c;
     }
 }
 
@@ -461,18 +513,31 @@ __global__ void __launch_bounds__(1024) k_ce_factors(CeHead* head, const int64_t
     }
 }
 
-// dx = alpha times the sum of the splits, rounded.
+// dx = alpha times the sum of the splits, rounded: 4 columns a thread, a row
+// a blockIdx.y stride.
 template <int DT>
-__global__ void __launch_bounds__(256) k_ce_dx(const CeHead* head, const float* acc, int splits, int64_t m, int64_t n,
-                                               uint16_t* dx, int64_t stride)
+__global__ void __launch_bounds__(256) k_ce_dx(const CeHead* head, const float* acc, int splits, int64_t split_stride,
+                                               int64_t m, int64_t n, int64_t acc_cols, uint16_t* dx, int64_t stride)
 {
     const float alpha = head->err ? NAN : head->alpha;
-    const int64_t total = m * n;
-    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
-        float s = 0.0f;
-        for (int k = 0; k < splits; k++)
-            s += acc[(int64_t)k * total + e];
-        dx[e / n * stride + e % n] = (uint16_t)from_f32<DT>(s * alpha);
+    const int64_t c = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+    if (c >= n) return;
+    for (int64_t i = blockIdx.y; i < m; i += gridDim.y) {
+        const float* src = acc + i * acc_cols + c;
+        float4 s = __ldcs(reinterpret_cast<const float4*>(src));
+        for (int k = 1; k < splits; k++) {
+            const float4 q = __ldcs(reinterpret_cast<const float4*>(src + k * split_stride));
+            s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
+        }
+        const uint2 h = make_uint2(from_f32x2<DT>(s.x * alpha, s.y * alpha), from_f32x2<DT>(s.z * alpha, s.w * alpha));
+        uint16_t* dst = dx + i * stride + c;
+        if (c + 4 <= n) {
+            *reinterpret_cast<uint2*>(dst) = h;
+        } else {
+            dst[0] = (uint16_t)h.x;
+            if (c + 1 < n) dst[1] = (uint16_t)(h.x >> 16);
+            if (c + 2 < n) dst[2] = (uint16_t)h.y;
+        }
     }
 }
 
@@ -496,7 +561,8 @@ zero_status_t cuda_failed(cudaError_t e, const char* what)
 
 // Byte offsets in the workspace.
 struct CeLayout {
-    int64_t coef, target_logit, part, g, acc, end;
+    int64_t coef, target_logit, block_total, part, g, acc, end;
+    int64_t acc_rows, acc_cols;                       // of one split's binary32 sums
 };
 
 CeLayout layout_of(const zero_ce_plan_t& p)
@@ -504,11 +570,14 @@ CeLayout layout_of(const zero_ce_plan_t& p)
     CeLayout l;
     l.coef = sizeof(CeHead);
     l.target_logit = l.coef + up256(p.tokens * 4);
-    l.part = l.target_logit + up256(p.tokens * 4);
+    l.block_total = l.target_logit + up256(p.tokens * 4);
+    l.part = l.block_total + up256(ceil_div(p.tokens, 32) * 8);
     l.g = l.part;                                     // the two passes do not meet
     l.acc = l.g + up256(p.tokens * p.piece * 2);
     const int64_t fwd = l.part + ceil_div(p.vocab, kBN) * 2 * p.tokens * 8;
-    const int64_t bwd = l.acc + (int64_t)p.splits * p.tokens * p.hidden * 4;
+    l.acc_rows = ceil_div(p.tokens, kBM) * kBM;
+    l.acc_cols = (p.hidden + 3) / 4 * 4;
+    const int64_t bwd = l.acc + p.splits * l.acc_rows * l.acc_cols * 4;
     l.end = up256(fwd > bwd ? fwd : bwd);
     return l;
 }
@@ -542,17 +611,23 @@ EncodeFn encode_fn()
     return fn;
 }
 
-// rows x cols 16-bit values, `stride` values between rows; boxes of 64
+// rows x cols values, `stride` values between rows; boxes of 128 bytes of
 // columns x box_rows rows, 128-byte swizzle; zeros outside.
-bool make_map(CUtensorMap* map, int dtype, const void* base, int64_t rows, int64_t cols, int64_t stride, int box_rows)
+bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t rows, int64_t cols, int64_t stride,
+              int box_rows)
 {
+    const int e = type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, step[2] = {1, 1};
-    return encode_fn()(map, dtype == ZERO_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-                       const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const cuuint64_t strides[1] = {(cuuint64_t)stride * e};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / e), (cuuint32_t)box_rows}, step[2] = {1, 1};
+    return encode_fn()(map, type, 2, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+CUtensorMapDataType map_type(int dtype)
+{
+    return dtype == ZERO_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
 
 int sm_count()
@@ -659,10 +734,11 @@ zero_status_t zero_ce_forward(const zero_ce_plan_t* plan, const void* x, const v
     if (p.tokens) {
         if (!encode_fn()) return set_error(ZERO_ECUDA, "zero_ce_forward: the driver has no cuTensorMapEncodeTiled");
         const CeLayout l = layout_of(p);
+        const CUtensorMapDataType type = map_type(p.dtype);
         GemmArgs g;
         std::memset(&g, 0, sizeof g);
-        if (!make_map(&g.a, p.dtype, x, p.tokens, p.hidden, p.x_stride, kBM / 2) ||
-            !make_map(&g.b, p.dtype, w, p.vocab, p.hidden, p.w_stride, kBN / 2))
+        if (!make_map(&g.a, type, x, p.tokens, p.hidden, p.x_stride, kBM / 2) ||
+            !make_map(&g.b, type, w, p.vocab, p.hidden, p.w_stride, kBN / 2))
             return set_error(ZERO_ECUDA, "zero_ce_forward: cuTensorMapEncodeTiled refused a buffer");
         g.m = p.tokens;
         g.n = p.vocab;
@@ -672,20 +748,18 @@ zero_status_t zero_ce_forward(const zero_ce_plan_t* plan, const void* x, const v
         g.splits = 1;
         g.head = reinterpret_cast<CeHead*>(ws);
         g.targets = targets;
-        g.vocab = p.vocab;
         g.part = reinterpret_cast<float2*>(ws + l.part);
         g.target_logit = reinterpret_cast<float*>(ws + l.target_logit);
         g.withhold = std::getenv("ZERO_TEST_WITHHOLD_TILE") != nullptr;
         e = gemm<kEpiLse, false, false>(p.dtype, g, s);
         if (e == cudaSuccess) {
-            k_ce_join<<<(unsigned)ceil_div(p.tokens, 128), 128, 0, s>>>(g.head, g.part, 2 * g.n_tiles, p.tokens, targets,
-                                                                        p.vocab, g.target_logit, loss, lse);
+            k_ce_join<<<(unsigned)ceil_div(p.tokens, 32), 1024, 0, s>>>(
+                g.head, g.part, 2 * g.n_tiles, p.tokens, targets, p.vocab, g.target_logit, loss, lse,
+                reinterpret_cast<float2*>(ws + l.block_total), total);
             e = cudaGetLastError();
         }
-    }
-    if (e == cudaSuccess && total) {
-        k_ce_total<<<1, 1024, 0, s>>>(loss, targets, p.tokens, p.vocab, total);
-        e = cudaGetLastError();
+    } else if (total) {
+        e = cudaMemsetAsync(total, 0, 8, s);
     }
     return e == cudaSuccess ? ZERO_OK : cuda_failed(e, "zero_ce_forward");
 }
@@ -718,17 +792,20 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
     float* coef = reinterpret_cast<float*>(ws + l.coef);
     uint16_t* G = reinterpret_cast<uint16_t*>(ws + l.g);
     float* acc = reinterpret_cast<float*>(ws + l.acc);
+    const CUtensorMapDataType type = map_type(p.dtype);
     const float up = p.dtype == ZERO_FP16 ? 16384.0f : 1.0f;
     k_ce_factors<<<1, 1024, 0, s>>>(head, targets, p.tokens, p.vocab, dloss, grad_scale, up, coef);
     cudaError_t e = cudaGetLastError();
     for (int64_t v0 = 0; v0 < p.vocab && e == cudaSuccess; v0 += p.piece) {
         const int64_t nv = p.vocab - v0 < p.piece ? p.vocab - v0 : p.piece;
-        GemmArgs g;
+        GemmArgs g;                                  // G of the piece
         std::memset(&g, 0, sizeof g);
-        bool ok = make_map(&g.a, p.dtype, x, p.tokens, p.hidden, p.x_stride, kBM / 2) &&
-                  make_map(&g.b, p.dtype, w, p.vocab, p.hidden, p.w_stride, kBN / 2);
+        bool ok = make_map(&g.a, type, x, p.tokens, p.hidden, p.x_stride, kBM / 2) &&
+                  make_map(&g.b, type, w, p.vocab, p.hidden, p.w_stride, kBN / 2) &&
+                  make_map(&g.c, type, G, p.tokens, p.piece, p.piece, 32);
         g.m = p.tokens;
         g.n = nv;
+        g.c_cols = p.piece;
         g.m_tiles = (int)ceil_div(p.tokens, kBM);
         g.n_tiles = (int)ceil_div(nv, kBN);
         g.k_blocks = (int)ceil_div(p.hidden, kBK);
@@ -736,45 +813,45 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
         g.b_y0 = (int)v0;
         g.head = head;
         g.targets = targets;
-        g.vocab = p.vocab;
         g.lse = lse;
         g.coef = coef;
-        g.g = G;
-        g.g_stride = p.piece;
         if (ok) e = gemm<kEpiGrad, false, false>(p.dtype, g, s);
+        g.n = p.hidden;
+        g.n_tiles = (int)ceil_div(p.hidden, kBN);
         if (ok && dx && e == cudaSuccess) {          // dx += G w
-            ok = make_map(&g.a, p.dtype, G, p.tokens, p.piece, p.piece, kBM / 2) &&
-                 make_map(&g.b, p.dtype, w, p.vocab, p.hidden, p.w_stride, 64);
-            g.n = p.hidden;
-            g.n_tiles = (int)ceil_div(p.hidden, kBN);
+            ok = make_map(&g.a, type, G, p.tokens, p.piece, p.piece, kBM / 2) &&
+                 make_map(&g.b, type, w, p.vocab, p.hidden, p.w_stride, 64) &&
+                 make_map(&g.c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, acc, p.splits * l.acc_rows, l.acc_cols, l.acc_cols, 32);
             g.k_blocks = (int)ceil_div(nv, kBK);
             g.splits = p.splits;
-            g.acc = acc;
             g.accumulate = v0 > 0;
             if (ok) e = gemm<kEpiAcc, false, true>(p.dtype, g, s);
         }
         if (ok && dw && e == cudaSuccess) {          // dw = G^T x
-            ok = make_map(&g.a, p.dtype, G, p.tokens, p.piece, p.piece, 64) &&
-                 make_map(&g.b, p.dtype, x, p.tokens, p.hidden, p.x_stride, 64);
+            ok = make_map(&g.a, type, G, p.tokens, p.piece, p.piece, 64) &&
+                 make_map(&g.b, type, x, p.tokens, p.hidden, p.x_stride, 64) &&
+                 make_map(&g.c, type, static_cast<uint16_t*>(dw) + v0 * p.w_stride, nv, p.hidden, p.w_stride, 32);
             g.b_y0 = 0;
             g.m = nv;
-            g.n = p.hidden;
             g.m_tiles = (int)ceil_div(nv, kBM);
-            g.n_tiles = (int)ceil_div(p.hidden, kBN);
             g.k_blocks = (int)ceil_div(p.tokens, kBK);
             g.splits = 1;
-            g.acc = nullptr;
-            g.out = static_cast<uint16_t*>(dw) + v0 * p.w_stride;
-            g.out_stride = p.w_stride;
-            if (ok) e = gemm<kEpiAcc, true, true>(p.dtype, g, s);
+            if (p.hidden % 8) {
+                g.out = static_cast<uint16_t*>(dw) + v0 * p.w_stride;
+                g.out_stride = p.w_stride;
+            }
+            if (ok) e = gemm<kEpiOut, true, true>(p.dtype, g, s);
         }
         if (!ok) return set_error(ZERO_ECUDA, "zero_ce_backward: cuTensorMapEncodeTiled refused a buffer");
     }
     if (dx && e == cudaSuccess) {
+        const dim3 grid((unsigned)ceil_div(l.acc_cols, 1024), (unsigned)(p.tokens < 4096 ? p.tokens : 4096));
+        uint16_t* out = static_cast<uint16_t*>(dx);
+        const int64_t apart = l.acc_rows * l.acc_cols;
         if (p.dtype == ZERO_BF16)
-            k_ce_dx<kBF16><<<152 * 8, 256, 0, s>>>(head, acc, p.splits, p.tokens, p.hidden, static_cast<uint16_t*>(dx), p.x_stride);
+            k_ce_dx<kBF16><<<grid, 256, 0, s>>>(head, acc, p.splits, apart, p.tokens, p.hidden, l.acc_cols, out, p.x_stride);
         else
-            k_ce_dx<kF16><<<152 * 8, 256, 0, s>>>(head, acc, p.splits, p.tokens, p.hidden, static_cast<uint16_t*>(dx), p.x_stride);
+            k_ce_dx<kF16><<<grid, 256, 0, s>>>(head, acc, p.splits, apart, p.tokens, p.hidden, l.acc_cols, out, p.x_stride);
         e = cudaGetLastError();
     }
     return e == cudaSuccess ? ZERO_OK : cuda_failed(e, "zero_ce_backward");
