@@ -595,7 +595,7 @@ typedef struct zero_ce_plan {
 } zero_ce_plan_t;
 
 /* Host only.  strides 0: hidden (then a multiple of 8); piece 0: chosen so
- * that G takes about 256 MiB, else rounded up to a multiple of 256.  tokens
+ * that G takes about 512 MiB, else rounded up to a multiple of 256.  tokens
  * >= 0, vocab >= 1, hidden >= 1.  Errors: ZERO_EINVAL, ZERO_EALIGN (a stride
  * that is not a multiple of 8), ZERO_EUNSUPPORTED. */
 zero_status_t zero_ce_plan(int64_t tokens, int64_t vocab, int64_t hidden, int32_t dtype, int64_t x_stride,

@@ -124,6 +124,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
     __syncthreads();
     tc::cluster_sync();
     tc::fence_after_sync();
+    if (EPI == kEpiLse) allow_next_grid();            // the join: it waits for this grid
     const uint32_t tmem = s_tmem;
     const int64_t tiles = (int64_t)g.m_tiles * g.n_tiles * g.splits;
     const int64_t first = blockIdx.x >> 1, stride = gridDim.x >> 1;
@@ -396,62 +397,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
     if (warp == 1) tc::tmem_free(tmem, 2 * kBN);
 }
 
+// Join of (maximum, sum) pairs.
+__device__ __forceinline__ void merge(float& mx, float& sum, float2 q)
+{
+    const float top = fmaxf(mx, q.x), ref = top == -INFINITY ? 0.0f : top;
+    sum = fmaf(sum, exp2f((mx - ref) * kLog2e), q.y * exp2f((q.x - ref) * kLog2e));
+    mx = top;
+}
+
+struct JoinArgs {
+    CeHead* head;
+    const float2* part;          // [strips][n]
+    int strips;
+    int64_t n;
+    const int64_t* targets;
+    int64_t vocab;
+    const float* target_logit;
+    float* loss;
+    float* lse;
+    float2* block_total;
+    float* total;
+};
+
+// lse and loss of token i from its joined maximum and sum.
+__device__ __forceinline__ float2 finish_token(const JoinArgs& a, int64_t i, float mx, float sum)
+{
+    float l = (mx == -INFINITY ? 0.0f : mx) + logf(sum), li = 0.0f, ci = 0.0f;
+    if (a.head->err) l = NAN;
+    a.lse[i] = l;
+    const int64_t t = a.targets[i];
+    if (t >= 0 && t < a.vocab) {
+        li = l - __ldcg(a.target_logit + i);
+        ci = 1.0f;
+    }
+    a.loss[i] = li;
+    return make_float2(li, ci);
+}
+
 // Per token: the strips' maxima and sums joined, in a fixed order (32 parts of
 // the strips, then the parts); the loss.  The last block to finish adds the
 // blocks' losses and counts, in block order.
-__global__ void __launch_bounds__(1024) k_ce_join(CeHead* head, const float2* part, int strips, int64_t n,
-                                                  const int64_t* targets, int64_t vocab, const float* target_logit,
-                                                  float* loss, float* lse, float2* block_total, float* total)
+__global__ void __launch_bounds__(1024) k_ce_join(const __grid_constant__ JoinArgs a)
 {
+    wait_prev_grid();                                 // launched while the products drain
     __shared__ float2 sh[32][33];
     __shared__ uint32_t last;
     const int tok = threadIdx.x & 31, p = threadIdx.x >> 5;
     const int64_t i = (int64_t)blockIdx.x * 32 + tok;
     float mx = -INFINITY, sum = 0.0f;
-    if (i < n)
-        for (int s = p; s < strips; s += 32) {
-            const float2 q = part[(int64_t)s * n + i];
-            const float top = fmaxf(mx, q.x), ref = top == -INFINITY ? 0.0f : top;
-            sum = fmaf(sum, exp2f((mx - ref) * kLog2e), q.y * exp2f((q.x - ref) * kLog2e));
-            mx = top;
-        }
+    if (i < a.n)
+        for (int s = p; s < a.strips; s += 32)
+            merge(mx, sum, a.part[(int64_t)s * a.n + i]);
     sh[p][tok] = make_float2(mx, sum);
     __syncthreads();
     if (p == 0) {
         for (int s = 1; s < 32; s++)
-            mx = fmaxf(mx, sh[s][tok].x);
-        const float ref = mx == -INFINITY ? 0.0f : mx;
-        sum = 0.0f;
-        for (int s = 0; s < 32; s++)
-            sum = fmaf(sh[s][tok].y, exp2f((sh[s][tok].x - ref) * kLog2e), sum);
-        float l = ref + logf(sum), li = 0.0f, ci = 0.0f;
-        if (head->err) l = NAN;
-        if (i < n) {
-            lse[i] = l;
-            const int64_t t = targets[i];
-            if (t >= 0 && t < vocab) {
-                li = l - target_logit[i];
-                ci = 1.0f;
-            }
-            loss[i] = li;
-        }
+            merge(mx, sum, sh[s][tok]);
+        float2 r = make_float2(0.0f, 0.0f);
+        if (i < a.n) r = finish_token(a, i, mx, sum);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            li += __shfl_down_sync(0xffffffffu, li, o);
-            ci += __shfl_down_sync(0xffffffffu, ci, o);
+            r.x += __shfl_down_sync(0xffffffffu, r.x, o);
+            r.y += __shfl_down_sync(0xffffffffu, r.y, o);
         }
         if (tok == 0) {
-            block_total[blockIdx.x] = make_float2(li, ci);
+            a.block_total[blockIdx.x] = r;
             __threadfence();
-            last = atomicAdd(&head->joined, 1u) == gridDim.x - 1;
+            last = atomicAdd(&a.head->joined, 1u) == gridDim.x - 1;
         }
     }
     __syncthreads();
-    if (!last || !total) return;
+    if (!last || !a.total) return;
     __threadfence();
     float s = 0.0f, c = 0.0f;
     for (unsigned k = threadIdx.x; k < gridDim.x; k += 1024) {
-        const float2 q = __ldcg(block_total + k);
+        const float2 q = __ldcg(a.block_total + k);
         s += q.x;
         c += q.y;                                     // at most 2^24 tokens: exact
     }
@@ -467,8 +487,177 @@ __global__ void __launch_bounds__(1024) k_ce_join(CeHead* head, const float2* pa
             s += sh[0][k].x;
             c += sh[0][k].y;
         }
-        total[0] = c > 0.0f ? s / c : 0.0f;
-        total[1] = c;
+        a.total[0] = c > 0.0f ? s / c : 0.0f;
+        a.total[1] = c;
+    }
+}
+
+// ---- few tokens -------------------------------------------------------------------
+// Up to kFewTokens tokens: w is read once and that is the time (411 MB at
+// vocabulary 50257, hidden 4096), so no tensor cores: the tokens lie in shared
+// memory, a warp takes kFewRows rows of w at a time, its lanes 8 values each,
+// and keeps a running maximum and sum per token.  The last block joins the
+// blocks' pairs.  A lane has 256 bytes of w in flight.  Products and sums are
+// binary32 multiply-adds.
+constexpr int kFewTokens = 4, kFewRows = 4, kFewAhead = 4, kFewThreads = 256, kFewBlocks = 608;
+constexpr int kFewSmem = 64 * 1024;                   // all tokens' values, 16 bits each
+
+template <int DT>
+__device__ __forceinline__ void unpack8(uint4 v, float f[8])
+{
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const float2 p = to_f32x2<DT>(u[k]);
+        f[2 * k] = p.x;
+        f[2 * k + 1] = p.y;
+    }
+}
+
+template <int DT, int T>
+__global__ void __launch_bounds__(kFewThreads) k_ce_few(const uint16_t* x, int64_t x_stride, const uint16_t* w,
+                                                        int64_t w_stride, int64_t hidden, float2* part,
+                                                        float* target_logit, const __grid_constant__ JoinArgs a)
+{
+    extern __shared__ __align__(16) uint16_t xs[];    // [T][wide]
+    __shared__ float2 sh[kFewThreads / 32][T];
+    __shared__ uint32_t last;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wide = (int)((hidden + 7) / 8 * 8);
+    for (int k = threadIdx.x; k < T * wide; k += kFewThreads) {
+        const int t = k / wide, j = k - t * wide;
+        xs[k] = j < hidden ? x[t * x_stride + j] : (uint16_t)0;
+    }
+    __syncthreads();
+    int64_t tgt[T];
+    float mx[T], sum[T];
+#pragma unroll
+    for (int t = 0; t < T; t++) {
+        tgt[t] = a.targets[t];
+        mx[t] = -INFINITY;
+        sum[t] = 0.0f;
+    }
+    const int64_t warps = (int64_t)gridDim.x * (kFewThreads / 32), me = (int64_t)blockIdx.x * (kFewThreads / 32) + warp;
+    const int64_t lo = a.vocab * me / warps, hi = a.vocab * (me + 1) / warps;
+    for (int64_t v = lo; v < hi; v += kFewRows) {
+        float acc[kFewRows][T];
+#pragma unroll
+        for (int q = 0; q < kFewRows; q++)
+#pragma unroll
+            for (int t = 0; t < T; t++)
+                acc[q][t] = 0.0f;
+        const uint16_t* row[kFewRows];
+#pragma unroll
+        for (int q = 0; q < kFewRows; q++)
+            row[q] = w + min(v + q, hi - 1) * w_stride;
+        auto add = [&](const uint4 r[kFewRows], int j) {
+            float wv[kFewRows][8];
+#pragma unroll
+            for (int q = 0; q < kFewRows; q++)
+                unpack8<DT>(r[q], wv[q]);
+#pragma unroll
+            for (int t = 0; t < T; t++) {
+                float xv[8];
+                unpack8<DT>(*reinterpret_cast<const uint4*>(xs + t * wide + j), xv);
+#pragma unroll
+                for (int q = 0; q < kFewRows; q++)
+#pragma unroll
+                    for (int k = 0; k < 8; k++)
+                        acc[q][t] = fmaf(wv[q][k], xv[k], acc[q][t]);
+            }
+        };
+        int j = lane * 8;
+        for (; j + 256 * (kFewAhead - 1) + 8 <= hidden; j += 256 * kFewAhead) {
+            uint4 r[kFewAhead][kFewRows];             // all loads before any use
+#pragma unroll
+            for (int u = 0; u < kFewAhead; u++)
+#pragma unroll
+                for (int q = 0; q < kFewRows; q++)
+                    r[u][q] = __ldcs(reinterpret_cast<const uint4*>(row[q] + j + 256 * u));
+#pragma unroll
+            for (int u = 0; u < kFewAhead; u++)
+                add(r[u], j + 256 * u);
+        }
+        for (; j + 8 <= hidden; j += 256) {
+            uint4 r[kFewRows];
+#pragma unroll
+            for (int q = 0; q < kFewRows; q++)
+                r[q] = __ldcs(reinterpret_cast<const uint4*>(row[q] + j));
+            add(r, j);
+        }
+        if (j < hidden) {                             // the rows' ragged end
+            uint4 r[kFewRows];
+#pragma unroll
+            for (int q = 0; q < kFewRows; q++) {
+                uint32_t u[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int k = 0; k < 8; k++)
+                    if (j + k < hidden) u[k >> 1] |= (uint32_t)row[q][j + k] << ((k & 1) * 16);
+                r[q] = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+            add(r, j);
+        }
+#pragma unroll
+        for (int t = 0; t < T; t++) {
+            float z[kFewRows], top = mx[t];
+#pragma unroll
+            for (int q = 0; q < kFewRows; q++) {
+                z[q] = acc[q][t];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    z[q] += __shfl_xor_sync(0xffffffffu, z[q], o);
+                if (v + q < hi) {
+                    if (v + q == tgt[t] && lane == 0) target_logit[t] = z[q];
+                } else {
+                    z[q] = -INFINITY;
+                }
+                top = fmaxf(top, z[q]);
+            }
+            const float ref = top == -INFINITY ? 0.0f : top;
+            sum[t] *= exp2f((mx[t] - ref) * kLog2e);
+#pragma unroll
+            for (int q = 0; q < kFewRows; q++)
+                sum[t] += exp2f((z[q] - ref) * kLog2e);
+            mx[t] = top;
+        }
+    }
+    if (lane == 0)
+#pragma unroll
+        for (int t = 0; t < T; t++)
+            sh[warp][t] = make_float2(mx[t], sum[t]);
+    __syncthreads();
+    if (threadIdx.x < T) {
+        float m = -INFINITY, s = 0.0f;
+        for (int k = 0; k < kFewThreads / 32; k++)
+            merge(m, s, sh[k][threadIdx.x]);
+        part[(int64_t)blockIdx.x * T + threadIdx.x] = make_float2(m, s);
+    }
+    __threadfence();                                  // pairs and target logits, before the count
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(&a.head->joined, 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    if (warp < T) {                                   // one warp a token: 32 parts, then a tree
+        float m = -INFINITY, s = 0.0f;
+        for (unsigned k = lane; k < gridDim.x; k += 32)
+            merge(m, s, __ldcg(part + (int64_t)k * T + warp));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float2 q = make_float2(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
+            merge(m, s, q);
+        }
+        if (lane == 0) sh[0][warp] = finish_token(a, warp, m, s);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && a.total) {
+        float s = 0.0f, c = 0.0f;
+        for (int t = 0; t < T; t++) {
+            s += sh[0][t].x;
+            c += sh[0][t].y;
+        }
+        a.total[0] = c > 0.0f ? s / c : 0.0f;
+        a.total[1] = c;
     }
 }
 
@@ -559,6 +748,19 @@ zero_status_t cuda_failed(cudaError_t e, const char* what)
     return set_error(ZERO_ECUDA, msg);
 }
 
+// The forward pass of few tokens has its own kernel.
+bool few_tokens(const zero_ce_plan_t& p)
+{
+    return p.tokens <= kFewTokens && p.tokens * ((p.hidden + 7) / 8 * 8) * 2 <= kFewSmem;
+}
+
+// Its blocks: four to an SM of 152, and no more than give every warp a row.
+int64_t few_blocks(const zero_ce_plan_t& p)
+{
+    const int64_t most = ceil_div(p.vocab, kFewThreads / 32);
+    return most < kFewBlocks ? most : kFewBlocks;
+}
+
 // Byte offsets in the workspace.
 struct CeLayout {
     int64_t coef, target_logit, block_total, part, g, acc, end;
@@ -574,7 +776,7 @@ CeLayout layout_of(const zero_ce_plan_t& p)
     l.part = l.block_total + up256(ceil_div(p.tokens, 32) * 8);
     l.g = l.part;                                     // the two passes do not meet
     l.acc = l.g + up256(p.tokens * p.piece * 2);
-    const int64_t fwd = l.part + ceil_div(p.vocab, kBN) * 2 * p.tokens * 8;
+    const int64_t fwd = l.part + (few_tokens(p) ? few_blocks(p) : ceil_div(p.vocab, kBN) * 2) * p.tokens * 8;
     l.acc_rows = ceil_div(p.tokens, kBM) * kBM;
     l.acc_cols = (p.hidden + 3) / 4 * 4;
     const int64_t bwd = l.acc + p.splits * l.acc_rows * l.acc_cols * 4;
@@ -650,6 +852,32 @@ cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t s)
     return cudaGetLastError();
 }
 
+template <int DT, int T>
+cudaError_t launch_few_t(const zero_ce_plan_t& p, const void* x, const void* w, unsigned char* ws, const CeLayout& l,
+                         const JoinArgs& j, cudaStream_t s)
+{
+    const size_t bytes = (size_t)(T * ((p.hidden + 7) / 8 * 8) * 2);
+    const cudaError_t e = cudaFuncSetAttribute((const void*)k_ce_few<DT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kFewSmem);
+    if (e != cudaSuccess) return e;
+    k_ce_few<DT, T><<<(unsigned)few_blocks(p), kFewThreads, bytes, s>>>(
+        static_cast<const uint16_t*>(x), p.x_stride, static_cast<const uint16_t*>(w), p.w_stride, p.hidden,
+        reinterpret_cast<float2*>(ws + l.part), reinterpret_cast<float*>(ws + l.target_logit), j);
+    return cudaGetLastError();
+}
+
+template <int DT>
+cudaError_t launch_few(const zero_ce_plan_t& p, const void* x, const void* w, unsigned char* ws, const CeLayout& l,
+                       const JoinArgs& j, cudaStream_t s)
+{
+    switch (p.tokens) {
+    case 1: return launch_few_t<DT, 1>(p, x, w, ws, l, j, s);
+    case 2: return launch_few_t<DT, 2>(p, x, w, ws, l, j, s);
+    case 3: return launch_few_t<DT, 3>(p, x, w, ws, l, j, s);
+    default: return launch_few_t<DT, 4>(p, x, w, ws, l, j, s);
+    }
+}
+
 template <int EPI, bool A_MN, bool B_MN>
 cudaError_t gemm(int dtype, const GemmArgs& g, cudaStream_t s)
 {
@@ -690,8 +918,11 @@ zero_status_t zero_ce_plan(int64_t tokens, int64_t vocab, int64_t hidden, int32_
     if (piece) {
         out->piece = up256(piece) < all ? up256(piece) : all;
     } else {
-        // about 256 MiB of G, in pieces of about the same size
-        const int64_t most = tokens ? (int64_t(1) << 27) / tokens / 256 * 256 : all;
+        // about 512 MiB of G, in pieces of about the same size: fewer pieces pass
+        // dx's sums through memory less often.  Backward pass of 8192 tokens,
+        // hidden 768, vocabulary 50257: 1475 us with 105 MB of G, 1333 with 210,
+        // 1283 with 415, 1250 with all of it (824)
+        const int64_t most = tokens ? (int64_t(1) << 28) / tokens / 256 * 256 : all;
         const int64_t fit = most < 256 ? 256 : (most < all ? most : all);
         out->piece = up256(ceil_div(vocab, ceil_div(all, fit)));
     }
@@ -734,6 +965,22 @@ zero_status_t zero_ce_forward(const zero_ce_plan_t* plan, const void* x, const v
     if (p.tokens) {
         if (!encode_fn()) return set_error(ZERO_ECUDA, "zero_ce_forward: the driver has no cuTensorMapEncodeTiled");
         const CeLayout l = layout_of(p);
+        JoinArgs j;
+        j.head = reinterpret_cast<CeHead*>(ws);
+        j.part = reinterpret_cast<float2*>(ws + l.part);
+        j.strips = 2 * (int)ceil_div(p.vocab, kBN);
+        j.n = p.tokens;
+        j.targets = targets;
+        j.vocab = p.vocab;
+        j.target_logit = reinterpret_cast<float*>(ws + l.target_logit);
+        j.loss = loss;
+        j.lse = lse;
+        j.block_total = reinterpret_cast<float2*>(ws + l.block_total);
+        j.total = total;
+        if (few_tokens(p)) {
+            e = p.dtype == ZERO_BF16 ? launch_few<kBF16>(p, x, w, ws, l, j, s) : launch_few<kF16>(p, x, w, ws, l, j, s);
+            return e == cudaSuccess ? ZERO_OK : cuda_failed(e, "zero_ce_forward");
+        }
         const CUtensorMapDataType type = map_type(p.dtype);
         GemmArgs g;
         std::memset(&g, 0, sizeof g);
@@ -753,10 +1000,7 @@ zero_status_t zero_ce_forward(const zero_ce_plan_t* plan, const void* x, const v
         g.withhold = std::getenv("ZERO_TEST_WITHHOLD_TILE") != nullptr;
         e = gemm<kEpiLse, false, false>(p.dtype, g, s);
         if (e == cudaSuccess) {
-            k_ce_join<<<(unsigned)ceil_div(p.tokens, 32), 1024, 0, s>>>(
-                g.head, g.part, 2 * g.n_tiles, p.tokens, targets, p.vocab, g.target_logit, loss, lse,
-                reinterpret_cast<float2*>(ws + l.block_total), total);
-            e = cudaGetLastError();
+            e = launch_kernel(k_ce_join, (int)ceil_div(p.tokens, 32), 1024, s, true, j);
         }
     } else if (total) {
         e = cudaMemsetAsync(total, 0, 8, s);
