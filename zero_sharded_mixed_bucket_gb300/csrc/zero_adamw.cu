@@ -57,26 +57,40 @@ __device__ __forceinline__ uint32_t hash_pair(uint64_t i, uint32_t mix)
     return h ^ (h >> 16);
 }
 
-// Codes of a block: magnitudes relative to its scale are binary32 numbers cut
-// to 4 fraction bits, so a code is the top of the number's bit pattern, less
-// the pattern of the least normal (exponent field `least`), plus 16.  Below
-// the least normal, adding it first lines the bits up with the even spacing
-// there.
-template <int LEAST>
-__device__ __forceinline__ float decode8(uint32_t c)
+// Codes.  Moved up to bits 26..19 a code is a binary32 pattern with the code's
+// exponent and fraction, subnormals (E = 0) included, whose value is the
+// code's times 2^-kUp: one multiplication by a power of two decodes it.  The
+// other way the product with 2^-kUp rounds to 19 bits below the code's last
+// one (to nearest; only below the least normal), and the random bits decide
+// the carry into it.
+constexpr float kUpM = 0x1p120f, kUpR = 0x1p112f, kDownM = 0x1p-120f, kDownR = 0x1p-112f;
+
+// Byte k of w at bits 31..24.
+template <int K>
+__device__ __forceinline__ uint32_t byte_on_top(uint32_t w)
 {
-    const bool low = c < 16u;
-    const float y = __uint_as_float((c + LEAST * 16u - (low ? 0u : 16u)) << 19);
-    return low ? __fsub_rn(y, __uint_as_float((uint32_t)LEAST << 23)) : y;
+    return K == 3 ? w : __byte_perm(w, 0, K == 2 ? 0x2444 : (K == 1 ? 0x1444 : 0x0444));
 }
 
-template <int LEAST, uint32_t MOST>
-__device__ __forceinline__ uint32_t encode8(float y, uint32_t rnd16)
+// `top`: the code in bits 31..24, zeros below (or bits that the masks drop).
+__device__ __forceinline__ float decode_m(uint32_t top)
 {
-    const float base = __uint_as_float((uint32_t)LEAST << 23);
-    const bool low = y < base;
-    const uint32_t b = __float_as_uint(low ? __fadd_rn(y, base) : y) + (rnd16 << 3);
-    return min((b >> 19) - LEAST * 16u + (low ? 0u : 16u), MOST);
+    return __fmul_rn(__uint_as_float((top & 0x80000000u) | ((top >> 5) & 0x03f80000u)), kUpM);
+}
+
+__device__ __forceinline__ float decode_r(uint32_t top) { return __fmul_rn(__uint_as_float((top >> 5) & 0x07f80000u), kUpR); }
+
+// Codes of m and r >= 0 relative to the scale (im, ir its inverse, exact).
+__device__ __forceinline__ uint32_t encode_m(float m, float im, uint32_t rnd8)
+{
+    const uint32_t c = (__float_as_uint(__fmul_rn(__fmul_rn(fabsf(m), im), kDownM)) + rnd8) >> 19;
+    return c ? c | ((__float_as_uint(m) >> 24) & 0x80u) : 0u;
+}
+
+__device__ __forceinline__ uint32_t encode_r(float r, float ir, uint32_t rnd8)
+{
+    const uint32_t c = (__float_as_uint(__fmul_rn(__fmul_rn(r, ir), kDownR)) + rnd8) >> 19;
+    return max(c, min(__float_as_uint(r), 1u));        // a nonzero root keeps a nonzero code
 }
 
 // A block's scale byte, from the bit pattern of its largest magnitude: the
@@ -85,8 +99,6 @@ __device__ __forceinline__ uint32_t encode8(float y, uint32_t rnd16)
 // within one step of the binade's end could only be cut to the largest code:
 // an average that moves by less than a step would stop there for good.
 __device__ __forceinline__ uint32_t scale_field(uint32_t most) { return min((most + (1u << 19)) >> 23, 253u); }
-
-constexpr int kLeastM = 121, kLeastR = 113;   // 2^-6, 2^-14
 
 __device__ __forceinline__ float pow2_field(uint32_t e) { return __uint_as_float(e << 23); }
 
@@ -168,7 +180,30 @@ __global__ void __launch_bounds__(kAdThreads) k_adamw32(const AdTable tab, const
 }
 
 // 8-bit moments: a warp takes a block of 256 values, 8 per lane, so the
-// block's largest magnitudes are one warp-wide maximum each.
+// block's largest magnitudes are one warp-wide maximum each; the next block's
+// loads are issued before this one's arithmetic, which is most of the time.
+template <int DT>
+struct Lane8 {
+    alignas(16) Bits<DT> g[8];
+    alignas(16) float w[8];
+    uint2 cm, cr;
+    uint32_t em, er;
+};
+
+template <int DT>
+__device__ __forceinline__ void ld_block8(Lane8<DT>& x, const zero_adamw_tensor_t& t, int64_t i, int cnt, bool vec)
+{
+    ld_any<8>(static_cast<const Bits<DT>*>(t.grad) + i, cnt, vec, x.g);
+    ld_any<8>(t.master + i, cnt, vec, x.w);
+    alignas(8) uint8_t m[8], r[8];
+    ld_any<8>(static_cast<const uint8_t*>(t.m) + i, cnt, vec, m);
+    ld_any<8>(static_cast<const uint8_t*>(t.v) + i, cnt, vec, r);
+    x.cm = *reinterpret_cast<const uint2*>(m);
+    x.cr = *reinterpret_cast<const uint2*>(r);
+    x.em = t.m_scale[i / kQBlock];
+    x.er = t.v_scale[i / kQBlock];
+}
+
 template <int DT>
 __global__ void __launch_bounds__(kAdThreads) k_adamw8(const AdTable tab, const __grid_constant__ AdHP hp,
                                                        const uint32_t* skip)
@@ -176,92 +211,128 @@ __global__ void __launch_bounds__(kAdThreads) k_adamw8(const AdTable tab, const 
     if (skip && *skip) return;
     constexpr int V = 8;
     const AdRec& r = tab.rec[tab.chunk_tensor[blockIdx.x]];
+    const zero_adamw_tensor_t t = r.t;
+    const int64_t start = r.start;
     const int64_t lo = ((int64_t)blockIdx.x - r.first_chunk) * kChunk;
-    const int64_t hi = min(lo + kChunk, r.t.numel);
+    const int64_t hi = min(lo + kChunk, t.numel);
     const bool vec = r.aligned;
-    const float keep = __fmaf_rn(-hp.a.lr, r.t.weight_decay, 1.0f);
-    const Bits<DT>* grad = static_cast<const Bits<DT>*>(r.t.grad);
-    Bits<DT>* param = static_cast<Bits<DT>*>(r.t.param);
-    uint8_t* mp = static_cast<uint8_t*>(r.t.m);
-    uint8_t* vp = static_cast<uint8_t*>(r.t.v);
+    const float keep = __fmaf_rn(-hp.a.lr, t.weight_decay, 1.0f);
     const int lane = threadIdx.x & 31;
-    for (int64_t b = lo + (threadIdx.x >> 5) * kQBlock; b < hi; b += kAdThreads / 32 * kQBlock) {
+    constexpr int64_t kStep = kAdThreads / 32 * kQBlock;
+    int64_t b = lo + (threadIdx.x >> 5) * kQBlock;
+    if (b >= hi) return;
+    Lane8<DT> x;
+    int cnt = (int)max((int64_t)0, min((int64_t)V, hi - b - lane * V));
+    ld_block8<DT>(x, t, b + lane * V, cnt, vec);
+    while (true) {
         const int64_t i = b + lane * V;
-        const int cnt = i < hi ? (int)min((int64_t)V, hi - i) : 0;
-        alignas(16) Bits<DT> g[V], p[V];
-        alignas(16) float w[V];
-        alignas(16) uint8_t cm[V], cr[V];
-        ld_any<V>(grad + i, cnt, vec, g);
-        ld_any<V>(r.t.master + i, cnt, vec, w);
-        ld_any<V>(mp + i, cnt, vec, cm);
-        ld_any<V>(vp + i, cnt, vec, cr);
-        const float sm = pow2_field(r.t.m_scale[b / kQBlock]), sr = pow2_field(r.t.v_scale[b / kQBlock]);
+        Lane8<DT> next;
+        const int64_t nb = b + kStep;
+        int ncnt = 0;
+        if (nb < hi) {
+            ncnt = (int)max((int64_t)0, min((int64_t)V, hi - nb - lane * V));
+            ld_block8<DT>(next, t, nb + lane * V, ncnt, vec);
+        }
+        const float sm = pow2_field(x.em), sr = pow2_field(x.er);
+        alignas(16) Bits<DT> p[V];
         float m[V], q[V];
         uint32_t most_m = 0, most_r = 0;
 #pragma unroll
         for (int j = 0; j < V; j++) {
-            const float gj = __fmul_rn(to_f32<DT>(g[j]), hp.gs);
-            const float a = __fmul_rn(decode8<kLeastM>(cm[j] & 127u), sm);
-            const float m0 = cm[j] > 127u ? -a : a;
-            const float r0 = __fmul_rn(decode8<kLeastR>(cr[j]), sr);
+            const uint32_t wm = j < 4 ? x.cm.x : x.cm.y, wr = j < 4 ? x.cr.x : x.cr.y;
+            const uint32_t tm = (j & 3) == 0 ? byte_on_top<0>(wm) : (j & 3) == 1 ? byte_on_top<1>(wm)
+                                : (j & 3) == 2 ? byte_on_top<2>(wm) : byte_on_top<3>(wm);
+            const uint32_t tr = (j & 3) == 0 ? byte_on_top<0>(wr) : (j & 3) == 1 ? byte_on_top<1>(wr)
+                                : (j & 3) == 2 ? byte_on_top<2>(wr) : byte_on_top<3>(wr);
+            const float gj = __fmul_rn(to_f32<DT>(x.g[j]), hp.gs);
+            const float m0 = __fmul_rn(decode_m(tm), sm), r0 = __fmul_rn(decode_r(tr), sr);
             m[j] = __fadd_rn(__fmul_rn(m0, hp.a.b1), __fmul_rn(gj, hp.a.omb1));
             q[j] = __fsqrt_rn(__fadd_rn(__fmul_rn(__fmul_rn(r0, r0), hp.a.b2), __fmul_rn(__fmul_rn(gj, gj), hp.a.omb2)));
             const float d = __fadd_rn(__fmul_rn(q[j], hp.root8), hp.a.eps);
-            w[j] = __fsub_rn(__fmul_rn(w[j], keep), __fdiv_rn(__fmul_rn(m[j], hp.step8), d));
-            p[j] = (Bits<DT>)from_f32<DT>(w[j]);
-            if (j < cnt) {
-                most_m = max(most_m, __float_as_uint(m[j]) & 0x7fffffffu);
-                most_r = max(most_r, __float_as_uint(q[j]) & 0x7fffffffu);
-            }
+            x.w[j] = __fsub_rn(__fmul_rn(x.w[j], keep), __fdiv_rn(__fmul_rn(m[j], hp.step8), d));
+            p[j] = (Bits<DT>)from_f32<DT>(x.w[j]);
+            most_m = max(most_m, __float_as_uint(m[j]) & 0x7fffffffu);    // values past cnt are 0: m = r = 0
+            most_r = max(most_r, __float_as_uint(q[j]) & 0x7fffffffu);
         }
+        st_any<V>(t.master + i, cnt, vec, x.w);
+        if (t.param) st_any<V>(static_cast<Bits<DT>*>(t.param) + i, cnt, vec, p);
         const uint32_t em = scale_field(__reduce_max_sync(0xffffffffu, most_m));
         const uint32_t er = scale_field(__reduce_max_sync(0xffffffffu, most_r));
         const float im = pow2_field(254u - em), ir = pow2_field(254u - er);
+        uint32_t cm[V], cr[V];
 #pragma unroll
         for (int j = 0; j < V; j += 2) {
-            const uint32_t h = hash_pair((uint64_t)(r.start + i + j), hp.mix);
+            const uint32_t h = hash_pair((uint64_t)(start + i + j), hp.mix);
+            const uint32_t r0 = (h & 0xffffu) << 3, r1 = (h >> 13) & 0x7fff8u;
+            cm[j] = encode_m(m[j], im, r0);
+            cm[j + 1] = encode_m(m[j + 1], im, r1);
+            cr[j] = encode_r(q[j], ir, r0);
+            cr[j + 1] = encode_r(q[j + 1], ir, r1);
+        }
+        if (em == 253u || er == 253u) {                // past the scales' range, or not finite: cut to the largest code
 #pragma unroll
-            for (int k = j; k < j + 2; k++) {
-                const uint32_t rnd = k == j ? h & 0xffffu : h >> 16;
-                const uint32_t c = encode8<kLeastM, 127u>(__fmul_rn(fabsf(m[k]), im), rnd);
-                cm[k] = (uint8_t)(c | (m[k] < 0.0f && c ? 128u : 0u));
-                cr[k] = (uint8_t)max(encode8<kLeastR, 255u>(__fmul_rn(q[k], ir), rnd), q[k] > 0.0f ? 1u : 0u);
+            for (int j = 0; j < V; j++) {
+                const uint32_t c = (__float_as_uint(__fmul_rn(__fmul_rn(fabsf(m[j]), im), kDownM)) >> 19);
+                if (c >= 127u) cm[j] = 127u | (m[j] < 0.0f ? 128u : 0u);
+                if ((__float_as_uint(__fmul_rn(__fmul_rn(q[j], ir), kDownR)) >> 19) >= 255u || cr[j] > 255u) cr[j] = 255u;
             }
         }
-        st_any<V>(r.t.master + i, cnt, vec, w);
-        st_any<V>(mp + i, cnt, vec, cm);
-        st_any<V>(vp + i, cnt, vec, cr);
-        if (param) st_any<V>(param + i, cnt, vec, p);
+        alignas(8) uint8_t om[V], orr[V];
+        uint2 pm, pr;
+        pm.x = cm[0] | cm[1] << 8 | cm[2] << 16 | cm[3] << 24;
+        pm.y = cm[4] | cm[5] << 8 | cm[6] << 16 | cm[7] << 24;
+        pr.x = cr[0] | cr[1] << 8 | cr[2] << 16 | cr[3] << 24;
+        pr.y = cr[4] | cr[5] << 8 | cr[6] << 16 | cr[7] << 24;
+        *reinterpret_cast<uint2*>(om) = pm;
+        *reinterpret_cast<uint2*>(orr) = pr;
+        st_any<V>(static_cast<uint8_t*>(t.m) + i, cnt, vec, om);
+        st_any<V>(static_cast<uint8_t*>(t.v) + i, cnt, vec, orr);
         if (lane == 0) {
-            r.t.m_scale[b / kQBlock] = (uint8_t)em;
-            r.t.v_scale[b / kQBlock] = (uint8_t)er;
+            t.m_scale[b / kQBlock] = (uint8_t)em;
+            t.v_scale[b / kQBlock] = (uint8_t)er;
         }
+        if (nb >= hi) break;
+        x = next;
+        cnt = ncnt;
+        b = nb;
     }
 }
 
-// Stored 8-bit moments as bfloat16 values (5 significant bits: exact).
+// Stored 8-bit moments as bfloat16 values (5 significant bits: the upper half
+// of the binary32 pattern, exact while it is normal).
+__device__ __forceinline__ uint32_t upper_halves(float lo, float hi)
+{
+    return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
+
 __global__ void __launch_bounds__(kAdThreads) k_adamw_states(const AdTable tab, uint16_t* m_out, uint16_t* r_out)
 {
     constexpr int V = 8;
     const AdRec& r = tab.rec[tab.chunk_tensor[blockIdx.x]];
+    const zero_adamw_tensor_t t = r.t;
+    const int64_t start = r.start;
     const int64_t lo = ((int64_t)blockIdx.x - r.first_chunk) * kChunk;
-    const int64_t hi = min(lo + kChunk, r.t.numel);
+    const int64_t hi = min(lo + kChunk, t.numel);
     const bool vec = r.aligned;
+#pragma unroll 4
     for (int64_t i = lo + threadIdx.x * V; i < hi; i += kAdThreads * V) {
         const int cnt = (int)min((int64_t)V, hi - i);
-        alignas(16) uint8_t cm[V], cr[V];
-        alignas(16) uint16_t m[V], q[V];
-        ld_any<V>(static_cast<const uint8_t*>(r.t.m) + i, cnt, vec, cm);
-        ld_any<V>(static_cast<const uint8_t*>(r.t.v) + i, cnt, vec, cr);
-        const float sm = pow2_field(r.t.m_scale[i / kQBlock]), sr = pow2_field(r.t.v_scale[i / kQBlock]);
+        alignas(8) uint8_t cm[V], cr[V];
+        ld_any<V>(static_cast<const uint8_t*>(t.m) + i, cnt, vec, cm);
+        ld_any<V>(static_cast<const uint8_t*>(t.v) + i, cnt, vec, cr);
+        const uint2 wm = *reinterpret_cast<const uint2*>(cm), wr = *reinterpret_cast<const uint2*>(cr);
+        const float sm = pow2_field(t.m_scale[i / kQBlock]), sr = pow2_field(t.v_scale[i / kQBlock]);
+        alignas(16) uint32_t m[V / 2], q[V / 2];
 #pragma unroll
-        for (int j = 0; j < V; j++) {
-            const float a = __fmul_rn(decode8<kLeastM>(cm[j] & 127u), sm);
-            m[j] = (uint16_t)from_f32<kBF16>(cm[j] > 127u ? -a : a);
-            q[j] = (uint16_t)from_f32<kBF16>(__fmul_rn(decode8<kLeastR>(cr[j]), sr));
+        for (int k = 0; k < 2; k++) {
+            const uint32_t a = k ? wm.y : wm.x, b = k ? wr.y : wr.x;
+            m[2 * k] = upper_halves(__fmul_rn(decode_m(byte_on_top<0>(a)), sm), __fmul_rn(decode_m(byte_on_top<1>(a)), sm));
+            m[2 * k + 1] = upper_halves(__fmul_rn(decode_m(byte_on_top<2>(a)), sm), __fmul_rn(decode_m(byte_on_top<3>(a)), sm));
+            q[2 * k] = upper_halves(__fmul_rn(decode_r(byte_on_top<0>(b)), sr), __fmul_rn(decode_r(byte_on_top<1>(b)), sr));
+            q[2 * k + 1] = upper_halves(__fmul_rn(decode_r(byte_on_top<2>(b)), sr), __fmul_rn(decode_r(byte_on_top<3>(b)), sr));
         }
-        st_any<V>(m_out + r.start + i, cnt, true, m);
-        st_any<V>(r_out + r.start + i, cnt, true, q);
+        st_any<V>(m_out + start + i, cnt, true, reinterpret_cast<const uint16_t*>(m));
+        st_any<V>(r_out + start + i, cnt, true, reinterpret_cast<const uint16_t*>(q));
     }
 }
 

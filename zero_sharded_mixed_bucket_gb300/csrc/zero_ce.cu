@@ -494,12 +494,14 @@ __global__ void __launch_bounds__(1024) k_ce_join(const __grid_constant__ JoinAr
 
 // ---- few tokens -------------------------------------------------------------------
 // Up to kFewTokens tokens: w is read once and that is the time (411 MB at
-// vocabulary 50257, hidden 4096), so no tensor cores: the tokens lie in shared
-// memory, a warp takes kFewRows rows of w at a time, its lanes 8 values each,
-// and keeps a running maximum and sum per token.  The last block joins the
-// blocks' pairs.  A lane has 256 bytes of w in flight.  Products and sums are
-// binary32 multiply-adds.
-constexpr int kFewTokens = 4, kFewRows = 4, kFewAhead = 4, kFewThreads = 256, kFewBlocks = 608;
+// vocabulary 50257, hidden 4096: 61 us at the copy bandwidth), so no tensor
+// cores: the tokens lie in shared memory, a warp takes a row of w at a time (3
+// or 4 tokens: two, which share the unpacked tokens), neighbouring warps
+// neighbouring rows, each lane with 128 bytes in flight, 24 warps to an SM.
+// Each lane keeps one row's logit; 32 of them at a time go into the warp's
+// running maximum and sum.  The last block joins the blocks' pairs.  Products
+// and sums are binary32 multiply-adds.
+constexpr int kFewTokens = 4, kFewThreads = 256, kFewBlocks = 456;
 constexpr int kFewSmem = 64 * 1024;                   // all tokens' values, 16 bits each
 
 template <int DT>
@@ -515,112 +517,138 @@ __device__ __forceinline__ void unpack8(uint4 v, float f[8])
 }
 
 template <int DT, int T>
-__global__ void __launch_bounds__(kFewThreads) k_ce_few(const uint16_t* x, int64_t x_stride, const uint16_t* w,
-                                                        int64_t w_stride, int64_t hidden, float2* part,
-                                                        float* target_logit, const __grid_constant__ JoinArgs a)
+__global__ void __launch_bounds__(kFewThreads, 3) k_ce_few(const uint16_t* x, int64_t x_stride, const uint16_t* w,
+                                                           int64_t w_stride, int64_t hidden, float2* part,
+                                                           float* target_logit, const __grid_constant__ JoinArgs a)
 {
+    constexpr int R = T <= 2 ? 1 : 2, U = 8 / R;      // rows at a time, loads in flight per row
     extern __shared__ __align__(16) uint16_t xs[];    // [T][wide]
     __shared__ float2 sh[kFewThreads / 32][T];
     __shared__ uint32_t last;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int wide = (int)((hidden + 7) / 8 * 8);
-    for (int k = threadIdx.x; k < T * wide; k += kFewThreads) {
-        const int t = k / wide, j = k - t * wide;
-        xs[k] = j < hidden ? x[t * x_stride + j] : (uint16_t)0;
-    }
+#pragma unroll
+    for (int t = 0; t < T; t++)
+        for (int j = threadIdx.x * 8; j < wide; j += kFewThreads * 8) {
+            const uint16_t* p = x + t * x_stride + j;
+            if (j + 8 <= hidden) {
+                *reinterpret_cast<uint4*>(xs + t * wide + j) = *reinterpret_cast<const uint4*>(p);
+            } else {
+                for (int k = 0; k < 8; k++)
+                    xs[t * wide + j + k] = j + k < hidden ? p[k] : (uint16_t)0;
+            }
+        }
     __syncthreads();
-    int64_t tgt[T];
-    float mx[T], sum[T];
+    float mx[T], sum[T], held[T];                     // held: the logit of row `lane` of the 32 under way
 #pragma unroll
     for (int t = 0; t < T; t++) {
-        tgt[t] = a.targets[t];
-        mx[t] = -INFINITY;
+        mx[t] = held[t] = -INFINITY;
         sum[t] = 0.0f;
     }
-    const int64_t warps = (int64_t)gridDim.x * (kFewThreads / 32), me = (int64_t)blockIdx.x * (kFewThreads / 32) + warp;
-    const int64_t lo = a.vocab * me / warps, hi = a.vocab * (me + 1) / warps;
-    for (int64_t v = lo; v < hi; v += kFewRows) {
-        float acc[kFewRows][T];
+    auto flush = [&]() {
 #pragma unroll
-        for (int q = 0; q < kFewRows; q++)
+        for (int t = 0; t < T; t++) {
+            float top = held[t];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            top = fmaxf(top, mx[t]);
+            const float ref = top == -INFINITY ? 0.0f : top;
+            float s = exp2f((held[t] - ref) * kLog2e);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                s += __shfl_xor_sync(0xffffffffu, s, o);
+            sum[t] = fmaf(sum[t], exp2f((mx[t] - ref) * kLog2e), s);
+            mx[t] = top;
+            held[t] = -INFINITY;
+        }
+    };
+    const int64_t warps = (int64_t)gridDim.x * (kFewThreads / 32), me = (int64_t)blockIdx.x * (kFewThreads / 32) + warp;
+    int have = 0;
+    for (int64_t v = me * R; v < a.vocab; v += warps * R) {
+        const uint16_t* row[R];
+        float acc[R][T];
+#pragma unroll
+        for (int q = 0; q < R; q++) {
+            row[q] = w + min(v + q, a.vocab - 1) * w_stride;
 #pragma unroll
             for (int t = 0; t < T; t++)
                 acc[q][t] = 0.0f;
-        const uint16_t* row[kFewRows];
+        }
+        auto add = [&](const uint4 r[R], int j) {
+            float wv[R][8];
 #pragma unroll
-        for (int q = 0; q < kFewRows; q++)
-            row[q] = w + min(v + q, hi - 1) * w_stride;
-        auto add = [&](const uint4 r[kFewRows], int j) {
-            float wv[kFewRows][8];
-#pragma unroll
-            for (int q = 0; q < kFewRows; q++)
+            for (int q = 0; q < R; q++)
                 unpack8<DT>(r[q], wv[q]);
 #pragma unroll
             for (int t = 0; t < T; t++) {
                 float xv[8];
                 unpack8<DT>(*reinterpret_cast<const uint4*>(xs + t * wide + j), xv);
 #pragma unroll
-                for (int q = 0; q < kFewRows; q++)
+                for (int q = 0; q < R; q++)
 #pragma unroll
                     for (int k = 0; k < 8; k++)
                         acc[q][t] = fmaf(wv[q][k], xv[k], acc[q][t]);
             }
         };
         int j = lane * 8;
-        for (; j + 256 * (kFewAhead - 1) + 8 <= hidden; j += 256 * kFewAhead) {
-            uint4 r[kFewAhead][kFewRows];             // all loads before any use
+        for (; j + 256 * (U - 1) + 8 <= hidden; j += 256 * U) {
+            uint4 r[U][R];                            // all loads before any use
 #pragma unroll
-            for (int u = 0; u < kFewAhead; u++)
+            for (int u = 0; u < U; u++)
 #pragma unroll
-                for (int q = 0; q < kFewRows; q++)
+                for (int q = 0; q < R; q++)
                     r[u][q] = __ldcs(reinterpret_cast<const uint4*>(row[q] + j + 256 * u));
 #pragma unroll
-            for (int u = 0; u < kFewAhead; u++)
+            for (int u = 0; u < U; u++)
                 add(r[u], j + 256 * u);
         }
-        for (; j + 8 <= hidden; j += 256) {
-            uint4 r[kFewRows];
+        for (; j + 256 * (U / 4 - 1) + 8 <= hidden && U >= 4; j += 256 * (U / 4)) {
+            uint4 r[U / 4][R];
 #pragma unroll
-            for (int q = 0; q < kFewRows; q++)
-                r[q] = __ldcs(reinterpret_cast<const uint4*>(row[q] + j));
-            add(r, j);
+            for (int u = 0; u < U / 4; u++)
+#pragma unroll
+                for (int q = 0; q < R; q++)
+                    r[u][q] = __ldcs(reinterpret_cast<const uint4*>(row[q] + j + 256 * u));
+#pragma unroll
+            for (int u = 0; u < U / 4; u++)
+                add(r[u], j + 256 * u);
         }
-        if (j < hidden) {                             // the rows' ragged end
-            uint4 r[kFewRows];
+        for (; j < hidden; j += 256) {                // what is left, and the rows' ragged end
+            uint4 r[R];
 #pragma unroll
-            for (int q = 0; q < kFewRows; q++) {
-                uint32_t u[4] = {0, 0, 0, 0};
+            for (int q = 0; q < R; q++) {
+                if (j + 8 <= hidden) {
+                    r[q] = __ldcs(reinterpret_cast<const uint4*>(row[q] + j));
+                } else {
+                    uint32_t u[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int k = 0; k < 8; k++)
-                    if (j + k < hidden) u[k >> 1] |= (uint32_t)row[q][j + k] << ((k & 1) * 16);
-                r[q] = make_uint4(u[0], u[1], u[2], u[3]);
+                    for (int k = 0; k < 8; k++)
+                        if (j + k < hidden) u[k >> 1] |= (uint32_t)row[q][j + k] << ((k & 1) * 16);
+                    r[q] = make_uint4(u[0], u[1], u[2], u[3]);
+                }
             }
             add(r, j);
         }
 #pragma unroll
-        for (int t = 0; t < T; t++) {
-            float z[kFewRows], top = mx[t];
+        for (int q = 0; q < R; q++) {
+            if (v + q >= a.vocab) break;
 #pragma unroll
-            for (int q = 0; q < kFewRows; q++) {
-                z[q] = acc[q][t];
+            for (int t = 0; t < T; t++) {
+                float z = acc[q][t];
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1)
-                    z[q] += __shfl_xor_sync(0xffffffffu, z[q], o);
-                if (v + q < hi) {
-                    if (v + q == tgt[t] && lane == 0) target_logit[t] = z[q];
-                } else {
-                    z[q] = -INFINITY;
-                }
-                top = fmaxf(top, z[q]);
+                    z += __shfl_xor_sync(0xffffffffu, z, o);
+                if (lane == have) held[t] = z;
+                if (lane == 0 && v + q == a.targets[t]) target_logit[t] = z;
             }
-            const float ref = top == -INFINITY ? 0.0f : top;
-            sum[t] *= exp2f((mx[t] - ref) * kLog2e);
-#pragma unroll
-            for (int q = 0; q < kFewRows; q++)
-                sum[t] += exp2f((z[q] - ref) * kLog2e);
-            mx[t] = top;
+            if (++have == 32) {
+                flush();
+                have = 0;
+            }
         }
     }
+    if (have) flush();
     if (lane == 0)
 #pragma unroll
         for (int t = 0; t < T; t++)
@@ -754,7 +782,7 @@ bool few_tokens(const zero_ce_plan_t& p)
     return p.tokens <= kFewTokens && p.tokens * ((p.hidden + 7) / 8 * 8) * 2 <= kFewSmem;
 }
 
-// Its blocks: four to an SM of 152, and no more than give every warp a row.
+// Its blocks: three to an SM of 152, and no more than give every warp a row.
 int64_t few_blocks(const zero_ce_plan_t& p)
 {
     const int64_t most = ceil_div(p.vocab, kFewThreads / 32);
