@@ -87,7 +87,8 @@
  * -----------
  *   The caller owns all memory; the library allocates nothing and never
  *   throws.  Between calls it keeps only: per process, the resident-block
- *   count of each kernel on each device (behind a lock); per thread, the
+ *   count of each kernel on each device (behind a lock) and which devices a
+ *   kernel's shared-memory limit was raised on; per thread, the
  *   error text, the profiling events, and whether each pointer it was given
  *   for a replicated output is device memory of the current device (asked
  *   of the driver on every call outside stream capture, so a freed address

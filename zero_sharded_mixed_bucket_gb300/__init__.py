@@ -385,8 +385,13 @@ def zero_pa_gather(plan: zero_pa_plan_t, shards, dst, stream=None):
 
 
 def _optr(x):
-    """A device pointer that may be absent: None, an int or a tensor."""
-    return None if x is None else _dptr(x)
+    """A device pointer that may be absent: None, a tensor or an int."""
+    if x is None:
+        return None
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        return int(x)
 
 
 def zero_ln_plan(rows: int, dim: int, dtype: int = ZERO_FP16, x_stride: int = 0, y_stride: int = 0) -> zero_ln_plan_t:

@@ -47,23 +47,53 @@ struct AdHP {
     uint32_t mix;                    // seed + t * constant
 };
 
-// The 16 random bits of values i and i+1 (i even), low and high half.
-__device__ __forceinline__ uint32_t hash_pair(uint64_t i, uint32_t mix)
+// Random bits of the 8 values from i on (a multiple of 8): hash_base once,
+// then pair k = 0..3's two 16-bit numbers, low and high half.
+constexpr uint32_t kHashA = 0x9E3779B1u, kHashB = 0x6A09E667u, kHashC = 0xBB67AE85u, kHashD = 0xA54FF53Bu;
+
+__device__ __forceinline__ uint32_t hash_base(uint64_t i, uint32_t mix)
 {
     const uint64_t j = i >> 1;
-    uint32_t h = (uint32_t)j * 0x9E3779B1u + (uint32_t)(j >> 32) * 0x6A09E667u + mix;
-    h = (h ^ (h >> 15)) * 0xBB67AE85u;
-    h = (h ^ (h >> 15)) * 0xA54FF53Bu;
+    return (uint32_t)j * kHashA + (uint32_t)(j >> 32) * kHashB + mix;
+}
+
+__device__ __forceinline__ uint32_t hash_pair(uint32_t base, uint32_t k)
+{
+    uint32_t h = base + k * kHashA;
+    h = (h ^ (h >> 15)) * kHashC;
+    h = (h ^ (h >> 15)) * kHashD;
     return h ^ (h >> 16);
 }
 
 // Codes.  Moved up to bits 26..19 a code is a binary32 pattern with the code's
 // exponent and fraction, subnormals (E = 0) included, whose value is the
-// code's times 2^-kUp: one multiplication by a power of two decodes it.  The
-// other way the product with 2^-kUp rounds to 19 bits below the code's last
-// one (to nearest; only below the least normal), and the random bits decide
-// the carry into it.
-constexpr float kUpM = 0x1p120f, kUpR = 0x1p112f, kDownM = 0x1p-120f, kDownR = 0x1p-112f;
+// code's times 2^-120 (m) or 2^-112 (r): one multiplication by a power of two,
+// the scale with it, decodes it.  The other way the product with the inverse
+// rounds to 19 bits below the code's last one (to nearest; only below the
+// least normal), and the random bits decide the carry into it.
+constexpr uint32_t kUpM = 120, kUpR = 112;
+
+// 2^(e - 127) for an exponent field 1..254, 0 for 0.
+__device__ __forceinline__ float pow2_field(uint32_t e) { return __uint_as_float(e << 23); }
+
+// Factors of a block with scale byte e: 2^(e - 127 + up) to decode, its
+// inverse to encode.  Scales from 2^6 (m) or 2^14 (r) on are out of one
+// factor's range; they take the rest, `over`, in a second one.
+struct Factors {
+    float dec, enc, over;        // over: 1 but for such scales
+};
+
+template <uint32_t UP>
+__device__ __forceinline__ Factors factors_of(uint32_t e)
+{
+    const uint32_t lim = 253u - UP;                    // dec's and enc's fields stay in 1..254
+    const uint32_t f = min(e, lim);
+    Factors r;
+    r.dec = e ? pow2_field(f + UP) : 0.0f;
+    r.enc = pow2_field(254u - UP - f);
+    r.over = pow2_field(127u + e - f);
+    return r;
+}
 
 // Byte k of w at bits 31..24.
 template <int K>
@@ -72,25 +102,40 @@ __device__ __forceinline__ uint32_t byte_on_top(uint32_t w)
     return K == 3 ? w : __byte_perm(w, 0, K == 2 ? 0x2444 : (K == 1 ? 0x1444 : 0x0444));
 }
 
-// `top`: the code in bits 31..24, zeros below (or bits that the masks drop).
-__device__ __forceinline__ float decode_m(uint32_t top)
+__device__ __forceinline__ uint32_t byte_on_top(uint2 w, int k)
 {
-    return __fmul_rn(__uint_as_float((top & 0x80000000u) | ((top >> 5) & 0x03f80000u)), kUpM);
+    const uint32_t x = k < 4 ? w.x : w.y;
+    return (k & 3) == 0 ? byte_on_top<0>(x) : (k & 3) == 1 ? byte_on_top<1>(x) : (k & 3) == 2 ? byte_on_top<2>(x)
+                                                                                             : byte_on_top<3>(x);
 }
 
-__device__ __forceinline__ float decode_r(uint32_t top) { return __fmul_rn(__uint_as_float((top >> 5) & 0x07f80000u), kUpR); }
-
-// Codes of m and r >= 0 relative to the scale (im, ir its inverse, exact).
-__device__ __forceinline__ uint32_t encode_m(float m, float im, uint32_t rnd8)
+// `top`: the code in bits 31..24, anything below.
+__device__ __forceinline__ float decode_m(uint32_t top, float dec)
 {
-    const uint32_t c = (__float_as_uint(__fmul_rn(__fmul_rn(fabsf(m), im), kDownM)) + rnd8) >> 19;
+    return __fmul_rn(__uint_as_float((top & 0x80000000u) | ((top >> 5) & 0x03f80000u)), dec);
+}
+
+__device__ __forceinline__ float decode_r(uint32_t top, float dec)
+{
+    return __fmul_rn(__uint_as_float((top >> 5) & 0x07f80000u), dec);
+}
+
+// Codes of m and r >= 0; rnd8: 16 random bits times 8.
+__device__ __forceinline__ uint32_t encode_m(float m, float enc, uint32_t rnd8)
+{
+    const uint32_t c = (__float_as_uint(__fmul_rn(fabsf(m), enc)) + rnd8) >> 19;
     return c ? c | ((__float_as_uint(m) >> 24) & 0x80u) : 0u;
 }
 
-__device__ __forceinline__ uint32_t encode_r(float r, float ir, uint32_t rnd8)
+__device__ __forceinline__ uint32_t encode_r(float r, float enc, uint32_t rnd8)
 {
-    const uint32_t c = (__float_as_uint(__fmul_rn(__fmul_rn(r, ir), kDownR)) + rnd8) >> 19;
+    const uint32_t c = (__float_as_uint(__fmul_rn(r, enc)) + rnd8) >> 19;
     return max(c, min(__float_as_uint(r), 1u));        // a nonzero root keeps a nonzero code
+}
+
+__device__ __forceinline__ uint32_t pack4(const uint32_t c[4])
+{
+    return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
 }
 
 // A block's scale byte, from the bit pattern of its largest magnitude: the
@@ -99,8 +144,6 @@ __device__ __forceinline__ uint32_t encode_r(float r, float ir, uint32_t rnd8)
 // within one step of the binade's end could only be cut to the largest code:
 // an average that moves by less than a step would stop there for good.
 __device__ __forceinline__ uint32_t scale_field(uint32_t most) { return min((most + (1u << 19)) >> 23, 253u); }
-
-__device__ __forceinline__ float pow2_field(uint32_t e) { return __uint_as_float(e << 23); }
 
 template <int V, typename T>
 __device__ __forceinline__ void ld_any(const T* p, int cnt, bool vec, T x[V])
@@ -180,121 +223,105 @@ __global__ void __launch_bounds__(kAdThreads) k_adamw32(const AdTable tab, const
 }
 
 // 8-bit moments: a warp takes a block of 256 values, 8 per lane, so the
-// block's largest magnitudes are one warp-wide maximum each; the next block's
-// loads are issued before this one's arithmetic, which is most of the time.
+// block's largest magnitudes are one warp-wide maximum each.  Most of the time
+// is instructions, about 85 a value: four correctly rounded operations
+// (square root, division) and the codes' integer work.
 template <int DT>
-struct Lane8 {
-    alignas(16) Bits<DT> g[8];
-    alignas(16) float w[8];
-    uint2 cm, cr;
-    uint32_t em, er;
-};
-
-template <int DT>
-__device__ __forceinline__ void ld_block8(Lane8<DT>& x, const zero_adamw_tensor_t& t, int64_t i, int cnt, bool vec)
-{
-    ld_any<8>(static_cast<const Bits<DT>*>(t.grad) + i, cnt, vec, x.g);
-    ld_any<8>(t.master + i, cnt, vec, x.w);
-    alignas(8) uint8_t m[8], r[8];
-    ld_any<8>(static_cast<const uint8_t*>(t.m) + i, cnt, vec, m);
-    ld_any<8>(static_cast<const uint8_t*>(t.v) + i, cnt, vec, r);
-    x.cm = *reinterpret_cast<const uint2*>(m);
-    x.cr = *reinterpret_cast<const uint2*>(r);
-    x.em = t.m_scale[i / kQBlock];
-    x.er = t.v_scale[i / kQBlock];
-}
-
-template <int DT>
-__global__ void __launch_bounds__(kAdThreads) k_adamw8(const AdTable tab, const __grid_constant__ AdHP hp,
-                                                       const uint32_t* skip)
+__global__ void __launch_bounds__(kAdThreads, 8) k_adamw8(const AdTable tab, const __grid_constant__ AdHP hp,
+                                                          const uint32_t* skip)
 {
     if (skip && *skip) return;
     constexpr int V = 8;
     const AdRec& r = tab.rec[tab.chunk_tensor[blockIdx.x]];
-    const zero_adamw_tensor_t t = r.t;
-    const int64_t start = r.start;
+    const zero_adamw_tensor_t& t = r.t;
     const int64_t lo = ((int64_t)blockIdx.x - r.first_chunk) * kChunk;
     const int64_t hi = min(lo + kChunk, t.numel);
     const bool vec = r.aligned;
     const float keep = __fmaf_rn(-hp.a.lr, t.weight_decay, 1.0f);
     const int lane = threadIdx.x & 31;
-    constexpr int64_t kStep = kAdThreads / 32 * kQBlock;
-    int64_t b = lo + (threadIdx.x >> 5) * kQBlock;
-    if (b >= hi) return;
-    Lane8<DT> x;
-    int cnt = (int)max((int64_t)0, min((int64_t)V, hi - b - lane * V));
-    ld_block8<DT>(x, t, b + lane * V, cnt, vec);
-    while (true) {
+    for (int64_t b = lo + (threadIdx.x >> 5) * kQBlock; b < hi; b += kAdThreads / 32 * kQBlock) {
         const int64_t i = b + lane * V;
-        Lane8<DT> next;
-        const int64_t nb = b + kStep;
-        int ncnt = 0;
-        if (nb < hi) {
-            ncnt = (int)max((int64_t)0, min((int64_t)V, hi - nb - lane * V));
-            ld_block8<DT>(next, t, nb + lane * V, ncnt, vec);
-        }
-        const float sm = pow2_field(x.em), sr = pow2_field(x.er);
-        alignas(16) Bits<DT> p[V];
+        const int cnt = i < hi ? (int)min((int64_t)V, hi - i) : 0;
+        alignas(16) Bits<DT> g[V];
+        alignas(16) float w[V];
+        alignas(8) uint8_t cm8[V], cr8[V];
+        ld_any<V>(static_cast<const Bits<DT>*>(t.grad) + i, cnt, vec, g);
+        ld_any<V>(t.master + i, cnt, vec, w);
+        ld_any<V>(static_cast<const uint8_t*>(t.m) + i, cnt, vec, cm8);
+        ld_any<V>(static_cast<const uint8_t*>(t.v) + i, cnt, vec, cr8);
+        const uint2 wm = *reinterpret_cast<const uint2*>(cm8), wr = *reinterpret_cast<const uint2*>(cr8);
+        const Factors om = factors_of<kUpM>(t.m_scale[b / kQBlock]), orr = factors_of<kUpR>(t.v_scale[b / kQBlock]);
         float m[V], q[V];
+#pragma unroll
+        for (int j = 0; j < V; j++) {
+            m[j] = decode_m(byte_on_top(wm, j), om.dec);
+            q[j] = decode_r(byte_on_top(wr, j), orr.dec);
+        }
+        if (om.over != 1.0f || orr.over != 1.0f) {
+#pragma unroll
+            for (int j = 0; j < V; j++) {
+                m[j] = __fmul_rn(m[j], om.over);
+                q[j] = __fmul_rn(q[j], orr.over);
+            }
+        }
+        alignas(16) Bits<DT> p[V];
         uint32_t most_m = 0, most_r = 0;
 #pragma unroll
         for (int j = 0; j < V; j++) {
-            const uint32_t wm = j < 4 ? x.cm.x : x.cm.y, wr = j < 4 ? x.cr.x : x.cr.y;
-            const uint32_t tm = (j & 3) == 0 ? byte_on_top<0>(wm) : (j & 3) == 1 ? byte_on_top<1>(wm)
-                                : (j & 3) == 2 ? byte_on_top<2>(wm) : byte_on_top<3>(wm);
-            const uint32_t tr = (j & 3) == 0 ? byte_on_top<0>(wr) : (j & 3) == 1 ? byte_on_top<1>(wr)
-                                : (j & 3) == 2 ? byte_on_top<2>(wr) : byte_on_top<3>(wr);
-            const float gj = __fmul_rn(to_f32<DT>(x.g[j]), hp.gs);
-            const float m0 = __fmul_rn(decode_m(tm), sm), r0 = __fmul_rn(decode_r(tr), sr);
-            m[j] = __fadd_rn(__fmul_rn(m0, hp.a.b1), __fmul_rn(gj, hp.a.omb1));
-            q[j] = __fsqrt_rn(__fadd_rn(__fmul_rn(__fmul_rn(r0, r0), hp.a.b2), __fmul_rn(__fmul_rn(gj, gj), hp.a.omb2)));
+            const float gj = __fmul_rn(to_f32<DT>(g[j]), hp.gs);
+            m[j] = __fadd_rn(__fmul_rn(m[j], hp.a.b1), __fmul_rn(gj, hp.a.omb1));
+            q[j] = __fsqrt_rn(__fadd_rn(__fmul_rn(__fmul_rn(q[j], q[j]), hp.a.b2), __fmul_rn(__fmul_rn(gj, gj), hp.a.omb2)));
             const float d = __fadd_rn(__fmul_rn(q[j], hp.root8), hp.a.eps);
-            x.w[j] = __fsub_rn(__fmul_rn(x.w[j], keep), __fdiv_rn(__fmul_rn(m[j], hp.step8), d));
-            p[j] = (Bits<DT>)from_f32<DT>(x.w[j]);
+            w[j] = __fsub_rn(__fmul_rn(w[j], keep), __fdiv_rn(__fmul_rn(m[j], hp.step8), d));
+            p[j] = (Bits<DT>)from_f32<DT>(w[j]);
             most_m = max(most_m, __float_as_uint(m[j]) & 0x7fffffffu);    // values past cnt are 0: m = r = 0
-            most_r = max(most_r, __float_as_uint(q[j]) & 0x7fffffffu);
+            most_r = max(most_r, __float_as_uint(q[j]));                  // a root has no sign
         }
-        st_any<V>(t.master + i, cnt, vec, x.w);
+        st_any<V>(t.master + i, cnt, vec, w);
         if (t.param) st_any<V>(static_cast<Bits<DT>*>(t.param) + i, cnt, vec, p);
         const uint32_t em = scale_field(__reduce_max_sync(0xffffffffu, most_m));
         const uint32_t er = scale_field(__reduce_max_sync(0xffffffffu, most_r));
-        const float im = pow2_field(254u - em), ir = pow2_field(254u - er);
+        const Factors nm = factors_of<kUpM>(em), nr = factors_of<kUpR>(er);
+        const bool far = nm.over != 1.0f || nr.over != 1.0f;
+        uint32_t nonzero = 0;                          // roots; scaled far down they may become 0
+        if (far) {
+            const float dm = pow2_field(254u - (127u + em - min(em, 253u - kUpM)));   // 1 / over
+            const float dr = pow2_field(254u - (127u + er - min(er, 253u - kUpR)));
+#pragma unroll
+            for (int j = 0; j < V; j++) {
+                nonzero |= (uint32_t)(q[j] > 0.0f) << j;
+                m[j] = __fmul_rn(m[j], dm);
+                q[j] = __fmul_rn(q[j], dr);
+            }
+        }
+        const uint32_t base = hash_base((uint64_t)(r.start + i), hp.mix);
         uint32_t cm[V], cr[V];
 #pragma unroll
         for (int j = 0; j < V; j += 2) {
-            const uint32_t h = hash_pair((uint64_t)(start + i + j), hp.mix);
+            const uint32_t h = hash_pair(base, j / 2);
             const uint32_t r0 = (h & 0xffffu) << 3, r1 = (h >> 13) & 0x7fff8u;
-            cm[j] = encode_m(m[j], im, r0);
-            cm[j + 1] = encode_m(m[j + 1], im, r1);
-            cr[j] = encode_r(q[j], ir, r0);
-            cr[j + 1] = encode_r(q[j + 1], ir, r1);
+            cm[j] = encode_m(m[j], nm.enc, r0);
+            cm[j + 1] = encode_m(m[j + 1], nm.enc, r1);
+            cr[j] = encode_r(q[j], nr.enc, r0);
+            cr[j + 1] = encode_r(q[j + 1], nr.enc, r1);
         }
-        if (em == 253u || er == 253u) {                // past the scales' range, or not finite: cut to the largest code
+        if (far) {                                     // the last scale, or not finite: cut to the largest code
 #pragma unroll
             for (int j = 0; j < V; j++) {
-                const uint32_t c = (__float_as_uint(__fmul_rn(__fmul_rn(fabsf(m[j]), im), kDownM)) >> 19);
-                if (c >= 127u) cm[j] = 127u | (m[j] < 0.0f ? 128u : 0u);
-                if ((__float_as_uint(__fmul_rn(__fmul_rn(q[j], ir), kDownR)) >> 19) >= 255u || cr[j] > 255u) cr[j] = 255u;
+                if ((cm[j] & ~0x80u) > 127u || (__float_as_uint(__fmul_rn(fabsf(m[j]), nm.enc)) >> 19) >= 127u)
+                    cm[j] = 127u | (m[j] < 0.0f ? 128u : 0u);
+                cr[j] = max(min(cr[j], 255u), nonzero >> j & 1u);
             }
         }
-        alignas(8) uint8_t om[V], orr[V];
-        uint2 pm, pr;
-        pm.x = cm[0] | cm[1] << 8 | cm[2] << 16 | cm[3] << 24;
-        pm.y = cm[4] | cm[5] << 8 | cm[6] << 16 | cm[7] << 24;
-        pr.x = cr[0] | cr[1] << 8 | cr[2] << 16 | cr[3] << 24;
-        pr.y = cr[4] | cr[5] << 8 | cr[6] << 16 | cr[7] << 24;
-        *reinterpret_cast<uint2*>(om) = pm;
-        *reinterpret_cast<uint2*>(orr) = pr;
-        st_any<V>(static_cast<uint8_t*>(t.m) + i, cnt, vec, om);
-        st_any<V>(static_cast<uint8_t*>(t.v) + i, cnt, vec, orr);
+        alignas(8) uint8_t nm8[V], nr8[V];
+        *reinterpret_cast<uint2*>(nm8) = make_uint2(pack4(cm), pack4(cm + 4));
+        *reinterpret_cast<uint2*>(nr8) = make_uint2(pack4(cr), pack4(cr + 4));
+        st_any<V>(static_cast<uint8_t*>(t.m) + i, cnt, vec, nm8);
+        st_any<V>(static_cast<uint8_t*>(t.v) + i, cnt, vec, nr8);
         if (lane == 0) {
             t.m_scale[b / kQBlock] = (uint8_t)em;
             t.v_scale[b / kQBlock] = (uint8_t)er;
         }
-        if (nb >= hi) break;
-        x = next;
-        cnt = ncnt;
-        b = nb;
     }
 }
 
@@ -321,15 +348,18 @@ __global__ void __launch_bounds__(kAdThreads) k_adamw_states(const AdTable tab, 
         ld_any<V>(static_cast<const uint8_t*>(t.m) + i, cnt, vec, cm);
         ld_any<V>(static_cast<const uint8_t*>(t.v) + i, cnt, vec, cr);
         const uint2 wm = *reinterpret_cast<const uint2*>(cm), wr = *reinterpret_cast<const uint2*>(cr);
-        const float sm = pow2_field(t.m_scale[i / kQBlock]), sr = pow2_field(t.v_scale[i / kQBlock]);
+        const Factors fm = factors_of<kUpM>(t.m_scale[i / kQBlock]), fr = factors_of<kUpR>(t.v_scale[i / kQBlock]);
         alignas(16) uint32_t m[V / 2], q[V / 2];
 #pragma unroll
-        for (int k = 0; k < 2; k++) {
-            const uint32_t a = k ? wm.y : wm.x, b = k ? wr.y : wr.x;
-            m[2 * k] = upper_halves(__fmul_rn(decode_m(byte_on_top<0>(a)), sm), __fmul_rn(decode_m(byte_on_top<1>(a)), sm));
-            m[2 * k + 1] = upper_halves(__fmul_rn(decode_m(byte_on_top<2>(a)), sm), __fmul_rn(decode_m(byte_on_top<3>(a)), sm));
-            q[2 * k] = upper_halves(__fmul_rn(decode_r(byte_on_top<0>(b)), sr), __fmul_rn(decode_r(byte_on_top<1>(b)), sr));
-            q[2 * k + 1] = upper_halves(__fmul_rn(decode_r(byte_on_top<2>(b)), sr), __fmul_rn(decode_r(byte_on_top<3>(b)), sr));
+        for (int k = 0; k < V / 2; k++) {
+            float x[2], y[2];
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                x[e] = __fmul_rn(decode_m(byte_on_top(wm, 2 * k + e), fm.dec), fm.over);
+                y[e] = __fmul_rn(decode_r(byte_on_top(wr, 2 * k + e), fr.dec), fr.over);
+            }
+            m[k] = upper_halves(x[0], x[1]);
+            q[k] = upper_halves(y[0], y[1]);
         }
         st_any<V>(m_out + start + i, cnt, true, reinterpret_cast<const uint16_t*>(m));
         st_any<V>(r_out + start + i, cnt, true, reinterpret_cast<const uint16_t*>(q));

@@ -592,43 +592,30 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_ce_few(const uint16_t* x, in
             }
         };
         int j = lane * 8;
-        for (; j + 256 * (U - 1) + 8 <= hidden; j += 256 * U) {
-            uint4 r[U][R];                            // all loads before any use
+        for (; j + 8 <= hidden; j += 256 * U) {
+            uint4 r[U][R];                            // all loads before any use; 0 past the row's end
 #pragma unroll
             for (int u = 0; u < U; u++)
 #pragma unroll
                 for (int q = 0; q < R; q++)
-                    r[u][q] = __ldcs(reinterpret_cast<const uint4*>(row[q] + j + 256 * u));
+                    r[u][q] = j + 256 * u + 8 <= hidden ? __ldcs(reinterpret_cast<const uint4*>(row[q] + j + 256 * u))
+                                                        : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int u = 0; u < U; u++)
-                add(r[u], j + 256 * u);
+                if (j + 256 * u + 8 <= hidden) add(r[u], j + 256 * u);
         }
-        for (; j + 256 * (U / 4 - 1) + 8 <= hidden && U >= 4; j += 256 * (U / 4)) {
-            uint4 r[U / 4][R];
-#pragma unroll
-            for (int u = 0; u < U / 4; u++)
-#pragma unroll
-                for (int q = 0; q < R; q++)
-                    r[u][q] = __ldcs(reinterpret_cast<const uint4*>(row[q] + j + 256 * u));
-#pragma unroll
-            for (int u = 0; u < U / 4; u++)
-                add(r[u], j + 256 * u);
-        }
-        for (; j < hidden; j += 256) {                // what is left, and the rows' ragged end
+        if (lane == (hidden / 8) % 32 && hidden % 8) {    // the rows' ragged end
+            const int e = (int)(hidden / 8 * 8);
             uint4 r[R];
 #pragma unroll
             for (int q = 0; q < R; q++) {
-                if (j + 8 <= hidden) {
-                    r[q] = __ldcs(reinterpret_cast<const uint4*>(row[q] + j));
-                } else {
-                    uint32_t u[4] = {0, 0, 0, 0};
+                uint32_t u[4] = {0, 0, 0, 0};
 #pragma unroll
-                    for (int k = 0; k < 8; k++)
-                        if (j + k < hidden) u[k >> 1] |= (uint32_t)row[q][j + k] << ((k & 1) * 16);
-                    r[q] = make_uint4(u[0], u[1], u[2], u[3]);
-                }
+                for (int k = 0; k < 8; k++)
+                    if (e + k < hidden) u[k >> 1] |= (uint32_t)row[q][e + k] << ((k & 1) * 16);
+                r[q] = make_uint4(u[0], u[1], u[2], u[3]);
             }
-            add(r, j);
+            add(r, e);
         }
 #pragma unroll
         for (int q = 0; q < R; q++) {
@@ -871,8 +858,8 @@ int sm_count()
 template <int EPI, int DT, bool A_MN, bool B_MN>
 cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t s)
 {
-    const void* k = (const void*)k_ce_gemm<EPI, DT, A_MN, B_MN>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kCeSmem);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem((const void*)k_ce_gemm<EPI, DT, A_MN, B_MN>, kCeSmem, done);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)g.m_tiles * g.n_tiles * g.splits;
     const int64_t pairs = sm_count() / 2;
@@ -885,8 +872,8 @@ cudaError_t launch_few_t(const zero_ce_plan_t& p, const void* x, const void* w, 
                          const JoinArgs& j, cudaStream_t s)
 {
     const size_t bytes = (size_t)(T * ((p.hidden + 7) / 8 * 8) * 2);
-    const cudaError_t e = cudaFuncSetAttribute((const void*)k_ce_few<DT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kFewSmem);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem((const void*)k_ce_few<DT, T>, kFewSmem, done);
     if (e != cudaSuccess) return e;
     k_ce_few<DT, T><<<(unsigned)few_blocks(p), kFewThreads, bytes, s>>>(
         static_cast<const uint16_t*>(x), p.x_stride, static_cast<const uint16_t*>(w), p.w_stride, p.hidden,

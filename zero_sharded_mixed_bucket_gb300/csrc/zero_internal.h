@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "zero_gb300.h"
 
 namespace zg {
@@ -182,6 +184,19 @@ template <typename K>
 inline cudaError_t launch_step_kernel(K kernel, int grid, cudaStream_t s, bool overlap, const StepArgs& a)
 {
     return launch_kernel(kernel, grid, kThreads, s, overlap, a);
+}
+
+// Raise a kernel's limit of dynamic shared memory to `bytes`, once per kernel
+// and device; `done` is the kernel's own mark of the devices that have it.
+inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = 1ull << (dev & 63);
+    if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_acquire) & bit))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
+    return e;
 }
 
 // Grid for a grid-stride kernel over `groups` work items of kThreads-thread

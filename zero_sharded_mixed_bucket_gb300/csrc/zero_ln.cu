@@ -11,6 +11,9 @@ namespace zg {
 namespace {
 
 constexpr int kLnThreads = 256;
+constexpr int kLnFwdAhead = 2, kLnBwdAhead = 2;   // batches of rows on their way or in use
+constexpr int kLnFwdRows = 8, kLnBwdRows = 4;     // rows of a batch, at one vector a lane
+constexpr int kLnFwdBlocks = 3, kLnBwdBlocks = 2; // blocks of 256 threads resident on an SM
 
 struct LnArgs {
     const void* x;
@@ -26,6 +29,7 @@ struct LnArgs {
     float* part;                 // [blocks][2][dim]: partial dweight, dbias
     int64_t rows, dim, x_stride, y_stride;
     float eps;
+    int warps;                   // of a group (row kernels)
 };
 
 template <int DT>
@@ -67,51 +71,93 @@ __device__ __forceinline__ float block_sum(float v, float* sh)
     return t;
 }
 
-// ---- rows in registers ---------------------------------------------------------------
-// Rows on 16-byte boundaries are held in registers, as they were loaded, from
-// the one time they are read: a group of 32 W lanes takes RB rows at a time,
-// all their loads issued at once, V 16-byte vectors to a lane.  A row's ragged
-// end is loaded value by value by the lane that has it.
-
-// Values of vector v of lane gl that exist.
-template <int DT, int W>
-__device__ __forceinline__ int vec_count(int64_t dim, int v, int gl)
+// ---- rows on 16-byte boundaries --------------------------------------------------------
+// A group of lanes takes RB rows at a time, V 16-byte vectors of a row to a
+// lane: W warps (V > 1 only where 8 warps are not enough), or L < 32 lanes of
+// one for short rows.  A block is as many groups as fit 8 warps.  Each lane
+// copies its vectors ahead of their use into slots of shared memory of its own
+// (cp.async; a row's ragged end is filled with zeros), S batches deep: the
+// bytes in flight do not depend on registers or on how far the other lanes
+// are, and nothing waits but a lane for its own copies.  The rows stay there
+// until they are done, read again for each use.
+// What bounds these kernels is issuing instructions (about 12 a value forward,
+// 20 backward, where the memory's rate leaves room for 20 to 30), so a batch
+// is as large as that allows: its sums, addresses and loop are shared
+// by all its values.
+__device__ __forceinline__ void copy_ahead(void* smem, const void* src, int bytes)
 {
-    constexpr int VE = kVecOf<DT>;
-    return (int)max((int64_t)0, min((int64_t)VE, dim - (int64_t)(v * 32 * W + gl) * VE));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 :: "r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(src), "r"(bytes) : "memory");
 }
 
-// Sums over the group of n values at once, the same in every lane.  sh: room
-// for [2][8 warps][n] of the block; `turn` alternates, so one barrier a call.
-template <int W, int N>
-__device__ __forceinline__ void group_sum(float (&x)[N], float* sh, int& turn)
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int PENDING>
+__device__ __forceinline__ void copies_wait()
 {
+    asm volatile("cp.async.wait_group %0;" :: "n"(PENDING) : "memory");
+}
+
+// Values of vector v of lane gl of a group of `lanes` that exist.
+template <int DT>
+__device__ __forceinline__ int vec_count(int64_t dim, int v, int gl, int lanes)
+{
+    constexpr int VE = kVecOf<DT>;
+    return (int)max((int64_t)0, min((int64_t)VE, dim - (int64_t)(v * lanes + gl) * VE));
+}
+
+// Lane l gets the sum over its L lanes (L <= 32) of value l % N (N a power of
+// two up to L): each step halves the values a lane still has, sending the
+// others' half away.
+template <int L, int N>
+__device__ __forceinline__ float lane_sums(float (&x)[N])
+{
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int h = N / 2; h > 0; h /= 2) {
+        const bool up = lane & h;
 #pragma unroll
-        for (int k = 0; k < N; k++)
-            x[k] += __shfl_xor_sync(0xffffffffu, x[k], o);
-    if constexpr (W > 1) {
-        const int warp = threadIdx.x >> 5, first = warp / W * W;
-        float* slot = sh + (turn & 1) * (kLnThreads / 32) * N;
-        if ((threadIdx.x & 31) == 0)
-#pragma unroll
-            for (int k = 0; k < N; k++)
-                slot[warp * N + k] = x[k];
-        if constexpr (W == kLnThreads / 32)
-            __syncthreads();
-        else
-            asm volatile("bar.sync %0, %1;" :: "r"(1 + first / W), "r"(32 * W) : "memory");
-#pragma unroll
-        for (int k = 0; k < N; k++) {
-            float t = slot[first * N + k];
-#pragma unroll
-            for (int q = 1; q < W; q++)
-                t += slot[(first + q) * N + k];
-            x[k] = t;
+        for (int k = 0; k < h; k++) {
+            const float keep = up ? x[k + h] : x[k], send = up ? x[k] : x[k + h];
+            x[k] = keep + __shfl_xor_sync(0xffffffffu, send, h);
         }
+    }
+    float s = x[0];
+#pragma unroll
+    for (int o = N; o < L; o <<= 1)
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+
+// Sums over the group of N values at once, the same in every lane.  sh: room
+// for [2][8 warps][N] of the block; `turn` alternates, so one barrier a call.
+template <int L, int N>
+__device__ __forceinline__ void group_sum(float (&x)[N], int warps, float* sh, int& turn)
+{
+    const int lane = threadIdx.x & 31;
+    float s = lane_sums<L, N>(x);
+    if (L == 32 && warps > 1) {
+        const int warp = threadIdx.x >> 5, group = warp / warps;
+        float* slot = sh + (turn & 1) * (kLnThreads / 32) * N;
+        if (lane < N) slot[warp * N + lane] = s;
+        asm volatile("bar.sync %0, %1;" :: "r"(1 + group), "r"(32 * warps) : "memory");
+        // lane l: value l % N of every (32 / N)th warp; then a tree over the lanes of
+        // the same value
+        s = 0.0f;
+        slot += group * warps * N;
+#pragma unroll
+        for (int q = 0; q < (kLnThreads / 32 * N + 31) / 32; q++) {
+            const int at = lane + 32 * q;
+            if (at < warps * N) s += slot[at];
+        }
+#pragma unroll
+        for (int o = N; o < 32; o <<= 1)
+            s += __shfl_xor_sync(0xffffffffu, s, o);
         turn++;
     }
+#pragma unroll
+    for (int k = 0; k < N; k++)
+        x[k] = __shfl_sync(0xffffffffu, s, k, L);
 }
 
 template <int DT>
@@ -168,216 +214,337 @@ __device__ __forceinline__ void ld_weight(const void* p, int64_t i, int cnt, flo
     }
 }
 
-template <int DT, int W, int V, int RB>
-__global__ void __launch_bounds__(kLnThreads) k_ln_forward_reg(const __grid_constant__ LnArgs a)
+template <int DT>
+__device__ __forceinline__ Vals<DT> from_slot(const uint4* slot)
 {
-    constexpr int VE = kVecOf<DT>, G = 32 * W, kGroups = kLnThreads / G;
-    __shared__ float sh[2 * (kLnThreads / 32) * RB];
-    const int gl = threadIdx.x % G;
+    const uint4 u = *slot;
+    Vals<DT> v;
+    v.w[0] = u.x; v.w[1] = u.y; v.w[2] = u.z; v.w[3] = u.w;
+    return v;
+}
+
+// 16 bytes, streaming.
+__device__ __forceinline__ void store16(char* p, const uint32_t w[4])
+{
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+}
+
+// A lane's vector out: all of it, or (RAGGED) the values that exist.
+template <int DT, bool RAGGED>
+__device__ __forceinline__ void store_vec(char* p, const Vals<DT>& v, int cnt)
+{
+    if (!RAGGED || cnt == kVecOf<DT>)
+        store16(p, v.w);
+    else
+        st_vals<DT>(p, 0, v, cnt);
+}
+
+template <int DT, bool RAGGED>
+__device__ __forceinline__ void weight_vec(const void* p, int64_t i, int cnt, float fill, float f[kVecOf<DT>])
+{
+    ld_weight<DT>(p, i, RAGGED ? cnt : kVecOf<DT>, fill, f);
+}
+
+// Rows of a group still to come, from this one on, that a batch of RB takes.
+__device__ __forceinline__ int rows_here(int64_t rows, int64_t r0, int RB)
+{
+    return (int)max((int64_t)0, min((int64_t)RB, rows - r0));
+}
+
+// Forward.  A lane's values are unpacked once for both statistics: with the
+// lane's own sum s and sum of squares m2 about its own mean, the row's sum of
+// squares about its mean is the sum of m2 + n (s/n - mean)^2 over the lanes.
+// RAGGED: dim is not a multiple of a vector's values.
+template <int DT, int L, int V, int RB, int S, int BLOCKS, bool RAGGED>
+__global__ void __launch_bounds__(kLnThreads, BLOCKS) k_ln_forward_rows(const __grid_constant__ LnArgs a)
+{
+    constexpr int VE = kVecOf<DT>, E = DT == kF32 ? 4 : 2, T = kLnThreads;
+    extern __shared__ uint4 slots[];                  // [S][RB * V][T]
+    __shared__ float sh[2 * (T / 32) * RB];
+    const int lanes = L < 32 ? L : 32 * a.warps, gl = threadIdx.x % lanes, group = threadIdx.x / lanes;
+    const int groups = blockDim.x / lanes;
     const float inv = 1.0f / (float)a.dim;
     int turn = 0;
-    const int64_t stride = (int64_t)gridDim.x * kGroups * RB;
-    for (int64_t r0 = ((int64_t)blockIdx.x * kGroups + threadIdx.x / G) * RB; r0 < a.rows; r0 += stride) {
-        Vals<DT> q[RB][V];
-        float mean[RB], rstd[RB];
+    int cnt[V], have = 0;
 #pragma unroll
-        for (int b = 0; b < RB; b++)
+    for (int v = 0; v < V; v++) {
+        cnt[v] = vec_count<DT>(a.dim, v, gl, lanes);
+        have += cnt[v];
+    }
+    const float n = (float)have, inv_n = have ? 1.0f / n : 0.0f;
+    const int64_t stride = (int64_t)gridDim.x * groups * RB;
+    int64_t r0 = ((int64_t)blockIdx.x * groups + group) * RB;
+    int64_t ahead = r0;
+    const int64_t x_row = a.x_stride * E, y_row = a.y_stride * E;
+    const int apart = lanes * 16;                     // bytes between a lane's vectors
+    const char* src = static_cast<const char*>(a.x) + r0 * x_row + gl * 16;
+    char* dst = static_cast<char*>(a.y) + r0 * y_row + gl * 16;
+    uint4* const mine = slots + threadIdx.x;
+    auto fetch = [&](uint4* at) {
+        const int here = rows_here(a.rows, ahead, RB);
+        const char* p = src;
 #pragma unroll
-            for (int v = 0; v < V; v++)               // rows past the end: the last one again, not written
-                q[b][v] = ld_vals<DT>(a.x, min(r0 + b, a.rows - 1) * a.x_stride + (int64_t)(v * G + gl) * VE,
-                                      vec_count<DT, W>(a.dim, v, gl));
+        for (int b = 0; b < RB; b++, p += x_row)
+            if (b < here)
+#pragma unroll
+                for (int v = 0; v < V; v++)
+                    if (cnt[v]) copy_ahead(at + (b * V + v) * T, p + v * apart, RAGGED ? cnt[v] * E : 16);
+        copies_issued();
+        ahead += stride;
+        src += stride * x_row;
+    };
+#pragma unroll
+    for (int k = 0; k < S * RB * V; k++)              // vectors past the row's end are never copied: 0
+        if (cnt[k % V] == 0) mine[k * T] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < S; k++)
+        fetch(mine + k * RB * V * T);
+    // groups of less than a warp go round together: their sums shuffle across the warp
+    const int64_t first = L < 32 ? r0 - (int64_t)((threadIdx.x & 31) / L) * RB : r0;
+    int slot = 0;
+    for (int64_t rw = first; rw < a.rows; rw += stride) {
+        copies_wait<S - 1>();
+        uint4* const q = mine + slot * RB * V * T;    // rows past the end: whatever is there, not written
+        float mean[RB], rstd[RB], own[RB];
 #pragma unroll
         for (int b = 0; b < RB; b++) {
-            float s = 0.0f;
+            float f[V][VE], s = 0.0f, m2 = 0.0f;
 #pragma unroll
             for (int v = 0; v < V; v++) {
-                float f[VE];
-                unpack<DT>(q[b][v], f);               // values past the row's end are 0
+                unpack<DT>(from_slot<DT>(q + (b * V + v) * T), f[v]);
 #pragma unroll
                 for (int k = 0; k < VE; k++)
-                    s += f[k];
+                    s += f[v][k];
+            }
+            own[b] = s * inv_n;
+#pragma unroll
+            for (int v = 0; v < V; v++) {
+                if (!RAGGED && V > 1 && cnt[v] == 0) continue;    // no distance past the end
+                if (RAGGED)
+#pragma unroll
+                    for (int k = 0; k < VE; k++)
+                        f[v][k] = k < cnt[v] ? f[v][k] : own[b];
+#pragma unroll
+                for (int k = 0; k < VE; k++) {
+                    const float c = f[v][k] - own[b];
+                    m2 = fmaf(c, c, m2);
+                }
             }
             mean[b] = s;
+            rstd[b] = m2;
         }
-        group_sum<W, RB>(mean, sh, turn);
+        group_sum<L, RB>(mean, a.warps, sh, turn);
 #pragma unroll
         for (int b = 0; b < RB; b++) {
             mean[b] *= inv;
-            float s = 0.0f;
-#pragma unroll
-            for (int v = 0; v < V; v++) {
-                const int cnt = vec_count<DT, W>(a.dim, v, gl);
-                float f[VE];
-                unpack<DT>(q[b][v], f);
-                if (cnt == VE) {
-#pragma unroll
-                    for (int k = 0; k < VE; k++) {
-                        const float c = f[k] - mean[b];
-                        s = fmaf(c, c, s);
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < VE; k++) {
-                        const float c = k < cnt ? f[k] - mean[b] : 0.0f;
-                        s = fmaf(c, c, s);
-                    }
-                }
-            }
-            rstd[b] = s;
+            const float c = own[b] - mean[b];
+            rstd[b] = have ? fmaf(n * c, c, rstd[b]) : 0.0f;
         }
-        group_sum<W, RB>(rstd, sh, turn);
+        group_sum<L, RB>(rstd, a.warps, sh, turn);
+        const int here = rows_here(a.rows, r0, RB);
 #pragma unroll
         for (int b = 0; b < RB; b++)
-            rstd[b] = 1.0f / sqrtf(fmaf(rstd[b], inv, a.eps));
+            rstd[b] = rsqrtf(fmaf(rstd[b], inv, a.eps));
 #pragma unroll
         for (int v = 0; v < V; v++) {
-            const int cnt = vec_count<DT, W>(a.dim, v, gl);
-            const int64_t j = (int64_t)(v * G + gl) * VE;
-            if (cnt == 0) continue;
+            if (cnt[v] == 0) continue;
+            const int64_t j = (int64_t)(v * lanes + gl) * VE;
             float w[VE], bias[VE];
-            ld_weight<DT>(a.weight, j, cnt, 1.0f, w);
-            ld_weight<DT>(a.bias, j, cnt, 0.0f, bias);
+            weight_vec<DT, RAGGED>(a.weight, j, cnt[v], 1.0f, w);
+            weight_vec<DT, RAGGED>(a.bias, j, cnt[v], 0.0f, bias);
+            char* p = dst + v * apart;
 #pragma unroll
-            for (int b = 0; b < RB; b++) {
-                if (r0 + b >= a.rows) break;
+            for (int b = 0; b < RB; b++, p += y_row) {
                 float f[VE];
-                unpack<DT>(q[b][v], f);
+                unpack<DT>(from_slot<DT>(q + (b * V + v) * T), f);
 #pragma unroll
                 for (int k = 0; k < VE; k++)
                     f[k] = fmaf((f[k] - mean[b]) * rstd[b], w[k], bias[k]);
-                st_vals<DT>(a.y, (r0 + b) * a.y_stride + j, pack<DT>(f), cnt);
+                if (b < here) store_vec<DT, RAGGED>(p, pack<DT>(f), cnt[v]);
             }
         }
         if (gl == 0) {
 #pragma unroll
             for (int b = 0; b < RB; b++) {
-                if (r0 + b >= a.rows) break;
-                if (a.mean) a.mean[r0 + b] = mean[b];
-                if (a.rstd) a.rstd[r0 + b] = rstd[b];
+                if (b < here && a.mean) a.mean[r0 + b] = mean[b];
+                if (b < here && a.rstd) a.rstd[r0 + b] = rstd[b];
             }
         }
+        fetch(q);
+        slot = slot == S - 1 ? 0 : slot + 1;
+        r0 += stride;
+        dst += stride * y_row;
     }
+    copies_wait<0>();
 }
 
-// dx of a row group, and the column sums of dy * xhat and dy over all its
-// rows in registers: x and dy are read once for both.  A block writes one
-// pair of partial sums per column (its groups joined in group order).
-template <int DT, int W, int V, int RB>
-__global__ void __launch_bounds__(kLnThreads) k_ln_backward_reg(const __grid_constant__ LnArgs a)
+// Backward: dx of the rows, and the column sums of dy * xhat and dy over all
+// the rows of a lane in registers, so x and dy are read once for both.  A
+// block writes one pair of partial sums per column (its groups joined in group
+// order).  With d = x - mean and g = dy * weight:
+//   dx = rstd g - rstd avg(g) - rstd^3 avg(g d) d;  dweight = sum (dy rstd) d
+template <int DT, int L, int V, int RB, int S, int BLOCKS, bool RAGGED>
+__global__ void __launch_bounds__(kLnThreads, BLOCKS) k_ln_backward_rows(const __grid_constant__ LnArgs a)
 {
-    constexpr int VE = kVecOf<DT>, G = 32 * W, kGroups = kLnThreads / G;
-    __shared__ float sh[2 * (kLnThreads / 32) * 2 * RB];
-    __shared__ float join[kGroups > 1 ? 2 * V * G * VE : 1];
-    const int gl = threadIdx.x % G, group = threadIdx.x / G;
+    constexpr int VE = kVecOf<DT>, E = DT == kF32 ? 4 : 2, T = kLnThreads;
+    extern __shared__ uint4 slots[];                  // [S][RB * V][x, dy][T]; at the end the groups' sums
+    __shared__ float sh[2 * (T / 32) * 2 * RB];
+    const int lanes = L < 32 ? L : 32 * a.warps, gl = threadIdx.x % lanes, group = threadIdx.x / lanes;
+    const int groups = blockDim.x / lanes;
     const float inv = 1.0f / (float)a.dim;
     int turn = 0;
+    int cnt[V];
     float dw[V][VE], db[V][VE];
 #pragma unroll
-    for (int v = 0; v < V; v++)
+    for (int v = 0; v < V; v++) {
+        cnt[v] = vec_count<DT>(a.dim, v, gl, lanes);
 #pragma unroll
         for (int k = 0; k < VE; k++)
             dw[v][k] = db[v][k] = 0.0f;
-    const int64_t stride = (int64_t)gridDim.x * kGroups * RB;
-    for (int64_t r0 = ((int64_t)blockIdx.x * kGroups + group) * RB; r0 < a.rows; r0 += stride) {
-        Vals<DT> x[RB][V], dy[RB][V];
+    }
+    const int64_t stride = (int64_t)gridDim.x * groups * RB;
+    int64_t r0 = ((int64_t)blockIdx.x * groups + group) * RB;
+    int64_t ahead = r0;
+    const int64_t x_row = a.x_stride * E, y_row = a.y_stride * E;
+    const int apart = lanes * 16;
+    const char* sx = static_cast<const char*>(a.x) + r0 * x_row + gl * 16;
+    const char* sy = static_cast<const char*>(a.dy) + r0 * y_row + gl * 16;
+    char* dst = static_cast<char*>(a.dx) + r0 * x_row + gl * 16;
+    uint4* const mine = slots + threadIdx.x;
+    auto fetch = [&](uint4* at) {
+        const int here = rows_here(a.rows, ahead, RB);
+        const char *px = sx, *py = sy;
+#pragma unroll
+        for (int b = 0; b < RB; b++, px += x_row, py += y_row)
+#pragma unroll
+            for (int v = 0; v < V; v++) {
+                uint4* p = at + (b * V + v) * 2 * T;
+                if (b < here) {
+                    if (cnt[v]) {
+                        copy_ahead(p, px + v * apart, RAGGED ? cnt[v] * E : 16);
+                        copy_ahead(p + T, py + v * apart, RAGGED ? cnt[v] * E : 16);
+                    }
+                } else {                              // rows past the end: all 0
+                    p[0] = p[T] = make_uint4(0, 0, 0, 0);
+                }
+            }
+        copies_issued();
+        ahead += stride;
+        sx += stride * x_row;
+        sy += stride * y_row;
+    };
+    float nmean[RB], nrstd[RB];
+    auto fetch_stats = [&](int64_t from) {
+        const int here = rows_here(a.rows, from, RB);
+#pragma unroll
+        for (int b = 0; b < RB; b++) {
+            nmean[b] = b < here ? a.mean_in[from + b] : 0.0f;
+            nrstd[b] = b < here ? a.rstd_in[from + b] : 0.0f;
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < S * RB * V * 2; k++)          // vectors past the row's end are never copied: 0
+        if (cnt[k / 2 % V] == 0) mine[k * T] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < S; k++)
+        fetch(mine + k * RB * V * 2 * T);
+    fetch_stats(r0);
+    const int64_t first = L < 32 ? r0 - (int64_t)((threadIdx.x & 31) / L) * RB : r0;
+    int slot = 0;
+    for (int64_t rw = first; rw < a.rows; rw += stride) {
+        copies_wait<S - 1>();
+        uint4* const q = mine + slot * RB * V * 2 * T;
         float mean[RB], rstd[RB], c[2 * RB];
 #pragma unroll
         for (int b = 0; b < RB; b++) {
-            const int64_t r = min(r0 + b, a.rows - 1);
-#pragma unroll
-            for (int v = 0; v < V; v++) {
-                const int cnt = r0 + b < a.rows ? vec_count<DT, W>(a.dim, v, gl) : 0;   // rows past the end are 0
-                const int64_t j = (int64_t)(v * G + gl) * VE;
-                x[b][v] = ld_vals<DT>(a.x, r * a.x_stride + j, cnt);
-                dy[b][v] = ld_vals<DT>(a.dy, r * a.y_stride + j, cnt);
-            }
-            mean[b] = a.mean_in[r];
-            rstd[b] = a.rstd_in[r];
+            mean[b] = nmean[b];
+            rstd[b] = nrstd[b];
             c[2 * b] = c[2 * b + 1] = 0.0f;
         }
+        fetch_stats(r0 + stride);
 #pragma unroll
         for (int v = 0; v < V; v++) {
-            const int cnt = vec_count<DT, W>(a.dim, v, gl);
-            const int64_t j = (int64_t)(v * G + gl) * VE;
+            if (cnt[v] == 0) continue;
             float w[VE];
-            ld_weight<DT>(a.weight, j, cnt, 1.0f, w);
+            weight_vec<DT, RAGGED>(a.weight, (int64_t)(v * lanes + gl) * VE, cnt[v], 1.0f, w);
 #pragma unroll
             for (int b = 0; b < RB; b++) {
                 float xf[VE], yf[VE];
-                unpack<DT>(x[b][v], xf);
-                unpack<DT>(dy[b][v], yf);             // 0 past the ends: adds nothing below, while x is finite
+                unpack<DT>(from_slot<DT>(q + (b * V + v) * 2 * T), xf);
+                unpack<DT>(from_slot<DT>(q + ((b * V + v) * 2 + 1) * T), yf);   // 0 past the ends
 #pragma unroll
                 for (int k = 0; k < VE; k++) {
-                    const float h = (xf[k] - mean[b]) * rstd[b], g = yf[k] * w[k];
-                    if (r0 + b < a.rows) {
-                        dw[v][k] = fmaf(yf[k], h, dw[v][k]);
-                        db[v][k] += yf[k];
-                    }
+                    const float d = xf[k] - mean[b], g = yf[k] * w[k];
+                    dw[v][k] = fmaf(yf[k] * rstd[b], d, dw[v][k]);
+                    db[v][k] += yf[k];
                     c[2 * b] += g;
-                    c[2 * b + 1] = fmaf(g, h, c[2 * b + 1]);
+                    c[2 * b + 1] = fmaf(g, d, c[2 * b + 1]);
                 }
             }
         }
-        if (!a.dx) continue;
-        group_sum<W, 2 * RB>(c, sh, turn);
-#pragma unroll
-        for (int v = 0; v < V; v++) {
-            const int cnt = vec_count<DT, W>(a.dim, v, gl);
-            const int64_t j = (int64_t)(v * G + gl) * VE;
-            if (cnt == 0) continue;
-            float w[VE];
-            ld_weight<DT>(a.weight, j, cnt, 1.0f, w);
+        if (a.dx) {
+            group_sum<L, 2 * RB>(c, a.warps, sh, turn);
+            const int here = rows_here(a.rows, r0, RB);
 #pragma unroll
             for (int b = 0; b < RB; b++) {
-                if (r0 + b >= a.rows) break;
-                float xf[VE], yf[VE];
-                unpack<DT>(x[b][v], xf);
-                unpack<DT>(dy[b][v], yf);
-                const float c1 = c[2 * b] * inv, c2 = c[2 * b + 1] * inv;
+                c[2 * b] = -(c[2 * b] * inv) * rstd[b];
+                c[2 * b + 1] = -(c[2 * b + 1] * inv * rstd[b]) * rstd[b] * rstd[b];
+            }
 #pragma unroll
-                for (int k = 0; k < VE; k++) {
-                    const float h = (xf[k] - mean[b]) * rstd[b];
-                    xf[k] = (fmaf(yf[k], w[k], -c1) - h * c2) * rstd[b];
+            for (int v = 0; v < V; v++) {
+                if (cnt[v] == 0) continue;
+                float w[VE];
+                weight_vec<DT, RAGGED>(a.weight, (int64_t)(v * lanes + gl) * VE, cnt[v], 1.0f, w);
+                char* p = dst + v * apart;
+#pragma unroll
+                for (int b = 0; b < RB; b++, p += x_row) {
+                    float xf[VE], yf[VE];
+                    unpack<DT>(from_slot<DT>(q + (b * V + v) * 2 * T), xf);
+                    unpack<DT>(from_slot<DT>(q + ((b * V + v) * 2 + 1) * T), yf);
+#pragma unroll
+                    for (int k = 0; k < VE; k++)
+                        xf[k] = fmaf(xf[k] - mean[b], c[2 * b + 1], fmaf(yf[k] * w[k], rstd[b], c[2 * b]));
+                    if (b < here) store_vec<DT, RAGGED>(p, pack<DT>(xf), cnt[v]);
                 }
-                st_vals<DT>(a.dx, (r0 + b) * a.x_stride + j, pack<DT>(xf), cnt);
             }
         }
+        fetch(q);
+        slot = slot == S - 1 ? 0 : slot + 1;
+        r0 += stride;
+        dst += stride * x_row;
     }
+    copies_wait<0>();
     if (!a.part) return;
-    if constexpr (kGroups > 1) {
-        for (int g = 1; g < kGroups; g++) {           // group g's sums through shared memory to group 0
-            __syncthreads();
-            if (group == g)
-#pragma unroll
-                for (int v = 0; v < V; v++)
-#pragma unroll
-                    for (int k = 0; k < VE; k++) {
-                        join[(v * VE + k) * G + gl] = dw[v][k];
-                        join[((V + v) * VE + k) * G + gl] = db[v][k];
-                    }
-            __syncthreads();
-            if (group == 0)
-#pragma unroll
-                for (int v = 0; v < V; v++)
-#pragma unroll
-                    for (int k = 0; k < VE; k++) {
-                        dw[v][k] += join[(v * VE + k) * G + gl];
-                        db[v][k] += join[((V + v) * VE + k) * G + gl];
-                    }
-        }
-        if (group != 0) return;
-    }
     float* pw = a.part + 2 * (int64_t)blockIdx.x * a.dim;
+    if (V == 1 && groups > 1) {
+        float* join = reinterpret_cast<float*>(slots);            // [group][dw, db][VE][lanes]: no more than the slots
+        const int one = 2 * VE * lanes;
+        __syncthreads();
 #pragma unroll
-    for (int v = 0; v < V; v++) {
-        const int cnt = vec_count<DT, W>(a.dim, v, gl);
-        const int64_t j = (int64_t)(v * G + gl) * VE;
+        for (int k = 0; k < VE; k++) {
+            join[group * one + k * lanes + gl] = dw[0][k];
+            join[group * one + (VE + k) * lanes + gl] = db[0][k];
+        }
+        __syncthreads();
+        for (int t = threadIdx.x; t < one; t += blockDim.x) {
+            float s = 0.0f;
+            for (int g = 0; g < groups; g++)
+                s += join[g * one + t];
+            const int k = t / lanes;                              // 0..2 VE - 1
+            const int64_t j = (int64_t)(t - k * lanes) * VE + (k < VE ? k : k - VE);
+            if (j < a.dim) pw[(k < VE ? 0 : a.dim) + j] = s;
+        }
+    } else {
 #pragma unroll
-        for (int k = 0; k < VE; k++)
-            if (k < cnt) {
-                pw[j + k] = dw[v][k];
-                pw[a.dim + j + k] = db[v][k];
-            }
+        for (int v = 0; v < V; v++) {
+            float* at = pw + (int64_t)(v * lanes + gl) * VE;
+#pragma unroll
+            for (int k = 0; k < VE; k++)
+                if (k < cnt[v]) {
+                    at[k] = dw[v][k];
+                    at[a.dim + k] = db[v][k];
+                }
+        }
     }
 }
 
@@ -455,19 +622,19 @@ __global__ void __launch_bounds__(kLnThreads) k_ln_dw_part(const __grid_constant
     a.part[(2 * (int64_t)blockIdx.y + 1) * a.dim + j] = db;
 }
 
-// The blocks' partial sums: 32 columns a block, its 8 warps a part of the
+// The blocks' partial sums: 32 columns a block, its 32 warps a part of the
 // partial sums each, joined in warp order.
 template <int DT>
-__global__ void __launch_bounds__(kLnThreads) k_ln_dw_sum(const float* part, int blocks, int64_t dim, void* dw, void* db)
+__global__ void __launch_bounds__(1024) k_ln_dw_sum(const float* part, int blocks, int64_t dim, void* dw, void* db)
 {
     wait_prev_grid();                                 // launched while the row kernel drains
-    __shared__ float sh[2][kLnThreads / 32][32];
+    __shared__ float sh[2][32][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t j = (int64_t)blockIdx.x * 32 + lane;
     float s = 0.0f, t = 0.0f;
     if (j < dim)
-#pragma unroll 4
-        for (int k = warp; k < blocks; k += kLnThreads / 32) {
+#pragma unroll 5
+        for (int k = warp; k < blocks; k += 32) {
             s += part[(2 * (int64_t)k) * dim + j];
             t += part[(2 * (int64_t)k + 1) * dim + j];
         }
@@ -475,7 +642,7 @@ __global__ void __launch_bounds__(kLnThreads) k_ln_dw_sum(const float* part, int
     sh[1][warp][lane] = t;
     __syncthreads();
     if (warp > 0 || j >= dim) return;
-    for (int k = 1; k < kLnThreads / 32; k++) {
+    for (int k = 1; k < 32; k++) {
         s += sh[0][k][lane];
         t += sh[1][k][lane];
     }
@@ -503,33 +670,101 @@ zero_status_t check_ln_plan(const zero_ln_plan_t* p)
     return ZERO_OK;
 }
 
-template <typename K>
-cudaError_t launch_rows(K kernel, const LnArgs& a, int64_t rows_per_block, int most, cudaStream_t s)
+constexpr int kSms = 152;
+
+cudaError_t launch_rows(void (*kernel)(const LnArgs), const LnArgs& a, int64_t blocks, int threads, size_t smem,
+                        cudaStream_t s)
 {
-    const int64_t need = (a.rows + rows_per_block - 1) / rows_per_block;
-    kernel<<<(unsigned)(need < most ? need : most), kLnThreads, 0, s>>>(a);
+    kernel<<<(unsigned)blocks, threads, smem, s>>>(a);
     return cudaGetLastError();
 }
 
-// Blocks of a row kernel: as many as are resident at once on the GPU's 152
-// SMs, each striding over the rows.
-constexpr int kSms = 152;
+// A row kernel; SMEM bytes of slots, its static part with them over the
+// default limit.
+template <void (*KERNEL)(const LnArgs), size_t SMEM>
+cudaError_t launch_slots(const LnArgs& a, int64_t blocks, int threads, cudaStream_t s)
+{
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem((const void*)KERNEL, (int)SMEM, done);
+    return e == cudaSuccess ? launch_rows(KERNEL, a, blocks, threads, SMEM, s) : e;
+}
+
+// How rows of `vecs` 16-byte vectors are dealt out.
+struct RowShape {
+    int warps;                   // of a group
+    int threads;                 // of a block
+    int groups;                  // of a block
+};
+
+RowShape shape_of(int64_t vecs, int L, int V)
+{
+    RowShape r;
+    if (L < 32) {
+        r.warps = 1;
+        r.threads = kLnThreads;
+        r.groups = kLnThreads / L;
+    } else {
+        r.warps = (int)((vecs + 32 * V - 1) / (32 * V));
+        r.groups = kLnThreads / 32 / r.warps;
+        r.threads = 32 * r.warps * r.groups;
+    }
+    return r;
+}
+
+template <int DT, int L, int V, int RB, int S, int BLOCKS>
+cudaError_t forward_rows(LnArgs a, int64_t vecs, cudaStream_t s)
+{
+    const RowShape h = shape_of(vecs, L, V);
+    a.warps = h.warps;
+    const int64_t at_once = (int64_t)h.groups * RB, need = (a.rows + at_once - 1) / at_once;
+    const int64_t most = (int64_t)kSms * (BLOCKS * kLnThreads / h.threads);   // resident at once
+    const int64_t blocks = need < most ? need : most;
+    constexpr size_t smem = (size_t)S * RB * V * kLnThreads * 16;
+    if (a.dim % kVecOf<DT>)
+        return launch_slots<k_ln_forward_rows<DT, 32, V, RB, S, BLOCKS, true>, smem>(a, blocks, h.threads, s);
+    return launch_slots<k_ln_forward_rows<DT, L, V, RB, S, BLOCKS, false>, smem>(a, blocks, h.threads, s);
+}
 
 template <int DT>
 cudaError_t forward(const LnArgs& a, bool vec, cudaStream_t s)
 {
     constexpr int VE = kVecOf<DT>;
     const int64_t vecs = (a.dim + VE - 1) / VE;
-    // a warp per row while a lane's part fits its registers (16 vectors), then
-    // a block; short rows several at a time
-    if (vec && vecs <= 32) return launch_rows(k_ln_forward_reg<DT, 1, 1, 4>, a, 32, kSms * 8, s);
-    if (vec && vecs <= 64) return launch_rows(k_ln_forward_reg<DT, 1, 2, 2>, a, 16, kSms * 8, s);
-    if (vec && vecs <= 128) return launch_rows(k_ln_forward_reg<DT, 1, 4, 2>, a, 16, kSms * 4, s);
-    if (vec && vecs <= 256) return launch_rows(k_ln_forward_reg<DT, 1, 8, 1>, a, 8, kSms * 4, s);
-    if (vec && vecs <= 512) return launch_rows(k_ln_forward_reg<DT, 8, 2, 2>, a, 2, kSms * 6, s);
-    if (vec && vecs <= 1024) return launch_rows(k_ln_forward_reg<DT, 8, 4, 1>, a, 1, kSms * 6, s);
-    if (vec && vecs <= 2048) return launch_rows(k_ln_forward_reg<DT, 8, 8, 1>, a, 1, kSms * 4, s);
-    return launch_rows(k_ln_forward<DT>, a, 1, kSms * 8, s);
+    const bool whole = a.dim % VE == 0;
+    if (vec && whole && vecs <= 8) return forward_rows<DT, 8, 1, kLnFwdRows, kLnFwdAhead, kLnFwdBlocks>(a, vecs, s);
+    if (vec && whole && vecs <= 16) return forward_rows<DT, 16, 1, kLnFwdRows, kLnFwdAhead, kLnFwdBlocks>(a, vecs, s);
+    if (vec && vecs <= 256) return forward_rows<DT, 32, 1, kLnFwdRows, kLnFwdAhead, kLnFwdBlocks>(a, vecs, s);
+    if (vec && vecs <= 512) return forward_rows<DT, 32, 2, kLnFwdRows / 2, kLnFwdAhead, kLnFwdBlocks>(a, vecs, s);
+    if (vec && vecs <= 1024) return forward_rows<DT, 32, 4, kLnFwdRows / 4, kLnFwdAhead, kLnFwdBlocks>(a, vecs, s);
+    if (vec && vecs <= 2048) return forward_rows<DT, 32, 8, 1, 2, 2>(a, vecs, s);
+    return launch_rows(k_ln_forward<DT>, a, a.rows < kSms * 8 ? a.rows : kSms * 8, kLnThreads, 0, s);
+}
+
+// Lanes of a backward group, vectors of a lane.
+int backward_lanes(int64_t vecs, bool whole) { return whole && vecs <= 8 ? 8 : whole && vecs <= 16 ? 16 : 32; }
+int backward_vectors(int64_t vecs) { return vecs <= 256 ? 1 : vecs <= 512 ? 2 : 4; }
+
+template <int DT, int L, int V, int RB>
+cudaError_t backward_rows(LnArgs a, int64_t vecs, int blocks, cudaStream_t s)
+{
+    const RowShape h = shape_of(vecs, L, V);
+    a.warps = h.warps;
+    constexpr int S = kLnBwdAhead;
+    constexpr size_t smem = (size_t)S * RB * V * 2 * kLnThreads * 16;
+    if (a.dim % kVecOf<DT>)
+        return launch_slots<k_ln_backward_rows<DT, 32, V, RB, S, kLnBwdBlocks, true>, smem>(a, blocks, h.threads, s);
+    return launch_slots<k_ln_backward_rows<DT, L, V, RB, S, kLnBwdBlocks, false>, smem>(a, blocks, h.threads, s);
+}
+
+// Blocks of the backward pass (the plan's): as many as are resident at once on
+// 152 SMs, and no more than have rows.
+int64_t backward_blocks(int64_t rows, int64_t vecs, bool whole)
+{
+    const int L = backward_lanes(vecs, whole), V = backward_vectors(vecs);
+    const RowShape h = shape_of(vecs <= 1024 ? vecs : 1024, L, V);
+    const int64_t at_once = (int64_t)h.groups * (kLnBwdRows / V), need = (rows + at_once - 1) / at_once;
+    const int64_t most = (int64_t)kSms * (kLnBwdBlocks * kLnThreads / h.threads);
+    return need < most ? need : most;
 }
 
 template <int DT>
@@ -541,17 +776,14 @@ cudaError_t backward(LnArgs a, bool vec, int blocks, void* dw, void* db, cudaStr
     if (!sums) a.part = nullptr;
     cudaError_t e = cudaSuccess;
     if (blocks && vec && vecs <= 1024) {
-        // the group's lanes hold one vector of the row each where they can: the
-        // column sums take 2 registers a value beside the rows themselves
-        if (vecs <= 32) k_ln_backward_reg<DT, 1, 1, 4><<<blocks, kLnThreads, 0, s>>>(a);
-        else if (vecs <= 64) k_ln_backward_reg<DT, 2, 1, 4><<<blocks, kLnThreads, 0, s>>>(a);
-        else if (vecs <= 128) k_ln_backward_reg<DT, 4, 1, 4><<<blocks, kLnThreads, 0, s>>>(a);
-        else if (vecs <= 256) k_ln_backward_reg<DT, 8, 1, 4><<<blocks, kLnThreads, 0, s>>>(a);
-        else if (vecs <= 512) k_ln_backward_reg<DT, 8, 2, 2><<<blocks, kLnThreads, 0, s>>>(a);
-        else k_ln_backward_reg<DT, 8, 4, 1><<<blocks, kLnThreads, 0, s>>>(a);
-        e = cudaGetLastError();
+        const int L = backward_lanes(vecs, a.dim % VE == 0);
+        if (L == 8) e = backward_rows<DT, 8, 1, kLnBwdRows>(a, vecs, blocks, s);
+        else if (L == 16) e = backward_rows<DT, 16, 1, kLnBwdRows>(a, vecs, blocks, s);
+        else if (vecs <= 256) e = backward_rows<DT, 32, 1, kLnBwdRows>(a, vecs, blocks, s);
+        else if (vecs <= 512) e = backward_rows<DT, 32, 2, kLnBwdRows / 2>(a, vecs, blocks, s);
+        else e = backward_rows<DT, 32, 4, kLnBwdRows / 4>(a, vecs, blocks, s);
     } else {
-        if (a.dx && a.rows) e = launch_rows(k_ln_dx<DT>, a, 1, kSms * 8, s);
+        if (a.dx && a.rows) e = launch_rows(k_ln_dx<DT>, a, a.rows < kSms * 8 ? a.rows : kSms * 8, kLnThreads, 0, s);
         if (e == cudaSuccess && sums && blocks) {
             const unsigned cols = (unsigned)((a.dim + kLnThreads - 1) / kLnThreads);
             k_ln_dw_part<DT><<<dim3(cols, (unsigned)blocks), kLnThreads, 0, s>>>(a);
@@ -559,7 +791,7 @@ cudaError_t backward(LnArgs a, bool vec, int blocks, void* dw, void* db, cudaStr
         }
     }
     if (e == cudaSuccess && sums)
-        e = launch_kernel(k_ln_dw_sum<DT>, (int)((a.dim + 31) / 32), kLnThreads, s, blocks > 0, (const float*)a.part,
+        e = launch_kernel(k_ln_dw_sum<DT>, (int)((a.dim + 31) / 32), 1024, s, blocks > 0, (const float*)a.part,
                           blocks, a.dim, dw, db);
     return e;
 }
@@ -600,12 +832,7 @@ zero_status_t zero_ln_plan(int64_t rows, int64_t dim, int32_t dtype, int64_t x_s
     out->y_stride = ys;
     out->dtype = dtype;
     const int64_t e = dtype == ZERO_FP32 ? 4 : 2;
-    // each block adds up its rows' weight gradients by itself: two blocks to an
-    // SM of 152, and no more than the rows it takes at a time give
-    const int64_t vecs = (dim * e + 15) / 16;
-    const int64_t at_once = vecs <= 32 ? 32 : vecs <= 64 ? 16 : vecs <= 128 ? 8 : vecs <= 256 ? 4 : vecs <= 512 ? 2 : 1;
-    const int64_t groups = (rows + at_once - 1) / at_once;
-    out->blocks = (int32_t)(groups < 304 ? groups : 304);
+    out->blocks = (int32_t)backward_blocks(rows, (dim * e + 15) / 16, dim * e % 16 == 0);   // each adds up its rows' weight gradients
     out->workspace_bytes = 16 + (int64_t)out->blocks * 2 * dim * 4;
     out->hbm_bytes_forward = rows * (2 * dim * e + 8) + 2 * dim * e;
     out->hbm_bytes_backward = rows * (3 * dim * e + 8) + 3 * dim * e;
