@@ -18,8 +18,8 @@ constexpr int kStages = 6;
 constexpr int kABytes = kBM / 2 * kBK * 2, kBBytes = kBN / 2 * kBK * 2;   // one CTA's part of a stage
 constexpr int kEpiWarps = 8;
 constexpr int kCeThreads = 64 + 32 * kEpiWarps;       // copying warp, issuing warp, epilogue warps
-constexpr int kOutBytes = 4096;                       // an epilogue warp's box of results: 32 rows of 128 bytes
-constexpr int kCeSmem = kStages * (kABytes + kBBytes) + kEpiWarps * kOutBytes + 1024;
+constexpr int kOutBytes = 4096, kOutBoxes = 1;        // an epilogue warp's boxes of results: 32 rows of 128 bytes
+constexpr int kCeSmem = kStages * (kABytes + kBBytes) + kEpiWarps * kOutBoxes * kOutBytes + 1024;
 constexpr int kStrip = kBN / 2;                       // vocabulary entries per (maximum, sum)
 constexpr int kChunk = 16;                            // loss: K-blocks the tensor cores add up by themselves
 constexpr int kGroup = 8;                             // row tiles that share the column tiles in L2
@@ -45,6 +45,8 @@ struct GemmArgs {
     int splits;                  // parts of the K-blocks, one result each (kEpiAcc), m_tiles * kBM rows apart
     int b_y0;                    // first vocabulary entry of the piece
     int accumulate;              // kEpiAcc: added to what is there
+    int a_rows;                  // rows of A that a CTA copies: 128, or fewer for one row tile of few tokens (the
+                                 //   others' results are not kept, so their operands may be anything)
     int withhold;                // test hook: the first copy is announced but not made, so the waits run out
     CeHead* head;
     const int64_t* targets;
@@ -71,19 +73,18 @@ struct Tile {
 // Tile of a place in the order: splits outermost, then groups of kGroup row
 // tiles, then column tiles, so that the tiles running at one time share rows
 // of A and of B in L2.
-__device__ __forceinline__ Tile tile_at(const GemmArgs& g, int64_t t)
+__device__ __forceinline__ Tile tile_at(const GemmArgs& g, uint32_t t)
 {
-    const int64_t per = (int64_t)g.m_tiles * g.n_tiles;
+    const uint32_t per = (uint32_t)g.m_tiles * (uint32_t)g.n_tiles, grouped = kGroup * (uint32_t)g.n_tiles;
     Tile r;
-    r.split = (int)(t / per);
-    t %= per;
-    const int group = (int)(t / ((int64_t)kGroup * g.n_tiles));
-    const int in = (int)(t - (int64_t)group * kGroup * g.n_tiles);
-    const int rows = min(kGroup, g.m_tiles - group * kGroup);
-    r.nt = in / rows;
-    r.mt = group * kGroup + in % rows;
-    r.kb0 = (int)((int64_t)g.k_blocks * r.split / g.splits);
-    r.kb1 = (int)((int64_t)g.k_blocks * (r.split + 1) / g.splits);
+    r.split = g.splits == 1 ? 0 : (int)(t / per);
+    t -= (uint32_t)r.split * per;
+    const uint32_t group = t / grouped, in = t - group * grouped;
+    const uint32_t rows = min((uint32_t)kGroup, (uint32_t)g.m_tiles - group * kGroup);
+    r.nt = (int)(in / rows);
+    r.mt = (int)(group * kGroup + in - (uint32_t)r.nt * rows);
+    r.kb0 = g.splits == 1 ? 0 : (int)((uint64_t)g.k_blocks * r.split / g.splits);
+    r.kb1 = g.splits == 1 ? g.k_blocks : (int)((uint64_t)g.k_blocks * (r.split + 1) / g.splits);
     return r;
 }
 
@@ -124,17 +125,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
     __syncthreads();
     tc::cluster_sync();
     tc::fence_after_sync();
-    if (EPI == kEpiLse) allow_next_grid();            // the join: it waits for this grid
+    wait_prev_grid();                                 // set up while the kernel before drains; this call's kernels
+    allow_next_grid();                                // all wait for their predecessor before they read or write
     const uint32_t tmem = s_tmem;
-    const int64_t tiles = (int64_t)g.m_tiles * g.n_tiles * g.splits;
-    const int64_t first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+    const uint32_t tiles = (uint32_t)g.m_tiles * (uint32_t)g.n_tiles * (uint32_t)g.splits;   // below 2^31: see the plan
+    const uint32_t first = blockIdx.x >> 1, stride = gridDim.x >> 1;
     constexpr int kChunkBlocks = EPI == kEpiLse ? kChunk : 1 << 30;
 
     if (warp == 0) {
         if (lane == 0) {
             bool ok = true;
             int it = 0;
-            for (int64_t t = first; t < tiles && ok; t += stride) {
+            for (uint32_t t = first; t < tiles && ok; t += stride) {
                 const Tile w = tile_at(g, t);
                 const int m0 = w.mt * kBM + (int)rank * (kBM / 2), n0 = w.nt * kBN + (int)rank * (kBN / 2);
                 for (int kb = w.kb0; kb < w.kb1; kb++, it++) {
@@ -145,15 +147,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
                     }
                     const uint32_t bar = tc::in_leader(full + 8 * s);
                     const uint32_t sa = sm + s * (kABytes + kBBytes), sb = sa + kABytes;
+                    const bool copies_a = rank == 0 || g.a_rows == kBM / 2;
                     if (rank == 0) {
-                        tc::mbar_arrive_expect_tx(full + 8 * s, 2 * (kABytes + kBBytes));
+                        const uint32_t a_bytes = g.a_rows == kBM / 2 ? 2 * kABytes : (uint32_t)g.a_rows * (kBK * 2);
+                        tc::mbar_arrive_expect_tx(full + 8 * s, a_bytes + 2 * kBBytes);
                         if (g.withhold && blockIdx.x == 0 && it == 0) continue;
                     }
                     if (A_MN) {
 #pragma unroll
                         for (int j = 0; j < kBM / 128; j++)
                             tc::tma_load(sa + j * tc::kBoxBytes, &g.a, m0 + 64 * j, kb * kBK, bar);
-                    } else {
+                    } else if (copies_a) {
                         tc::tma_load(sa, &g.a, kb * kBK, m0, bar);
                     }
                     if (B_MN) {
@@ -179,7 +183,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
             constexpr uint32_t idesc = tc::instr_desc<DT == kBF16, A_MN, B_MN>(kBM, kBN);
             int it = 0, unit = 0;
             bool ok = true;
-            for (int64_t t = first; t < tiles && ok; t += stride) {
+            for (uint32_t t = first; t < tiles && ok; t += stride) {
                 const Tile w = tile_at(g, t);
                 for (int c0 = w.kb0; c0 < w.kb1 && ok; c0 += kChunkBlocks, unit++) {
                     const int buf = unit & 1;
@@ -217,10 +221,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
         const int band = warp & 3;                    // the warp's 32 lanes of tensor memory
         const int half = (warp - 2) >> 2;             // and its 128 columns
         const uint32_t src = tmem + ((uint32_t)(band * 32) << 16) + half * kStrip;
-        const uint32_t box = sm + kStages * (kABytes + kBBytes) + (warp - 2) * kOutBytes;
+        const uint32_t box = sm + kStages * (kABytes + kBBytes) + (warp - 2) * (kOutBoxes * kOutBytes);
         int unit = 0;
         bool ok = true;
-        for (int64_t t = first; t < tiles && ok; t += stride) {
+        for (uint32_t t = first; t < tiles && ok; t += stride) {
             const Tile w = tile_at(g, t);
             const int64_t row = (int64_t)w.mt * kBM + rank * (kBM / 2) + band * 32 + lane;
             const bool live = row < g.m;
@@ -352,17 +356,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
                             if (col0 + k < g.n) g.out[row * g.out_stride + col0 + k] = (uint16_t)from_f32<DT>(z[k]);
                     continue;
                 }
-                // the warp's box: 32 rows of 128 bytes with the copy's swizzle (16-byte
+                // the warp's boxes: 32 rows of 128 bytes with the copy's swizzle (16-byte
                 // unit j of row i at j ^ (i & 7): no bank conflicts); one copy out per box
                 const int y = row0 + (EPI == kEpiAcc ? w.split * g.m_tiles * kBM : 0);
                 constexpr int kCols = EPI == kEpiAcc ? 32 : 64;       // columns of a box
 #pragma unroll
                 for (int c = 0; c < kStrip; c += kCols) {
-                    if (lane == 0) tc::bulk_wait_read();
+                    const uint32_t to = box + c / kCols % kOutBoxes * kOutBytes;
+                    if (lane == 0) tc::bulk_wait_read<kOutBoxes - 1>();
                     __syncwarp();
 #pragma unroll
                     for (int k = 0; k < 8; k++) {
-                        const uint32_t at = box + lane * 128 + ((k ^ (lane & 7)) << 4);
+                        const uint32_t at = to + lane * 128 + ((k ^ (lane & 7)) << 4);
                         if constexpr (EPI == kEpiAcc) {
                             const float* p = z + c + 4 * k;
                             tc::st_shared16(at, __float_as_uint(p[0]), __float_as_uint(p[1]), __float_as_uint(p[2]),
@@ -378,11 +383,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
                     const int64_t x = col0 + c;
                     if (lane == 0 && row0 < g.m && x < (EPI == kEpiGrad ? g.c_cols : g.n)) {
                         if (EPI == kEpiAcc && g.accumulate)
-                            tc::tma_add(&g.c, (int)x, y, box);
+                            tc::tma_add(&g.c, (int)x, y, to);
                         else
-                            tc::tma_store(&g.c, (int)x, y, box);
-                        tc::bulk_commit();
+                            tc::tma_store(&g.c, (int)x, y, to);
                     }
+                    if (lane == 0) tc::bulk_commit();             // one group a box, empty ones too
                 }
             }
         }
@@ -439,7 +444,7 @@ __device__ __forceinline__ float2 finish_token(const JoinArgs& a, int64_t i, flo
 // blocks' losses and counts, in block order.
 __global__ void __launch_bounds__(1024) k_ce_join(const __grid_constant__ JoinArgs a)
 {
-    wait_prev_grid();                                 // launched while the products drain
+    wait_prev_grid();
     __shared__ float2 sh[32][33];
     __shared__ uint32_t last;
     const int tok = threadIdx.x & 31, p = threadIdx.x >> 5;
@@ -682,6 +687,7 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_ce_few(const uint16_t* x, in
 __global__ void __launch_bounds__(1024) k_ce_factors(CeHead* head, const int64_t* targets, int64_t n, int64_t vocab,
                                                      const float* dloss, float scale, float up, float* coef)
 {
+    allow_next_grid();
     __shared__ float sm[1024];
     __shared__ int64_t sc[1024];
     float most = 0.0f;
@@ -723,6 +729,7 @@ template <int DT>
 __global__ void __launch_bounds__(256) k_ce_dx(const CeHead* head, const float* acc, int splits, int64_t split_stride,
                                                int64_t m, int64_t n, int64_t acc_cols, uint16_t* dx, int64_t stride)
 {
+    wait_prev_grid();
     const float alpha = head->err ? NAN : head->alpha;
     const int64_t c = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
     if (c >= n) return;
@@ -847,12 +854,32 @@ CUtensorMapDataType map_type(int dtype)
     return dtype == ZERO_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
 
+// GemmArgs::a_rows where the rows of A are tokens.
+int a_rows_of(int64_t tokens) { return tokens >= kBM / 2 ? kBM / 2 : (int)((tokens + 7) / 8 * 8); }
+
 int sm_count()
 {
     int dev = 0, n = 0;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
     return n > 1 ? n : 152;
+}
+
+// A launch that may begin while the stream's kernel before it drains.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
 template <int EPI, int DT, bool A_MN, bool B_MN>
@@ -863,8 +890,8 @@ cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t s)
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)g.m_tiles * g.n_tiles * g.splits;
     const int64_t pairs = sm_count() / 2;
-    k_ce_gemm<EPI, DT, A_MN, B_MN><<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), kCeThreads, kCeSmem, s>>>(g);
-    return cudaGetLastError();
+    return launch_after(k_ce_gemm<EPI, DT, A_MN, B_MN>, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), kCeThreads,
+                        kCeSmem, s, g);
 }
 
 template <int DT, int T>
@@ -922,6 +949,8 @@ zero_status_t zero_ce_plan(int64_t tokens, int64_t vocab, int64_t hidden, int32_
     if (xs % 8 || ws % 8) return set_error(ZERO_EALIGN, "zero_ce_plan: row strides must be multiples of 8 values");
     if (xs >= (int64_t(1) << 38) || ws >= (int64_t(1) << 38))
         return set_error(ZERO_EUNSUPPORTED, "zero_ce_plan: a stride is 2^38 or more");
+    if (ceil_div(tokens, kBM) * ceil_div(vocab, kBN) > (int64_t(1) << 30) || ceil_div(vocab, kBM) * ceil_div(hidden, kBN) > (int64_t(1) << 30))
+        return set_error(ZERO_EUNSUPPORTED, "zero_ce_plan: over 2^30 tiles");
     std::memset(out, 0, sizeof *out);
     out->tokens = tokens;
     out->vocab = vocab;
@@ -999,7 +1028,8 @@ zero_status_t zero_ce_forward(const zero_ce_plan_t* plan, const void* x, const v
         const CUtensorMapDataType type = map_type(p.dtype);
         GemmArgs g;
         std::memset(&g, 0, sizeof g);
-        if (!make_map(&g.a, type, x, p.tokens, p.hidden, p.x_stride, kBM / 2) ||
+        g.a_rows = a_rows_of(p.tokens);
+        if (!make_map(&g.a, type, x, p.tokens, p.hidden, p.x_stride, g.a_rows) ||
             !make_map(&g.b, type, w, p.vocab, p.hidden, p.w_stride, kBN / 2))
             return set_error(ZERO_ECUDA, "zero_ce_forward: cuTensorMapEncodeTiled refused a buffer");
         g.m = p.tokens;
@@ -1015,7 +1045,7 @@ zero_status_t zero_ce_forward(const zero_ce_plan_t* plan, const void* x, const v
         g.withhold = std::getenv("ZERO_TEST_WITHHOLD_TILE") != nullptr;
         e = gemm<kEpiLse, false, false>(p.dtype, g, s);
         if (e == cudaSuccess) {
-            e = launch_kernel(k_ce_join, (int)ceil_div(p.tokens, 32), 1024, s, true, j);
+            e = launch_after(k_ce_join, dim3((unsigned)ceil_div(p.tokens, 32)), 1024, 0, s, j);
         }
     } else if (total) {
         e = cudaMemsetAsync(total, 0, 8, s);
@@ -1059,7 +1089,8 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
         const int64_t nv = p.vocab - v0 < p.piece ? p.vocab - v0 : p.piece;
         GemmArgs g;                                  // G of the piece
         std::memset(&g, 0, sizeof g);
-        bool ok = make_map(&g.a, type, x, p.tokens, p.hidden, p.x_stride, kBM / 2) &&
+        g.a_rows = a_rows_of(p.tokens);
+        bool ok = make_map(&g.a, type, x, p.tokens, p.hidden, p.x_stride, g.a_rows) &&
                   make_map(&g.b, type, w, p.vocab, p.hidden, p.w_stride, kBN / 2) &&
                   make_map(&g.c, type, G, p.tokens, p.piece, p.piece, 32);
         g.m = p.tokens;
@@ -1078,7 +1109,7 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
         g.n = p.hidden;
         g.n_tiles = (int)ceil_div(p.hidden, kBN);
         if (ok && dx && e == cudaSuccess) {          // dx += G w
-            ok = make_map(&g.a, type, G, p.tokens, p.piece, p.piece, kBM / 2) &&
+            ok = make_map(&g.a, type, G, p.tokens, p.piece, p.piece, g.a_rows) &&
                  make_map(&g.b, type, w, p.vocab, p.hidden, p.w_stride, 64) &&
                  make_map(&g.c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, acc, p.splits * l.acc_rows, l.acc_cols, l.acc_cols, 32);
             g.k_blocks = (int)ceil_div(nv, kBK);
@@ -1091,6 +1122,7 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
                  make_map(&g.b, type, x, p.tokens, p.hidden, p.x_stride, 64) &&
                  make_map(&g.c, type, static_cast<uint16_t*>(dw) + v0 * p.w_stride, nv, p.hidden, p.w_stride, 32);
             g.b_y0 = 0;
+            g.a_rows = kBM / 2;
             g.m = nv;
             g.m_tiles = (int)ceil_div(nv, kBM);
             g.k_blocks = (int)ceil_div(p.tokens, kBK);
@@ -1108,10 +1140,11 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
         uint16_t* out = static_cast<uint16_t*>(dx);
         const int64_t apart = l.acc_rows * l.acc_cols;
         if (p.dtype == ZERO_BF16)
-            k_ce_dx<kBF16><<<grid, 256, 0, s>>>(head, acc, p.splits, apart, p.tokens, p.hidden, l.acc_cols, out, p.x_stride);
+            e = launch_after(k_ce_dx<kBF16>, grid, 256, 0, s, head, acc, p.splits, apart, p.tokens, p.hidden, l.acc_cols, out,
+                             p.x_stride);
         else
-            k_ce_dx<kF16><<<grid, 256, 0, s>>>(head, acc, p.splits, apart, p.tokens, p.hidden, l.acc_cols, out, p.x_stride);
-        e = cudaGetLastError();
+            e = launch_after(k_ce_dx<kF16>, grid, 256, 0, s, head, acc, p.splits, apart, p.tokens, p.hidden, l.acc_cols, out,
+                             p.x_stride);
     }
     return e == cudaSuccess ? ZERO_OK : cuda_failed(e, "zero_ce_backward");
 }
