@@ -402,6 +402,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
     if (warp == 1) tc::tmem_free(tmem, 2 * kBN);
 }
 
+// The head cleared, before a forward pass.
+__global__ void k_ce_clear(CeHead* head)
+{
+    allow_next_grid();
+    wait_prev_grid();
+    head->err = 0;
+    head->joined = 0;
+}
+
 // Join of (maximum, sum) pairs.
 __device__ __forceinline__ void merge(float& mx, float& sum, float2 q)
 {
@@ -440,32 +449,53 @@ __device__ __forceinline__ float2 finish_token(const JoinArgs& a, int64_t i, flo
 }
 
 // Per token: the strips' maxima and sums joined, in a fixed order (32 parts of
-// the strips, then the parts); the loss.  The last block to finish adds the
-// blocks' losses and counts, in block order.
+// the strips, then a tree over the parts); the loss.  The last block to finish
+// adds the blocks' losses and counts, in block order.
 __global__ void __launch_bounds__(1024) k_ce_join(const __grid_constant__ JoinArgs a)
 {
     wait_prev_grid();
     __shared__ float2 sh[32][33];
     __shared__ uint32_t last;
-    const int tok = threadIdx.x & 31, p = threadIdx.x >> 5;
-    const int64_t i = (int64_t)blockIdx.x * 32 + tok;
-    float mx = -INFINITY, sum = 0.0f;
-    if (i < a.n)
-        for (int s = p; s < a.strips; s += 32)
-            merge(mx, sum, a.part[(int64_t)s * a.n + i]);
-    sh[p][tok] = make_float2(mx, sum);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    {
+        const int64_t i = (int64_t)blockIdx.x * 32 + lane;        // the warp's part of 32 tokens
+        float mx = -INFINITY, sum = 0.0f;
+        if (i < a.n)
+            for (int s = warp; s < a.strips; s += 128) {
+                float2 q[4];
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+                    q[k] = s + 32 * k < a.strips ? a.part[(int64_t)(s + 32 * k) * a.n + i] : make_float2(-INFINITY, 0.0f);
+                const float top = fmaxf(fmaxf(fmaxf(q[0].x, q[1].x), fmaxf(q[2].x, q[3].x)), mx);
+                const float ref = top == -INFINITY ? 0.0f : top;
+                sum *= exp2f((mx - ref) * kLog2e);
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+                    sum = fmaf(q[k].y, exp2f((q[k].x - ref) * kLog2e), sum);
+                mx = top;
+            }
+        sh[warp][lane] = make_float2(mx, sum);
+    }
     __syncthreads();
-    if (p == 0) {
-        for (int s = 1; s < 32; s++)
-            merge(mx, sum, sh[s][tok]);
-        float2 r = make_float2(0.0f, 0.0f);
-        if (i < a.n) r = finish_token(a, i, mx, sum);
+    const int64_t i = (int64_t)blockIdx.x * 32 + warp;            // the warp's token
+    float2 r = sh[lane][warp];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float2 q = make_float2(__shfl_xor_sync(0xffffffffu, r.x, o), __shfl_xor_sync(0xffffffffu, r.y, o));
+        merge(r.x, r.y, q);
+    }
+    r = lane == 0 && i < a.n ? finish_token(a, i, r.x, r.y) : make_float2(0.0f, 0.0f);
+    __syncthreads();
+    if (lane == 0) sh[0][warp] = r;
+    __syncthreads();
+    if (warp == 0) {
+        r = sh[0][lane];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             r.x += __shfl_down_sync(0xffffffffu, r.x, o);
             r.y += __shfl_down_sync(0xffffffffu, r.y, o);
         }
-        if (tok == 0) {
+        if (lane == 0) {
             a.block_total[blockIdx.x] = r;
             __threadfence();
             last = atomicAdd(&a.head->joined, 1u) == gridDim.x - 1;
@@ -485,7 +515,7 @@ __global__ void __launch_bounds__(1024) k_ce_join(const __grid_constant__ JoinAr
         s += __shfl_down_sync(0xffffffffu, s, o);
         c += __shfl_down_sync(0xffffffffu, c, o);
     }
-    if (tok == 0) sh[0][p] = make_float2(s, c);
+    if (lane == 0) sh[0][warp] = make_float2(s, c);
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int k = 1; k < 32; k++) {
@@ -501,12 +531,13 @@ __global__ void __launch_bounds__(1024) k_ce_join(const __grid_constant__ JoinAr
 // Up to kFewTokens tokens: w is read once and that is the time (411 MB at
 // vocabulary 50257, hidden 4096: 61 us at the copy bandwidth), so no tensor
 // cores: the tokens lie in shared memory, a warp takes a row of w at a time (3
-// or 4 tokens: two, which share the unpacked tokens), neighbouring warps
+// tokens: two, which share the unpacked tokens), neighbouring warps
 // neighbouring rows, each lane with 128 bytes in flight, 24 warps to an SM.
 // Each lane keeps one row's logit; 32 of them at a time go into the warp's
 // running maximum and sum.  The last block joins the blocks' pairs.  Products
-// and sums are binary32 multiply-adds.
-constexpr int kFewTokens = 4, kFewThreads = 256, kFewBlocks = 456;
+// and sums are binary32 multiply-adds.  At 4 tokens the multiply-adds bound it
+// (90 us at hidden 4096; the tensor cores' path takes 87).
+constexpr int kFewTokens = 3, kFewThreads = 256, kFewBlocks = 456;
 constexpr int kFewSmem = 64 * 1024;                   // all tokens' values, 16 bits each
 
 template <int DT>
@@ -527,6 +558,7 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_ce_few(const uint16_t* x, in
                                                            float* target_logit, const __grid_constant__ JoinArgs a)
 {
     constexpr int R = T <= 2 ? 1 : 2, U = 8 / R;      // rows at a time, loads in flight per row
+    wait_prev_grid();
     extern __shared__ __align__(16) uint16_t xs[];    // [T][wide]
     __shared__ float2 sh[kFewThreads / 32][T];
     __shared__ uint32_t last;
@@ -857,14 +889,6 @@ CUtensorMapDataType map_type(int dtype)
 // GemmArgs::a_rows where the rows of A are tokens.
 int a_rows_of(int64_t tokens) { return tokens >= kBM / 2 ? kBM / 2 : (int)((tokens + 7) / 8 * 8); }
 
-int sm_count()
-{
-    int dev = 0, n = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return n > 1 ? n : 152;
-}
-
 // A launch that may begin while the stream's kernel before it drains.
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args)
@@ -880,6 +904,14 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t sm
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+int sm_count()
+{
+    int dev = 0, n = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n > 1 ? n : 152;
 }
 
 template <int EPI, int DT, bool A_MN, bool B_MN>
@@ -902,10 +934,9 @@ cudaError_t launch_few_t(const zero_ce_plan_t& p, const void* x, const void* w, 
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem((const void*)k_ce_few<DT, T>, kFewSmem, done);
     if (e != cudaSuccess) return e;
-    k_ce_few<DT, T><<<(unsigned)few_blocks(p), kFewThreads, bytes, s>>>(
-        static_cast<const uint16_t*>(x), p.x_stride, static_cast<const uint16_t*>(w), p.w_stride, p.hidden,
-        reinterpret_cast<float2*>(ws + l.part), reinterpret_cast<float*>(ws + l.target_logit), j);
-    return cudaGetLastError();
+    return launch_after(k_ce_few<DT, T>, dim3((unsigned)few_blocks(p)), kFewThreads, bytes, s, static_cast<const uint16_t*>(x),
+                        p.x_stride, static_cast<const uint16_t*>(w), p.w_stride, p.hidden,
+                        reinterpret_cast<float2*>(ws + l.part), reinterpret_cast<float*>(ws + l.target_logit), j);
 }
 
 template <int DT>
@@ -915,8 +946,7 @@ cudaError_t launch_few(const zero_ce_plan_t& p, const void* x, const void* w, un
     switch (p.tokens) {
     case 1: return launch_few_t<DT, 1>(p, x, w, ws, l, j, s);
     case 2: return launch_few_t<DT, 2>(p, x, w, ws, l, j, s);
-    case 3: return launch_few_t<DT, 3>(p, x, w, ws, l, j, s);
-    default: return launch_few_t<DT, 4>(p, x, w, ws, l, j, s);
+    default: return launch_few_t<DT, 3>(p, x, w, ws, l, j, s);
     }
 }
 
@@ -1004,7 +1034,8 @@ zero_status_t zero_ce_forward(const zero_ce_plan_t* plan, const void* x, const v
         return set_error(ZERO_EALIGN, "zero_ce_forward: x, w and workspace must be 16-byte aligned, the others to their type");
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
-    cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(CeHead), s);
+    k_ce_clear<<<1, 1, 0, s>>>(reinterpret_cast<CeHead*>(ws));
+    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_failed(e, "zero_ce_forward");
     if (p.tokens) {
         if (!encode_fn()) return set_error(ZERO_ECUDA, "zero_ce_forward: the driver has no cuTensorMapEncodeTiled");

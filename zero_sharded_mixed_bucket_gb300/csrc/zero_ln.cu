@@ -731,8 +731,8 @@ cudaError_t forward(const LnArgs& a, bool vec, cudaStream_t s)
     constexpr int VE = kVecOf<DT>;
     const int64_t vecs = (a.dim + VE - 1) / VE;
     const bool whole = a.dim % VE == 0;
-    if (vec && whole && vecs <= 8) return forward_rows<DT, 8, 1, kLnFwdRows, kLnFwdAhead, kLnFwdBlocks>(a, vecs, s);
-    if (vec && whole && vecs <= 16) return forward_rows<DT, 16, 1, kLnFwdRows, kLnFwdAhead, kLnFwdBlocks>(a, vecs, s);
+    if (vec && whole && vecs <= 8) return forward_rows<DT, 8, 1, 4, 3, 3>(a, vecs, s);
+    if (vec && whole && vecs <= 16) return forward_rows<DT, 16, 1, 4, 3, 3>(a, vecs, s);
     if (vec && vecs <= 256) return forward_rows<DT, 32, 1, kLnFwdRows, kLnFwdAhead, kLnFwdBlocks>(a, vecs, s);
     if (vec && vecs <= 512) return forward_rows<DT, 32, 2, kLnFwdRows / 2, kLnFwdAhead, kLnFwdBlocks>(a, vecs, s);
     if (vec && vecs <= 1024) return forward_rows<DT, 32, 4, kLnFwdRows / 4, kLnFwdAhead, kLnFwdBlocks>(a, vecs, s);
