@@ -12,7 +12,11 @@ namespace {
 
 constexpr int kQBlock = 256;         // values per scale byte
 constexpr int kChunk = 4096;         // values per block of threads: one tensor's, from a multiple of kChunk
-constexpr int kAdThreads = 128;
+// Threads per block, each measured: the binary32 step is bound by memory and
+// likes 4 warps, the 8-bit one by instructions, and its warps keep out of step
+// best as blocks of their own (4.25 ms for the 1.56e9 values of the 48-layer
+// d=1600 list; 4.53 as pairs, 4.68 as fours).
+constexpr int kAd32Threads = 128, kAd8Threads = 32, kStateThreads = 64;
 
 // One tensor in the table.
 struct AdRec {
@@ -76,30 +80,33 @@ constexpr uint32_t kUpM = 120, kUpR = 112;
 // 2^(e - 127) for an exponent field 1..254, 0 for 0.
 __device__ __forceinline__ float pow2_field(uint32_t e) { return __uint_as_float(e << 23); }
 
-// Factors of a block with scale byte e: 2^(e - 127 + up) to decode, its
-// inverse to encode.  Scales from 2^6 (m) or 2^14 (r) on are out of one
-// factor's range; they take the rest, `over`, in a second one.
-struct Factors {
-    float dec, enc, over;        // over: 1 but for such scales
-};
+// Factor that decodes a block with scale byte e: 2^(e - 127 + UP), 0 for e = 0;
+// and its inverse, which encodes.  Scales from 2^7 (m) or 2^15 (r) on are out
+// of one factor's range: `far_scale`; such a block multiplies by the rest,
+// 2^(e - kFarScale), or its inverse, besides.
+template <uint32_t UP>
+constexpr uint32_t kFarScale = 253u - UP;
 
 template <uint32_t UP>
-__device__ __forceinline__ Factors factors_of(uint32_t e)
-{
-    const uint32_t lim = 253u - UP;                    // dec's and enc's fields stay in 1..254
-    const uint32_t f = min(e, lim);
-    Factors r;
-    r.dec = e ? pow2_field(f + UP) : 0.0f;
-    r.enc = pow2_field(254u - UP - f);
-    r.over = pow2_field(127u + e - f);
-    return r;
-}
+__device__ __forceinline__ bool far_scale(uint32_t e) { return e > kFarScale<UP>; }
 
-// Byte k of w at bits 31..24.
+template <uint32_t UP>
+__device__ __forceinline__ float dec_factor(uint32_t e) { return e ? pow2_field(min(e, kFarScale<UP>) + UP) : 0.0f; }
+
+template <uint32_t UP>
+__device__ __forceinline__ float enc_factor(uint32_t e) { return pow2_field(254u - UP - min(e, kFarScale<UP>)); }
+
+template <uint32_t UP>
+__device__ __forceinline__ float rest_factor(uint32_t e) { return pow2_field(127u + e - min(e, kFarScale<UP>)); }
+
+template <uint32_t UP>
+__device__ __forceinline__ float rest_inverse(uint32_t e) { return pow2_field(127u - e + min(e, kFarScale<UP>)); }
+
+// Byte k of w at bits 31..24, zeros below.
 template <int K>
 __device__ __forceinline__ uint32_t byte_on_top(uint32_t w)
 {
-    return K == 3 ? w : __byte_perm(w, 0, K == 2 ? 0x2444 : (K == 1 ? 0x1444 : 0x0444));
+    return K == 0 ? w << 24 : K == 3 ? w & 0xff000000u : __byte_perm(w, 0, K == 2 ? 0x2444 : 0x1444);
 }
 
 __device__ __forceinline__ uint32_t byte_on_top(uint2 w, int k)
@@ -109,33 +116,33 @@ __device__ __forceinline__ uint32_t byte_on_top(uint2 w, int k)
                                                                                              : byte_on_top<3>(x);
 }
 
-// `top`: the code in bits 31..24, anything below.
+// `top`: the code in bits 31..24, zeros below; `dec`: the block's factor.
 __device__ __forceinline__ float decode_m(uint32_t top, float dec)
 {
-    return __fmul_rn(__uint_as_float((top & 0x80000000u) | ((top >> 5) & 0x03f80000u)), dec);
+    // the arithmetic shift leaves the sign in bit 31, the mask only that copy of it
+    return __fmul_rn(__uint_as_float((uint32_t)((int32_t)top >> 5) & 0x83f80000u), dec);
 }
 
-__device__ __forceinline__ float decode_r(uint32_t top, float dec)
+__device__ __forceinline__ float decode_r(uint32_t top, float dec) { return __fmul_rn(__uint_as_float(top >> 5), dec); }
+
+// Four codes of m in a word, from the scaled values plus the random bits (as
+// bit patterns: sign, then the code from bit 19 on); no negative zero.
+__device__ __forceinline__ uint32_t pack_m(const uint32_t u[4])
 {
-    return __fmul_rn(__uint_as_float((top >> 5) & 0x07f80000u), dec);
+    const uint32_t mag = ((u[0] >> 19) & 0x7fu) | ((u[1] >> 11) & 0x7f00u) | ((u[2] >> 3) & 0x7f0000u) | ((u[3] << 5) & 0x7f000000u);
+    const uint32_t sign = ((u[0] >> 24) & 0x80u) | ((u[1] >> 16) & 0x8000u) | ((u[2] >> 8) & 0x800000u) | (u[3] & 0x80000000u);
+    return mag | (sign & (mag + 0x7f7f7f7fu));          // bit 7 of a byte of the sum: its magnitude is not 0
 }
 
-// Codes of m and r >= 0; rnd8: 16 random bits times 8.
-__device__ __forceinline__ uint32_t encode_m(float m, float enc, uint32_t rnd8)
+// Four codes of r; a nonzero root keeps a nonzero code.
+__device__ __forceinline__ uint32_t pack_r(const uint32_t u[4], const float r[4])
 {
-    const uint32_t c = (__float_as_uint(__fmul_rn(fabsf(m), enc)) + rnd8) >> 19;
-    return c ? c | ((__float_as_uint(m) >> 24) & 0x80u) : 0u;
-}
-
-__device__ __forceinline__ uint32_t encode_r(float r, float enc, uint32_t rnd8)
-{
-    const uint32_t c = (__float_as_uint(__fmul_rn(r, enc)) + rnd8) >> 19;
-    return max(c, min(__float_as_uint(r), 1u));        // a nonzero root keeps a nonzero code
-}
-
-__device__ __forceinline__ uint32_t pack4(const uint32_t c[4])
-{
-    return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+    uint32_t w = __byte_perm(__byte_perm(u[0] >> 19, u[1] >> 19, 0x0040), __byte_perm(u[2] >> 19, u[3] >> 19, 0x0040), 0x5410);
+    if ((w - 0x01010101u) & ~w & 0x80808080u)           // some byte is 0
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            if (!(w >> (8 * k) & 0xffu) && r[k] > 0.0f) w |= 1u << (8 * k);
+    return w;
 }
 
 // A block's scale byte, from the bit pattern of its largest magnitude: the
@@ -182,17 +189,30 @@ __device__ __forceinline__ void st_any(T* p, int cnt, bool vec, const T x[V])
     }
 }
 
+// The block's record, in shared memory: in global memory a store might alias
+// it, and every pointer would be read again after each one.
+__device__ __forceinline__ const AdRec& record_of(const AdTable& tab, AdRec& held)
+{
+    const AdRec& r = tab.rec[tab.chunk_tensor[blockIdx.x]];
+    static_assert(sizeof(AdRec) % 4 == 0 && sizeof(AdRec) / 4 <= 32, "one word a thread");
+    if (threadIdx.x < sizeof(AdRec) / 4)
+        reinterpret_cast<uint32_t*>(&held)[threadIdx.x] = reinterpret_cast<const uint32_t*>(&r)[threadIdx.x];
+    __syncthreads();
+    return held;
+}
+
 template <int DT>
 using Bits = typename std::conditional<DT == kF32, uint32_t, uint16_t>::type;
 
 // Binary32 moments: groups of 4 values, one 16-byte access per binary32 array.
 template <int DT>
-__global__ void __launch_bounds__(kAdThreads) k_adamw32(const AdTable tab, const __grid_constant__ AdHP hp,
+__global__ void __launch_bounds__(kAd32Threads) k_adamw32(const AdTable tab, const __grid_constant__ AdHP hp,
                                                         const uint32_t* skip)
 {
     if (skip && *skip) return;
     constexpr int V = 4;
-    const AdRec& r = tab.rec[tab.chunk_tensor[blockIdx.x]];
+    __shared__ AdRec held;
+    const AdRec& r = record_of(tab, held);
     const int64_t lo = ((int64_t)blockIdx.x - r.first_chunk) * kChunk;
     const int64_t hi = min(lo + kChunk, r.t.numel);
     const bool vec = r.aligned;
@@ -201,7 +221,7 @@ __global__ void __launch_bounds__(kAdThreads) k_adamw32(const AdTable tab, const
     Bits<DT>* param = static_cast<Bits<DT>*>(r.t.param);
     float* mp = static_cast<float*>(r.t.m);
     float* vp = static_cast<float*>(r.t.v);
-    for (int64_t i = lo + threadIdx.x * V; i < hi; i += kAdThreads * V) {
+    for (int64_t i = lo + threadIdx.x * V; i < hi; i += kAd32Threads * V) {
         const int cnt = (int)min((int64_t)V, hi - i);
         alignas(16) Bits<DT> g[V], p[V];
         alignas(16) float w[V], m[V], v[V];
@@ -223,12 +243,16 @@ __global__ void __launch_bounds__(kAdThreads) k_adamw32(const AdTable tab, const
 }
 
 // 8-bit moments: a warp takes a block of 256 values, 8 per lane, so the
-// block's largest magnitudes are one warp-wide maximum each.  Most of the time
-// is instructions, about 85 a value: four correctly rounded operations
-// (square root, division) and the codes' integer work.
+// block's largest magnitudes are one warp-wide maximum each.  Instructions
+// bound it, about 86 a value (a correctly rounded square root and division,
+// the codes' integer work): the 30 warps of an SM issue in 74 % of the cycles.
+// Copying the next block's inputs ahead into shared memory costs more
+// instructions than the latency it hides (412 us against 357 for the 1.24e8
+// values of the 12-layer d=768 list), packed pairs of binary32 operations more
+// moves (553).
 template <int DT>
-__global__ void __launch_bounds__(kAdThreads, 8) k_adamw8(const AdTable tab, const __grid_constant__ AdHP hp,
-                                                          const uint32_t* skip)
+__global__ void __launch_bounds__(kAd8Threads, 32) k_adamw8(const AdTable tab, const __grid_constant__ AdHP hp,
+                                                           const uint32_t* skip)
 {
     if (skip && *skip) return;
     constexpr int V = 8;
@@ -239,7 +263,7 @@ __global__ void __launch_bounds__(kAdThreads, 8) k_adamw8(const AdTable tab, con
     const bool vec = r.aligned;
     const float keep = __fmaf_rn(-hp.a.lr, t.weight_decay, 1.0f);
     const int lane = threadIdx.x & 31;
-    for (int64_t b = lo + (threadIdx.x >> 5) * kQBlock; b < hi; b += kAdThreads / 32 * kQBlock) {
+    for (int64_t b = lo + (threadIdx.x >> 5) * kQBlock; b < hi; b += kAd8Threads / 32 * kQBlock) {
         const int64_t i = b + lane * V;
         const int cnt = i < hi ? (int)min((int64_t)V, hi - i) : 0;
         alignas(16) Bits<DT> g[V];
@@ -250,18 +274,19 @@ __global__ void __launch_bounds__(kAdThreads, 8) k_adamw8(const AdTable tab, con
         ld_any<V>(static_cast<const uint8_t*>(t.m) + i, cnt, vec, cm8);
         ld_any<V>(static_cast<const uint8_t*>(t.v) + i, cnt, vec, cr8);
         const uint2 wm = *reinterpret_cast<const uint2*>(cm8), wr = *reinterpret_cast<const uint2*>(cr8);
-        const Factors om = factors_of<kUpM>(t.m_scale[b / kQBlock]), orr = factors_of<kUpR>(t.v_scale[b / kQBlock]);
+        const uint32_t em0 = t.m_scale[b / kQBlock], er0 = t.v_scale[b / kQBlock];
+        const float dm = dec_factor<kUpM>(em0), dr = dec_factor<kUpR>(er0);
         float m[V], q[V];
 #pragma unroll
         for (int j = 0; j < V; j++) {
-            m[j] = decode_m(byte_on_top(wm, j), om.dec);
-            q[j] = decode_r(byte_on_top(wr, j), orr.dec);
+            m[j] = decode_m(byte_on_top(wm, j), dm);
+            q[j] = decode_r(byte_on_top(wr, j), dr);
         }
-        if (om.over != 1.0f || orr.over != 1.0f) {
+        if (far_scale<kUpM>(em0) || far_scale<kUpR>(er0)) {
 #pragma unroll
             for (int j = 0; j < V; j++) {
-                m[j] = __fmul_rn(m[j], om.over);
-                q[j] = __fmul_rn(q[j], orr.over);
+                m[j] = __fmul_rn(m[j], rest_factor<kUpM>(em0));
+                q[j] = __fmul_rn(q[j], rest_factor<kUpR>(er0));
             }
         }
         alignas(16) Bits<DT> p[V];
@@ -274,48 +299,44 @@ __global__ void __launch_bounds__(kAdThreads, 8) k_adamw8(const AdTable tab, con
             const float d = __fadd_rn(__fmul_rn(q[j], hp.root8), hp.a.eps);
             w[j] = __fsub_rn(__fmul_rn(w[j], keep), __fdiv_rn(__fmul_rn(m[j], hp.step8), d));
             p[j] = (Bits<DT>)from_f32<DT>(w[j]);
-            most_m = max(most_m, __float_as_uint(m[j]) & 0x7fffffffu);    // values past cnt are 0: m = r = 0
-            most_r = max(most_r, __float_as_uint(q[j]));                  // a root has no sign
+        }
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {               // values past cnt are 0: m = r = 0; a root has no sign
+            most_m = __vimax3_u32(most_m, __float_as_uint(m[j]) & 0x7fffffffu, __float_as_uint(m[j + 1]) & 0x7fffffffu);
+            most_r = __vimax3_u32(most_r, __float_as_uint(q[j]), __float_as_uint(q[j + 1]));
         }
         st_any<V>(t.master + i, cnt, vec, w);
         if (t.param) st_any<V>(static_cast<Bits<DT>*>(t.param) + i, cnt, vec, p);
         const uint32_t em = scale_field(__reduce_max_sync(0xffffffffu, most_m));
         const uint32_t er = scale_field(__reduce_max_sync(0xffffffffu, most_r));
-        const Factors nm = factors_of<kUpM>(em), nr = factors_of<kUpR>(er);
-        const bool far = nm.over != 1.0f || nr.over != 1.0f;
-        uint32_t nonzero = 0;                          // roots; scaled far down they may become 0
-        if (far) {
-            const float dm = pow2_field(254u - (127u + em - min(em, 253u - kUpM)));   // 1 / over
-            const float dr = pow2_field(254u - (127u + er - min(er, 253u - kUpR)));
-#pragma unroll
-            for (int j = 0; j < V; j++) {
-                nonzero |= (uint32_t)(q[j] > 0.0f) << j;
-                m[j] = __fmul_rn(m[j], dm);
-                q[j] = __fmul_rn(q[j], dr);
-            }
-        }
+        const float cm = enc_factor<kUpM>(em), cr = enc_factor<kUpR>(er);
         const uint32_t base = hash_base((uint64_t)(r.start + i), hp.mix);
-        uint32_t cm[V], cr[V];
+        const bool far = far_scale<kUpM>(em) || far_scale<kUpR>(er);
+        uint32_t um[V], ur[V];
 #pragma unroll
         for (int j = 0; j < V; j += 2) {
             const uint32_t h = hash_pair(base, j / 2);
-            const uint32_t r0 = (h & 0xffffu) << 3, r1 = (h >> 13) & 0x7fff8u;
-            cm[j] = encode_m(m[j], nm.enc, r0);
-            cm[j + 1] = encode_m(m[j + 1], nm.enc, r1);
-            cr[j] = encode_r(q[j], nr.enc, r0);
-            cr[j + 1] = encode_r(q[j + 1], nr.enc, r1);
+            const uint32_t r0 = (h << 3) & 0x7fff8u, r1 = (h >> 13) & 0x7fff8u;
+            um[j] = __float_as_uint(__fmul_rn(m[j], cm)) + r0;
+            um[j + 1] = __float_as_uint(__fmul_rn(m[j + 1], cm)) + r1;
+            ur[j] = __float_as_uint(__fmul_rn(q[j], cr)) + r0;
+            ur[j + 1] = __float_as_uint(__fmul_rn(q[j + 1], cr)) + r1;
         }
-        if (far) {                                     // the last scale, or not finite: cut to the largest code
+        if (far) {
+            // two factors; the last scale, and what is not finite, is cut to the
+            // largest code
 #pragma unroll
             for (int j = 0; j < V; j++) {
-                if ((cm[j] & ~0x80u) > 127u || (__float_as_uint(__fmul_rn(fabsf(m[j]), nm.enc)) >> 19) >= 127u)
-                    cm[j] = 127u | (m[j] < 0.0f ? 128u : 0u);
-                cr[j] = max(min(cr[j], 255u), nonzero >> j & 1u);
+                const uint32_t h = hash_pair(base, j / 2), rnd = j & 1 ? (h >> 13) & 0x7fff8u : (h << 3) & 0x7fff8u;
+                const uint32_t xm = __float_as_uint(__fmul_rn(__fmul_rn(fabsf(m[j]), rest_inverse<kUpM>(em)), cm));
+                const uint32_t xr = __float_as_uint(__fmul_rn(__fmul_rn(q[j], rest_inverse<kUpR>(er)), cr));
+                um[j] = (min((min(xm, 0x7f800000u) + rnd) >> 19, 127u) << 19) | (m[j] < 0.0f ? 0x80000000u : 0u);
+                ur[j] = min((min(xr, 0x7f800000u) + rnd) >> 19, 255u) << 19;
             }
         }
         alignas(8) uint8_t nm8[V], nr8[V];
-        *reinterpret_cast<uint2*>(nm8) = make_uint2(pack4(cm), pack4(cm + 4));
-        *reinterpret_cast<uint2*>(nr8) = make_uint2(pack4(cr), pack4(cr + 4));
+        *reinterpret_cast<uint2*>(nm8) = make_uint2(pack_m(um), pack_m(um + 4));
+        *reinterpret_cast<uint2*>(nr8) = make_uint2(pack_r(ur, q), pack_r(ur + 4, q + 4));
         st_any<V>(static_cast<uint8_t*>(t.m) + i, cnt, vec, nm8);
         st_any<V>(static_cast<uint8_t*>(t.v) + i, cnt, vec, nr8);
         if (lane == 0) {
@@ -332,7 +353,7 @@ __device__ __forceinline__ uint32_t upper_halves(float lo, float hi)
     return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
 }
 
-__global__ void __launch_bounds__(kAdThreads) k_adamw_states(const AdTable tab, uint16_t* m_out, uint16_t* r_out)
+__global__ void __launch_bounds__(kStateThreads) k_adamw_states(const AdTable tab, uint16_t* m_out, uint16_t* r_out)
 {
     constexpr int V = 8;
     const AdRec& r = tab.rec[tab.chunk_tensor[blockIdx.x]];
@@ -342,21 +363,24 @@ __global__ void __launch_bounds__(kAdThreads) k_adamw_states(const AdTable tab, 
     const int64_t hi = min(lo + kChunk, t.numel);
     const bool vec = r.aligned;
 #pragma unroll 4
-    for (int64_t i = lo + threadIdx.x * V; i < hi; i += kAdThreads * V) {
+    for (int64_t i = lo + threadIdx.x * V; i < hi; i += kStateThreads * V) {
         const int cnt = (int)min((int64_t)V, hi - i);
         alignas(8) uint8_t cm[V], cr[V];
         ld_any<V>(static_cast<const uint8_t*>(t.m) + i, cnt, vec, cm);
         ld_any<V>(static_cast<const uint8_t*>(t.v) + i, cnt, vec, cr);
         const uint2 wm = *reinterpret_cast<const uint2*>(cm), wr = *reinterpret_cast<const uint2*>(cr);
-        const Factors fm = factors_of<kUpM>(t.m_scale[i / kQBlock]), fr = factors_of<kUpR>(t.v_scale[i / kQBlock]);
+        const uint32_t em = t.m_scale[i / kQBlock], er = t.v_scale[i / kQBlock];
+        const float dm = dec_factor<kUpM>(em), dr = dec_factor<kUpR>(er);
         alignas(16) uint32_t m[V / 2], q[V / 2];
 #pragma unroll
         for (int k = 0; k < V / 2; k++) {
             float x[2], y[2];
 #pragma unroll
             for (int e = 0; e < 2; e++) {
-                x[e] = __fmul_rn(decode_m(byte_on_top(wm, 2 * k + e), fm.dec), fm.over);
-                y[e] = __fmul_rn(decode_r(byte_on_top(wr, 2 * k + e), fr.dec), fr.over);
+                x[e] = decode_m(byte_on_top(wm, 2 * k + e), dm);
+                y[e] = decode_r(byte_on_top(wr, 2 * k + e), dr);
+                if (far_scale<kUpM>(em)) x[e] = __fmul_rn(x[e], rest_factor<kUpM>(em));
+                if (far_scale<kUpR>(er)) y[e] = __fmul_rn(y[e], rest_factor<kUpR>(er));
             }
             m[k] = upper_halves(x[0], x[1]);
             q[k] = upper_halves(y[0], y[1]);
@@ -367,7 +391,7 @@ __global__ void __launch_bounds__(kAdThreads) k_adamw_states(const AdTable tab, 
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kAdThreads) k_adamw_check(const AdTable tab, uint32_t* flag)
+__global__ void __launch_bounds__(kAd32Threads) k_adamw_check(const AdTable tab, uint32_t* flag)
 {
     constexpr int V = 8;
     const AdRec& r = tab.rec[tab.chunk_tensor[blockIdx.x]];
@@ -375,7 +399,7 @@ __global__ void __launch_bounds__(kAdThreads) k_adamw_check(const AdTable tab, u
     const int64_t hi = min(lo + kChunk, r.t.numel);
     const Bits<DT>* grad = static_cast<const Bits<DT>*>(r.t.grad);
     uint32_t bad = 0;
-    for (int64_t i = lo + threadIdx.x * V; i < hi; i += kAdThreads * V) {
+    for (int64_t i = lo + threadIdx.x * V; i < hi; i += kAd32Threads * V) {
         const int cnt = (int)min((int64_t)V, hi - i);
         alignas(16) Bits<DT> g[V];
         ld_any<V>(grad + i, cnt, r.aligned, g);
@@ -542,11 +566,11 @@ zero_status_t zero_adamw_check(const zero_adamw_plan_t* plan, const void* table,
         const AdTable tab = table_of(table, plan->n_tensors);
         const unsigned grid = (unsigned)plan->n_chunks;
         if (plan->dtype == ZERO_FP32)
-            k_adamw_check<kF32><<<grid, kAdThreads, 0, s>>>(tab, flag);
+            k_adamw_check<kF32><<<grid, kAd32Threads, 0, s>>>(tab, flag);
         else if (plan->dtype == ZERO_BF16)
-            k_adamw_check<kBF16><<<grid, kAdThreads, 0, s>>>(tab, flag);
+            k_adamw_check<kBF16><<<grid, kAd32Threads, 0, s>>>(tab, flag);
         else
-            k_adamw_check<kF16><<<grid, kAdThreads, 0, s>>>(tab, flag);
+            k_adamw_check<kF16><<<grid, kAd32Threads, 0, s>>>(tab, flag);
         err = cudaGetLastError();
     }
     return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_adamw_check");
@@ -587,13 +611,13 @@ zero_status_t zero_adamw_step(const zero_adamw_plan_t* plan, const void* table, 
     const unsigned grid = (unsigned)plan->n_chunks;
     const int dt = plan->dtype;
     if (plan->state_bits == 32) {
-        if (dt == ZERO_FP32) k_adamw32<kF32><<<grid, kAdThreads, 0, s>>>(tab, h, skip);
-        else if (dt == ZERO_BF16) k_adamw32<kBF16><<<grid, kAdThreads, 0, s>>>(tab, h, skip);
-        else k_adamw32<kF16><<<grid, kAdThreads, 0, s>>>(tab, h, skip);
+        if (dt == ZERO_FP32) k_adamw32<kF32><<<grid, kAd32Threads, 0, s>>>(tab, h, skip);
+        else if (dt == ZERO_BF16) k_adamw32<kBF16><<<grid, kAd32Threads, 0, s>>>(tab, h, skip);
+        else k_adamw32<kF16><<<grid, kAd32Threads, 0, s>>>(tab, h, skip);
     } else {
-        if (dt == ZERO_FP32) k_adamw8<kF32><<<grid, kAdThreads, 0, s>>>(tab, h, skip);
-        else if (dt == ZERO_BF16) k_adamw8<kBF16><<<grid, kAdThreads, 0, s>>>(tab, h, skip);
-        else k_adamw8<kF16><<<grid, kAdThreads, 0, s>>>(tab, h, skip);
+        if (dt == ZERO_FP32) k_adamw8<kF32><<<grid, kAd8Threads, 0, s>>>(tab, h, skip);
+        else if (dt == ZERO_BF16) k_adamw8<kBF16><<<grid, kAd8Threads, 0, s>>>(tab, h, skip);
+        else k_adamw8<kF16><<<grid, kAd8Threads, 0, s>>>(tab, h, skip);
     }
     const cudaError_t err = cudaGetLastError();
     return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_adamw_step");
@@ -610,7 +634,7 @@ zero_status_t zero_adamw_states(const zero_adamw_plan_t* plan, const void* table
     if (!aligned_to(m, 16) || !aligned_to(root_v, 16))
         return set_error(ZERO_EALIGN, "zero_adamw_states: an output is not 16-byte aligned");
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    k_adamw_states<<<(unsigned)plan->n_chunks, kAdThreads, 0, s>>>(table_of(table, plan->n_tensors),
+    k_adamw_states<<<(unsigned)plan->n_chunks, kStateThreads, 0, s>>>(table_of(table, plan->n_tensors),
                                                                    static_cast<uint16_t*>(m),
                                                                    static_cast<uint16_t*>(root_v));
     const cudaError_t err = cudaGetLastError();

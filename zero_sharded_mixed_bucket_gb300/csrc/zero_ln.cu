@@ -5,6 +5,7 @@
 #include <cstring>
 
 #include "dev_common.cuh"
+#include "dev_copy.cuh"
 #include "nvtx_ranges.h"
 
 namespace zg {
@@ -84,20 +85,6 @@ __device__ __forceinline__ float block_sum(float v, float* sh)
 // 20 backward, where the memory's rate leaves room for 20 to 30), so a batch
 // is as large as that allows: its sums, addresses and loop are shared
 // by all its values.
-__device__ __forceinline__ void copy_ahead(void* smem, const void* src, int bytes)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                 :: "r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(src), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-template <int PENDING>
-__device__ __forceinline__ void copies_wait()
-{
-    asm volatile("cp.async.wait_group %0;" :: "n"(PENDING) : "memory");
-}
-
 // Values of vector v of lane gl of a group of `lanes` that exist.
 template <int DT>
 __device__ __forceinline__ int vec_count(int64_t dim, int v, int gl, int lanes)
@@ -288,7 +275,7 @@ __global__ void __launch_bounds__(kLnThreads, BLOCKS) k_ln_forward_rows(const __
             if (b < here)
 #pragma unroll
                 for (int v = 0; v < V; v++)
-                    if (cnt[v]) copy_ahead(at + (b * V + v) * T, p + v * apart, RAGGED ? cnt[v] * E : 16);
+                    if (cnt[v]) copy_ahead<16>(at + (b * V + v) * T, p + v * apart, RAGGED ? cnt[v] * E : 16);
         copies_issued();
         ahead += stride;
         src += stride * x_row;
@@ -421,8 +408,8 @@ __global__ void __launch_bounds__(kLnThreads, BLOCKS) k_ln_backward_rows(const _
                 uint4* p = at + (b * V + v) * 2 * T;
                 if (b < here) {
                     if (cnt[v]) {
-                        copy_ahead(p, px + v * apart, RAGGED ? cnt[v] * E : 16);
-                        copy_ahead(p + T, py + v * apart, RAGGED ? cnt[v] * E : 16);
+                        copy_ahead<16>(p, px + v * apart, RAGGED ? cnt[v] * E : 16);
+                        copy_ahead<16>(p + T, py + v * apart, RAGGED ? cnt[v] * E : 16);
                     }
                 } else {                              // rows past the end: all 0
                     p[0] = p[T] = make_uint4(0, 0, 0, 0);
