@@ -535,9 +535,193 @@ __global__ void __launch_bounds__(kLnThreads, BLOCKS) k_ln_backward_rows(const _
     }
 }
 
-// ---- any row -------------------------------------------------------------------------
-// Rows off 16-byte boundaries, or longer than the registers hold: a block per
-// row, values read again for every use (from cache).
+// ---- rows off 16-byte boundaries -------------------------------------------------------
+// The same groups, a lane's K values of a row one group of lanes apart: one
+// access a value, neighbouring lanes neighbouring values, kept in registers as
+// binary32.  What bounds these is the accesses.
+template <int DT, int K>
+__device__ __forceinline__ void ld_strided(const void* p, int64_t at, int gl, int lanes, int here, float f[K])
+{
+    // loads without branches, so that all of them are on their way at once: past
+    // the row's end its first value again, dropped
+    const char* row = static_cast<const char*>(p) + at * (DT == kF32 ? 4 : 2);
+#pragma unroll
+    for (int k = 0; k < K; k++)
+        f[k] = ld1<DT>(row, k < here ? gl + k * lanes : 0);
+#pragma unroll
+    for (int k = 0; k < K; k++)
+        f[k] = k < here ? f[k] : 0.0f;
+}
+
+template <int DT, int L, int K, int RB>
+__global__ void __launch_bounds__(kLnThreads, 2) k_ln_forward_any(const __grid_constant__ LnArgs a)
+{
+    __shared__ float sh[2 * (kLnThreads / 32) * RB];
+    const int lanes = L < 32 ? L : 32 * a.warps, gl = threadIdx.x % lanes, group = threadIdx.x / lanes;
+    const int groups = blockDim.x / lanes;
+    const int here = gl < a.dim ? (int)((a.dim - 1 - gl) / lanes) + 1 : 0;         // values of the row that the lane has
+    const float inv = 1.0f / (float)a.dim;
+    int turn = 0;
+    const int64_t stride = (int64_t)gridDim.x * groups * RB;
+    int64_t r0 = ((int64_t)blockIdx.x * groups + group) * RB;
+    const int64_t first = L < 32 ? r0 - (int64_t)((threadIdx.x & 31) / L) * RB : r0;
+    for (int64_t rw = first; rw < a.rows; rw += stride, r0 += stride) {
+        const int rows = rows_here(a.rows, r0, RB);
+        float f[RB][K], mean[RB], rstd[RB];
+#pragma unroll
+        for (int b = 0; b < RB; b++)
+            ld_strided<DT, K>(a.x, min(r0 + b, a.rows - 1) * a.x_stride, gl, lanes, here, f[b]);   // past the end: not written
+#pragma unroll
+        for (int b = 0; b < RB; b++) {
+            float s = 0.0f;
+#pragma unroll
+            for (int k = 0; k < K; k++)
+                s += f[b][k];
+            mean[b] = s;
+        }
+        group_sum<L, RB>(mean, a.warps, sh, turn);
+#pragma unroll
+        for (int b = 0; b < RB; b++) {
+            mean[b] *= inv;
+            float s = 0.0f;
+#pragma unroll
+            for (int k = 0; k < K; k++) {
+                f[b][k] -= mean[b];
+                if (k < here) s = fmaf(f[b][k], f[b][k], s);
+            }
+            rstd[b] = s;
+        }
+        group_sum<L, RB>(rstd, a.warps, sh, turn);
+#pragma unroll
+        for (int b = 0; b < RB; b++)
+            rstd[b] = rsqrtf(fmaf(rstd[b], inv, a.eps));
+#pragma unroll
+        for (int k0 = 0; k0 < K; k0 += 8) {
+            float w[8], bias[8];
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                const int j = k0 + k < here ? gl + (k0 + k) * lanes : 0;
+                w[k] = a.weight ? ld1<DT>(a.weight, j) : 1.0f;
+                bias[k] = a.bias ? ld1<DT>(a.bias, j) : 0.0f;
+            }
+#pragma unroll
+            for (int b = 0; b < RB; b++) {
+                char* row = static_cast<char*>(a.y) + (r0 + b) * a.y_stride * (DT == kF32 ? 4 : 2);
+#pragma unroll
+                for (int k = 0; k < 8; k++)
+                    if (b < rows && k0 + k < here)
+                        st1<DT>(row, gl + (k0 + k) * lanes, fmaf(f[b][k0 + k] * rstd[b], w[k], bias[k]));
+            }
+        }
+        if (gl == 0) {
+#pragma unroll
+            for (int b = 0; b < RB; b++) {
+                if (b < rows && a.mean) a.mean[r0 + b] = mean[b];
+                if (b < rows && a.rstd) a.rstd[r0 + b] = rstd[b];
+            }
+        }
+    }
+}
+
+template <int DT, int L, int K, int RB>
+__global__ void __launch_bounds__(kLnThreads, 2) k_ln_backward_any(const __grid_constant__ LnArgs a)
+{
+    __shared__ float sh[2 * (kLnThreads / 32) * 2 * RB];
+    __shared__ float join[K == 8 ? 2 * K * kLnThreads : 1];       // [group][dw, db][K][lanes]
+    const int lanes = L < 32 ? L : 32 * a.warps, gl = threadIdx.x % lanes, group = threadIdx.x / lanes;
+    const int groups = blockDim.x / lanes;
+    const int here = gl < a.dim ? (int)((a.dim - 1 - gl) / lanes) + 1 : 0;
+    const float inv = 1.0f / (float)a.dim;
+    int turn = 0;
+    float dw[K], db[K];
+#pragma unroll
+    for (int k = 0; k < K; k++)
+        dw[k] = db[k] = 0.0f;
+    const int64_t stride = (int64_t)gridDim.x * groups * RB;
+    int64_t r0 = ((int64_t)blockIdx.x * groups + group) * RB;
+    const int64_t first = L < 32 ? r0 - (int64_t)((threadIdx.x & 31) / L) * RB : r0;
+    for (int64_t rw = first; rw < a.rows; rw += stride, r0 += stride) {
+        const int rows = rows_here(a.rows, r0, RB);
+        float x[RB][K], dy[RB][K], rstd[RB], c[2 * RB];
+#pragma unroll
+        for (int b = 0; b < RB; b++) {
+            const int64_t r = min(r0 + b, a.rows - 1);
+            ld_strided<DT, K>(a.x, r * a.x_stride, gl, lanes, here, x[b]);
+            ld_strided<DT, K>(a.dy, r * a.y_stride, gl, lanes, b < rows ? here : 0, dy[b]);
+        }
+#pragma unroll
+        for (int b = 0; b < RB; b++) {
+            const int64_t r = min(r0 + b, a.rows - 1);
+            const float mean = a.mean_in[r];
+            rstd[b] = a.rstd_in[r];
+            c[2 * b] = c[2 * b + 1] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < K; k++) {
+                x[b][k] -= mean;
+                if (b < rows) {
+                    dw[k] = fmaf(dy[b][k] * rstd[b], x[b][k], dw[k]);
+                    db[k] += dy[b][k];
+                }
+            }
+        }
+        if (!a.dx) continue;
+        if (a.weight) {
+            float w[K];
+            ld_strided<DT, K>(a.weight, 0, gl, lanes, here, w);
+#pragma unroll
+            for (int b = 0; b < RB; b++)
+#pragma unroll
+                for (int k = 0; k < K; k++)
+                    dy[b][k] *= w[k];
+        }
+#pragma unroll
+        for (int b = 0; b < RB; b++)
+#pragma unroll
+            for (int k = 0; k < K; k++) {
+                c[2 * b] += dy[b][k];
+                c[2 * b + 1] = fmaf(dy[b][k], x[b][k], c[2 * b + 1]);
+            }
+        group_sum<L, 2 * RB>(c, a.warps, sh, turn);
+#pragma unroll
+        for (int b = 0; b < RB; b++) {
+            const float k0 = -(c[2 * b] * inv) * rstd[b];
+            const float k1 = -(c[2 * b + 1] * inv * rstd[b]) * rstd[b] * rstd[b];
+            char* row = static_cast<char*>(a.dx) + (r0 + b) * a.x_stride * (DT == kF32 ? 4 : 2);
+#pragma unroll
+            for (int k = 0; k < K; k++)
+                if (b < rows && k < here) st1<DT>(row, gl + k * lanes, fmaf(x[b][k], k1, fmaf(dy[b][k], rstd[b], k0)));
+        }
+    }
+    if (!a.part) return;
+    float* pw = a.part + 2 * (int64_t)blockIdx.x * a.dim;
+    if (K == 8 && groups > 1) {
+        const int one = 2 * K * lanes;
+#pragma unroll
+        for (int k = 0; k < K; k++) {
+            join[group * one + k * lanes + gl] = dw[k];
+            join[group * one + (K + k) * lanes + gl] = db[k];
+        }
+        __syncthreads();
+        for (int t = threadIdx.x; t < one; t += blockDim.x) {
+            float s = 0.0f;
+            for (int g = 0; g < groups; g++)
+                s += join[g * one + t];
+            const int64_t j = t < K * lanes ? t : t - K * lanes;
+            if (j < a.dim) pw[(t < K * lanes ? 0 : a.dim) + j] = s;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; k++)
+            if (k < here) {
+                pw[gl + (int64_t)k * lanes] = dw[k];
+                pw[a.dim + gl + (int64_t)k * lanes] = db[k];
+            }
+    }
+}
+
+// ---- long rows -------------------------------------------------------------------------
+// More than the registers of a block hold: a block per row, values read again
+// for every use (from cache).
 template <int DT>
 __global__ void __launch_bounds__(kLnThreads) k_ln_forward(const __grid_constant__ LnArgs a)
 {
@@ -712,6 +896,16 @@ cudaError_t forward_rows(LnArgs a, int64_t vecs, cudaStream_t s)
     return launch_slots<k_ln_forward_rows<DT, L, V, RB, S, BLOCKS, false>, smem>(a, blocks, h.threads, s);
 }
 
+template <int DT, int L, int K, int RB>
+cudaError_t forward_any(LnArgs a, int64_t eights, cudaStream_t s)
+{
+    const RowShape h = shape_of(eights, L, K / 8);
+    a.warps = h.warps;
+    const int64_t at_once = (int64_t)h.groups * RB, need = (a.rows + at_once - 1) / at_once;
+    const int64_t most = (int64_t)kSms * (2 * kLnThreads / h.threads);
+    return launch_rows(k_ln_forward_any<DT, L, K, RB>, a, need < most ? need : most, h.threads, 0, s);
+}
+
 template <int DT>
 cudaError_t forward(const LnArgs& a, bool vec, cudaStream_t s)
 {
@@ -724,6 +918,14 @@ cudaError_t forward(const LnArgs& a, bool vec, cudaStream_t s)
     if (vec && vecs <= 512) return forward_rows<DT, 32, 2, kLnFwdRows / 2, kLnFwdAhead, kLnFwdBlocks>(a, vecs, s);
     if (vec && vecs <= 1024) return forward_rows<DT, 32, 4, kLnFwdRows / 4, kLnFwdAhead, kLnFwdBlocks>(a, vecs, s);
     if (vec && vecs <= 2048) return forward_rows<DT, 32, 8, 1, 2, 2>(a, vecs, s);
+    if (!vec) {
+        const int64_t eights = (a.dim + 7) / 8;
+        if (eights <= 8) return forward_any<DT, 8, 8, 4>(a, eights, s);
+        if (eights <= 16) return forward_any<DT, 16, 8, 4>(a, eights, s);
+        if (eights <= 256) return forward_any<DT, 32, 8, 4>(a, eights, s);
+        if (eights <= 512) return forward_any<DT, 32, 16, 2>(a, eights, s);
+        if (eights <= 1024) return forward_any<DT, 32, 32, 1>(a, eights, s);
+    }
     return launch_rows(k_ln_forward<DT>, a, a.rows < kSms * 8 ? a.rows : kSms * 8, kLnThreads, 0, s);
 }
 
@@ -754,6 +956,14 @@ int64_t backward_blocks(int64_t rows, int64_t vecs, bool whole)
     return need < most ? need : most;
 }
 
+template <int DT, int L, int K, int RB>
+cudaError_t backward_any(LnArgs a, int64_t eights, int blocks, cudaStream_t s)
+{
+    const RowShape h = shape_of(eights, L, K / 8);
+    a.warps = h.warps;
+    return launch_rows(k_ln_backward_any<DT, L, K, RB>, a, blocks, h.threads, 0, s);
+}
+
 template <int DT>
 cudaError_t backward(LnArgs a, bool vec, int blocks, void* dw, void* db, cudaStream_t s)
 {
@@ -769,6 +979,12 @@ cudaError_t backward(LnArgs a, bool vec, int blocks, void* dw, void* db, cudaStr
         else if (vecs <= 256) e = backward_rows<DT, 32, 1, kLnBwdRows>(a, vecs, blocks, s);
         else if (vecs <= 512) e = backward_rows<DT, 32, 2, kLnBwdRows / 2>(a, vecs, blocks, s);
         else e = backward_rows<DT, 32, 4, kLnBwdRows / 4>(a, vecs, blocks, s);
+    } else if (blocks && !vec && a.dim <= 4096) {
+        const int64_t eights = (a.dim + 7) / 8;
+        if (eights <= 8) e = backward_any<DT, 8, 8, 2>(a, eights, blocks, s);
+        else if (eights <= 16) e = backward_any<DT, 16, 8, 2>(a, eights, blocks, s);
+        else if (eights <= 256) e = backward_any<DT, 32, 8, 2>(a, eights, blocks, s);
+        else e = backward_any<DT, 32, 16, 1>(a, eights, blocks, s);
     } else {
         if (a.dx && a.rows) e = launch_rows(k_ln_dx<DT>, a, a.rows < kSms * 8 ? a.rows : kSms * 8, kLnThreads, 0, s);
         if (e == cudaSuccess && sums && blocks) {
