@@ -327,3 +327,48 @@ def test_8bit_moments_follow_a_decaying_gradient():
     # variance is at most (move per step) * gap, so v's relative excess stays below
     # gap^2-sized terms, a few percent, and the mean over 4096 values is tight
     assert abs(np.sqrt((r1 ** 2).mean()) - want1) < 0.1 * want1
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_offsets_past_32_bits(bits):
+    """A tensor of 2^33 + 777 values: the values around 2^32 and at the end as in
+    a short list (8 bits: with the same random numbers, which go by a value's
+    place)."""
+    n, zero = 2 ** 33 + 777, torch.uint8 if bits == 8 else torch.float32
+    if bits == 32:
+        n = 2 ** 32 + 777
+    grad = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    master = torch.zeros(n, device="cuda")
+    m, v = (torch.zeros(n, dtype=zero, device="cuda") for _ in range(2))
+    sc = [torch.zeros(-(-n // 256), dtype=torch.uint8, device="cuda") for _ in range(2)] if bits == 8 else [None, None]
+    g = torch.Generator(device="cuda").manual_seed(0)
+    marks = [2 ** 32 - 512, (n - 1500) // 256 * 256]
+    for a in marks:
+        k = min(1024, n - a)
+        grad[a:a + k] = torch.randn(k, device="cuda", generator=g).bfloat16()
+        master[a:a + k] = torch.randn(k, device="cuda", generator=g)
+    old = [(grad[a:a + 1024].float().cpu().numpy(), master[a:a + 1024].cpu().numpy()) for a in marks]
+    rec = [zg.adamw_tensor(grad=grad, master=master, m=m, v=v, numel=n, m_scale=sc[0], v_scale=sc[1])]
+    plan = zg.zero_adamw_plan(rec, zg.ZERO_BF16, bits)
+    table = torch.empty(plan.table_bytes, dtype=torch.uint8, device="cuda")
+    zg.zero_adamw_table_init(plan, rec, table)
+    hp = _hp(t=1, grad_scale=1.0)
+    zg.zero_adamw_step(plan, table, hp)
+    b1, b2 = F(hp.beta1), F(hp.beta2)
+    for a, (g0, w0) in zip(marks, old):
+        k = g0.size
+        m1, v1 = g0 * (F(1) - b1), (g0 * g0) * (F(1) - b2)
+        if bits == 32:
+            assert np.array_equal(m[a:a + k].cpu().numpy(), m1) and np.array_equal(v[a:a + k].cpu().numpy(), v1)
+            continue
+        r1 = np.sqrt(v1)
+        w1 = w0 - (m1 * F(float(F(hp.lr)) / (1 - float(b1)))) / (r1 * F(1 / np.sqrt(1 - float(b2))) + F(hp.eps))
+        rnd = _random(k, a, hp)
+        cm, em = _codes(np.abs(m1), rnd, 6, 127, False)
+        cr, er = _codes(r1, rnd, 14, 255, True)
+        assert np.array_equal(m[a:a + k].cpu().numpy(), cm + np.where((m1 < 0) & (cm > 0), 128, 0))
+        assert np.array_equal(v[a:a + k].cpu().numpy(), cr)
+        assert np.array_equal(master[a:a + k].cpu().numpy(), w1)
+        assert np.array_equal(sc[0][a // 256:a // 256 + em.size].cpu().numpy(), em)
+    del grad, master, m, v, sc
+    torch.cuda.empty_cache()

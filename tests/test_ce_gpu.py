@@ -325,3 +325,33 @@ def test_bounded_wait_is_reported():
     j.forward()
     zg.zero_ce_status(j.plan, j.ws)
     j.check_forward()
+
+
+@pytest.mark.parametrize("n", [2, 70])
+def test_offsets_past_32_bits(n):
+    """A weight of 2^23 + 5 rows of 576 values: 4.8e9 values, 9.7 GB."""
+    v, d = 2 ** 23 + 5, 576
+    g = torch.Generator(device="cuda").manual_seed(0)
+    w = torch.empty(v, d, dtype=torch.bfloat16, device="cuda")
+    for a in range(0, v, 1 << 20):
+        w[a:a + (1 << 20)] = torch.randn(min(1 << 20, v - a), d, device="cuda", generator=g) * 0.05
+    x = torch.randn(n, d, device="cuda", generator=g).bfloat16()
+    t = torch.randint(v - 1000, v, (n,), device="cuda", generator=g)
+    p = zg.zero_ce_plan(n, v, d, zg.ZERO_BF16)
+    ws = torch.empty(p.workspace_bytes, dtype=torch.uint8, device="cuda")
+    loss, lse, dx, dw = torch.empty(n, device="cuda"), torch.empty(n, device="cuda"), torch.empty_like(x), torch.empty_like(w)
+    zg.zero_ce_forward(p, x, w, t, loss, lse, None, ws)
+    zg.zero_ce_backward(p, x, w, t, lse, None, 1.0, dx, dw, ws)
+    z = torch.cat([x.double() @ w[a:a + (1 << 19)].double().t() for a in range(0, v, 1 << 19)], 1)
+    want = torch.logsumexp(z, 1)
+    # one logit is off by e(d) sum |x w| < 1e-3 here (sum |x w| < 40), the rest by less
+    assert ((lse.double() - want).abs() <= 1e-3).all()
+    assert ((loss.double() - (want - z.gather(1, t[:, None])[:, 0])).abs() <= 2e-3).all()
+    G = torch.softmax(z, 1)
+    G[torch.arange(n), t] -= 1
+    G /= n
+    for a, b in ((0, 300), (2 ** 22 - 100, 2 ** 22 + 100), (v - 1000, v)):
+        ref = G[:, a:b].t() @ x.double()
+        assert (dw[a:b].double() - ref).norm() <= 2.0 ** -7 * ref.norm() + 1e-12
+    ref = sum(G[:, a:a + (1 << 19)] @ w[a:a + (1 << 19)].double() for a in range(0, v, 1 << 19))
+    assert (dx.double() - ref).norm() <= 2.0 ** -7 * ref.norm()
