@@ -530,9 +530,10 @@ zero_status_t zero_pa_gather(const zero_pa_plan_t* plan, const void* const* shar
  * rounded once to its type.  All of x, weight, bias, y, dy, dx, dweight,
  * dbias have the plan's dtype; mean and rstd are binary32, one per row.
  * Rows may lie further apart than dim (strides, in values); what is between
- * them is neither read nor written.  Pointers need the alignment of their
- * type only: rows that start on 16-byte boundaries take 16-byte accesses,
- * others single-value ones.  72 bytes. */
+ * them is neither read nor written.  Outputs must not overlap inputs.
+ * Pointers need the alignment of their type only: rows that start on 16-byte
+ * boundaries take 16-byte accesses, others single-value ones (two to three
+ * times slower in 16-bit types).  72 bytes. */
 typedef struct zero_ln_plan {
     int64_t rows, dim;
     int64_t x_stride;            /* values between rows of x and dx */
@@ -556,8 +557,7 @@ zero_status_t zero_ln_plan(int64_t rows, int64_t dim, int32_t dtype, int64_t x_s
 zero_status_t zero_ln_forward(const zero_ln_plan_t* plan, const void* x, const void* weight, const void* bias,
                               float eps, void* y, float* mean, float* rstd, void* stream);
 /* mean and rstd as the forward pass wrote them.  dx, dweight, dbias NULL:
- * not computed; dx must not overlap dy or x.  dweight and dbias are
- * overwritten, with zeros when there are no rows.  workspace:
+ * not computed.  dweight and dbias are overwritten, with zeros when there are no rows.  workspace:
  * plan->workspace_bytes, 16-byte aligned (may be NULL when neither dweight
  * nor dbias is wanted). */
 zero_status_t zero_ln_backward(const zero_ln_plan_t* plan, const void* dy, const void* x, const void* weight,
@@ -655,7 +655,8 @@ zero_status_t zero_ce_status(const zero_ce_plan_t* plan, const void* workspace, 
  *     w = w - (m * (lr/bc1)) / (r * (1/sqrt(bc2)) + eps)
  * master is the binary32 weight; param (may be NULL) receives its cast to
  * the plan's dtype, the type of grad.  Non-finite gradients poison the
- * values they meet: see zero_adamw_check.  72 bytes. */
+ * values they meet: see zero_adamw_check.  With eps 0 a weight whose
+ * gradients were all zero becomes 0/0, as the formula says.  72 bytes. */
 typedef struct zero_adamw_tensor {
     const void* grad;
     void* param;                 /* NULL: not written */

@@ -355,3 +355,12 @@ def test_offsets_past_32_bits(n):
         assert (dw[a:b].double() - ref).norm() <= 2.0 ** -7 * ref.norm() + 1e-12
     ref = sum(G[:, a:a + (1 << 19)] @ w[a:a + (1 << 19)].double() for a in range(0, v, 1 << 19))
     assert (dx.double() - ref).norm() <= 2.0 ** -7 * ref.norm()
+
+
+def test_tiny_upstream_gradients():
+    """dloss down to binary32's subnormals: the row factors' inverse stays finite."""
+    j = Job(40, 300, 64, "bf16")
+    j.forward()
+    for d in (1e-30, 1e-39, 0.0):
+        j.backward(1.0, dloss=torch.full((40,), d, device="cuda"))
+        assert j.dx.isfinite().all() and j.dw.isfinite().all()

@@ -18,8 +18,8 @@ constexpr int kStages = 6;
 constexpr int kABytes = kBM / 2 * kBK * 2, kBBytes = kBN / 2 * kBK * 2;   // one CTA's part of a stage
 constexpr int kEpiWarps = 8;
 constexpr int kCeThreads = 64 + 32 * kEpiWarps;       // copying warp, issuing warp, epilogue warps
-constexpr int kOutBytes = 4096, kOutBoxes = 1;        // an epilogue warp's boxes of results: 32 rows of 128 bytes
-constexpr int kCeSmem = kStages * (kABytes + kBBytes) + kEpiWarps * kOutBoxes * kOutBytes + 1024;
+constexpr int kOutBytes = 4096;                       // an epilogue warp's box of results: 32 rows of 128 bytes
+constexpr int kCeSmem = kStages * (kABytes + kBBytes) + kEpiWarps * kOutBytes + 1024;
 constexpr int kStrip = kBN / 2;                       // vocabulary entries per (maximum, sum)
 constexpr int kChunk = 16;                            // loss: K-blocks the tensor cores add up by themselves
 constexpr int kGroup = 8;                             // row tiles that share the column tiles in L2
@@ -72,7 +72,8 @@ struct Tile {
 
 // Tile of a place in the order: splits outermost, then groups of kGroup row
 // tiles, then column tiles, so that the tiles running at one time share rows
-// of A and of B in L2.
+// of A and of B in L2.  32-bit arithmetic: with one K-block to a tile the 64-bit
+// divisions of three roles were in the way.
 __device__ __forceinline__ Tile tile_at(const GemmArgs& g, uint32_t t)
 {
     const uint32_t per = (uint32_t)g.m_tiles * (uint32_t)g.n_tiles, grouped = kGroup * (uint32_t)g.n_tiles;
@@ -94,10 +95,20 @@ __device__ __forceinline__ Tile tile_at(const GemmArgs& g, uint32_t t)
 // products, which accumulate in one of two halves of tensor memory while the
 // epilogue warps read the other.  Every wait is bounded; one that runs out
 // sets head->err and ends its role, and the others run out in turn.
+//
+// Bound by the tensor cores, and at length by the power they take: the logits
+// of 8192 tokens, hidden 4096, vocabulary 50257 take 1.77 ms alone (1905
+// TFLOP/s) and 1.91 ms in a loop (1766; the same bfloat16 product in a library
+// sustains 1714).  256 x 256 by a pair halves what each SM reads of B and what L2
+// delivers, beside 128 x 256 by one CTA with its epilogue in line (11.8 ms for
+// loss and gradients, then 9.9); results through shared memory as tiled copies
+// in place of 2-byte stores: 8.4 ms.  With few tokens w's bytes bound it.
+//
 // A chunk is the K-range that is accumulated in tensor memory at one go: the
 // tensor cores cut their binary32 sums toward zero, 256 times along K = 4096,
 // which is off by 1e-6 of the loss; the loss adds chunks of kChunk K-blocks in
-// registers, rounding to nearest.  The other products are rounded to 16 bits.
+// registers, rounding to nearest (2.6e-7).  The other products are rounded to
+// 16 bits.
 template <int EPI, int DT, bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_gemm(const __grid_constant__ GemmArgs g)
 {
@@ -221,7 +232,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
         const int band = warp & 3;                    // the warp's 32 lanes of tensor memory
         const int half = (warp - 2) >> 2;             // and its 128 columns
         const uint32_t src = tmem + ((uint32_t)(band * 32) << 16) + half * kStrip;
-        const uint32_t box = sm + kStages * (kABytes + kBBytes) + (warp - 2) * (kOutBoxes * kOutBytes);
+        const uint32_t box = sm + kStages * (kABytes + kBBytes) + (warp - 2) * kOutBytes;
         int unit = 0;
         bool ok = true;
         for (uint32_t t = first; t < tiles && ok; t += stride) {
@@ -356,18 +367,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
                             if (col0 + k < g.n) g.out[row * g.out_stride + col0 + k] = (uint16_t)from_f32<DT>(z[k]);
                     continue;
                 }
-                // the warp's boxes: 32 rows of 128 bytes with the copy's swizzle (16-byte
-                // unit j of row i at j ^ (i & 7): no bank conflicts); one copy out per box
+                // the warp's box: 32 rows of 128 bytes with the copy's swizzle (16-byte
+                // unit j of row i at j ^ (i & 7): no bank conflicts); one copy out per
+                // box (a second box for a stage less: 2 % slower)
                 const int y = row0 + (EPI == kEpiAcc ? w.split * g.m_tiles * kBM : 0);
                 constexpr int kCols = EPI == kEpiAcc ? 32 : 64;       // columns of a box
 #pragma unroll
                 for (int c = 0; c < kStrip; c += kCols) {
-                    const uint32_t to = box + c / kCols % kOutBoxes * kOutBytes;
-                    if (lane == 0) tc::bulk_wait_read<kOutBoxes - 1>();
+                    if (lane == 0) tc::bulk_wait_read();
                     __syncwarp();
 #pragma unroll
                     for (int k = 0; k < 8; k++) {
-                        const uint32_t at = to + lane * 128 + ((k ^ (lane & 7)) << 4);
+                        const uint32_t at = box + lane * 128 + ((k ^ (lane & 7)) << 4);
                         if constexpr (EPI == kEpiAcc) {
                             const float* p = z + c + 4 * k;
                             tc::st_shared16(at, __float_as_uint(p[0]), __float_as_uint(p[1]), __float_as_uint(p[2]),
@@ -383,11 +394,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
                     const int64_t x = col0 + c;
                     if (lane == 0 && row0 < g.m && x < (EPI == kEpiGrad ? g.c_cols : g.n)) {
                         if (EPI == kEpiAcc && g.accumulate)
-                            tc::tma_add(&g.c, (int)x, y, to);
+                            tc::tma_add(&g.c, (int)x, y, box);
                         else
-                            tc::tma_store(&g.c, (int)x, y, to);
+                            tc::tma_store(&g.c, (int)x, y, box);
+                        tc::bulk_commit();
                     }
-                    if (lane == 0) tc::bulk_commit();             // one group a box, empty ones too
                 }
             }
         }
@@ -744,6 +755,7 @@ __global__ void __launch_bounds__(1024) k_ce_factors(CeHead* head, const int64_t
         __syncthreads();
     }
     most = sm[0];
+    if (most > 0.0f) most = fmaxf(most, 0x1p-120f);          // its inverse stays finite
     const float inv = most > 0.0f ? 1.0f / most : (most == 0.0f ? 0.0f : most);
     if (threadIdx.x == 0) {
         head->err = 0;
