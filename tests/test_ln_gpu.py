@@ -66,6 +66,9 @@ SHAPES = [  # rows, dim, x pad, y pad, shift of the first row in values
     (300, 64, 0, 0, 0), (33, 255, 1, 0, 0), (257, 1000, 0, 24, 0), (64, 1600, 0, 0, 0), (130, 4096, 0, 0, 0),
     (19, 4096, 8, 8, 8), (19, 4096, 0, 0, 1), (1003, 771, 5, 5, 0), (9, 8192, 0, 0, 0), (6, 8200, 0, 0, 0),
     (3, 16384, 0, 0, 0), (2, 20000, 0, 0, 0), (2, 70001, 0, 0, 0), (2500, 96, 0, 0, 0), (9000, 8, 0, 0, 0),
+    # rows on 4-byte boundaries, and rows of a block of 512 threads
+    (300, 134, 0, 0, 0), (37, 770, 0, 0, 2), (611, 1438, 0, 2, 0), (11, 5806, 0, 0, 0), (350, 10460, 0, 0, 0),
+    (5, 13001, 1, 1, 0), (170, 12000, 0, 0, 0), (3, 30002, 0, 0, 0), (2, 32768, 0, 0, 0),
 ]
 
 

@@ -72,7 +72,7 @@ __device__ __forceinline__ float block_sum(float v, float* sh)
     return t;
 }
 
-// ---- rows on 16-byte boundaries --------------------------------------------------------
+// ---- rows on 16-byte (or 4-byte) boundaries ---------------------------------------------
 // A group of lanes takes RB rows at a time, V 16-byte vectors of a row to a
 // lane: W warps (V > 1 only where 8 warps are not enough), or L < 32 lanes of
 // one for short rows.  A block is as many groups as fit 8 warps.  Each lane
@@ -117,15 +117,15 @@ __device__ __forceinline__ float lane_sums(float (&x)[N])
 }
 
 // Sums over the group of N values at once, the same in every lane.  sh: room
-// for [2][8 warps][N] of the block; `turn` alternates, so one barrier a call.
-template <int L, int N>
+// for [2][T / 32 warps][N] of the block; `turn` alternates, so one barrier a call.
+template <int L, int N, int T = kLnThreads>
 __device__ __forceinline__ void group_sum(float (&x)[N], int warps, float* sh, int& turn)
 {
     const int lane = threadIdx.x & 31;
     float s = lane_sums<L, N>(x);
     if (L == 32 && warps > 1) {
         const int warp = threadIdx.x >> 5, group = warp / warps;
-        float* slot = sh + (turn & 1) * (kLnThreads / 32) * N;
+        float* slot = sh + (turn & 1) * (T / 32) * N;
         if (lane < N) slot[warp * N + lane] = s;
         asm volatile("bar.sync %0, %1;" :: "r"(1 + group), "r"(32 * warps) : "memory");
         // lane l: value l % N of every (32 / N)th warp; then a tree over the lanes of
@@ -133,7 +133,7 @@ __device__ __forceinline__ void group_sum(float (&x)[N], int warps, float* sh, i
         s = 0.0f;
         slot += group * warps * N;
 #pragma unroll
-        for (int q = 0; q < (kLnThreads / 32 * N + 31) / 32; q++) {
+        for (int q = 0; q < (T / 32 * N + 31) / 32; q++) {
             const int at = lane + 32 * q;
             if (at < warps * N) s += slot[at];
         }
@@ -216,14 +216,34 @@ __device__ __forceinline__ void store16(char* p, const uint32_t w[4])
     __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
 }
 
-// A lane's vector out: all of it, or (RAGGED) the values that exist.
-template <int DT, bool RAGGED>
+// A lane's vector out: all of it, or (RAGGED) the values that exist; rows on
+// ALIGN-byte boundaries (16 or 4).
+template <int DT, bool RAGGED, int ALIGN>
 __device__ __forceinline__ void store_vec(char* p, const Vals<DT>& v, int cnt)
 {
-    if (!RAGGED || cnt == kVecOf<DT>)
-        store16(p, v.w);
-    else
+    if (RAGGED && cnt < kVecOf<DT>) {
         st_vals<DT>(p, 0, v, cnt);
+    } else if (ALIGN == 16) {
+        store16(p, v.w);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            __stcs(reinterpret_cast<uint32_t*>(p) + k, v.w[k]);
+    }
+}
+
+// `bytes` of a lane's vector ahead, the rest of the slot 0.
+template <int ALIGN>
+__device__ __forceinline__ void vec_ahead(uint4* slot, const char* src, int bytes)
+{
+    if (ALIGN == 16) {
+        copy_ahead<16>(slot, src, bytes);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            copy_ahead<4>(reinterpret_cast<uint32_t*>(slot) + k, 4 * k < bytes ? src + 4 * k : src,
+                          max(0, min(4, bytes - 4 * k)));
+    }
 }
 
 template <int DT, bool RAGGED>
@@ -242,10 +262,10 @@ __device__ __forceinline__ int rows_here(int64_t rows, int64_t r0, int RB)
 // lane's own sum s and sum of squares m2 about its own mean, the row's sum of
 // squares about its mean is the sum of m2 + n (s/n - mean)^2 over the lanes.
 // RAGGED: dim is not a multiple of a vector's values.
-template <int DT, int L, int V, int RB, int S, int BLOCKS, bool RAGGED>
-__global__ void __launch_bounds__(kLnThreads, BLOCKS) k_ln_forward_rows(const __grid_constant__ LnArgs a)
+template <int DT, int L, int V, int RB, int S, int T, int BLOCKS, bool RAGGED, int ALIGN>
+__global__ void __launch_bounds__(T, BLOCKS) k_ln_forward_rows(const __grid_constant__ LnArgs a)
 {
-    constexpr int VE = kVecOf<DT>, E = DT == kF32 ? 4 : 2, T = kLnThreads;
+    constexpr int VE = kVecOf<DT>, E = DT == kF32 ? 4 : 2;
     extern __shared__ uint4 slots[];                  // [S][RB * V][T]
     __shared__ float sh[2 * (T / 32) * RB];
     const int lanes = L < 32 ? L : 32 * a.warps, gl = threadIdx.x % lanes, group = threadIdx.x / lanes;
@@ -275,7 +295,8 @@ __global__ void __launch_bounds__(kLnThreads, BLOCKS) k_ln_forward_rows(const __
             if (b < here)
 #pragma unroll
                 for (int v = 0; v < V; v++)
-                    if (cnt[v]) copy_ahead<16>(at + (b * V + v) * T, p + v * apart, RAGGED ? cnt[v] * E : 16);
+                    if (cnt[v])
+                        vec_ahead<ALIGN>(at + (b * V + v) * T, p + v * apart, RAGGED ? cnt[v] * E : 16);
         copies_issued();
         ahead += stride;
         src += stride * x_row;
@@ -320,14 +341,14 @@ __global__ void __launch_bounds__(kLnThreads, BLOCKS) k_ln_forward_rows(const __
             mean[b] = s;
             rstd[b] = m2;
         }
-        group_sum<L, RB>(mean, a.warps, sh, turn);
+        group_sum<L, RB, T>(mean, a.warps, sh, turn);
 #pragma unroll
         for (int b = 0; b < RB; b++) {
             mean[b] *= inv;
             const float c = own[b] - mean[b];
             rstd[b] = have ? fmaf(n * c, c, rstd[b]) : 0.0f;
         }
-        group_sum<L, RB>(rstd, a.warps, sh, turn);
+        group_sum<L, RB, T>(rstd, a.warps, sh, turn);
         const int here = rows_here(a.rows, r0, RB);
 #pragma unroll
         for (int b = 0; b < RB; b++)
@@ -347,7 +368,7 @@ __global__ void __launch_bounds__(kLnThreads, BLOCKS) k_ln_forward_rows(const __
 #pragma unroll
                 for (int k = 0; k < VE; k++)
                     f[k] = fmaf((f[k] - mean[b]) * rstd[b], w[k], bias[k]);
-                if (b < here) store_vec<DT, RAGGED>(p, pack<DT>(f), cnt[v]);
+                if (b < here) store_vec<DT, RAGGED, ALIGN>(p, pack<DT>(f), cnt[v]);
             }
         }
         if (gl == 0) {
@@ -370,10 +391,10 @@ __global__ void __launch_bounds__(kLnThreads, BLOCKS) k_ln_forward_rows(const __
 // block writes one pair of partial sums per column (its groups joined in group
 // order).  With d = x - mean and g = dy * weight:
 //   dx = rstd g - rstd avg(g) - rstd^3 avg(g d) d;  dweight = sum (dy rstd) d
-template <int DT, int L, int V, int RB, int S, int BLOCKS, bool RAGGED>
-__global__ void __launch_bounds__(kLnThreads, BLOCKS) k_ln_backward_rows(const __grid_constant__ LnArgs a)
+template <int DT, int L, int V, int RB, int S, int T, int BLOCKS, bool RAGGED, int ALIGN>
+__global__ void __launch_bounds__(T, BLOCKS) k_ln_backward_rows(const __grid_constant__ LnArgs a)
 {
-    constexpr int VE = kVecOf<DT>, E = DT == kF32 ? 4 : 2, T = kLnThreads;
+    constexpr int VE = kVecOf<DT>, E = DT == kF32 ? 4 : 2;
     extern __shared__ uint4 slots[];                  // [S][RB * V][x, dy][T]; at the end the groups' sums
     __shared__ float sh[2 * (T / 32) * 2 * RB];
     const int lanes = L < 32 ? L : 32 * a.warps, gl = threadIdx.x % lanes, group = threadIdx.x / lanes;
@@ -408,8 +429,8 @@ __global__ void __launch_bounds__(kLnThreads, BLOCKS) k_ln_backward_rows(const _
                 uint4* p = at + (b * V + v) * 2 * T;
                 if (b < here) {
                     if (cnt[v]) {
-                        copy_ahead<16>(p, px + v * apart, RAGGED ? cnt[v] * E : 16);
-                        copy_ahead<16>(p + T, py + v * apart, RAGGED ? cnt[v] * E : 16);
+                        vec_ahead<ALIGN>(p, px + v * apart, RAGGED ? cnt[v] * E : 16);
+                        vec_ahead<ALIGN>(p + T, py + v * apart, RAGGED ? cnt[v] * E : 16);
                     }
                 } else {                              // rows past the end: all 0
                     p[0] = p[T] = make_uint4(0, 0, 0, 0);
@@ -470,7 +491,7 @@ __global__ void __launch_bounds__(kLnThreads, BLOCKS) k_ln_backward_rows(const _
             }
         }
         if (a.dx) {
-            group_sum<L, 2 * RB>(c, a.warps, sh, turn);
+            group_sum<L, 2 * RB, T>(c, a.warps, sh, turn);
             const int here = rows_here(a.rows, r0, RB);
 #pragma unroll
             for (int b = 0; b < RB; b++) {
@@ -491,7 +512,7 @@ __global__ void __launch_bounds__(kLnThreads, BLOCKS) k_ln_backward_rows(const _
 #pragma unroll
                     for (int k = 0; k < VE; k++)
                         xf[k] = fmaf(xf[k] - mean[b], c[2 * b + 1], fmaf(yf[k] * w[k], rstd[b], c[2 * b]));
-                    if (b < here) store_vec<DT, RAGGED>(p, pack<DT>(xf), cnt[v]);
+                    if (b < here) store_vec<DT, RAGGED, ALIGN>(p, pack<DT>(xf), cnt[v]);
                 }
             }
         }
@@ -535,7 +556,7 @@ __global__ void __launch_bounds__(kLnThreads, BLOCKS) k_ln_backward_rows(const _
     }
 }
 
-// ---- rows off 16-byte boundaries -------------------------------------------------------
+// ---- other rows ------------------------------------------------------------------------
 // The same groups, a lane's K values of a row one group of lanes apart: one
 // access a value, neighbouring lanes neighbouring values, kept in registers as
 // binary32.  What bounds these is the accesses.
@@ -867,33 +888,36 @@ struct RowShape {
     int groups;                  // of a block
 };
 
-RowShape shape_of(int64_t vecs, int L, int V)
+RowShape shape_of(int64_t vecs, int L, int V, int T = kLnThreads)
 {
     RowShape r;
     if (L < 32) {
         r.warps = 1;
-        r.threads = kLnThreads;
-        r.groups = kLnThreads / L;
+        r.threads = T;
+        r.groups = T / L;
     } else {
         r.warps = (int)((vecs + 32 * V - 1) / (32 * V));
-        r.groups = kLnThreads / 32 / r.warps;
+        r.groups = T / 32 / r.warps;
         r.threads = 32 * r.warps * r.groups;
     }
     return r;
 }
 
-template <int DT, int L, int V, int RB, int S, int BLOCKS>
-cudaError_t forward_rows(LnArgs a, int64_t vecs, cudaStream_t s)
+template <int DT, int L, int V, int RB, int S, int T, int BLOCKS>
+cudaError_t forward_rows(LnArgs a, int64_t vecs, int align, cudaStream_t s)
 {
-    const RowShape h = shape_of(vecs, L, V);
+    const RowShape h = shape_of(vecs, L, V, T);
     a.warps = h.warps;
     const int64_t at_once = (int64_t)h.groups * RB, need = (a.rows + at_once - 1) / at_once;
-    const int64_t most = (int64_t)kSms * (BLOCKS * kLnThreads / h.threads);   // resident at once
+    const int64_t most = (int64_t)kSms * (BLOCKS * T / h.threads);            // resident at once
     const int64_t blocks = need < most ? need : most;
-    constexpr size_t smem = (size_t)S * RB * V * kLnThreads * 16;
+    constexpr size_t smem = (size_t)S * RB * V * T * 16;
+    if constexpr (DT != kF32)
+        if (align < 16)
+            return launch_slots<k_ln_forward_rows<DT, 32, V, RB, S, T, BLOCKS, true, 4>, smem>(a, blocks, h.threads, s);
     if (a.dim % kVecOf<DT>)
-        return launch_slots<k_ln_forward_rows<DT, 32, V, RB, S, BLOCKS, true>, smem>(a, blocks, h.threads, s);
-    return launch_slots<k_ln_forward_rows<DT, L, V, RB, S, BLOCKS, false>, smem>(a, blocks, h.threads, s);
+        return launch_slots<k_ln_forward_rows<DT, 32, V, RB, S, T, BLOCKS, true, 16>, smem>(a, blocks, h.threads, s);
+    return launch_slots<k_ln_forward_rows<DT, L, V, RB, S, T, BLOCKS, false, 16>, smem>(a, blocks, h.threads, s);
 }
 
 template <int DT, int L, int K, int RB>
@@ -906,19 +930,27 @@ cudaError_t forward_any(LnArgs a, int64_t eights, cudaStream_t s)
     return launch_rows(k_ln_forward_any<DT, L, K, RB>, a, need < most ? need : most, h.threads, 0, s);
 }
 
+// align: 16, 4 or 0, the boundary that every row starts on (of 0: its type's).
+// 16-bit rows on 4-byte boundaries go the aligned rows' way in 4-byte copies of
+// two values (32768 x 1602: 70 us against 84 value by value, backward 115 against
+// 175); forward not the short ones (65536 x 134: 23 against 21, backward 35
+// against 42).  In 32 bits such a copy is one value and loses (16384 x 1023:
+// 43 against 30).
 template <int DT>
-cudaError_t forward(const LnArgs& a, bool vec, cudaStream_t s)
+cudaError_t forward(const LnArgs& a, int align, cudaStream_t s)
 {
-    constexpr int VE = kVecOf<DT>;
+    constexpr int VE = kVecOf<DT>, T = kLnThreads, R = kLnFwdRows, S = kLnFwdAhead, B = kLnFwdBlocks;
     const int64_t vecs = (a.dim + VE - 1) / VE;
-    const bool whole = a.dim % VE == 0;
-    if (vec && whole && vecs <= 8) return forward_rows<DT, 8, 1, 4, 3, 3>(a, vecs, s);
-    if (vec && whole && vecs <= 16) return forward_rows<DT, 16, 1, 4, 3, 3>(a, vecs, s);
-    if (vec && vecs <= 256) return forward_rows<DT, 32, 1, kLnFwdRows, kLnFwdAhead, kLnFwdBlocks>(a, vecs, s);
-    if (vec && vecs <= 512) return forward_rows<DT, 32, 2, kLnFwdRows / 2, kLnFwdAhead, kLnFwdBlocks>(a, vecs, s);
-    if (vec && vecs <= 1024) return forward_rows<DT, 32, 4, kLnFwdRows / 4, kLnFwdAhead, kLnFwdBlocks>(a, vecs, s);
-    if (vec && vecs <= 2048) return forward_rows<DT, 32, 8, 1, 2, 2>(a, vecs, s);
-    if (!vec) {
+    const bool whole = a.dim % VE == 0 && align == 16;
+    if (whole && vecs <= 8) return forward_rows<DT, 8, 1, 4, 3, T, 3>(a, vecs, align, s);
+    if (whole && vecs <= 16) return forward_rows<DT, 16, 1, 4, 3, T, 3>(a, vecs, align, s);
+    if (align == 16 || (DT != kF32 && align == 4 && vecs > 64)) {
+        if (vecs <= 256) return forward_rows<DT, 32, 1, R, S, T, B>(a, vecs, align, s);
+        if (vecs <= 512) return forward_rows<DT, 32, 2, R / 2, S, T, B>(a, vecs, align, s);
+        if (vecs <= 1024) return forward_rows<DT, 32, 4, R / 4, S, T, B>(a, vecs, align, s);
+        if (vecs <= 2048) return forward_rows<DT, 32, 8, 1, 2, T, 2>(a, vecs, align, s);
+        if (vecs <= 4096) return forward_rows<DT, 32, 8, 1, 2, 2 * T, 1>(a, vecs, align, s);
+    } else {
         const int64_t eights = (a.dim + 7) / 8;
         if (eights <= 8) return forward_any<DT, 8, 8, 4>(a, eights, s);
         if (eights <= 16) return forward_any<DT, 16, 8, 4>(a, eights, s);
@@ -929,30 +961,46 @@ cudaError_t forward(const LnArgs& a, bool vec, cudaStream_t s)
     return launch_rows(k_ln_forward<DT>, a, a.rows < kSms * 8 ? a.rows : kSms * 8, kLnThreads, 0, s);
 }
 
-// Lanes of a backward group, vectors of a lane.
-int backward_lanes(int64_t vecs, bool whole) { return whole && vecs <= 8 ? 8 : whole && vecs <= 16 ? 16 : 32; }
-int backward_vectors(int64_t vecs) { return vecs <= 256 ? 1 : vecs <= 512 ? 2 : 4; }
+// How the backward pass deals out a row: lanes of a group, vectors of a lane,
+// threads and resident blocks, rows at a time.  The plan's blocks go by it
+// (as for rows on 16-byte boundaries) whatever the pointers turn out to be.
+struct BackwardShape {
+    int L, V, T, blocks, rows;
+};
 
-template <int DT, int L, int V, int RB>
-cudaError_t backward_rows(LnArgs a, int64_t vecs, int blocks, cudaStream_t s)
+BackwardShape backward_shape(int64_t vecs, bool whole)
 {
-    const RowShape h = shape_of(vecs, L, V);
+    const int L = whole && vecs <= 8 ? 8 : whole && vecs <= 16 ? 16 : 32;
+    if (vecs <= 256) return {L, 1, kLnThreads, kLnBwdBlocks, kLnBwdRows};
+    if (vecs <= 512) return {L, 2, kLnThreads, kLnBwdBlocks, kLnBwdRows / 2};
+    if (vecs <= 1024) return {L, 4, kLnThreads, kLnBwdBlocks, kLnBwdRows / 4};
+    // up to 2048 vectors (8192 x 10464 of 16 bits: 158 us; x read twice, dy twice, in two kernels: 352)
+    return {L, 4, 2 * kLnThreads, 1, kLnBwdRows / 4};
+}
+
+template <int DT, int L, int V, int RB, int T, int BLOCKS>
+cudaError_t backward_rows(LnArgs a, int64_t vecs, int align, int blocks, cudaStream_t s)
+{
+    const RowShape h = shape_of(vecs, L, V, T);
     a.warps = h.warps;
     constexpr int S = kLnBwdAhead;
-    constexpr size_t smem = (size_t)S * RB * V * 2 * kLnThreads * 16;
+    constexpr size_t smem = (size_t)S * RB * V * 2 * T * 16;
+    if constexpr (DT != kF32)
+        if (align < 16)
+            return launch_slots<k_ln_backward_rows<DT, 32, V, RB, S, T, BLOCKS, true, 4>, smem>(a, blocks, h.threads, s);
     if (a.dim % kVecOf<DT>)
-        return launch_slots<k_ln_backward_rows<DT, 32, V, RB, S, kLnBwdBlocks, true>, smem>(a, blocks, h.threads, s);
-    return launch_slots<k_ln_backward_rows<DT, L, V, RB, S, kLnBwdBlocks, false>, smem>(a, blocks, h.threads, s);
+        return launch_slots<k_ln_backward_rows<DT, 32, V, RB, S, T, BLOCKS, true, 16>, smem>(a, blocks, h.threads, s);
+    return launch_slots<k_ln_backward_rows<DT, L, V, RB, S, T, BLOCKS, false, 16>, smem>(a, blocks, h.threads, s);
 }
 
 // Blocks of the backward pass (the plan's): as many as are resident at once on
 // 152 SMs, and no more than have rows.
 int64_t backward_blocks(int64_t rows, int64_t vecs, bool whole)
 {
-    const int L = backward_lanes(vecs, whole), V = backward_vectors(vecs);
-    const RowShape h = shape_of(vecs <= 1024 ? vecs : 1024, L, V);
-    const int64_t at_once = (int64_t)h.groups * (kLnBwdRows / V), need = (rows + at_once - 1) / at_once;
-    const int64_t most = (int64_t)kSms * (kLnBwdBlocks * kLnThreads / h.threads);
+    const BackwardShape b = backward_shape(vecs, whole);
+    const RowShape h = shape_of(vecs <= 2048 ? vecs : 2048, b.L, b.V, b.T);
+    const int64_t at_once = (int64_t)h.groups * b.rows, need = (rows + at_once - 1) / at_once;
+    const int64_t most = (int64_t)kSms * (b.blocks * b.T / h.threads);
     return need < most ? need : most;
 }
 
@@ -965,22 +1013,22 @@ cudaError_t backward_any(LnArgs a, int64_t eights, int blocks, cudaStream_t s)
 }
 
 template <int DT>
-cudaError_t backward(LnArgs a, bool vec, int blocks, void* dw, void* db, cudaStream_t s)
+cudaError_t backward(LnArgs a, int align, int blocks, void* dw, void* db, cudaStream_t s)
 {
-    constexpr int VE = kVecOf<DT>;
-    const int64_t vecs = (a.dim + VE - 1) / VE;
+    constexpr int VE = kVecOf<DT>, T = kLnThreads, R = kLnBwdRows, B = kLnBwdBlocks;
+    const int64_t vecs = (a.dim + VE - 1) / VE, eights = (a.dim + 7) / 8;
     const bool sums = dw || db;
     if (!sums) a.part = nullptr;
     cudaError_t e = cudaSuccess;
-    if (blocks && vec && vecs <= 1024) {
-        const int L = backward_lanes(vecs, a.dim % VE == 0);
-        if (L == 8) e = backward_rows<DT, 8, 1, kLnBwdRows>(a, vecs, blocks, s);
-        else if (L == 16) e = backward_rows<DT, 16, 1, kLnBwdRows>(a, vecs, blocks, s);
-        else if (vecs <= 256) e = backward_rows<DT, 32, 1, kLnBwdRows>(a, vecs, blocks, s);
-        else if (vecs <= 512) e = backward_rows<DT, 32, 2, kLnBwdRows / 2>(a, vecs, blocks, s);
-        else e = backward_rows<DT, 32, 4, kLnBwdRows / 4>(a, vecs, blocks, s);
-    } else if (blocks && !vec && a.dim <= 4096) {
-        const int64_t eights = (a.dim + 7) / 8;
+    if (blocks && vecs <= 2048 && (align == 16 || (DT != kF32 && align == 4 && vecs > 16))) {
+        const int L = align == 16 ? backward_shape(vecs, a.dim % VE == 0).L : 32;
+        if (L == 8) e = backward_rows<DT, 8, 1, R, T, B>(a, vecs, align, blocks, s);
+        else if (L == 16) e = backward_rows<DT, 16, 1, R, T, B>(a, vecs, align, blocks, s);
+        else if (vecs <= 256) e = backward_rows<DT, 32, 1, R, T, B>(a, vecs, align, blocks, s);
+        else if (vecs <= 512) e = backward_rows<DT, 32, 2, R / 2, T, B>(a, vecs, align, blocks, s);
+        else if (vecs <= 1024) e = backward_rows<DT, 32, 4, R / 4, T, B>(a, vecs, align, blocks, s);
+        else e = backward_rows<DT, 32, 4, R / 4, 2 * T, 1>(a, vecs, align, blocks, s);
+    } else if (blocks && align < 16 && a.dim <= 4096) {
         if (eights <= 8) e = backward_any<DT, 8, 8, 2>(a, eights, blocks, s);
         else if (eights <= 16) e = backward_any<DT, 16, 8, 2>(a, eights, blocks, s);
         else if (eights <= 256) e = backward_any<DT, 32, 8, 2>(a, eights, blocks, s);
@@ -999,12 +1047,14 @@ cudaError_t backward(LnArgs a, bool vec, int blocks, void* dw, void* db, cudaStr
     return e;
 }
 
-// Rows of x and y (or dy, dx) and the vectors start on 16-byte boundaries.
-bool on_vectors(const zero_ln_plan_t& p, const void* a, const void* b, const void* c, const void* d, const void* e)
+// The boundary that every row of x and y (or dy, dx: a, b, c) starts on: 16, 4
+// or 0 bytes (their type's).  weight and bias off 16-byte boundaries count as 0.
+int rows_align(const zero_ln_plan_t& p, const void* a, const void* b, const void* c, const void* weight, const void* bias)
 {
-    const int64_t ve = p.dtype == ZERO_FP32 ? 4 : 8;
-    const uintptr_t any = (uintptr_t)a | (uintptr_t)b | (uintptr_t)c | (uintptr_t)d | (uintptr_t)e;
-    return any % 16 == 0 && p.x_stride % ve == 0 && p.y_stride % ve == 0;
+    const uint64_t e = p.dtype == ZERO_FP32 ? 4 : 2;
+    const uint64_t any = (uintptr_t)a | (uintptr_t)b | (uintptr_t)c | (uint64_t)p.x_stride * e | (uint64_t)p.y_stride * e;
+    if (((uintptr_t)weight | (uintptr_t)bias) % 16) return 0;
+    return any % 16 == 0 ? 16 : any % 4 == 0 ? 4 : 0;
 }
 
 }  // namespace
@@ -1061,10 +1111,10 @@ zero_status_t zero_ln_forward(const zero_ln_plan_t* plan, const void* x, const v
     a.rows = plan->rows; a.dim = plan->dim; a.x_stride = plan->x_stride; a.y_stride = plan->y_stride;
     a.eps = eps;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool vec = on_vectors(*plan, x, y, weight, bias, nullptr);
-    const cudaError_t err = plan->dtype == ZERO_FP32   ? forward<kF32>(a, vec, s)
-                            : plan->dtype == ZERO_BF16 ? forward<kBF16>(a, vec, s)
-                                                       : forward<kF16>(a, vec, s);
+    const int align = rows_align(*plan, x, y, nullptr, weight, bias);
+    const cudaError_t err = plan->dtype == ZERO_FP32   ? forward<kF32>(a, align, s)
+                            : plan->dtype == ZERO_BF16 ? forward<kBF16>(a, align, s)
+                                                       : forward<kF16>(a, align, s);
     return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_ln_forward");
 }
 
@@ -1089,10 +1139,10 @@ zero_status_t zero_ln_backward(const zero_ln_plan_t* plan, const void* dy, const
     a.rows = plan->rows; a.dim = plan->dim; a.x_stride = plan->x_stride; a.y_stride = plan->y_stride;
     a.part = static_cast<float*>(workspace) + 4;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool vec = on_vectors(*plan, x, dy, weight, dx, nullptr);
-    const cudaError_t err = plan->dtype == ZERO_FP32   ? backward<kF32>(a, vec, plan->blocks, dweight, dbias, s)
-                            : plan->dtype == ZERO_BF16 ? backward<kBF16>(a, vec, plan->blocks, dweight, dbias, s)
-                                                       : backward<kF16>(a, vec, plan->blocks, dweight, dbias, s);
+    const int align = rows_align(*plan, x, dy, dx, weight, nullptr);
+    const cudaError_t err = plan->dtype == ZERO_FP32   ? backward<kF32>(a, align, plan->blocks, dweight, dbias, s)
+                            : plan->dtype == ZERO_BF16 ? backward<kBF16>(a, align, plan->blocks, dweight, dbias, s)
+                                                       : backward<kF16>(a, align, plan->blocks, dweight, dbias, s);
     return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_ln_backward");
 }
 
