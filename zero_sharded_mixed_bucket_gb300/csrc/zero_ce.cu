@@ -461,7 +461,8 @@ __device__ __forceinline__ float2 finish_token(const JoinArgs& a, int64_t i, flo
 
 // Per token: the strips' maxima and sums joined, in a fixed order (32 parts of
 // the strips, then a tree over the parts); the loss.  The last block to finish
-// adds the blocks' losses and counts, in block order.
+// adds the blocks' losses and counts, in block order.  8 us for 1023 tokens and
+// 393 strips, all of it latency.
 __global__ void __launch_bounds__(1024) k_ce_join(const __grid_constant__ JoinArgs a)
 {
     wait_prev_grid();
