@@ -115,6 +115,7 @@ SHAPES = [  # tokens, vocab, hidden, pad, piece
     (5, 300, 33, 8, 256), (64, 256, 64, 0, 0), (128, 256, 128, 0, 0), (129, 513, 136, 8, 256), (127, 255, 200, 0, 0),
     (256, 2048, 256, 0, 0), (257, 2049, 264, 0, 768), (300, 4099, 100, 0, 1024), (1000, 700, 1000, 0, 0),
     (20, 50257, 64, 0, 0), (1025, 1031, 520, 0, 0), (600, 3001, 1600, 0, 1280),
+    (3000, 100, 264, 0, 0), (2500, 700, 33, 8, 256), (5000, 2, 64, 0, 0),   # dw's product in parts
 ]
 
 

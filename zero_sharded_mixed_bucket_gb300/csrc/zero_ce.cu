@@ -768,11 +768,11 @@ __global__ void __launch_bounds__(1024) k_ce_factors(CeHead* head, const int64_t
     }
 }
 
-// dx = alpha times the sum of the splits, rounded: 4 columns a thread, a row
-// a blockIdx.y stride.
+// dx (or dw, where its product is split): alpha times the sum of the splits,
+// rounded; 4 columns a thread, a row a blockIdx.y stride.
 template <int DT>
-__global__ void __launch_bounds__(256) k_ce_dx(const CeHead* head, const float* acc, int splits, int64_t split_stride,
-                                               int64_t m, int64_t n, int64_t acc_cols, uint16_t* dx, int64_t stride)
+__global__ void __launch_bounds__(256) k_ce_sum(const CeHead* head, const float* acc, int splits, int64_t split_stride,
+                                               int64_t m, int64_t n, int64_t acc_cols, uint16_t* out, int64_t stride)
 {
     wait_prev_grid();
     const float alpha = head->err ? NAN : head->alpha;
@@ -786,7 +786,7 @@ __global__ void __launch_bounds__(256) k_ce_dx(const CeHead* head, const float* 
             s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
         }
         const uint2 h = make_uint2(from_f32x2<DT>(s.x * alpha, s.y * alpha), from_f32x2<DT>(s.z * alpha, s.w * alpha));
-        uint16_t* dst = dx + i * stride + c;
+        uint16_t* dst = out + i * stride + c;
         if (c + 4 <= n) {
             *reinterpret_cast<uint2*>(dst) = h;
         } else {
@@ -828,9 +828,35 @@ int64_t few_blocks(const zero_ce_plan_t& p)
     return most < kFewBlocks ? most : kFewBlocks;
 }
 
+// Parts of K, each at least 8 K-blocks, that a product of `tiles` tiles is summed
+// in until its tiles fill the 76 pairs of SMs.
+int64_t parts_of(int64_t tiles, int64_t blocks)
+{
+    int64_t best = 1;
+    double cost = 1e30;
+    for (int64_t s = 1; s <= 32 && s * 8 <= blocks; s++) {
+        const double c = (double)ceil_div(tiles * s, 76) / (double)s * (1.0 + 0.01 * (double)s);
+        if (c < cost * 0.97) {
+            cost = c;
+            best = s;
+        }
+    }
+    return best;
+}
+
+// dw's, whose K are the tokens: in parts where half of the pairs would idle, so
+// with a small vocabulary (16384 tokens, hidden 768, vocabulary 256: the backward
+// pass takes 70 us, 138 in one part; 4096 tokens, hidden 512, vocabulary 1000: 44
+// and 58); else its tiles are rounded where they are.
+int64_t dw_parts(const zero_ce_plan_t& p)
+{
+    const int64_t tiles = ceil_div(p.piece, kBM) * ceil_div(p.hidden, kBN);
+    return tiles <= 38 ? parts_of(tiles, ceil_div(p.tokens, kBK)) : 1;
+}
+
 // Byte offsets in the workspace.
 struct CeLayout {
-    int64_t coef, target_logit, block_total, part, g, acc, end;
+    int64_t coef, target_logit, block_total, part, g, acc, acc_w, end;
     int64_t acc_rows, acc_cols;                       // of one split's binary32 sums
 };
 
@@ -846,7 +872,8 @@ CeLayout layout_of(const zero_ce_plan_t& p)
     const int64_t fwd = l.part + (few_tokens(p) ? few_blocks(p) : ceil_div(p.vocab, kBN) * 2) * p.tokens * 8;
     l.acc_rows = ceil_div(p.tokens, kBM) * kBM;
     l.acc_cols = (p.hidden + 3) / 4 * 4;
-    const int64_t bwd = l.acc + p.splits * l.acc_rows * l.acc_cols * 4;
+    l.acc_w = l.acc + up256(p.splits * l.acc_rows * l.acc_cols * 4);
+    const int64_t parts = dw_parts(p), bwd = l.acc_w + (parts > 1 ? parts * p.piece * l.acc_cols * 4 : 0);
     l.end = up256(fwd > bwd ? fwd : bwd);
     return l;
 }
@@ -963,6 +990,14 @@ cudaError_t launch_few(const zero_ce_plan_t& p, const void* x, const void* w, un
     }
 }
 
+cudaError_t launch_sum(int dtype, const CeHead* head, const float* acc, int splits, int64_t apart, int64_t rows, int64_t cols,
+                       int64_t acc_cols, uint16_t* out, int64_t stride, cudaStream_t s)
+{
+    const dim3 grid((unsigned)ceil_div(acc_cols, 1024), (unsigned)(rows < 4096 ? rows : 4096));
+    return launch_after(dtype == ZERO_BF16 ? k_ce_sum<kBF16> : k_ce_sum<kF16>, grid, 256, 0, s, head, acc, splits, apart, rows,
+                        cols, acc_cols, out, stride);
+}
+
 template <int EPI, bool A_MN, bool B_MN>
 cudaError_t gemm(int dtype, const GemmArgs& g, cudaStream_t s)
 {
@@ -1013,19 +1048,8 @@ zero_status_t zero_ce_plan(int64_t tokens, int64_t vocab, int64_t hidden, int32_
         const int64_t fit = most < 256 ? 256 : (most < all ? most : all);
         out->piece = up256(ceil_div(vocab, ceil_div(all, fit)));
     }
-    // dx has few tiles when there are few tokens: its K (the piece) is then
-    // summed in parts, each at least 8 K-blocks, until the tiles fill the GPU
-    const int64_t tiles = ceil_div(tokens, kBM) * ceil_div(hidden, kBN), blocks = ceil_div(out->piece, kBK);
-    int64_t best = 1;
-    double cost = 1e30;
-    for (int64_t s = 1; s <= 32 && s * 8 <= blocks; s++) {
-        const double c = (double)ceil_div(tiles * s, 76) / (double)s * (1.0 + 0.01 * (double)s);
-        if (c < cost * 0.97) {
-            cost = c;
-            best = s;
-        }
-    }
-    out->splits = (int32_t)best;
+    // dx has few tiles when there are few tokens; its K is the piece
+    out->splits = (int32_t)parts_of(ceil_div(tokens, kBM) * ceil_div(hidden, kBN), ceil_div(out->piece, kBK));
     out->workspace_bytes = layout_of(*out).end;
     out->flops_forward = 2 * tokens * vocab * hidden;
     out->flops_backward = 3 * out->flops_forward;
@@ -1163,33 +1187,36 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
         }
         if (ok && dw && e == cudaSuccess) {          // dw = G^T x
             ok = make_map(&g.a, type, G, p.tokens, p.piece, p.piece, 64) &&
-                 make_map(&g.b, type, x, p.tokens, p.hidden, p.x_stride, 64) &&
-                 make_map(&g.c, type, static_cast<uint16_t*>(dw) + v0 * p.w_stride, nv, p.hidden, p.w_stride, 32);
+                 make_map(&g.b, type, x, p.tokens, p.hidden, p.x_stride, 64);
+            uint16_t* out = static_cast<uint16_t*>(dw) + v0 * p.w_stride;
             g.b_y0 = 0;
             g.a_rows = kBM / 2;
             g.m = nv;
             g.m_tiles = (int)ceil_div(nv, kBM);
             g.k_blocks = (int)ceil_div(p.tokens, kBK);
-            g.splits = 1;
-            if (p.hidden % 8) {
-                g.out = static_cast<uint16_t*>(dw) + v0 * p.w_stride;
-                g.out_stride = p.w_stride;
+            g.splits = (int)dw_parts(p);
+            g.accumulate = 0;
+            if (g.splits > 1) {
+                float* sums = reinterpret_cast<float*>(ws + l.acc_w);
+                const int64_t rows = (int64_t)g.m_tiles * kBM;
+                ok = ok && make_map(&g.c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, sums, g.splits * rows, l.acc_cols, l.acc_cols, 32);
+                if (ok) e = gemm<kEpiAcc, true, true>(p.dtype, g, s);
+                if (ok && e == cudaSuccess)
+                    e = launch_sum(p.dtype, head, sums, g.splits, rows * l.acc_cols, nv, p.hidden, l.acc_cols, out, p.w_stride, s);
+            } else {
+                ok = ok && make_map(&g.c, type, out, nv, p.hidden, p.w_stride, 32);
+                if (p.hidden % 8) {
+                    g.out = out;
+                    g.out_stride = p.w_stride;
+                }
+                if (ok) e = gemm<kEpiOut, true, true>(p.dtype, g, s);
             }
-            if (ok) e = gemm<kEpiOut, true, true>(p.dtype, g, s);
         }
         if (!ok) return set_error(ZERO_ECUDA, "zero_ce_backward: cuTensorMapEncodeTiled refused a buffer");
     }
-    if (dx && e == cudaSuccess) {
-        const dim3 grid((unsigned)ceil_div(l.acc_cols, 1024), (unsigned)(p.tokens < 4096 ? p.tokens : 4096));
-        uint16_t* out = static_cast<uint16_t*>(dx);
-        const int64_t apart = l.acc_rows * l.acc_cols;
-        if (p.dtype == ZERO_BF16)
-            e = launch_after(k_ce_dx<kBF16>, grid, 256, 0, s, head, acc, p.splits, apart, p.tokens, p.hidden, l.acc_cols, out,
-                             p.x_stride);
-        else
-            e = launch_after(k_ce_dx<kF16>, grid, 256, 0, s, head, acc, p.splits, apart, p.tokens, p.hidden, l.acc_cols, out,
-                             p.x_stride);
-    }
+    if (dx && e == cudaSuccess)
+        e = launch_sum(p.dtype, head, acc, p.splits, l.acc_rows * l.acc_cols, p.tokens, p.hidden, l.acc_cols,
+                       static_cast<uint16_t*>(dx), p.x_stride, s);
     return e == cudaSuccess ? ZERO_OK : cuda_failed(e, "zero_ce_backward");
 }
 
