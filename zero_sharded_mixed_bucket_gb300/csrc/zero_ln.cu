@@ -81,7 +81,7 @@ __device__ __forceinline__ float block_sum(float v, float* sh)
 // bytes in flight do not depend on registers or on how far the other lanes
 // are, and nothing waits but a lane for its own copies.  The rows stay there
 // until they are done, read again for each use.
-// What bounds these kernels is issuing instructions (about 19 a value forward,
+// What bounds these kernels is issuing instructions (about 17 a value forward,
 // 30 backward), so a batch is as large as registers allow: its sums, addresses
 // and loop are shared by all its values.  8192 x 4096 bfloat16 forward: 26.8 us,
 // 5.0 TB/s (a device copy of the same bytes 23.5; rows in registers, a block to
