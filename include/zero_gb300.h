@@ -574,7 +574,9 @@ zero_status_t zero_ln_backward(const zero_ln_plan_t* plan, const void* dy, const
  * 256 vocabulary entries.  The backward pass computes z again, a piece of the
  * vocabulary at a time, and holds G of one piece in 16 bits.
  * x, w, dx and dw have the plan's dtype (ZERO_FP16 or ZERO_BF16; ZERO_FP32 is
- * ZERO_EUNSUPPORTED); products are accumulated in binary32, softmax
+ * ZERO_EUNSUPPORTED); products are accumulated in binary32 (1024 values at a
+ * time on the tensor cores, which round toward zero, those sums to nearest; the
+ * loss and G use the same z), softmax
  * statistics and loss are binary32, dx and dw are rounded once, and G is
  * rounded once, to the dtype (the operand type of the products that use it),
  * scaled so that its largest row factor is 1 (binary16: 2^14).

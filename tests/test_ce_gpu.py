@@ -365,3 +365,58 @@ def test_tiny_upstream_gradients():
     for d in (1e-30, 1e-39, 0.0):
         j.backward(1.0, dloss=torch.full((40,), d, device="cuda"))
         assert j.dx.isfinite().all() and j.dw.isfinite().all()
+
+
+@pytest.mark.parametrize("n", [2, 64])
+def test_gradients_of_confident_tokens(n):
+    """Hidden states along their targets' weights: z_t = 25, every product of
+    the same sign, the rest near 0, so p_t - 1 is -5e-9 and the whole gradient
+    about that.  What may be left is the logit's change from the loss to its
+    gradient: none where both sum alike (n > 3), but lse's rounding, 2^-20 at 25,
+    and exp's; where the loss of up to 3 tokens is summed apart, 32 steps a part,
+    each cut by half of 2^-23 on average, of a sum that is half the part's."""
+    v, d = 300, 4096
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = (torch.randn(v, d, device="cuda", generator=g) / 64).bfloat16()
+    t = torch.randint(0, v, (n,), device="cuda", generator=g)
+    x = (25 * w[t].float()).bfloat16()
+    p = zg.zero_ce_plan(n, v, d, zg.ZERO_BF16)
+    ws = torch.empty(p.workspace_bytes, dtype=torch.uint8, device="cuda")
+    loss, lse, dx, dw = torch.empty(n, device="cuda"), torch.empty(n, device="cuda"), torch.empty_like(x), torch.empty_like(w)
+    zg.zero_ce_forward(p, x, w, t, loss, lse, None, ws)
+    zg.zero_ce_backward(p, x, w, t, lse, torch.ones(n, device="cuda"), 1.0, dx, dw, ws)
+    z = x.double() @ w.double().t()
+    assert 20 < z.gather(1, t[:, None]).min() and z.gather(1, t[:, None]).max() < 32
+    G = torch.softmax(z, 1)
+    G[torch.arange(n), t] -= 1
+    assert G.abs().max() < 1e-6
+    off = 2.0 ** -19 if n > 3 else 16 * 2.0 ** -23 * 32 / 2
+    rest = 2.0 ** -10 * G.abs().sum(1)               # the others' relative errors, far above theirs
+    assert ((dx.double() - G @ w.double()).abs() <= (off + rest)[:, None] * w.double().abs().max()).all()
+    assert ((dw.double() - G.t() @ x.double()).abs() <= n * (off + rest.max()) * x.double().abs().max()).all()
+
+
+def test_long_sums_are_not_cut_short():
+    """dw over 131072 tokens, all products of one sign.  The tensor cores cut
+    their running sums toward zero, by up to 2^-23 at each of 64 steps of 16
+    in 1024 values; longer sums are added to nearest.  So the mean error of the
+    gradients, over 2.6 million of them whose own roundings average out
+    (2^-11 / 1600), stays below 64 * 2^-23 and exp's 2^-21."""
+    n, v, d = 131072, 2048, 1280
+    p = zg.zero_ce_plan(n, v, d, zg.ZERO_FP16)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = (0.5 + torch.rand(n, d, device="cuda", generator=g)).half()
+    w = (torch.randn(v, d, device="cuda", generator=g) * 0.02).half()
+    t = torch.zeros(n, dtype=torch.int64, device="cuda")     # entry 0 alone has negative products
+    ws = torch.empty(p.workspace_bytes, dtype=torch.uint8, device="cuda")
+    loss, lse, dw = torch.empty(n, device="cuda"), torch.empty(n, device="cuda"), torch.empty_like(w)
+    zg.zero_ce_forward(p, x, w, t, loss, lse, None, ws)
+    zg.zero_ce_backward(p, x, w, t, lse, None, 2048.0, None, dw, ws)
+    want = torch.zeros(v, d, dtype=torch.float64, device="cuda")
+    for a in range(0, n, 16384):
+        q = torch.softmax(x[a:a + 16384].double() @ w.double().t(), 1)
+        want += q.t() @ x[a:a + 16384].double()
+    want = want[1:] * (2048.0 / n)
+    assert want.min() > 2.0 ** -13                           # normal numbers
+    off = ((dw[1:].double() - want) / want).mean()
+    assert off.abs() <= 64 * 2.0 ** -23 + 2.0 ** -21 + 6 * 2.0 ** -11 / 1600

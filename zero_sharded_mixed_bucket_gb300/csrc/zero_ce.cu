@@ -21,7 +21,7 @@ constexpr int kCeThreads = 64 + 32 * kEpiWarps;       // copying warp, issuing w
 constexpr int kOutBytes = 4096;                       // an epilogue warp's box of results: 32 rows of 128 bytes
 constexpr int kCeSmem = kStages * (kABytes + kBBytes) + kEpiWarps * kOutBytes + 1024;
 constexpr int kStrip = kBN / 2;                       // vocabulary entries per (maximum, sum)
-constexpr int kChunk = 16;                            // loss: K-blocks the tensor cores add up by themselves
+constexpr int kChunk = 16, kChunkFew = 8;             // K-blocks the tensor cores add up by themselves
 constexpr int kGroup = 8;                             // row tiles that share the column tiles in L2
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -42,6 +42,7 @@ struct GemmArgs {
     int64_t m, n;                // rows, columns of the product that exist
     int m_tiles, n_tiles;
     int k_blocks;                // K-blocks in all
+    int chunk;                   // of them added up in tensor memory at one go
     int splits;                  // parts of the K-blocks, one result each (kEpiAcc), m_tiles * kBM rows apart
     int b_y0;                    // first vocabulary entry of the piece
     int accumulate;              // kEpiAcc: added to what is there
@@ -105,10 +106,16 @@ __device__ __forceinline__ Tile tile_at(const GemmArgs& g, uint32_t t)
 // in place of 2-byte stores: 8.4 ms.  With few tokens w's bytes bound it.
 //
 // A chunk is the K-range that is accumulated in tensor memory at one go: the
-// tensor cores cut their binary32 sums toward zero, 256 times along K = 4096,
-// which is off by 1e-6 of the loss; the loss adds chunks of kChunk K-blocks in
-// registers, rounding to nearest (2.6e-7).  The other products are rounded to
-// 16 bits.
+// tensor cores cut their binary32 sums toward zero at every step, 256 steps
+// along K = 4096, which is off by 1e-6 of the loss; so chunks of kChunk K-blocks
+// are added in registers, rounding to nearest (2.6e-7).  In the gradients one
+// chain over all of K took 8e-4 off a dw of 131072 tokens whose products have one
+// sign, half a unit in binary16's last place, and left p - 1 of a confident
+// token at hidden 4096 off by 1.5e-4: there z has to be the sum that lse was made
+// from.  Where lse comes from k_ce_few, whose sums are another's, G's chunks
+// are kChunkFew K-blocks, so that what is cut stays at 1e-5 of such a token.
+// The chunks cost the backward pass 1 to 1.5 % (8192 tokens: 6.19 ms at hidden
+// 4096, 6.10 in one chain; 1.23 and 1.21 at 768).
 template <int EPI, int DT, bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_gemm(const __grid_constant__ GemmArgs g)
 {
@@ -141,7 +148,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
     const uint32_t tmem = s_tmem;
     const uint32_t tiles = (uint32_t)g.m_tiles * (uint32_t)g.n_tiles * (uint32_t)g.splits;   // below 2^31: see the plan
     const uint32_t first = blockIdx.x >> 1, stride = gridDim.x >> 1;
-    constexpr int kChunkBlocks = EPI == kEpiLse ? kChunk : 1 << 30;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -196,14 +202,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
             bool ok = true;
             for (uint32_t t = first; t < tiles && ok; t += stride) {
                 const Tile w = tile_at(g, t);
-                for (int c0 = w.kb0; c0 < w.kb1 && ok; c0 += kChunkBlocks, unit++) {
+                for (int c0 = w.kb0; c0 < w.kb1 && ok; c0 += g.chunk, unit++) {
                     const int buf = unit & 1;
                     if (!tc::mbar_wait(acc_empty + 8 * buf, ((unit >> 1) & 1) ^ 1)) {
                         ok = false;
                         break;
                     }
                     tc::fence_after_sync();
-                    const int c1 = min(w.kb1, (EPI == kEpiLse ? c0 + kChunkBlocks : w.kb1));
+                    const int c1 = min(w.kb1, c0 + g.chunk);
                     for (int kb = c0; kb < c1; kb++, it++) {
                         const int s = it % kStages;
                         if (!tc::mbar_wait(full + 8 * s, (it / kStages) & 1)) {
@@ -220,10 +226,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
                         tc::mma_commit(empty + 8 * s);
                     }
                     if (ok) tc::mma_commit(acc_full + 8 * buf);
-                    if (EPI != kEpiLse) {
-                        unit++;
-                        break;
-                    }
                 }
             }
             if (!ok) atomicOr(&g.head->err, 1u);
@@ -240,33 +242,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
             const int64_t row = (int64_t)w.mt * kBM + rank * (kBM / 2) + band * 32 + lane;
             const bool live = row < g.m;
             const int64_t col0 = (int64_t)w.nt * kBN + half * kStrip;
-            if constexpr (EPI == kEpiLse) {
-                float z[kStrip];
-                for (int c0 = w.kb0; c0 < w.kb1; c0 += kChunkBlocks, unit++) {
-                    const int buf = unit & 1;
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(acc_full + 8 * buf, (unit >> 1) & 1));
-                    if (!ok) break;
-                    tc::fence_after_sync();
-#pragma unroll
-                    for (int q = 0; q < kStrip / 32; q++) {
-                        uint32_t r[32];
-                        tc::tmem_ld32(src + buf * kBN + 32 * q, r);
-                        tc::tmem_ld_wait();
-                        if (c0 == w.kb0) {
-#pragma unroll
-                            for (int k = 0; k < 32; k++)
-                                z[32 * q + k] = __uint_as_float(r[k]);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 32; k++)
-                                z[32 * q + k] += __uint_as_float(r[k]);
-                        }
-                    }
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive_leader(acc_empty + 8 * buf);
+            float cf = 0.0f, base = 0.0f;
+            int tgt = -1;                                 // kEpiGrad: the strip's column that is the row's target
+            if constexpr (EPI == kEpiGrad) {
+                if (live) {
+                    cf = g.coef[row];
+                    base = g.lse[row] * kLog2e;
+                    const int64_t at = g.targets[row] - g.b_y0 - col0;
+                    if (cf != 0.0f && at >= 0 && at < kStrip) tgt = (int)at;
                 }
+            }
+            // the warp's columns into registers, chunk after chunk, and tensor memory is
+            // free again; a part of K may be empty
+            float z[kStrip];
+            if (w.kb0 == w.kb1) {
+#pragma unroll
+                for (int k = 0; k < kStrip; k++)
+                    z[k] = 0.0f;
+            }
+            for (int c0 = w.kb0; c0 < w.kb1; c0 += g.chunk, unit++) {
+                const int buf = unit & 1;
+                ok = __all_sync(0xffffffffu, tc::mbar_wait(acc_full + 8 * buf, (unit >> 1) & 1));
                 if (!ok) break;
+                tc::fence_after_sync();
+                if (c0 == w.kb0) {
+#pragma unroll
+                    for (int q = 0; q < kStrip / 32; q++)
+                        tc::tmem_ld32(src + buf * kBN + 32 * q, reinterpret_cast<uint32_t*>(z) + 32 * q);
+                    tc::tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int q = 0; q < kStrip / 16; q++) {       // 16 at a time: registers
+                        uint32_t r[16];
+                        tc::tmem_ld16(src + buf * kBN + 16 * q, r);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 16; k++)
+                            z[16 * q + k] += __uint_as_float(r[k]);
+                    }
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_leader(acc_empty + 8 * buf);
+            }
+            if (!ok) break;
+            if constexpr (EPI == kEpiLse) {
                 // the strip's maximum and its sum
                 const int64_t left = g.n - col0;
                 if (left < kStrip) {
@@ -274,13 +294,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
                     for (int k = 0; k < kStrip; k++)
                         if (k >= left) z[k] = -INFINITY;
                 }
-                const int64_t tgt = (live ? g.targets[row] : -1) - col0;
-                const bool here = tgt >= 0 && tgt < kStrip && tgt < left;
+                const int64_t at = (live ? g.targets[row] : -1) - col0;
+                const bool here = at >= 0 && at < kStrip && at < left;
                 if (__any_sync(0xffffffffu, here)) {
                     float zt = 0.0f;
 #pragma unroll
                     for (int k = 0; k < kStrip; k++)
-                        if (k == tgt) zt = z[k];
+                        if (k == at) zt = z[k];
                     if (here) g.target_logit[row] = zt;
                 }
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -296,49 +316,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
                 if (live)
                     g.part[((int64_t)w.nt * 2 + half) * g.m + row] = make_float2(top, (s4[0] + s4[1]) + (s4[2] + s4[3]));
             } else {
-                const int buf = unit & 1;
-                const bool some = w.kb1 > w.kb0;      // else nothing was accumulated, and nothing is waited for
-                if (some) {
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(acc_full + 8 * buf, (unit >> 1) & 1));
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    unit++;
-                }
-                float cf = 0.0f, base = 0.0f, alpha = 0.0f;
-                int64_t tgt = -1;
-                if constexpr (EPI == kEpiGrad) {
-                    if (live) {
-                        cf = g.coef[row];
-                        base = g.lse[row] * kLog2e;
-                        if (cf != 0.0f) tgt = g.targets[row] - g.b_y0 - col0;
-                    }
-                } else if constexpr (EPI == kEpiOut) {
-                    alpha = g.head->alpha;
-                }
-                // all of the warp's columns into registers, and tensor memory is free again
-                float z[kStrip];
-#pragma unroll
-                for (int q = 0; q < kStrip / 32; q++) {
-                    uint32_t* r = reinterpret_cast<uint32_t*>(z) + 32 * q;
-                    if (some) {
-                        tc::tmem_ld32(src + buf * kBN + 32 * q, r);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 32; k++)
-                            r[k] = 0;
-                    }
-                }
-                if (some) {
-                    tc::tmem_ld_wait();
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive_leader(acc_empty + 8 * buf);
-                }
                 if constexpr (EPI == kEpiGrad) {
 #pragma unroll
                     for (int k = 0; k < kStrip; k++)
                         z[k] = exp2_fast(fmaf(z[k], kLog2e, -base));
-                    if (__any_sync(0xffffffffu, tgt >= 0 && tgt < kStrip)) {
+                    if (__any_sync(0xffffffffu, tgt >= 0)) {
 #pragma unroll
                         for (int k = 0; k < kStrip; k++)
                             if (k == tgt) z[k] -= 1.0f;
@@ -353,12 +335,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
                     for (int k = 0; k < kStrip; k++)
                         z[k] *= cf;
                 } else if constexpr (EPI == kEpiOut) {
+                    const float alpha = g.head->alpha;
 #pragma unroll
                     for (int k = 0; k < kStrip; k++)
                         z[k] *= alpha;
                 }
                 const uint32_t keep = EPI == kEpiGrad && cf == 0.0f ? 0u : 0xffffffffu;   // 0 whatever the logit
-                const int row0 = w.mt * kBM + (int)rank * (kBM / 2) + band * 32;
                 if (EPI == kEpiOut && g.out) {
                     // rows that do not end on a 16-byte unit, which is what a tiled copy writes
                     if (live)
@@ -370,6 +352,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
                 // the warp's box: 32 rows of 128 bytes with the copy's swizzle (16-byte
                 // unit j of row i at j ^ (i & 7): no bank conflicts); one copy out per
                 // box (a second box for a stage less: 2 % slower)
+                const int row0 = w.mt * kBM + (int)rank * (kBM / 2) + band * 32;
                 const int y = row0 + (EPI == kEpiAcc ? w.split * g.m_tiles * kBM : 0);
                 constexpr int kCols = EPI == kEpiAcc ? 32 : 64;       // columns of a box
 #pragma unroll
@@ -1105,6 +1088,7 @@ zero_status_t zero_ce_forward(const zero_ce_plan_t* plan, const void* x, const v
         g.m_tiles = (int)ceil_div(p.tokens, kBM);
         g.n_tiles = (int)ceil_div(p.vocab, kBN);
         g.k_blocks = (int)ceil_div(p.hidden, kBK);
+        g.chunk = kChunk;
         g.splits = 1;
         g.head = reinterpret_cast<CeHead*>(ws);
         g.targets = targets;
@@ -1167,6 +1151,7 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
         g.m_tiles = (int)ceil_div(p.tokens, kBM);
         g.n_tiles = (int)ceil_div(nv, kBN);
         g.k_blocks = (int)ceil_div(p.hidden, kBK);
+        g.chunk = few_tokens(p) ? kChunkFew : kChunk;
         g.splits = 1;
         g.b_y0 = (int)v0;
         g.head = head;
@@ -1176,6 +1161,7 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
         if (ok) e = gemm<kEpiGrad, false, false>(p.dtype, g, s);
         g.n = p.hidden;
         g.n_tiles = (int)ceil_div(p.hidden, kBN);
+        g.chunk = kChunk;
         if (ok && dx && e == cudaSuccess) {          // dx += G w
             ok = make_map(&g.a, type, G, p.tokens, p.piece, p.piece, g.a_rows) &&
                  make_map(&g.b, type, w, p.vocab, p.hidden, p.w_stride, 64) &&
