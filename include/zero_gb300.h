@@ -610,7 +610,8 @@ zero_status_t zero_ce_forward(const zero_ce_plan_t* plan, const void* x, const v
                               float* loss, float* lse, float* total, void* workspace, void* stream);
 /* lse as the forward pass wrote it.  s_i = dloss[i] * grad_scale, or with
  * dloss NULL grad_scale / (number of tokens that have a loss): the gradient
- * of the mean, times grad_scale (the loss scale).  dx, dw NULL: not
+ * of the mean, times grad_scale (the loss scale).  An s_i that is not finite
+ * makes its token's dx NaN, and dw, and no other token's dx.  dx, dw NULL: not
  * computed; they are overwritten otherwise (with zeros where there are no
  * tokens). */
 zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const void* w, const int64_t* targets,

@@ -420,3 +420,32 @@ def test_long_sums_are_not_cut_short():
     assert want.min() > 2.0 ** -13                           # normal numbers
     off = ((dw[1:].double() - want) / want).mean()
     assert off.abs() <= 64 * 2.0 ** -23 + 2.0 ** -21 + 6 * 2.0 ** -11 / 1600
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_one_nonfinite_upstream_gradient(dtype):
+    """An infinity or NaN in dloss, or a dloss that overflows with the scale,
+    is its own token's: the others' dx is what it is without."""
+    j = Job(130, 300, 64, dtype)
+    j.t[:8] = torch.tensor([1, 2, 3, -100, 4, 5, 6, 7], device="cuda")
+    j.forward()
+    j.define()
+    g = torch.Generator(device="cuda").manual_seed(5)
+    clean = 0.5 + torch.rand(130, device="cuda", generator=g)
+    for bad, scale in ((float("inf"), 2.0), (-float("inf"), 2.0), (float("nan"), 2.0), (1e38, 64.0)):
+        dl = clean.clone()
+        dl[2] = 0.0                                  # without the bad one
+        j.backward(scale, dloss=dl)
+        j.check_backward(dl.double() * scale)
+        want = j.dx.clone()
+        dl[2] = bad
+        j.backward(scale, dloss=dl)
+        assert not j.dx[2].isfinite().any() and not j.dw.isfinite().any()
+        keep = torch.arange(130, device="cuda") != 2
+        assert torch.equal(j.dx[keep], want[keep]), (bad, scale)
+        dl[2], dl[3] = 1.0, bad                      # and at a token without a target it counts for nothing
+        j.backward(scale, dloss=dl)
+        dl[3] = 1.0
+        got = j.dx.clone(), j.dw.clone()
+        j.backward(scale, dloss=dl)
+        assert torch.equal(got[0], j.dx) and torch.equal(got[1], j.dw)

@@ -711,6 +711,8 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_ce_few(const uint16_t* x, in
 // One block: the row factors of G and what the products are multiplied by.
 // Row factor = s_i / max |s| (times 2^14 in binary16, which keeps small
 // probabilities out of its subnormals), so that equal factors are exactly 1.
+// s_i = dloss[i] * scale; one that is not finite is no one's maximum, and its
+// own row's factor is NaN.
 __global__ void __launch_bounds__(1024) k_ce_factors(CeHead* head, const int64_t* targets, int64_t n, int64_t vocab,
                                                      const float* dloss, float scale, float up, float* coef)
 {
@@ -723,8 +725,8 @@ __global__ void __launch_bounds__(1024) k_ce_factors(CeHead* head, const int64_t
         const int64_t t = targets[i];
         if (t >= 0 && t < vocab) {
             c++;
-            const float d = dloss ? fabsf(dloss[i]) : 1.0f;
-            most = !(d <= most) ? d : most;                  // NaN stays
+            const float d = dloss ? fabsf(dloss[i] * scale) : 1.0f;
+            if (d < INFINITY) most = fmaxf(most, d);
         }
     }
     sm[threadIdx.x] = most;
@@ -732,22 +734,26 @@ __global__ void __launch_bounds__(1024) k_ce_factors(CeHead* head, const int64_t
     __syncthreads();
     for (int o = 512; o > 0; o >>= 1) {
         if (threadIdx.x < o) {
-            const float x = sm[threadIdx.x], y = sm[threadIdx.x + o];
-            sm[threadIdx.x] = !(y <= x) ? y : x;
+            sm[threadIdx.x] = fmaxf(sm[threadIdx.x], sm[threadIdx.x + o]);
             sc[threadIdx.x] += sc[threadIdx.x + o];
         }
         __syncthreads();
     }
     most = sm[0];
     if (most > 0.0f) most = fmaxf(most, 0x1p-120f);          // its inverse stays finite
-    const float inv = most > 0.0f ? 1.0f / most : (most == 0.0f ? 0.0f : most);
+    const float inv = most > 0.0f ? 1.0f / most : 0.0f;
     if (threadIdx.x == 0) {
         head->err = 0;
-        head->alpha = (dloss ? scale * most : (sc[0] ? scale / (float)sc[0] : 0.0f)) / up;
+        head->alpha = (dloss ? most : (sc[0] ? scale / (float)sc[0] : 0.0f)) / up;
     }
     for (int64_t i = threadIdx.x; i < n; i += 1024) {
         const int64_t t = targets[i];
-        coef[i] = t >= 0 && t < vocab ? (dloss ? dloss[i] * inv * up : up) : 0.0f;
+        float c = 0.0f;
+        if (t >= 0 && t < vocab) {
+            const float d = dloss ? dloss[i] * scale : 1.0f;
+            c = !dloss ? up : fabsf(d) < INFINITY ? d * inv * up : NAN;
+        }
+        coef[i] = c;
     }
 }
 
