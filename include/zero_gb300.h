@@ -581,7 +581,8 @@ zero_status_t zero_ln_backward(const zero_ln_plan_t* plan, const void* dy, const
  * rounded once, to the dtype (the operand type of the products that use it),
  * scaled so that its largest row factor is 1 (binary16: 2^14).
  * A token whose target is outside 0..vocab-1 (such as -100) has no loss: its
- * loss is 0 and its row of dx is 0.  Rows may lie further apart than hidden (strides in
+ * loss is 0 and its row of dx is 0, whatever x and w hold (its row of x still
+ * enters dw's product, times 0: an infinity or NaN there makes dw NaN).  Rows may lie further apart than hidden (strides in
  * values, multiples of 8).  All pointers 16-byte aligned but targets, loss,
  * lse, total and dloss (alignment of their type).  Results do not depend on
  * timing: equal calls give equal bits.  96 bytes. */

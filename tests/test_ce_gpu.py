@@ -449,3 +449,22 @@ def test_one_nonfinite_upstream_gradient(dtype):
         got = j.dx.clone(), j.dw.clone()
         j.backward(scale, dloss=dl)
         assert torch.equal(got[0], j.dx) and torch.equal(got[1], j.dw)
+
+
+@pytest.mark.parametrize("n,piece", [(3, 0), (140, 256)])
+def test_tokens_without_a_target_have_no_gradient_whatever_w_holds(n, piece):
+    """A weight of -inf masks an entry of the vocabulary: its products with
+    probabilities of 0 are NaN, and so is dx, but not of a token whose gradient
+    is 0 by itself."""
+    j = Job(n, 600, 64, "bf16", piece=piece, ignore=0.0)
+    j.x.copy_(j.x.abs() + 0.1)
+    j.w[17] = -float("inf")
+    j.t[:] = 5
+    j.t[n - 1], j.t[1] = -100, 600
+    j.forward()
+    assert j.lse.isfinite().all() and j.loss[1] == 0 and j.loss[n - 1] == 0
+    for dl in (None, torch.ones(n, device="cuda")):
+        j.dx.fill_(GUARD)
+        j.backward(8.0, dloss=dl)
+        assert not j.dx[1].any() and not j.dx[n - 1].any()
+        assert j.dx[0].isnan().all() and _guards_kept(j.fx, j.dx)

@@ -758,10 +758,13 @@ __global__ void __launch_bounds__(1024) k_ce_factors(CeHead* head, const int64_t
 }
 
 // dx (or dw, where its product is split): alpha times the sum of the splits,
-// rounded; 4 columns a thread, a row a blockIdx.y stride.
+// rounded; 4 columns a thread, a row a blockIdx.y stride.  coef: dx's row
+// factors; a row whose factor is 0 is 0, also where w holds infinities, whose
+// products with G's zeros are NaN.
 template <int DT>
 __global__ void __launch_bounds__(256) k_ce_sum(const CeHead* head, const float* acc, int splits, int64_t split_stride,
-                                               int64_t m, int64_t n, int64_t acc_cols, uint16_t* out, int64_t stride)
+                                               int64_t m, int64_t n, int64_t acc_cols, const float* coef, uint16_t* out,
+                                               int64_t stride)
 {
     wait_prev_grid();
     const float alpha = head->err ? NAN : head->alpha;
@@ -774,7 +777,8 @@ __global__ void __launch_bounds__(256) k_ce_sum(const CeHead* head, const float*
             const float4 q = __ldcs(reinterpret_cast<const float4*>(src + k * split_stride));
             s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
         }
-        const uint2 h = make_uint2(from_f32x2<DT>(s.x * alpha, s.y * alpha), from_f32x2<DT>(s.z * alpha, s.w * alpha));
+        uint2 h = make_uint2(from_f32x2<DT>(s.x * alpha, s.y * alpha), from_f32x2<DT>(s.z * alpha, s.w * alpha));
+        if (coef && coef[i] == 0.0f && alpha == alpha) h = make_uint2(0, 0);
         uint16_t* dst = out + i * stride + c;
         if (c + 4 <= n) {
             *reinterpret_cast<uint2*>(dst) = h;
@@ -980,11 +984,11 @@ cudaError_t launch_few(const zero_ce_plan_t& p, const void* x, const void* w, un
 }
 
 cudaError_t launch_sum(int dtype, const CeHead* head, const float* acc, int splits, int64_t apart, int64_t rows, int64_t cols,
-                       int64_t acc_cols, uint16_t* out, int64_t stride, cudaStream_t s)
+                       int64_t acc_cols, const float* coef, uint16_t* out, int64_t stride, cudaStream_t s)
 {
     const dim3 grid((unsigned)ceil_div(acc_cols, 1024), (unsigned)(rows < 4096 ? rows : 4096));
     return launch_after(dtype == ZERO_BF16 ? k_ce_sum<kBF16> : k_ce_sum<kF16>, grid, 256, 0, s, head, acc, splits, apart, rows,
-                        cols, acc_cols, out, stride);
+                        cols, acc_cols, coef, out, stride);
 }
 
 template <int EPI, bool A_MN, bool B_MN>
@@ -1194,7 +1198,8 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
                 ok = ok && make_map(&g.c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, sums, g.splits * rows, l.acc_cols, l.acc_cols, 32);
                 if (ok) e = gemm<kEpiAcc, true, true>(p.dtype, g, s);
                 if (ok && e == cudaSuccess)
-                    e = launch_sum(p.dtype, head, sums, g.splits, rows * l.acc_cols, nv, p.hidden, l.acc_cols, out, p.w_stride, s);
+                    e = launch_sum(p.dtype, head, sums, g.splits, rows * l.acc_cols, nv, p.hidden, l.acc_cols,
+                                   nullptr, out, p.w_stride, s);
             } else {
                 ok = ok && make_map(&g.c, type, out, nv, p.hidden, p.w_stride, 32);
                 if (p.hidden % 8) {
@@ -1207,7 +1212,7 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
         if (!ok) return set_error(ZERO_ECUDA, "zero_ce_backward: cuTensorMapEncodeTiled refused a buffer");
     }
     if (dx && e == cudaSuccess)
-        e = launch_sum(p.dtype, head, acc, p.splits, l.acc_rows * l.acc_cols, p.tokens, p.hidden, l.acc_cols,
+        e = launch_sum(p.dtype, head, acc, p.splits, l.acc_rows * l.acc_cols, p.tokens, p.hidden, l.acc_cols, coef,
                        static_cast<uint16_t*>(dx), p.x_stride, s);
     return e == cudaSuccess ? ZERO_OK : cuda_failed(e, "zero_ce_backward");
 }
