@@ -88,6 +88,7 @@ class Head:
         hp = zg.zero_adamw_t(t=self.t + 1, grad_scale=1.0 / self.scale, seed=self.t, **self.hp)
         zg.zero_adamw_step(self.adamw, self.table, hp, self.flag, s)
         if self.flag.item():
+            zg.zero_ce_status(self.ce, self.ce_ws, s)     # raises if the gradients did not finish
             self.scale = max(1.0, self.scale / 2)
             return False
         self.t += 1

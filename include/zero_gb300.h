@@ -619,8 +619,8 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
                                const float* lse, const float* dloss, float grad_scale, void* dx, void* dw,
                                void* workspace, void* stream);
 /* Synchronises `stream`; ZERO_ETIMEOUT if a bounded wait inside the last
- * forward or backward call with this workspace ran out (its outputs are then
- * NaN or incomplete). */
+ * forward or backward call with this workspace ran out.  Losses, dx and dw
+ * are then NaN, so zero_adamw_check sees them too. */
 zero_status_t zero_ce_status(const zero_ce_plan_t* plan, const void* workspace, void* stream);
 
 /* ---- AdamW over a list of tensors -------------------------------------------

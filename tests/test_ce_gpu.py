@@ -468,3 +468,30 @@ def test_tokens_without_a_target_have_no_gradient_whatever_w_holds(n, piece):
         j.backward(8.0, dloss=dl)
         assert not j.dx[1].any() and not j.dx[n - 1].any()
         assert j.dx[0].isnan().all() and _guards_kept(j.fx, j.dx)
+
+
+@pytest.mark.parametrize("hook,n,v,d,with_dx", [("1", 130, 600, 128, False), ("1", 130, 600, 128, True),
+                                                ("2", 130, 600, 128, False), ("2", 2500, 700, 33, False),
+                                                ("2", 2500, 700, 33, True)])
+def test_bounded_wait_of_the_gradients_is_seen(hook, n, v, d, with_dx):
+    """A wait that runs out in the product that makes G (1) or in dw's (2; one
+    part, or several): the call reports it, and no gradient of an earlier step is
+    left to be taken for this one's, with dx or without."""
+    j = Job(n, v, d, "bf16")
+    j.forward()
+    j.dw.fill_(0.5)
+    j.dx.fill_(0.5)
+    os.environ["ZERO_TEST_WITHHOLD_TILE"] = hook
+    try:
+        zg.zero_ce_backward(j.plan, j.x, j.w, j.t, j.lse, None, 1.0, j.dx if with_dx else None, j.dw, j.ws,
+                            torch.cuda.current_stream())
+    finally:
+        del os.environ["ZERO_TEST_WITHHOLD_TILE"]
+    with pytest.raises(zg.ZeroError) as e:
+        zg.zero_ce_status(j.plan, j.ws)
+    assert e.value.status == zg.ZERO_ETIMEOUT
+    assert j.dw.isnan().all() and _guards_kept(j.fw, j.dw)
+    assert j.dx.isnan().all() if with_dx else (j.dx == 0.5).all()
+    j.backward()
+    zg.zero_ce_status(j.plan, j.ws)
+    assert j.dx.isfinite().all() and j.dw.isfinite().all()

@@ -48,7 +48,8 @@ struct GemmArgs {
     int accumulate;              // kEpiAcc: added to what is there
     int a_rows;                  // rows of A that a CTA copies: 128, or fewer for one row tile of few tokens (the
                                  //   others' results are not kept, so their operands may be anything)
-    int withhold;                // test hook: the first copy is announced but not made, so the waits run out
+    int withhold;                // test hook (environment ZERO_TEST_WITHHOLD_TILE): the first copy is announced but
+                                 //   not made, so the waits run out
     CeHead* head;
     const int64_t* targets;
     float2* part;                // kEpiLse: [strips][m], a strip's maximum and sum
@@ -757,16 +758,38 @@ __global__ void __launch_bounds__(1024) k_ce_factors(CeHead* head, const int64_t
     }
 }
 
+// A gradient that a timed-out product left incomplete, or did not write at all.
+struct Spoiled {
+    uint16_t* out;               // NULL: none
+    int64_t rows, cols, stride;
+};
+
+__device__ void spoil(const CeHead* head, const Spoiled& o)
+{
+    if (!o.out || !head->err) return;
+    for (int64_t i = blockIdx.y; i < o.rows; i += gridDim.y)
+        for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < o.cols; c += (int64_t)gridDim.x * 256)
+            o.out[i * o.stride + c] = 0x7fff;                     // NaN in both types
+}
+
+__global__ void __launch_bounds__(256) k_ce_spoil(const CeHead* head, const Spoiled o)
+{
+    wait_prev_grid();
+    spoil(head, o);
+}
+
 // dx (or dw, where its product is split): alpha times the sum of the splits,
 // rounded; 4 columns a thread, a row a blockIdx.y stride.  coef: dx's row
 // factors; a row whose factor is 0 is 0, also where w holds infinities, whose
-// products with G's zeros are NaN.
+// products with G's zeros are NaN.  The last kernel of a backward pass also
+// turns dw into NaN if a wait ran out (dx is by way of alpha).
 template <int DT>
 __global__ void __launch_bounds__(256) k_ce_sum(const CeHead* head, const float* acc, int splits, int64_t split_stride,
                                                int64_t m, int64_t n, int64_t acc_cols, const float* coef, uint16_t* out,
-                                               int64_t stride)
+                                               int64_t stride, const Spoiled dw)
 {
     wait_prev_grid();
+    spoil(head, dw);
     const float alpha = head->err ? NAN : head->alpha;
     const int64_t c = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
     if (c >= n) return;
@@ -947,6 +970,13 @@ int sm_count()
     return n > 1 ? n : 152;
 }
 
+// Test hook: which product's first copy is withheld: 0 none, 1 the logits', 2 dw's.
+int withheld_product()
+{
+    const char* v = std::getenv("ZERO_TEST_WITHHOLD_TILE");
+    return !v ? 0 : v[0] == '2' ? 2 : 1;
+}
+
 template <int EPI, int DT, bool A_MN, bool B_MN>
 cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t s)
 {
@@ -984,11 +1014,11 @@ cudaError_t launch_few(const zero_ce_plan_t& p, const void* x, const void* w, un
 }
 
 cudaError_t launch_sum(int dtype, const CeHead* head, const float* acc, int splits, int64_t apart, int64_t rows, int64_t cols,
-                       int64_t acc_cols, const float* coef, uint16_t* out, int64_t stride, cudaStream_t s)
+                       int64_t acc_cols, const float* coef, uint16_t* out, int64_t stride, const Spoiled& dw, cudaStream_t s)
 {
     const dim3 grid((unsigned)ceil_div(acc_cols, 1024), (unsigned)(rows < 4096 ? rows : 4096));
     return launch_after(dtype == ZERO_BF16 ? k_ce_sum<kBF16> : k_ce_sum<kF16>, grid, 256, 0, s, head, acc, splits, apart, rows,
-                        cols, acc_cols, coef, out, stride);
+                        cols, acc_cols, coef, out, stride, dw);
 }
 
 template <int EPI, bool A_MN, bool B_MN>
@@ -1104,7 +1134,7 @@ zero_status_t zero_ce_forward(const zero_ce_plan_t* plan, const void* x, const v
         g.targets = targets;
         g.part = reinterpret_cast<float2*>(ws + l.part);
         g.target_logit = reinterpret_cast<float*>(ws + l.target_logit);
-        g.withhold = std::getenv("ZERO_TEST_WITHHOLD_TILE") != nullptr;
+        g.withhold = withheld_product() > 0;
         e = gemm<kEpiLse, false, false>(p.dtype, g, s);
         if (e == cudaSuccess) {
             e = launch_after(k_ce_join, dim3((unsigned)ceil_div(p.tokens, 32)), 1024, 0, s, j);
@@ -1144,6 +1174,7 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
     uint16_t* G = reinterpret_cast<uint16_t*>(ws + l.g);
     float* acc = reinterpret_cast<float*>(ws + l.acc);
     const CUtensorMapDataType type = map_type(p.dtype);
+    const int withheld = withheld_product();
     const float up = p.dtype == ZERO_FP16 ? 16384.0f : 1.0f;
     k_ce_factors<<<1, 1024, 0, s>>>(head, targets, p.tokens, p.vocab, dloss, grad_scale, up, coef);
     cudaError_t e = cudaGetLastError();
@@ -1168,10 +1199,12 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
         g.targets = targets;
         g.lse = lse;
         g.coef = coef;
+        g.withhold = v0 == 0 && withheld == 1;
         if (ok) e = gemm<kEpiGrad, false, false>(p.dtype, g, s);
         g.n = p.hidden;
         g.n_tiles = (int)ceil_div(p.hidden, kBN);
         g.chunk = kChunk;
+        g.withhold = 0;
         if (ok && dx && e == cudaSuccess) {          // dx += G w
             ok = make_map(&g.a, type, G, p.tokens, p.piece, p.piece, g.a_rows) &&
                  make_map(&g.b, type, w, p.vocab, p.hidden, p.w_stride, 64) &&
@@ -1191,6 +1224,7 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
             g.m_tiles = (int)ceil_div(nv, kBM);
             g.k_blocks = (int)ceil_div(p.tokens, kBK);
             g.splits = (int)dw_parts(p);
+            g.withhold = v0 == 0 && withheld == 2;
             g.accumulate = 0;
             if (g.splits > 1) {
                 float* sums = reinterpret_cast<float*>(ws + l.acc_w);
@@ -1199,7 +1233,7 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
                 if (ok) e = gemm<kEpiAcc, true, true>(p.dtype, g, s);
                 if (ok && e == cudaSuccess)
                     e = launch_sum(p.dtype, head, sums, g.splits, rows * l.acc_cols, nv, p.hidden, l.acc_cols,
-                                   nullptr, out, p.w_stride, s);
+                                   nullptr, out, p.w_stride, Spoiled{}, s);
             } else {
                 ok = ok && make_map(&g.c, type, out, nv, p.hidden, p.w_stride, 32);
                 if (p.hidden % 8) {
@@ -1211,9 +1245,12 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
         }
         if (!ok) return set_error(ZERO_ECUDA, "zero_ce_backward: cuTensorMapEncodeTiled refused a buffer");
     }
+    const Spoiled all{static_cast<uint16_t*>(dw), p.vocab, p.hidden, p.w_stride};
     if (dx && e == cudaSuccess)
         e = launch_sum(p.dtype, head, acc, p.splits, l.acc_rows * l.acc_cols, p.tokens, p.hidden, l.acc_cols, coef,
-                       static_cast<uint16_t*>(dx), p.x_stride, s);
+                       static_cast<uint16_t*>(dx), p.x_stride, all, s);
+    else if (e == cudaSuccess)
+        e = launch_after(k_ce_spoil, dim3(1, 608), 256, 0, s, head, all);
     return e == cudaSuccess ? ZERO_OK : cuda_failed(e, "zero_ce_backward");
 }
 
