@@ -64,16 +64,19 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The cluster address, in the pair's first CTA, of what lies at this address here.
+__device__ __forceinline__ uint32_t in_leader(uint32_t addr)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+
 // Arrive on the barrier at this offset in the pair's first CTA.
 __device__ __forceinline__ void mbar_arrive_leader(uint32_t bar)
 {
-    asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
-                 "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" :: "r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(in_leader(bar)) : "memory");
 }
-
-// The address, in the pair's first CTA, of what lies at this address here
-// (shared::cluster addresses of a pair differ in bit 24).
-__device__ __forceinline__ uint32_t in_leader(uint32_t addr) { return addr & 0xfeffffffu; }
 
 // Tiled bulk copy of a box at element coordinates (x, y) into this CTA's
 // shared memory, completing on a barrier of either CTA of the pair; x starts

@@ -154,6 +154,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
         if (lane == 0) {
             bool ok = true;
             int it = 0;
+            const uint32_t lead_full = tc::in_leader(full);
             for (uint32_t t = first; t < tiles && ok; t += stride) {
                 const Tile w = tile_at(g, t);
                 const int m0 = w.mt * kBM + (int)rank * (kBM / 2), n0 = w.nt * kBN + (int)rank * (kBN / 2);
@@ -163,7 +164,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
                         ok = false;
                         break;
                     }
-                    const uint32_t bar = tc::in_leader(full + 8 * s);
+                    const uint32_t bar = lead_full + 8 * s;
                     const uint32_t sa = sm + s * (kABytes + kBBytes), sb = sa + kABytes;
                     const bool copies_a = rank == 0 || g.a_rows == kBM / 2;
                     if (rank == 0) {
