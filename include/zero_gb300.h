@@ -601,7 +601,8 @@ typedef struct zero_ce_plan {
 /* Host only.  strides 0: hidden (then a multiple of 8); piece 0: chosen so
  * that G takes about 512 MiB, else rounded up to a multiple of 256.  tokens
  * >= 0, vocab >= 1, hidden >= 1.  Errors: ZERO_EINVAL, ZERO_EALIGN (a stride
- * that is not a multiple of 8), ZERO_EUNSUPPORTED. */
+ * that is not a multiple of 8), ZERO_EUNSUPPORTED (tokens or vocab over 2^24,
+ * hidden over 2^20, their product about 2^58 or more). */
 zero_status_t zero_ce_plan(int64_t tokens, int64_t vocab, int64_t hidden, int32_t dtype, int64_t x_stride,
                            int64_t w_stride, int64_t piece, zero_ce_plan_t* out);
 /* loss, lse: binary32, one per token.  total (may be NULL): {mean loss of the

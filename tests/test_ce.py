@@ -82,3 +82,26 @@ def test_call_refusals():
     p.splits += 1
     for f, a in ((F, [A] * 7), (B, ok), (zg.zero_ce_status, [A])):
         _refused(zg.ZERO_EINVAL, f, p, *a)
+
+
+@pytest.mark.parametrize("piece", [1 << 62, (1 << 63) - 256, (1 << 63) - 1])
+def test_plan_of_a_huge_piece(piece):
+    p, q = zg.zero_ce_plan(8, 1000, 64, zg.ZERO_BF16, piece=piece), zg.zero_ce_plan(8, 1000, 64, zg.ZERO_BF16, piece=1024)
+    assert bytes(p) == bytes(q) and p.piece == 1024
+
+
+def test_plan_counts_stay_in_range():
+    """Sizes that are each allowed, but whose product is not."""
+    for n, v, d in ((1 << 24, 1 << 22, 1 << 18), (1 << 24, 1 << 22, 1 << 13), (1 << 24, 8, 1 << 20), (1 << 20, 1 << 20, 1 << 20),
+                    (8, 1 << 24, 1 << 20), (1 << 24, 1 << 22, 4096), (1 << 20, 1 << 18, 1 << 20)):
+        try:
+            p = zg.zero_ce_plan(n, v, d, zg.ZERO_BF16)
+        except zg.ZeroError as e:
+            assert e.status == zg.ZERO_EUNSUPPORTED and n * v * d >= 1 << 57
+            continue
+        assert p.flops_forward == 2 * n * v * d and p.flops_backward == 6 * n * v * d
+        assert p.workspace_bytes >= n * p.piece * 2
+        tiles = -(-n // 256) * -(-v // 256)
+        assert tiles / 76 * -(-d // 64) < 1 << 31            # K-blocks that one pair of SMs counts
+    _refused(zg.ZERO_EUNSUPPORTED, zg.zero_ce_plan, 1 << 24, 1 << 22, 1 << 18, zg.ZERO_BF16)
+    assert zg.zero_ce_plan(1 << 20, 1 << 18, 1 << 14, zg.ZERO_BF16).flops_forward == 1 << 53

@@ -1053,6 +1053,11 @@ zero_status_t zero_ce_plan(int64_t tokens, int64_t vocab, int64_t hidden, int32_
         return set_error(ZERO_EUNSUPPORTED, "zero_ce_plan: a stride is 2^38 or more");
     if (ceil_div(tokens, kBM) * ceil_div(vocab, kBN) > (int64_t(1) << 30) || ceil_div(vocab, kBM) * ceil_div(hidden, kBN) > (int64_t(1) << 30))
         return set_error(ZERO_EUNSUPPORTED, "zero_ce_plan: over 2^30 tiles");
+    // a pair's count of K-blocks stays far inside an int, and 6 tokens vocab hidden inside int64_t
+    if (ceil_div(tokens, kBM) * ceil_div(vocab, kBM) * ceil_div(hidden, kBK) > (int64_t(1) << 36) ||
+        ceil_div(tokens, kBM) * ceil_div(hidden, kBN) * ceil_div(vocab, kBK) > (int64_t(1) << 36) ||
+        ceil_div(vocab, kBM) * ceil_div(hidden, kBN) * ceil_div(tokens, kBK) > (int64_t(1) << 36))
+        return set_error(ZERO_EUNSUPPORTED, "zero_ce_plan: tokens * vocab * hidden is about 2^58 or more");
     std::memset(out, 0, sizeof *out);
     out->tokens = tokens;
     out->vocab = vocab;
@@ -1062,7 +1067,7 @@ zero_status_t zero_ce_plan(int64_t tokens, int64_t vocab, int64_t hidden, int32_
     out->dtype = dtype;
     const int64_t all = up256(vocab);
     if (piece) {
-        out->piece = up256(piece) < all ? up256(piece) : all;
+        out->piece = piece < all ? up256(piece) : all;
     } else {
         // about 512 MiB of G, in pieces of about the same size: fewer pieces pass
         // dx's sums through memory less often.  Backward pass of 8192 tokens,
