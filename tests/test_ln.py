@@ -65,3 +65,16 @@ def test_call_refusals():
     p.blocks += 1
     _refused(zg.ZERO_EINVAL, F, p, A, A, A, 1e-5, A)
     _refused(zg.ZERO_EINVAL, B, p, A, A, A, A, A, A, A, A, A)
+
+
+def test_plan_byte_counts_stay_in_range():
+    """Rows and widths that are each allowed: the counts of bytes are right, or the plan is refused."""
+    for rows, dim in ((1 << 40, (1 << 20) - 1), (1 << 40, 1 << 19), (1 << 39, (1 << 20) - 3), (1 << 38, 1 << 20)):
+        for dtype, e in ((zg.ZERO_FP32, 4), (zg.ZERO_BF16, 2)):
+            try:
+                p = zg.zero_ln_plan(rows, dim, dtype)
+            except zg.ZeroError as err:
+                assert err.status == zg.ZERO_EUNSUPPORTED and rows * dim > 1 << 58
+                continue
+            assert p.hbm_bytes_forward == 2 * rows * dim * e + 8 * rows + 2 * dim * e
+            assert p.hbm_bytes_backward == 3 * rows * dim * e + 8 * rows + 3 * dim * e

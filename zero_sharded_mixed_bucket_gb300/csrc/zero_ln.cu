@@ -1087,7 +1087,7 @@ zero_status_t zero_ln_plan(int64_t rows, int64_t dim, int32_t dtype, int64_t x_s
     const int64_t xs = x_stride ? x_stride : dim, ys = y_stride ? y_stride : dim;
     if (xs < dim || ys < dim || xs > (int64_t(1) << 40) || ys > (int64_t(1) << 40))
         return set_error(ZERO_EINVAL, "zero_ln_plan: a stride is below dim or above 2^40");
-    if (rows && (xs > INT64_MAX / 8 / rows || ys > INT64_MAX / 8 / rows))
+    if (rows && (xs > INT64_MAX / 16 / rows || ys > INT64_MAX / 16 / rows))   // 3 * 4 bytes of each below INT64_MAX
         return set_error(ZERO_EUNSUPPORTED, "zero_ln_plan: the rows span too many bytes");
     std::memset(out, 0, sizeof *out);
     out->rows = rows;
