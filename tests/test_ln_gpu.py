@@ -234,3 +234,31 @@ def test_runs_on_the_given_stream():
     zg.zero_ln_forward(plan, late, w, b, 1e-5, y, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("rows,dim,shift", [(5, 48, 0), (9, 768, 0), (9, 771, 1), (5, 2000, 0), (3, 4096, 1), (3, 9000, 1)])
+@pytest.mark.parametrize("size,up", [(1e-22, 1.0), (1e-12, 1e-6), (1e10, 1e6), (1e17, 1e-12)])
+def test_backward_of_rows_of_any_size(rows, dim, shift, size, up):
+    """1/rstd far from 1: xhat is of order 1 whatever x's size, and no power of
+    rstd beyond the first belongs in the result."""
+    x, dy, w, b = _inputs(rows, dim, "fp32", dim, dim, shift)
+    x *= size
+    dy *= up
+    m, r, _, _ = _definition(x, None, None, 0.0)
+    mean, rstd = m.float(), r.float()
+    plan = zg.zero_ln_plan(rows, dim, zg.ZERO_FP32)
+    (_, dx), (_, dw), (_, db) = _buf(rows, dim, dim, torch.float32, shift), _buf(1, dim, dim, torch.float32), _buf(1, dim, dim, torch.float32)
+    ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    zg.zero_ln_backward(plan, dy, x, w, mean, rstd, dx, dw, db, ws)
+    m, r = mean.double(), rstd.double()
+    h = (x.double() - m[:, None]) * r[:, None]
+    g = dy.double() * w.double()
+    c1, c2 = g.mean(1, keepdim=True), (g * h).mean(1, keepdim=True)
+    want = (g - c1 - h * c2) * r[:, None]
+    depth = dim / 32 + 40
+    d1 = (depth + 3) * E32 * g.abs().mean(1, keepdim=True)
+    d2 = (depth + 6) * E32 * (g * h).abs().mean(1, keepdim=True)
+    tol = r[:, None] * (d1 + h.abs() * d2 + 6 * E32 * (g.abs() + c1.abs() + (h * c2).abs()))
+    _within(dx, want, tol + 1.01 * E32 * want.abs(), "dx")
+    _within(dw[0], (dy.double() * h).sum(0), (rows + 8) * E32 * (dy.double() * h).abs().sum(0), "dweight")
+    _within(db[0], dy.double().sum(0), (rows + 2) * E32 * dy.double().abs().sum(0), "dbias")

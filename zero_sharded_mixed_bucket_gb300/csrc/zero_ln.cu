@@ -392,8 +392,10 @@ __global__ void __launch_bounds__(T, BLOCKS) k_ln_forward_rows(const __grid_cons
 // Backward: dx of the rows, and the column sums of dy * xhat and dy over all
 // the rows of a lane in registers, so x and dy are read once for both.  A
 // block writes one pair of partial sums per column (its groups joined in group
-// order).  With d = x - mean and g = dy * weight:
-//   dx = rstd g - rstd avg(g) - rstd^3 avg(g d) d;  dweight = sum (dy rstd) d
+// order).  xhat = (x - mean) rstd is formed first, of order 1 whatever the row's
+// size: the same with x - mean and powers of rstd in the averages is an
+// operation less a value, and loses rows around 1e-22 or 1e17 to overflow and
+// underflow.
 template <int DT, int L, int V, int RB, int S, int T, int BLOCKS, bool RAGGED, int ALIGN>
 __global__ void __launch_bounds__(T, BLOCKS) k_ln_backward_rows(const __grid_constant__ LnArgs a)
 {
@@ -485,11 +487,11 @@ __global__ void __launch_bounds__(T, BLOCKS) k_ln_backward_rows(const __grid_con
                 unpack<DT>(from_slot<DT>(q + ((b * V + v) * 2 + 1) * T), yf);   // 0 past the ends
 #pragma unroll
                 for (int k = 0; k < VE; k++) {
-                    const float d = xf[k] - mean[b], g = yf[k] * w[k];
-                    dw[v][k] = fmaf(yf[k] * rstd[b], d, dw[v][k]);
+                    const float h = RAGGED && k >= cnt[v] ? 0.0f : (xf[k] - mean[b]) * rstd[b], g = yf[k] * w[k];
+                    dw[v][k] = fmaf(yf[k], h, dw[v][k]);
                     db[v][k] += yf[k];
                     c[2 * b] += g;
-                    c[2 * b + 1] = fmaf(g, d, c[2 * b + 1]);
+                    c[2 * b + 1] = fmaf(g, h, c[2 * b + 1]);
                 }
             }
         }
@@ -498,8 +500,8 @@ __global__ void __launch_bounds__(T, BLOCKS) k_ln_backward_rows(const __grid_con
             const int here = rows_here(a.rows, r0, RB);
 #pragma unroll
             for (int b = 0; b < RB; b++) {
-                c[2 * b] = -(c[2 * b] * inv) * rstd[b];
-                c[2 * b + 1] = -(c[2 * b + 1] * inv * rstd[b]) * rstd[b] * rstd[b];
+                c[2 * b] *= -inv;
+                c[2 * b + 1] *= -inv;
             }
 #pragma unroll
             for (int v = 0; v < V; v++) {
@@ -514,7 +516,7 @@ __global__ void __launch_bounds__(T, BLOCKS) k_ln_backward_rows(const __grid_con
                     unpack<DT>(from_slot<DT>(q + ((b * V + v) * 2 + 1) * T), yf);
 #pragma unroll
                     for (int k = 0; k < VE; k++)
-                        xf[k] = fmaf(xf[k] - mean[b], c[2 * b + 1], fmaf(yf[k] * w[k], rstd[b], c[2 * b]));
+                        xf[k] = fmaf((xf[k] - mean[b]) * rstd[b], c[2 * b + 1], fmaf(yf[k], w[k], c[2 * b])) * rstd[b];
                     if (b < here) store_vec<DT, RAGGED, ALIGN>(p, pack<DT>(xf), cnt[v]);
                 }
             }
@@ -686,9 +688,9 @@ __global__ void __launch_bounds__(kLnThreads, 2) k_ln_backward_any(const __grid_
             c[2 * b] = c[2 * b + 1] = 0.0f;
 #pragma unroll
             for (int k = 0; k < K; k++) {
-                x[b][k] -= mean;
+                x[b][k] = ((k < here ? x[b][k] : mean) - mean) * rstd[b];            // xhat; 0 past the end
                 if (b < rows) {
-                    dw[k] = fmaf(dy[b][k] * rstd[b], x[b][k], dw[k]);
+                    dw[k] = fmaf(dy[b][k], x[b][k], dw[k]);
                     db[k] += dy[b][k];
                 }
             }
@@ -713,8 +715,7 @@ __global__ void __launch_bounds__(kLnThreads, 2) k_ln_backward_any(const __grid_
         group_sum<L, 2 * RB>(c, a.warps, sh, turn);
 #pragma unroll
         for (int b = 0; b < RB; b++) {
-            const float k0 = -(c[2 * b] * inv) * rstd[b];
-            const float k1 = -(c[2 * b + 1] * inv * rstd[b]) * rstd[b] * rstd[b];
+            const float k0 = c[2 * b] * -inv * rstd[b], k1 = c[2 * b + 1] * -inv * rstd[b];
             char* row = static_cast<char*>(a.dx) + (r0 + b) * a.x_stride * (DT == kF32 ? 4 : 2);
 #pragma unroll
             for (int k = 0; k < K; k++)
