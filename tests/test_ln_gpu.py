@@ -262,3 +262,23 @@ def test_backward_of_rows_of_any_size(rows, dim, shift, size, up):
     _within(dx, want, tol + 1.01 * E32 * want.abs(), "dx")
     _within(dw[0], (dy.double() * h).sum(0), (rows + 8) * E32 * (dy.double() * h).abs().sum(0), "dweight")
     _within(db[0], dy.double().sum(0), (rows + 2) * E32 * dy.double().abs().sum(0), "dbias")
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("dim", [56, 104, 208, 2256, 4280, 8560, 60, 61, 95, 191, 3000, 9000, 9001, 16872])
+def test_constant_rows_have_no_variance(dim, dtype):
+    """Rows of one value, a whole number whose sums are exact in binary32: the
+    mean is that number, y the bias and rstd 1/sqrt(eps), whatever dim is and
+    however small eps (an error of one unit in the mean's last place is 0.02 of a
+    standard deviation at eps = 1e-5)."""
+    code, dt, u, tiny = DT[dtype]
+    x, _, w, b = _inputs(5, dim, dtype, dim, dim, 0)
+    for k, c in enumerate((1000, -1000, 500, 7, 0)):
+        x[k] = c
+    plan = zg.zero_ln_plan(5, dim, code)
+    y, mean, rstd = torch.empty_like(x), torch.empty(5, device="cuda"), torch.empty(5, device="cuda")
+    for eps in (1e-5, 1e-12):
+        zg.zero_ln_forward(plan, x, w, b, eps, y, mean, rstd)
+        assert mean.tolist() == [1000.0, -1000.0, 500.0, 7.0, 0.0]
+        assert torch.equal(y, b.expand(5, dim))
+        assert ((rstd.double() * eps ** 0.5 - 1).abs() <= 4 * E32).all()

@@ -59,6 +59,22 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
+// s / n, where inv is 1 / n: the product, corrected by what it leaves of s (NaN
+// for an infinite s).  The product alone is off by a unit in the last place for a
+// quarter of all n, and a row of one value has to have that value as its mean:
+// the unit is 0.02 of 1/rstd for a row of 1000 with eps = 1e-5.
+__device__ __forceinline__ float quotient(float s, float n, float inv)
+{
+    const float q = s * inv;
+    return fmaf(fmaf(-q, n, s), inv, q);
+}
+
+// A row's mean from its sum; of an infinite sum that infinity.
+__device__ __forceinline__ float mean_of(float s, float n, float inv)
+{
+    return fabsf(s) < INFINITY ? quotient(s, n, inv) : s;
+}
+
 // Sum over the block, the same value in every thread.
 __device__ __forceinline__ float block_sum(float v, float* sh)
 {
@@ -119,10 +135,10 @@ __device__ __forceinline__ float lane_sums(float (&x)[N])
     return s;
 }
 
-// Sums over the group of N values at once, the same in every lane.  sh: room
+// finish(sum) over the group of N values at once, the same in every lane.  sh: room
 // for [2][T / 32 warps][N] of the block; `turn` alternates, so one barrier a call.
-template <int L, int N, int T = kLnThreads>
-__device__ __forceinline__ void group_sum(float (&x)[N], int warps, float* sh, int& turn)
+template <int L, int N, int T = kLnThreads, typename F>
+__device__ __forceinline__ void group_sum(float (&x)[N], int warps, float* sh, int& turn, F finish)
 {
     const int lane = threadIdx.x & 31;
     float s = lane_sums<L, N>(x);
@@ -145,6 +161,7 @@ __device__ __forceinline__ void group_sum(float (&x)[N], int warps, float* sh, i
             s += __shfl_xor_sync(0xffffffffu, s, o);
         turn++;
     }
+    s = finish(s);                                    // once, before all lanes have it
 #pragma unroll
     for (int k = 0; k < N; k++)
         x[k] = __shfl_sync(0xffffffffu, s, k, L);
@@ -327,7 +344,7 @@ __global__ void __launch_bounds__(T, BLOCKS) k_ln_forward_rows(const __grid_cons
                 for (int k = 0; k < VE; k++)
                     s += f[v][k];
             }
-            own[b] = s * inv_n;
+            own[b] = quotient(s, n, inv_n);
 #pragma unroll
             for (int v = 0; v < V; v++) {
                 if (!RAGGED && V > 1 && cnt[v] == 0) continue;    // no distance past the end
@@ -344,18 +361,14 @@ __global__ void __launch_bounds__(T, BLOCKS) k_ln_forward_rows(const __grid_cons
             mean[b] = s;
             rstd[b] = m2;
         }
-        group_sum<L, RB, T>(mean, a.warps, sh, turn);
+        group_sum<L, RB, T>(mean, a.warps, sh, turn, [&](float t) { return mean_of(t, (float)a.dim, inv); });
 #pragma unroll
         for (int b = 0; b < RB; b++) {
-            mean[b] *= inv;
             const float c = own[b] - mean[b];
             rstd[b] = have ? fmaf(n * c, c, rstd[b]) : 0.0f;
         }
-        group_sum<L, RB, T>(rstd, a.warps, sh, turn);
+        group_sum<L, RB, T>(rstd, a.warps, sh, turn, [&](float t) { return rsqrtf(fmaf(t, inv, a.eps)); });
         const int here = rows_here(a.rows, r0, RB);
-#pragma unroll
-        for (int b = 0; b < RB; b++)
-            rstd[b] = rsqrtf(fmaf(rstd[b], inv, a.eps));
 #pragma unroll
         for (int v = 0; v < V; v++) {
             if (cnt[v] == 0) continue;
@@ -496,13 +509,8 @@ __global__ void __launch_bounds__(T, BLOCKS) k_ln_backward_rows(const __grid_con
             }
         }
         if (a.dx) {
-            group_sum<L, 2 * RB, T>(c, a.warps, sh, turn);
+            group_sum<L, 2 * RB, T>(c, a.warps, sh, turn, [&](float t) { return t * -inv; });
             const int here = rows_here(a.rows, r0, RB);
-#pragma unroll
-            for (int b = 0; b < RB; b++) {
-                c[2 * b] *= -inv;
-                c[2 * b + 1] *= -inv;
-            }
 #pragma unroll
             for (int v = 0; v < V; v++) {
                 if (cnt[v] == 0) continue;
@@ -610,10 +618,9 @@ __global__ void __launch_bounds__(kLnThreads, 2) k_ln_forward_any(const __grid_c
                 s += f[b][k];
             mean[b] = s;
         }
-        group_sum<L, RB>(mean, a.warps, sh, turn);
+        group_sum<L, RB>(mean, a.warps, sh, turn, [&](float t) { return mean_of(t, (float)a.dim, inv); });
 #pragma unroll
         for (int b = 0; b < RB; b++) {
-            mean[b] *= inv;
             float s = 0.0f;
 #pragma unroll
             for (int k = 0; k < K; k++) {
@@ -622,10 +629,7 @@ __global__ void __launch_bounds__(kLnThreads, 2) k_ln_forward_any(const __grid_c
             }
             rstd[b] = s;
         }
-        group_sum<L, RB>(rstd, a.warps, sh, turn);
-#pragma unroll
-        for (int b = 0; b < RB; b++)
-            rstd[b] = rsqrtf(fmaf(rstd[b], inv, a.eps));
+        group_sum<L, RB>(rstd, a.warps, sh, turn, [&](float t) { return rsqrtf(fmaf(t, inv, a.eps)); });
 #pragma unroll
         for (int k0 = 0; k0 < K; k0 += 8) {
             float w[8], bias[8];
@@ -712,10 +716,10 @@ __global__ void __launch_bounds__(kLnThreads, 2) k_ln_backward_any(const __grid_
                 c[2 * b] += dy[b][k];
                 c[2 * b + 1] = fmaf(dy[b][k], x[b][k], c[2 * b + 1]);
             }
-        group_sum<L, 2 * RB>(c, a.warps, sh, turn);
+        group_sum<L, 2 * RB>(c, a.warps, sh, turn, [&](float t) { return t * -inv; });
 #pragma unroll
         for (int b = 0; b < RB; b++) {
-            const float k0 = c[2 * b] * -inv * rstd[b], k1 = c[2 * b + 1] * -inv * rstd[b];
+            const float k0 = c[2 * b] * rstd[b], k1 = c[2 * b + 1] * rstd[b];
             char* row = static_cast<char*>(a.dx) + (r0 + b) * a.x_stride * (DT == kF32 ? 4 : 2);
 #pragma unroll
             for (int k = 0; k < K; k++)
@@ -764,7 +768,7 @@ __global__ void __launch_bounds__(kLnThreads) k_ln_forward(const __grid_constant
         float s = 0.0f;
         for (int64_t j = threadIdx.x; j < a.dim; j += kLnThreads)
             s += ld1<DT>(a.x, xo + j);
-        const float mean = block_sum(s, sh) * inv;
+        const float mean = mean_of(block_sum(s, sh), (float)a.dim, inv);
         float q = 0.0f;
         for (int64_t j = threadIdx.x; j < a.dim; j += kLnThreads) {
             const float c = ld1<DT>(a.x, xo + j) - mean;
