@@ -372,3 +372,104 @@ def test_offsets_past_32_bits(bits):
         assert np.array_equal(sc[0][a // 256:a // 256 + em.size].cpu().numpy(), em)
     del grad, master, m, v, sc
     torch.cuda.empty_cache()
+
+
+def _step8(T, hp):
+    """The 8-bit step of a list in binary32 (t = hp.t), compared with the kernel's bit for bit."""
+    old = [{n: T.host(k, n) for n in T.view[k]} for k in range(len(T.sizes))]
+    zg.zero_adamw_step(T.plan, T.table, hp)
+    b1, b2 = F(hp.beta1), F(hp.beta2)
+    bc1, bc2 = 1 - float(b1) ** hp.t, 1 - float(b2) ** hp.t
+    with np.errstate(all="ignore"):
+        for k, n in enumerate(T.sizes):
+            o = old[k]
+            g = o["grad"] * F(hp.grad_scale)
+            m0, r0 = _unpack(o)
+            m = m0 * b1 + g * (F(1) - b1)
+            r = np.sqrt((r0 * r0) * b2 + (g * g) * (F(1) - b2))
+            w = o["master"] * _keep(hp, T.decay[k]) - (m * F(float(F(hp.lr)) / bc1)) / (r * F(1 / np.sqrt(bc2)) + F(hp.eps))
+            rnd = _random(n, int(T.starts[k]), hp)
+            cm, em = _codes(np.abs(m), rnd, 6, 127, False)
+            cr, er = _codes(r, rnd, 14, 255, True)
+            cm = cm + np.where((m < 0) & (cm > 0), 128, 0)
+            assert np.array_equal(T.host(k, "m_scale"), em) and np.array_equal(T.host(k, "v_scale"), er)
+            assert np.array_equal(T.host(k, "m"), cm) and np.array_equal(T.host(k, "v"), cr)
+            assert np.array_equal(T.host(k, "master"), w, equal_nan=True)
+
+
+@pytest.mark.parametrize("shifts", [(0,), (1,)])
+def test_8bit_scales_of_the_whole_range(shifts):
+    """Blocks of every scale byte, gradients from 1e-20 to 1e18: those whose
+    decoding or encoding takes two factors, and the last scale, which cuts."""
+    n = 253 * 256 * 3 - 100
+    T = Tensors([n], "fp32", 8, seed=9, shifts=shifts)
+    v, rng = T.view[0], np.random.default_rng(10)
+    nb = v["m_scale"].numel()
+    v["m_scale"].copy_(torch.from_numpy((1 + np.arange(nb) % 253).astype(np.uint8)))
+    v["v_scale"].copy_(torch.from_numpy((1 + rng.permutation(nb) % 253).astype(np.uint8)))
+    size = np.repeat(10.0 ** rng.uniform(-20, 18, nb), 256)[:n] * (np.repeat(rng.random(nb), 256)[:n] < 0.7)
+    v["grad"].copy_(torch.from_numpy((rng.standard_normal(n) * size).astype(F)))
+    for t in (5, 6):
+        _step8(T, _hp(t=t))
+        out = [torch.zeros(T.plan.flat_elems, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        zg.zero_adamw_states(T.plan, T.table, *out)
+        for got, want in zip(out, _unpack({q: T.host(0, q) for q in ("m", "v", "m_scale", "v_scale")})):
+            got = got[:n].float().cpu().numpy()
+            normal = np.abs(want) >= 2.0 ** -126
+            assert np.array_equal(got[normal], want[normal])
+            assert (np.abs(got - want) < 2.0 ** -133).all()          # bfloat16's subnormals
+    assert T.guards_kept()
+    big = T.host(0, "m_scale") > 133
+    assert big.any() and (T.host(0, "v_scale") > 141).any() and (T.host(0, "v_scale") == 253).any()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_8bit_block_of_a_nonfinite_gradient(bad):
+    """A NaN or infinity that is not checked for takes its block of 256 with it:
+    the last scale, the largest codes at the value, the least nonzero root
+    beside it; the neighbouring blocks are what they are without."""
+    T, clean = Tensors([1000], "fp32", 8, seed=11), Tensors([1000], "fp32", 8, seed=11)
+    T.view[0]["grad"][300] = bad
+    _step8(T, _hp())
+    zg.zero_adamw_step(clean.plan, clean.table, _hp())
+    v, c = T.view[0], clean.view[0]
+    assert v["m_scale"][1] == 253 and v["v_scale"][1] == 253
+    assert v["m"][300] == (255 if bad < 0 else 127) and v["v"][300] == 255 and not v["master"][300].isfinite()
+    keep = torch.ones(1000, dtype=torch.bool)
+    keep[256:512] = False
+    for q in ("m", "v", "master", "param"):
+        assert torch.equal(v[q][keep.cuda()], c[q][keep.cuda()])
+    assert not v["m"][301:512].any() and (v["v"][301:512] == 1).all()
+    rest = torch.arange(1000) != 300
+    assert torch.equal(v["master"][rest.cuda()], c["master"][rest.cuda()])
+
+
+def test_binary32_weights_past_32_bits():
+    """The weights, too, of values around 2^32 in one tensor."""
+    n = 2 ** 32 + 2000
+    grad, master = torch.zeros(n, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, device="cuda")
+    m, v = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    marks = [2 ** 31 - 512, 2 ** 32 - 512, n - 1024]
+    g = torch.Generator(device="cuda").manual_seed(0)
+    for a in marks:
+        grad[a:a + 1024] = torch.randn(1024, device="cuda", generator=g).bfloat16()
+        master[a:a + 1024] = torch.randn(1024, device="cuda", generator=g)
+    g0, w0 = ([t[a:a + 1024].clone() for a in marks] for t in (grad, master))
+    rec = [zg.adamw_tensor(grad=grad, master=master, m=m, v=v, numel=n, weight_decay=0.1)]
+    plan = zg.zero_adamw_plan(rec, zg.ZERO_BF16, 32)
+    table = torch.empty(plan.table_bytes, dtype=torch.uint8, device="cuda")
+    zg.zero_adamw_table_init(plan, rec, table)
+    zg.zero_adamw_step(plan, table, _hp(t=1, grad_scale=1.0))
+    # the same values as a short list
+    for k, a in enumerate(marks):
+        ts = {"grad": g0[k], "master": w0[k].clone(), "m": torch.zeros(1024, device="cuda"), "v": torch.zeros(1024, device="cuda")}
+        r = [zg.adamw_tensor(numel=1024, weight_decay=0.1, **ts)]
+        p = zg.zero_adamw_plan(r, zg.ZERO_BF16, 32)
+        tab = torch.empty(p.table_bytes, dtype=torch.uint8, device="cuda")
+        zg.zero_adamw_table_init(p, r, tab)
+        zg.zero_adamw_step(p, tab, _hp(t=1, grad_scale=1.0))
+        for q, big in (("master", master), ("m", m), ("v", v)):
+            assert torch.equal(ts[q], big[a:a + 1024]), (k, q)
+        assert not torch.equal(ts["master"], w0[k])
+    del grad, master, m, v
+    torch.cuda.empty_cache()

@@ -495,3 +495,17 @@ def test_bounded_wait_of_the_gradients_is_seen(hook, n, v, d, with_dx):
     j.backward()
     zg.zero_ce_status(j.plan, j.ws)
     assert j.dx.isfinite().all() and j.dw.isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_tiny_upstream_gradients_against_the_definition(dtype):
+    """dloss far below 1, as it is (bfloat16) and scaled up (binary16)."""
+    j = Job(40, 300, 64, dtype)
+    j.forward()
+    j.define()
+    g = torch.Generator(device="cuda").manual_seed(6)
+    dl = (1 + torch.rand(40, device="cuda", generator=g)) * 1e-30
+    scale = 1.0 if dtype == "bf16" else 2.0 ** 100
+    j.backward(scale, dloss=dl)
+    j.check_backward(dl.double() * scale)
+    assert j.dx[0].any() and j.dw[0].any()

@@ -71,3 +71,12 @@ def test_overflowed_step_is_skipped():
     assert not h.update() and h.scale == 2.0 ** 39 and h.t == 0
     for k, w in h.master.items():
         assert torch.equal(w, before[k])
+
+
+def test_8_and_32_bit_moments_end_at_the_same_loss():
+    """8-bit moments are off by a thirtieth of themselves at random, so the
+    steps are, and the training ends at 32-bit moments' loss: within a quarter of it."""
+    M = _example()
+    a, b = (M.main(["--steps", "120", "--vocab", "1500", "--hidden", "192", "--tokens", "1024", "--bits", n]) for n in ("8", "32"))
+    a, b = (sum(x[-10:]) / 10 for x in (a, b))
+    assert abs(a - b) <= 0.25 * b + 0.02
