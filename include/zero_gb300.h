@@ -532,7 +532,8 @@ zero_status_t zero_pa_gather(const zero_pa_plan_t* plan, const void* const* shar
  * Rows may lie further apart than dim (strides, in values); what is between
  * them is neither read nor written.  Outputs must not overlap inputs.
  * Pointers need the alignment of their type only: rows that start on 16-byte
- * boundaries take 16-byte accesses, others single-value ones (two to three
+ * boundaries take 16-byte accesses, 16-bit ones on 4-byte boundaries 4-byte
+ * accesses (1.6 times slower), others single-value ones (two to two and a half
  * times slower in 16-bit types).  72 bytes. */
 typedef struct zero_ln_plan {
     int64_t rows, dim;
@@ -571,21 +572,25 @@ zero_status_t zero_ln_backward(const zero_ln_plan_t* plan, const void* dy, const
  *   z = x w^T;  lse_i = log sum_v exp z_iv;  loss_i = lse_i - z_i,t(i)
  *   G_iv = s_i (exp(z_iv - lse_i) - [v = t(i)]);  dx = G w;  dw = G^T x
  * The forward pass keeps one running maximum and sum per token and strip of
- * 256 vocabulary entries.  The backward pass computes z again, a piece of the
+ * 128 vocabulary entries.  The backward pass computes z again, a piece of the
  * vocabulary at a time, and holds G of one piece in 16 bits.
  * x, w, dx and dw have the plan's dtype (ZERO_FP16 or ZERO_BF16; ZERO_FP32 is
  * ZERO_EUNSUPPORTED); products are accumulated in binary32 (1024 values at a
- * time on the tensor cores, which round toward zero, those sums to nearest; the
- * loss and G use the same z), softmax
+ * time on the tensor cores, which round toward zero, those sums to nearest;
+ * the loss of more than 3 tokens and G use the same z, up to 3 tokens' loss is
+ * summed by plain multiply-adds and G's z in steps of 512), softmax
  * statistics and loss are binary32, dx and dw are rounded once, and G is
  * rounded once, to the dtype (the operand type of the products that use it),
- * scaled so that its largest row factor is 1 (binary16: 2^14).
+ * scaled so that its largest row factor is 1 (binary16: 2^14, so its absolute
+ * spacing, 2^-38 of the largest |s_i|, cuts small probabilities of tokens whose
+ * factors are some 10^6 times below it).
  * A token whose target is outside 0..vocab-1 (such as -100) has no loss: its
  * loss is 0 and its row of dx is 0, whatever x and w hold (its row of x still
- * enters dw's product, times 0: an infinity or NaN there makes dw NaN).  Rows may lie further apart than hidden (strides in
- * values, multiples of 8).  All pointers 16-byte aligned but targets, loss,
- * lse, total and dloss (alignment of their type).  Results do not depend on
- * timing: equal calls give equal bits.  96 bytes. */
+ * enters dw's product, times 0: an infinity or NaN there makes dw NaN).  Rows
+ * may lie further apart than hidden (strides in values, multiples of 8).  All
+ * pointers 16-byte aligned but targets, loss, lse, total and dloss (alignment
+ * of their type).  Results do not depend on timing: equal calls give equal
+ * bits.  96 bytes. */
 typedef struct zero_ce_plan {
     int64_t tokens, vocab, hidden;
     int64_t x_stride, w_stride;  /* values between rows of x and dx, of w and dw */
@@ -659,8 +664,10 @@ zero_status_t zero_ce_status(const zero_ce_plan_t* plan, const void* workspace, 
  *     r = sqrt(b2*(r*r) + (1-b2)*(g*g));
  *     w = w - (m * (lr/bc1)) / (r * (1/sqrt(bc2)) + eps)
  * master is the binary32 weight; param (may be NULL) receives its cast to
- * the plan's dtype, the type of grad.  Non-finite gradients poison the
- * values they meet: see zero_adamw_check.  With eps 0 a weight whose
+ * the plan's dtype, the type of grad.  A non-finite gradient that is not
+ * checked for (zero_adamw_check) makes its weight non-finite too, and 8-bit
+ * moments of its whole block useless: scale 253, the largest codes there, 0 and
+ * the least nonzero root beside it.  With eps 0 a weight whose
  * gradients were all zero becomes 0/0, as the formula says.  72 bytes. */
 typedef struct zero_adamw_tensor {
     const void* grad;
@@ -714,7 +721,8 @@ zero_status_t zero_adamw_check(const zero_adamw_plan_t* plan, const void* table,
  * when it is nonzero. */
 zero_status_t zero_adamw_step(const zero_adamw_plan_t* plan, const void* table, const zero_adamw_t* hp,
                               const uint32_t* skip, void* stream);
-/* 8-bit states: the stored m and r = sqrt(v) as bfloat16 values, exact, in
+/* 8-bit states: the stored m and r = sqrt(v) as bfloat16 values, exact (m of
+ * scale bytes below 4, under 2^-122, cut to bfloat16's subnormals), in
  * the plan's flat order (flat_elems each, 16-byte aligned; the gaps between
  * tensors are not written): for a checkpoint. */
 zero_status_t zero_adamw_states(const zero_adamw_plan_t* plan, const void* table, void* m, void* root_v,
