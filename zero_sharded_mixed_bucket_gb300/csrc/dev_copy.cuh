@@ -7,11 +7,11 @@
 
 namespace zg {
 
-// N (4, 8 or 16) bytes at an N-byte boundary: `bytes` of them from src, the rest 0.
+// N (4 or 16) bytes at an N-byte boundary: `bytes` of them from src, the rest 0.
 template <int N>
 __device__ __forceinline__ void copy_ahead(void* smem, const void* src, int bytes = N)
 {
-    static_assert(N == 4 || N == 8 || N == 16, "");
+    static_assert(N == 4 || N == 16, "");
     if constexpr (N == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                      :: "r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(src), "r"(bytes) : "memory");

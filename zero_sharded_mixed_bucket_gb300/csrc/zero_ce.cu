@@ -1168,7 +1168,8 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (!p.tokens) {
         if (dw) k_ce_zero<<<1024, 256, 0, s>>>(static_cast<uint16_t*>(dw), p.vocab, p.hidden, p.w_stride);
-        const cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(CeHead), s);
+        cudaError_t e = cudaGetLastError();
+        if (e == cudaSuccess) e = cudaMemsetAsync(workspace, 0, sizeof(CeHead), s);
         return e == cudaSuccess ? ZERO_OK : cuda_failed(e, "zero_ce_backward");
     }
     if (!dx && !dw) return ZERO_OK;

@@ -928,11 +928,13 @@ cudaError_t forward_rows(LnArgs a, int64_t vecs, int align, cudaStream_t s)
     const int64_t most = (int64_t)kSms * (BLOCKS * T / h.threads);            // resident at once
     const int64_t blocks = need < most ? need : most;
     constexpr size_t smem = (size_t)S * RB * V * T * 16;
-    if constexpr (DT != kF32)
-        if (align < 16)
-            return launch_slots<k_ln_forward_rows<DT, 32, V, RB, S, T, BLOCKS, true, 4>, smem>(a, blocks, h.threads, s);
-    if (a.dim % kVecOf<DT>)
-        return launch_slots<k_ln_forward_rows<DT, 32, V, RB, S, T, BLOCKS, true, 16>, smem>(a, blocks, h.threads, s);
+    if constexpr (L == 32) {                          // fewer lanes: whole rows on 16-byte boundaries only
+        if constexpr (DT != kF32)
+            if (align < 16)
+                return launch_slots<k_ln_forward_rows<DT, L, V, RB, S, T, BLOCKS, true, 4>, smem>(a, blocks, h.threads, s);
+        if (a.dim % kVecOf<DT>)
+            return launch_slots<k_ln_forward_rows<DT, L, V, RB, S, T, BLOCKS, true, 16>, smem>(a, blocks, h.threads, s);
+    }
     return launch_slots<k_ln_forward_rows<DT, L, V, RB, S, T, BLOCKS, false, 16>, smem>(a, blocks, h.threads, s);
 }
 
@@ -1001,11 +1003,13 @@ cudaError_t backward_rows(LnArgs a, int64_t vecs, int align, int blocks, cudaStr
     a.warps = h.warps;
     constexpr int S = kLnBwdAhead;
     constexpr size_t smem = (size_t)S * RB * V * 2 * T * 16;
-    if constexpr (DT != kF32)
-        if (align < 16)
-            return launch_slots<k_ln_backward_rows<DT, 32, V, RB, S, T, BLOCKS, true, 4>, smem>(a, blocks, h.threads, s);
-    if (a.dim % kVecOf<DT>)
-        return launch_slots<k_ln_backward_rows<DT, 32, V, RB, S, T, BLOCKS, true, 16>, smem>(a, blocks, h.threads, s);
+    if constexpr (L == 32) {
+        if constexpr (DT != kF32)
+            if (align < 16)
+                return launch_slots<k_ln_backward_rows<DT, L, V, RB, S, T, BLOCKS, true, 4>, smem>(a, blocks, h.threads, s);
+        if (a.dim % kVecOf<DT>)
+            return launch_slots<k_ln_backward_rows<DT, L, V, RB, S, T, BLOCKS, true, 16>, smem>(a, blocks, h.threads, s);
+    }
     return launch_slots<k_ln_backward_rows<DT, L, V, RB, S, T, BLOCKS, false, 16>, smem>(a, blocks, h.threads, s);
 }
 
