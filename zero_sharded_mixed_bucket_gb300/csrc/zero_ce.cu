@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(1024) k_ce_join(const __grid_constant__ JoinAr
 // Each lane keeps one row's logit; 32 of them at a time go into the warp's
 // running maximum and sum.  The last block joins the blocks' pairs.  Products
 // and sums are binary32 multiply-adds.  At 4 tokens the multiply-adds bound it
-// (90 us at hidden 4096; the tensor cores' path takes 87).
+// (90 us at hidden 4096; the tensor cores' path takes 83).
 constexpr int kFewTokens = 3, kFewThreads = 256, kFewBlocks = 456;
 constexpr int kFewSmem = 64 * 1024;                   // all tokens' values, 16 bits each
 

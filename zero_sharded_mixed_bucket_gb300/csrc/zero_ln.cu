@@ -97,13 +97,20 @@ __device__ __forceinline__ float block_sum(float v, float* sh)
 // bytes in flight do not depend on registers or on how far the other lanes
 // are, and nothing waits but a lane for its own copies.  The rows stay there
 // until they are done, read again for each use.
-// What bounds these kernels is issuing instructions (about 17 a value forward,
-// 30 backward), so a batch is as large as registers allow: its sums, addresses
-// and loop are shared by all its values.  8192 x 4096 bfloat16 forward: 26.8 us,
-// 5.0 TB/s (a device copy of the same bytes 23.5; rows in registers, a block to
-// a row: 35).  32768 x 1600 binary16 backward: 73.9 us, 4.3 TB/s (adding two
-// arrays into a third of these sizes: 47.5; weight gradients in a pass of their
-// own: 220; batches ahead in registers: 82).
+// What bounds these kernels is what few warps can issue: 17 instructions a value
+// forward, 30 backward, so a batch is as large as registers allow (its sums,
+// addresses and loop are shared by all its values), and registers leave 5.4 and
+// 3.2 warps to a scheduler, which issues in 69 and 62 % of the cycles.  A warp's
+// 5.1 cycles an instruction backward are 1 to issue, 1.1 in turn behind another,
+// 0.75 of fixed latencies, 0.7 at the batch's barrier, 0.4 each for the arithmetic
+// pipe and shared memory, 0.2 for loads; DRAM is half idle.  (Packed pairs of
+// binary32 operations, fewer instructions, gained nothing: 79 us for 74.5.)
+// 8192 x 4096 bfloat16 forward: 26.8 us, 5.0 TB/s (a device copy of the same
+// bytes 23.5; rows in registers, a block to a row: 35).  32768 x 1600 binary16
+// backward: 74.3 us, 4.2 TB/s (adding two arrays into a third of these sizes:
+// 47.5; weight gradients in a pass of their own: 220; batches ahead in
+// registers: 82).  In 32 bits: 8192 x 4096 forward 46.4 us, 5.8 TB/s, backward
+// 85, 4.7.
 // Values of vector v of lane gl of a group of `lanes` that exist.
 template <int DT>
 __device__ __forceinline__ int vec_count(int64_t dim, int v, int gl, int lanes)
@@ -572,8 +579,8 @@ __global__ void __launch_bounds__(T, BLOCKS) k_ln_backward_rows(const __grid_con
 // ---- other rows ------------------------------------------------------------------------
 // The same groups, a lane's K values of a row one group of lanes apart: one
 // access a value, neighbouring lanes neighbouring values, kept in registers as
-// binary32.  What bounds these is the accesses: 8192 x 4095 bfloat16 forward 51
-// us, 2.6 TB/s, backward 109; 16384 x 1023 binary32 30 and 58.  Whole 16-byte
+// binary32.  What bounds these is the accesses: 8192 x 4095 bfloat16 forward 52
+// us, 2.6 TB/s, backward 111; 16384 x 1023 binary32 30 and 57.  Whole 16-byte
 // copies around a row, realigned in shared memory on the way in and by shuffles
 // on the way out, take 59 and 92, and 39 and 62: the windows' ragged ends cost
 // what the wide accesses save.  4-byte copies of 16-bit rows with the odd value
@@ -754,10 +761,12 @@ __global__ void __launch_bounds__(kLnThreads, 2) k_ln_backward_any(const __grid_
 }
 
 // ---- long rows -------------------------------------------------------------------------
-// More than a block holds: a block per row, values read again for every use
-// (from cache), so the accesses bound it: 2048 x 20480 bfloat16 forward 63 us,
-// 2.7 TB/s.  Backward in two kernels, rows for dx and columns for the weight
-// gradients: 2048 x 20480 232 us, 1.1 TB/s.
+// More than a block holds (forward over 4096 vectors of 16 bytes, backward over
+// 2048): a block per row, values read again for every use (from cache), so the
+// accesses bound it: 2048 x 40960 bfloat16 forward 274 us, 1.2 TB/s.  Backward in
+// two kernels, rows for dx and columns for the weight gradients: 2048 x 20480 232
+// us, 1.1 TB/s.  (Forward that size is in shared memory, one block of 10 warps
+// an SM: 64 us, 2.6 TB/s.)
 template <int DT>
 __global__ void __launch_bounds__(kLnThreads) k_ln_forward(const __grid_constant__ LnArgs a)
 {
