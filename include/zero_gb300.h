@@ -691,7 +691,7 @@ typedef struct zero_adamw_plan {
     int64_t table_bytes;         /* device memory of the list */
     int64_t hbm_bytes;           /* algorithmic HBM bytes of one step */
     int32_t dtype, state_bits;   /* zero_dtype_t; 8 or 32 */
-    int64_t reserved;
+    int64_t mark;                /* of the fields above: a plan is used as zero_adamw_plan made it */
 } zero_adamw_plan_t;
 
 /* Hyper-parameters of one step.  32 bytes. */

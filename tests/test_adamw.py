@@ -88,3 +88,16 @@ def test_step_refusals():
     p8 = zg.zero_adamw_plan([_t(m_scale=A, v_scale=A)], zg.ZERO_BF16, 8)
     _refused(zg.ZERO_ENOMEM, zg.zero_adamw_states, p8, A, None, A)
     _refused(zg.ZERO_EALIGN, zg.zero_adamw_states, p8, A, A, A + 2)
+
+
+@pytest.mark.parametrize("numel,flat,chunks", [(1 << 62, 1 << 62, 3), (4300, 1 << 20, 3), (4300, 4608, 1), (4300, 4608, 40)])
+def test_plans_that_no_list_has(numel, flat, chunks):
+    """Counts that agree with one another, but not with any list of two tensors:
+    with more chunks than the table was filled for, what lies past it would be read."""
+    p = zg.zero_adamw_plan([_t(4200), _t(100)], zg.ZERO_BF16, 32)
+    assert (p.numel, p.flat_elems, p.n_chunks) == (4300, 4608, 3)
+    p.table_bytes += 4 * (chunks - 3)
+    p.numel, p.flat_elems, p.n_chunks, p.hbm_bytes = numel, flat, chunks, (numel * 28 + (1 << 63)) % (1 << 64) - (1 << 63)
+    hp = zg.zero_adamw_t(t=1, lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, grad_scale=1.0)
+    _refused(zg.ZERO_EINVAL, zg.zero_adamw_step, p, A, hp)
+    _refused(zg.ZERO_EINVAL, zg.zero_adamw_check, p, A, A)

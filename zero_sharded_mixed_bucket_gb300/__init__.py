@@ -105,7 +105,7 @@ class zero_adamw_tensor_t(ctypes.Structure):
 
 class zero_adamw_plan_t(ctypes.Structure):
     _fields_ = [(n, c_i64) for n in ("n_tensors", "numel", "flat_elems", "n_chunks", "table_bytes", "hbm_bytes")] + \
-               [("dtype", c_i32), ("state_bits", c_i32), ("reserved", c_i64)]
+               [("dtype", c_i32), ("state_bits", c_i32), ("mark", c_i64)]
 
 
 class zero_adamw_t(ctypes.Structure):

@@ -463,15 +463,22 @@ zero_status_t cuda_failed(cudaError_t e, const char* what)
     return set_error(ZERO_ECUDA, msg);
 }
 
+// A mark over a plan's other fields (FNV-1a by 64-bit words): the list that they
+// were counted from is not at hand when a plan is used.
+int64_t mark_of(const zero_adamw_plan_t& p)
+{
+    const uint64_t f[] = {(uint64_t)p.n_tensors,   (uint64_t)p.numel,     (uint64_t)p.flat_elems, (uint64_t)p.n_chunks,
+                          (uint64_t)p.table_bytes, (uint64_t)p.hbm_bytes, (uint64_t)p.dtype,      (uint64_t)p.state_bits};
+    uint64_t h = 0xcbf29ce484222325ull;
+    for (uint64_t x : f)
+        h = (h ^ x) * 0x100000001b3ull;
+    return (int64_t)(h ^ (h >> 32));
+}
+
 zero_status_t check_adamw_plan(const zero_adamw_plan_t* p, const void* table)
 {
     if (!p) return set_error(ZERO_EINVAL, "AdamW plan is NULL");
-    const int64_t e = p->dtype == ZERO_FP32 ? 4 : 2;
-    if ((p->state_bits != 8 && p->state_bits != 32) ||
-        (p->dtype != ZERO_FP16 && p->dtype != ZERO_BF16 && p->dtype != ZERO_FP32) || p->n_tensors < 0 ||
-        p->n_tensors > (int64_t(1) << 20) || p->numel < 0 || p->n_chunks < 0 || p->n_chunks > INT32_MAX ||
-        p->table_bytes != chunk_map_offset(p->n_tensors) + p->n_chunks * 4 || p->flat_elems < p->numel ||
-        p->flat_elems % kQBlock || p->hbm_bytes != p->numel * (2 * e + (p->state_bits == 32 ? 24 : 12)))
+    if (p->mark != mark_of(*p))
         return set_error(ZERO_EINVAL, "AdamW plan was not made by zero_adamw_plan");
     if (p->n_chunks && !table) return set_error(ZERO_ENOMEM, "AdamW table is NULL");
     if (!aligned_to(table, 16)) return set_error(ZERO_EALIGN, "AdamW table is not 16-byte aligned");
@@ -516,6 +523,7 @@ zero_status_t zero_adamw_plan(const zero_adamw_tensor_t* tensors, int64_t n_tens
     out->dtype = dtype;
     out->state_bits = state_bits;
     out->hbm_bytes = numel * (2 * (dtype == ZERO_FP32 ? 4 : 2) + (state_bits == 32 ? 24 : 12));
+    out->mark = mark_of(*out);
     return ZERO_OK;
 }
 
