@@ -565,6 +565,66 @@ zero_status_t zero_ln_backward(const zero_ln_plan_t* plan, const void* dy, const
                                const float* mean, const float* rstd, void* dx, void* dweight, void* dbias,
                                void* workspace, void* stream);
 
+/* ---- root-mean-square norm -------------------------------------------------
+ * The norm of a block that adds its output x to a residual stream, and its
+ * gradient, on rows of `dim` values (Zhang & Sennrich, "Root Mean Square Layer
+ * Normalization"):
+ *   h  = x + residual, rounded to the dtype (h = x without a residual)
+ *   y  = h * rstd * weight,  rstd = 1/sqrt(avg(h^2) + eps), avg over the row
+ *   dx = rstd * (g - xhat * avg(g * xhat)) + dh,  g = dy * weight, xhat = h * rstd
+ *   dweight = sum over rows of dy * xhat
+ * dh is the gradient that reaches h by the stream itself; dx is that of x and of
+ * the residual alike.  All of x, residual, h, weight, y, dy, dh, dx, dweight
+ * have the plan's dtype; rstd is binary32, one per row.  Sums are binary32 in
+ * an order fixed by the plan and the pointers' alignment; each output is rounded
+ * once.  Squares are summed as they are: a row with values over 2^63 or so in
+ * bfloat16 or binary32 has an infinite sum, and y 0.
+ * y may also be (or be as well) q, one byte per value with a scale byte for every
+ * `block` (32 or 128) values of a row, the last block of a row maybe shorter:
+ *   q = e4m3 (1 sign, 4 exponent, 3 fraction bits, 448 the largest) of
+ *   y * 2^(127 - e), rounded to nearest even once, from binary32;
+ *   e: the least byte >= 0 with the block's largest |y| <= 448 * 2^(e - 127);
+ *   a block with an infinity or a NaN: e = 255, codes 0x7f or 0xff (NaN).
+ * Strides and pointers as for layer norm (x_stride: rows of x, residual, h, dh
+ * and dx; y_stride: of y, dy, q and values); q_scale rows are scale_cols bytes
+ * apart.  Outputs must not overlap inputs, but h may be x or residual itself and
+ * dx may be dh itself.  88 bytes. */
+typedef struct zero_rms_plan {
+    int64_t rows, dim;
+    int64_t x_stride, y_stride;
+    int64_t scale_cols;          /* ceil(dim / block); 0 without 8-bit results */
+    int64_t workspace_bytes;     /* zero_rms_backward's workspace */
+    int64_t hbm_bytes_forward;   /* algorithmic HBM bytes, with a residual; with a block: q, else y */
+    int64_t hbm_bytes_backward;
+    int32_t dtype;               /* zero_dtype_t */
+    int32_t block;               /* 0: no 8-bit results */
+    int32_t blocks;              /* backward: row groups summed apart */
+    int32_t reserved;
+    int64_t reserved2;
+} zero_rms_plan_t;
+
+/* Host only.  strides 0: dim.  rows >= 0, 1 <= dim <= 2^20, strides >= dim.
+ * Errors: ZERO_EINVAL, ZERO_EUNSUPPORTED (rows or dim too large, another block). */
+zero_status_t zero_rms_plan(int64_t rows, int64_t dim, int32_t dtype, int64_t x_stride, int64_t y_stride, int32_t block,
+                            zero_rms_plan_t* out);
+/* residual NULL: h = x, and h must be NULL; else h is written.  weight NULL:
+ * ones.  y NULL or q NULL: not written (not both).  rstd NULL: not written.
+ * Asynchronous on `stream`.  Errors: ZERO_EINVAL (plan not made by
+ * zero_rms_plan, eps < 0 or NaN, q without a block), ZERO_ENOMEM, ZERO_EALIGN,
+ * ZERO_ECUDA. */
+zero_status_t zero_rms_forward(const zero_rms_plan_t* plan, const void* x, const void* residual, const void* weight,
+                               float eps, void* h, void* y, void* q, uint8_t* q_scale, float* rstd, void* stream);
+/* 8-bit results as bfloat16 values, exact (under 2^-133 cut to its subnormals). */
+zero_status_t zero_rms_values(const zero_rms_plan_t* plan, const void* q, const uint8_t* q_scale, void* values,
+                              void* stream);
+/* h and rstd as the forward pass had them.  dh NULL: 0.  dx, dweight NULL: not
+ * computed; dweight is overwritten, with zeros when there are no rows.
+ * workspace: plan->workspace_bytes, 16-byte aligned (may be NULL without
+ * dweight). */
+zero_status_t zero_rms_backward(const zero_rms_plan_t* plan, const void* dy, const void* dh, const void* h,
+                                const void* weight, const float* rstd, void* dx, void* dweight, void* workspace,
+                                void* stream);
+
 /* ---- softmax cross entropy over a large vocabulary ---------------------------
  * The loss of tokens' last hidden states x [tokens, hidden] against a weight
  * w [vocab, hidden] (a vocabulary projection, or a tied embedding), without
@@ -721,6 +781,29 @@ zero_status_t zero_adamw_check(const zero_adamw_plan_t* plan, const void* table,
  * when it is nonzero. */
 zero_status_t zero_adamw_step(const zero_adamw_plan_t* plan, const void* table, const zero_adamw_t* hp,
                               const uint32_t* skip, void* stream);
+/* The global norm of the list's gradients, norm = |grad_scale| sqrt(sum g^2),
+ * and the factor that clips them, as in the sharded step: min(1, max_norm /
+ * (norm + 1e-6)), 1 where max_norm <= 0.  norm: device memory, {norm, factor}.
+ * flag (may be NULL): what zero_adamw_check gives, in the same pass.  An infinite
+ * gradient makes norm +inf and the factor 0, a NaN both NaN: pass flag to the
+ * step.  Squares are summed in binary32 32 (binary32 gradients: 16) at a time,
+ * those sums in binary64; where binary32 overflows or underflows, all in
+ * binary64.  Equal lists give equal bits.  workspace: zero_adamw_norm_workspace
+ * bytes of device memory, 16-byte aligned, contents scratch.  Asynchronous.
+ * Errors: ZERO_EINVAL (grad_scale not finite, max_norm NaN), ZERO_ENOMEM,
+ * ZERO_EALIGN, ZERO_ECUDA. */
+zero_status_t zero_adamw_norm(const zero_adamw_plan_t* plan, const void* table, float grad_scale, float max_norm,
+                              float* norm, uint32_t* flag, void* workspace, void* stream);
+/* Host only. */
+zero_status_t zero_adamw_norm_workspace(const zero_adamw_plan_t* plan, int64_t* bytes);
+/* zero_adamw_step with every gradient times norm[1] besides, as zero_adamw_norm
+ * wrote it: g = grad * (norm[1] * grad_scale), the factors' product rounded once. */
+zero_status_t zero_adamw_step_clipped(const zero_adamw_plan_t* plan, const void* table, const zero_adamw_t* hp,
+                                      const float* norm, const uint32_t* skip, void* stream);
+/* The gradients themselves times norm[1], each rounded to the list's dtype, in
+ * place (norm[1] = 1 leaves them): for an optimizer that is not this one.  The
+ * list's grad pointers must be writable then. */
+zero_status_t zero_adamw_clip(const zero_adamw_plan_t* plan, const void* table, const float* norm, void* stream);
 /* 8-bit states: the stored m and r = sqrt(v) as bfloat16 values, exact (m of
  * scale bytes below 4, under 2^-122, cut to bfloat16's subnormals), in
  * the plan's flat order (flat_elems each, 16-byte aligned; the gaps between

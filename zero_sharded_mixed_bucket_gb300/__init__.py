@@ -30,9 +30,11 @@ __all__ = [
     "zero_step_begin", "zero_step_bucket", "zero_step_end", "zero_gather_layer", "zero_last_error",
     "zero_step_buckets", "zero_step_buckets_async",
     "zero_ln_plan_t", "zero_ln_plan", "zero_ln_forward", "zero_ln_backward",
+    "zero_rms_plan_t", "zero_rms_plan", "zero_rms_forward", "zero_rms_values", "zero_rms_backward",
     "zero_ce_plan_t", "zero_ce_plan", "zero_ce_forward", "zero_ce_backward", "zero_ce_status",
     "zero_adamw_tensor_t", "zero_adamw_plan_t", "zero_adamw_t", "adamw_tensor", "zero_adamw_plan",
     "zero_adamw_table_init", "zero_adamw_check", "zero_adamw_step", "zero_adamw_states",
+    "zero_adamw_norm", "zero_adamw_norm_workspace", "zero_adamw_step_clipped", "zero_adamw_clip",
     "zero_version", "zero_set_profile_events", "zero_fetch_schedule", "Fetcher", "DeviceBuffers", "ptr_array",
 ]
 
@@ -90,6 +92,12 @@ class zero_ln_plan_t(ctypes.Structure):
     _fields_ = [(n, c_i64) for n in ("rows", "dim", "x_stride", "y_stride", "workspace_bytes", "hbm_bytes_forward",
                                       "hbm_bytes_backward")] + \
                [("dtype", c_i32), ("blocks", c_i32), ("reserved", c_i64)]
+
+
+class zero_rms_plan_t(ctypes.Structure):
+    _fields_ = [("rows", c_i64), ("dim", c_i64), ("x_stride", c_i64), ("y_stride", c_i64), ("scale_cols", c_i64),
+                ("workspace_bytes", c_i64), ("hbm_bytes_forward", c_i64), ("hbm_bytes_backward", c_i64),
+                ("dtype", c_i32), ("block", c_i32), ("blocks", c_i32), ("reserved", c_i32), ("reserved2", c_i64)]
 
 
 class zero_ce_plan_t(ctypes.Structure):
@@ -163,6 +171,10 @@ def lib():
             "zero_ln_plan": [c_i64, c_i64, c_i32, c_i64, c_i64, P(zero_ln_plan_t)],
             "zero_ln_forward": [P(zero_ln_plan_t), c_vp, c_vp, c_vp, c_f, c_vp, c_vp, c_vp, c_vp],
             "zero_ln_backward": [P(zero_ln_plan_t)] + [c_vp] * 10,
+            "zero_rms_plan": [c_i64, c_i64, c_i32, c_i64, c_i64, c_i32, P(zero_rms_plan_t)],
+            "zero_rms_forward": [P(zero_rms_plan_t), c_vp, c_vp, c_vp, c_f] + [c_vp] * 6,
+            "zero_rms_values": [P(zero_rms_plan_t)] + [c_vp] * 4,
+            "zero_rms_backward": [P(zero_rms_plan_t)] + [c_vp] * 9,
             "zero_ce_plan": [c_i64, c_i64, c_i64, c_i32, c_i64, c_i64, c_i64, P(zero_ce_plan_t)],
             "zero_ce_forward": [P(zero_ce_plan_t)] + [c_vp] * 8,
             "zero_ce_backward": [P(zero_ce_plan_t)] + [c_vp] * 5 + [c_f] + [c_vp] * 4,
@@ -172,6 +184,10 @@ def lib():
             "zero_adamw_check": [P(zero_adamw_plan_t), c_vp, c_vp, c_vp],
             "zero_adamw_step": [P(zero_adamw_plan_t), c_vp, P(zero_adamw_t), c_vp, c_vp],
             "zero_adamw_states": [P(zero_adamw_plan_t), c_vp, c_vp, c_vp, c_vp],
+            "zero_adamw_norm": [P(zero_adamw_plan_t), c_vp, c_f, c_f, c_vp, c_vp, c_vp, c_vp],
+            "zero_adamw_norm_workspace": [P(zero_adamw_plan_t), P(c_i64)],
+            "zero_adamw_step_clipped": [P(zero_adamw_plan_t), c_vp, P(zero_adamw_t), c_vp, c_vp, c_vp],
+            "zero_adamw_clip": [P(zero_adamw_plan_t), c_vp, c_vp, c_vp],
             "zero_step_begin": [cfg, plan, bufs, adam, state, c_vp],
             "zero_step_bucket": [cfg, plan, bufs, adam, state, c_i64, P(c_vp), c_vp],
             "zero_step_end": [cfg, plan, bufs, adam, state, c_vp, res],
@@ -414,6 +430,34 @@ def zero_ln_backward(plan: zero_ln_plan_t, dy, x, weight, mean, rstd, dx=None, d
                                   _optr(dx), _optr(dweight), _optr(dbias), _optr(workspace), _stream(stream)))
 
 
+def zero_rms_plan(rows: int, dim: int, dtype: int = ZERO_FP16, x_stride: int = 0, y_stride: int = 0,
+                  block: int = 0) -> zero_rms_plan_t:
+    """Root-mean-square norm of `rows` rows of `dim` values; strides in values between rows (0: dim); block: values to a
+    scale of 8-bit results (0: none)."""
+    p = zero_rms_plan_t()
+    _check(lib().zero_rms_plan(rows, dim, dtype, x_stride, y_stride, block, ctypes.byref(p)))
+    return p
+
+
+def zero_rms_forward(plan: zero_rms_plan_t, x, residual, weight, eps: float, h, y, q=None, q_scale=None, rstd=None,
+                     stream=None):
+    """h = x + residual; y (and q with q_scale, in 8 bits) = norm of h's rows (pointers or tensors; residual and h, weight,
+    y or q, rstd may be None)."""
+    _check(lib().zero_rms_forward(ctypes.byref(plan), _optr(x), _optr(residual), _optr(weight), eps, _optr(h), _optr(y),
+                                  _optr(q), _optr(q_scale), _optr(rstd), _stream(stream)))
+
+
+def zero_rms_values(plan: zero_rms_plan_t, q, q_scale, values, stream=None):
+    """8-bit results as bfloat16 values."""
+    _check(lib().zero_rms_values(ctypes.byref(plan), _optr(q), _optr(q_scale), _optr(values), _stream(stream)))
+
+
+def zero_rms_backward(plan: zero_rms_plan_t, dy, dh, h, weight, rstd, dx=None, dweight=None, workspace=None, stream=None):
+    """Gradients of zero_rms_forward (dh: the stream's own, or None); those passed as None are not computed."""
+    _check(lib().zero_rms_backward(ctypes.byref(plan), _optr(dy), _optr(dh), _optr(h), _optr(weight), _optr(rstd),
+                                   _optr(dx), _optr(dweight), _optr(workspace), _stream(stream)))
+
+
 def zero_ce_plan(tokens: int, vocab: int, hidden: int, dtype: int = ZERO_FP16, x_stride: int = 0, w_stride: int = 0,
                  piece: int = 0) -> zero_ce_plan_t:
     """Cross entropy of `tokens` hidden states against a [vocab, hidden] weight; strides in values between rows."""
@@ -473,6 +517,32 @@ def zero_adamw_check(plan: zero_adamw_plan_t, table, flag, stream=None):
 def zero_adamw_step(plan: zero_adamw_plan_t, table, hp: zero_adamw_t, skip=None, stream=None):
     """One AdamW step of the whole list; skip: None, or a device flag that stops it when nonzero."""
     _check(lib().zero_adamw_step(ctypes.byref(plan), _optr(table), ctypes.byref(hp), _optr(skip), _stream(stream)))
+
+
+def zero_adamw_norm_workspace(plan: zero_adamw_plan_t) -> int:
+    """Bytes of zero_adamw_norm's workspace."""
+    n = c_i64()
+    _check(lib().zero_adamw_norm_workspace(ctypes.byref(plan), ctypes.byref(n)))
+    return n.value
+
+
+def zero_adamw_norm(plan: zero_adamw_plan_t, table, grad_scale: float, max_norm: float, norm, flag, workspace,
+                    stream=None):
+    """norm (two device floats) = {norm of the list's gradients, factor that clips it to max_norm}; flag: None, or as
+    zero_adamw_check."""
+    _check(lib().zero_adamw_norm(ctypes.byref(plan), _optr(table), grad_scale, max_norm, _optr(norm), _optr(flag),
+                                 _optr(workspace), _stream(stream)))
+
+
+def zero_adamw_step_clipped(plan: zero_adamw_plan_t, table, hp: zero_adamw_t, norm, skip=None, stream=None):
+    """zero_adamw_step with the gradients times norm[1] besides, as zero_adamw_norm wrote it."""
+    _check(lib().zero_adamw_step_clipped(ctypes.byref(plan), _optr(table), ctypes.byref(hp), _optr(norm), _optr(skip),
+                                         _stream(stream)))
+
+
+def zero_adamw_clip(plan: zero_adamw_plan_t, table, norm, stream=None):
+    """The list's gradients times norm[1], in place."""
+    _check(lib().zero_adamw_clip(ctypes.byref(plan), _optr(table), _optr(norm), _stream(stream)))
 
 
 def zero_adamw_states(plan: zero_adamw_plan_t, table, m, root_v, stream=None):

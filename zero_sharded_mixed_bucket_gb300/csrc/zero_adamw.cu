@@ -1,5 +1,6 @@
 // AdamW over a list of tensors: the plan, the list's table in device memory,
-// and the step with binary32 or 8-bit moments.
+// the step with binary32 or 8-bit moments, the gradients' global norm and
+// clipping.
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -209,9 +210,10 @@ using Bits = typename std::conditional<DT == kF32, uint32_t, uint16_t>::type;
 // bytes each, 6.8 TB/s, a device copy's rate.
 template <int DT>
 __global__ void __launch_bounds__(kAd32Threads) k_adamw32(const AdTable tab, const __grid_constant__ AdHP hp,
-                                                        const uint32_t* skip)
+                                                        const uint32_t* skip, const float* norm)
 {
     if (skip && *skip) return;
+    const float gs = norm ? __fmul_rn(norm[1], hp.gs) : hp.gs;
     constexpr int V = 4;
     __shared__ AdRec held;
     const AdRec& r = record_of(tab, held);
@@ -234,7 +236,7 @@ __global__ void __launch_bounds__(kAd32Threads) k_adamw32(const AdTable tab, con
 #pragma unroll
         for (int j = 0; j < V; j++) {
             w[j] = __fmul_rn(w[j], keep);
-            adam1(__fmul_rn(to_f32<DT>(g[j]), hp.gs), w[j], m[j], v[j], hp.a);
+            adam1(__fmul_rn(to_f32<DT>(g[j]), gs), w[j], m[j], v[j], hp.a);
             p[j] = (Bits<DT>)from_f32<DT>(w[j]);
         }
         st_any<V>(r.t.master + i, cnt, vec, w);
@@ -254,9 +256,10 @@ __global__ void __launch_bounds__(kAd32Threads) k_adamw32(const AdTable tab, con
 // moves (553).
 template <int DT>
 __global__ void __launch_bounds__(kAd8Threads, 32) k_adamw8(const AdTable tab, const __grid_constant__ AdHP hp,
-                                                           const uint32_t* skip)
+                                                           const uint32_t* skip, const float* norm)
 {
     if (skip && *skip) return;
+    const float gs = norm ? __fmul_rn(norm[1], hp.gs) : hp.gs;
     constexpr int V = 8;
     const AdRec& r = tab.rec[tab.chunk_tensor[blockIdx.x]];
     const zero_adamw_tensor_t& t = r.t;
@@ -295,7 +298,7 @@ __global__ void __launch_bounds__(kAd8Threads, 32) k_adamw8(const AdTable tab, c
         uint32_t most_m = 0, most_r = 0;
 #pragma unroll
         for (int j = 0; j < V; j++) {
-            const float gj = __fmul_rn(to_f32<DT>(g[j]), hp.gs);
+            const float gj = __fmul_rn(to_f32<DT>(g[j]), gs);
             m[j] = __fadd_rn(__fmul_rn(m[j], hp.a.b1), __fmul_rn(gj, hp.a.omb1));
             q[j] = __fsqrt_rn(__fadd_rn(__fmul_rn(__fmul_rn(q[j], q[j]), hp.a.b2), __fmul_rn(__fmul_rn(gj, gj), hp.a.omb2)));
             const float d = __fadd_rn(__fmul_rn(q[j], hp.root8), hp.a.eps);
@@ -414,6 +417,192 @@ __global__ void __launch_bounds__(kAd32Threads) k_adamw_check(const AdTable tab,
     if (__syncthreads_or((int)bad) && threadIdx.x == 0) *flag = 1u;
 }
 
+// ---- the gradients' norm --------------------------------------------------------------
+// sqrt(sum of g^2) over the list.  A block takes a run of consecutive chunks, whose
+// tensors' values lie side by side, so it streams; kNormUnroll 16-byte loads of a
+// thread are on their way at once.  A thread adds up the squares of a batch (32
+// 16-bit values, 16 of 32 bits) in binary32 and the batches in binary64: one
+// binary64 operation to a batch is out of the way of memory, one to a value is not
+// (GB300 has 2 of them a clock and SM, a fifth of what the values would need).  A
+// batch whose binary32 sum overflows, or is so small that squares may have
+// been cut off below 2^-126, is read again and summed in binary64 alone; so is one
+// that holds an infinity or a NaN, which is where those are counted.
+constexpr int kNormThreads = 256, kNormUnroll = 4;
+constexpr int64_t kNormBlocks = 152 * 8;              // all resident at once
+// Up to so many chunks one block does all and needs no second kernel.
+constexpr int64_t kNormAlone = 8;
+
+struct NormPart {
+    double sum;
+    uint64_t bad;                // a gradient is inf or NaN
+};
+
+struct NormOut {
+    NormPart* part;
+    float* norm;                 // {norm, factor}
+    uint32_t* flag;
+    double scale;                // |grad_scale|
+    double max_norm;             // 0: no clipping
+};
+
+template <int DT>
+__device__ __noinline__ double squares64(const Bits<DT>* p, int n, uint64_t& bad)
+{
+    double s = 0.0;
+    for (int j = 0; j < n; j++) {
+        const float g = to_f32<DT>(p[j]);
+        if (nonfinite32(__float_as_uint(g))) bad = 1;
+        s = fma((double)g, (double)g, s);
+    }
+    return s;
+}
+
+// The sum, and the factor that clips, as the sharded step has them.
+__device__ __forceinline__ void norm_out(const NormOut& o, double sum, uint64_t bad)
+{
+    const double norm = sqrt(sum) * o.scale;
+    o.norm[0] = (float)norm;
+    const double c = o.max_norm / (norm + 1e-6);
+    o.norm[1] = o.max_norm > 0.0 && !(c >= 1.0) ? (float)c : 1.0f;      // NaN of a NaN
+    if (o.flag) *o.flag = bad != 0;
+}
+
+// Sum over the block, in a fixed order, in thread 0.
+__device__ __forceinline__ NormPart norm_join(double sum, uint64_t bad)
+{
+    __shared__ double sh[kNormThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        sum += __shfl_down_sync(0xffffffffu, sum, o);
+    if (lane == 0) sh[warp] = sum;
+    const int any = __syncthreads_or(bad != 0);
+    NormPart r{0.0, (uint64_t)(any != 0)};
+    if (threadIdx.x == 0)
+        for (int k = 0; k < kNormThreads / 32; k++)
+            r.sum += sh[k];
+    return r;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kNormThreads, 8) k_adamw_norm(const AdTable tab, int64_t n_chunks,
+                                                                const __grid_constant__ NormOut out)
+{
+    constexpr int V = kVecOf<DT>, U = kNormUnroll, kBatch = kNormThreads * V;
+    allow_next_grid();
+    double sum = 0.0;
+    uint64_t bad = 0;
+    int64_t c = n_chunks * blockIdx.x / gridDim.x;
+    const int64_t end = n_chunks * (blockIdx.x + 1) / gridDim.x;
+    while (c < end) {
+        const AdRec& r = tab.rec[tab.chunk_tensor[c]];
+        const Bits<DT>* g = static_cast<const Bits<DT>*>(r.t.grad);
+        const int64_t numel = r.t.numel, first = r.first_chunk;
+        const int64_t stop = min(end, first + (numel + kChunk - 1) / kChunk);
+        const int64_t lo = (c - first) * kChunk, hi = min((stop - first) * kChunk, numel);
+        const bool vec = ((uintptr_t)g & 15u) == 0;
+        c = stop;
+        for (int64_t i0 = lo; i0 < hi; i0 += U * kBatch) {
+            const int64_t i = i0 + threadIdx.x * V;
+            float s = 0.0f;
+            uint32_t any = 0;
+            auto add = [&](const uint4& q) {
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    any |= w[k];
+                    if constexpr (DT == kF32) {
+                        s = fmaf(__uint_as_float(w[k]), __uint_as_float(w[k]), s);
+                    } else {
+                        const float2 f = to_f32x2<DT>(w[k]);
+                        s = fmaf(f.x, f.x, s);
+                        s = fmaf(f.y, f.y, s);
+                    }
+                }
+            };
+            if (vec && i0 + U * kBatch <= hi) {
+                uint4 q[U];
+#pragma unroll
+                for (int u = 0; u < U; u++)
+                    q[u] = *reinterpret_cast<const uint4*>(g + i + u * kBatch);
+#pragma unroll
+                for (int u = 0; u < U; u++)
+                    add(q[u]);
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    const int64_t left = hi - (i + u * kBatch);
+                    alignas(16) Bits<DT> x[V];
+                    const int cnt = left <= 0 ? 0 : left < V ? (int)left : V;
+                    if (vec && cnt == V) {
+                        *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(g + i + u * kBatch);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < V; j++)
+                            x[j] = j < cnt ? g[i + u * kBatch + j] : Bits<DT>(0);
+                    }
+                    add(*reinterpret_cast<const uint4*>(x));
+                }
+            }
+            any &= DT == kF32 ? 0x7fffffffu : 0x7fff7fffu;            // zeros of either sign
+            // 2^-80: what 32 squares below 2^-126 lost is nothing beside it
+            if (s >= 0x1p-80f && s < INFINITY) {
+                sum += (double)s;
+            } else if (any) {
+#pragma unroll 1
+                for (int u = 0; u < U; u++) {
+                    const int64_t left = hi - (i + u * kBatch);
+                    if (left > 0) sum += squares64<DT>(g + i + u * kBatch, left < V ? (int)left : V, bad);
+                }
+            }
+        }
+    }
+    const NormPart r = norm_join(sum, bad);
+    if (threadIdx.x) return;
+    if (gridDim.x == 1)
+        norm_out(out, r.sum, r.bad);
+    else
+        out.part[blockIdx.x] = r;
+}
+
+// One block: the blocks' sums, in a fixed order.
+__global__ void __launch_bounds__(kNormThreads) k_adamw_norm_join(int parts, const __grid_constant__ NormOut out)
+{
+    wait_prev_grid();
+    double sum = 0.0;
+    uint64_t bad = 0;
+    for (int k = threadIdx.x; k < parts; k += kNormThreads) {
+        sum += out.part[k].sum;
+        bad |= out.part[k].bad;
+    }
+    const NormPart r = norm_join(sum, bad);
+    if (threadIdx.x == 0) norm_out(out, r.sum, r.bad);
+}
+
+// Gradients times the factor, rounded to their type; nothing to do where it is 1.
+template <int DT>
+__global__ void __launch_bounds__(kAd32Threads) k_adamw_clip(const AdTable tab, const float* norm)
+{
+    const float factor = norm[1];
+    if (factor == 1.0f) return;
+    constexpr int V = kVecOf<DT>;
+    const AdRec& r = tab.rec[tab.chunk_tensor[blockIdx.x]];
+    const int64_t lo = ((int64_t)blockIdx.x - r.first_chunk) * kChunk;
+    const int64_t hi = min(lo + kChunk, r.t.numel);
+    Bits<DT>* grad = static_cast<Bits<DT>*>(const_cast<void*>(r.t.grad));
+    const bool vec = ((uintptr_t)grad & 15u) == 0;
+#pragma unroll 4
+    for (int64_t i = lo + threadIdx.x * V; i < hi; i += kAd32Threads * V) {
+        const int cnt = (int)min((int64_t)V, hi - i);
+        alignas(16) Bits<DT> g[V];
+        ld_any<V>(grad + i, cnt, vec, g);
+#pragma unroll
+        for (int j = 0; j < V; j++)
+            g[j] = (Bits<DT>)from_f32<DT>(__fmul_rn(to_f32<DT>(g[j]), factor));
+        st_any<V>(grad + i, cnt, vec, g);
+    }
+}
+
 // One warp: the tensors' places in the flat order and in the chunk order.
 __global__ void __launch_bounds__(32) k_adamw_places(AdRec* rec, int64_t n)
 {
@@ -483,6 +672,65 @@ zero_status_t check_adamw_plan(const zero_adamw_plan_t* p, const void* table)
     if (p->n_chunks && !table) return set_error(ZERO_ENOMEM, "AdamW table is NULL");
     if (!aligned_to(table, 16)) return set_error(ZERO_EALIGN, "AdamW table is not 16-byte aligned");
     return ZERO_OK;
+}
+
+// Blocks of the norm's kernel, a function of the list alone.
+int64_t norm_blocks(const zero_adamw_plan_t& p)
+{
+    return p.n_chunks <= kNormAlone ? 1 : p.n_chunks < kNormBlocks ? p.n_chunks : kNormBlocks;
+}
+
+// The step; norm: NULL, or device memory whose second value multiplies the gradients besides.
+zero_status_t adamw_step(const zero_adamw_plan_t* plan, const void* table, const zero_adamw_t* hp, const float* norm,
+                         const uint32_t* skip, void* stream)
+{
+    const zero_status_t st = check_adamw_plan(plan, table);
+    if (st != ZERO_OK) return st;
+    if (!hp) return set_error(ZERO_EINVAL, "zero_adamw_step: hyper-parameters are NULL");
+    if (hp->t < 1) return set_error(ZERO_EINVAL, "zero_adamw_step: t must be at least 1");
+    if (!(hp->beta1 >= 0.0f && hp->beta1 < 1.0f) || !(hp->beta2 >= 0.0f && hp->beta2 < 1.0f))
+        return set_error(ZERO_EINVAL, "zero_adamw_step: betas must be in [0, 1)");
+    if (!(hp->eps >= 0.0f) || !std::isfinite(hp->lr) || !std::isfinite(hp->grad_scale))
+        return set_error(ZERO_EINVAL, "zero_adamw_step: eps must be >= 0, lr and grad_scale finite");
+    if (!aligned_to(skip, 4)) return set_error(ZERO_EALIGN, "zero_adamw_step: skip is not 4-byte aligned");
+    if (plan->n_chunks == 0) return ZERO_OK;
+    AdHP h;
+    std::memset(&h, 0, sizeof h);
+    const double bc1 = 1.0 - std::pow((double)hp->beta1, (double)hp->t);
+    const double bc2 = 1.0 - std::pow((double)hp->beta2, (double)hp->t);
+    h.a.lr = hp->lr;
+    h.a.b1 = hp->beta1;
+    h.a.omb1 = 1.0f - hp->beta1;
+    h.a.b2 = hp->beta2;
+    h.a.omb2 = 1.0f - hp->beta2;
+    h.a.eps = hp->eps;
+    h.a.bc1 = (float)bc1;
+    h.a.bc2 = (float)bc2;
+    h.gs = hp->grad_scale;
+    h.step8 = (float)((double)hp->lr / bc1);
+    h.root8 = (float)(1.0 / std::sqrt(bc2));
+    h.mix = hp->seed + (uint32_t)hp->t * 0x510E527Fu;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const AdTable tab = table_of(table, plan->n_tensors);
+    const unsigned grid = (unsigned)plan->n_chunks;
+    const int dt = plan->dtype;
+    if (plan->state_bits == 32) {
+        if (dt == ZERO_FP32) k_adamw32<kF32><<<grid, kAd32Threads, 0, s>>>(tab, h, skip, norm);
+        else if (dt == ZERO_BF16) k_adamw32<kBF16><<<grid, kAd32Threads, 0, s>>>(tab, h, skip, norm);
+        else k_adamw32<kF16><<<grid, kAd32Threads, 0, s>>>(tab, h, skip, norm);
+    } else {
+        // a chunk's 16 blocks go to one warp, or in a short list to as many as fill
+        // the 152 x 32 warps resident at once (148 tensors of up to 8894 values, step
+        // and read-out: 17 us, with one warp 35; one of 1.7 million: 12 and 23)
+        unsigned share = 1;
+        while (share < kChunk / kQBlock && grid * share < 152u * 32u) share *= 2;
+        const dim3 grid8(grid, share);
+        if (dt == ZERO_FP32) k_adamw8<kF32><<<grid8, kAd8Threads, 0, s>>>(tab, h, skip, norm);
+        else if (dt == ZERO_BF16) k_adamw8<kBF16><<<grid8, kAd8Threads, 0, s>>>(tab, h, skip, norm);
+        else k_adamw8<kF16><<<grid8, kAd8Threads, 0, s>>>(tab, h, skip, norm);
+    }
+    const cudaError_t err = cudaGetLastError();
+    return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_adamw_step");
 }
 
 }  // namespace
@@ -592,53 +840,67 @@ zero_status_t zero_adamw_step(const zero_adamw_plan_t* plan, const void* table, 
                               const uint32_t* skip, void* stream)
 {
     NvtxRange range("zero_adamw_step");
+    return adamw_step(plan, table, hp, nullptr, skip, stream);
+}
+
+zero_status_t zero_adamw_step_clipped(const zero_adamw_plan_t* plan, const void* table, const zero_adamw_t* hp,
+                                      const float* norm, const uint32_t* skip, void* stream)
+{
+    NvtxRange range("zero_adamw_step_clipped");
+    if (!norm) return set_error(ZERO_ENOMEM, "zero_adamw_step_clipped: norm is NULL");
+    if (!aligned_to(norm, 4)) return set_error(ZERO_EALIGN, "zero_adamw_step_clipped: norm is not 4-byte aligned");
+    return adamw_step(plan, table, hp, norm, skip, stream);
+}
+
+zero_status_t zero_adamw_norm_workspace(const zero_adamw_plan_t* plan, int64_t* bytes)
+{
+    if (!plan) return set_error(ZERO_EINVAL, "AdamW plan is NULL");
+    if (!bytes) return set_error(ZERO_EINVAL, "zero_adamw_norm_workspace: bytes is NULL");
+    if (plan->mark != mark_of(*plan)) return set_error(ZERO_EINVAL, "AdamW plan was not made by zero_adamw_plan");
+    *bytes = norm_blocks(*plan) * (int64_t)sizeof(NormPart);
+    return ZERO_OK;
+}
+
+zero_status_t zero_adamw_norm(const zero_adamw_plan_t* plan, const void* table, float grad_scale, float max_norm,
+                              float* norm, uint32_t* flag, void* workspace, void* stream)
+{
+    NvtxRange range("zero_adamw_norm");
     const zero_status_t st = check_adamw_plan(plan, table);
     if (st != ZERO_OK) return st;
-    if (!hp) return set_error(ZERO_EINVAL, "zero_adamw_step: hyper-parameters are NULL");
-    if (hp->t < 1) return set_error(ZERO_EINVAL, "zero_adamw_step: t must be at least 1");
-    if (!(hp->beta1 >= 0.0f && hp->beta1 < 1.0f) || !(hp->beta2 >= 0.0f && hp->beta2 < 1.0f))
-        return set_error(ZERO_EINVAL, "zero_adamw_step: betas must be in [0, 1)");
-    if (!(hp->eps >= 0.0f) || !std::isfinite(hp->lr) || !std::isfinite(hp->grad_scale))
-        return set_error(ZERO_EINVAL, "zero_adamw_step: eps must be >= 0, lr and grad_scale finite");
-    if (!aligned_to(skip, 4)) return set_error(ZERO_EALIGN, "zero_adamw_step: skip is not 4-byte aligned");
+    if (!std::isfinite(grad_scale)) return set_error(ZERO_EINVAL, "zero_adamw_norm: grad_scale is not finite");
+    if (std::isnan(max_norm)) return set_error(ZERO_EINVAL, "zero_adamw_norm: max_norm is NaN");
+    if (!norm || !workspace) return set_error(ZERO_ENOMEM, "zero_adamw_norm: norm or workspace is NULL");
+    if (!aligned_to(norm, 4) || !aligned_to(flag, 4) || !aligned_to(workspace, 16))
+        return set_error(ZERO_EALIGN, "zero_adamw_norm: norm and flag must be 4-byte aligned, workspace 16-byte");
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const AdTable tab = table_of(table, plan->n_tensors);
+    const NormOut o{static_cast<NormPart*>(workspace), norm, flag, std::fabs((double)grad_scale),
+                    max_norm > 0.0f ? (double)max_norm : 0.0};
+    const unsigned grid = (unsigned)norm_blocks(*plan);
+    if (plan->dtype == ZERO_FP32) k_adamw_norm<kF32><<<grid, kNormThreads, 0, s>>>(tab, plan->n_chunks, o);
+    else if (plan->dtype == ZERO_BF16) k_adamw_norm<kBF16><<<grid, kNormThreads, 0, s>>>(tab, plan->n_chunks, o);
+    else k_adamw_norm<kF16><<<grid, kNormThreads, 0, s>>>(tab, plan->n_chunks, o);
+    cudaError_t err = cudaGetLastError();
+    if (err == cudaSuccess && grid > 1) err = launch_kernel(k_adamw_norm_join, 1, kNormThreads, s, true, (int)grid, o);
+    return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_adamw_norm");
+}
+
+zero_status_t zero_adamw_clip(const zero_adamw_plan_t* plan, const void* table, const float* norm, void* stream)
+{
+    NvtxRange range("zero_adamw_clip");
+    const zero_status_t st = check_adamw_plan(plan, table);
+    if (st != ZERO_OK) return st;
+    if (!norm) return set_error(ZERO_ENOMEM, "zero_adamw_clip: norm is NULL");
+    if (!aligned_to(norm, 4)) return set_error(ZERO_EALIGN, "zero_adamw_clip: norm is not 4-byte aligned");
     if (plan->n_chunks == 0) return ZERO_OK;
-    AdHP h;
-    std::memset(&h, 0, sizeof h);
-    const double bc1 = 1.0 - std::pow((double)hp->beta1, (double)hp->t);
-    const double bc2 = 1.0 - std::pow((double)hp->beta2, (double)hp->t);
-    h.a.lr = hp->lr;
-    h.a.b1 = hp->beta1;
-    h.a.omb1 = 1.0f - hp->beta1;
-    h.a.b2 = hp->beta2;
-    h.a.omb2 = 1.0f - hp->beta2;
-    h.a.eps = hp->eps;
-    h.a.bc1 = (float)bc1;
-    h.a.bc2 = (float)bc2;
-    h.gs = hp->grad_scale;
-    h.step8 = (float)((double)hp->lr / bc1);
-    h.root8 = (float)(1.0 / std::sqrt(bc2));
-    h.mix = hp->seed + (uint32_t)hp->t * 0x510E527Fu;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const AdTable tab = table_of(table, plan->n_tensors);
     const unsigned grid = (unsigned)plan->n_chunks;
-    const int dt = plan->dtype;
-    if (plan->state_bits == 32) {
-        if (dt == ZERO_FP32) k_adamw32<kF32><<<grid, kAd32Threads, 0, s>>>(tab, h, skip);
-        else if (dt == ZERO_BF16) k_adamw32<kBF16><<<grid, kAd32Threads, 0, s>>>(tab, h, skip);
-        else k_adamw32<kF16><<<grid, kAd32Threads, 0, s>>>(tab, h, skip);
-    } else {
-        // a chunk's 16 blocks go to one warp, or in a short list to as many as fill
-        // the 152 x 32 warps resident at once (148 tensors of up to 8894 values, step
-        // and read-out: 17 us, with one warp 35; one of 1.7 million: 12 and 23)
-        unsigned share = 1;
-        while (share < kChunk / kQBlock && grid * share < 152u * 32u) share *= 2;
-        const dim3 grid8(grid, share);
-        if (dt == ZERO_FP32) k_adamw8<kF32><<<grid8, kAd8Threads, 0, s>>>(tab, h, skip);
-        else if (dt == ZERO_BF16) k_adamw8<kBF16><<<grid8, kAd8Threads, 0, s>>>(tab, h, skip);
-        else k_adamw8<kF16><<<grid8, kAd8Threads, 0, s>>>(tab, h, skip);
-    }
+    if (plan->dtype == ZERO_FP32) k_adamw_clip<kF32><<<grid, kAd32Threads, 0, s>>>(tab, norm);
+    else if (plan->dtype == ZERO_BF16) k_adamw_clip<kBF16><<<grid, kAd32Threads, 0, s>>>(tab, norm);
+    else k_adamw_clip<kF16><<<grid, kAd32Threads, 0, s>>>(tab, norm);
     const cudaError_t err = cudaGetLastError();
-    return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_adamw_step");
+    return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_adamw_clip");
 }
 
 zero_status_t zero_adamw_states(const zero_adamw_plan_t* plan, const void* table, void* m, void* root_v, void* stream)

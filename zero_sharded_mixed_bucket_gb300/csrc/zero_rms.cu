@@ -1,0 +1,1068 @@
+// Root-mean-square norm of rows with the residual's addition: the plan, the
+// forward kernels (results in the rows' type, or in 8 bits with a scale per
+// block), the read-out of 8-bit results, and the backward pass.
+#include <cuda_fp8.h>
+
+#include <cmath>
+#include <cstdio>
+#include <cstring>
+
+#include "dev_rows.cuh"
+#include "nvtx_ranges.h"
+
+namespace zg {
+
+using namespace rows;
+
+namespace {
+
+struct RmsArgs {
+    const void* x;               // forward: a block's output; backward: h
+    const void* r;               // forward: the stream; backward: the stream's own gradient (either may be NULL)
+    const void* dy;
+    const void* weight;
+    const float* rstd_in;
+    void* h;
+    void* y;
+    uint8_t* q;
+    uint8_t* q_scale;
+    float* rstd;
+    void* dx;
+    float* part;                 // [blocks][dim]: partial dweight
+    int64_t rows, dim, x_stride, y_stride, scale_cols;
+    float eps;
+    int warps;                   // of a group
+    int take;                    // rows of a batch, up to the kernel's RB
+    int block;                   // values to a scale
+    int q_wide;                  // a vector's codes are stored at once
+};
+
+// ---- 8-bit results ------------------------------------------------------------------------
+// Codes are e4m3 (448 the largest), a block's scale 2^(e - 127) the least power of
+// two that keeps its largest magnitude within 448.  A power of two scales
+// exactly, so each value is rounded once.  A block with an infinity or a NaN:
+// scale byte 255, NaN codes.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t most)
+{
+    if (most >= 0x7f800000u) return 255u;
+    const int e = (int)(most >> 23) - 8 + ((most & 0x7fffffu) > 0x600000u);
+    return (uint32_t)max(e, 0);
+}
+
+// 2^(127 - e), NaN for 255.
+__device__ __forceinline__ float scale_up(uint32_t e) { return __uint_as_float(e == 255u ? 0x7fffffffu : (254u - e) << 23); }
+
+__device__ __forceinline__ uint32_t codes2(float a, float b)
+{
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ uint32_t code1(float a) { return codes2(a, 0.0f) & 0xffu; }
+
+// 2^(e - 127), NaN for 255.
+__device__ __forceinline__ float scale_of(uint32_t e)
+{
+    return __uint_as_float(e == 255u ? 0x7fffffffu : e ? e << 23 : 0x00400000u);
+}
+
+__device__ __forceinline__ float2 values2(uint32_t codes)
+{
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+__device__ __forceinline__ uint32_t magnitude(float f) { return __float_as_uint(f) & 0x7fffffffu; }
+
+// ---- rows on 16-byte (or 4-byte) boundaries ---------------------------------------------
+// Dealt out as layer norm's: a group of lanes to a row, V vectors to a lane,
+// `take` rows (RB at most) at a time, copied ahead into per-lane slots.  The sum
+// x + r is rounded to the rows' type first (what the stream holds, and what
+// backward sees), then kept in registers; its slot is free for the next copy
+// before the group has its sum.  Q: 8-bit results besides; a block of 128 (32)
+// values is then 128 / VE neighbouring lanes of a warp.
+template <int DT, int L, int V, int RB, int S, int T, int BLOCKS, bool RAGGED, int ALIGN, bool Q>
+__global__ void __launch_bounds__(T, BLOCKS) k_rms_forward_rows(const __grid_constant__ RmsArgs a)
+{
+    static_assert(!Q || L == 32, "blocks of values lie inside a warp");
+    constexpr int VE = kVecOf<DT>, E = DT == kF32 ? 4 : 2;
+    extern __shared__ uint4 slots[];                  // [S][RB * V][x, r][T]
+    __shared__ float sh[2 * (T / 32) * RB];
+    const int lanes = L < 32 ? L : 32 * a.warps, gl = threadIdx.x % lanes, group = threadIdx.x / lanes;
+    const int groups = blockDim.x / lanes;
+    const float inv = 1.0f / (float)a.dim;
+    int turn = 0;
+    int cnt[V];
+#pragma unroll
+    for (int v = 0; v < V; v++)
+        cnt[v] = vec_count<DT>(a.dim, v, gl, lanes);
+    const int64_t stride = (int64_t)gridDim.x * groups * a.take;
+    int64_t r0 = ((int64_t)blockIdx.x * groups + group) * a.take;
+    int64_t ahead = r0;
+    const int64_t x_row = a.x_stride * E, y_row = a.y_stride * E;
+    const int apart = lanes * 16;                     // bytes between a lane's vectors
+    const char* sx = static_cast<const char*>(a.x) + r0 * x_row + gl * 16;
+    const char* sr = static_cast<const char*>(a.r) + r0 * x_row + gl * 16;
+    const bool add = a.r != nullptr;
+    uint4* const mine = slots + threadIdx.x;
+    auto fetch = [&](uint4* at) {
+        const int here = rows_here(a.rows, ahead, a.take);
+        const char *px = sx, *pr = sr;
+#pragma unroll
+        for (int b = 0; b < RB; b++, px += x_row, pr += x_row)
+            if (b < here)
+#pragma unroll
+                for (int v = 0; v < V; v++)
+                    if (cnt[v]) {
+                        uint4* p = at + (b * V + v) * 2 * T;
+                        vec_ahead<ALIGN>(p, px + v * apart, RAGGED ? cnt[v] * E : 16);
+                        if (add) vec_ahead<ALIGN>(p + T, pr + v * apart, RAGGED ? cnt[v] * E : 16);
+                    }
+        copies_issued();
+        ahead += stride;
+        sx += stride * x_row;
+        sr += stride * x_row;
+    };
+#pragma unroll
+    for (int k = 0; k < S * RB * V * 2; k++)          // vectors past the row's end are never copied: 0
+        if (cnt[k / 2 % V] == 0) mine[k * T] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < S; k++)
+        fetch(mine + k * RB * V * 2 * T);
+    // groups of less than a warp go round together: their sums shuffle across the warp
+    const int64_t first = L < 32 ? r0 - (int64_t)((threadIdx.x & 31) / L) * a.take : r0;
+    int slot = 0;
+    for (int64_t rw = first; rw < a.rows; rw += stride) {
+        copies_wait<S - 1>();
+        uint4* const q = mine + slot * RB * V * 2 * T;    // rows past the end: whatever is there, not written
+        const int here = rows_here(a.rows, r0, a.take);
+        Vals<DT> h[RB][V];
+        float ss[RB];
+#pragma unroll
+        for (int b = 0; b < RB; b++) {
+            ss[b] = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; v++) {
+                h[b][v] = from_slot<DT>(q + (b * V + v) * 2 * T);
+                float f[VE];
+                unpack<DT>(h[b][v], f);
+                if (add) {
+                    float g[VE];
+                    unpack<DT>(from_slot<DT>(q + ((b * V + v) * 2 + 1) * T), g);
+#pragma unroll
+                    for (int k = 0; k < VE; k++)
+                        f[k] += g[k];
+                    h[b][v] = pack<DT>(f);
+                    unpack<DT>(h[b][v], f);
+                }
+#pragma unroll
+                for (int k = 0; k < VE; k++)
+                    ss[b] = fmaf(f[k], f[k], ss[b]);
+            }
+        }
+        fetch(q);
+        slot = slot == S - 1 ? 0 : slot + 1;
+        if (a.h) {
+            char* p = static_cast<char*>(a.h) + r0 * x_row + gl * 16;
+#pragma unroll
+            for (int b = 0; b < RB; b++, p += x_row)
+#pragma unroll
+                for (int v = 0; v < V; v++)
+                    if (b < here && cnt[v]) store_vec<DT, RAGGED, ALIGN>(p + v * apart, h[b][v], cnt[v]);
+        }
+        group_sum<L, RB, T>(ss, a.warps, sh, turn, [&](float t) { return rsqrtf(fmaf(t, inv, a.eps)); });
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            if (!Q && cnt[v] == 0) continue;
+            const int64_t j = (int64_t)(v * lanes + gl) * VE;
+            float w[VE];
+            if (cnt[v]) weight_vec<DT, RAGGED>(a.weight, j, cnt[v], 1.0f, w);
+            char* p = static_cast<char*>(a.y) + r0 * y_row + gl * 16 + v * apart;
+#pragma unroll
+            for (int b = 0; b < RB; b++, p += y_row) {
+                float f[VE];
+                unpack<DT>(h[b][v], f);
+#pragma unroll
+                for (int k = 0; k < VE; k++)
+                    f[k] = cnt[v] && (!RAGGED || k < cnt[v]) ? f[k] * ss[b] * w[k] : 0.0f;
+                if (a.y && b < here && cnt[v]) store_vec<DT, RAGGED, ALIGN>(p, pack<DT>(f), cnt[v]);
+                if constexpr (Q) {
+                    uint32_t most = 0;
+#pragma unroll
+                    for (int k = 0; k < VE; k++)
+                        most = max(most, magnitude(f[k]));
+                    const int span = a.block / VE;    // lanes of a block
+                    for (int o = 1; o < span; o <<= 1)
+                        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+                    if (b < here && cnt[v]) {
+                        const uint32_t e = scale_byte(most);
+                        const float up = scale_up(e);
+                        uint32_t c[VE / 4];
+#pragma unroll
+                        for (int k = 0; k < VE / 4; k++)
+                            c[k] = codes2(f[4 * k] * up, f[4 * k + 1] * up) | codes2(f[4 * k + 2] * up, f[4 * k + 3] * up) << 16;
+                        uint8_t* at = a.q + (r0 + b) * a.y_stride + j;
+                        if (a.q_wide && (!RAGGED || cnt[v] == VE)) {
+                            if constexpr (VE == 8)
+                                __stcs(reinterpret_cast<uint2*>(at), make_uint2(c[0], c[1]));
+                            else
+                                __stcs(reinterpret_cast<uint32_t*>(at), c[0]);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < VE; k++)
+                                if (k < cnt[v]) at[k] = (uint8_t)(c[k >> 2] >> (8 * (k & 3)));
+                        }
+                        if ((threadIdx.x & (span - 1)) == 0) a.q_scale[(r0 + b) * a.scale_cols + j / a.block] = (uint8_t)e;
+                    }
+                }
+            }
+        }
+        if (gl == 0 && a.rstd) {
+#pragma unroll
+            for (int b = 0; b < RB; b++)
+                if (b < here) a.rstd[r0 + b] = ss[b];
+        }
+        r0 += stride;
+    }
+    copies_wait<0>();
+}
+
+// Backward: the stream's gradient of the rows, and the column sums of dy * xhat
+// over all the rows of a lane in registers, so h and dy are read once for both.
+// A block writes one partial sum per column (its groups joined in group order).
+template <int DT, int L, int V, int RB, int S, int T, int BLOCKS, bool RAGGED, int ALIGN>
+__global__ void __launch_bounds__(T, BLOCKS) k_rms_backward_rows(const __grid_constant__ RmsArgs a)
+{
+    constexpr int VE = kVecOf<DT>, E = DT == kF32 ? 4 : 2;
+    extern __shared__ uint4 slots[];                  // [S][RB * V][h, dy, r][T]; at the end the groups' sums
+    __shared__ float sh[2 * (T / 32) * RB];
+    const int lanes = L < 32 ? L : 32 * a.warps, gl = threadIdx.x % lanes, group = threadIdx.x / lanes;
+    const int groups = blockDim.x / lanes;
+    const float inv = 1.0f / (float)a.dim;
+    int turn = 0;
+    int cnt[V];
+    float dw[V][VE];
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+        cnt[v] = vec_count<DT>(a.dim, v, gl, lanes);
+#pragma unroll
+        for (int k = 0; k < VE; k++)
+            dw[v][k] = 0.0f;
+    }
+    const int64_t stride = (int64_t)gridDim.x * groups * a.take;
+    int64_t r0 = ((int64_t)blockIdx.x * groups + group) * a.take;
+    int64_t ahead = r0;
+    const int64_t x_row = a.x_stride * E, y_row = a.y_stride * E;
+    const int apart = lanes * 16;
+    const char* sx = static_cast<const char*>(a.x) + r0 * x_row + gl * 16;
+    const char* sr = static_cast<const char*>(a.r) + r0 * x_row + gl * 16;
+    const char* sy = static_cast<const char*>(a.dy) + r0 * y_row + gl * 16;
+    const bool add = a.r != nullptr;
+    uint4* const mine = slots + threadIdx.x;
+    auto fetch = [&](uint4* at) {
+        const int here = rows_here(a.rows, ahead, a.take);
+        const char *px = sx, *py = sy, *pr = sr;
+#pragma unroll
+        for (int b = 0; b < RB; b++, px += x_row, py += y_row, pr += x_row)
+#pragma unroll
+            for (int v = 0; v < V; v++) {
+                uint4* p = at + (b * V + v) * 3 * T;
+                if (b < here) {
+                    if (cnt[v]) {
+                        vec_ahead<ALIGN>(p, px + v * apart, RAGGED ? cnt[v] * E : 16);
+                        vec_ahead<ALIGN>(p + T, py + v * apart, RAGGED ? cnt[v] * E : 16);
+                        if (add) vec_ahead<ALIGN>(p + 2 * T, pr + v * apart, RAGGED ? cnt[v] * E : 16);
+                    }
+                } else {                              // rows past the end: all 0
+                    p[0] = p[T] = make_uint4(0, 0, 0, 0);
+                }
+            }
+        copies_issued();
+        ahead += stride;
+        sx += stride * x_row;
+        sy += stride * y_row;
+        sr += stride * x_row;
+    };
+    float next[RB];
+    auto fetch_stats = [&](int64_t from) {
+        const int here = rows_here(a.rows, from, a.take);
+#pragma unroll
+        for (int b = 0; b < RB; b++)
+            next[b] = b < here ? a.rstd_in[from + b] : 0.0f;
+    };
+#pragma unroll
+    for (int k = 0; k < S * RB * V * 3; k++)          // vectors past the row's end are never copied: 0
+        if (cnt[k / 3 % V] == 0) mine[k * T] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < S; k++)
+        fetch(mine + k * RB * V * 3 * T);
+    fetch_stats(r0);
+    const int64_t first = L < 32 ? r0 - (int64_t)((threadIdx.x & 31) / L) * a.take : r0;
+    int slot = 0;
+    for (int64_t rw = first; rw < a.rows; rw += stride) {
+        copies_wait<S - 1>();
+        uint4* const q = mine + slot * RB * V * 3 * T;
+        float rstd[RB], c[RB];
+#pragma unroll
+        for (int b = 0; b < RB; b++) {
+            rstd[b] = next[b];
+            c[b] = 0.0f;
+        }
+        fetch_stats(r0 + stride);
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            if (cnt[v] == 0) continue;
+            float w[VE];
+            weight_vec<DT, RAGGED>(a.weight, (int64_t)(v * lanes + gl) * VE, cnt[v], 1.0f, w);
+#pragma unroll
+            for (int b = 0; b < RB; b++) {
+                float xf[VE], yf[VE];
+                unpack<DT>(from_slot<DT>(q + (b * V + v) * 3 * T), xf);
+                unpack<DT>(from_slot<DT>(q + ((b * V + v) * 3 + 1) * T), yf);   // 0 past the ends
+#pragma unroll
+                for (int k = 0; k < VE; k++) {
+                    const float n = xf[k] * rstd[b];
+                    dw[v][k] = fmaf(yf[k], n, dw[v][k]);
+                    c[b] = fmaf(yf[k] * w[k], n, c[b]);
+                }
+            }
+        }
+        if (a.dx) {
+            group_sum<L, RB, T>(c, a.warps, sh, turn, [&](float t) { return t * -inv; });
+            const int here = rows_here(a.rows, r0, a.take);
+#pragma unroll
+            for (int v = 0; v < V; v++) {
+                if (cnt[v] == 0) continue;
+                float w[VE];
+                weight_vec<DT, RAGGED>(a.weight, (int64_t)(v * lanes + gl) * VE, cnt[v], 1.0f, w);
+                char* p = static_cast<char*>(a.dx) + r0 * x_row + gl * 16 + v * apart;
+#pragma unroll
+                for (int b = 0; b < RB; b++, p += x_row) {
+                    float xf[VE], yf[VE];
+                    unpack<DT>(from_slot<DT>(q + (b * V + v) * 3 * T), xf);
+                    unpack<DT>(from_slot<DT>(q + ((b * V + v) * 3 + 1) * T), yf);
+#pragma unroll
+                    for (int k = 0; k < VE; k++)
+                        xf[k] = fmaf(xf[k] * rstd[b], c[b], yf[k] * w[k]) * rstd[b];
+                    if (add) {
+                        unpack<DT>(from_slot<DT>(q + ((b * V + v) * 3 + 2) * T), yf);
+#pragma unroll
+                        for (int k = 0; k < VE; k++)
+                            xf[k] += yf[k];
+                    }
+                    if (b < here) store_vec<DT, RAGGED, ALIGN>(p, pack<DT>(xf), cnt[v]);
+                }
+            }
+        }
+        fetch(q);
+        slot = slot == S - 1 ? 0 : slot + 1;
+        r0 += stride;
+    }
+    copies_wait<0>();
+    if (!a.part) return;
+    float* pw = a.part + (int64_t)blockIdx.x * a.dim;
+    if (V == 1 && groups > 1) {
+        float* join = reinterpret_cast<float*>(slots);            // [group][VE][lanes]: no more than the slots
+        const int one = VE * lanes;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < VE; k++)
+            join[group * one + k * lanes + gl] = dw[0][k];
+        __syncthreads();
+        for (int t = threadIdx.x; t < one; t += blockDim.x) {
+            float s = 0.0f;
+            for (int g = 0; g < groups; g++)
+                s += join[g * one + t];
+            const int k = t / lanes;
+            const int64_t j = (int64_t)(t - k * lanes) * VE + k;
+            if (j < a.dim) pw[j] = s;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; v++)
+#pragma unroll
+            for (int k = 0; k < VE; k++)
+                if (k < cnt[v]) pw[(int64_t)(v * lanes + gl) * VE + k] = dw[v][k];
+    }
+}
+
+// ---- other rows ------------------------------------------------------------------------
+// One access a value.  A group of warps to a row, each warp blocks of 128
+// neighbouring values, four of a block to a lane, 32 apart: neighbouring lanes
+// neighbouring values, and a block's largest magnitude stays inside the warp.
+// Place of a lane's value k:
+__device__ __forceinline__ int place(int k, int warp, int warps, int lane)
+{
+    return ((k >> 2) * warps + warp) * 128 + (k & 3) * 32 + lane;
+}
+
+template <int DT, int K>
+__device__ __forceinline__ void ld_places(const void* p, int64_t at, int dim, int warp, int warps, int lane, float f[K])
+{
+    // loads without branches, so that all of them are on their way at once: past
+    // the row's end its first value again, dropped
+    const char* row = static_cast<const char*>(p) + at * (DT == kF32 ? 4 : 2);
+#pragma unroll
+    for (int k = 0; k < K; k++) {
+        const int j = place(k, warp, warps, lane);
+        f[k] = ld1<DT>(row, j < dim ? j : 0);
+    }
+#pragma unroll
+    for (int k = 0; k < K; k++)
+        if (place(k, warp, warps, lane) >= dim) f[k] = 0.0f;
+}
+
+// 8-bit results of a block of 128 values, f[k] at j0 + 32 k + lane.
+__device__ __forceinline__ void codes_out(const RmsArgs& a, int64_t row, int64_t j0, int lane, const float f[4])
+{
+    uint32_t most[4], e[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+        most[k] = j0 + 32 * k + lane < a.dim ? magnitude(f[k]) : 0u;
+    if (a.block == 128) {
+        e[0] = scale_byte(__reduce_max_sync(0xffffffffu, max(max(most[0], most[1]), max(most[2], most[3]))));
+        e[1] = e[2] = e[3] = e[0];
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            e[k] = scale_byte(__reduce_max_sync(0xffffffffu, most[k]));
+    }
+    uint8_t* at = a.q + row * a.y_stride;
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const int64_t j = j0 + 32 * k + lane;
+        if (j >= a.dim) break;
+        at[j] = (uint8_t)code1(f[k] * scale_up(e[k]));
+        if (j % a.block == 0) a.q_scale[row * a.scale_cols + j / a.block] = (uint8_t)e[k];
+    }
+}
+
+template <int DT, int K, int RB, int T>
+__global__ void __launch_bounds__(T, 512 / T) k_rms_forward_any(const __grid_constant__ RmsArgs a)
+{
+    __shared__ float sh[2 * (T / 32) * RB];
+    const int lane = threadIdx.x & 31, warps = a.warps, group = (int)(threadIdx.x >> 5) / warps, warp = (int)(threadIdx.x >> 5) % warps;
+    const int groups = blockDim.x / (32 * warps), dim = (int)a.dim;
+    const float inv = 1.0f / (float)a.dim;
+    int turn = 0;
+    const int64_t stride = (int64_t)gridDim.x * groups * a.take;
+    for (int64_t r0 = ((int64_t)blockIdx.x * groups + group) * a.take; r0 < a.rows; r0 += stride) {
+        const int rows = rows_here(a.rows, r0, a.take);
+        float f[RB][K], ss[RB];
+#pragma unroll
+        for (int b = 0; b < RB; b++) {
+            const int64_t at = (r0 + min(b, rows - 1)) * a.x_stride;         // past the end: not written
+            ld_places<DT, K>(a.x, at, dim, warp, warps, lane, f[b]);
+        }
+        if (a.r) {
+#pragma unroll
+            for (int b = 0; b < RB; b++) {
+                const int64_t at = (r0 + min(b, rows - 1)) * a.x_stride;
+                float g[K];
+                ld_places<DT, K>(a.r, at, dim, warp, warps, lane, g);
+#pragma unroll
+                for (int k = 0; k < K; k++)
+                    f[b][k] = to_f32<DT>(from_f32<DT>(f[b][k] + g[k]));
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < RB; b++) {
+            ss[b] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < K; k++)
+                ss[b] = fmaf(f[b][k], f[b][k], ss[b]);
+        }
+        if (a.h) {
+#pragma unroll
+            for (int b = 0; b < RB; b++)
+#pragma unroll
+                for (int k = 0; k < K; k++) {
+                    const int j = place(k, warp, warps, lane);
+                    if (b < rows && j < dim) st1<DT>(a.h, (r0 + b) * a.x_stride + j, f[b][k]);
+                }
+        }
+        group_sum<32, RB, T>(ss, warps, sh, turn, [&](float t) { return rsqrtf(fmaf(t, inv, a.eps)); });
+#pragma unroll
+        for (int k = 0; k < K; k++) {
+            const int j = place(k, warp, warps, lane);
+            const float w = !a.weight ? 1.0f : ld1<DT>(a.weight, j < dim ? j : 0);
+#pragma unroll
+            for (int b = 0; b < RB; b++) {
+                f[b][k] = f[b][k] * ss[b] * w;
+                if (a.y && b < rows && j < dim) st1<DT>(a.y, (r0 + b) * a.y_stride + j, f[b][k]);
+            }
+        }
+        if (a.q) {
+#pragma unroll
+            for (int b = 0; b < RB; b++)
+#pragma unroll
+                for (int k = 0; k < K; k += 4)
+                    if (b < rows) codes_out(a, r0 + b, ((k >> 2) * warps + warp) * 128, lane, f[b] + k);
+        }
+        if (lane == 0 && warp == 0 && a.rstd) {
+#pragma unroll
+            for (int b = 0; b < RB; b++)
+                if (b < rows) a.rstd[r0 + b] = ss[b];
+        }
+    }
+}
+
+template <int DT, int K, int T>
+__global__ void __launch_bounds__(T, 512 / T) k_rms_backward_any(const __grid_constant__ RmsArgs a)
+{
+    __shared__ float sh[2 * (T / 32)];
+    __shared__ float join[K <= 8 ? T * K : 1];        // [warp][K][32]
+    const int lane = threadIdx.x & 31, warps = a.warps, group = (int)(threadIdx.x >> 5) / warps, warp = (int)(threadIdx.x >> 5) % warps;
+    const int groups = blockDim.x / (32 * warps), dim = (int)a.dim;
+    const float inv = 1.0f / (float)a.dim;
+    int turn = 0;
+    float dw[K];
+#pragma unroll
+    for (int k = 0; k < K; k++)
+        dw[k] = 0.0f;
+    const int64_t stride = (int64_t)gridDim.x * groups;
+    for (int64_t row = (int64_t)blockIdx.x * groups + group; row < a.rows; row += stride) {
+        float n[K], g[K], c[1] = {0.0f};
+        ld_places<DT, K>(a.x, row * a.x_stride, dim, warp, warps, lane, n);
+        ld_places<DT, K>(a.dy, row * a.y_stride, dim, warp, warps, lane, g);
+        const float rstd = a.rstd_in[row];
+#pragma unroll
+        for (int k = 0; k < K; k++) {
+            n[k] *= rstd;                             // xhat; 0 past the end
+            dw[k] = fmaf(g[k], n[k], dw[k]);
+        }
+        if (!a.dx) continue;
+#pragma unroll
+        for (int k = 0; k < K; k++) {
+            const int j = place(k, warp, warps, lane);
+            if (a.weight) g[k] *= ld1<DT>(a.weight, j < dim ? j : 0);
+            c[0] = fmaf(g[k], n[k], c[0]);
+        }
+        group_sum<32, 1, T>(c, warps, sh, turn, [&](float t) { return t * -inv; });
+#pragma unroll
+        for (int k = 0; k < K; k++)
+            g[k] = fmaf(n[k], c[0], g[k]) * rstd;
+        if (a.r) {
+            ld_places<DT, K>(a.r, row * a.x_stride, dim, warp, warps, lane, n);
+#pragma unroll
+            for (int k = 0; k < K; k++)
+                g[k] += n[k];
+        }
+#pragma unroll
+        for (int k = 0; k < K; k++) {
+            const int j = place(k, warp, warps, lane);
+            if (j < dim) st1<DT>(a.dx, row * a.x_stride + j, g[k]);
+        }
+    }
+    if (!a.part) return;
+    float* pw = a.part + (int64_t)blockIdx.x * a.dim;
+    if (K <= 8 && groups > 1) {
+#pragma unroll
+        for (int k = 0; k < K; k++)
+            join[((threadIdx.x >> 5) * K + k) * 32 + lane] = dw[k];
+        __syncthreads();
+        for (int t = threadIdx.x; t < warps * K * 32; t += blockDim.x) {
+            const int w = t / (K * 32), k = t / 32 % K, j = place(k, w, warps, t % 32);
+            float s = 0.0f;
+            for (int g = 0; g < groups; g++)
+                s += join[((g * warps + w) * K + k) * 32 + t % 32];
+            if (j < dim) pw[j] = s;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; k++) {
+            const int j = place(k, warp, warps, lane);
+            if (j < dim) pw[j] = dw[k];
+        }
+    }
+}
+
+// ---- long rows -------------------------------------------------------------------------
+// A block per row, values read again for every use (from cache).  Warps take
+// blocks of 128 values in turn, so a thread reads of h what it wrote.
+constexpr int kLongThreads = 512;
+
+__device__ __forceinline__ float long_sum(float v, float* sh)
+{
+    v = warp_sum(v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float t = 0.0f;
+    for (int k = 0; k < kLongThreads / 32; k++)
+        t += sh[k];
+    return t;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kLongThreads) k_rms_forward_long(const __grid_constant__ RmsArgs a)
+{
+    __shared__ float sh[kLongThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float inv = 1.0f / (float)a.dim;
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        const int64_t xo = r * a.x_stride, yo = r * a.y_stride;
+        float ss = 0.0f;
+        for (int64_t j0 = warp * 128; j0 < a.dim; j0 += kLongThreads * 4)
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const int64_t j = j0 + 32 * k + lane;
+                if (j >= a.dim) continue;
+                float f = ld1<DT>(a.x, xo + j);
+                if (a.r) f = to_f32<DT>(from_f32<DT>(f + ld1<DT>(a.r, xo + j)));
+                if (a.h) st1<DT>(a.h, xo + j, f);
+                ss = fmaf(f, f, ss);
+            }
+        const float rstd = rsqrtf(fmaf(long_sum(ss, sh), inv, a.eps));
+        const void* h = a.h ? a.h : a.x;
+        for (int64_t j0 = warp * 128; j0 < a.dim; j0 += kLongThreads * 4) {
+            float f[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const int64_t j = j0 + 32 * k + lane;
+                if (j >= a.dim) {
+                    f[k] = 0.0f;
+                    continue;
+                }
+                f[k] = ld1<DT>(h, xo + j) * rstd * (a.weight ? ld1<DT>(a.weight, j) : 1.0f);
+                if (a.y) st1<DT>(a.y, yo + j, f[k]);
+            }
+            if (a.q) codes_out(a, r, j0, lane, f);
+        }
+        if (threadIdx.x == 0 && a.rstd) a.rstd[r] = rstd;
+    }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kLongThreads) k_rms_dx_long(const __grid_constant__ RmsArgs a)
+{
+    __shared__ float sh[kLongThreads / 32];
+    const float inv = 1.0f / (float)a.dim;
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        const int64_t xo = r * a.x_stride, yo = r * a.y_stride;
+        const float rstd = a.rstd_in[r];
+        float s = 0.0f;
+        for (int64_t j = threadIdx.x; j < a.dim; j += kLongThreads) {
+            const float g = ld1<DT>(a.dy, yo + j) * (a.weight ? ld1<DT>(a.weight, j) : 1.0f);
+            s = fmaf(g, ld1<DT>(a.x, xo + j) * rstd, s);
+        }
+        const float c = long_sum(s, sh) * -inv;
+        for (int64_t j = threadIdx.x; j < a.dim; j += kLongThreads) {
+            const float g = ld1<DT>(a.dy, yo + j) * (a.weight ? ld1<DT>(a.weight, j) : 1.0f);
+            float d = fmaf(ld1<DT>(a.x, xo + j) * rstd, c, g) * rstd;
+            if (a.r) d += ld1<DT>(a.r, xo + j);
+            st1<DT>(a.dx, xo + j, d);
+        }
+    }
+}
+
+// Column sums over the row group blockIdx.y: one thread a column.
+template <int DT>
+__global__ void __launch_bounds__(kRowThreads) k_rms_dw_part(const __grid_constant__ RmsArgs a)
+{
+    const int64_t j = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
+    if (j >= a.dim) return;
+    const int64_t G = gridDim.y, per = (a.rows + G - 1) / G;
+    const int64_t lo = min(blockIdx.y * per, a.rows), hi = min(lo + per, a.rows);
+    float dw = 0.0f;
+#pragma unroll 4
+    for (int64_t r = lo; r < hi; r++)
+        dw = fmaf(ld1<DT>(a.dy, r * a.y_stride + j), ld1<DT>(a.x, r * a.x_stride + j) * a.rstd_in[r], dw);
+    a.part[(int64_t)blockIdx.y * a.dim + j] = dw;
+}
+
+// The blocks' partial sums: 32 columns a block, its 32 warps a part of the
+// partial sums each, joined in warp order.
+template <int DT>
+__global__ void __launch_bounds__(1024) k_rms_dw_sum(const float* part, int blocks, int64_t dim, void* dw)
+{
+    wait_prev_grid();                                 // launched while the row kernel drains
+    __shared__ float sh[32][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t j = (int64_t)blockIdx.x * 32 + lane;
+    float s = 0.0f;
+    if (j < dim)
+#pragma unroll 10
+        for (int k = warp; k < blocks; k += 32)
+            s += part[(int64_t)k * dim + j];
+    sh[warp][lane] = s;
+    __syncthreads();
+    if (warp > 0 || j >= dim) return;
+    for (int k = 1; k < 32; k++)
+        s += sh[k][lane];
+    st1<DT>(dw, j, s);
+}
+
+// ---- read-out --------------------------------------------------------------------------
+// 8-bit results as bfloat16 values: 8 codes a thread where rows start on 8 bytes of
+// codes and 16 of values, else one.
+template <int N>
+__global__ void __launch_bounds__(256) k_rms_values(const __grid_constant__ RmsArgs a, uint16_t* out)
+{
+    const int64_t per = (a.dim + N - 1) / N;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.rows * per; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / per, j = (i - row * per) * N;
+        const uint8_t* src = a.q + row * a.y_stride + j;
+        uint16_t* dst = out + row * a.y_stride + j;
+        const float up = scale_of(a.q_scale[row * a.scale_cols + j / a.block]);
+        if (N == 8 && j + 8 <= a.dim) {
+            const uint2 c = __ldcs(reinterpret_cast<const uint2*>(src));
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const float2 f = values2((k < 2 ? c.x : c.y) >> (16 * (k & 1)) & 0xffffu);
+                w[k] = from_f32x2<kBF16>(f.x * up, f.y * up);
+            }
+            __stcs(reinterpret_cast<uint4*>(dst), make_uint4(w[0], w[1], w[2], w[3]));
+        } else {
+            for (int k = 0; k < N && j + k < a.dim; k++)
+                dst[k] = (uint16_t)from_f32<kBF16>(values2(src[k]).x * up);
+        }
+    }
+}
+
+// ---- host ---------------------------------------------------------------------------------
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+zero_status_t cuda_failed(cudaError_t e, const char* what)
+{
+    char msg[200];
+    std::snprintf(msg, sizeof msg, "%s: launch failed: %s", what, cudaGetErrorString(e));
+    return set_error(ZERO_ECUDA, msg);
+}
+
+zero_status_t check_rms_plan(const zero_rms_plan_t* p)
+{
+    if (!p) return set_error(ZERO_EINVAL, "root-mean-square norm plan is NULL");
+    zero_rms_plan_t fresh;
+    const zero_status_t st = zero_rms_plan(p->rows, p->dim, p->dtype, p->x_stride, p->y_stride, p->block, &fresh);
+    if (st != ZERO_OK) return st;
+    if (std::memcmp(&fresh, p, sizeof fresh) != 0)
+        return set_error(ZERO_EINVAL, "root-mean-square norm plan was not made by zero_rms_plan");
+    return ZERO_OK;
+}
+
+// Rows of a batch: RB where there are enough to keep `most` resident blocks busy,
+// else fewer, so that few rows spread over the SMs.
+int rows_of_batch(int64_t rows, int64_t groups, int64_t most, int RB)
+{
+    const int64_t each = (rows + groups * most - 1) / (groups * most);
+    return (int)(each < 1 ? 1 : each < RB ? each : RB);
+}
+
+int64_t blocks_for(int64_t rows, int64_t at_once, int64_t most)
+{
+    const int64_t need = (rows + at_once - 1) / at_once;
+    return need < most ? need : most;
+}
+
+cudaError_t launch_rms(void (*kernel)(const RmsArgs), const RmsArgs& a, int64_t blocks, int threads, size_t smem,
+                       cudaStream_t s)
+{
+    kernel<<<(unsigned)blocks, threads, smem, s>>>(a);
+    return cudaGetLastError();
+}
+
+// A row kernel; SMEM bytes of slots.
+template <void (*KERNEL)(const RmsArgs), size_t SMEM>
+cudaError_t launch_slots(const RmsArgs& a, int64_t blocks, int threads, cudaStream_t s)
+{
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem((const void*)KERNEL, (int)SMEM, done);
+    return e == cudaSuccess ? launch_rms(KERNEL, a, blocks, threads, SMEM, s) : e;
+}
+
+template <int DT, int L, int V, int RB, int S, int T, int BLOCKS>
+cudaError_t forward_rows(RmsArgs a, int64_t vecs, int align, cudaStream_t s)
+{
+    const RowShape h = shape_of(vecs, L, V, T);
+    a.warps = h.warps;
+    const int64_t most = (int64_t)kSms * (BLOCKS * T / h.threads);            // resident at once
+    a.take = rows_of_batch(a.rows, h.groups, most, RB);
+    const int64_t blocks = blocks_for(a.rows, (int64_t)h.groups * a.take, most);
+    constexpr size_t smem = (size_t)S * RB * V * 2 * T * 16;
+    if constexpr (L == 32) {                          // fewer lanes: whole rows on 16-byte boundaries only
+        if constexpr (DT != kF32)
+            if (align < 16)
+                return a.q ? launch_slots<k_rms_forward_rows<DT, L, V, RB, S, T, BLOCKS, true, 4, true>, smem>(a, blocks, h.threads, s)
+                           : launch_slots<k_rms_forward_rows<DT, L, V, RB, S, T, BLOCKS, true, 4, false>, smem>(a, blocks, h.threads, s);
+        if (a.dim % kVecOf<DT>)
+            return a.q ? launch_slots<k_rms_forward_rows<DT, L, V, RB, S, T, BLOCKS, true, 16, true>, smem>(a, blocks, h.threads, s)
+                       : launch_slots<k_rms_forward_rows<DT, L, V, RB, S, T, BLOCKS, true, 16, false>, smem>(a, blocks, h.threads, s);
+        if (a.q) return launch_slots<k_rms_forward_rows<DT, L, V, RB, S, T, BLOCKS, false, 16, true>, smem>(a, blocks, h.threads, s);
+    }
+    return launch_slots<k_rms_forward_rows<DT, L, V, RB, S, T, BLOCKS, false, 16, false>, smem>(a, blocks, h.threads, s);
+}
+
+// Warps to a row of 128-value blocks, K / 4 of them to a warp; groups and threads of a block.
+RowShape any_shape(int64_t dim, int K, int T)
+{
+    RowShape r;
+    r.warps = (int)((dim + 32 * K - 1) / (32 * K));
+    r.groups = T / 32 / r.warps;
+    r.threads = 32 * r.warps * r.groups;
+    return r;
+}
+
+template <int DT, int K, int RB, int T>
+cudaError_t forward_any(RmsArgs a, cudaStream_t s)
+{
+    const RowShape h = any_shape(a.dim, K, T);
+    a.warps = h.warps;
+    const int64_t most = (int64_t)kSms * (512 / h.threads);
+    a.take = rows_of_batch(a.rows, h.groups, most, RB);
+    return launch_rms(k_rms_forward_any<DT, K, RB, T>, a, blocks_for(a.rows, (int64_t)h.groups * a.take, most), h.threads, 0, s);
+}
+
+// align: 16, 4 or 0, the boundary that every row starts on (of 0: its type's).
+template <int DT>
+cudaError_t forward(const RmsArgs& a, int align, cudaStream_t s)
+{
+    constexpr int VE = kVecOf<DT>, T = kRowThreads;
+    const int64_t vecs = (a.dim + VE - 1) / VE;
+    const bool whole = a.dim % VE == 0 && align == 16 && !a.q;
+    if (whole && vecs <= 8) return forward_rows<DT, 8, 1, 4, 2, T, 3>(a, vecs, align, s);
+    if (whole && vecs <= 16) return forward_rows<DT, 16, 1, 4, 2, T, 3>(a, vecs, align, s);
+    if (align == 16 || (DT != kF32 && align == 4 && vecs > 64)) {
+        if (vecs <= 256) return forward_rows<DT, 32, 1, 4, 2, T, 3>(a, vecs, align, s);
+        if (vecs <= 512) return forward_rows<DT, 32, 2, 2, 2, T, 3>(a, vecs, align, s);
+        if (vecs <= 1024) return forward_rows<DT, 32, 4, 1, 2, T, 3>(a, vecs, align, s);
+        if (vecs <= 2048) return forward_rows<DT, 32, 8, 1, 1, T, 2>(a, vecs, align, s);
+        if (vecs <= 4096) return forward_rows<DT, 32, 8, 1, 1, 2 * T, 1>(a, vecs, align, s);
+    } else {
+        if (a.dim <= 128) return forward_any<DT, 4, 4, T>(a, s);
+        if (a.dim <= 2048) return forward_any<DT, 8, 4, T>(a, s);
+        if (a.dim <= 4096) return forward_any<DT, 16, 2, T>(a, s);
+        if (a.dim <= 8192) return forward_any<DT, 16, 1, 2 * T>(a, s);
+        if (a.dim <= 16384) return forward_any<DT, 32, 1, 2 * T>(a, s);
+    }
+    return launch_rms(k_rms_forward_long<DT>, a, a.rows < kSms * 4 ? a.rows : kSms * 4, kLongThreads, 0, s);
+}
+
+// How the backward pass deals out a row: lanes of a group, vectors of a lane,
+// threads and resident blocks, rows at a time.  The plan's blocks go by it
+// (as for rows on 16-byte boundaries) whatever the pointers turn out to be.
+struct BackwardShape {
+    int L, V, T, blocks, rows;
+};
+
+BackwardShape backward_shape(int64_t vecs, bool whole)
+{
+    const int L = whole && vecs <= 8 ? 8 : whole && vecs <= 16 ? 16 : 32;
+    if (vecs <= 256) return {L, 1, kRowThreads, 2, 4};
+    if (vecs <= 512) return {L, 2, kRowThreads, 2, 2};
+    if (vecs <= 1024) return {L, 4, kRowThreads, 2, 1};
+    return {L, 4, 2 * kRowThreads, 1, 1};
+}
+
+int64_t backward_most(const BackwardShape& b, const RowShape& h) { return (int64_t)kSms * (b.blocks * b.T / h.threads); }
+
+template <int DT, int L, int V, int RB, int T, int BLOCKS>
+cudaError_t backward_rows(RmsArgs a, int64_t vecs, int align, int blocks, cudaStream_t s)
+{
+    const RowShape h = shape_of(vecs, L, V, T);
+    a.warps = h.warps;
+    a.take = rows_of_batch(a.rows, h.groups, backward_most({L, V, T, BLOCKS, RB}, h), RB);
+    constexpr int S = 2;
+    constexpr size_t smem = (size_t)S * RB * V * 3 * T * 16;
+    if constexpr (L == 32) {
+        if constexpr (DT != kF32)
+            if (align < 16)
+                return launch_slots<k_rms_backward_rows<DT, L, V, RB, S, T, BLOCKS, true, 4>, smem>(a, blocks, h.threads, s);
+        if (a.dim % kVecOf<DT>)
+            return launch_slots<k_rms_backward_rows<DT, L, V, RB, S, T, BLOCKS, true, 16>, smem>(a, blocks, h.threads, s);
+    }
+    return launch_slots<k_rms_backward_rows<DT, L, V, RB, S, T, BLOCKS, false, 16>, smem>(a, blocks, h.threads, s);
+}
+
+// Blocks of the backward pass (the plan's): as many as are resident at once on
+// 152 SMs, and no more than have rows.
+int64_t backward_blocks(int64_t rows, int64_t vecs, bool whole)
+{
+    const BackwardShape b = backward_shape(vecs, whole);
+    const RowShape h = shape_of(vecs <= 2048 ? vecs : 2048, b.L, b.V, b.T);
+    const int64_t most = backward_most(b, h);
+    return blocks_for(rows, (int64_t)h.groups * rows_of_batch(rows, h.groups, most, b.rows), most);
+}
+
+template <int DT, int K, int T>
+cudaError_t backward_any(RmsArgs a, int blocks, cudaStream_t s)
+{
+    const RowShape h = any_shape(a.dim, K, T);
+    a.warps = h.warps;
+    return launch_rms(k_rms_backward_any<DT, K, T>, a, blocks, h.threads, 0, s);
+}
+
+template <int DT>
+cudaError_t backward(RmsArgs a, int align, int blocks, void* dw, cudaStream_t s)
+{
+    constexpr int VE = kVecOf<DT>, T = kRowThreads;
+    const int64_t vecs = (a.dim + VE - 1) / VE;
+    if (!dw) a.part = nullptr;
+    cudaError_t e = cudaSuccess;
+    if (blocks && vecs <= 2048 && (align == 16 || (DT != kF32 && align == 4 && vecs > 16))) {
+        const int L = align == 16 ? backward_shape(vecs, a.dim % VE == 0).L : 32;
+        if (L == 8) e = backward_rows<DT, 8, 1, 4, T, 2>(a, vecs, align, blocks, s);
+        else if (L == 16) e = backward_rows<DT, 16, 1, 4, T, 2>(a, vecs, align, blocks, s);
+        else if (vecs <= 256) e = backward_rows<DT, 32, 1, 4, T, 2>(a, vecs, align, blocks, s);
+        else if (vecs <= 512) e = backward_rows<DT, 32, 2, 2, T, 2>(a, vecs, align, blocks, s);
+        else if (vecs <= 1024) e = backward_rows<DT, 32, 4, 1, T, 2>(a, vecs, align, blocks, s);
+        else e = backward_rows<DT, 32, 4, 1, 2 * T, 1>(a, vecs, align, blocks, s);
+    } else if (blocks && align < 16 && a.dim <= 8192) {
+        if (a.dim <= 128) e = backward_any<DT, 4, T>(a, blocks, s);
+        else if (a.dim <= 2048) e = backward_any<DT, 8, T>(a, blocks, s);
+        else if (a.dim <= 4096) e = backward_any<DT, 16, T>(a, blocks, s);
+        else e = backward_any<DT, 16, 2 * T>(a, blocks, s);
+    } else {
+        if (a.dx && a.rows) e = launch_rms(k_rms_dx_long<DT>, a, a.rows < kSms * 4 ? a.rows : kSms * 4, kLongThreads, 0, s);
+        if (e == cudaSuccess && dw && blocks) {
+            const unsigned cols = (unsigned)((a.dim + kRowThreads - 1) / kRowThreads);
+            k_rms_dw_part<DT><<<dim3(cols, (unsigned)blocks), kRowThreads, 0, s>>>(a);
+            e = cudaGetLastError();
+        }
+    }
+    if (e == cudaSuccess && dw)
+        e = launch_kernel(k_rms_dw_sum<DT>, (int)((a.dim + 31) / 32), 1024, s, blocks > 0, (const float*)a.part, blocks,
+                          a.dim, dw);
+    return e;
+}
+
+// The boundary that every row of the given arrays starts on: 16, 4 or 0 bytes
+// (their type's).  A weight off 16-byte boundaries counts as 0.
+int rows_align(const zero_rms_plan_t& p, const void* weight, const void* const* arrays, int n)
+{
+    const uint64_t e = p.dtype == ZERO_FP32 ? 4 : 2;
+    uint64_t any = (uint64_t)p.x_stride * e | (uint64_t)p.y_stride * e;
+    for (int k = 0; k < n; k++)
+        any |= (uintptr_t)arrays[k];
+    if ((uintptr_t)weight % 16) return 0;
+    return any % 16 == 0 ? 16 : any % 4 == 0 ? 4 : 0;
+}
+
+RmsArgs args_of(const zero_rms_plan_t& p)
+{
+    RmsArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.rows = p.rows; a.dim = p.dim; a.x_stride = p.x_stride; a.y_stride = p.y_stride;
+    a.block = p.block; a.scale_cols = p.scale_cols;
+    return a;
+}
+
+}  // namespace
+}  // namespace zg
+
+using namespace zg;
+
+extern "C" {
+
+zero_status_t zero_rms_plan(int64_t rows, int64_t dim, int32_t dtype, int64_t x_stride, int64_t y_stride, int32_t block,
+                            zero_rms_plan_t* out)
+{
+    if (!out) return set_error(ZERO_EINVAL, "zero_rms_plan: out is NULL");
+    if (dtype != ZERO_FP16 && dtype != ZERO_BF16 && dtype != ZERO_FP32)
+        return set_error(ZERO_EINVAL, "zero_rms_plan: dtype unknown");
+    if (rows < 0 || dim < 1) return set_error(ZERO_EINVAL, "zero_rms_plan: rows must be >= 0 and dim >= 1");
+    if (block != 0 && block != 32 && block != 128)
+        return set_error(ZERO_EUNSUPPORTED, "zero_rms_plan: block must be 0, 32 or 128");
+    if (rows > (int64_t(1) << 40) || dim > (int64_t(1) << 20))
+        return set_error(ZERO_EUNSUPPORTED, "zero_rms_plan: rows exceed 2^40 or dim exceeds 2^20");
+    const int64_t xs = x_stride ? x_stride : dim, ys = y_stride ? y_stride : dim;
+    if (xs < dim || ys < dim || xs > (int64_t(1) << 40) || ys > (int64_t(1) << 40))
+        return set_error(ZERO_EINVAL, "zero_rms_plan: a stride is below dim or above 2^40");
+    if (rows && (xs > INT64_MAX / 32 / rows || ys > INT64_MAX / 32 / rows))   // 5 * 4 bytes of each below INT64_MAX
+        return set_error(ZERO_EUNSUPPORTED, "zero_rms_plan: the rows span too many bytes");
+    std::memset(out, 0, sizeof *out);
+    out->rows = rows;
+    out->dim = dim;
+    out->x_stride = xs;
+    out->y_stride = ys;
+    out->dtype = dtype;
+    out->block = block;
+    out->scale_cols = block ? (dim + block - 1) / block : 0;
+    const int64_t e = dtype == ZERO_FP32 ? 4 : 2;
+    out->blocks = (int32_t)backward_blocks(rows, (dim * e + 15) / 16, dim * e % 16 == 0);   // each adds up its rows' weight gradients
+    out->workspace_bytes = 16 + (int64_t)out->blocks * dim * 4;
+    out->hbm_bytes_forward = rows * (3 * dim * e + 4 + (block ? dim + out->scale_cols : dim * e)) + dim * e;
+    out->hbm_bytes_backward = rows * (4 * dim * e + 4) + 2 * dim * e;
+    return ZERO_OK;
+}
+
+zero_status_t zero_rms_forward(const zero_rms_plan_t* plan, const void* x, const void* residual, const void* weight,
+                               float eps, void* h, void* y, void* q, uint8_t* q_scale, float* rstd, void* stream)
+{
+    NvtxRange range("zero_rms_forward");
+    const zero_status_t st = check_rms_plan(plan);
+    if (st != ZERO_OK) return st;
+    if (!(eps >= 0.0f)) return set_error(ZERO_EINVAL, "zero_rms_forward: eps must be >= 0");
+    if (q && !plan->block) return set_error(ZERO_EINVAL, "zero_rms_forward: the plan has no block for 8-bit results");
+    if (h && !residual) return set_error(ZERO_EINVAL, "zero_rms_forward: h without a residual");
+    if (plan->rows == 0) return ZERO_OK;
+    if (!x || (!y && !q) || (residual && !h) || (q && !q_scale))
+        return set_error(ZERO_ENOMEM, "zero_rms_forward: x, both of y and q, h of a residual or q_scale of q is NULL");
+    const size_t e = plan->dtype == ZERO_FP32 ? 4 : 2;
+    if (!aligned_to(x, e) || !aligned_to(residual, e) || !aligned_to(weight, e) || !aligned_to(h, e) ||
+        !aligned_to(y, e) || !aligned_to(rstd, 4))
+        return set_error(ZERO_EALIGN, "zero_rms_forward: a pointer is not aligned to its type");
+    RmsArgs a = args_of(*plan);
+    a.x = x; a.r = residual; a.weight = weight; a.h = h; a.y = y; a.rstd = rstd; a.eps = eps;
+    a.q = static_cast<uint8_t*>(q);
+    a.q_scale = q_scale;
+    a.q_wide = aligned_to(q, 8) && plan->y_stride % 8 == 0;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const void* arrays[] = {x, residual, h, y};
+    const int align = rows_align(*plan, weight, arrays, 4);
+    const cudaError_t err = plan->dtype == ZERO_FP32   ? forward<kF32>(a, align, s)
+                            : plan->dtype == ZERO_BF16 ? forward<kBF16>(a, align, s)
+                                                       : forward<kF16>(a, align, s);
+    return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_rms_forward");
+}
+
+zero_status_t zero_rms_values(const zero_rms_plan_t* plan, const void* q, const uint8_t* q_scale, void* values, void* stream)
+{
+    NvtxRange range("zero_rms_values");
+    const zero_status_t st = check_rms_plan(plan);
+    if (st != ZERO_OK) return st;
+    if (!plan->block) return set_error(ZERO_EINVAL, "zero_rms_values: the plan has no block for 8-bit results");
+    if (plan->rows == 0) return ZERO_OK;
+    if (!q || !q_scale || !values) return set_error(ZERO_ENOMEM, "zero_rms_values: a buffer is NULL");
+    if (!aligned_to(values, 2)) return set_error(ZERO_EALIGN, "zero_rms_values: values is not aligned to its type");
+    RmsArgs a = args_of(*plan);
+    a.q = static_cast<uint8_t*>(const_cast<void*>(q));
+    a.q_scale = const_cast<uint8_t*>(q_scale);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool wide = aligned_to(q, 8) && aligned_to(values, 16) && plan->y_stride % 8 == 0;
+    const int64_t n = plan->rows * (wide ? (plan->dim + 7) / 8 : plan->dim), most = (int64_t)kSms * 8;
+    const unsigned grid = (unsigned)blocks_for(n, 256, most);
+    if (wide) k_rms_values<8><<<grid, 256, 0, s>>>(a, static_cast<uint16_t*>(values));
+    else k_rms_values<1><<<grid, 256, 0, s>>>(a, static_cast<uint16_t*>(values));
+    const cudaError_t err = cudaGetLastError();
+    return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_rms_values");
+}
+
+zero_status_t zero_rms_backward(const zero_rms_plan_t* plan, const void* dy, const void* dh, const void* h,
+                                const void* weight, const float* rstd, void* dx, void* dweight, void* workspace,
+                                void* stream)
+{
+    NvtxRange range("zero_rms_backward");
+    const zero_status_t st = check_rms_plan(plan);
+    if (st != ZERO_OK) return st;
+    if (plan->rows && (!dy || !h || !rstd)) return set_error(ZERO_ENOMEM, "zero_rms_backward: dy, h or rstd is NULL");
+    if (dweight && !workspace) return set_error(ZERO_ENOMEM, "zero_rms_backward: workspace is NULL");
+    const size_t e = plan->dtype == ZERO_FP32 ? 4 : 2;
+    if (!aligned_to(dy, e) || !aligned_to(dh, e) || !aligned_to(h, e) || !aligned_to(weight, e) || !aligned_to(dx, e) ||
+        !aligned_to(dweight, e) || !aligned_to(rstd, 4))
+        return set_error(ZERO_EALIGN, "zero_rms_backward: a pointer is not aligned to its type");
+    if (!aligned_to(workspace, 16)) return set_error(ZERO_EALIGN, "zero_rms_backward: workspace is not 16-byte aligned");
+    if (!dx && !dweight) return ZERO_OK;
+    RmsArgs a = args_of(*plan);
+    a.x = h; a.r = dx ? dh : nullptr; a.dy = dy; a.weight = weight; a.rstd_in = rstd; a.dx = dx;
+    a.part = static_cast<float*>(workspace) + 4;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const void* arrays[] = {dy, a.r, h, dx};
+    const int align = rows_align(*plan, weight, arrays, 4);
+    const cudaError_t err = plan->dtype == ZERO_FP32   ? backward<kF32>(a, align, plan->blocks, dweight, s)
+                            : plan->dtype == ZERO_BF16 ? backward<kBF16>(a, align, plan->blocks, dweight, s)
+                                                       : backward<kF16>(a, align, plan->blocks, dweight, s);
+    return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_rms_backward");
+}
+
+}  // extern "C"
