@@ -689,6 +689,64 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
  * are then NaN, so zero_adamw_check sees them too. */
 zero_status_t zero_ce_status(const zero_ce_plan_t* plan, const void* workspace, void* stream);
 
+/* ---- log probabilities over a large vocabulary ---------------------------------
+ * What a policy's update and a scored answer need of the last hidden states x
+ * [tokens, hidden] against a weight w [vocab, hidden], without the logits in
+ * memory (the products are cross entropy's):
+ *   z = x w^T * scale (scale: the inverse temperature);  lse_i = log sum_v exp z_iv
+ *   logp_i = z_i,t(i) - lse_i;  p = exp(z - lse);  entropy_i = -sum_v p_iv log p_iv
+ *   the `top` most likely entries, in falling order of their logits, the lower
+ *   index first where they are equal
+ *   G_iv = a_i ([v = t(i)] - p_iv) - b_i p_iv (log p_iv + entropy_i)
+ *   dx = scale * G w;  dw = scale * G^T x
+ * with a = dlogp * grad_scale and b = dentropy * grad_scale.  Types, strides,
+ * alignment, sums, statistics and the 16-bit G are as for cross entropy (G's rows
+ * are scaled by the largest |a_i| + 4 |b_i|); top_index has 8-byte alignment, other
+ * binary32 arrays 4-byte.  A token whose target is outside 0..vocab-1 has logp 0
+ * and no dlogp; its entropy, alternatives and dentropy are like any other's.
+ * Alternatives are logits above -infinity that are numbers; where there are fewer
+ * than `top`, log probability -infinity and index -1.  The order is that of the
+ * logits as computed: those closer than their binary32 sums' rounding may
+ * change places.  A row with a NaN logit or an infinite one has NaN logp and
+ * entropy.  Results do not depend on timing: equal calls give equal bits.
+ * 104 bytes. */
+typedef struct zero_lp_plan {
+    int64_t tokens, vocab, hidden;
+    int64_t x_stride, w_stride;  /* values between rows of x and dx, of w and dw */
+    int64_t piece;               /* vocabulary entries per piece of the backward pass, a multiple of 256 */
+    int64_t rows;                /* tokens per piece of the forward pass, a multiple of 256 */
+    int64_t workspace_bytes;
+    int64_t flops_forward;       /* 2 tokens vocab hidden */
+    int64_t flops_backward;      /* 6 tokens vocab hidden: z again, dx, dw */
+    int32_t dtype;
+    int32_t splits;              /* parts of the vocabulary that dx's product sums apart */
+    int32_t top;
+    int32_t reserved;
+    int64_t reserved2;
+} zero_lp_plan_t;
+
+/* Host only.  As zero_ce_plan; 0 <= top <= 32 alternatives (more:
+ * ZERO_EUNSUPPORTED). */
+zero_status_t zero_lp_plan(int64_t tokens, int64_t vocab, int64_t hidden, int32_t dtype, int64_t x_stride, int64_t w_stride,
+                           int64_t piece, int32_t top, zero_lp_plan_t* out);
+/* scale > 0.  logp, lse, entropy (may be NULL): binary32, one per token.
+ * top_logp, top_index: [tokens, top] (NULL where top is 0).  workspace:
+ * plan->workspace_bytes, contents scratch.  Asynchronous. */
+zero_status_t zero_lp_forward(const zero_lp_plan_t* plan, const void* x, const void* w, const int64_t* targets, float scale,
+                              float* logp, float* lse, float* entropy, float* top_logp, int64_t* top_index, void* workspace,
+                              void* stream);
+/* lse and entropy as the forward pass wrote them with the same scale.  dlogp,
+ * dentropy: binary32, one per token, NULL: 0 (entropy may be NULL without
+ * dentropy).  A factor that is not finite makes its token's dx NaN, and dw, and
+ * no other token's dx.  dx, dw NULL: not computed; they are overwritten otherwise
+ * (dw with zeros where there are no tokens). */
+zero_status_t zero_lp_backward(const zero_lp_plan_t* plan, const void* x, const void* w, const int64_t* targets, float scale,
+                               const float* lse, const float* entropy, const float* dlogp, const float* dentropy,
+                               float grad_scale, void* dx, void* dw, void* workspace, void* stream);
+/* As zero_ce_status; after ZERO_ETIMEOUT the forward pass' results and the
+ * gradients are NaN. */
+zero_status_t zero_lp_status(const zero_lp_plan_t* plan, const void* workspace, void* stream);
+
 /* ---- AdamW over a list of tensors -------------------------------------------
  * One optimizer step of every tensor of a list in one kernel launch, for
  * parameters that are not laid out as one flat partitioned vector (a head or

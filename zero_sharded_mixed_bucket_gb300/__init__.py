@@ -32,6 +32,7 @@ __all__ = [
     "zero_ln_plan_t", "zero_ln_plan", "zero_ln_forward", "zero_ln_backward",
     "zero_rms_plan_t", "zero_rms_plan", "zero_rms_forward", "zero_rms_values", "zero_rms_backward",
     "zero_ce_plan_t", "zero_ce_plan", "zero_ce_forward", "zero_ce_backward", "zero_ce_status",
+    "zero_lp_plan_t", "zero_lp_plan", "zero_lp_forward", "zero_lp_backward", "zero_lp_status",
     "zero_adamw_tensor_t", "zero_adamw_plan_t", "zero_adamw_t", "adamw_tensor", "zero_adamw_plan",
     "zero_adamw_table_init", "zero_adamw_check", "zero_adamw_step", "zero_adamw_states",
     "zero_adamw_norm", "zero_adamw_norm_workspace", "zero_adamw_step_clipped", "zero_adamw_clip",
@@ -104,6 +105,13 @@ class zero_ce_plan_t(ctypes.Structure):
     _fields_ = [(n, c_i64) for n in ("tokens", "vocab", "hidden", "x_stride", "w_stride", "piece", "workspace_bytes",
                                       "flops_forward", "flops_backward")] + \
                [("dtype", c_i32), ("splits", c_i32), ("reserved", c_i64 * 2)]
+
+
+class zero_lp_plan_t(ctypes.Structure):
+    _fields_ = [("tokens", c_i64), ("vocab", c_i64), ("hidden", c_i64), ("x_stride", c_i64), ("w_stride", c_i64),
+                ("piece", c_i64), ("rows", c_i64), ("workspace_bytes", c_i64), ("flops_forward", c_i64),
+                ("flops_backward", c_i64), ("dtype", c_i32), ("splits", c_i32), ("top", c_i32), ("reserved", c_i32),
+                ("reserved2", c_i64)]
 
 
 class zero_adamw_tensor_t(ctypes.Structure):
@@ -179,6 +187,10 @@ def lib():
             "zero_ce_forward": [P(zero_ce_plan_t)] + [c_vp] * 8,
             "zero_ce_backward": [P(zero_ce_plan_t)] + [c_vp] * 5 + [c_f] + [c_vp] * 4,
             "zero_ce_status": [P(zero_ce_plan_t), c_vp, c_vp],
+            "zero_lp_plan": [c_i64, c_i64, c_i64, c_i32, c_i64, c_i64, c_i64, c_i32, P(zero_lp_plan_t)],
+            "zero_lp_forward": [P(zero_lp_plan_t)] + [c_vp] * 3 + [c_f] + [c_vp] * 7,
+            "zero_lp_backward": [P(zero_lp_plan_t)] + [c_vp] * 3 + [c_f] + [c_vp] * 4 + [c_f] + [c_vp] * 4,
+            "zero_lp_status": [P(zero_lp_plan_t), c_vp, c_vp],
             "zero_adamw_plan": [P(zero_adamw_tensor_t), c_i64, c_i32, c_i32, P(zero_adamw_plan_t)],
             "zero_adamw_table_init": [P(zero_adamw_plan_t), P(zero_adamw_tensor_t), c_vp, c_vp],
             "zero_adamw_check": [P(zero_adamw_plan_t), c_vp, c_vp, c_vp],
@@ -482,6 +494,36 @@ def zero_ce_backward(plan: zero_ce_plan_t, x, w, targets, lse, dloss, grad_scale
 def zero_ce_status(plan: zero_ce_plan_t, workspace, stream=None):
     """Synchronise; raises ZeroError (ZERO_ETIMEOUT) if a wait inside the last call ran out."""
     _check(lib().zero_ce_status(ctypes.byref(plan), _optr(workspace), _stream(stream)))
+
+
+def zero_lp_plan(tokens: int, vocab: int, hidden: int, dtype: int = ZERO_FP16, x_stride: int = 0, w_stride: int = 0,
+                 piece: int = 0, top: int = 0) -> zero_lp_plan_t:
+    """Log probabilities of `tokens` hidden states against a [vocab, hidden] weight, with `top` alternatives each; strides in
+    values between rows."""
+    p = zero_lp_plan_t()
+    _check(lib().zero_lp_plan(tokens, vocab, hidden, dtype, x_stride, w_stride, piece, top, ctypes.byref(p)))
+    return p
+
+
+def zero_lp_forward(plan: zero_lp_plan_t, x, w, targets, scale: float, logp, lse, entropy, top_logp, top_index, workspace,
+                    stream=None):
+    """logp, lse and entropy (or None) per token, and its alternatives' log probabilities and indices (None without; pointers
+    or tensors; targets and top_index int64)."""
+    _check(lib().zero_lp_forward(ctypes.byref(plan), _optr(x), _optr(w), _optr(targets), scale, _optr(logp), _optr(lse),
+                                 _optr(entropy), _optr(top_logp), _optr(top_index), _optr(workspace), _stream(stream)))
+
+
+def zero_lp_backward(plan: zero_lp_plan_t, x, w, targets, scale: float, lse, entropy, dlogp, dentropy, grad_scale: float, dx,
+                     dw, workspace, stream=None):
+    """dx and dw (None: not computed) of sum(dlogp * logp + dentropy * entropy) * grad_scale (either may be None)."""
+    _check(lib().zero_lp_backward(ctypes.byref(plan), _optr(x), _optr(w), _optr(targets), scale, _optr(lse), _optr(entropy),
+                                  _optr(dlogp), _optr(dentropy), grad_scale, _optr(dx), _optr(dw), _optr(workspace),
+                                  _stream(stream)))
+
+
+def zero_lp_status(plan: zero_lp_plan_t, workspace, stream=None):
+    """Synchronise; raises ZeroError (ZERO_ETIMEOUT) if a wait inside the last call ran out."""
+    _check(lib().zero_lp_status(ctypes.byref(plan), _optr(workspace), _stream(stream)))
 
 
 def adamw_tensor(grad, master, m, v, numel: int, param=None, m_scale=None, v_scale=None,

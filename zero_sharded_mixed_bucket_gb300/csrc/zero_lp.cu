@@ -1,0 +1,771 @@
+// Log probabilities of given tokens over a large vocabulary, entropies, the most
+// likely alternatives, and the gradients of the first two, without stored
+// logits: the plan and the small kernels around the products that cross entropy
+// uses too.
+#include "dev_vocab.cuh"
+#include "nvtx_ranges.h"
+
+namespace zg {
+
+using namespace vocab;
+
+namespace {
+
+constexpr int kMostTop = 32;                          // alternatives: a warp's lanes
+constexpr int kSampleStrips = 32;                     // strips that give the alternatives' threshold
+constexpr unsigned kAll = 0xffffffffu;
+
+struct LpArgs {
+    CeHead* head;
+    const int64_t* targets;
+    int64_t n, vocab;            // rows here
+    float scale;
+    const float2* part;          // [strips][n] maximum, sum
+    const float* part_t;         // [strips][n]
+    int strips;
+    const float* target_logit;   // [n]
+    float* logp;
+    float* lse;
+    float* entropy;              // may be NULL
+    float2* stat;                // [n] maximum, log of the sum
+    int top;
+    uint64_t* cand;              // [n][strips][top]
+    const uint8_t* cand_count;   // [strips][n]
+    float* least;                // [n]
+    float* top_logp;
+    int64_t* top_index;
+};
+
+// The head cleared, before a forward pass.
+__global__ void k_lp_clear(CeHead* head)
+{
+    allow_next_grid();
+    wait_prev_grid();
+    head->err = 0;
+    head->joined = 0;
+}
+
+// Maximum, sum of e = exp((z - maximum) scale), sum of e (z - maximum), of some
+// logits of a row.
+struct Stat {
+    float mx, sum, t;
+};
+
+__device__ __forceinline__ Stat none() { return {-INFINITY, 0.0f, 0.0f}; }
+
+// The same over two sets.  One that adds nothing adds nothing to t either, however
+// far off (or minus infinity) its maximum is; a NaN is in the sum.
+__device__ __forceinline__ Stat join(const Stat& a, const Stat& b, float scale_log2e)
+{
+    Stat r;
+    r.mx = fmaxf(a.mx, b.mx);
+    const float ref = r.mx == -INFINITY ? 0.0f : r.mx;
+    const float da = a.mx - ref, db = b.mx - ref;
+    const float fa = exp2f(da * scale_log2e), fb = exp2f(db * scale_log2e);
+    r.sum = fmaf(a.sum, fa, b.sum * fb);
+    r.t = (fa > 0.0f ? fa * fmaf(da, a.sum, a.t) : 0.0f) + (fb > 0.0f ? fb * fmaf(db, b.sum, b.t) : 0.0f);
+    return r;
+}
+
+__device__ __forceinline__ Stat shuffled(const Stat& a, int o)
+{
+    return {__shfl_xor_sync(kAll, a.mx, o), __shfl_xor_sync(kAll, a.sum, o), __shfl_xor_sync(kAll, a.t, o)};
+}
+
+__device__ __forceinline__ Stat warp_join(Stat a, float scale_log2e)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        a = join(a, shuffled(a, o), scale_log2e);
+    return a;
+}
+
+// (z - maximum) scale - log sum, rather than z scale - lse: a likely token's log
+// probability keeps its digits.
+__device__ __forceinline__ float logp_of(float z, float2 stat, float scale) { return fmaf(z - stat.x, scale, -stat.y); }
+
+__device__ __forceinline__ float2 finish_row(const LpArgs& a, int64_t i, const Stat& r)
+{
+    float2 st = make_float2(r.mx, logf(r.sum));
+    if (a.head->err) st.y = NAN;
+    a.lse[i] = fmaf(r.mx, a.scale, st.y);
+    if (a.entropy) a.entropy[i] = fmaf(-a.scale, r.t / r.sum, st.y);
+    const int64_t t = a.targets[i];
+    a.logp[i] = t >= 0 && t < a.vocab ? logp_of(__ldcg(a.target_logit + i), st, a.scale) : 0.0f;
+    return st;
+}
+
+// Per row: the strips' statistics joined, in a fixed order (32 parts of the
+// strips, then a tree over the parts).
+__global__ void __launch_bounds__(1024) k_lp_join(const __grid_constant__ LpArgs a)
+{
+    wait_prev_grid();
+    __shared__ Stat sh[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float c = a.scale * kLog2e;
+    {
+        const int64_t i = (int64_t)blockIdx.x * 32 + lane;        // the warp's part of 32 rows
+        Stat r = none();
+        if (i < a.n)
+            for (int s = warp; s < a.strips; s += 128) {
+                Stat q[4];
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    q[k] = none();
+                    if (s + 32 * k < a.strips) {
+                        const float2 p = a.part[(int64_t)(s + 32 * k) * a.n + i];
+                        q[k] = {p.x, p.y, a.part_t[(int64_t)(s + 32 * k) * a.n + i]};
+                    }
+                }
+                r = join(r, join(join(q[0], q[1], c), join(q[2], q[3], c), c), c);
+            }
+        sh[warp][lane] = r;
+    }
+    __syncthreads();
+    const int64_t i = (int64_t)blockIdx.x * 32 + warp;            // the warp's row
+    const Stat r = warp_join(sh[lane][warp], c);
+    if (lane == 0 && i < a.n) a.stat[i] = finish_row(a, i, r);
+}
+
+// ---- alternatives ---------------------------------------------------------------------
+// A warp's list: lane j has the jth largest key, 0 where there are fewer.
+__device__ __forceinline__ uint64_t key_max(uint64_t a, uint64_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint64_t key_min(uint64_t a, uint64_t b) { return a > b ? b : a; }
+
+// Falling order over the lanes of what rises and then falls, or the other way.
+__device__ __forceinline__ uint64_t sorted_bitonic(uint64_t x, int lane)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const uint64_t y = __shfl_xor_sync(kAll, x, o);
+        x = lane & o ? key_min(x, y) : key_max(x, y);
+    }
+    return x;
+}
+
+// The 32 largest of two lists.
+__device__ __forceinline__ uint64_t lists_merged(uint64_t a, uint64_t b, int lane)
+{
+    return sorted_bitonic(key_max(a, __shfl_sync(kAll, b, 31 - lane)), lane);
+}
+
+__device__ __forceinline__ uint64_t sorted(uint64_t x, int lane)
+{
+#pragma unroll
+    for (int n = 2; n <= 32; n <<= 1)
+#pragma unroll
+        for (int o = n >> 1; o > 0; o >>= 1) {
+            const uint64_t y = __shfl_xor_sync(kAll, x, o);
+            const bool low = !(lane & o), falls = n == 32 || !(lane & n);
+            x = low == falls ? key_max(x, y) : key_min(x, y);
+        }
+    return x;
+}
+
+// A key of each lane (0: none) into the list, of which the first `top` count.
+// Whether one was.
+__device__ __forceinline__ bool offer(uint64_t& list, uint64_t key, int top, int lane)
+{
+    unsigned b = __ballot_sync(kAll, key > __shfl_sync(kAll, list, top - 1));
+    if (!b) return false;
+    if (__popc(b) > 6) {
+        list = lists_merged(list, sorted(key, lane), lane);
+        return true;
+    }
+    for (; b; b &= b - 1) {
+        const uint64_t k = __shfl_sync(kAll, key, __ffs(b) - 1), up = __shfl_up_sync(kAll, list, 1);
+        const int at = __popc(__ballot_sync(kAll, list > k));
+        list = lane < at ? list : lane == at ? k : up;
+    }
+    return true;
+}
+
+__device__ __forceinline__ void write_top(const LpArgs& a, int64_t i, uint64_t list, float2 stat, int lane)
+{
+    if (lane >= a.top) return;
+    const bool failed = a.head->err;
+    a.top_logp[i * a.top + lane] = failed ? NAN : list ? logp_of(logit_of(list), stat, a.scale) : -INFINITY;
+    a.top_index[i * a.top + lane] = list && !failed ? (int64_t)(0xffffffffu - (uint32_t)list) : -1;
+}
+
+// Per row: the first `top` of its strips' keys, by W warps (1 where there are
+// rows enough to fill the GPU with).  FINAL: written out; else the last of them
+// becomes the row's `least`.
+template <int W, bool FINAL>
+__global__ void __launch_bounds__(256) k_lp_top(const __grid_constant__ LpArgs a, int strips)
+{
+    wait_prev_grid();
+    if constexpr (!FINAL) allow_next_grid();
+    __shared__ uint64_t sh[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t i = W == 1 ? (int64_t)blockIdx.x * 8 + warp : blockIdx.x;
+    uint64_t list = 0;
+    if (i < a.n)
+        for (int s0 = W == 1 ? 0 : warp * 32; s0 < strips; s0 += 32 * W) {
+            const int s = s0 + lane;
+            // a strip's keys fall; the first is on its way with the count, what is there if there is none
+            const uint64_t* src = a.cand + (i * a.strips + min(s, strips - 1)) * a.top;
+            uint64_t key = src[0];
+            // (no more than there is room for, also where a wait ran out and no count was written)
+            const int n = s < strips ? min((int)a.cand_count[(int64_t)s * a.n + i], a.top) : 0;
+            const int most = __reduce_max_sync(kAll, n);
+            for (int k = 0; k < most; k++) {
+                const uint64_t next = k + 1 < n ? src[k + 1] : 0;
+                if (!offer(list, k < n ? key : 0, a.top, lane)) break;
+                key = next;
+            }
+        }
+    if constexpr (W > 1) {
+        sh[warp][lane] = list;
+        for (int o = 4; o > 0; o >>= 1) {
+            __syncthreads();
+            if (warp < o) sh[warp][lane] = list = lists_merged(list, sh[warp + o][lane], lane);
+        }
+        if (warp) return;
+    }
+    if (i >= a.n) return;
+    if constexpr (FINAL) {
+        write_top(a, i, list, a.stat[i], lane);
+    } else {
+        if (lane == a.top - 1) a.least[i] = list ? logit_of(list) : -INFINITY;
+    }
+}
+
+// ---- few rows -------------------------------------------------------------------------
+// Up to kFewTokens rows, as cross entropy's: w is read once and that is the time.
+// Each lane keeps one row's logit; 32 of them at a time go into the warp's
+// statistics and list.  The last block joins the blocks'.
+template <int DT, int T>
+__global__ void __launch_bounds__(kFewThreads, 3) k_lp_few(const uint16_t* x, int64_t x_stride, const uint16_t* w,
+                                                           int64_t w_stride, int64_t hidden, Stat* part, float* target_logit,
+                                                           const __grid_constant__ LpArgs a)
+{
+    constexpr int R = T <= 2 ? 1 : 2, U = 8 / R;      // rows of w at a time, loads in flight per row
+    constexpr int kWarps = kFewThreads / 32;
+    wait_prev_grid();
+    extern __shared__ __align__(16) uint16_t xs[];    // [T][wide]
+    __shared__ Stat sh[kWarps][T];
+    __shared__ uint64_t lists[kWarps][T][32];
+    __shared__ uint32_t last;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wide = (int)((hidden + 7) / 8 * 8);
+    const float c = a.scale * kLog2e;
+#pragma unroll
+    for (int t = 0; t < T; t++)
+        for (int j = threadIdx.x * 8; j < wide; j += kFewThreads * 8) {
+            const uint16_t* p = x + t * x_stride + j;
+            if (j + 8 <= hidden) {
+                *reinterpret_cast<uint4*>(xs + t * wide + j) = *reinterpret_cast<const uint4*>(p);
+            } else {
+                for (int k = 0; k < 8; k++)
+                    xs[t * wide + j + k] = j + k < hidden ? p[k] : (uint16_t)0;
+            }
+        }
+    __syncthreads();
+    Stat st[T];
+    float held[T];                                    // the logit of row `lane` of the 32 under way
+    uint64_t list[T];
+#pragma unroll
+    for (int t = 0; t < T; t++) {
+        st[t] = none();
+        held[t] = -INFINITY;
+        list[t] = 0;
+    }
+    const int64_t warps = (int64_t)gridDim.x * kWarps, me = (int64_t)blockIdx.x * kWarps + warp;
+    int have = 0;
+    int64_t mine = 0;                                 // the vocabulary entry that the lane holds
+    auto flush = [&]() {
+#pragma unroll
+        for (int t = 0; t < T; t++) {
+            const bool any = lane < have;
+            // one logit; a NaN is in the sum, a maximum would drop it
+            const Stat one = any && held[t] != -INFINITY ? Stat{held[t], held[t] == held[t] ? 1.0f : held[t], 0.0f} : none();
+            st[t] = join(st[t], warp_join(one, c), c);
+            if (a.top) offer(list[t], any && held[t] > -INFINITY ? key_of(held[t], (uint32_t)mine) : 0, a.top, lane);
+        }
+        have = 0;
+    };
+    for (int64_t v = me * R; v < a.vocab; v += warps * R) {
+        const uint16_t* row[R];
+        float acc[R][T];
+#pragma unroll
+        for (int q = 0; q < R; q++) {
+            row[q] = w + min(v + q, a.vocab - 1) * w_stride;
+#pragma unroll
+            for (int t = 0; t < T; t++)
+                acc[q][t] = 0.0f;
+        }
+        auto add = [&](const uint4 r[R], int j) {
+            float wv[R][8];
+#pragma unroll
+            for (int q = 0; q < R; q++)
+                unpack8<DT>(r[q], wv[q]);
+#pragma unroll
+            for (int t = 0; t < T; t++) {
+                float xv[8];
+                unpack8<DT>(*reinterpret_cast<const uint4*>(xs + t * wide + j), xv);
+#pragma unroll
+                for (int q = 0; q < R; q++)
+#pragma unroll
+                    for (int k = 0; k < 8; k++)
+                        acc[q][t] = fmaf(wv[q][k], xv[k], acc[q][t]);
+            }
+        };
+        int j = lane * 8;
+        for (; j + 8 <= hidden; j += 256 * U) {
+            uint4 r[U][R];                            // all loads before any use; 0 past the row's end
+#pragma unroll
+            for (int u = 0; u < U; u++)
+#pragma unroll
+                for (int q = 0; q < R; q++)
+                    r[u][q] = j + 256 * u + 8 <= hidden ? __ldcs(reinterpret_cast<const uint4*>(row[q] + j + 256 * u))
+                                                        : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int u = 0; u < U; u++)
+                if (j + 256 * u + 8 <= hidden) add(r[u], j + 256 * u);
+        }
+        if (lane == (hidden / 8) % 32 && hidden % 8) {    // the rows' ragged end
+            const int e = (int)(hidden / 8 * 8);
+            uint4 r[R];
+#pragma unroll
+            for (int q = 0; q < R; q++) {
+                uint32_t u[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int k = 0; k < 8; k++)
+                    if (e + k < hidden) u[k >> 1] |= (uint32_t)row[q][e + k] << ((k & 1) * 16);
+                r[q] = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+            add(r, e);
+        }
+#pragma unroll
+        for (int q = 0; q < R; q++) {
+            if (v + q >= a.vocab) break;
+#pragma unroll
+            for (int t = 0; t < T; t++) {
+                float z = acc[q][t];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    z += __shfl_xor_sync(kAll, z, o);
+                if (lane == have) held[t] = z;
+                if (lane == 0 && v + q == a.targets[t]) target_logit[t] = z;
+            }
+            if (lane == have) mine = v + q;
+            if (++have == 32) flush();
+        }
+    }
+    if (have) flush();
+#pragma unroll
+    for (int t = 0; t < T; t++) {
+        if (lane == 0) sh[warp][t] = st[t];
+        lists[warp][t][lane] = list[t];
+    }
+    __syncthreads();
+    if (warp < T) {                                   // a warp a row: the block's
+        const int t = warp;
+        const Stat r = warp_join(lane < kWarps ? sh[lane][t] : none(), c);
+        if (lane == 0) part[(int64_t)blockIdx.x * T + t] = r;
+        if (a.top) {
+            uint64_t best = lists[0][t][lane];
+            for (int k = 1; k < kWarps; k++)
+                best = lists_merged(best, lists[k][t][lane], lane);
+            if (lane < a.top) a.cand[((int64_t)t * gridDim.x + blockIdx.x) * a.top + lane] = best;
+        }
+    }
+    __threadfence();                                  // statistics, keys and target logits, before the count
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(&a.head->joined, 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    __shared__ float2 done[T];
+    if (warp < T) {                                   // one warp a row: 32 parts, then a tree
+        Stat r = none();
+        for (unsigned k = lane; k < gridDim.x; k += 32) {
+            const Stat* p = part + (int64_t)k * T + warp;
+            r = join(r, Stat{__ldcg(&p->mx), __ldcg(&p->sum), __ldcg(&p->t)}, c);
+        }
+        r = warp_join(r, c);
+        if (lane == 0) done[warp] = finish_row(a, warp, r);
+    }
+    if (!a.top) return;
+    for (int t = 0; t < T; t++) {
+        const uint64_t* keys = a.cand + (int64_t)t * gridDim.x * a.top;
+        const int n = (int)gridDim.x * a.top;
+        uint64_t best = 0;
+        for (int k0 = warp * 32; k0 < n; k0 += 4 * kFewThreads) {
+            uint64_t key[4];
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+                const int k = k0 + u * kFewThreads + lane;
+                key[u] = k < n ? __ldcg(reinterpret_cast<const unsigned long long*>(keys + k)) : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; u++)
+                offer(best, key[u], a.top, lane);
+        }
+        __syncthreads();
+        lists[warp][0][lane] = best;
+        for (int o = kWarps / 2; o > 0; o >>= 1) {
+            __syncthreads();
+            if (warp < o) lists[warp][0][lane] = best = lists_merged(best, lists[warp + o][0][lane], lane);
+        }
+        if (warp == 0) write_top(a, t, best, done[t], lane);
+    }
+}
+
+// One block: the row factors of G and what the products are multiplied by.  G =
+// a ([v = t] - p) - b p (log p + H) in 16 bits; |p (log p + H)| is below 5 for up
+// to 2^24 entries, so rows are scaled by the largest |a| + 4 |b| (binary16: to 2^14
+// instead of 1, which keeps small probabilities out of its subnormals; 1.25 times
+// that is in its range).  A factor that is not finite is no one's maximum, and its
+// own row's are NaN.  Every factor's size 2^-120 at least, so that its inverse is finite.
+__global__ void __launch_bounds__(1024) k_lp_factors(CeHead* head, const int64_t* targets, int64_t n, int64_t vocab,
+                                                     const float* dlogp, const float* dentropy, float scale, float up,
+                                                     float* coef, float* coef_h)
+{
+    allow_next_grid();
+    __shared__ float sm[32];
+    auto factor = [&](int64_t i, float& b) {
+        const int64_t t = targets[i];
+        b = dentropy ? dentropy[i] * scale : 0.0f;
+        return dlogp && t >= 0 && t < vocab ? dlogp[i] * scale : 0.0f;
+    };
+    float most = 0.0f;
+    for (int64_t i = threadIdx.x; i < n; i += 1024) {
+        float b;
+        const float a = factor(i, b), d = fabsf(a) + 4.0f * fabsf(b);
+        if (d < INFINITY) most = fmaxf(most, d);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        most = fmaxf(most, __shfl_xor_sync(kAll, most, o));
+    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = most;
+    __syncthreads();
+    most = sm[threadIdx.x & 31];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        most = fmaxf(most, __shfl_xor_sync(kAll, most, o));
+    if (most > 0.0f) most = fmaxf(most, 0x1p-120f);
+    const float inv = most > 0.0f ? 1.0f / most : 0.0f;
+    if (threadIdx.x == 0) {
+        head->err = 0;
+        head->alpha = most / up;
+    }
+    for (int64_t i = threadIdx.x; i < n; i += 1024) {
+        float b;
+        const float a = factor(i, b);
+        const bool fine = fabsf(a) + 4.0f * fabsf(b) < INFINITY;
+        coef[i] = fine ? a * inv * up : NAN;
+        if (dentropy) coef_h[i] = fine ? b * inv * up : 0.0f;
+    }
+}
+
+// ---- host ---------------------------------------------------------------------------------
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+zero_status_t cuda_failed(cudaError_t e, const char* what)
+{
+    char msg[200];
+    std::snprintf(msg, sizeof msg, "%s: %s", what, cudaGetErrorString(e));
+    return set_error(ZERO_ECUDA, msg);
+}
+
+int64_t strips_of(int64_t vocab) { return ceil_div(vocab, kBN) * 2; }
+
+// Rows at a time of a forward pass: what the strips leave (12 bytes each, and 9 and
+// up with alternatives) takes about 512 MiB.
+int64_t rows_at_once(int64_t tokens, int64_t vocab, int64_t top)
+{
+    const int64_t per = strips_of(vocab) * (12 + (top ? 1 + 8 * top : 0));
+    const int64_t fit = (int64_t(1) << 29) / per / kBM * kBM;
+    return fit < kBM ? kBM : fit;
+}
+
+// Strips whose alternatives are found first, to give every row a threshold for the
+// others'; 0: all at once, each strip with its `top` largest.
+int sample_strips(int64_t rows, int64_t vocab, int64_t top)
+{
+    if (!top) return 0;
+    const int64_t tiles = ceil_div(rows, kBM) * ceil_div(vocab, kBN);
+    return tiles >= 76 * 6 && vocab >= 4 * kSampleStrips * kStrip ? kSampleStrips : 0;
+}
+
+// Byte offsets of a forward pass in the workspace.
+struct LpLayout {
+    int64_t target_logit, stat, least, part, part_t, count, cand, end;
+};
+
+LpLayout lp_layout(const zero_lp_plan_t& p, bool few)
+{
+    LpLayout l;
+    const int64_t rows = p.rows < p.tokens ? p.rows : p.tokens;
+    const int64_t strips = few ? kFewBlocks : strips_of(p.vocab);
+    l.target_logit = sizeof(CeHead);
+    l.stat = l.target_logit + up256(rows * 4);
+    l.least = l.stat + up256(rows * 8);
+    l.part = l.least + up256(rows * 4);
+    l.part_t = l.part + up256(strips * rows * (few ? (int64_t)sizeof(Stat) : 8));
+    l.count = l.part_t + (few ? 0 : up256(strips * rows * 4));
+    l.cand = l.count + (few || !p.top ? 0 : up256(strips * rows));
+    l.end = l.cand + up256(strips * rows * p.top * 8);
+    return l;
+}
+
+zero_status_t products_plan(const zero_lp_plan_t& p, zero_ce_plan_t* out)
+{
+    return zero_ce_plan(p.tokens, p.vocab, p.hidden, p.dtype, p.x_stride, p.w_stride, p.piece, out);
+}
+
+zero_status_t check_lp_plan(const zero_lp_plan_t* p, zero_ce_plan_t* products)
+{
+    if (!p) return set_error(ZERO_EINVAL, "log probabilities' plan is NULL");
+    zero_lp_plan_t fresh;
+    const zero_status_t st = zero_lp_plan(p->tokens, p->vocab, p->hidden, p->dtype, p->x_stride, p->w_stride, p->piece, p->top,
+                                          &fresh);
+    if (st != ZERO_OK) return st;
+    if (std::memcmp(&fresh, p, sizeof fresh) != 0)
+        return set_error(ZERO_EINVAL, "log probabilities' plan was not made by zero_lp_plan");
+    return products_plan(fresh, products);
+}
+
+template <int DT, int T>
+cudaError_t launch_few_t(const zero_lp_plan_t& p, int64_t blocks, const void* x, const void* w, unsigned char* ws,
+                         const LpLayout& l, const LpArgs& a, cudaStream_t s)
+{
+    const size_t bytes = (size_t)(T * ((p.hidden + 7) / 8 * 8) * 2);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem((const void*)k_lp_few<DT, T>, kFewSmem, done);
+    if (e != cudaSuccess) return e;
+    return launch_after(k_lp_few<DT, T>, dim3((unsigned)blocks), kFewThreads, bytes, s, static_cast<const uint16_t*>(x),
+                        p.x_stride, static_cast<const uint16_t*>(w), p.w_stride, p.hidden, reinterpret_cast<Stat*>(ws + l.part),
+                        reinterpret_cast<float*>(ws + l.target_logit), a);
+}
+
+template <int DT>
+cudaError_t launch_few(const zero_lp_plan_t& p, int64_t blocks, const void* x, const void* w, unsigned char* ws,
+                       const LpLayout& l, const LpArgs& a, cudaStream_t s)
+{
+    switch (p.tokens) {
+    case 1: return launch_few_t<DT, 1>(p, blocks, x, w, ws, l, a, s);
+    case 2: return launch_few_t<DT, 2>(p, blocks, x, w, ws, l, a, s);
+    default: return launch_few_t<DT, 3>(p, blocks, x, w, ws, l, a, s);
+    }
+}
+
+template <bool FINAL>
+cudaError_t launch_top(const LpArgs& a, int strips, cudaStream_t s)
+{
+    if (a.n >= 8 * 152) return launch_after(k_lp_top<1, FINAL>, dim3((unsigned)ceil_div(a.n, 8)), 256, 0, s, a, strips);
+    return launch_after(k_lp_top<8, FINAL>, dim3((unsigned)a.n), 256, 0, s, a, strips);
+}
+
+// The forward pass of rows [r0, r0 + a.n).
+cudaError_t forward_rows(const zero_lp_plan_t& p, const void* x, const void* w, unsigned char* ws, const LpLayout& l, LpArgs a,
+                         int64_t r0, bool first, cudaStream_t s, bool& ok)
+{
+    const CUtensorMapDataType type = map_type(p.dtype);
+    const void* xr = static_cast<const uint16_t*>(x) + r0 * p.x_stride;
+    GemmArgs g;
+    std::memset(&g, 0, sizeof g);
+    g.a_rows = a_rows_of(a.n);
+    ok = make_map(&g.a, type, xr, a.n, p.hidden, p.x_stride, g.a_rows) &&
+         make_map(&g.b, type, w, p.vocab, p.hidden, p.w_stride, kBN / 2);
+    if (!ok) return cudaSuccess;
+    g.m = a.n;
+    g.m_tiles = (int)ceil_div(a.n, kBM);
+    g.k_blocks = (int)ceil_div(p.hidden, kBK);
+    g.chunk = kChunk;
+    g.splits = 1;
+    g.head = a.head;
+    g.targets = a.targets;
+    g.target_logit = reinterpret_cast<float*>(ws + l.target_logit);
+    g.scale_log2e = a.scale * kLog2e;
+    g.top = a.top;
+    g.strips = a.strips;
+    auto product = [&](int64_t v0, int64_t v1, const float* least) {
+        const int64_t s0 = v0 / kStrip;
+        g.b_y0 = (int)v0;
+        g.n = v1 - v0;
+        g.n_tiles = (int)ceil_div(g.n, kBN);
+        g.part = const_cast<float2*>(a.part) + s0 * a.n;
+        g.part_t = const_cast<float*>(a.part_t) + s0 * a.n;
+        g.cand = a.cand + s0 * a.top;
+        g.cand_count = const_cast<uint8_t*>(a.cand_count) + s0 * a.n;
+        g.least = least;
+        g.withhold = first && v0 == 0 && withheld_product() > 0;
+        return a.top ? gemm<kEpiTop, false, false>(p.dtype, g, s) : gemm<kEpiStat, false, false>(p.dtype, g, s);
+    };
+    const int sample = sample_strips(a.n, p.vocab, a.top);
+    const int64_t v1 = (int64_t)sample * kStrip;
+    cudaError_t e = cudaSuccess;
+    if (sample) {
+        e = product(0, v1, nullptr);
+        if (e == cudaSuccess) e = launch_top<false>(a, sample, s);
+    }
+    if (e == cudaSuccess) e = product(v1, p.vocab, sample ? a.least : nullptr);
+    if (e == cudaSuccess) e = launch_after(k_lp_join, dim3((unsigned)ceil_div(a.n, 32)), 1024, 0, s, a);
+    if (e == cudaSuccess && a.top) e = launch_top<true>(a, a.strips, s);
+    return e;
+}
+
+}  // namespace
+}  // namespace zg
+
+using namespace zg;
+
+extern "C" {
+
+zero_status_t zero_lp_plan(int64_t tokens, int64_t vocab, int64_t hidden, int32_t dtype, int64_t x_stride, int64_t w_stride,
+                           int64_t piece, int32_t top, zero_lp_plan_t* out)
+{
+    if (!out) return set_error(ZERO_EINVAL, "zero_lp_plan: out is NULL");
+    if (top < 0) return set_error(ZERO_EINVAL, "zero_lp_plan: top must be >= 0");
+    if (top > kMostTop) return set_error(ZERO_EUNSUPPORTED, "zero_lp_plan: top exceeds 32");
+    zero_ce_plan_t c;
+    const zero_status_t st = zero_ce_plan(tokens, vocab, hidden, dtype, x_stride, w_stride, piece, &c);
+    if (st != ZERO_OK) return st;
+    std::memset(out, 0, sizeof *out);
+    out->tokens = tokens;
+    out->vocab = vocab;
+    out->hidden = hidden;
+    out->x_stride = c.x_stride;
+    out->w_stride = c.w_stride;
+    out->piece = c.piece;
+    out->dtype = dtype;
+    out->splits = c.splits;
+    out->top = top;
+    out->rows = rows_at_once(tokens, vocab, top);
+    const int64_t forward = lp_layout(*out, few_tokens(c)).end;
+    out->workspace_bytes = forward > c.workspace_bytes ? forward : c.workspace_bytes;
+    out->flops_forward = c.flops_forward;
+    out->flops_backward = c.flops_backward;
+    return ZERO_OK;
+}
+
+zero_status_t zero_lp_forward(const zero_lp_plan_t* plan, const void* x, const void* w, const int64_t* targets, float scale,
+                              float* logp, float* lse, float* entropy, float* top_logp, int64_t* top_index, void* workspace,
+                              void* stream)
+{
+    NvtxRange range("zero_lp_forward");
+    zero_ce_plan_t c;
+    const zero_status_t st = check_lp_plan(plan, &c);
+    if (st != ZERO_OK) return st;
+    const zero_lp_plan_t& p = *plan;
+    if (!(scale > 0.0f) || !std::isfinite(scale * kLog2e))
+        return set_error(ZERO_EINVAL, "zero_lp_forward: scale must be positive and finite");
+    if (!workspace) return set_error(ZERO_ENOMEM, "zero_lp_forward: workspace is NULL");
+    if (p.tokens && (!x || !w || !targets || !logp || !lse || (p.top && (!top_logp || !top_index))))
+        return set_error(ZERO_ENOMEM, "zero_lp_forward: a buffer is NULL");
+    if (!p.top && (top_logp || top_index))
+        return set_error(ZERO_EINVAL, "zero_lp_forward: the plan has no alternatives");
+    if (!aligned_to(x, 16) || !aligned_to(w, 16) || !aligned_to(workspace, 16) || !aligned_to(targets, 8) ||
+        !aligned_to(logp, 4) || !aligned_to(lse, 4) || !aligned_to(entropy, 4) || !aligned_to(top_logp, 4) ||
+        !aligned_to(top_index, 8))
+        return set_error(ZERO_EALIGN, "zero_lp_forward: x, w and workspace must be 16-byte aligned, the others to their type");
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    k_lp_clear<<<1, 1, 0, s>>>(reinterpret_cast<CeHead*>(ws));
+    cudaError_t e = cudaGetLastError();
+    const bool few = few_tokens(c);
+    const LpLayout l = lp_layout(p, few);
+    for (int64_t r0 = 0; r0 < p.tokens && e == cudaSuccess; r0 += p.rows) {
+        LpArgs a;
+        std::memset(&a, 0, sizeof a);
+        a.head = reinterpret_cast<CeHead*>(ws);
+        a.targets = targets + r0;
+        a.n = p.tokens - r0 < p.rows ? p.tokens - r0 : p.rows;
+        a.vocab = p.vocab;
+        a.scale = scale;
+        a.part = reinterpret_cast<float2*>(ws + l.part);
+        a.part_t = reinterpret_cast<float*>(ws + l.part_t);
+        a.strips = (int)strips_of(p.vocab);
+        a.target_logit = reinterpret_cast<float*>(ws + l.target_logit);
+        a.logp = logp + r0;
+        a.lse = lse + r0;
+        a.entropy = entropy ? entropy + r0 : nullptr;
+        a.stat = reinterpret_cast<float2*>(ws + l.stat);
+        a.top = p.top;
+        a.cand = reinterpret_cast<uint64_t*>(ws + l.cand);
+        a.cand_count = ws + l.count;
+        a.least = reinterpret_cast<float*>(ws + l.least);
+        a.top_logp = top_logp + r0 * p.top;
+        a.top_index = top_index + r0 * p.top;
+        if (few) {
+            const int64_t blocks = few_blocks(c);
+            e = p.dtype == ZERO_BF16 ? launch_few<kBF16>(p, blocks, x, w, ws, l, a, s) : launch_few<kF16>(p, blocks, x, w, ws, l, a, s);
+            break;
+        }
+        if (!encode_fn()) return set_error(ZERO_ECUDA, "zero_lp_forward: the driver has no cuTensorMapEncodeTiled");
+        bool ok = true;
+        e = forward_rows(p, x, w, ws, l, a, r0, r0 == 0, s, ok);
+        if (!ok) return set_error(ZERO_ECUDA, "zero_lp_forward: cuTensorMapEncodeTiled refused a buffer");
+    }
+    return e == cudaSuccess ? ZERO_OK : cuda_failed(e, "zero_lp_forward");
+}
+
+zero_status_t zero_lp_backward(const zero_lp_plan_t* plan, const void* x, const void* w, const int64_t* targets, float scale,
+                               const float* lse, const float* entropy, const float* dlogp, const float* dentropy,
+                               float grad_scale, void* dx, void* dw, void* workspace, void* stream)
+{
+    NvtxRange range("zero_lp_backward");
+    zero_ce_plan_t p;
+    const zero_status_t st = check_lp_plan(plan, &p);
+    if (st != ZERO_OK) return st;
+    if (!(scale > 0.0f) || !std::isfinite(scale * kLog2e))
+        return set_error(ZERO_EINVAL, "zero_lp_backward: scale must be positive and finite");
+    if (!std::isfinite(grad_scale * scale)) return set_error(ZERO_EINVAL, "zero_lp_backward: grad_scale is not finite");
+    if (!workspace) return set_error(ZERO_ENOMEM, "zero_lp_backward: workspace is NULL");
+    if (p.tokens && (!x || !w || !targets || !lse || (dentropy && !entropy)))
+        return set_error(ZERO_ENOMEM, "zero_lp_backward: a buffer is NULL");
+    if (!aligned_to(x, 16) || !aligned_to(w, 16) || !aligned_to(dx, 16) || !aligned_to(dw, 16) || !aligned_to(workspace, 16) ||
+        !aligned_to(targets, 8) || !aligned_to(lse, 4) || !aligned_to(entropy, 4) || !aligned_to(dlogp, 4) ||
+        !aligned_to(dentropy, 4))
+        return set_error(ZERO_EALIGN, "zero_lp_backward: x, w, dx, dw and workspace must be 16-byte aligned, the others to their type");
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!p.tokens) {
+        if (dw) k_ce_zero<<<1024, 256, 0, s>>>(static_cast<uint16_t*>(dw), p.vocab, p.hidden, p.w_stride);
+        cudaError_t e = cudaGetLastError();
+        if (e == cudaSuccess) e = cudaMemsetAsync(workspace, 0, sizeof(CeHead), s);
+        return e == cudaSuccess ? ZERO_OK : cuda_failed(e, "zero_lp_backward");
+    }
+    if (!dx && !dw) return ZERO_OK;
+    if (!encode_fn()) return set_error(ZERO_ECUDA, "zero_lp_backward: the driver has no cuTensorMapEncodeTiled");
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    const CeLayout l = layout_of(p);
+    CeHead* head = reinterpret_cast<CeHead*>(ws);
+    float* coef = reinterpret_cast<float*>(ws + l.coef);
+    float* coef_h = reinterpret_cast<float*>(ws + l.target_logit);   // free in a backward pass
+    const float up = p.dtype == ZERO_FP16 ? 16384.0f : 1.0f;
+    k_lp_factors<<<1, 1024, 0, s>>>(head, targets, p.tokens, p.vocab, dlogp, dentropy, grad_scale * scale, up, coef, coef_h);
+    cudaError_t e = cudaGetLastError();
+    GemmArgs base;
+    std::memset(&base, 0, sizeof base);
+    base.head = head;
+    base.targets = targets;
+    base.lse = lse;
+    base.coef = coef;
+    base.coef_h = dentropy ? coef_h : nullptr;
+    base.entropy = entropy;
+    base.scale_log2e = scale * kLog2e;
+    bool ok = true;
+    if (e == cudaSuccess) e = launch_gradients<kEpiLpGrad>(p, l, base, x, w, dx, dw, ws, s, ok);
+    if (!ok) return set_error(ZERO_ECUDA, "zero_lp_backward: cuTensorMapEncodeTiled refused a buffer");
+    return e == cudaSuccess ? ZERO_OK : cuda_failed(e, "zero_lp_backward");
+}
+
+zero_status_t zero_lp_status(const zero_lp_plan_t* plan, const void* workspace, void* stream)
+{
+    zero_ce_plan_t c;
+    const zero_status_t st = check_lp_plan(plan, &c);
+    if (st != ZERO_OK) return st;
+    if (!workspace) return set_error(ZERO_ENOMEM, "zero_lp_status: workspace is NULL");
+    if (!aligned_to(workspace, 16)) return set_error(ZERO_EALIGN, "zero_lp_status: workspace is not 16-byte aligned");
+    uint32_t err = 0;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMemcpyAsync(&err, workspace, 4, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return cuda_failed(e, "zero_lp_status");
+    return err ? set_error(ZERO_ETIMEOUT, "a bounded wait inside the log probabilities' kernels ran out") : ZERO_OK;
+}
+
+}  // extern "C"
