@@ -29,9 +29,9 @@ constexpr int kFewTokens = 3, kFewThreads = 256, kFewBlocks = 456;   // tokens w
 constexpr int kFewSmem = 64 * 1024;                   // all tokens' values, 16 bits each
 
 // Epilogues: softmax statistics; G of cross entropy; binary32 sums; 16-bit results
-// times alpha; statistics with the entropy's sum, and alternatives besides; G of
-// log probabilities and entropies.
-enum { kEpiLse, kEpiGrad, kEpiAcc, kEpiOut, kEpiStat, kEpiTop, kEpiLpGrad };
+// times alpha; statistics with the entropy's sum, besides the logits themselves, or
+// the alternatives among them; G of log probabilities and entropies.
+enum { kEpiLse, kEpiGrad, kEpiAcc, kEpiOut, kEpiStat, kEpiKeep, kEpiTop, kEpiLpGrad };
 
 // Workspace head.
 struct CeHead {
@@ -43,7 +43,7 @@ struct CeHead {
 
 struct GemmArgs {
     CUtensorMap a, b;
-    CUtensorMap c;               // results: G, binary32 sums or rounded gradients
+    CUtensorMap c;               // results: G, binary32 sums or logits, or rounded gradients
     int64_t m, n;                // rows, columns of the product that exist
     int m_tiles, n_tiles;
     int k_blocks;                // K-blocks in all
@@ -65,13 +65,13 @@ struct GemmArgs {
     uint16_t* out;               // kEpiOut: stored from registers, when a row's end is not on 16 bytes (else NULL)
     int64_t out_stride;
     float scale_log2e;           // log probabilities: the logits' scale times log2 e
-    float* part_t;               // kEpiStat, kEpiTop: [strips][m], a strip's sum of e (z - maximum)
+    float* part_t;               // kEpiStat, kEpiKeep, kEpiTop: [strips][m], a strip's sum of e (z - maximum)
     const float* coef_h;         // kEpiLpGrad: row factors of the entropy's gradient (NULL: none)
     const float* entropy;        //   [m]
-    const float* least;          // kEpiTop: [m], alternatives are at least this (NULL: any)
-    uint64_t* cand;              //   [m][strips][top]: keys of a strip's alternatives
-    uint8_t* cand_count;         //   [strips][m]
-    int top, strips;
+    const float* least;          // kEpiTop: [m], alternatives are at least this
+    uint64_t* cand;              //   [m][strips][top]: keys of a strip's alternatives, of strips of this product
+    uint8_t* cand_count;         //   [m][count_stride]
+    int top, strips, count_stride;
 };
 
 template <int DT>
@@ -132,12 +132,10 @@ __device__ __forceinline__ Tile tile_at(const GemmArgs& g, uint32_t t)
 // A strip's statistics for log probabilities, and (TOP) its alternatives.
 //
 // Alternatives: the `top` largest logits of the strip that are at least the row's
-// `least`, a value that the row's first strips already have `top` logits of; keys
-// in falling order.  A lane keeps the maxima of 8 groups of 16 columns, and a round
-// takes the largest of all from each lane that still has one, group by group as
-// lanes have need, so what it costs goes by how many there are: without `least` a
-// strip takes `top` rounds, with that of 4096 entries two of 8 alternatives or three
-// of 20.
+// `least`, a value that the row is known to have `top` logits of; keys in falling
+// order.  A lane keeps the maxima of 8 groups of 16 columns, and a round takes
+// the largest of all from each lane that still has one, group by group as lanes
+// have need: what it costs goes by how many there are.
 template <bool TOP>
 __device__ __forceinline__ void lp_statistics(const GemmArgs& g, float (&z)[kStrip], int strip, int64_t row, bool live,
                                               uint32_t index0)
@@ -170,7 +168,7 @@ __device__ __forceinline__ void lp_statistics(const GemmArgs& g, float (&z)[kStr
         g.part_t[(int64_t)strip * g.m + row] = t;
     }
     if constexpr (TOP) {
-        const float least = live && g.least ? g.least[row] : -INFINITY;
+        const float least = live ? g.least[row] : INFINITY;
         uint64_t* out = g.cand + (row * g.strips + strip) * g.top;
         int n = 0;
         for (int round = 0; round < g.top; round++) {
@@ -202,7 +200,7 @@ __device__ __forceinline__ void lp_statistics(const GemmArgs& g, float (&z)[kStr
                 if (group == q) out[n++] = key_of(cur, index0 + kG * q + at);
             }
         }
-        if (live) g.cand_count[(int64_t)strip * g.m + row] = (uint8_t)n;
+        if (live) g.cand_count[row * g.count_stride + strip] = (uint8_t)n;
     }
 }
 
@@ -410,7 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
                 if (lane == 0) tc::mbar_arrive_leader(acc_empty + 8 * buf);
             }
             if (!ok) break;
-            if constexpr (EPI == kEpiLse || EPI == kEpiStat || EPI == kEpiTop) {
+            if constexpr (EPI == kEpiLse || EPI == kEpiStat || EPI == kEpiKeep || EPI == kEpiTop) {
                 // the strip's maximum and its sum
                 const int64_t left = g.n - col0;
                 if (left < kStrip) {
@@ -443,7 +441,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
                 } else {
                     lp_statistics<EPI == kEpiTop>(g, z, w.nt * 2 + half, row, live, (uint32_t)(g.b_y0 + col0));
                 }
-            } else {
+            }
+            if constexpr (EPI != kEpiLse && EPI != kEpiStat && EPI != kEpiTop) {
                 if constexpr (EPI == kEpiGrad) {
 #pragma unroll
                     for (int k = 0; k < kStrip; k++)
@@ -507,7 +506,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
                 // box (a second box for a stage less: 2 % slower)
                 const int row0 = w.mt * kBM + (int)rank * (kBM / 2) + band * 32;
                 const int y = row0 + (EPI == kEpiAcc ? w.split * g.m_tiles * kBM : 0);
-                constexpr int kCols = EPI == kEpiAcc ? 32 : 64;       // columns of a box
+                constexpr bool kSingle = EPI == kEpiAcc || EPI == kEpiKeep;       // binary32
+                constexpr int kCols = kSingle ? 32 : 64;              // columns of a box
 #pragma unroll
                 for (int c = 0; c < kStrip; c += kCols) {
                     if (lane == 0) tc::bulk_wait_read();
@@ -515,7 +515,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
 #pragma unroll
                     for (int k = 0; k < 8; k++) {
                         const uint32_t at = box + lane * 128 + ((k ^ (lane & 7)) << 4);
-                        if constexpr (EPI == kEpiAcc) {
+                        if constexpr (kSingle) {
                             const float* p = z + c + 4 * k;
                             tc::st_shared16(at, __float_as_uint(p[0]), __float_as_uint(p[1]), __float_as_uint(p[2]),
                                             __float_as_uint(p[3]));

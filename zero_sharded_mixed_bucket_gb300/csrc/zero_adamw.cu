@@ -418,9 +418,9 @@ __global__ void __launch_bounds__(kAd32Threads) k_adamw_check(const AdTable tab,
 }
 
 // ---- the gradients' norm --------------------------------------------------------------
-// sqrt(sum of g^2) over the list.  A block takes a run of consecutive chunks, whose
-// tensors' values lie side by side, so it streams; kNormUnroll 16-byte loads of a
-// thread are on their way at once.  A thread adds up the squares of a batch (32
+// sqrt(sum of g^2) over the list.  A group of G threads takes a run of consecutive
+// chunks, whose tensors' values lie side by side, so it streams; kNormUnroll 16-byte
+// loads of a thread are on their way at once.  A thread adds up the squares of a batch (32
 // 16-bit values, 16 of 32 bits) in binary32 and the batches in binary64: one
 // binary64 operation to a batch is out of the way of memory, one to a value is not
 // (GB300 has 2 of them a clock and SM, a fifth of what the values would need).  A
@@ -429,8 +429,9 @@ __global__ void __launch_bounds__(kAd32Threads) k_adamw_check(const AdTable tab,
 // that holds an infinity or a NaN, which is where those are counted.
 constexpr int kNormThreads = 256, kNormUnroll = 4;
 constexpr int64_t kNormBlocks = 152 * 8;              // all resident at once
-// Up to so many chunks one block does all and needs no second kernel.
-constexpr int64_t kNormAlone = 8;
+// Up to so many chunks one block does all, a chunk to each of its warps, and needs no
+// second kernel.
+constexpr int kNormAlone = 32;
 
 struct NormPart {
     double sum;
@@ -468,9 +469,10 @@ __device__ __forceinline__ void norm_out(const NormOut& o, double sum, uint64_t 
 }
 
 // Sum over the block, in a fixed order, in thread 0.
+template <int T>
 __device__ __forceinline__ NormPart norm_join(double sum, uint64_t bad)
 {
-    __shared__ double sh[kNormThreads / 32];
+    __shared__ double sh[T / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -479,21 +481,22 @@ __device__ __forceinline__ NormPart norm_join(double sum, uint64_t bad)
     const int any = __syncthreads_or(bad != 0);
     NormPart r{0.0, (uint64_t)(any != 0)};
     if (threadIdx.x == 0)
-        for (int k = 0; k < kNormThreads / 32; k++)
+        for (int k = 0; k < T / 32; k++)
             r.sum += sh[k];
     return r;
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kNormThreads, 8) k_adamw_norm(const AdTable tab, int64_t n_chunks,
-                                                                const __grid_constant__ NormOut out)
+template <int DT, int G, int T>
+__global__ void __launch_bounds__(T, T < 1024 ? 2048 / T : 1) k_adamw_norm(const AdTable tab, int64_t n_chunks,
+                                                            const __grid_constant__ NormOut out)
 {
-    constexpr int V = kVecOf<DT>, U = kNormUnroll, kBatch = kNormThreads * V;
+    constexpr int V = kVecOf<DT>, U = kNormUnroll, kBatch = G * V;
     allow_next_grid();
     double sum = 0.0;
     uint64_t bad = 0;
-    int64_t c = n_chunks * blockIdx.x / gridDim.x;
-    const int64_t end = n_chunks * (blockIdx.x + 1) / gridDim.x;
+    const int64_t groups = (int64_t)gridDim.x * (T / G), group = (int64_t)blockIdx.x * (T / G) + threadIdx.x / G;
+    int64_t c = n_chunks * group / groups;
+    const int64_t end = n_chunks * (group + 1) / groups;
     while (c < end) {
         const AdRec& r = tab.rec[tab.chunk_tensor[c]];
         const Bits<DT>* g = static_cast<const Bits<DT>*>(r.t.grad);
@@ -503,7 +506,7 @@ __global__ void __launch_bounds__(kNormThreads, 8) k_adamw_norm(const AdTable ta
         const bool vec = ((uintptr_t)g & 15u) == 0;
         c = stop;
         for (int64_t i0 = lo; i0 < hi; i0 += U * kBatch) {
-            const int64_t i = i0 + threadIdx.x * V;
+            const int64_t i = i0 + threadIdx.x % G * V;
             float s = 0.0f;
             uint32_t any = 0;
             auto add = [&](const uint4& q) {
@@ -557,9 +560,9 @@ __global__ void __launch_bounds__(kNormThreads, 8) k_adamw_norm(const AdTable ta
             }
         }
     }
-    const NormPart r = norm_join(sum, bad);
+    const NormPart r = norm_join<T>(sum, bad);
     if (threadIdx.x) return;
-    if (gridDim.x == 1)
+    if (G < T)
         norm_out(out, r.sum, r.bad);
     else
         out.part[blockIdx.x] = r;
@@ -575,7 +578,7 @@ __global__ void __launch_bounds__(kNormThreads) k_adamw_norm_join(int parts, con
         sum += out.part[k].sum;
         bad |= out.part[k].bad;
     }
-    const NormPart r = norm_join(sum, bad);
+    const NormPart r = norm_join<kNormThreads>(sum, bad);
     if (threadIdx.x == 0) norm_out(out, r.sum, r.bad);
 }
 
@@ -672,6 +675,13 @@ zero_status_t check_adamw_plan(const zero_adamw_plan_t* p, const void* table)
     if (p->n_chunks && !table) return set_error(ZERO_ENOMEM, "AdamW table is NULL");
     if (!aligned_to(table, 16)) return set_error(ZERO_EALIGN, "AdamW table is not 16-byte aligned");
     return ZERO_OK;
+}
+
+template <int DT>
+void launch_norm(const AdTable& tab, int64_t n_chunks, const NormOut& o, unsigned grid, cudaStream_t s)
+{
+    if (grid == 1) k_adamw_norm<DT, 32, 32 * kNormAlone><<<1, 32 * kNormAlone, 0, s>>>(tab, n_chunks, o);
+    else k_adamw_norm<DT, kNormThreads, kNormThreads><<<grid, kNormThreads, 0, s>>>(tab, n_chunks, o);
 }
 
 // Blocks of the norm's kernel, a function of the list alone.
@@ -877,9 +887,9 @@ zero_status_t zero_adamw_norm(const zero_adamw_plan_t* plan, const void* table, 
     const NormOut o{static_cast<NormPart*>(workspace), norm, flag, std::fabs((double)grad_scale),
                     max_norm > 0.0f ? (double)max_norm : 0.0};
     const unsigned grid = (unsigned)norm_blocks(*plan);
-    if (plan->dtype == ZERO_FP32) k_adamw_norm<kF32><<<grid, kNormThreads, 0, s>>>(tab, plan->n_chunks, o);
-    else if (plan->dtype == ZERO_BF16) k_adamw_norm<kBF16><<<grid, kNormThreads, 0, s>>>(tab, plan->n_chunks, o);
-    else k_adamw_norm<kF16><<<grid, kNormThreads, 0, s>>>(tab, plan->n_chunks, o);
+    if (plan->dtype == ZERO_FP32) launch_norm<kF32>(tab, plan->n_chunks, o, grid, s);
+    else if (plan->dtype == ZERO_BF16) launch_norm<kBF16>(tab, plan->n_chunks, o, grid, s);
+    else launch_norm<kF16>(tab, plan->n_chunks, o, grid, s);
     cudaError_t err = cudaGetLastError();
     if (err == cudaSuccess && grid > 1) err = launch_kernel(k_adamw_norm_join, 1, kNormThreads, s, true, (int)grid, o);
     return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_adamw_norm");

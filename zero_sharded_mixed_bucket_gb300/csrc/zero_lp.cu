@@ -12,7 +12,7 @@ using namespace vocab;
 namespace {
 
 constexpr int kMostTop = 32;                          // alternatives: a warp's lanes
-constexpr int kSampleStrips = 32;                     // strips that give the alternatives' threshold
+constexpr int64_t kSample = 4096;                     // entries that give the alternatives' threshold
 constexpr unsigned kAll = 0xffffffffu;
 
 struct LpArgs {
@@ -29,9 +29,13 @@ struct LpArgs {
     float* entropy;              // may be NULL
     float2* stat;                // [n] maximum, log of the sum
     int top;
-    uint64_t* cand;              // [n][strips][top]
-    const uint8_t* cand_count;   // [strips][n]
-    float* least;                // [n]
+    const float* logits;         // [n][logit_stride]: of the first `sampled` entries
+    int64_t logit_stride, sampled;
+    uint64_t* first;             // [n][top]: the alternatives among those
+    float* least;                // [n]: the last of them
+    uint64_t* cand;              // [n][cand_strips][top]: those of the strips behind; few rows: of the blocks
+    const uint8_t* cand_count;   // [n][count_stride]
+    int cand_strips, count_stride;
     float* top_logp;
     int64_t* top_index;
 };
@@ -95,36 +99,49 @@ __device__ __forceinline__ float2 finish_row(const LpArgs& a, int64_t i, const S
     return st;
 }
 
-// Per row: the strips' statistics joined, in a fixed order (32 parts of the
-// strips, then a tree over the parts).
-__global__ void __launch_bounds__(1024) k_lp_join(const __grid_constant__ LpArgs a)
+// Per row: the strips' statistics joined, in a fixed order: kJoinParts parts of the
+// strips, a thread each, kJoinRows rows side by side, then a tree over the parts.
+constexpr int kJoinRows = 8, kJoinParts = 64, kJoinThreads = kJoinRows * kJoinParts, kJoinAhead = 8;
+
+__global__ void __launch_bounds__(kJoinThreads) k_lp_join(const __grid_constant__ LpArgs a)
 {
     wait_prev_grid();
-    __shared__ Stat sh[32][33];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ Stat sh[kJoinThreads / 32][kJoinRows];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = threadIdx.x / kJoinRows;
     const float c = a.scale * kLog2e;
-    {
-        const int64_t i = (int64_t)blockIdx.x * 32 + lane;        // the warp's part of 32 rows
-        Stat r = none();
-        if (i < a.n)
-            for (int s = warp; s < a.strips; s += 128) {
-                Stat q[4];
+    const int64_t i = (int64_t)blockIdx.x * kJoinRows + threadIdx.x % kJoinRows;
+    Stat r = none();
+    if (i < a.n)
+        for (int s = part; s < a.strips; s += kJoinParts * kJoinAhead) {
+            Stat q[kJoinAhead];
 #pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    q[k] = none();
-                    if (s + 32 * k < a.strips) {
-                        const float2 p = a.part[(int64_t)(s + 32 * k) * a.n + i];
-                        q[k] = {p.x, p.y, a.part_t[(int64_t)(s + 32 * k) * a.n + i]};
-                    }
+            for (int k = 0; k < kJoinAhead; k++) {
+                const int at = s + k * kJoinParts;
+                q[k] = none();
+                if (at < a.strips) {
+                    const float2 p = a.part[(int64_t)at * a.n + i];
+                    q[k] = {p.x, p.y, a.part_t[(int64_t)at * a.n + i]};
                 }
-                r = join(r, join(join(q[0], q[1], c), join(q[2], q[3], c), c), c);
             }
-        sh[warp][lane] = r;
-    }
+#pragma unroll
+            for (int n = kJoinAhead / 2; n > 0; n /= 2)
+#pragma unroll
+                for (int k = 0; k < n; k++)
+                    q[k] = join(q[k], q[k + n], c);
+            r = join(r, q[0], c);
+        }
+    r = join(r, shuffled(r, 8), c);
+    r = join(r, shuffled(r, 16), c);
+    if (lane < kJoinRows) sh[warp][lane] = r;
     __syncthreads();
-    const int64_t i = (int64_t)blockIdx.x * 32 + warp;            // the warp's row
-    const Stat r = warp_join(sh[lane][warp], c);
-    if (lane == 0 && i < a.n) a.stat[i] = finish_row(a, i, r);
+    if (warp < kJoinRows / 2) {                       // a warp two rows, 16 lanes each
+        r = sh[lane & 15][2 * warp + (lane >> 4)];
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1)
+            r = join(r, shuffled(r, o), c);
+        const int64_t at = (int64_t)blockIdx.x * kJoinRows + 2 * warp + (lane >> 4);
+        if ((lane & 15) == 0 && at < a.n) a.stat[at] = finish_row(a, at, r);
+    }
 }
 
 // ---- alternatives ---------------------------------------------------------------------
@@ -162,22 +179,46 @@ __device__ __forceinline__ uint64_t sorted(uint64_t x, int lane)
     return x;
 }
 
-// A key of each lane (0: none) into the list, of which the first `top` count.
-// Whether one was.
-__device__ __forceinline__ bool offer(uint64_t& list, uint64_t key, int top, int lane)
+// Keys on their way into a warp's list, gathered so that 32 at a time are sorted.
+struct Gather {
+    uint64_t* held;              // [64] of the warp, shared memory
+    int n;                       // so many are held
+    uint64_t list;
+
+    // A key of each lane with `in`.
+    __device__ __forceinline__ void add(bool in, uint64_t key, int lane)
+    {
+        const unsigned b = __ballot_sync(kAll, in);
+        if (!b) return;
+        if (in) held[n + __popc(b & ((1u << lane) - 1))] = key;
+        n += __popc(b);
+        __syncwarp();
+        if (n < 32) return;
+        list = lists_merged(list, sorted(held[lane], lane), lane);
+        n -= 32;
+        const uint64_t rest = held[32 + lane];
+        __syncwarp();
+        held[lane] = rest;
+        __syncwarp();
+    }
+
+    __device__ __forceinline__ uint64_t all(int lane)
+    {
+        if (n) list = lists_merged(list, sorted(lane < n ? held[lane] : 0, lane), lane);
+        return list;
+    }
+};
+
+// The lists of a block's 8 warps, in warp 0.
+__device__ __forceinline__ uint64_t block_merged(uint64_t list, uint64_t (*sh)[32], int warp, int lane)
 {
-    unsigned b = __ballot_sync(kAll, key > __shfl_sync(kAll, list, top - 1));
-    if (!b) return false;
-    if (__popc(b) > 6) {
-        list = lists_merged(list, sorted(key, lane), lane);
-        return true;
+    __syncthreads();
+    sh[warp][lane] = list;
+    for (int o = 4; o > 0; o >>= 1) {
+        __syncthreads();
+        if (warp < o) sh[warp][lane] = list = lists_merged(list, sh[warp + o][lane], lane);
     }
-    for (; b; b &= b - 1) {
-        const uint64_t k = __shfl_sync(kAll, key, __ffs(b) - 1), up = __shfl_up_sync(kAll, list, 1);
-        const int at = __popc(__ballot_sync(kAll, list > k));
-        list = lane < at ? list : lane == at ? k : up;
-    }
-    return true;
+    return list;
 }
 
 __device__ __forceinline__ void write_top(const LpArgs& a, int64_t i, uint64_t list, float2 stat, int lane)
@@ -188,50 +229,160 @@ __device__ __forceinline__ void write_top(const LpArgs& a, int64_t i, uint64_t l
     a.top_index[i * a.top + lane] = list && !failed ? (int64_t)(0xffffffffu - (uint32_t)list) : -1;
 }
 
-// Per row: the first `top` of its strips' keys, by W warps (1 where there are
-// rows enough to fill the GPU with).  FINAL: written out; else the last of them
-// becomes the row's `least`.
+// Per row: the first `top` of the logits that were kept, by W warps.  Of the strips'
+// maxima, a few to a lane, the top-th largest lane's is a bound that the row is known
+// to have `top` logits of; only strips whose maximum is no less have any to look at,
+// and they have about as many as are wanted (of 32 strips 9 for 8, 31 for 20).
+// FINAL: written out; else kept for k_lp_top, the last of them as the row's `least`.
 template <int W, bool FINAL>
-__global__ void __launch_bounds__(256) k_lp_top(const __grid_constant__ LpArgs a, int strips)
+__global__ void __launch_bounds__(256) k_lp_first(const __grid_constant__ LpArgs a)
 {
+    constexpr int U = 4;                              // strips on their way
     wait_prev_grid();
     if constexpr (!FINAL) allow_next_grid();
-    __shared__ uint64_t sh[8][32];
+    __shared__ uint64_t sh[8][32], held[8][64];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t i = W == 1 ? (int64_t)blockIdx.x * 8 + warp : blockIdx.x;
-    uint64_t list = 0;
-    if (i < a.n)
-        for (int s0 = W == 1 ? 0 : warp * 32; s0 < strips; s0 += 32 * W) {
-            const int s = s0 + lane;
-            // a strip's keys fall; the first is on its way with the count, what is there if there is none
-            const uint64_t* src = a.cand + (i * a.strips + min(s, strips - 1)) * a.top;
-            uint64_t key = src[0];
-            // (no more than there is room for, also where a wait ran out and no count was written)
-            const int n = s < strips ? min((int)a.cand_count[(int64_t)s * a.n + i], a.top) : 0;
-            const int most = __reduce_max_sync(kAll, n);
-            for (int k = 0; k < most; k++) {
-                const uint64_t next = k + 1 < n ? src[k + 1] : 0;
-                if (!offer(list, k < n ? key : 0, a.top, lane)) break;
-                key = next;
+    const int64_t i = W == 1 ? (int64_t)blockIdx.x * 8 + warp : min((int64_t)blockIdx.x, a.n - 1);
+    const int strips = (int)((a.sampled + kStrip - 1) / kStrip);
+    const float2* part = a.part + min(i, a.n - 1);
+    const int s0 = W == 1 ? 0 : warp * 32;
+    float most = -INFINITY;
+    for (int s = s0 + lane; s < strips; s += 32 * W)
+        most = fmaxf(most, part[(int64_t)s * a.n].x);
+    uint64_t bound = sorted(key_of(most, 0), lane);
+    if constexpr (W > 1) {
+        bound = block_merged(bound, sh, warp, lane);
+        if (warp == 0) sh[0][lane] = bound;
+        __syncthreads();
+        bound = sh[0][lane];
+    }
+    const float least = fmaxf(logit_of(__shfl_sync(kAll, bound, a.top - 1)), -3.4028235e38f);    // -infinity is none
+    Gather g{held[warp], 0, 0};
+    if (i < a.n) {
+        const float* z = a.logits + i * a.logit_stride;
+        for (int sw = s0; sw < strips; sw += 32 * W) {
+            unsigned todo = __ballot_sync(kAll, sw + lane < strips && part[(int64_t)(sw + lane) * a.n].x >= least);
+            while (todo) {
+                int at[U];
+                float4 q[U];
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    at[u] = todo ? (sw + __ffs(todo) - 1) * kStrip + 4 * lane : (int)a.sampled;
+                    todo &= todo - 1;
+                    if (at[u] < a.sampled) q[u] = *reinterpret_cast<const float4*>(z + at[u]);
+                }
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    const float f[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        const bool in = at[u] + k < a.sampled && f[k] >= least;
+                        g.add(in, key_of(f[k], (uint32_t)(at[u] + k)), lane);
+                    }
+                }
             }
         }
+    }
+    uint64_t list = g.all(lane);
     if constexpr (W > 1) {
-        sh[warp][lane] = list;
-        for (int o = 4; o > 0; o >>= 1) {
-            __syncthreads();
-            if (warp < o) sh[warp][lane] = list = lists_merged(list, sh[warp + o][lane], lane);
-        }
+        list = block_merged(list, sh, warp, lane);
         if (warp) return;
     }
     if (i >= a.n) return;
     if constexpr (FINAL) {
         write_top(a, i, list, a.stat[i], lane);
     } else {
+        if (lane < a.top) a.first[i * a.top + lane] = list;
         if (lane == a.top - 1) a.least[i] = list ? logit_of(list) : -INFINITY;
     }
 }
 
+// Per row: its first `top` alternatives, from those of the sample and of the strips
+// behind; a warp a row.  A strip has few or none, and a lane 16 strips' counts: the
+// keys' places are listed first (in whatever order), so that every lane then has
+// keys to load; of those, the ones below a bound that the row is known to have
+// `top` of are dropped before any are sorted.
+constexpr int kPlaces = 512, kTopWarps = 4;
+
+__global__ void __launch_bounds__(32 * kTopWarps) k_lp_top(const __grid_constant__ LpArgs a)
+{
+    constexpr int U = 8;                              // keys of a lane on their way
+    wait_prev_grid();
+    __shared__ uint32_t places[kTopWarps][kPlaces + 32 * kMostTop];
+    __shared__ uint64_t held[kTopWarps][64];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t i = (int64_t)blockIdx.x * kTopWarps + warp;
+    if (i >= a.n) return;
+    const uint64_t* keys = a.cand + i * a.cand_strips * a.top;
+    const uint8_t* counts = a.cand_count + i * a.count_stride;
+    uint32_t* mine = places[warp];
+    Gather g{held[warp], 0, lane < a.top ? a.first[i * a.top + lane] : 0};
+    int listed = 0;
+    auto look = [&]() {
+        __syncwarp();
+        for (int k0 = 0; k0 < listed; k0 += 32 * U) {
+            uint64_t key[U], most = 0;
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int k = k0 + 32 * u + lane;
+                key[u] = k < listed ? keys[mine[k]] : 0;
+                most = key_max(most, key[u]);
+            }
+            // the top-th of the list, or of the lanes' largest
+            const uint64_t bound = key_max(__shfl_sync(kAll, g.list, a.top - 1), __shfl_sync(kAll, sorted(most, lane), a.top - 1));
+#pragma unroll
+            for (int u = 0; u < U; u++)
+                g.add(key[u] && key[u] >= bound, key[u], lane);
+        }
+        __syncwarp();
+        listed = 0;
+    };
+    for (int s0 = 0; s0 < a.cand_strips; s0 += 512) {
+        const int s = s0 + 16 * lane;
+        uint4 q = make_uint4(0, 0, 0, 0);
+        if (s < a.cand_strips) q = *reinterpret_cast<const uint4*>(counts + s);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        // (no more than there is room for, also where a wait ran out and no count was written)
+        auto count = [&](int k) { return s + k < a.cand_strips ? min((int)(w[k >> 2] >> (8 * (k & 3)) & 0xffu), a.top) : 0; };
+        int sum = 0;
+#pragma unroll
+        for (int k = 0; k < 16; k++)
+            sum += count(k);
+        const int total = __reduce_add_sync(kAll, sum);
+        // all 16 of a lane at once, or one after another
+        const int steps = listed + total <= kPlaces + 32 * kMostTop ? 1 : 16;
+        for (int step = 0; step < steps; step++) {
+            int n = 0;
+#pragma unroll
+            for (int k = 0; k < 16; k++)
+                if (steps == 1 || k == step) n += count(k);
+            int at = n;                               // inclusive sums over the lanes
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int p = __shfl_up_sync(kAll, at, o);
+                if (lane >= o) at += p;
+            }
+            const int added = __shfl_sync(kAll, at, 31);
+            at += listed - n;
+#pragma unroll
+            for (int k = 0; k < 16; k++)
+                if (steps == 1 || k == step)
+                    for (int j = 0; j < count(k); j++)
+                        mine[at++] = (uint32_t)(s + k) * (uint32_t)a.top + j;
+            listed += added;
+            if (listed > kPlaces) look();
+        }
+    }
+    look();
+    write_top(a, i, g.all(lane), a.stat[i], lane);
+}
+
 // ---- few rows -------------------------------------------------------------------------
+__device__ __forceinline__ uint64_t load_key(const uint64_t* p)
+{
+    return __ldcg(reinterpret_cast<const unsigned long long*>(p));
+}
+
 // Up to kFewTokens rows, as cross entropy's: w is read once and that is the time.
 // Each lane keeps one row's logit; 32 of them at a time go into the warp's
 // statistics and list.  The last block joins the blocks'.
@@ -245,8 +396,10 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_lp_few(const uint16_t* x, in
     wait_prev_grid();
     extern __shared__ __align__(16) uint16_t xs[];    // [T][wide]
     __shared__ Stat sh[kWarps][T];
-    __shared__ uint64_t lists[kWarps][T][32];
+    __shared__ uint64_t lists[kWarps][32], least;
     __shared__ uint32_t last;
+    __shared__ float2 done;
+    __shared__ int chosen, which[kFewBlocks];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int wide = (int)((hidden + 7) / 8 * 8);
     const float c = a.scale * kLog2e;
@@ -281,7 +434,8 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_lp_few(const uint16_t* x, in
             // one logit; a NaN is in the sum, a maximum would drop it
             const Stat one = any && held[t] != -INFINITY ? Stat{held[t], held[t] == held[t] ? 1.0f : held[t], 0.0f} : none();
             st[t] = join(st[t], warp_join(one, c), c);
-            if (a.top) offer(list[t], any && held[t] > -INFINITY ? key_of(held[t], (uint32_t)mine) : 0, a.top, lane);
+            if (a.top)
+                list[t] = lists_merged(list[t], sorted(any && held[t] > -INFINITY ? key_of(held[t], (uint32_t)mine) : 0, lane), lane);
         }
         have = 0;
     };
@@ -355,61 +509,64 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_lp_few(const uint16_t* x, in
     }
     if (have) flush();
 #pragma unroll
-    for (int t = 0; t < T; t++) {
+    for (int t = 0; t < T; t++)
         if (lane == 0) sh[warp][t] = st[t];
-        lists[warp][t][lane] = list[t];
-    }
     __syncthreads();
     if (warp < T) {                                   // a warp a row: the block's
-        const int t = warp;
-        const Stat r = warp_join(lane < kWarps ? sh[lane][t] : none(), c);
-        if (lane == 0) part[(int64_t)blockIdx.x * T + t] = r;
-        if (a.top) {
-            uint64_t best = lists[0][t][lane];
-            for (int k = 1; k < kWarps; k++)
-                best = lists_merged(best, lists[k][t][lane], lane);
-            if (lane < a.top) a.cand[((int64_t)t * gridDim.x + blockIdx.x) * a.top + lane] = best;
-        }
+        const Stat r = warp_join(lane < kWarps ? sh[lane][warp] : none(), c);
+        if (lane == 0) part[(int64_t)warp * gridDim.x + blockIdx.x] = r;
     }
+    if (a.top)
+#pragma unroll
+        for (int t = 0; t < T; t++) {
+            const uint64_t best = block_merged(list[t], lists, warp, lane);
+            if (warp == 0 && lane < a.top) a.cand[((int64_t)t * gridDim.x + blockIdx.x) * a.top + lane] = best;
+        }
     __threadfence();                                  // statistics, keys and target logits, before the count
     __syncthreads();
     if (threadIdx.x == 0) last = atomicAdd(&a.head->joined, 1u) == gridDim.x - 1;
     __syncthreads();
     if (!last) return;
     __threadfence();
-    __shared__ float2 done[T];
-    if (warp < T) {                                   // one warp a row: 32 parts, then a tree
+    // the blocks' statistics, two to a thread, in a fixed order; of their lists, those
+    // that start no lower than the top-th of the threads' best
+    constexpr int kEach = (kFewBlocks + kFewThreads - 1) / kFewThreads;
+    const int blocks = (int)gridDim.x;
+    for (int t = 0; t < T; t++) {
         Stat r = none();
-        for (unsigned k = lane; k < gridDim.x; k += 32) {
-            const Stat* p = part + (int64_t)k * T + warp;
+        uint64_t best[kEach], most = 0;
+#pragma unroll
+        for (int u = 0; u < kEach; u++) {
+            const int k = (int)threadIdx.x + u * kFewThreads;
+            best[u] = 0;
+            if (k >= blocks) continue;
+            const Stat* p = part + (int64_t)t * blocks + k;
+            if (a.top) best[u] = load_key(a.cand + ((int64_t)t * blocks + k) * a.top);
             r = join(r, Stat{__ldcg(&p->mx), __ldcg(&p->sum), __ldcg(&p->t)}, c);
+            most = key_max(most, best[u]);
         }
         r = warp_join(r, c);
-        if (lane == 0) done[warp] = finish_row(a, warp, r);
-    }
-    if (!a.top) return;
-    for (int t = 0; t < T; t++) {
-        const uint64_t* keys = a.cand + (int64_t)t * gridDim.x * a.top;
-        const int n = (int)gridDim.x * a.top;
-        uint64_t best = 0;
-        for (int k0 = warp * 32; k0 < n; k0 += 4 * kFewThreads) {
-            uint64_t key[4];
-#pragma unroll
-            for (int u = 0; u < 4; u++) {
-                const int k = k0 + u * kFewThreads + lane;
-                key[u] = k < n ? __ldcg(reinterpret_cast<const unsigned long long*>(keys + k)) : 0;
-            }
-#pragma unroll
-            for (int u = 0; u < 4; u++)
-                offer(best, key[u], a.top, lane);
-        }
         __syncthreads();
-        lists[warp][0][lane] = best;
-        for (int o = kWarps / 2; o > 0; o >>= 1) {
-            __syncthreads();
-            if (warp < o) lists[warp][0][lane] = best = lists_merged(best, lists[warp + o][0][lane], lane);
+        if (lane == 0) sh[warp][0] = r;
+        __syncthreads();
+        if (warp == 0) {
+            r = warp_join(lane < kWarps ? sh[lane][0] : none(), c);
+            if (lane == 0) done = finish_row(a, t, r);
         }
-        if (warp == 0) write_top(a, t, best, done[t], lane);
+        if (!a.top) continue;
+        uint64_t bound = block_merged(sorted(most, lane), lists, warp, lane);
+        if (warp == 0 && lane == a.top - 1) least = bound;
+        if (threadIdx.x == 0) chosen = 0;
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kEach; u++)               // 0: the block has none
+            if (best[u] && best[u] >= least) which[atomicAdd(&chosen, 1)] = (int)threadIdx.x + u * kFewThreads;
+        __syncthreads();
+        uint64_t mine = 0;
+        for (int k = warp; k < chosen; k += kWarps)
+            mine = lists_merged(mine, lane < a.top ? load_key(a.cand + ((int64_t)t * blocks + which[k]) * a.top + lane) : 0, lane);
+        mine = block_merged(mine, lists, warp, lane);
+        if (warp == 0) write_top(a, t, mine, done, lane);
     }
 }
 
@@ -472,42 +629,49 @@ zero_status_t cuda_failed(cudaError_t e, const char* what)
 
 int64_t strips_of(int64_t vocab) { return ceil_div(vocab, kBN) * 2; }
 
-// Rows at a time of a forward pass: what the strips leave (12 bytes each, and 9 and
-// up with alternatives) takes about 512 MiB.
-int64_t rows_at_once(int64_t tokens, int64_t vocab, int64_t top)
+// Entries whose logits are kept, so that every row has a threshold for the others'
+// alternatives: all of them where that is little (32 MB), or they are few.
+int64_t sampled_entries(int64_t rows, int64_t vocab, int64_t top)
 {
-    const int64_t per = strips_of(vocab) * (12 + (top ? 1 + 8 * top : 0));
+    if (!top) return 0;
+    return vocab <= kSample + kSample / 4 || rows * vocab <= (int64_t(1) << 23) ? vocab : kSample;
+}
+
+// Rows at a time of a forward pass: what the strips leave (12 bytes each, and 9 and
+// up with alternatives) and the logits that are kept take about 512 MiB.
+int64_t rows_at_once(int64_t vocab, int64_t top)
+{
+    const int64_t kept = vocab < kSample + kSample / 4 ? vocab : kSample + kSample / 4;
+    const int64_t per = strips_of(vocab) * (12 + (top ? 1 + 8 * top : 0)) + (top ? 4 * kept + 8 * top : 0);
     const int64_t fit = (int64_t(1) << 29) / per / kBM * kBM;
     return fit < kBM ? kBM : fit;
 }
 
-// Strips whose alternatives are found first, to give every row a threshold for the
-// others'; 0: all at once, each strip with its `top` largest.
-int sample_strips(int64_t rows, int64_t vocab, int64_t top)
-{
-    if (!top) return 0;
-    const int64_t tiles = ceil_div(rows, kBM) * ceil_div(vocab, kBN);
-    return tiles >= 76 * 6 && vocab >= 4 * kSampleStrips * kStrip ? kSampleStrips : 0;
-}
-
 // Byte offsets of a forward pass in the workspace.
 struct LpLayout {
-    int64_t target_logit, stat, least, part, part_t, count, cand, end;
+    int64_t target_logit, stat, least, part, part_t, logits, first, count, cand, end;
+    int64_t sampled, logit_stride;
+    int cand_strips, count_stride;
 };
 
 LpLayout lp_layout(const zero_lp_plan_t& p, bool few)
 {
     LpLayout l;
-    const int64_t rows = p.rows < p.tokens ? p.rows : p.tokens;
-    const int64_t strips = few ? kFewBlocks : strips_of(p.vocab);
+    const int64_t rows = p.rows < p.tokens ? p.rows : p.tokens, strips = strips_of(p.vocab);
+    l.sampled = few ? 0 : sampled_entries(rows, p.vocab, p.top);
+    l.logit_stride = (l.sampled + 3) / 4 * 4;
+    l.cand_strips = few ? kFewBlocks : p.top && l.sampled < p.vocab ? (int)(strips - l.sampled / kStrip) : 0;
+    l.count_stride = (l.cand_strips + 15) / 16 * 16;
     l.target_logit = sizeof(CeHead);
     l.stat = l.target_logit + up256(rows * 4);
     l.least = l.stat + up256(rows * 8);
     l.part = l.least + up256(rows * 4);
-    l.part_t = l.part + up256(strips * rows * (few ? (int64_t)sizeof(Stat) : 8));
-    l.count = l.part_t + (few ? 0 : up256(strips * rows * 4));
-    l.cand = l.count + (few || !p.top ? 0 : up256(strips * rows));
-    l.end = l.cand + up256(strips * rows * p.top * 8);
+    l.part_t = l.part + up256(few ? kFewBlocks * rows * (int64_t)sizeof(Stat) : strips * rows * 8);
+    l.logits = l.part_t + (few ? 0 : up256(strips * rows * 4));
+    l.first = l.logits + up256(rows * l.logit_stride * 4);
+    l.count = l.first + up256(rows * p.top * 8);
+    l.cand = l.count + (few ? 0 : up256(l.count_stride * rows));
+    l.end = l.cand + up256(l.cand_strips * rows * p.top * 8);
     return l;
 }
 
@@ -552,11 +716,13 @@ cudaError_t launch_few(const zero_lp_plan_t& p, int64_t blocks, const void* x, c
     }
 }
 
+// Warps to a row: 8 where there are strips for them and few rows.
 template <bool FINAL>
-cudaError_t launch_top(const LpArgs& a, int strips, cudaStream_t s)
+cudaError_t launch_first(const LpArgs& a, cudaStream_t s)
 {
-    if (a.n >= 8 * 152) return launch_after(k_lp_top<1, FINAL>, dim3((unsigned)ceil_div(a.n, 8)), 256, 0, s, a, strips);
-    return launch_after(k_lp_top<8, FINAL>, dim3((unsigned)a.n), 256, 0, s, a, strips);
+    if (a.n > 2 * 152 || a.sampled <= 64 * kStrip)
+        return launch_after(k_lp_first<1, FINAL>, dim3((unsigned)ceil_div(a.n, 8)), 256, 0, s, a);
+    return launch_after(k_lp_first<8, FINAL>, dim3((unsigned)a.n), 256, 0, s, a);
 }
 
 // The forward pass of rows [r0, r0 + a.n).
@@ -569,7 +735,8 @@ cudaError_t forward_rows(const zero_lp_plan_t& p, const void* x, const void* w, 
     std::memset(&g, 0, sizeof g);
     g.a_rows = a_rows_of(a.n);
     ok = make_map(&g.a, type, xr, a.n, p.hidden, p.x_stride, g.a_rows) &&
-         make_map(&g.b, type, w, p.vocab, p.hidden, p.w_stride, kBN / 2);
+         make_map(&g.b, type, w, p.vocab, p.hidden, p.w_stride, kBN / 2) &&
+         (!a.top || make_map(&g.c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.logits, a.n, a.sampled, a.logit_stride, 32));
     if (!ok) return cudaSuccess;
     g.m = a.n;
     g.m_tiles = (int)ceil_div(a.n, kBM);
@@ -581,30 +748,30 @@ cudaError_t forward_rows(const zero_lp_plan_t& p, const void* x, const void* w, 
     g.target_logit = reinterpret_cast<float*>(ws + l.target_logit);
     g.scale_log2e = a.scale * kLog2e;
     g.top = a.top;
-    g.strips = a.strips;
-    auto product = [&](int64_t v0, int64_t v1, const float* least) {
+    g.strips = a.cand_strips;
+    g.count_stride = a.count_stride;
+    g.cand = a.cand;
+    g.cand_count = const_cast<uint8_t*>(a.cand_count);
+    g.least = a.least;
+    auto product = [&](int64_t v0, int64_t v1) {
         const int64_t s0 = v0 / kStrip;
         g.b_y0 = (int)v0;
         g.n = v1 - v0;
         g.n_tiles = (int)ceil_div(g.n, kBN);
         g.part = const_cast<float2*>(a.part) + s0 * a.n;
         g.part_t = const_cast<float*>(a.part_t) + s0 * a.n;
-        g.cand = a.cand + s0 * a.top;
-        g.cand_count = const_cast<uint8_t*>(a.cand_count) + s0 * a.n;
-        g.least = least;
         g.withhold = first && v0 == 0 && withheld_product() > 0;
-        return a.top ? gemm<kEpiTop, false, false>(p.dtype, g, s) : gemm<kEpiStat, false, false>(p.dtype, g, s);
+        return !a.top ? gemm<kEpiStat, false, false>(p.dtype, g, s)
+               : v0 == 0 ? gemm<kEpiKeep, false, false>(p.dtype, g, s) : gemm<kEpiTop, false, false>(p.dtype, g, s);
     };
-    const int sample = sample_strips(a.n, p.vocab, a.top);
-    const int64_t v1 = (int64_t)sample * kStrip;
-    cudaError_t e = cudaSuccess;
-    if (sample) {
-        e = product(0, v1, nullptr);
-        if (e == cudaSuccess) e = launch_top<false>(a, sample, s);
+    const bool two = a.top && a.sampled < p.vocab;
+    cudaError_t e = product(0, two ? a.sampled : p.vocab);
+    if (two) {
+        if (e == cudaSuccess) e = launch_first<false>(a, s);
+        if (e == cudaSuccess) e = product(a.sampled, p.vocab);
     }
-    if (e == cudaSuccess) e = product(v1, p.vocab, sample ? a.least : nullptr);
-    if (e == cudaSuccess) e = launch_after(k_lp_join, dim3((unsigned)ceil_div(a.n, 32)), 1024, 0, s, a);
-    if (e == cudaSuccess && a.top) e = launch_top<true>(a, a.strips, s);
+    if (e == cudaSuccess) e = launch_after(k_lp_join, dim3((unsigned)ceil_div(a.n, kJoinRows)), kJoinThreads, 0, s, a);
+    if (e == cudaSuccess && a.top) e = two ? launch_after(k_lp_top, dim3((unsigned)ceil_div(a.n, kTopWarps)), 32 * kTopWarps, 0, s, a) : launch_first<true>(a, s);
     return e;
 }
 
@@ -634,7 +801,7 @@ zero_status_t zero_lp_plan(int64_t tokens, int64_t vocab, int64_t hidden, int32_
     out->dtype = dtype;
     out->splits = c.splits;
     out->top = top;
-    out->rows = rows_at_once(tokens, vocab, top);
+    out->rows = rows_at_once(vocab, top);
     const int64_t forward = lp_layout(*out, few_tokens(c)).end;
     out->workspace_bytes = forward > c.workspace_bytes ? forward : c.workspace_bytes;
     out->flops_forward = c.flops_forward;
@@ -685,8 +852,14 @@ zero_status_t zero_lp_forward(const zero_lp_plan_t* plan, const void* x, const v
         a.entropy = entropy ? entropy + r0 : nullptr;
         a.stat = reinterpret_cast<float2*>(ws + l.stat);
         a.top = p.top;
+        a.logits = reinterpret_cast<const float*>(ws + l.logits);
+        a.logit_stride = l.logit_stride;
+        a.sampled = l.sampled;
+        a.first = reinterpret_cast<uint64_t*>(ws + l.first);
         a.cand = reinterpret_cast<uint64_t*>(ws + l.cand);
         a.cand_count = ws + l.count;
+        a.cand_strips = l.cand_strips;
+        a.count_stride = l.count_stride;
         a.least = reinterpret_cast<float*>(ws + l.least);
         a.top_logp = top_logp + r0 * p.top;
         a.top_index = top_index + r0 * p.top;

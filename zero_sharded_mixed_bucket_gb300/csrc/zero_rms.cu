@@ -73,14 +73,22 @@ __device__ __forceinline__ float2 values2(uint32_t codes)
 
 __device__ __forceinline__ uint32_t magnitude(float f) { return __float_as_uint(f) & 0x7fffffffu; }
 
+// The largest of three magnitudes, NaN if one is.
+__device__ __forceinline__ float most_of(float a, float b, float c)
+{
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // ---- rows on 16-byte (or 4-byte) boundaries ---------------------------------------------
 // Dealt out as layer norm's: a group of lanes to a row, V vectors to a lane,
 // `take` rows (RB at most) at a time, copied ahead into per-lane slots.  The sum
 // x + r is rounded to the rows' type first (what the stream holds, and what
 // backward sees), then kept in registers; its slot is free for the next copy
-// before the group has its sum.  Q: 8-bit results besides; a block of 128 (32)
-// values is then 128 / VE neighbouring lanes of a warp.
-template <int DT, int L, int V, int RB, int S, int T, int BLOCKS, bool RAGGED, int ALIGN, bool Q>
+// before the group has its sum.  Q: values to a scale of 8-bit results, 0: none; a
+// block of them is Q / VE neighbouring lanes of a warp.
+template <int DT, int L, int V, int RB, int S, int T, int BLOCKS, bool RAGGED, int ALIGN, int Q>
 __global__ void __launch_bounds__(T, BLOCKS) k_rms_forward_rows(const __grid_constant__ RmsArgs a)
 {
     static_assert(!Q || L == 32, "blocks of values lie inside a warp");
@@ -185,16 +193,17 @@ __global__ void __launch_bounds__(T, BLOCKS) k_rms_forward_rows(const __grid_con
                 for (int k = 0; k < VE; k++)
                     f[k] = cnt[v] && (!RAGGED || k < cnt[v]) ? f[k] * ss[b] * w[k] : 0.0f;
                 if (a.y && b < here && cnt[v]) store_vec<DT, RAGGED, ALIGN>(p, pack<DT>(f), cnt[v]);
-                if constexpr (Q) {
-                    uint32_t most = 0;
+                if constexpr (Q > 0) {
+                    constexpr int kSpan = Q / VE;     // lanes of a block
+                    float most = 0.0f;
 #pragma unroll
-                    for (int k = 0; k < VE; k++)
-                        most = max(most, magnitude(f[k]));
-                    const int span = a.block / VE;    // lanes of a block
-                    for (int o = 1; o < span; o <<= 1)
-                        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+                    for (int k = 0; k < VE; k += 2)
+                        most = most_of(most, f[k], f[k + 1]);
+#pragma unroll
+                    for (int o = 1; o < kSpan; o <<= 1)
+                        most = most_of(most, 0.0f, __shfl_xor_sync(0xffffffffu, most, o));
                     if (b < here && cnt[v]) {
-                        const uint32_t e = scale_byte(most);
+                        const uint32_t e = scale_byte(__float_as_uint(most));
                         const float up = scale_up(e);
                         uint32_t c[VE / 4];
 #pragma unroll
@@ -211,7 +220,7 @@ __global__ void __launch_bounds__(T, BLOCKS) k_rms_forward_rows(const __grid_con
                             for (int k = 0; k < VE; k++)
                                 if (k < cnt[v]) at[k] = (uint8_t)(c[k >> 2] >> (8 * (k & 3)));
                         }
-                        if ((threadIdx.x & (span - 1)) == 0) a.q_scale[(r0 + b) * a.scale_cols + j / a.block] = (uint8_t)e;
+                        if ((threadIdx.x & (kSpan - 1)) == 0) a.q_scale[(r0 + b) * a.scale_cols + j / Q] = (uint8_t)e;
                     }
                 }
             }
@@ -693,29 +702,55 @@ __global__ void __launch_bounds__(1024) k_rms_dw_sum(const float* part, int bloc
 }
 
 // ---- read-out --------------------------------------------------------------------------
-// 8-bit results as bfloat16 values: 8 codes a thread where rows start on 8 bytes of
-// codes and 16 of values, else one.
+// 8-bit results as bfloat16 values.  N codes to a thread at once, 8 where rows start
+// on 8 bytes of codes and 16 of values, else one; blockDim.x threads along a row,
+// blockDim.y rows, and each thread kValuesRows of them, all read before any is written.
+constexpr int kValuesRows = 4;
+
 template <int N>
 __global__ void __launch_bounds__(256) k_rms_values(const __grid_constant__ RmsArgs a, uint16_t* out)
 {
-    const int64_t per = (a.dim + N - 1) / N;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.rows * per; i += (int64_t)gridDim.x * 256) {
-        const int64_t row = i / per, j = (i - row * per) * N;
-        const uint8_t* src = a.q + row * a.y_stride + j;
-        uint16_t* dst = out + row * a.y_stride + j;
-        const float up = scale_of(a.q_scale[row * a.scale_cols + j / a.block]);
-        if (N == 8 && j + 8 <= a.dim) {
-            const uint2 c = __ldcs(reinterpret_cast<const uint2*>(src));
-            uint32_t w[4];
+    const int64_t j = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * N;
+    if (j >= a.dim) return;
+    const int64_t step = blockDim.y;
+    for (int64_t r0 = (int64_t)blockIdx.y * step * kValuesRows + threadIdx.y; r0 < a.rows; r0 += gridDim.y * step * kValuesRows) {
+        uint2 c[kValuesRows];
+        uint32_t e[kValuesRows];
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
-                const float2 f = values2((k < 2 ? c.x : c.y) >> (16 * (k & 1)) & 0xffffu);
+        for (int b = 0; b < kValuesRows; b++) {
+            const int64_t r = r0 + b * step;
+            if (r >= a.rows) break;
+            const uint8_t* src = a.q + r * a.y_stride + j;
+            e[b] = a.q_scale[r * a.scale_cols + j / a.block];
+            if (N == 8 && j + 8 <= a.dim) {
+                c[b] = __ldcs(reinterpret_cast<const uint2*>(src));
+            } else {
+                c[b] = make_uint2(0, 0);
+                for (int k = 0; k < N && j + k < a.dim; k++) {
+                    if (k < 4) c[b].x |= (uint32_t)src[k] << (8 * k);
+                    else c[b].y |= (uint32_t)src[k] << (8 * (k - 4));
+                }
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < kValuesRows; b++) {
+            const int64_t r = r0 + b * step;
+            if (r >= a.rows) break;
+            uint16_t* dst = out + r * a.y_stride + j;
+            const float up = scale_of(e[b]);
+            uint32_t w[N / 2 + 1];
+#pragma unroll
+            for (int k = 0; k < (N + 1) / 2; k++) {
+                const float2 f = values2((k < 2 ? c[b].x : c[b].y) >> (16 * (k & 1)) & 0xffffu);
                 w[k] = from_f32x2<kBF16>(f.x * up, f.y * up);
             }
-            __stcs(reinterpret_cast<uint4*>(dst), make_uint4(w[0], w[1], w[2], w[3]));
-        } else {
-            for (int k = 0; k < N && j + k < a.dim; k++)
-                dst[k] = (uint16_t)from_f32<kBF16>(values2(src[k]).x * up);
+            if (N == 8 && j + 8 <= a.dim) {
+                __stcs(reinterpret_cast<uint4*>(dst), make_uint4(w[0], w[1], w[2], w[3]));
+            } else {
+#pragma unroll
+                for (int k = 0; k < N; k++)
+                    if (j + k < a.dim) dst[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+            }
         }
     }
 }
@@ -771,6 +806,14 @@ cudaError_t launch_slots(const RmsArgs& a, int64_t blocks, int threads, cudaStre
     return e == cudaSuccess ? launch_rms(KERNEL, a, blocks, threads, SMEM, s) : e;
 }
 
+template <int DT, int L, int V, int RB, int S, int T, int BLOCKS, bool RAGGED, int ALIGN, size_t SMEM>
+cudaError_t forward_codes(const RmsArgs& a, int64_t blocks, int threads, cudaStream_t s)
+{
+    if (!a.q) return launch_slots<k_rms_forward_rows<DT, L, V, RB, S, T, BLOCKS, RAGGED, ALIGN, 0>, SMEM>(a, blocks, threads, s);
+    return a.block == 32 ? launch_slots<k_rms_forward_rows<DT, L, V, RB, S, T, BLOCKS, RAGGED, ALIGN, 32>, SMEM>(a, blocks, threads, s)
+                         : launch_slots<k_rms_forward_rows<DT, L, V, RB, S, T, BLOCKS, RAGGED, ALIGN, 128>, SMEM>(a, blocks, threads, s);
+}
+
 template <int DT, int L, int V, int RB, int S, int T, int BLOCKS>
 cudaError_t forward_rows(RmsArgs a, int64_t vecs, int align, cudaStream_t s)
 {
@@ -782,15 +825,12 @@ cudaError_t forward_rows(RmsArgs a, int64_t vecs, int align, cudaStream_t s)
     constexpr size_t smem = (size_t)S * RB * V * 2 * T * 16;
     if constexpr (L == 32) {                          // fewer lanes: whole rows on 16-byte boundaries only
         if constexpr (DT != kF32)
-            if (align < 16)
-                return a.q ? launch_slots<k_rms_forward_rows<DT, L, V, RB, S, T, BLOCKS, true, 4, true>, smem>(a, blocks, h.threads, s)
-                           : launch_slots<k_rms_forward_rows<DT, L, V, RB, S, T, BLOCKS, true, 4, false>, smem>(a, blocks, h.threads, s);
-        if (a.dim % kVecOf<DT>)
-            return a.q ? launch_slots<k_rms_forward_rows<DT, L, V, RB, S, T, BLOCKS, true, 16, true>, smem>(a, blocks, h.threads, s)
-                       : launch_slots<k_rms_forward_rows<DT, L, V, RB, S, T, BLOCKS, true, 16, false>, smem>(a, blocks, h.threads, s);
-        if (a.q) return launch_slots<k_rms_forward_rows<DT, L, V, RB, S, T, BLOCKS, false, 16, true>, smem>(a, blocks, h.threads, s);
+            if (align < 16) return forward_codes<DT, L, V, RB, S, T, BLOCKS, true, 4, smem>(a, blocks, h.threads, s);
+        if (a.dim % kVecOf<DT>) return forward_codes<DT, L, V, RB, S, T, BLOCKS, true, 16, smem>(a, blocks, h.threads, s);
+        return forward_codes<DT, L, V, RB, S, T, BLOCKS, false, 16, smem>(a, blocks, h.threads, s);
+    } else {
+        return launch_slots<k_rms_forward_rows<DT, L, V, RB, S, T, BLOCKS, false, 16, 0>, smem>(a, blocks, h.threads, s);
     }
-    return launch_slots<k_rms_forward_rows<DT, L, V, RB, S, T, BLOCKS, false, 16, false>, smem>(a, blocks, h.threads, s);
 }
 
 // Warps to a row of 128-value blocks, K / 4 of them to a warp; groups and threads of a block.
@@ -820,8 +860,8 @@ cudaError_t forward(const RmsArgs& a, int align, cudaStream_t s)
     constexpr int VE = kVecOf<DT>, T = kRowThreads;
     const int64_t vecs = (a.dim + VE - 1) / VE;
     const bool whole = a.dim % VE == 0 && align == 16 && !a.q;
-    if (whole && vecs <= 8) return forward_rows<DT, 8, 1, 4, 2, T, 3>(a, vecs, align, s);
-    if (whole && vecs <= 16) return forward_rows<DT, 16, 1, 4, 2, T, 3>(a, vecs, align, s);
+    if (whole && vecs <= 8) return forward_rows<DT, 8, 1, 4, 2, T, 2>(a, vecs, align, s);
+    if (whole && vecs <= 16) return forward_rows<DT, 16, 1, 4, 2, T, 2>(a, vecs, align, s);
     if (align == 16 || (DT != kF32 && align == 4 && vecs > 64)) {
         if (vecs <= 256) return forward_rows<DT, 32, 1, 4, 2, T, 3>(a, vecs, align, s);
         if (vecs <= 512) return forward_rows<DT, 32, 2, 2, 2, T, 3>(a, vecs, align, s);
@@ -1030,10 +1070,13 @@ zero_status_t zero_rms_values(const zero_rms_plan_t* plan, const void* q, const 
     a.q_scale = const_cast<uint8_t*>(q_scale);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool wide = aligned_to(q, 8) && aligned_to(values, 16) && plan->y_stride % 8 == 0;
-    const int64_t n = plan->rows * (wide ? (plan->dim + 7) / 8 : plan->dim), most = (int64_t)kSms * 8;
-    const unsigned grid = (unsigned)blocks_for(n, 256, most);
-    if (wide) k_rms_values<8><<<grid, 256, 0, s>>>(a, static_cast<uint16_t*>(values));
-    else k_rms_values<1><<<grid, 256, 0, s>>>(a, static_cast<uint16_t*>(values));
+    const int64_t per = wide ? (plan->dim + 7) / 8 : plan->dim;
+    unsigned along = 32;
+    while (along < 256 && along < per) along *= 2;
+    const int64_t high = (plan->rows + 256 / along * kValuesRows - 1) / (256 / along * kValuesRows);
+    const dim3 block(along, 256 / along), grid((unsigned)((per + along - 1) / along), (unsigned)(high < 65535 ? high : 65535));
+    if (wide) k_rms_values<8><<<grid, block, 0, s>>>(a, static_cast<uint16_t*>(values));
+    else k_rms_values<1><<<grid, block, 0, s>>>(a, static_cast<uint16_t*>(values));
     const cudaError_t err = cudaGetLastError();
     return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_rms_values");
 }
