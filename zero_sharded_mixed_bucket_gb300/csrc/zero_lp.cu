@@ -237,7 +237,7 @@ __device__ __forceinline__ void write_top(const LpArgs& a, int64_t i, uint64_t l
 template <int W, bool FINAL>
 __global__ void __launch_bounds__(256) k_lp_first(const __grid_constant__ LpArgs a)
 {
-    constexpr int U = 4;                              // strips on their way
+    constexpr int U = 8;                              // strips on their way
     wait_prev_grid();
     if constexpr (!FINAL) allow_next_grid();
     __shared__ uint64_t sh[8][32], held[8][64];
@@ -274,10 +274,16 @@ __global__ void __launch_bounds__(256) k_lp_first(const __grid_constant__ LpArgs
 #pragma unroll
                 for (int u = 0; u < U; u++) {
                     const float f[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+                    // a lane seldom has two: the next of all lanes that have one, again and again
+                    unsigned in = 0;
 #pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        const bool in = at[u] + k < a.sampled && f[k] >= least;
-                        g.add(in, key_of(f[k], (uint32_t)(at[u] + k)), lane);
+                    for (int k = 0; k < 4; k++)
+                        if (at[u] + k < a.sampled && f[k] >= least) in |= 1u << k;
+                    while (__any_sync(kAll, in)) {
+                        const int k = in ? __ffs(in) - 1 : 0;
+                        const float v = k == 0 ? f[0] : k == 1 ? f[1] : k == 2 ? f[2] : f[3];
+                        g.add(in, key_of(v, (uint32_t)(at[u] + k)), lane);
+                        in &= in - 1;
                     }
                 }
             }
