@@ -78,6 +78,14 @@ __device__ __forceinline__ __nv_bfloat162 scale_of(uint32_t e, uint32_t& rest)
     return *reinterpret_cast<const __nv_bfloat162*>(&two);
 }
 
+// A pair of values times 2^rest.
+__device__ __forceinline__ uint32_t scaled_more(uint32_t v, uint32_t rest)
+{
+    const uint32_t one = (rest + 127u) << 7, two = one | one << 16;
+    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&two));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 __device__ __forceinline__ uint32_t magnitude(float f) { return __float_as_uint(f) & 0x7fffffffu; }
 
 // The largest of three magnitudes, NaN if one is.
@@ -129,17 +137,16 @@ __device__ __forceinline__ Vals<DT> weight_held(const void* p, int64_t i, int cn
     return v;
 }
 
-// ---- rows on 16-byte (or 4-byte) boundaries ---------------------------------------------
+// ---- rows on 16-byte boundaries -----------------------------------------------------------
 // Dealt out as layer norm's: a group of lanes to a row, V vectors to a lane,
 // `take` rows (RB at most) at a time, copied ahead into per-lane slots.  The sum
 // x + r is rounded to the rows' type first (what the stream holds, and what
 // backward sees), then kept in registers; its slot is free for the next copy
 // before the group has its sum.  Q: values to a scale of 8-bit results, 0: none; a
-// block of them is Q / VE neighbouring lanes of a warp.
-template <int DT, int L, int V, int RB, int S, int T, int BLOCKS, bool RAGGED, int ALIGN, int Q>
+// block of them is Q / VE neighbouring lanes of a warp, or the row.
+template <int DT, int L, int V, int RB, int S, int T, int BLOCKS, bool RAGGED, int Q>
 __global__ void __launch_bounds__(T, BLOCKS) k_rms_forward_rows(const __grid_constant__ RmsArgs a)
 {
-    static_assert(!Q || L == 32, "blocks of values lie inside a warp");
     constexpr int VE = kVecOf<DT>, E = DT == kF32 ? 4 : 2;
     constexpr bool kHold = V <= 4;
     extern __shared__ uint4 slots[];                  // [S][RB * V][x, r][T]
@@ -174,8 +181,8 @@ __global__ void __launch_bounds__(T, BLOCKS) k_rms_forward_rows(const __grid_con
                 for (int v = 0; v < V; v++)
                     if (cnt[v]) {
                         uint4* p = at + (b * V + v) * 2 * T;
-                        vec_ahead<ALIGN>(p, px + v * apart, RAGGED ? cnt[v] * E : 16);
-                        if (add) vec_ahead<ALIGN>(p + T, pr + v * apart, RAGGED ? cnt[v] * E : 16);
+                        vec_ahead<16>(p, px + v * apart, RAGGED ? cnt[v] * E : 16);
+                        if (add) vec_ahead<16>(p + T, pr + v * apart, RAGGED ? cnt[v] * E : 16);
                     }
         copies_issued();
         ahead += stride;
@@ -219,7 +226,7 @@ __global__ void __launch_bounds__(T, BLOCKS) k_rms_forward_rows(const __grid_con
             for (int b = 0; b < RB; b++, p += x_row)
 #pragma unroll
                 for (int v = 0; v < V; v++)
-                    if (b < here && cnt[v]) store_vec<DT, RAGGED, ALIGN>(p + v * apart, h[b][v], cnt[v]);
+                    if (b < here && cnt[v]) store_vec<DT, RAGGED, 16>(p + v * apart, h[b][v], cnt[v]);
         }
         group_sum<L, RB, T>(ss, a.warps, sh, turn, [&](float t) { return rsqrtf(fmaf(t, inv, a.eps)); });
 #pragma unroll
@@ -236,9 +243,9 @@ __global__ void __launch_bounds__(T, BLOCKS) k_rms_forward_rows(const __grid_con
 #pragma unroll
                 for (int k = 0; k < VE; k++)
                     f[k] = f[k] * ss[b] * w[k];
-                if (a.y && b < here && cnt[v]) store_vec<DT, RAGGED, ALIGN>(p, pack<DT>(f), cnt[v]);
+                if (a.y && b < here && cnt[v]) store_vec<DT, RAGGED, 16>(p, pack<DT>(f), cnt[v]);
                 if constexpr (Q > 0) {
-                    constexpr int kSpan = Q / VE;     // lanes of a block
+                    constexpr int kSpan = Q / VE < L ? Q / VE : L;            // lanes of a block; a shorter row is one
                     float most = 0.0f;
 #pragma unroll
                     for (int k = 0; k < VE; k += 2)
@@ -282,7 +289,7 @@ __global__ void __launch_bounds__(T, BLOCKS) k_rms_forward_rows(const __grid_con
 // Backward: the stream's gradient of the rows, and the column sums of dy * xhat
 // over all the rows of a lane in registers, so h and dy are read once for both.
 // A block writes one partial sum per column (its groups joined in group order).
-template <int DT, int L, int V, int RB, int S, int T, int BLOCKS, bool RAGGED, int ALIGN>
+template <int DT, int L, int V, int RB, int S, int T, int BLOCKS, bool RAGGED>
 __global__ void __launch_bounds__(T, BLOCKS) k_rms_backward_rows(const __grid_constant__ RmsArgs a)
 {
     constexpr int VE = kVecOf<DT>, E = DT == kF32 ? 4 : 2;
@@ -325,9 +332,9 @@ __global__ void __launch_bounds__(T, BLOCKS) k_rms_backward_rows(const __grid_co
                 uint4* p = at + (b * V + v) * 3 * T;
                 if (b < here) {
                     if (cnt[v]) {
-                        vec_ahead<ALIGN>(p, px + v * apart, RAGGED ? cnt[v] * E : 16);
-                        vec_ahead<ALIGN>(p + T, py + v * apart, RAGGED ? cnt[v] * E : 16);
-                        if (add) vec_ahead<ALIGN>(p + 2 * T, pr + v * apart, RAGGED ? cnt[v] * E : 16);
+                        vec_ahead<16>(p, px + v * apart, RAGGED ? cnt[v] * E : 16);
+                        vec_ahead<16>(p + T, py + v * apart, RAGGED ? cnt[v] * E : 16);
+                        if (add) vec_ahead<16>(p + 2 * T, pr + v * apart, RAGGED ? cnt[v] * E : 16);
                     }
                 } else {                              // rows past the end: all 0
                     p[0] = p[T] = make_uint4(0, 0, 0, 0);
@@ -419,7 +426,7 @@ __global__ void __launch_bounds__(T, BLOCKS) k_rms_backward_rows(const __grid_co
                         for (int k = 0; k < VE; k++)
                             xf[k] *= rstd[b];
                     }
-                    if (b < here) store_vec<DT, RAGGED, ALIGN>(p, pack<DT>(xf), cnt[v]);
+                    if (b < here) store_vec<DT, RAGGED, 16>(p, pack<DT>(xf), cnt[v]);
                 }
             }
         }
@@ -456,39 +463,51 @@ __global__ void __launch_bounds__(T, BLOCKS) k_rms_backward_rows(const __grid_co
 }
 
 // ---- other rows ------------------------------------------------------------------------
-// One access a value.  A group of warps to a row, each warp blocks of 128
-// neighbouring values, four of a block to a lane, 32 apart: neighbouring lanes
-// neighbouring values, and a block's largest magnitude stays inside the warp.
-// Place of a lane's value k:
-__device__ __forceinline__ int place(int k, int warp, int warps, int lane)
-{
-    return ((k >> 2) * warps + warp) * 128 + (k & 3) * 32 + lane;
-}
+// One access a value.  W warps to a row (known to the compiler, so that a lane's places
+// are distances from one address), each with blocks of 128 neighbouring values, four
+// of a block to a lane, 32 apart: neighbouring lanes neighbouring values, and a
+// block's largest magnitude stays inside the warp.
+template <int W>
+__host__ __device__ constexpr int place(int k) { return (k >> 2) * W * 128 + (k & 3) * 32; }
 
-template <int DT, int K>
-__device__ __forceinline__ void ld_places(const void* p, int64_t at, int dim, int warp, int warps, int lane, float f[K])
+constexpr int kAnyResident = 1024;                    // threads on an SM
+
+// Values of the lane that are `left` or more places before the row's end; 0 for the rest.
+template <int DT, int K, int W>
+__device__ __forceinline__ void ld_places(const char* p, int left, float f[K])
 {
-    // loads without branches, so that all of them are on their way at once: past
-    // the row's end its first value again, dropped
-    const char* row = static_cast<const char*>(p) + at * (DT == kF32 ? 4 : 2);
+    constexpr int E = DT == kF32 ? 4 : 2;
 #pragma unroll
     for (int k = 0; k < K; k++) {
-        const int j = place(k, warp, warps, lane);
-        f[k] = ld1<DT>(row, j < dim ? j : 0);
+        uint32_t u = 0;
+        if (place<W>(k) < left) {
+            if constexpr (DT == kF32) u = *reinterpret_cast<const uint32_t*>(p + place<W>(k) * E);
+            else u = *reinterpret_cast<const uint16_t*>(p + place<W>(k) * E);
+        }
+        f[k] = to_f32<DT>(u);
     }
-#pragma unroll
-    for (int k = 0; k < K; k++)
-        if (place(k, warp, warps, lane) >= dim) f[k] = 0.0f;
 }
 
-// 8-bit results of a block of 128 values, f[k] at j0 + 32 k + lane.
-__device__ __forceinline__ void codes_out(const RmsArgs& a, int64_t row, int64_t j0, int lane, const float f[4])
+template <int DT, int K, int W>
+__device__ __forceinline__ void st_places(char* p, int left, const float f[K])
+{
+    constexpr int E = DT == kF32 ? 4 : 2;
+#pragma unroll
+    for (int k = 0; k < K; k++)
+        if (place<W>(k) < left) st1<DT>(p + place<W>(k) * E, 0, f[k]);
+}
+
+// 8-bit results of a block of 128 values of which the lane's are 32 apart and `left`
+// or more places before the row's end; q and q_scale: of the lane's first, and of the
+// block's first scale.
+template <int BLOCK>
+__device__ __forceinline__ void codes_out(uint8_t* q, uint8_t* q_scale, int left, int lane, const float f[4])
 {
     uint32_t most[4], e[4];
 #pragma unroll
     for (int k = 0; k < 4; k++)
-        most[k] = j0 + 32 * k + lane < a.dim ? magnitude(f[k]) : 0u;
-    if (a.block == 128) {
+        most[k] = 32 * k < left ? magnitude(f[k]) : 0u;
+    if (BLOCK == 128) {
         e[0] = scale_byte(__reduce_max_sync(0xffffffffu, max(max(most[0], most[1]), max(most[2], most[3]))));
         e[1] = e[2] = e[3] = e[0];
     } else {
@@ -496,39 +515,47 @@ __device__ __forceinline__ void codes_out(const RmsArgs& a, int64_t row, int64_t
         for (int k = 0; k < 4; k++)
             e[k] = scale_byte(__reduce_max_sync(0xffffffffu, most[k]));
     }
-    uint8_t* at = a.q + row * a.y_stride;
 #pragma unroll
     for (int k = 0; k < 4; k++) {
-        const int64_t j = j0 + 32 * k + lane;
-        if (j >= a.dim) break;
-        at[j] = (uint8_t)code1(f[k] * scale_up(e[k]));
-        if (j % a.block == 0) a.q_scale[row * a.scale_cols + j / a.block] = (uint8_t)e[k];
+        if (32 * k < left) q[32 * k] = (uint8_t)code1(f[k] * scale_up(e[k]));
+        if ((BLOCK == 32 || k == 0) && lane == 0 && 32 * k < left) q_scale[k] = (uint8_t)e[k];
     }
 }
 
-template <int DT, int K, int RB, int T>
-__global__ void __launch_bounds__(T, 512 / T) k_rms_forward_any(const __grid_constant__ RmsArgs a)
+template <int DT, int K, int W, int RB, int T>
+__global__ void __launch_bounds__(T, (K > 16 ? 512 : 1024) / T) k_rms_forward_any(const __grid_constant__ RmsArgs a)
 {
+    constexpr int E = DT == kF32 ? 4 : 2;
     __shared__ float sh[2 * (T / 32) * RB];
-    const int lane = threadIdx.x & 31, warps = a.warps, group = (int)(threadIdx.x >> 5) / warps, warp = (int)(threadIdx.x >> 5) % warps;
-    const int groups = blockDim.x / (32 * warps), dim = (int)a.dim;
+    const int lane = threadIdx.x & 31, group = (int)(threadIdx.x >> 5) / W, warp = (int)(threadIdx.x >> 5) % W;
+    const int groups = T / (32 * W), j0 = warp * 128 + lane, left = (int)a.dim - j0;
     const float inv = 1.0f / (float)a.dim;
     int turn = 0;
+    float w[K];
+    auto weights = [&]() {
+        if (a.weight) {
+            ld_places<DT, K, W>(static_cast<const char*>(a.weight) + j0 * E, left, w);
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; k++)
+                w[k] = 1.0f;
+        }
+    };
+    if (K <= 16) weights();
+    const int64_t x_row = a.x_stride * E, y_row = a.y_stride * E;
     const int64_t stride = (int64_t)gridDim.x * groups * a.take;
     for (int64_t r0 = ((int64_t)blockIdx.x * groups + group) * a.take; r0 < a.rows; r0 += stride) {
         const int rows = rows_here(a.rows, r0, a.take);
+        const int64_t x_at = r0 * x_row + j0 * E, y_at = r0 * y_row + j0 * E;
         float f[RB][K], ss[RB];
 #pragma unroll
-        for (int b = 0; b < RB; b++) {
-            const int64_t at = (r0 + min(b, rows - 1)) * a.x_stride;         // past the end: not written
-            ld_places<DT, K>(a.x, at, dim, warp, warps, lane, f[b]);
-        }
+        for (int b = 0; b < RB; b++)                  // rows past the end: the last again, not written
+            ld_places<DT, K, W>(static_cast<const char*>(a.x) + x_at + min(b, rows - 1) * x_row, left, f[b]);
         if (a.r) {
 #pragma unroll
             for (int b = 0; b < RB; b++) {
-                const int64_t at = (r0 + min(b, rows - 1)) * a.x_stride;
                 float g[K];
-                ld_places<DT, K>(a.r, at, dim, warp, warps, lane, g);
+                ld_places<DT, K, W>(static_cast<const char*>(a.r) + x_at + min(b, rows - 1) * x_row, left, g);
 #pragma unroll
                 for (int k = 0; k < K; k++)
                     f[b][k] = to_f32<DT>(from_f32<DT>(f[b][k] + g[k]));
@@ -540,109 +567,104 @@ __global__ void __launch_bounds__(T, 512 / T) k_rms_forward_any(const __grid_con
 #pragma unroll
             for (int k = 0; k < K; k++)
                 ss[b] = fmaf(f[b][k], f[b][k], ss[b]);
+            if (a.h && b < rows) st_places<DT, K, W>(static_cast<char*>(a.h) + x_at + b * x_row, left, f[b]);
         }
-        if (a.h) {
+        group_sum<32, RB, T>(ss, W, sh, turn, [&](float t) { return rsqrtf(fmaf(t, inv, a.eps)); });
+        if (K > 16) weights();
 #pragma unroll
-            for (int b = 0; b < RB; b++)
+        for (int b = 0; b < RB; b++) {
 #pragma unroll
-                for (int k = 0; k < K; k++) {
-                    const int j = place(k, warp, warps, lane);
-                    if (b < rows && j < dim) st1<DT>(a.h, (r0 + b) * a.x_stride + j, f[b][k]);
+            for (int k = 0; k < K; k++)
+                f[b][k] = f[b][k] * ss[b] * w[k];
+            if (b >= rows) continue;
+            if (a.y) st_places<DT, K, W>(static_cast<char*>(a.y) + y_at + b * y_row, left, f[b]);
+            if (a.q) {
+                uint8_t* q = a.q + (r0 + b) * a.y_stride + j0;
+                uint8_t* q_scale = a.q_scale + (r0 + b) * a.scale_cols;
+#pragma unroll
+                for (int k = 0; k < K; k += 4) {
+                    if (a.block == 128)
+                        codes_out<128>(q + place<W>(k), q_scale + (k >> 2) * W + warp, left - place<W>(k), lane, f[b] + k);
+                    else
+                        codes_out<32>(q + place<W>(k), q_scale + 4 * ((k >> 2) * W + warp), left - place<W>(k), lane, f[b] + k);
                 }
-        }
-        group_sum<32, RB, T>(ss, warps, sh, turn, [&](float t) { return rsqrtf(fmaf(t, inv, a.eps)); });
-#pragma unroll
-        for (int k = 0; k < K; k++) {
-            const int j = place(k, warp, warps, lane);
-            const float w = !a.weight ? 1.0f : ld1<DT>(a.weight, j < dim ? j : 0);
-#pragma unroll
-            for (int b = 0; b < RB; b++) {
-                f[b][k] = f[b][k] * ss[b] * w;
-                if (a.y && b < rows && j < dim) st1<DT>(a.y, (r0 + b) * a.y_stride + j, f[b][k]);
             }
-        }
-        if (a.q) {
-#pragma unroll
-            for (int b = 0; b < RB; b++)
-#pragma unroll
-                for (int k = 0; k < K; k += 4)
-                    if (b < rows) codes_out(a, r0 + b, ((k >> 2) * warps + warp) * 128, lane, f[b] + k);
-        }
-        if (lane == 0 && warp == 0 && a.rstd) {
-#pragma unroll
-            for (int b = 0; b < RB; b++)
-                if (b < rows) a.rstd[r0 + b] = ss[b];
+            if (lane == 0 && warp == 0 && a.rstd) a.rstd[r0 + b] = ss[b];
         }
     }
 }
 
-template <int DT, int K, int T>
-__global__ void __launch_bounds__(T, 512 / T) k_rms_backward_any(const __grid_constant__ RmsArgs a)
+template <int DT, int K, int W, int RB, int T>
+__global__ void __launch_bounds__(T, kAnyResident / T) k_rms_backward_any(const __grid_constant__ RmsArgs a)
 {
-    __shared__ float sh[2 * (T / 32)];
-    __shared__ float join[K <= 8 ? T * K : 1];        // [warp][K][32]
-    const int lane = threadIdx.x & 31, warps = a.warps, group = (int)(threadIdx.x >> 5) / warps, warp = (int)(threadIdx.x >> 5) % warps;
-    const int groups = blockDim.x / (32 * warps), dim = (int)a.dim;
+    constexpr int E = DT == kF32 ? 4 : 2, kGroups = T / (32 * W);
+    __shared__ float sh[2 * (T / 32) * RB];
+    __shared__ float join[kGroups > 1 ? T * K : 1];   // [warp][K][32]
+    const int lane = threadIdx.x & 31, group = (int)(threadIdx.x >> 5) / W, warp = (int)(threadIdx.x >> 5) % W;
+    const int j0 = warp * 128 + lane, left = (int)a.dim - j0;
     const float inv = 1.0f / (float)a.dim;
     int turn = 0;
-    float dw[K];
+    float dw[K], w[K];
 #pragma unroll
-    for (int k = 0; k < K; k++)
+    for (int k = 0; k < K; k++) {
         dw[k] = 0.0f;
-    const int64_t stride = (int64_t)gridDim.x * groups;
-    for (int64_t row = (int64_t)blockIdx.x * groups + group; row < a.rows; row += stride) {
-        float n[K], g[K], c[1] = {0.0f};
-        ld_places<DT, K>(a.x, row * a.x_stride, dim, warp, warps, lane, n);
-        ld_places<DT, K>(a.dy, row * a.y_stride, dim, warp, warps, lane, g);
-        const float rstd = a.rstd_in[row];
+        w[k] = 1.0f;
+    }
+    if (a.weight) ld_places<DT, K, W>(static_cast<const char*>(a.weight) + j0 * E, left, w);
+    const int64_t x_row = a.x_stride * E, y_row = a.y_stride * E, stride = (int64_t)gridDim.x * kGroups * RB;
+    for (int64_t r0 = ((int64_t)blockIdx.x * kGroups + group) * RB; r0 < a.rows; r0 += stride) {
+        const int64_t x_at = r0 * x_row + j0 * E, y_at = r0 * y_row + j0 * E;
+        float n[RB][K], g[RB][K], r[RB][K], rstd[RB], c[RB];
 #pragma unroll
-        for (int k = 0; k < K; k++) {
-            n[k] *= rstd;                             // xhat; 0 past the end
-            dw[k] = fmaf(g[k], n[k], dw[k]);
+        for (int b = 0; b < RB; b++) {                // rows past the end: none of their places is there
+            const bool there = RB == 1 || r0 + b < a.rows;
+            const int here = there ? left : 0;
+            ld_places<DT, K, W>(static_cast<const char*>(a.x) + x_at + b * x_row, here, n[b]);
+            ld_places<DT, K, W>(static_cast<const char*>(a.dy) + y_at + b * y_row, here, g[b]);
+            if (a.r) ld_places<DT, K, W>(static_cast<const char*>(a.r) + x_at + b * x_row, here, r[b]);
+            rstd[b] = there ? a.rstd_in[r0 + b] : 0.0f;
+        }
+#pragma unroll
+        for (int b = 0; b < RB; b++) {
+            c[b] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < K; k++) {
+                n[b][k] *= rstd[b];                   // xhat; 0 past the end
+                dw[k] = fmaf(g[b][k], n[b][k], dw[k]);
+                g[b][k] *= w[k];
+                c[b] = fmaf(g[b][k], n[b][k], c[b]);
+            }
         }
         if (!a.dx) continue;
+        group_sum<32, RB, T>(c, W, sh, turn, [&](float t) { return t * -inv; });
 #pragma unroll
-        for (int k = 0; k < K; k++) {
-            const int j = place(k, warp, warps, lane);
-            if (a.weight) g[k] *= ld1<DT>(a.weight, j < dim ? j : 0);
-            c[0] = fmaf(g[k], n[k], c[0]);
-        }
-        group_sum<32, 1, T>(c, warps, sh, turn, [&](float t) { return t * -inv; });
+        for (int b = 0; b < RB; b++) {
 #pragma unroll
-        for (int k = 0; k < K; k++)
-            g[k] = fmaf(n[k], c[0], g[k]) * rstd;
-        if (a.r) {
-            ld_places<DT, K>(a.r, row * a.x_stride, dim, warp, warps, lane, n);
-#pragma unroll
-            for (int k = 0; k < K; k++)
-                g[k] += n[k];
-        }
-#pragma unroll
-        for (int k = 0; k < K; k++) {
-            const int j = place(k, warp, warps, lane);
-            if (j < dim) st1<DT>(a.dx, row * a.x_stride + j, g[k]);
+            for (int k = 0; k < K; k++) {
+                g[b][k] = fmaf(n[b][k], c[b], g[b][k]);
+                g[b][k] = a.r ? fmaf(g[b][k], rstd[b], r[b][k]) : g[b][k] * rstd[b];
+            }
+            st_places<DT, K, W>(static_cast<char*>(a.dx) + x_at + b * x_row, RB == 1 || r0 + b < a.rows ? left : 0, g[b]);
         }
     }
     if (!a.part) return;
     float* pw = a.part + (int64_t)blockIdx.x * a.dim;
-    if (K <= 8 && groups > 1) {
+    if constexpr (kGroups > 1) {
 #pragma unroll
         for (int k = 0; k < K; k++)
             join[((threadIdx.x >> 5) * K + k) * 32 + lane] = dw[k];
         __syncthreads();
-        for (int t = threadIdx.x; t < warps * K * 32; t += blockDim.x) {
-            const int w = t / (K * 32), k = t / 32 % K, j = place(k, w, warps, t % 32);
+        for (int t = threadIdx.x; t < W * K * 32; t += T) {
+            const int of = t / (K * 32), k = t / 32 % K, j = of * 128 + place<W>(k) + t % 32;
             float s = 0.0f;
-            for (int g = 0; g < groups; g++)
-                s += join[((g * warps + w) * K + k) * 32 + t % 32];
-            if (j < dim) pw[j] = s;
+            for (int g = 0; g < kGroups; g++)
+                s += join[((g * W + of) * K + k) * 32 + t % 32];
+            if (j < a.dim) pw[j] = s;
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < K; k++) {
-            const int j = place(k, warp, warps, lane);
-            if (j < dim) pw[j] = dw[k];
-        }
+        for (int k = 0; k < K; k++)
+            if (place<W>(k) < left) pw[j0 + place<W>(k)] = dw[k];
     }
 }
 
@@ -696,7 +718,12 @@ __global__ void __launch_bounds__(kLongThreads) k_rms_forward_long(const __grid_
                 f[k] = ld1<DT>(h, xo + j) * rstd * (a.weight ? ld1<DT>(a.weight, j) : 1.0f);
                 if (a.y) st1<DT>(a.y, yo + j, f[k]);
             }
-            if (a.q) codes_out(a, r, j0, lane, f);
+            if (a.q) {
+                const int left = (int)(a.dim - j0) - lane;
+                uint8_t* q = a.q + yo + j0 + lane;
+                if (a.block == 128) codes_out<128>(q, a.q_scale + r * a.scale_cols + j0 / 128, left, lane, f);
+                else codes_out<32>(q, a.q_scale + r * a.scale_cols + j0 / 32, left, lane, f);
+            }
         }
         if (threadIdx.x == 0 && a.rstd) a.rstd[r] = rstd;
     }
@@ -763,15 +790,44 @@ __global__ void __launch_bounds__(1024) k_rms_dw_sum(const float* part, int bloc
 }
 
 // ---- read-out --------------------------------------------------------------------------
-// 8-bit results as bfloat16 values.  N codes to a thread at once: 16 where rows start
-// on 16 bytes and end on them, else one; blockDim.x threads along a row,
-// blockDim.y rows, and each thread kValuesRows of them, all read before any is written.
+// 8-bit results as bfloat16 values.  Rows that start and end on 16 codes: 16 to a
+// thread at once; blockDim.x threads along a row, blockDim.y rows, and each thread
+// kValuesRows of them, all read before any is written.
 constexpr int kValuesRows = 4;
 
-template <int N>
+// Other rows: a warp 256 values of one, a code a lane at a time.
+__global__ void __launch_bounds__(256) k_rms_values_any(const __grid_constant__ RmsArgs a, uint16_t* out, int64_t per)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = (int64_t)gridDim.x * 8, all = a.rows * per;
+    for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < all; i += warps) {
+        const int64_t row = i / per;
+        const int j0 = (int)(i - row * per) * 256, left = (int)a.dim - j0 - lane;
+        const uint8_t* src = a.q + row * a.y_stride + j0 + lane;
+        const uint8_t* scale = a.q_scale + row * a.scale_cols + (a.block == 32 ? j0 >> 5 : j0 >> 7);
+        uint16_t* dst = out + row * a.y_stride + j0 + lane;
+        uint32_t c[8], e[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            if (32 * k < left) {
+                c[k] = src[32 * k];
+                e[k] = scale[a.block == 32 ? k : k >> 2];
+            }
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            if (32 * k < left) {
+                uint32_t rest;
+                __nv_bfloat162 up = scale_of(e[k], rest);
+                uint32_t v = values2(c[k] << 8, up);
+                if (rest) v = scaled_more(v, rest);
+                dst[32 * k] = (uint16_t)v;
+            }
+    }
+}
+
 __global__ void __launch_bounds__(256) k_rms_values(const __grid_constant__ RmsArgs a, uint16_t* out)
 {
-    const int j = (int)(blockIdx.x * blockDim.x + threadIdx.x) * N;
+    const int j = (int)(blockIdx.x * blockDim.x + threadIdx.x) * 16;
     if (j >= a.dim) return;
     const int64_t step = blockDim.y, apart = step * a.y_stride, scales_apart = step * a.scale_cols;
     for (int64_t r0 = (int64_t)blockIdx.y * step * kValuesRows + threadIdx.y; r0 < a.rows; r0 += gridDim.y * step * kValuesRows) {
@@ -785,8 +841,7 @@ __global__ void __launch_bounds__(256) k_rms_values(const __grid_constant__ RmsA
         for (int b = 0; b < kValuesRows; b++) {
             if (b < rows) {
                 e[b] = *scale;
-                if (N == 16) c[b] = __ldcs(reinterpret_cast<const uint4*>(src));
-                else c[b].x = *src;
+                c[b] = __ldcs(reinterpret_cast<const uint4*>(src));
             }
             scale += scales_apart;
             src += apart;
@@ -799,22 +854,14 @@ __global__ void __launch_bounds__(256) k_rms_values(const __grid_constant__ RmsA
             const uint32_t q[4] = {c[b].x, c[b].y, c[b].z, c[b].w};
             uint32_t w[8];
 #pragma unroll
-            for (int k = 0; k < (N == 16 ? 8 : 1); k++)
+            for (int k = 0; k < 8; k++)
                 w[k] = values2(__byte_perm(q[k >> 1], 0, k & 1 ? 0x3424 : 0x1404), up);
-            if (rest) {
-                const uint32_t one = (rest + 127u) << 7, two = one | one << 16;
+            if (rest)
 #pragma unroll
-                for (int k = 0; k < (N == 16 ? 8 : 1); k++) {
-                    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]), *reinterpret_cast<const __nv_bfloat162*>(&two));
-                    w[k] = *reinterpret_cast<const uint32_t*>(&v);
-                }
-            }
-            if (N == 16) {
-                __stcs(reinterpret_cast<uint4*>(dst), make_uint4(w[0], w[1], w[2], w[3]));
-                __stcs(reinterpret_cast<uint4*>(dst) + 1, make_uint4(w[4], w[5], w[6], w[7]));
-            } else {
-                *dst = (uint16_t)w[0];
-            }
+                for (int k = 0; k < 8; k++)
+                    w[k] = scaled_more(w[k], rest);
+            __stcs(reinterpret_cast<uint4*>(dst), make_uint4(w[0], w[1], w[2], w[3]));
+            __stcs(reinterpret_cast<uint4*>(dst) + 1, make_uint4(w[4], w[5], w[6], w[7]));
             dst += apart;
         }
     }
@@ -872,7 +919,7 @@ cudaError_t launch_slots(const RmsArgs& a, int64_t blocks, int threads, cudaStre
 }
 
 template <int DT, int L, int V, int RB, int S, int T, int BLOCKS, int Q>
-cudaError_t forward_shape(RmsArgs a, int64_t vecs, int align, cudaStream_t s)
+cudaError_t forward_shape(RmsArgs a, int64_t vecs, cudaStream_t s)
 {
     const RowShape h = shape_of(vecs, L, V, T);
     a.warps = h.warps;
@@ -881,76 +928,63 @@ cudaError_t forward_shape(RmsArgs a, int64_t vecs, int align, cudaStream_t s)
     const int64_t blocks = blocks_for(a.rows, (int64_t)h.groups * a.take, most);
     constexpr size_t smem = (size_t)S * RB * V * 2 * T * 16;
     if constexpr (L == 32) {                          // fewer lanes: whole rows on 16-byte boundaries only
-        if constexpr (DT != kF32)
-            if (align < 16)
-                return launch_slots<k_rms_forward_rows<DT, L, V, RB, S, T, BLOCKS, true, 4, Q>, smem>(a, blocks, h.threads, s);
         if (a.dim % kVecOf<DT>)
-            return launch_slots<k_rms_forward_rows<DT, L, V, RB, S, T, BLOCKS, true, 16, Q>, smem>(a, blocks, h.threads, s);
+            return launch_slots<k_rms_forward_rows<DT, L, V, RB, S, T, BLOCKS, true, Q>, smem>(a, blocks, h.threads, s);
     }
-    return launch_slots<k_rms_forward_rows<DT, L, V, RB, S, T, BLOCKS, false, 16, Q>, smem>(a, blocks, h.threads, s);
+    return launch_slots<k_rms_forward_rows<DT, L, V, RB, S, T, BLOCKS, false, Q>, smem>(a, blocks, h.threads, s);
 }
 
 // The same shape with 8-bit results and without.
-template <int DT, int V, int RB, int S, int T, int BLOCKS>
-cudaError_t forward_rows(const RmsArgs& a, int64_t vecs, int align, cudaStream_t s)
+template <int DT, int L, int V, int RB, int S, int T, int BLOCKS>
+cudaError_t forward_rows(const RmsArgs& a, int64_t vecs, cudaStream_t s)
 {
-    return !a.q ? forward_shape<DT, 32, V, RB, S, T, BLOCKS, 0>(a, vecs, align, s)
-           : a.block == 32 ? forward_shape<DT, 32, V, RB, S, T, BLOCKS, 32>(a, vecs, align, s)
-                           : forward_shape<DT, 32, V, RB, S, T, BLOCKS, 128>(a, vecs, align, s);
+    return !a.q ? forward_shape<DT, L, V, RB, S, T, BLOCKS, 0>(a, vecs, s)
+           : a.block == 32 ? forward_shape<DT, L, V, RB, S, T, BLOCKS, 32>(a, vecs, s)
+                           : forward_shape<DT, L, V, RB, S, T, BLOCKS, 128>(a, vecs, s);
 }
 
-// Warps to a row of 128-value blocks, K / 4 of them to a warp; groups and threads of a block.
-RowShape any_shape(int64_t dim, int K, int T)
-{
-    RowShape r;
-    r.warps = (int)((dim + 32 * K - 1) / (32 * K));
-    r.groups = T / 32 / r.warps;
-    r.threads = 32 * r.warps * r.groups;
-    return r;
-}
-
-template <int DT, int K, int RB, int T>
+template <int DT, int K, int W, int RB, int T>
 cudaError_t forward_any(RmsArgs a, cudaStream_t s)
 {
-    const RowShape h = any_shape(a.dim, K, T);
-    a.warps = h.warps;
-    const int64_t most = (int64_t)kSms * (512 / h.threads);
-    a.take = rows_of_batch(a.rows, h.groups, most, RB);
-    return launch_rms(k_rms_forward_any<DT, K, RB, T>, a, blocks_for(a.rows, (int64_t)h.groups * a.take, most), h.threads, 0, s);
+    constexpr int64_t groups = T / (32 * W), most = (int64_t)kSms * ((K > 16 ? 512 : 1024) / T);
+    a.take = rows_of_batch(a.rows, groups, most, RB);
+    return launch_rms(k_rms_forward_any<DT, K, W, RB, T>, a, blocks_for(a.rows, groups * a.take, most), T, 0, s);
 }
 
-// align: 16, 4 or 0, the boundary that every row starts on (of 0: its type's).
+// aligned: every row starts on 16 bytes.
 template <int DT>
-cudaError_t forward(const RmsArgs& a, int align, cudaStream_t s)
+cudaError_t forward(const RmsArgs& a, bool aligned, cudaStream_t s)
 {
     constexpr int VE = kVecOf<DT>, T = kRowThreads;
     const int64_t vecs = (a.dim + VE - 1) / VE;
-    const bool whole = a.dim % VE == 0 && align == 16 && !a.q;
-    if (whole && vecs <= 8) return forward_shape<DT, 8, 1, 4, 2, T, 2, 0>(a, vecs, align, s);
-    if (whole && vecs <= 16) return forward_shape<DT, 16, 1, 4, 2, T, 2, 0>(a, vecs, align, s);
-    if (align == 16 || (DT != kF32 && align == 4 && vecs > 64)) {
-        if (vecs <= 256) return forward_rows<DT, 1, 4, 2, T, 2>(a, vecs, align, s);
+    const bool whole = a.dim % VE == 0 && aligned;
+    if (whole && vecs <= 8) return forward_rows<DT, 8, 1, 4, 2, T, 2>(a, vecs, s);
+    if (whole && vecs <= 16) return forward_rows<DT, 16, 1, 4, 2, T, 2>(a, vecs, s);
+    if (aligned) {
+        if (vecs <= 256) return forward_rows<DT, 32, 1, 4, 2, T, 2>(a, vecs, s);
         // 8192 x 4096 bfloat16: 47.7 us as two vectors a lane, 49.2 as one; into 8 bits 44.1 and 41.5
-        if (vecs <= 512 && !a.q) return forward_shape<DT, 32, 2, 2, 2, T, 2, 0>(a, vecs, align, s);
+        if (vecs <= 512 && !a.q) return forward_shape<DT, 32, 2, 2, 2, T, 2, 0>(a, vecs, s);
         if (vecs <= 512)
-            return a.block == 32 ? forward_shape<DT, 32, 1, 4, 2, 2 * T, 1, 32>(a, vecs, align, s)
-                                 : forward_shape<DT, 32, 1, 4, 2, 2 * T, 1, 128>(a, vecs, align, s);
-        if (vecs <= 1024) return forward_rows<DT, 2, 2, 2, 2 * T, 1>(a, vecs, align, s);
-        if (vecs <= 2048) return forward_rows<DT, 4, 1, 2, 2 * T, 1>(a, vecs, align, s);
-        if (vecs <= 4096) return forward_rows<DT, 8, 1, 1, 2 * T, 1>(a, vecs, align, s);
+            return a.block == 32 ? forward_shape<DT, 32, 1, 4, 2, 2 * T, 1, 32>(a, vecs, s)
+                                 : forward_shape<DT, 32, 1, 4, 2, 2 * T, 1, 128>(a, vecs, s);
+        if (vecs <= 1024) return forward_rows<DT, 32, 2, 2, 2, 2 * T, 1>(a, vecs, s);
+        if (vecs <= 2048) return forward_rows<DT, 32, 4, 1, 2, 2 * T, 1>(a, vecs, s);
+        if (vecs <= 4096) return forward_rows<DT, 32, 8, 1, 1, 2 * T, 1>(a, vecs, s);
     } else {
-        if (a.dim <= 128) return forward_any<DT, 4, 4, T>(a, s);
-        if (a.dim <= 2048) return forward_any<DT, 8, 4, T>(a, s);
-        if (a.dim <= 4096) return forward_any<DT, 16, 2, T>(a, s);
-        if (a.dim <= 8192) return forward_any<DT, 16, 1, 2 * T>(a, s);
-        if (a.dim <= 16384) return forward_any<DT, 32, 1, 2 * T>(a, s);
+        if (a.dim <= 128) return forward_any<DT, 4, 1, 4, T>(a, s);
+        if (a.dim <= 256) return forward_any<DT, 8, 1, 2, T>(a, s);
+        if (a.dim <= 512) return forward_any<DT, 8, 2, 2, T>(a, s);
+        if (a.dim <= 1024) return forward_any<DT, 8, 4, 2, T>(a, s);
+        if (a.dim <= 2048) return forward_any<DT, 8, 8, 2, T>(a, s);
+        if (a.dim <= 4096) return forward_any<DT, 8, 16, 2, 2 * T>(a, s);
+        if (a.dim <= 8192) return forward_any<DT, 16, 16, 1, 2 * T>(a, s);
+        if (a.dim <= 16384) return forward_any<DT, 32, 16, 1, 2 * T>(a, s);
     }
     return launch_rms(k_rms_forward_long<DT>, a, a.rows < kSms * 4 ? a.rows : kSms * 4, kLongThreads, 0, s);
 }
 
 // How the backward pass deals out a row: lanes of a group, vectors of a lane,
-// threads and resident blocks, rows at a time.  The plan's blocks go by it
-// (as for rows on 16-byte boundaries) whatever the pointers turn out to be.
+// threads and resident blocks, rows at a time.
 struct BackwardShape {
     int L, V, T, blocks, rows;
 };
@@ -967,7 +1001,7 @@ BackwardShape backward_shape(int64_t vecs, bool whole)
 int64_t backward_most(const BackwardShape& b, const RowShape& h) { return (int64_t)kSms * (b.blocks * b.T / h.threads); }
 
 template <int DT, int L, int V, int RB, int T, int BLOCKS>
-cudaError_t backward_rows(RmsArgs a, int64_t vecs, int align, int blocks, cudaStream_t s)
+cudaError_t backward_rows(RmsArgs a, int64_t vecs, int64_t blocks, cudaStream_t s)
 {
     const RowShape h = shape_of(vecs, L, V, T);
     a.warps = h.warps;
@@ -975,53 +1009,67 @@ cudaError_t backward_rows(RmsArgs a, int64_t vecs, int align, int blocks, cudaSt
     constexpr int S = 2;
     constexpr size_t smem = (size_t)S * RB * V * 3 * T * 16;
     if constexpr (L == 32) {
-        if constexpr (DT != kF32)
-            if (align < 16)
-                return launch_slots<k_rms_backward_rows<DT, L, V, RB, S, T, BLOCKS, true, 4>, smem>(a, blocks, h.threads, s);
         if (a.dim % kVecOf<DT>)
-            return launch_slots<k_rms_backward_rows<DT, L, V, RB, S, T, BLOCKS, true, 16>, smem>(a, blocks, h.threads, s);
+            return launch_slots<k_rms_backward_rows<DT, L, V, RB, S, T, BLOCKS, true>, smem>(a, blocks, h.threads, s);
     }
-    return launch_slots<k_rms_backward_rows<DT, L, V, RB, S, T, BLOCKS, false, 16>, smem>(a, blocks, h.threads, s);
+    return launch_slots<k_rms_backward_rows<DT, L, V, RB, S, T, BLOCKS, false>, smem>(a, blocks, h.threads, s);
 }
 
-// Blocks of the backward pass (the plan's): as many as are resident at once on
-// 152 SMs, and no more than have rows.
-int64_t backward_blocks(int64_t rows, int64_t vecs, bool whole)
+// Its blocks: as many as are resident at once on 152 SMs, and no more than have rows.
+int64_t backward_blocks(int64_t rows, int64_t vecs, int L)
 {
-    const BackwardShape b = backward_shape(vecs, whole);
-    const RowShape h = shape_of(vecs <= 2048 ? vecs : 2048, b.L, b.V, b.T);
+    BackwardShape b = backward_shape(vecs, false);
+    const RowShape h = shape_of(vecs <= 2048 ? vecs : 2048, b.L = L, b.V, b.T);
     const int64_t most = backward_most(b, h);
     return blocks_for(rows, (int64_t)h.groups * rows_of_batch(rows, h.groups, most, b.rows), most);
 }
 
-template <int DT, int K, int T>
-cudaError_t backward_any(RmsArgs a, int blocks, cudaStream_t s)
+// Warps to a row in the kernel for other rows, of 8 values a lane up to 8192; threads of
+// its blocks, and the blocks: as many as are resident, and no more than have rows.
+// (Two rows of a group at a time, with half of the warps: 8192 x 4095 123 us for 86;
+// short rows are two at a time, 65536 x 67 24 us for 32.)
+constexpr int64_t any_warps(int64_t dim) { return dim <= 256 ? 1 : dim <= 512 ? 2 : dim <= 1024 ? 4 : dim <= 2048 ? 8 : dim <= 4096 ? 16 : 32; }
+constexpr int64_t any_threads(int64_t W) { return W <= 8 ? 256 : 32 * W; }
+
+int64_t any_blocks(int64_t rows, int64_t dim)
 {
-    const RowShape h = any_shape(a.dim, K, T);
-    a.warps = h.warps;
-    return launch_rms(k_rms_backward_any<DT, K, T>, a, blocks, h.threads, 0, s);
+    const int64_t W = any_warps(dim), T = any_threads(W);
+    return blocks_for(rows, T / (32 * W) * (dim <= 128 ? 2 : 1), kSms * (kAnyResident / T));
+}
+
+template <int DT, int K, int W, int RB = 1>
+cudaError_t backward_any(const RmsArgs& a, int64_t& blocks, cudaStream_t s)
+{
+    constexpr int T = (int)any_threads(W);
+    blocks = any_blocks(a.rows, a.dim);
+    return launch_rms(k_rms_backward_any<DT, K, W, RB, T>, a, blocks, T, 0, s);
 }
 
 template <int DT>
-cudaError_t backward(RmsArgs a, int align, int blocks, void* dw, cudaStream_t s)
+cudaError_t backward(RmsArgs a, bool aligned, int64_t most, void* dw, cudaStream_t s)
 {
     constexpr int VE = kVecOf<DT>, T = kRowThreads;
     const int64_t vecs = (a.dim + VE - 1) / VE;
     if (!dw) a.part = nullptr;
     cudaError_t e = cudaSuccess;
-    if (blocks && vecs <= 2048 && (align == 16 || (DT != kF32 && align == 4 && vecs > 16))) {
-        const int L = align == 16 ? backward_shape(vecs, a.dim % VE == 0).L : 32;
-        if (L == 8) e = backward_rows<DT, 8, 1, 4, T, 2>(a, vecs, align, blocks, s);
-        else if (L == 16) e = backward_rows<DT, 16, 1, 4, T, 2>(a, vecs, align, blocks, s);
-        else if (vecs <= 256) e = backward_rows<DT, 32, 1, 4, T, 2>(a, vecs, align, blocks, s);
-        else if (vecs <= 512) e = backward_rows<DT, 32, 1, 4, 2 * T, 1>(a, vecs, align, blocks, s);
-        else if (vecs <= 1024) e = backward_rows<DT, 32, 2, 2, 2 * T, 1>(a, vecs, align, blocks, s);
-        else e = backward_rows<DT, 32, 4, 1, 2 * T, 1>(a, vecs, align, blocks, s);
-    } else if (blocks && align < 16 && a.dim <= 8192) {
-        if (a.dim <= 128) e = backward_any<DT, 4, T>(a, blocks, s);
-        else if (a.dim <= 2048) e = backward_any<DT, 8, T>(a, blocks, s);
-        else if (a.dim <= 4096) e = backward_any<DT, 16, T>(a, blocks, s);
-        else e = backward_any<DT, 16, 2 * T>(a, blocks, s);
+    int64_t blocks = most;                            // partial sums of the weight's gradient
+    if (a.rows && vecs <= 2048 && aligned) {
+        const int L = backward_shape(vecs, a.dim % VE == 0).L;
+        blocks = backward_blocks(a.rows, vecs, L);
+        if (L == 8) e = backward_rows<DT, 8, 1, 4, T, 2>(a, vecs, blocks, s);
+        else if (L == 16) e = backward_rows<DT, 16, 1, 4, T, 2>(a, vecs, blocks, s);
+        else if (vecs <= 256) e = backward_rows<DT, 32, 1, 4, T, 2>(a, vecs, blocks, s);
+        else if (vecs <= 512) e = backward_rows<DT, 32, 1, 4, 2 * T, 1>(a, vecs, blocks, s);
+        else if (vecs <= 1024) e = backward_rows<DT, 32, 2, 2, 2 * T, 1>(a, vecs, blocks, s);
+        else e = backward_rows<DT, 32, 4, 1, 2 * T, 1>(a, vecs, blocks, s);
+    } else if (a.rows && !aligned && a.dim <= 8192) {
+        if (a.dim <= 128) e = backward_any<DT, 4, 1, 2>(a, blocks, s);
+        else if (a.dim <= 256) e = backward_any<DT, 8, 1>(a, blocks, s);
+        else if (a.dim <= 512) e = backward_any<DT, 8, 2>(a, blocks, s);
+        else if (a.dim <= 1024) e = backward_any<DT, 8, 4>(a, blocks, s);
+        else if (a.dim <= 2048) e = backward_any<DT, 8, 8>(a, blocks, s);
+        else if (a.dim <= 4096) e = backward_any<DT, 8, 16>(a, blocks, s);
+        else e = backward_any<DT, 8, 32>(a, blocks, s);
     } else {
         if (a.dx && a.rows) e = launch_rms(k_rms_dx_long<DT>, a, a.rows < kSms * 4 ? a.rows : kSms * 4, kLongThreads, 0, s);
         if (e == cudaSuccess && dw && blocks) {
@@ -1031,21 +1079,19 @@ cudaError_t backward(RmsArgs a, int align, int blocks, void* dw, cudaStream_t s)
         }
     }
     if (e == cudaSuccess && dw)
-        e = launch_kernel(k_rms_dw_sum<DT>, (int)((a.dim + 31) / 32), 1024, s, blocks > 0, (const float*)a.part, blocks,
+        e = launch_kernel(k_rms_dw_sum<DT>, (int)((a.dim + 31) / 32), 1024, s, blocks > 0, (const float*)a.part, (int)blocks,
                           a.dim, dw);
     return e;
 }
 
-// The boundary that every row of the given arrays starts on: 16, 4 or 0 bytes
-// (their type's).  A weight off 16-byte boundaries counts as 0.
-int rows_align(const zero_rms_plan_t& p, const void* weight, const void* const* arrays, int n)
+// Whether every row of the given arrays, and the weight, starts on 16 bytes.
+bool rows_aligned(const zero_rms_plan_t& p, const void* weight, const void* const* arrays, int n)
 {
     const uint64_t e = p.dtype == ZERO_FP32 ? 4 : 2;
     uint64_t any = (uint64_t)p.x_stride * e | (uint64_t)p.y_stride * e;
     for (int k = 0; k < n; k++)
         any |= (uintptr_t)arrays[k];
-    if ((uintptr_t)weight % 16) return 0;
-    return any % 16 == 0 ? 16 : any % 4 == 0 ? 4 : 0;
+    return (any | (uintptr_t)weight) % 16 == 0;
 }
 
 RmsArgs args_of(const zero_rms_plan_t& p)
@@ -1089,7 +1135,11 @@ zero_status_t zero_rms_plan(int64_t rows, int64_t dim, int32_t dtype, int64_t x_
     out->block = block;
     out->scale_cols = block ? (dim + block - 1) / block : 0;
     const int64_t e = dtype == ZERO_FP32 ? 4 : 2;
-    out->blocks = (int32_t)backward_blocks(rows, (dim * e + 15) / 16, dim * e % 16 == 0);   // each adds up its rows' weight gradients
+    // each adds up its rows' weight gradients; the most of any alignment of the pointers
+    const int64_t vecs = (dim * e + 15) / 16;
+    const int64_t by_vec = backward_blocks(rows, vecs, 32), by_some = backward_blocks(rows, vecs, backward_shape(vecs, dim * e % 16 == 0).L);
+    const int64_t by_one = dim <= 8192 ? any_blocks(rows, dim) : 0, more = by_vec > by_some ? by_vec : by_some;
+    out->blocks = (int32_t)(more > by_one ? more : by_one);
     out->workspace_bytes = 16 + (int64_t)out->blocks * dim * 4;
     out->hbm_bytes_forward = rows * (3 * dim * e + 4 + (block ? dim + out->scale_cols : dim * e)) + dim * e;
     out->hbm_bytes_backward = rows * (4 * dim * e + 4) + 2 * dim * e;
@@ -1119,10 +1169,10 @@ zero_status_t zero_rms_forward(const zero_rms_plan_t* plan, const void* x, const
     a.q_wide = aligned_to(q, 8) && plan->y_stride % 8 == 0;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const void* arrays[] = {x, residual, h, y};
-    const int align = rows_align(*plan, weight, arrays, 4);
-    const cudaError_t err = plan->dtype == ZERO_FP32   ? forward<kF32>(a, align, s)
-                            : plan->dtype == ZERO_BF16 ? forward<kBF16>(a, align, s)
-                                                       : forward<kF16>(a, align, s);
+    const bool aligned = rows_aligned(*plan, weight, arrays, 4);
+    const cudaError_t err = plan->dtype == ZERO_FP32   ? forward<kF32>(a, aligned, s)
+                            : plan->dtype == ZERO_BF16 ? forward<kBF16>(a, aligned, s)
+                                                       : forward<kF16>(a, aligned, s);
     return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_rms_forward");
 }
 
@@ -1140,13 +1190,17 @@ zero_status_t zero_rms_values(const zero_rms_plan_t* plan, const void* q, const 
     a.q_scale = const_cast<uint8_t*>(q_scale);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool wide = aligned_to(q, 16) && aligned_to(values, 16) && plan->y_stride % 16 == 0 && plan->dim % 16 == 0;
-    const int64_t per = wide ? plan->dim / 16 : plan->dim;
-    unsigned along = 32;
-    while (along < 256 && along < per) along *= 2;
-    const int64_t high = (plan->rows + 256 / along * kValuesRows - 1) / (256 / along * kValuesRows);
-    const dim3 block(along, 256 / along), grid((unsigned)((per + along - 1) / along), (unsigned)(high < 65535 ? high : 65535));
-    if (wide) k_rms_values<16><<<grid, block, 0, s>>>(a, static_cast<uint16_t*>(values));
-    else k_rms_values<1><<<grid, block, 0, s>>>(a, static_cast<uint16_t*>(values));
+    if (wide) {
+        unsigned along = 32;
+        while (along < 256 && along < plan->dim / 16) along *= 2;
+        const int64_t high = (plan->rows + 256 / along * kValuesRows - 1) / (256 / along * kValuesRows);
+        const dim3 block(along, 256 / along);
+        const dim3 grid((unsigned)((plan->dim / 16 + along - 1) / along), (unsigned)(high < 65535 ? high : 65535));
+        k_rms_values<<<grid, block, 0, s>>>(a, static_cast<uint16_t*>(values));
+    } else {
+        const int64_t per = (plan->dim + 255) / 256;
+        k_rms_values_any<<<(unsigned)blocks_for(plan->rows * per, 8, kSms * 32), 256, 0, s>>>(a, static_cast<uint16_t*>(values), per);
+    }
     const cudaError_t err = cudaGetLastError();
     return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_rms_values");
 }
@@ -1171,10 +1225,10 @@ zero_status_t zero_rms_backward(const zero_rms_plan_t* plan, const void* dy, con
     a.part = static_cast<float*>(workspace) + 4;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const void* arrays[] = {dy, a.r, h, dx};
-    const int align = rows_align(*plan, weight, arrays, 4);
-    const cudaError_t err = plan->dtype == ZERO_FP32   ? backward<kF32>(a, align, plan->blocks, dweight, s)
-                            : plan->dtype == ZERO_BF16 ? backward<kBF16>(a, align, plan->blocks, dweight, s)
-                                                       : backward<kF16>(a, align, plan->blocks, dweight, s);
+    const bool aligned = rows_aligned(*plan, weight, arrays, 4);
+    const cudaError_t err = plan->dtype == ZERO_FP32   ? backward<kF32>(a, aligned, plan->blocks, dweight, s)
+                            : plan->dtype == ZERO_BF16 ? backward<kBF16>(a, aligned, plan->blocks, dweight, s)
+                                                       : backward<kF16>(a, aligned, plan->blocks, dweight, s);
     return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_rms_backward");
 }
 
