@@ -135,7 +135,9 @@ __device__ __forceinline__ Tile tile_at(const GemmArgs& g, uint32_t t)
 // `least`, a value that the row is known to have `top` logits of; keys in falling
 // order.  A lane keeps the maxima of 8 groups of 16 columns, and a round takes
 // the largest of all from each lane that still has one, group by group as lanes
-// have need: what it costs goes by how many there are.
+// have need: what it costs goes by how many there are.  (`least` from 4096 entries
+// leaves two rounds for 8 alternatives, three for 20, beside the next tile's products;
+// without it a strip takes `top` rounds, 40 us a tile for 20.)
 template <bool TOP>
 __device__ __forceinline__ void lp_statistics(const GemmArgs& g, float (&z)[kStrip], int strip, int64_t row, bool live,
                                               uint32_t index0)

@@ -29,8 +29,8 @@ struct LpArgs {
     float* entropy;              // may be NULL
     float2* stat;                // [n] maximum, log of the sum
     int top;
-    const float* logits;         // [n][logit_stride]: of the first `sampled` entries
-    int64_t logit_stride, sampled;
+    const float* logits;         // [n][logit_stride]: of the first `kept` entries
+    int64_t logit_stride, kept;
     uint64_t* first;             // [n][top]: the alternatives among those
     float* least;                // [n]: the last of them
     uint64_t* cand;              // [n][cand_strips][top]: those of the strips behind; few rows: of the blocks
@@ -179,22 +179,39 @@ __device__ __forceinline__ uint64_t sorted(uint64_t x, int lane)
     return x;
 }
 
-// Keys on their way into a warp's list, gathered so that 32 at a time are sorted.
+// Keys on their way into a warp's list, gathered so that 32 at a time are sorted;
+// those below a bound that the row is known to have `top` of are dropped.
 struct Gather {
     uint64_t* held;              // [64] of the warp, shared memory
     int n;                       // so many are held
+    int top;
+    uint64_t bound;
+    float least;                 // the bound's logit
     uint64_t list;
+
+    __device__ __forceinline__ void raise(uint64_t b)
+    {
+        bound = key_max(bound, b);
+        least = logit_of(bound);
+    }
+
+    __device__ __forceinline__ void sort(uint64_t key, int lane)
+    {
+        list = lists_merged(list, sorted(key, lane), lane);
+        raise(__shfl_sync(kAll, list, top - 1));
+    }
 
     // A key of each lane with `in`.
     __device__ __forceinline__ void add(bool in, uint64_t key, int lane)
     {
+        in = in && key >= bound;
         const unsigned b = __ballot_sync(kAll, in);
         if (!b) return;
         if (in) held[n + __popc(b & ((1u << lane) - 1))] = key;
         n += __popc(b);
         __syncwarp();
         if (n < 32) return;
-        list = lists_merged(list, sorted(held[lane], lane), lane);
+        sort(held[lane], lane);
         n -= 32;
         const uint64_t rest = held[32 + lane];
         __syncwarp();
@@ -204,10 +221,16 @@ struct Gather {
 
     __device__ __forceinline__ uint64_t all(int lane)
     {
-        if (n) list = lists_merged(list, sorted(lane < n ? held[lane] : 0, lane), lane);
+        if (n) sort(lane < n ? held[lane] : 0, lane);
         return list;
     }
 };
+
+// An empty list; -infinity is no alternative, and NaN none.
+__device__ __forceinline__ Gather gather(uint64_t* held, int top)
+{
+    return {held, 0, top, key_of(-3.4028235e38f, 0xffffffffu), -3.4028235e38f, 0};
+}
 
 // The lists of a block's 8 warps, in warp 0.
 __device__ __forceinline__ uint64_t block_merged(uint64_t list, uint64_t (*sh)[32], int warp, int lane)
@@ -230,71 +253,91 @@ __device__ __forceinline__ void write_top(const LpArgs& a, int64_t i, uint64_t l
 }
 
 // Per row: the first `top` of the logits that were kept, by W warps.  Of the strips'
-// maxima, a few to a lane, the top-th largest lane's is a bound that the row is known
-// to have `top` logits of; only strips whose maximum is no less have any to look at,
-// and they have about as many as are wanted (of 32 strips 9 for 8, 31 for 20).
-// FINAL: written out; else kept for k_lp_top, the last of them as the row's `least`.
+// maxima, two sets to a lane, the top-th largest set's is a bound that the row is
+// known to have `top` logits of; only strips whose maximum is no less are read, 9 of
+// 393 for 8 alternatives, 22 for 20 or 45 for 32, and have about as many logits to
+// sort.  FINAL: written out; else kept for k_lp_top, the last of them as the row's
+// `least`.
 template <int W, bool FINAL>
 __global__ void __launch_bounds__(256) k_lp_first(const __grid_constant__ LpArgs a)
 {
-    constexpr int U = 8;                              // strips on their way
+    constexpr int U = 8;                              // maxima, or strips, on their way
     wait_prev_grid();
     if constexpr (!FINAL) allow_next_grid();
     __shared__ uint64_t sh[8][32], held[8][64];
+    __shared__ int chosen[8][32 * U];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t i = W == 1 ? (int64_t)blockIdx.x * 8 + warp : min((int64_t)blockIdx.x, a.n - 1);
-    const int strips = (int)((a.sampled + kStrip - 1) / kStrip);
-    const float2* part = a.part + min(i, a.n - 1);
-    const int s0 = W == 1 ? 0 : warp * 32;
-    float most = -INFINITY;
-    for (int s = s0 + lane; s < strips; s += 32 * W)
-        most = fmaxf(most, part[(int64_t)s * a.n].x);
-    uint64_t bound = sorted(key_of(most, 0), lane);
+    const int64_t i = W == 1 ? (int64_t)blockIdx.x * 8 + warp : blockIdx.x;
+    if (W == 1 && i >= a.n) return;
+    const float2* part = a.part + i;
+    const int strips = (int)((a.kept + kStrip - 1) / kStrip), kept = (int)a.kept;
+    const int first = (W == 1 ? 0 : warp * 32) + lane;            // strips first, first + 32 W, ...
+    float most[2] = {-INFINITY, -INFINITY};
+    for (int s0 = first - lane; s0 < strips; s0 += 32 * W * U) {
+        float m[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int s = s0 + lane + 32 * W * u;
+            m[u] = s < strips ? part[(int64_t)s * a.n].x : -INFINITY;
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++)
+            most[u & 1] = fmaxf(most[u & 1], m[u]);
+    }
+    uint64_t bound = lists_merged(sorted(key_of(most[0], 0), lane), sorted(key_of(most[1], 0), lane), lane);
     if constexpr (W > 1) {
         bound = block_merged(bound, sh, warp, lane);
         if (warp == 0) sh[0][lane] = bound;
         __syncthreads();
         bound = sh[0][lane];
     }
-    const float least = fmaxf(logit_of(__shfl_sync(kAll, bound, a.top - 1)), -3.4028235e38f);    // -infinity is none
-    Gather g{held[warp], 0, 0};
-    if (i < a.n) {
-        const float* z = a.logits + i * a.logit_stride;
-        for (int sw = s0; sw < strips; sw += 32 * W) {
-            unsigned todo = __ballot_sync(kAll, sw + lane < strips && part[(int64_t)(sw + lane) * a.n].x >= least);
-            while (todo) {
-                int at[U];
-                float4 q[U];
+    Gather g = gather(held[warp], a.top);
+    g.raise(__shfl_sync(kAll, bound, a.top - 1) & ~0xffffffffull);            // of whatever index
+    const float* z = a.logits + i * a.logit_stride;
+    int* mine = chosen[warp];
+    for (int s0 = first - lane; s0 < strips; s0 += 32 * W * U) {
+        int n = 0;                                    // strips to look at
 #pragma unroll
-                for (int u = 0; u < U; u++) {
-                    at[u] = todo ? (sw + __ffs(todo) - 1) * kStrip + 4 * lane : (int)a.sampled;
-                    todo &= todo - 1;
-                    if (at[u] < a.sampled) q[u] = *reinterpret_cast<const float4*>(z + at[u]);
-                }
+        for (int u = 0; u < U; u++) {
+            const int s = s0 + lane + 32 * W * u;
+            const bool in = s < strips && part[(int64_t)s * a.n].x >= g.least;
+            const unsigned b = __ballot_sync(kAll, in);
+            if (in) mine[n + __popc(b & ((1u << lane) - 1))] = s;
+            n += __popc(b);
+        }
+        __syncwarp();
+        for (int k0 = 0; k0 < n; k0 += U) {
+            int at[U];
+            float4 q[U];
 #pragma unroll
-                for (int u = 0; u < U; u++) {
-                    const float f[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
-                    // a lane seldom has two: the next of all lanes that have one, again and again
-                    unsigned in = 0;
+            for (int u = 0; u < U; u++) {
+                at[u] = k0 + u < n ? mine[k0 + u] * kStrip + 4 * lane : kept;
+                if (at[u] < kept) q[u] = *reinterpret_cast<const float4*>(z + at[u]);
+            }
 #pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        if (at[u] + k < a.sampled && f[k] >= least) in |= 1u << k;
-                    while (__any_sync(kAll, in)) {
-                        const int k = in ? __ffs(in) - 1 : 0;
-                        const float v = k == 0 ? f[0] : k == 1 ? f[1] : k == 2 ? f[2] : f[3];
-                        g.add(in, key_of(v, (uint32_t)(at[u] + k)), lane);
-                        in &= in - 1;
-                    }
+            for (int u = 0; u < U; u++) {
+                if (k0 + u >= n) break;
+                const float f[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+                // a lane seldom has two: the next of all lanes that have one, again and again
+                unsigned in = 0;
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+                    if (at[u] + k < kept && f[k] >= g.least) in |= 1u << k;
+                while (__any_sync(kAll, in)) {
+                    const int k = in ? __ffs(in) - 1 : 0;
+                    const float v = k == 0 ? f[0] : k == 1 ? f[1] : k == 2 ? f[2] : f[3];
+                    g.add(in, key_of(v, (uint32_t)(at[u] + k)), lane);
+                    in &= in - 1;
                 }
             }
         }
+        __syncwarp();
     }
     uint64_t list = g.all(lane);
     if constexpr (W > 1) {
         list = block_merged(list, sh, warp, lane);
         if (warp) return;
     }
-    if (i >= a.n) return;
     if constexpr (FINAL) {
         write_top(a, i, list, a.stat[i], lane);
     } else {
@@ -322,7 +365,9 @@ __global__ void __launch_bounds__(32 * kTopWarps) k_lp_top(const __grid_constant
     const uint64_t* keys = a.cand + i * a.cand_strips * a.top;
     const uint8_t* counts = a.cand_count + i * a.count_stride;
     uint32_t* mine = places[warp];
-    Gather g{held[warp], 0, lane < a.top ? a.first[i * a.top + lane] : 0};
+    Gather g = gather(held[warp], a.top);
+    g.list = lane < a.top ? a.first[i * a.top + lane] : 0;
+    g.raise(__shfl_sync(kAll, g.list, a.top - 1));
     int listed = 0;
     auto look = [&]() {
         __syncwarp();
@@ -334,11 +379,10 @@ __global__ void __launch_bounds__(32 * kTopWarps) k_lp_top(const __grid_constant
                 key[u] = k < listed ? keys[mine[k]] : 0;
                 most = key_max(most, key[u]);
             }
-            // the top-th of the list, or of the lanes' largest
-            const uint64_t bound = key_max(__shfl_sync(kAll, g.list, a.top - 1), __shfl_sync(kAll, sorted(most, lane), a.top - 1));
+            g.raise(__shfl_sync(kAll, sorted(most, lane), a.top - 1));          // the lanes' largest
 #pragma unroll
             for (int u = 0; u < U; u++)
-                g.add(key[u] && key[u] >= bound, key[u], lane);
+                g.add(key[u] != 0, key[u], lane);
         }
         __syncwarp();
         listed = 0;
@@ -635,20 +679,21 @@ zero_status_t cuda_failed(cudaError_t e, const char* what)
 
 int64_t strips_of(int64_t vocab) { return ceil_div(vocab, kBN) * 2; }
 
-// Entries whose logits are kept, so that every row has a threshold for the others'
-// alternatives: all of them where that is little (32 MB), or they are few.
-int64_t sampled_entries(int64_t rows, int64_t vocab, int64_t top)
+// Entries whose logits are kept in memory for the alternatives: all of them up to 256
+// MB, or where they are few; else those that give every row a threshold for the
+// others.  (1023 rows of 50257, hidden 1600, 20 alternatives: 148 us with all, 157
+// with 4096; 4096 rows, hidden 768, 8 alternatives: 412 and 315, 256 rows 48 and 60.)
+int64_t kept_entries(int64_t rows, int64_t vocab, int64_t top)
 {
-    if (!top) return 0;
-    return vocab <= kSample + kSample / 4 || rows * vocab <= (int64_t(1) << 23) ? vocab : kSample;
+    return !top ? 0 : vocab <= kSample + kSample / 4 || rows * vocab <= (int64_t(1) << 26) ? vocab : kSample;
 }
 
-// Rows at a time of a forward pass: what the strips leave (12 bytes each, and 9 and
-// up with alternatives) and the logits that are kept take about 512 MiB.
-int64_t rows_at_once(int64_t vocab, int64_t top)
+// Rows at a time of a forward pass: what the strips leave (12 bytes each, and 9 and up
+// for alternatives) and the logits that are kept take about 512 MiB.
+int64_t rows_at_once(int64_t tokens, int64_t vocab, int64_t top)
 {
-    const int64_t kept = vocab < kSample + kSample / 4 ? vocab : kSample + kSample / 4;
-    const int64_t per = strips_of(vocab) * (12 + (top ? 1 + 8 * top : 0)) + (top ? 4 * kept + 8 * top : 0);
+    const int64_t kept = kept_entries(tokens, vocab, top);
+    const int64_t per = strips_of(vocab) * (12 + (kept < vocab && top ? 1 + 8 * top : 0)) + 4 * kept + 8 * top;
     const int64_t fit = (int64_t(1) << 29) / per / kBM * kBM;
     return fit < kBM ? kBM : fit;
 }
@@ -656,7 +701,7 @@ int64_t rows_at_once(int64_t vocab, int64_t top)
 // Byte offsets of a forward pass in the workspace.
 struct LpLayout {
     int64_t target_logit, stat, least, part, part_t, logits, first, count, cand, end;
-    int64_t sampled, logit_stride;
+    int64_t kept, logit_stride;
     int cand_strips, count_stride;
 };
 
@@ -664,10 +709,10 @@ LpLayout lp_layout(const zero_lp_plan_t& p, bool few)
 {
     LpLayout l;
     const int64_t rows = p.rows < p.tokens ? p.rows : p.tokens, strips = strips_of(p.vocab);
-    l.sampled = few ? 0 : sampled_entries(rows, p.vocab, p.top);
-    l.logit_stride = (l.sampled + 3) / 4 * 4;
-    l.cand_strips = few ? kFewBlocks : p.top && l.sampled < p.vocab ? (int)(strips - l.sampled / kStrip) : 0;
-    l.count_stride = (l.cand_strips + 15) / 16 * 16;
+    l.kept = few ? 0 : kept_entries(p.tokens, p.vocab, p.top);
+    l.logit_stride = (l.kept + 3) / 4 * 4;
+    l.cand_strips = few ? kFewBlocks : l.kept < p.vocab && p.top ? (int)(strips - l.kept / kStrip) : 0;
+    l.count_stride = few ? 0 : (l.cand_strips + 15) / 16 * 16;
     l.target_logit = sizeof(CeHead);
     l.stat = l.target_logit + up256(rows * 4);
     l.least = l.stat + up256(rows * 8);
@@ -676,7 +721,7 @@ LpLayout lp_layout(const zero_lp_plan_t& p, bool few)
     l.logits = l.part_t + (few ? 0 : up256(strips * rows * 4));
     l.first = l.logits + up256(rows * l.logit_stride * 4);
     l.count = l.first + up256(rows * p.top * 8);
-    l.cand = l.count + (few ? 0 : up256(l.count_stride * rows));
+    l.cand = l.count + up256(l.count_stride * rows);
     l.end = l.cand + up256(l.cand_strips * rows * p.top * 8);
     return l;
 }
@@ -722,11 +767,11 @@ cudaError_t launch_few(const zero_lp_plan_t& p, int64_t blocks, const void* x, c
     }
 }
 
-// Warps to a row: 8 where there are strips for them and few rows.
+// Warps to a row: 8 where there are few rows and more than a sample's strips.
 template <bool FINAL>
 cudaError_t launch_first(const LpArgs& a, cudaStream_t s)
 {
-    if (a.n > 2 * 152 || a.sampled <= 64 * kStrip)
+    if (a.n > 2 * 152 || a.kept <= 64 * kStrip)
         return launch_after(k_lp_first<1, FINAL>, dim3((unsigned)ceil_div(a.n, 8)), 256, 0, s, a);
     return launch_after(k_lp_first<8, FINAL>, dim3((unsigned)a.n), 256, 0, s, a);
 }
@@ -742,7 +787,7 @@ cudaError_t forward_rows(const zero_lp_plan_t& p, const void* x, const void* w, 
     g.a_rows = a_rows_of(a.n);
     ok = make_map(&g.a, type, xr, a.n, p.hidden, p.x_stride, g.a_rows) &&
          make_map(&g.b, type, w, p.vocab, p.hidden, p.w_stride, kBN / 2) &&
-         (!a.top || make_map(&g.c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.logits, a.n, a.sampled, a.logit_stride, 32));
+         (!a.top || make_map(&g.c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.logits, a.n, a.kept, a.logit_stride, 32));
     if (!ok) return cudaSuccess;
     g.m = a.n;
     g.m_tiles = (int)ceil_div(a.n, kBM);
@@ -770,14 +815,15 @@ cudaError_t forward_rows(const zero_lp_plan_t& p, const void* x, const void* w, 
         return !a.top ? gemm<kEpiStat, false, false>(p.dtype, g, s)
                : v0 == 0 ? gemm<kEpiKeep, false, false>(p.dtype, g, s) : gemm<kEpiTop, false, false>(p.dtype, g, s);
     };
-    const bool two = a.top && a.sampled < p.vocab;
-    cudaError_t e = product(0, two ? a.sampled : p.vocab);
+    const bool two = a.top && a.kept < p.vocab;
+    cudaError_t e = product(0, two ? a.kept : p.vocab);
     if (two) {
         if (e == cudaSuccess) e = launch_first<false>(a, s);
-        if (e == cudaSuccess) e = product(a.sampled, p.vocab);
+        if (e == cudaSuccess) e = product(a.kept, p.vocab);
     }
     if (e == cudaSuccess) e = launch_after(k_lp_join, dim3((unsigned)ceil_div(a.n, kJoinRows)), kJoinThreads, 0, s, a);
-    if (e == cudaSuccess && a.top) e = two ? launch_after(k_lp_top, dim3((unsigned)ceil_div(a.n, kTopWarps)), 32 * kTopWarps, 0, s, a) : launch_first<true>(a, s);
+    if (e == cudaSuccess && a.top)
+        e = two ? launch_after(k_lp_top, dim3((unsigned)ceil_div(a.n, kTopWarps)), 32 * kTopWarps, 0, s, a) : launch_first<true>(a, s);
     return e;
 }
 
@@ -807,7 +853,7 @@ zero_status_t zero_lp_plan(int64_t tokens, int64_t vocab, int64_t hidden, int32_
     out->dtype = dtype;
     out->splits = c.splits;
     out->top = top;
-    out->rows = rows_at_once(vocab, top);
+    out->rows = rows_at_once(tokens, vocab, top);
     const int64_t forward = lp_layout(*out, few_tokens(c)).end;
     out->workspace_bytes = forward > c.workspace_bytes ? forward : c.workspace_bytes;
     out->flops_forward = c.flops_forward;
@@ -860,7 +906,7 @@ zero_status_t zero_lp_forward(const zero_lp_plan_t* plan, const void* x, const v
         a.top = p.top;
         a.logits = reinterpret_cast<const float*>(ws + l.logits);
         a.logit_stride = l.logit_stride;
-        a.sampled = l.sampled;
+        a.kept = l.kept;
         a.first = reinterpret_cast<uint64_t*>(ws + l.first);
         a.cand = reinterpret_cast<uint64_t*>(ws + l.cand);
         a.cand_count = ws + l.count;
