@@ -445,11 +445,11 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_lp_few(const uint16_t* x, in
     constexpr int kWarps = kFewThreads / 32;
     wait_prev_grid();
     extern __shared__ __align__(16) uint16_t xs[];    // [T][wide]
+    constexpr int kPer = T == 1 ? 8 : T == 2 ? 4 : 2; // warps to a row, at the end
     __shared__ Stat sh[kWarps][T];
-    __shared__ uint64_t lists[kWarps][32], least;
+    __shared__ uint64_t lists[kWarps][T][32], joined[kWarps][32], least[T];
     __shared__ uint32_t last;
-    __shared__ float2 done;
-    __shared__ int chosen, which[kFewBlocks];
+    __shared__ int chosen[T], which[T][kFewBlocks];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int wide = (int)((hidden + 7) / 8 * 8);
     const float c = a.scale * kLog2e;
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_lp_few(const uint16_t* x, in
     }
     const int64_t warps = (int64_t)gridDim.x * kWarps, me = (int64_t)blockIdx.x * kWarps + warp;
     int have = 0;
-    int64_t mine = 0;                                 // the vocabulary entry that the lane holds
+    int64_t holds = 0;                                // the vocabulary entry that the lane holds
     auto flush = [&]() {
 #pragma unroll
         for (int t = 0; t < T; t++) {
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_lp_few(const uint16_t* x, in
             const Stat one = any && held[t] != -INFINITY ? Stat{held[t], held[t] == held[t] ? 1.0f : held[t], 0.0f} : none();
             st[t] = join(st[t], warp_join(one, c), c);
             if (a.top)
-                list[t] = lists_merged(list[t], sorted(any && held[t] > -INFINITY ? key_of(held[t], (uint32_t)mine) : 0, lane), lane);
+                list[t] = lists_merged(list[t], sorted(any && held[t] > -INFINITY ? key_of(held[t], (uint32_t)holds) : 0, lane), lane);
         }
         have = 0;
     };
@@ -553,71 +553,88 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_lp_few(const uint16_t* x, in
                 if (lane == have) held[t] = z;
                 if (lane == 0 && v + q == a.targets[t]) target_logit[t] = z;
             }
-            if (lane == have) mine = v + q;
+            if (lane == have) holds = v + q;
             if (++have == 32) flush();
         }
     }
     if (have) flush();
 #pragma unroll
-    for (int t = 0; t < T; t++)
+    for (int t = 0; t < T; t++) {
         if (lane == 0) sh[warp][t] = st[t];
-    __syncthreads();
-    if (warp < T) {                                   // a warp a row: the block's
-        const Stat r = warp_join(lane < kWarps ? sh[lane][warp] : none(), c);
-        if (lane == 0) part[(int64_t)warp * gridDim.x + blockIdx.x] = r;
+        lists[warp][t][lane] = list[t];
     }
-    if (a.top)
-#pragma unroll
-        for (int t = 0; t < T; t++) {
-            const uint64_t best = block_merged(list[t], lists, warp, lane);
-            if (warp == 0 && lane < a.top) a.cand[((int64_t)t * gridDim.x + blockIdx.x) * a.top + lane] = best;
+    // the warps' statistics and lists: kPer warps to a row
+    const int t = warp / kPer, wi = warp % kPer;
+    const bool on = t < T;
+    auto merged = [&](uint64_t x) {                   // of a row's warps, in its first
+        __syncthreads();
+        joined[warp][lane] = x;
+        for (int o = kPer / 2; o > 0; o >>= 1) {
+            __syncthreads();
+            if (wi < o) joined[warp][lane] = x = lists_merged(x, joined[warp + o][lane], lane);
         }
+        return x;
+    };
+    __syncthreads();
+    if (on && wi == 0) {
+        const Stat r = warp_join(lane < kWarps ? sh[lane][t] : none(), c);
+        if (lane == 0) part[(int64_t)t * gridDim.x + blockIdx.x] = r;
+    }
+    if (a.top) {
+        uint64_t best = 0;
+        if (on)
+            for (int k = wi; k < kWarps; k += kPer)
+                best = lists_merged(best, lists[k][t][lane], lane);
+        best = merged(best);
+        if (on && wi == 0 && lane < a.top) a.cand[((int64_t)t * gridDim.x + blockIdx.x) * a.top + lane] = best;
+    }
     __threadfence();                                  // statistics, keys and target logits, before the count
     __syncthreads();
     if (threadIdx.x == 0) last = atomicAdd(&a.head->joined, 1u) == gridDim.x - 1;
+    if (threadIdx.x < T) chosen[threadIdx.x] = 0;
     __syncthreads();
     if (!last) return;
     __threadfence();
-    // the blocks' statistics, two to a thread, in a fixed order; of their lists, those
-    // that start no lower than the top-th of the threads' best
-    constexpr int kEach = (kFewBlocks + kFewThreads - 1) / kFewThreads;
+    // the blocks' statistics, kEach to a lane, in a fixed order; of their lists, those
+    // that start no lower than the top-th of the lanes' best
+    constexpr int kEach = (kFewBlocks + 32 * kPer - 1) / (32 * kPer);
     const int blocks = (int)gridDim.x;
-    for (int t = 0; t < T; t++) {
-        Stat r = none();
-        uint64_t best[kEach], most = 0;
+    Stat r = none();
+    uint64_t best[kEach], most = 0;
 #pragma unroll
-        for (int u = 0; u < kEach; u++) {
-            const int k = (int)threadIdx.x + u * kFewThreads;
-            best[u] = 0;
-            if (k >= blocks) continue;
-            const Stat* p = part + (int64_t)t * blocks + k;
-            if (a.top) best[u] = load_key(a.cand + ((int64_t)t * blocks + k) * a.top);
-            r = join(r, Stat{__ldcg(&p->mx), __ldcg(&p->sum), __ldcg(&p->t)}, c);
-            most = key_max(most, best[u]);
-        }
-        r = warp_join(r, c);
-        __syncthreads();
-        if (lane == 0) sh[warp][0] = r;
-        __syncthreads();
-        if (warp == 0) {
-            r = warp_join(lane < kWarps ? sh[lane][0] : none(), c);
-            if (lane == 0) done = finish_row(a, t, r);
-        }
-        if (!a.top) continue;
-        uint64_t bound = block_merged(sorted(most, lane), lists, warp, lane);
-        if (warp == 0 && lane == a.top - 1) least = bound;
-        if (threadIdx.x == 0) chosen = 0;
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < kEach; u++)               // 0: the block has none
-            if (best[u] && best[u] >= least) which[atomicAdd(&chosen, 1)] = (int)threadIdx.x + u * kFewThreads;
-        __syncthreads();
-        uint64_t mine = 0;
-        for (int k = warp; k < chosen; k += kWarps)
-            mine = lists_merged(mine, lane < a.top ? load_key(a.cand + ((int64_t)t * blocks + which[k]) * a.top + lane) : 0, lane);
-        mine = block_merged(mine, lists, warp, lane);
-        if (warp == 0) write_top(a, t, mine, done, lane);
+    for (int u = 0; u < kEach; u++) {
+        const int k = wi * 32 + lane + u * 32 * kPer;
+        best[u] = 0;
+        if (!on || k >= blocks) continue;
+        const Stat* p = part + (int64_t)t * blocks + k;
+        if (a.top) best[u] = load_key(a.cand + ((int64_t)t * blocks + k) * a.top);
+        r = join(r, Stat{__ldcg(&p->mx), __ldcg(&p->sum), __ldcg(&p->t)}, c);
+        most = key_max(most, best[u]);
     }
+    r = warp_join(r, c);
+    if (lane == 0) sh[warp][0] = r;
+    __syncthreads();
+    float2 done = make_float2(0.0f, 0.0f);
+    if (on && wi == 0) {
+        r = warp_join(lane < kPer ? sh[warp + lane][0] : none(), c);
+        if (lane == 0) done = finish_row(a, t, r);
+        done.x = __shfl_sync(kAll, done.x, 0);
+        done.y = __shfl_sync(kAll, done.y, 0);
+    }
+    if (!a.top) return;
+    const uint64_t bound = merged(sorted(most, lane));
+    if (on && wi == 0 && lane == a.top - 1) least[t] = bound;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kEach; u++)                   // 0: the block has none
+        if (best[u] && best[u] >= least[t]) which[t][atomicAdd(&chosen[t], 1)] = wi * 32 + lane + u * 32 * kPer;
+    __syncthreads();
+    uint64_t mine = 0;
+    if (on)
+        for (int k = wi; k < chosen[t]; k += kPer)
+            mine = lists_merged(mine, lane < a.top ? load_key(a.cand + ((int64_t)t * blocks + which[t][k]) * a.top + lane) : 0, lane);
+    mine = merged(mine);
+    if (on && wi == 0) write_top(a, t, mine, done, lane);
 }
 
 // One block: the row factors of G and what the products are multiplied by.  G =
