@@ -31,9 +31,9 @@ def test_plan(n, v, d, top):
     assert p.flops_forward == 2 * n * v * d and p.flops_backward == 6 * n * v * d
     assert p.workspace_bytes >= c.workspace_bytes and p.rows % 256 == 0 and p.rows >= 256
     strips = -(-v // 256) * 2
-    assert p.workspace_bytes <= max(c.workspace_bytes, 2 * (1 << 29) + min(n, 256) * strips * (16 + 8 * top))
+    assert p.workspace_bytes <= max(c.workspace_bytes, (5 << 29) + min(n, 256) * strips * (12 + 512))
     if n > 3:
-        assert p.workspace_bytes >= min(n, p.rows) * strips * 8 * top
+        assert p.workspace_bytes >= min(n, p.rows) * (strips * 12 + (4 * v if top else 0))
 
 
 def test_plan_refusals():

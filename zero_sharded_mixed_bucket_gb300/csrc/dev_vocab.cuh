@@ -29,9 +29,9 @@ constexpr int kFewTokens = 3, kFewThreads = 256, kFewBlocks = 456;   // tokens w
 constexpr int kFewSmem = 64 * 1024;                   // all tokens' values, 16 bits each
 
 // Epilogues: softmax statistics; G of cross entropy; binary32 sums; 16-bit results
-// times alpha; statistics with the entropy's sum, besides the logits themselves, or
-// the alternatives among them; G of log probabilities and entropies.
-enum { kEpiLse, kEpiGrad, kEpiAcc, kEpiOut, kEpiStat, kEpiKeep, kEpiTop, kEpiLpGrad };
+// times alpha; statistics with the entropy's sum, and besides all logits, or those of
+// strips that reach a bound; G of log probabilities and entropies.
+enum { kEpiLse, kEpiGrad, kEpiAcc, kEpiOut, kEpiStat, kEpiKeep, kEpiSome, kEpiLpGrad };
 
 // Workspace head.
 struct CeHead {
@@ -65,13 +65,12 @@ struct GemmArgs {
     uint16_t* out;               // kEpiOut: stored from registers, when a row's end is not on 16 bytes (else NULL)
     int64_t out_stride;
     float scale_log2e;           // log probabilities: the logits' scale times log2 e
-    float* part_t;               // kEpiStat, kEpiKeep, kEpiTop: [strips][m], a strip's sum of e (z - maximum)
+    float* part_t;               // log probabilities' statistics: [strips][m], a strip's sum of e (z - maximum)
     const float* coef_h;         // kEpiLpGrad: row factors of the entropy's gradient (NULL: none)
     const float* entropy;        //   [m]
-    const float* least;          // kEpiTop: [m], alternatives are at least this
-    uint64_t* cand;              //   [m][strips][top]: keys of a strip's alternatives, of strips of this product
-    uint8_t* cand_count;         //   [m][count_stride]
-    int top, strips, count_stride;
+    const float* least;          // kEpiSome: [m], the rows' bounds
+    float* logits;               //   [m][logit_stride], of this product's first entry on
+    int64_t logit_stride;        //   a multiple of kStrip
 };
 
 template <int DT>
@@ -129,32 +128,14 @@ __device__ __forceinline__ Tile tile_at(const GemmArgs& g, uint32_t t)
     return r;
 }
 
-// A strip's statistics for log probabilities, and (TOP) its alternatives.
-//
-// Alternatives: the `top` largest logits of the strip that are at least the row's
-// `least`, a value that the row is known to have `top` logits of; keys in falling
-// order.  A lane keeps the maxima of 8 groups of 16 columns, and a round takes
-// the largest of all from each lane that still has one, group by group as lanes
-// have need: what it costs goes by how many there are.  (`least` from 4096 entries
-// leaves two rounds for 8 alternatives, three for 20, beside the next tile's products;
-// without it a strip takes `top` rounds, 40 us a tile for 20.)
-template <bool TOP>
-__device__ __forceinline__ void lp_statistics(const GemmArgs& g, float (&z)[kStrip], int strip, int64_t row, bool live,
-                                              uint32_t index0)
+// A strip's statistics for log probabilities; its maximum.
+__device__ __forceinline__ float lp_statistics(const GemmArgs& g, const float (&z)[kStrip], int strip, int64_t row, bool live)
 {
-    constexpr int kG = 16, kGroups = kStrip / kG;
-    float gm[kGroups];
+    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int q = 0; q < kGroups; q++) {
-        gm[q] = z[kG * q];
-#pragma unroll
-        for (int k = 1; k < kG; k++)
-            gm[q] = fmaxf(gm[q], z[kG * q + k]);
-    }
-    float top = gm[0];
-#pragma unroll
-    for (int q = 1; q < kGroups; q++)
-        top = fmaxf(top, gm[q]);
+    for (int k = 0; k < kStrip; k++)
+        m4[k & 3] = fmaxf(m4[k & 3], z[k]);
+    const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
     // (z - top) first: the largest term is exactly 1; held finite beside a term of 0
     const float ref = top == -INFINITY ? 0.0f : top;
     float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f}, t4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -164,46 +145,11 @@ __device__ __forceinline__ void lp_statistics(const GemmArgs& g, float (&z)[kStr
         s4[k & 3] += e;
         t4[k & 3] = fmaf(e, fmaxf(d, -3e38f), t4[k & 3]);
     }
-    const float s = (s4[0] + s4[1]) + (s4[2] + s4[3]), t = (t4[0] + t4[1]) + (t4[2] + t4[3]);
     if (live) {
-        g.part[(int64_t)strip * g.m + row] = make_float2(top, s);
-        g.part_t[(int64_t)strip * g.m + row] = t;
+        g.part[(int64_t)strip * g.m + row] = make_float2(top, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+        g.part_t[(int64_t)strip * g.m + row] = (t4[0] + t4[1]) + (t4[2] + t4[3]);
     }
-    if constexpr (TOP) {
-        const float least = live ? g.least[row] : INFINITY;
-        uint64_t* out = g.cand + (row * g.strips + strip) * g.top;
-        int n = 0;
-        for (int round = 0; round < g.top; round++) {
-            float cur = gm[0];
-#pragma unroll
-            for (int q = 1; q < kGroups; q++)
-                cur = fmaxf(cur, gm[q]);
-            const bool on = live && cur >= least && cur > -INFINITY;
-            if (!__any_sync(0xffffffffu, on)) break;
-            int group = kGroups;
-#pragma unroll
-            for (int q = kGroups - 1; q >= 0; q--)
-                if (on && gm[q] == cur) group = q;
-#pragma unroll
-            for (int q = 0; q < kGroups; q++) {
-                if (!__any_sync(0xffffffffu, group == q)) continue;
-                int at = 0;
-#pragma unroll
-                for (int k = kG - 1; k >= 0; k--)
-                    if (z[kG * q + k] == cur) at = k;
-                const int gone = group == q ? at : kG;
-                float m = -INFINITY;
-#pragma unroll
-                for (int k = 0; k < kG; k++) {
-                    if (k == gone) z[kG * q + k] = -INFINITY;
-                    m = fmaxf(m, z[kG * q + k]);
-                }
-                gm[q] = m;
-                if (group == q) out[n++] = key_of(cur, index0 + kG * q + at);
-            }
-        }
-        if (live) g.cand_count[row * g.count_stride + strip] = (uint8_t)n;
-    }
+    return top;
 }
 
 // C = A B^T for 256 x 256 tiles, a pair of CTAs per tile, each pair striding
@@ -410,7 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
                 if (lane == 0) tc::mbar_arrive_leader(acc_empty + 8 * buf);
             }
             if (!ok) break;
-            if constexpr (EPI == kEpiLse || EPI == kEpiStat || EPI == kEpiKeep || EPI == kEpiTop) {
+            if constexpr (EPI == kEpiLse || EPI == kEpiStat || EPI == kEpiKeep || EPI == kEpiSome) {
                 // the strip's maximum and its sum
                 const int64_t left = g.n - col0;
                 if (left < kStrip) {
@@ -441,10 +387,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1) k_ce_
                     if (live)
                         g.part[((int64_t)w.nt * 2 + half) * g.m + row] = make_float2(top, (s4[0] + s4[1]) + (s4[2] + s4[3]));
                 } else {
-                    lp_statistics<EPI == kEpiTop>(g, z, w.nt * 2 + half, row, live, (uint32_t)(g.b_y0 + col0));
+                    const float top = lp_statistics(g, z, w.nt * 2 + half, row, live);
+                    if constexpr (EPI == kEpiSome) {
+                        // a row's strip is its lane's alone, 512 bytes, which few rows have to write
+                        const bool in = live && left > 0 && top >= g.least[row];
+                        if (__any_sync(0xffffffffu, in)) {
+                            float* dst = g.logits + row * g.logit_stride + col0;
+#pragma unroll
+                            for (int k = 0; k < kStrip; k += 4)
+                                if (in) *reinterpret_cast<float4*>(dst + k) = make_float4(z[k], z[k + 1], z[k + 2], z[k + 3]);
+                        }
+                    }
                 }
             }
-            if constexpr (EPI != kEpiLse && EPI != kEpiStat && EPI != kEpiTop) {
+            if constexpr (EPI != kEpiLse && EPI != kEpiStat && EPI != kEpiSome) {
                 if constexpr (EPI == kEpiGrad) {
 #pragma unroll
                     for (int k = 0; k < kStrip; k++)

@@ -12,7 +12,7 @@ using namespace vocab;
 namespace {
 
 constexpr int kMostTop = 32;                          // alternatives: a warp's lanes
-constexpr int64_t kSample = 4096;                     // entries that give the alternatives' threshold
+constexpr int64_t kSample = 4096;                     // entries that give the rows their bounds
 constexpr unsigned kAll = 0xffffffffu;
 
 struct LpArgs {
@@ -29,13 +29,10 @@ struct LpArgs {
     float* entropy;              // may be NULL
     float2* stat;                // [n] maximum, log of the sum
     int top;
-    const float* logits;         // [n][logit_stride]: of the first `kept` entries
-    int64_t logit_stride, kept;
-    uint64_t* first;             // [n][top]: the alternatives among those
-    float* least;                // [n]: the last of them
-    uint64_t* cand;              // [n][cand_strips][top]: those of the strips behind; few rows: of the blocks
-    const uint8_t* cand_count;   // [n][count_stride]
-    int cand_strips, count_stride;
+    const float* logits;         // [n][logit_stride]: all, or those of the sample and of strips that reach `least`
+    int64_t logit_stride;
+    float* least;                // [n]: the last alternative of the row's sample (NULL: all logits are kept)
+    uint64_t* cand;              // few rows: [n][blocks][top]
     float* top_logp;
     int64_t* top_index;
 };
@@ -252,14 +249,14 @@ __device__ __forceinline__ void write_top(const LpArgs& a, int64_t i, uint64_t l
     a.top_index[i * a.top + lane] = list && !failed ? (int64_t)(0xffffffffu - (uint32_t)list) : -1;
 }
 
-// Per row: the first `top` of the logits that were kept, by W warps.  Of the strips'
-// maxima, two sets to a lane, the top-th largest set's is a bound that the row is
-// known to have `top` logits of; only strips whose maximum is no less are read, 9 of
-// 393 for 8 alternatives, 22 for 20 or 45 for 32, and have about as many logits to
-// sort.  FINAL: written out; else kept for k_lp_top, the last of them as the row's
-// `least`.
+// Per row: the first `top` of its logits, by W warps.  Of the strips' maxima, two
+// sets to a lane, the top-th largest set's is a bound that the row is known to have
+// `top` logits of; only strips whose maximum is no less are read, 9 of 393 for 8
+// alternatives, 22 for 20 or 45 for 32, and have about as many logits to sort.
+// FINAL: written out; else only the sample's are there, and their last becomes the
+// row's `least`.
 template <int W, bool FINAL>
-__global__ void __launch_bounds__(256) k_lp_first(const __grid_constant__ LpArgs a)
+__global__ void __launch_bounds__(256) k_lp_top(const __grid_constant__ LpArgs a)
 {
     constexpr int U = 8;                              // maxima, or strips, on their way
     wait_prev_grid();
@@ -270,7 +267,7 @@ __global__ void __launch_bounds__(256) k_lp_first(const __grid_constant__ LpArgs
     const int64_t i = W == 1 ? (int64_t)blockIdx.x * 8 + warp : blockIdx.x;
     if (W == 1 && i >= a.n) return;
     const float2* part = a.part + i;
-    const int strips = (int)((a.kept + kStrip - 1) / kStrip), kept = (int)a.kept;
+    const int strips = FINAL ? a.strips : (int)(kSample / kStrip);
     const int first = (W == 1 ? 0 : warp * 32) + lane;            // strips first, first + 32 W, ...
     float most[2] = {-INFINITY, -INFINITY};
     for (int s0 = first - lane; s0 < strips; s0 += 32 * W * U) {
@@ -293,6 +290,7 @@ __global__ void __launch_bounds__(256) k_lp_first(const __grid_constant__ LpArgs
     }
     Gather g = gather(held[warp], a.top);
     g.raise(__shfl_sync(kAll, bound, a.top - 1) & ~0xffffffffull);            // of whatever index
+    if (FINAL && a.least) g.raise(key_of(fmaxf(a.least[i], -3.4028235e38f), 0xffffffffu));       // others are not there
     const float* z = a.logits + i * a.logit_stride;
     int* mine = chosen[warp];
     for (int s0 = first - lane; s0 < strips; s0 += 32 * W * U) {
@@ -311,8 +309,8 @@ __global__ void __launch_bounds__(256) k_lp_first(const __grid_constant__ LpArgs
             float4 q[U];
 #pragma unroll
             for (int u = 0; u < U; u++) {
-                at[u] = k0 + u < n ? mine[k0 + u] * kStrip + 4 * lane : kept;
-                if (at[u] < kept) q[u] = *reinterpret_cast<const float4*>(z + at[u]);
+                at[u] = k0 + u < n ? mine[k0 + u] * kStrip + 4 * lane : 0;
+                if (k0 + u < n) q[u] = *reinterpret_cast<const float4*>(z + at[u]);
             }
 #pragma unroll
             for (int u = 0; u < U; u++) {
@@ -322,7 +320,7 @@ __global__ void __launch_bounds__(256) k_lp_first(const __grid_constant__ LpArgs
                 unsigned in = 0;
 #pragma unroll
                 for (int k = 0; k < 4; k++)
-                    if (at[u] + k < kept && f[k] >= g.least) in |= 1u << k;
+                    if (at[u] + k < a.vocab && f[k] >= g.least) in |= 1u << k;
                 while (__any_sync(kAll, in)) {
                     const int k = in ? __ffs(in) - 1 : 0;
                     const float v = k == 0 ? f[0] : k == 1 ? f[1] : k == 2 ? f[2] : f[3];
@@ -341,90 +339,8 @@ __global__ void __launch_bounds__(256) k_lp_first(const __grid_constant__ LpArgs
     if constexpr (FINAL) {
         write_top(a, i, list, a.stat[i], lane);
     } else {
-        if (lane < a.top) a.first[i * a.top + lane] = list;
         if (lane == a.top - 1) a.least[i] = list ? logit_of(list) : -INFINITY;
     }
-}
-
-// Per row: its first `top` alternatives, from those of the sample and of the strips
-// behind; a warp a row.  A strip has few or none, and a lane 16 strips' counts: the
-// keys' places are listed first (in whatever order), so that every lane then has
-// keys to load; of those, the ones below a bound that the row is known to have
-// `top` of are dropped before any are sorted.
-constexpr int kPlaces = 512, kTopWarps = 4;
-
-__global__ void __launch_bounds__(32 * kTopWarps) k_lp_top(const __grid_constant__ LpArgs a)
-{
-    constexpr int U = 8;                              // keys of a lane on their way
-    wait_prev_grid();
-    __shared__ uint32_t places[kTopWarps][kPlaces + 32 * kMostTop];
-    __shared__ uint64_t held[kTopWarps][64];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t i = (int64_t)blockIdx.x * kTopWarps + warp;
-    if (i >= a.n) return;
-    const uint64_t* keys = a.cand + i * a.cand_strips * a.top;
-    const uint8_t* counts = a.cand_count + i * a.count_stride;
-    uint32_t* mine = places[warp];
-    Gather g = gather(held[warp], a.top);
-    g.list = lane < a.top ? a.first[i * a.top + lane] : 0;
-    g.raise(__shfl_sync(kAll, g.list, a.top - 1));
-    int listed = 0;
-    auto look = [&]() {
-        __syncwarp();
-        for (int k0 = 0; k0 < listed; k0 += 32 * U) {
-            uint64_t key[U], most = 0;
-#pragma unroll
-            for (int u = 0; u < U; u++) {
-                const int k = k0 + 32 * u + lane;
-                key[u] = k < listed ? keys[mine[k]] : 0;
-                most = key_max(most, key[u]);
-            }
-            g.raise(__shfl_sync(kAll, sorted(most, lane), a.top - 1));          // the lanes' largest
-#pragma unroll
-            for (int u = 0; u < U; u++)
-                g.add(key[u] != 0, key[u], lane);
-        }
-        __syncwarp();
-        listed = 0;
-    };
-    for (int s0 = 0; s0 < a.cand_strips; s0 += 512) {
-        const int s = s0 + 16 * lane;
-        uint4 q = make_uint4(0, 0, 0, 0);
-        if (s < a.cand_strips) q = *reinterpret_cast<const uint4*>(counts + s);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-        // (no more than there is room for, also where a wait ran out and no count was written)
-        auto count = [&](int k) { return s + k < a.cand_strips ? min((int)(w[k >> 2] >> (8 * (k & 3)) & 0xffu), a.top) : 0; };
-        int sum = 0;
-#pragma unroll
-        for (int k = 0; k < 16; k++)
-            sum += count(k);
-        const int total = __reduce_add_sync(kAll, sum);
-        // all 16 of a lane at once, or one after another
-        const int steps = listed + total <= kPlaces + 32 * kMostTop ? 1 : 16;
-        for (int step = 0; step < steps; step++) {
-            int n = 0;
-#pragma unroll
-            for (int k = 0; k < 16; k++)
-                if (steps == 1 || k == step) n += count(k);
-            int at = n;                               // inclusive sums over the lanes
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int p = __shfl_up_sync(kAll, at, o);
-                if (lane >= o) at += p;
-            }
-            const int added = __shfl_sync(kAll, at, 31);
-            at += listed - n;
-#pragma unroll
-            for (int k = 0; k < 16; k++)
-                if (steps == 1 || k == step)
-                    for (int j = 0; j < count(k); j++)
-                        mine[at++] = (uint32_t)(s + k) * (uint32_t)a.top + j;
-            listed += added;
-            if (listed > kPlaces) look();
-        }
-    }
-    look();
-    write_top(a, i, g.all(lane), a.stat[i], lane);
 }
 
 // ---- few rows -------------------------------------------------------------------------
@@ -696,50 +612,42 @@ zero_status_t cuda_failed(cudaError_t e, const char* what)
 
 int64_t strips_of(int64_t vocab) { return ceil_div(vocab, kBN) * 2; }
 
-// Entries whose logits are kept in memory for the alternatives: all of them up to 256
-// MB, or where they are few; else those that give every row a threshold for the
-// others.  (1023 rows of 50257, hidden 1600, 20 alternatives: 148 us with all, 157
-// with 4096; 4096 rows, hidden 768, 8 alternatives: 412 and 315, 256 rows 48 and 60.)
-int64_t kept_entries(int64_t rows, int64_t vocab, int64_t top)
+// Whether all logits are kept in memory for the alternatives: up to 256 MB, or where
+// a sample would be most of them; else those of a sample, which gives every row a bound,
+// and of the strips that reach it.  KEPT
+bool all_kept(int64_t tokens, int64_t vocab)
 {
-    return !top ? 0 : vocab <= kSample + kSample / 4 || rows * vocab <= (int64_t(1) << 26) ? vocab : kSample;
+    return vocab <= kSample + kSample / 4 || tokens * vocab <= (int64_t(1) << 26);
 }
 
-// Rows at a time of a forward pass: what the strips leave (12 bytes each, and 9 and up
-// for alternatives) and the logits that are kept take about 512 MiB.
-int64_t rows_at_once(int64_t tokens, int64_t vocab, int64_t top)
+int64_t logit_stride(int64_t vocab) { return ceil_div(vocab, kStrip) * kStrip; }
+
+// Rows at a time of a forward pass: what the strips leave, 12 bytes each, takes about
+// 512 MiB, or with alternatives that and the logits 2 GiB.
+int64_t rows_at_once(int64_t vocab, int64_t top)
 {
-    const int64_t kept = kept_entries(tokens, vocab, top);
-    const int64_t per = strips_of(vocab) * (12 + (kept < vocab && top ? 1 + 8 * top : 0)) + 4 * kept + 8 * top;
-    const int64_t fit = (int64_t(1) << 29) / per / kBM * kBM;
+    const int64_t per = strips_of(vocab) * 12 + (top ? 4 * logit_stride(vocab) : 0);
+    const int64_t fit = (int64_t(1) << (top ? 31 : 29)) / per / kBM * kBM;
     return fit < kBM ? kBM : fit;
 }
 
 // Byte offsets of a forward pass in the workspace.
 struct LpLayout {
-    int64_t target_logit, stat, least, part, part_t, logits, first, count, cand, end;
-    int64_t kept, logit_stride;
-    int cand_strips, count_stride;
+    int64_t target_logit, stat, least, part, part_t, logits, cand, end;
 };
 
 LpLayout lp_layout(const zero_lp_plan_t& p, bool few)
 {
     LpLayout l;
     const int64_t rows = p.rows < p.tokens ? p.rows : p.tokens, strips = strips_of(p.vocab);
-    l.kept = few ? 0 : kept_entries(p.tokens, p.vocab, p.top);
-    l.logit_stride = (l.kept + 3) / 4 * 4;
-    l.cand_strips = few ? kFewBlocks : l.kept < p.vocab && p.top ? (int)(strips - l.kept / kStrip) : 0;
-    l.count_stride = few ? 0 : (l.cand_strips + 15) / 16 * 16;
     l.target_logit = sizeof(CeHead);
     l.stat = l.target_logit + up256(rows * 4);
     l.least = l.stat + up256(rows * 8);
     l.part = l.least + up256(rows * 4);
     l.part_t = l.part + up256(few ? kFewBlocks * rows * (int64_t)sizeof(Stat) : strips * rows * 8);
     l.logits = l.part_t + (few ? 0 : up256(strips * rows * 4));
-    l.first = l.logits + up256(rows * l.logit_stride * 4);
-    l.count = l.first + up256(rows * p.top * 8);
-    l.cand = l.count + up256(l.count_stride * rows);
-    l.end = l.cand + up256(l.cand_strips * rows * p.top * 8);
+    l.cand = l.logits + (few || !p.top ? 0 : up256(rows * logit_stride(p.vocab) * 4));
+    l.end = l.cand + (few ? up256(kFewBlocks * rows * p.top * 8) : 0);
     return l;
 }
 
@@ -786,11 +694,11 @@ cudaError_t launch_few(const zero_lp_plan_t& p, int64_t blocks, const void* x, c
 
 // Warps to a row: 8 where there are few rows and more than a sample's strips.
 template <bool FINAL>
-cudaError_t launch_first(const LpArgs& a, cudaStream_t s)
+cudaError_t launch_top(const LpArgs& a, cudaStream_t s)
 {
-    if (a.n > 2 * 152 || a.kept <= 64 * kStrip)
-        return launch_after(k_lp_first<1, FINAL>, dim3((unsigned)ceil_div(a.n, 8)), 256, 0, s, a);
-    return launch_after(k_lp_first<8, FINAL>, dim3((unsigned)a.n), 256, 0, s, a);
+    if (a.n > 2 * 152 || !FINAL || a.strips <= 64)
+        return launch_after(k_lp_top<1, FINAL>, dim3((unsigned)ceil_div(a.n, 8)), 256, 0, s, a);
+    return launch_after(k_lp_top<8, FINAL>, dim3((unsigned)a.n), 256, 0, s, a);
 }
 
 // The forward pass of rows [r0, r0 + a.n).
@@ -804,7 +712,7 @@ cudaError_t forward_rows(const zero_lp_plan_t& p, const void* x, const void* w, 
     g.a_rows = a_rows_of(a.n);
     ok = make_map(&g.a, type, xr, a.n, p.hidden, p.x_stride, g.a_rows) &&
          make_map(&g.b, type, w, p.vocab, p.hidden, p.w_stride, kBN / 2) &&
-         (!a.top || make_map(&g.c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.logits, a.n, a.kept, a.logit_stride, 32));
+         (!a.top || make_map(&g.c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.logits, a.n, p.vocab, a.logit_stride, 32));
     if (!ok) return cudaSuccess;
     g.m = a.n;
     g.m_tiles = (int)ceil_div(a.n, kBM);
@@ -815,12 +723,8 @@ cudaError_t forward_rows(const zero_lp_plan_t& p, const void* x, const void* w, 
     g.targets = a.targets;
     g.target_logit = reinterpret_cast<float*>(ws + l.target_logit);
     g.scale_log2e = a.scale * kLog2e;
-    g.top = a.top;
-    g.strips = a.cand_strips;
-    g.count_stride = a.count_stride;
-    g.cand = a.cand;
-    g.cand_count = const_cast<uint8_t*>(a.cand_count);
     g.least = a.least;
+    g.logit_stride = a.logit_stride;
     auto product = [&](int64_t v0, int64_t v1) {
         const int64_t s0 = v0 / kStrip;
         g.b_y0 = (int)v0;
@@ -828,19 +732,18 @@ cudaError_t forward_rows(const zero_lp_plan_t& p, const void* x, const void* w, 
         g.n_tiles = (int)ceil_div(g.n, kBN);
         g.part = const_cast<float2*>(a.part) + s0 * a.n;
         g.part_t = const_cast<float*>(a.part_t) + s0 * a.n;
+        g.logits = const_cast<float*>(a.logits) + v0;
         g.withhold = first && v0 == 0 && withheld_product() > 0;
         return !a.top ? gemm<kEpiStat, false, false>(p.dtype, g, s)
-               : v0 == 0 ? gemm<kEpiKeep, false, false>(p.dtype, g, s) : gemm<kEpiTop, false, false>(p.dtype, g, s);
+               : v0 == 0 ? gemm<kEpiKeep, false, false>(p.dtype, g, s) : gemm<kEpiSome, false, false>(p.dtype, g, s);
     };
-    const bool two = a.top && a.kept < p.vocab;
-    cudaError_t e = product(0, two ? a.kept : p.vocab);
-    if (two) {
-        if (e == cudaSuccess) e = launch_first<false>(a, s);
-        if (e == cudaSuccess) e = product(a.kept, p.vocab);
+    cudaError_t e = product(0, a.least ? kSample : p.vocab);
+    if (a.least) {
+        if (e == cudaSuccess) e = launch_top<false>(a, s);
+        if (e == cudaSuccess) e = product(kSample, p.vocab);
     }
     if (e == cudaSuccess) e = launch_after(k_lp_join, dim3((unsigned)ceil_div(a.n, kJoinRows)), kJoinThreads, 0, s, a);
-    if (e == cudaSuccess && a.top)
-        e = two ? launch_after(k_lp_top, dim3((unsigned)ceil_div(a.n, kTopWarps)), 32 * kTopWarps, 0, s, a) : launch_first<true>(a, s);
+    if (e == cudaSuccess && a.top) e = launch_top<true>(a, s);
     return e;
 }
 
@@ -870,7 +773,7 @@ zero_status_t zero_lp_plan(int64_t tokens, int64_t vocab, int64_t hidden, int32_
     out->dtype = dtype;
     out->splits = c.splits;
     out->top = top;
-    out->rows = rows_at_once(tokens, vocab, top);
+    out->rows = rows_at_once(vocab, top);
     const int64_t forward = lp_layout(*out, few_tokens(c)).end;
     out->workspace_bytes = forward > c.workspace_bytes ? forward : c.workspace_bytes;
     out->flops_forward = c.flops_forward;
@@ -922,14 +825,9 @@ zero_status_t zero_lp_forward(const zero_lp_plan_t* plan, const void* x, const v
         a.stat = reinterpret_cast<float2*>(ws + l.stat);
         a.top = p.top;
         a.logits = reinterpret_cast<const float*>(ws + l.logits);
-        a.logit_stride = l.logit_stride;
-        a.kept = l.kept;
-        a.first = reinterpret_cast<uint64_t*>(ws + l.first);
+        a.logit_stride = logit_stride(p.vocab);
         a.cand = reinterpret_cast<uint64_t*>(ws + l.cand);
-        a.cand_count = ws + l.count;
-        a.cand_strips = l.cand_strips;
-        a.count_stride = l.count_stride;
-        a.least = reinterpret_cast<float*>(ws + l.least);
+        a.least = p.top && !all_kept(p.tokens, p.vocab) ? reinterpret_cast<float*>(ws + l.least) : nullptr;
         a.top_logp = top_logp + r0 * p.top;
         a.top_index = top_index + r0 * p.top;
         if (few) {
