@@ -265,6 +265,28 @@ def test_infinite_and_nan_logits(n):
     assert (j.ti[0] == -1).all() and j.logp[0].isnan()
 
 
+@pytest.mark.parametrize("n", [1, 3, 70])
+def test_logits_of_the_lowest_value(n):
+    """Entries masked by bfloat16's lowest value: probability 0, nothing in the entropy, no gradient."""
+    j = Job(n, 1000, 64, "bf16", top=4, ignore=0.0)
+    j.x[:, 0] = 1
+    j.w[:, 0] = 0
+    j.w[300:900] = 0
+    j.w[300:900, 0] = torch.finfo(torch.bfloat16).min
+    j.t.fill_(5)
+    j.forward()
+    keep = torch.cat([torch.arange(300), torch.arange(900, 1000)]).cuda()
+    lp = torch.log_softmax(j.x.double() @ j.w[keep].double().t(), 1)
+    assert (j.logp.double() - lp[:, 5]).abs().max() < 1e-5 and (j.ent.double() + (lp.exp() * lp).sum(1)).abs().max() < 1e-4
+    assert torch.isin(j.ti, keep).all()
+    one = torch.ones(n, device="cuda")
+    j.backward(one, one)
+    assert j.dw.isfinite().all() and (j.dw[300:900] == 0).all()
+    j.t.fill_(400)                                    # a masked entry given: its log probability is what the logits say
+    j.forward()
+    assert (j.logp < -3e38).all()
+
+
 def test_tokens_without_a_target_and_factors_of_zero():
     j = Job(300, 700, 64, "bf16", ignore=1.0)
     j.t.fill_(-100)
