@@ -68,6 +68,14 @@ __device__ __forceinline__ Stat join(const Stat& a, const Stat& b, float scale_l
     return r;
 }
 
+// b added to a, whose maximum is no less.
+__device__ __forceinline__ void add(Stat& a, const Stat& b, float scale_log2e)
+{
+    const float d = b.mx - (a.mx == -INFINITY ? 0.0f : a.mx), f = exp2_fast(d * scale_log2e);
+    a.sum = fmaf(b.sum, f, a.sum);
+    a.t += f > 0.0f ? f * fmaf(d, b.sum, b.t) : 0.0f;
+}
+
 __device__ __forceinline__ Stat shuffled(const Stat& a, int o)
 {
     return {__shfl_xor_sync(kAll, a.mx, o), __shfl_xor_sync(kAll, a.sum, o), __shfl_xor_sync(kAll, a.t, o)};
@@ -111,6 +119,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_lp_join(const __grid_constant_
     if (i < a.n)
         for (int s = part; s < a.strips; s += kJoinParts * kJoinAhead) {
             Stat q[kJoinAhead];
+            float top = r.mx;
 #pragma unroll
             for (int k = 0; k < kJoinAhead; k++) {
                 const int at = s + k * kJoinParts;
@@ -119,13 +128,12 @@ __global__ void __launch_bounds__(kJoinThreads) k_lp_join(const __grid_constant_
                     const float2 p = a.part[(int64_t)at * a.n + i];
                     q[k] = {p.x, p.y, a.part_t[(int64_t)at * a.n + i]};
                 }
+                top = fmaxf(top, q[k].mx);
             }
+            r = join(r, Stat{top, 0.0f, 0.0f}, c);    // to the new maximum
 #pragma unroll
-            for (int n = kJoinAhead / 2; n > 0; n /= 2)
-#pragma unroll
-                for (int k = 0; k < n; k++)
-                    q[k] = join(q[k], q[k + n], c);
-            r = join(r, q[0], c);
+            for (int k = 0; k < kJoinAhead; k++)
+                add(r, q[k], c);
         }
     r = join(r, shuffled(r, 8), c);
     r = join(r, shuffled(r, 16), c);
