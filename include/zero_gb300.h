@@ -585,9 +585,12 @@ zero_status_t zero_ln_backward(const zero_ln_plan_t* plan, const void* dy, const
  *   y * 2^(127 - e), rounded to nearest even once, from binary32;
  *   e: the least byte >= 0 with the block's largest |y| <= 448 * 2^(e - 127);
  *   a block with an infinity or a NaN: e = 255, codes 0x7f or 0xff (NaN).
- * Strides and pointers as for layer norm (x_stride: rows of x, residual, h, dh
- * and dx; y_stride: of y, dy, q and values); q_scale rows are scale_cols bytes
- * apart.  Outputs must not overlap inputs, but h may be x or residual itself and
+ * Rows may lie further apart than dim (strides, in values; x_stride: rows of x,
+ * residual, h, dh and dx; y_stride: of y, dy, q and values); what is between them is
+ * neither read nor written.  q_scale rows are scale_cols bytes apart.  Pointers need
+ * the alignment of their type only: rows that all start on 16-byte boundaries (the
+ * weight too) take 16-byte accesses, others single-value ones (1.4 to 1.7 times
+ * slower).  Outputs must not overlap inputs, but h may be x or residual itself and
  * dx may be dh itself.  88 bytes. */
 typedef struct zero_rms_plan {
     int64_t rows, dim;
@@ -708,8 +711,9 @@ zero_status_t zero_ce_status(const zero_ce_plan_t* plan, const void* workspace, 
  * than `top`, log probability -infinity and index -1.  The order is that of the
  * logits as computed: those closer than their binary32 sums' rounding may
  * change places.  A row with a NaN logit or an infinite one has NaN logp and
- * entropy.  Results do not depend on timing: equal calls give equal bits.
- * 104 bytes. */
+ * entropy.  With alternatives the workspace holds logits of `rows` tokens at a time
+ * while they are sought (binary32, 2 GiB at most unless 256 rows need more).
+ * Results do not depend on timing: equal calls give equal bits.  104 bytes. */
 typedef struct zero_lp_plan {
     int64_t tokens, vocab, hidden;
     int64_t x_stride, w_stride;  /* values between rows of x and dx, of w and dw */

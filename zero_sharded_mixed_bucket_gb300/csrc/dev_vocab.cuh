@@ -128,7 +128,10 @@ __device__ __forceinline__ Tile tile_at(const GemmArgs& g, uint32_t t)
     return r;
 }
 
-// A strip's statistics for log probabilities; its maximum.
+// A strip's statistics for log probabilities; its maximum.  Entropy is log S - T / S of
+// S = sum e and T = sum e (z - max): neither is a difference of large numbers, so a
+// likely token's keeps its digits.  Two instructions a logit more than the loss: 8192
+// x 50257 x 768 384 us, the loss 382-400.
 __device__ __forceinline__ float lp_statistics(const GemmArgs& g, const float (&z)[kStrip], int strip, int64_t row, bool live)
 {
     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};

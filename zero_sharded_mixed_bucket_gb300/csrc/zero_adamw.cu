@@ -426,7 +426,9 @@ __global__ void __launch_bounds__(kAd32Threads) k_adamw_check(const AdTable tab,
 // (GB300 has 2 of them a clock and SM, a fifth of what the values would need).  A
 // batch whose binary32 sum overflows, or is so small that squares may have
 // been cut off below 2^-126, is read again and summed in binary64 alone; so is one
-// that holds an infinity or a NaN, which is where those are counted.
+// that holds an infinity or a NaN, which is where those are counted.  Bound by
+// memory: 1.56e9 bfloat16 values 447-453 us, 6.9 TB/s; the 12-layer d=768 list 44
+// before a step of 514.
 constexpr int kNormThreads = 256, kNormUnroll = 4;
 constexpr int64_t kNormBlocks = 152 * 8;              // all resident at once
 // Up to so many chunks one block does all, a chunk to each of its warps, and needs no
@@ -583,6 +585,8 @@ __global__ void __launch_bounds__(kNormThreads) k_adamw_norm_join(int parts, con
 }
 
 // Gradients times the factor, rounded to their type; nothing to do where it is 1.
+// Bound by memory, of the 12-layer d=768 list in binary16 75 us, 6.6 TB/s; with a factor of 1 18 us, its
+// blocks' launch.
 template <int DT>
 __global__ void __launch_bounds__(kAd32Threads) k_adamw_clip(const AdTable tab, const float* norm)
 {

@@ -37,6 +37,14 @@ struct RmsArgs {
     int q_wide;                  // a vector's codes are stored at once
 };
 
+// 1 / sqrt(a), the approximation once corrected by what it leaves (an error of the
+// row's factor moves every value of the row at once).
+__device__ __forceinline__ float inverse_root(float a)
+{
+    const float r = rsqrtf(a), better = fmaf(0.5f * r, fmaf(-a * r, r, 1.0f), r);
+    return r > 0.0f && r < INFINITY ? better : r;
+}
+
 // ---- 8-bit results ------------------------------------------------------------------------
 // Codes are e4m3 (448 the largest), a block's scale 2^(e - 127) the least power of
 // two that keeps its largest magnitude within 448.  A power of two scales
@@ -143,7 +151,13 @@ __device__ __forceinline__ Vals<DT> weight_held(const void* p, int64_t i, int cn
 // x + r is rounded to the rows' type first (what the stream holds, and what
 // backward sees), then kept in registers; its slot is free for the next copy
 // before the group has its sum.  Q: values to a scale of 8-bit results, 0: none; a
-// block of them is Q / VE neighbouring lanes of a warp, or the row.
+// block of them is Q / VE neighbouring lanes of a warp, or a whole shorter row.
+// Bound by memory: 8192 x 4096 bfloat16 with a residual 47.5 us, 5.6 TB/s (a device
+// copy of the same bytes takes 43.3), issuing in 42 % of the cycles, 16
+// instructions a value; into 8 bits 41.5, 22 instructions a value in 55 %.  The
+// lane's weights stay in registers (read for every batch they are what a warp
+// waits for after the sum: 49.2), so blocks are few and large: with three blocks of
+// 256 threads an SM 49 and 47 us.
 template <int DT, int L, int V, int RB, int S, int T, int BLOCKS, bool RAGGED, int Q>
 __global__ void __launch_bounds__(T, BLOCKS) k_rms_forward_rows(const __grid_constant__ RmsArgs a)
 {
@@ -228,7 +242,7 @@ __global__ void __launch_bounds__(T, BLOCKS) k_rms_forward_rows(const __grid_con
                 for (int v = 0; v < V; v++)
                     if (b < here && cnt[v]) store_vec<DT, RAGGED, 16>(p + v * apart, h[b][v], cnt[v]);
         }
-        group_sum<L, RB, T>(ss, a.warps, sh, turn, [&](float t) { return rsqrtf(fmaf(t, inv, a.eps)); });
+        group_sum<L, RB, T>(ss, a.warps, sh, turn, [&](float t) { return inverse_root(fmaf(t, inv, a.eps)); });
 #pragma unroll
         for (int v = 0; v < V; v++) {
             if (!Q && cnt[v] == 0) continue;
@@ -289,6 +303,10 @@ __global__ void __launch_bounds__(T, BLOCKS) k_rms_forward_rows(const __grid_con
 // Backward: the stream's gradient of the rows, and the column sums of dy * xhat
 // over all the rows of a lane in registers, so h and dy are read once for both.
 // A block writes one partial sum per column (its groups joined in group order).
+// Bound by memory: 32768 x 1600 binary16 69.9 us with the sums' join, 6.0 TB/s; 26
+// instructions a value in 58 % of the cycles.  Weights read for every batch: 80.6;
+// as packed pairs of binary32 operations no less (70.9); two rows a batch instead of
+// four 85, one 107.
 template <int DT, int L, int V, int RB, int S, int T, int BLOCKS, bool RAGGED>
 __global__ void __launch_bounds__(T, BLOCKS) k_rms_backward_rows(const __grid_constant__ RmsArgs a)
 {
@@ -466,7 +484,11 @@ __global__ void __launch_bounds__(T, BLOCKS) k_rms_backward_rows(const __grid_co
 // One access a value.  W warps to a row (known to the compiler, so that a lane's places
 // are distances from one address), each with blocks of 128 neighbouring values, four
 // of a block to a lane, 32 apart: neighbouring lanes neighbouring values, and a
-// block's largest magnitude stays inside the warp.
+// block's largest magnitude stays inside the warp.  Bound by the accesses, 4 a value,
+// and the instructions around them: 8192 x 4095 bfloat16 66 us, into 8 bits 71,
+// backward 88 (with the warps' number unknown to the compiler 114, 196 and 188).
+// 16-bit rows on 4-byte boundaries gain nothing by copies of two values (8192 x
+// 4094: 68 and 92 us, here 66 and 86).
 template <int W>
 __host__ __device__ constexpr int place(int k) { return (k >> 2) * W * 128 + (k & 3) * 32; }
 
@@ -569,7 +591,7 @@ __global__ void __launch_bounds__(T, (K > 16 ? 512 : 1024) / T) k_rms_forward_an
                 ss[b] = fmaf(f[b][k], f[b][k], ss[b]);
             if (a.h && b < rows) st_places<DT, K, W>(static_cast<char*>(a.h) + x_at + b * x_row, left, f[b]);
         }
-        group_sum<32, RB, T>(ss, W, sh, turn, [&](float t) { return rsqrtf(fmaf(t, inv, a.eps)); });
+        group_sum<32, RB, T>(ss, W, sh, turn, [&](float t) { return inverse_root(fmaf(t, inv, a.eps)); });
         if (K > 16) weights();
 #pragma unroll
         for (int b = 0; b < RB; b++) {
@@ -669,8 +691,11 @@ __global__ void __launch_bounds__(T, kAnyResident / T) k_rms_backward_any(const 
 }
 
 // ---- long rows -------------------------------------------------------------------------
-// A block per row, values read again for every use (from cache).  Warps take
-// blocks of 128 values in turn, so a thread reads of h what it wrote.
+// More than a block's registers hold (over 4096 vectors, or 16384 values off their
+// boundaries; backward 2048 and 8192): a block per row, values read again for every
+// use (from cache), so the accesses bound it: 512 x 40000 bfloat16 70 us forward, 2.3
+// TB/s, 162 backward.  Warps take blocks of 128 values in turn, so a thread reads of h
+// what it wrote.
 constexpr int kLongThreads = 512;
 
 __device__ __forceinline__ float long_sum(float v, float* sh)
@@ -704,7 +729,7 @@ __global__ void __launch_bounds__(kLongThreads) k_rms_forward_long(const __grid_
                 if (a.h) st1<DT>(a.h, xo + j, f);
                 ss = fmaf(f, f, ss);
             }
-        const float rstd = rsqrtf(fmaf(long_sum(ss, sh), inv, a.eps));
+        const float rstd = inverse_root(fmaf(long_sum(ss, sh), inv, a.eps));
         const void* h = a.h ? a.h : a.x;
         for (int64_t j0 = warp * 128; j0 < a.dim; j0 += kLongThreads * 4) {
             float f[4];
@@ -768,7 +793,8 @@ __global__ void __launch_bounds__(kRowThreads) k_rms_dw_part(const __grid_consta
 }
 
 // The blocks' partial sums: 32 columns a block, its 32 warps a part of the
-// partial sums each, joined in warp order.
+// partial sums each, joined in warp order.  Bound by its own latency, 4.4 us of the
+// 69.9 above.
 template <int DT>
 __global__ void __launch_bounds__(1024) k_rms_dw_sum(const float* part, int blocks, int64_t dim, void* dw)
 {
@@ -792,7 +818,9 @@ __global__ void __launch_bounds__(1024) k_rms_dw_sum(const float* part, int bloc
 // ---- read-out --------------------------------------------------------------------------
 // 8-bit results as bfloat16 values.  Rows that start and end on 16 codes: 16 to a
 // thread at once; blockDim.x threads along a row, blockDim.y rows, and each thread
-// kValuesRows of them, all read before any is written.
+// kValuesRows of them, all read before any is written.  8192 x 4096: 20.8 us, 4.9
+// TB/s, a third of the issue slots used; more warps an SM with fewer loads each on
+// their way were slower (24.9 with 48 of them).  Other rows 41 us.
 constexpr int kValuesRows = 4;
 
 // Other rows: a warp 256 values of one, a code a lane at a time.
