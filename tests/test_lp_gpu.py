@@ -118,7 +118,7 @@ class Job:
 SHAPES = [  # tokens, vocab, hidden, pad, piece, top, scale
     (1, 1, 8, 0, 0, 1, 1.0), (1, 2, 8, 8, 0, 5, 1.0), (1, 257, 64, 0, 0, 8, 0.7), (1, 1000, 768, 0, 256, 32, 1.0), (1, 50257, 256, 0, 0, 8, 1.0),
     (2, 3, 1, 0, 0, 4, 1.0), (2, 5000, 72, 0, 0, 3, 1.3), (3, 1000, 72, 0, 512, 20, 1.0), (3, 9, 33, 8, 0, 0, 2.0),
-    (4, 2, 8, 0, 0, 2, 1.0), (5, 300, 33, 8, 256, 7, 1.25), (64, 256, 64, 0, 0, 1, 1.0), (128, 256, 128, 0, 0, 32, 1.0),
+    (1, 700, 40_000, 0, 0, 9, 1.0), (3, 300, 11_000, 0, 0, 2, 1.0), (4, 2, 8, 0, 0, 2, 1.0), (5, 300, 33, 8, 256, 7, 1.25), (64, 256, 64, 0, 0, 1, 1.0), (128, 256, 128, 0, 0, 32, 1.0),
     (129, 513, 136, 8, 256, 8, 0.5), (127, 255, 200, 0, 0, 0, 1.0), (257, 2049, 264, 0, 768, 20, 1.0), (300, 4099, 100, 0, 1024, 5, 1.0),
     (20, 50257, 64, 0, 0, 32, 1.0), (1025, 1031, 520, 0, 0, 4, 1.0), (600, 3001, 1600, 0, 1280, 0, 1.25), (600, 50257, 64, 0, 0, 8, 1.0),
     (700, 50257, 40, 0, 0, 32, 0.8), (1500, 50257, 72, 8, 0, 20, 1.0), (3000, 23_000, 33, 0, 0, 8, 1.0), (2000, 16500, 72, 0, 0, 20, 1.0), (5000, 2, 64, 0, 0, 2, 1.0),

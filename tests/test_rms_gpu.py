@@ -190,6 +190,30 @@ def test_8bit_blocks_that_are_not_finite_and_the_scale_range(d):
     unit = torch.exp2(sc[[0, 3]].double() - 127).repeat_interleave(128, 1)[:, :d]
     got = q[[0, 3]].view(torch.float8_e4m3fn).double() * unit
     assert bool(((got - y64).abs() <= y64.abs() * 2.0 ** -4 * 1.001 + unit * 2.0 ** -10 * 1.001 + 2.0 ** -149).all())
+    # read out: exact but below bfloat16's smallest numbers, to the nearest of those
+    off = (v[[0, 3]].double() - got).abs()
+    assert bool((off <= 2.0 ** -134).all()) and bool((off[got.abs() >= 2.0 ** -126] == 0).all())
+
+
+def test_every_code_and_scale_read_out():
+    """All 256 codes under scale bytes from 0 to 255, 16 codes at a time and one by one."""
+    scales = torch.tensor(list(range(0, 16)) + list(range(100, 150)) + list(range(230, 256)), dtype=torch.uint8, device="cuda")
+    n = len(scales)
+    for d, stride in ((256, 256), (256, 257), (255, 255)):
+        p = zg.zero_rms_plan(n, d, zg.ZERO_BF16, y_stride=stride, block=128)
+        q = torch.zeros(n, stride, dtype=torch.uint8, device="cuda")
+        q[:, :d] = torch.arange(d, device="cuda").to(torch.uint8)
+        v = torch.full((n, stride), GUARD, dtype=torch.bfloat16, device="cuda")
+        zg.zero_rms_values(p, q, scales[:, None].expand(n, 2).contiguous(), v)
+        want = q[:, :d].contiguous().view(torch.float8_e4m3fn).double() * torch.exp2(scales.double() - 127)[:, None]
+        want[scales == 255] = float("nan")
+        got = v[:, :d].double()
+        assert torch.equal(got.isnan(), want.isnan()) and bool((v[:, d:] == GUARD).all())
+        fine = ~want.isnan()
+        big = fine & (want.abs() > torch.finfo(torch.bfloat16).max)
+        assert bool((got[big] == want[big].sign() * float("inf")).all())
+        fine &= ~big
+        assert bool(((got - want).abs()[fine] <= 2.0 ** -134).all()) and torch.equal(got[fine & (want.abs() >= 2.0 ** -126)], want[fine & (want.abs() >= 2.0 ** -126)])
 
 
 @pytest.mark.parametrize("dtype", list(DT))
@@ -238,10 +262,12 @@ def test_no_rows_and_no_outputs():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-def test_offsets_past_32_bits(dtype):
+@pytest.mark.parametrize("odd", [0, 1])
+@pytest.mark.parametrize("d", [1000, 20_000])
+def test_offsets_past_32_bits(d, odd, dtype):
     """Rows 2^31 values apart: only three exist, the rest of the buffer is never touched."""
     code, dt = DT[dtype]
-    d, stride = 1000, (1 << 31) + (8 if dtype == "bf16" else 4)
+    stride = (1 << 31) + (16 if dtype == "bf16" else 4) + odd
     big = torch.empty(2 * stride + d, dtype=dt, device="cuda")
     v = big.as_strided((3, d), (stride, 1))
     x = torch.randn(3, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3)).to(dt)
@@ -252,13 +278,22 @@ def test_offsets_past_32_bits(dtype):
     zg.zero_rms_forward(p, v, None, None, EPS, None, y, q, sc, rstd)
     _, y64 = _want(x, None, d)
     assert _close_y(y, y64, dt, d)
+    if dtype == "bf16":                               # codes and values as far apart
+        f = zg.zero_rms_plan(3, d, code, stride, stride, 128)
+        fq, fv = (torch.empty(2 * stride + d, dtype=t, device="cuda").as_strided((3, d), (stride, 1)) for t in (torch.uint8, torch.bfloat16))
+        near = torch.empty(3, d, dtype=torch.bfloat16, device="cuda")
+        zg.zero_rms_forward(f, v, None, None, EPS, None, None, fq, sc, rstd)
+        zg.zero_rms_values(f, fq, sc, fv)
+        zg.zero_rms_values(p, q, sc, near)
+        assert torch.equal(fq, q) and torch.equal(fv, near)
+        del fq, fv
     dw = torch.empty(d, dtype=dt, device="cuda")
     ws = torch.empty(p.workspace_bytes, dtype=torch.uint8, device="cuda")
     far = torch.empty(2 * stride + d, dtype=dt, device="cuda").as_strided((3, d), (stride, 1))
     zg.zero_rms_backward(p, y, None, v, None, rstd, far, dw, ws)
     want = rstd.double()[:, None] * (y.double() - x.double() * rstd.double()[:, None] * (y.double() * x.double() * rstd.double()[:, None]).mean(1, keepdim=True))
     mag = rstd.double()[:, None] * y.double().abs()
-    assert bool(((far.double() - want).abs() <= want.abs() * _half(dt) * 1.001 + U * 120 * mag + U).all())
+    assert bool(((far.double() - want).abs() <= want.abs() * _half(dt) * 1.001 + U * (_chain(d) + 100) * mag + U).all())
 
 
 def test_streams_graphs_and_repeats():

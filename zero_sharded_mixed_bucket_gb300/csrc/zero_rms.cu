@@ -69,10 +69,11 @@ __device__ __forceinline__ uint32_t code1(float a) { return codes2(a, 0.0f) & 0x
 
 // Two codes (bytes 8 and 24 up of w) as bfloat16 values times `scale`.  A code's seven
 // low bits, moved into a bfloat16's exponent and fraction, are 2^-120 times its value,
-// subnormal or not.
+// subnormal or not (all ones: NaN).
 __device__ __forceinline__ uint32_t values2(uint32_t w, __nv_bfloat162 scale)
 {
-    const uint32_t bits = (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u);
+    const uint32_t size = (w >> 4) & 0x07f007f0u;
+    const uint32_t bits = (w & 0x80008000u) | size | (__vcmpeq2(size, 0x07f007f0u) & 0x7fff7fffu);   // the last is NaN
     const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&bits), scale);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
