@@ -151,7 +151,7 @@ def test_clipped_step_is_the_step_of_scaled_gradients(bits, dtype):
 
 def test_graph_replays_and_streams():
     """The norm and the step captured once, replayed over changing gradients; two lists' norms at the same time."""
-    T, P = (Tensors([100_003, 2, 640], "bf16", 32, seed=8) for _ in range(2))
+    T, P = (Tensors([400_003, 2, 640], "bf16", 32, seed=8) for _ in range(2))
     N, M = Norm(T.plan), Norm(P.plan)
     st, other = torch.cuda.Stream(), torch.cuda.Stream()
     graph = torch.cuda.CUDAGraph()
@@ -162,7 +162,7 @@ def test_graph_replays_and_streams():
             zg.zero_adamw_step_clipped(T.plan, T.table, _hp(), N.norm, N.flag, s)
     for turn in range(3):
         for X in (T, P):
-            X.view[0]["grad"].copy_(torch.randn(100_003, device="cuda", generator=torch.Generator(device="cuda").manual_seed(turn)) * 10 ** turn)
+            X.view[0]["grad"].copy_(torch.randn(400_003, device="cuda", generator=torch.Generator(device="cuda").manual_seed(turn)) * 10 ** turn)
         torch.cuda.synchronize()
         graph.replay()
         with torch.cuda.stream(other):

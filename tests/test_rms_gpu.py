@@ -229,6 +229,28 @@ def test_stream_updated_in_place(d, dtype):
         assert b[own].kept()
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("d,pad", [(256, 0), (4096, 0), (257, 1), (4097, 0), (40_000, 0)])
+def test_stream_of_any_bit_patterns(d, pad, dtype):
+    """x + residual is the binary32 sum rounded once, for every exponent, subnormal numbers, infinities and NaN."""
+    code, dt = DT[dtype]
+    g = torch.Generator(device="cuda").manual_seed(d)
+    kind = torch.int32 if dtype == "fp32" else torch.int16
+    lim = torch.iinfo(kind)
+    bits = lambda: torch.randint(lim.min, lim.max + 1, (64, d + pad), device="cuda", generator=g, dtype=torch.int64).to(kind).view(dt)  # noqa: E731
+    x, r = bits(), bits()
+    r[::4] = -x[::4]                                  # sums of 0
+    r[1::4] = (x[1::4].float() * 2.0 ** -9).to(dt)    # sums between two numbers
+    h, y = torch.empty_like(x), torch.empty_like(x)
+    p = zg.zero_rms_plan(64, d, code, d + pad, d + pad)
+    zg.zero_rms_forward(p, x, r, None, EPS, h, y)
+    want = (x.float() + r.float()).to(dt)[:, :d]
+    got = h[:, :d]
+    assert torch.equal(got.isnan(), want.isnan())
+    keep = ~want.isnan()
+    assert torch.equal(got[keep].view(kind), want[keep].view(kind))
+
+
 def test_gradients_against_differences():
     """Central differences of sum(c y) + sum(k h) in binary64 of the formula, through the kernels' gradients in binary32."""
     n, d = 3, 40
