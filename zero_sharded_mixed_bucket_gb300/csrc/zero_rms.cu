@@ -821,7 +821,7 @@ __global__ void __launch_bounds__(1024) k_rms_dw_sum(const float* part, int bloc
 // thread at once; blockDim.x threads along a row, blockDim.y rows, and each thread
 // kValuesRows of them, all read before any is written.  8192 x 4096: 20.8 us, 4.9
 // TB/s, a third of the issue slots used; more warps an SM with fewer loads each on
-// their way were slower (24.9 with 48 of them).  Other rows 41 us.
+// their way were slower (24.9 with 48 of them).  Other rows 46 us.
 constexpr int kValuesRows = 4;
 
 // Other rows: a warp 256 values of one, a code a lane at a time.
