@@ -710,8 +710,9 @@ zero_status_t zero_ce_status(const zero_ce_plan_t* plan, const void* workspace, 
  * Alternatives are logits above -infinity that are numbers; where there are fewer
  * than `top`, log probability -infinity and index -1.  The order is that of the
  * logits as computed: those closer than their binary32 sums' rounding may
- * change places.  A row with a NaN logit or an infinite one has NaN logp and
- * entropy.  With alternatives the workspace holds logits of `rows` tokens at a time
+ * change places.  A row with a logit that is NaN or +infinity, or with none above
+ * -infinity, has NaN logp and entropy; a -infinity beside others adds nothing to
+ * either.  With alternatives the workspace holds logits of `rows` tokens at a time
  * while they are sought (binary32, 2 GiB at most unless 256 rows need more).
  * Results do not depend on timing: equal calls give equal bits.  104 bytes. */
 typedef struct zero_lp_plan {
