@@ -73,7 +73,8 @@ def _close_y(y, y64, dt, dim):
 
 SHAPES = [(1, 1), (3, 2), (5, 7), (2, 8), (9, 16), (33, 31), (700, 64), (701, 65), (130, 96), (67, 128), (66, 129), (40, 255),
           (37, 256), (257, 768), (255, 771), (31, 1000), (64, 2048), (13, 2049), (1, 4096), (9, 4096), (7, 4097), (5, 8192),
-          (5, 8200), (3, 10007), (3, 16384), (2, 16391), (2, 32768), (2, 40001), (1, 100_000)]
+          (5, 8200), (3, 10007), (3, 16384), (2, 16391), (2, 32768), (2, 40001), (1, 100_000),
+          (160, 9001), (310, 16391), (306, 32800)]
 
 
 @pytest.mark.parametrize("dtype", list(DT))

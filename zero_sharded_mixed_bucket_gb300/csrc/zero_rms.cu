@@ -3,6 +3,7 @@
 // block), the read-out of 8-bit results, and the backward pass.
 #include <cuda_fp8.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -487,7 +488,7 @@ __global__ void __launch_bounds__(T, BLOCKS) k_rms_backward_rows(const __grid_co
 // of a block to a lane, 32 apart: neighbouring lanes neighbouring values, and a
 // block's largest magnitude stays inside the warp.  Bound by the accesses, 4 a value,
 // and the instructions around them: 8192 x 4095 bfloat16 66 us, into 8 bits 71,
-// backward 88 (with the warps' number unknown to the compiler 114, 196 and 188).
+// backward 88, 2048 x 16383 98 (with the warps' number unknown to the compiler 114, 196 and 188).
 // 16-bit rows on 4-byte boundaries gain nothing by copies of two values (8192 x
 // 4094: 68 and 92 us, here 66 and 86).
 template <int W>
@@ -627,24 +628,28 @@ __global__ void __launch_bounds__(T, kAnyResident / T) k_rms_backward_any(const 
     const int j0 = warp * 128 + lane, left = (int)a.dim - j0;
     const float inv = 1.0f / (float)a.dim;
     int turn = 0;
-    float dw[K], w[K];
+    constexpr bool kHeld = K <= 8;                    // else the weight is read for each row, and dh where it is added
+    float dw[K], w[kHeld ? K : 1];
 #pragma unroll
     for (int k = 0; k < K; k++) {
         dw[k] = 0.0f;
-        w[k] = 1.0f;
+        if (kHeld) w[k] = 1.0f;
     }
-    if (a.weight) ld_places<DT, K, W>(static_cast<const char*>(a.weight) + j0 * E, left, w);
+    const char* weight = static_cast<const char*>(a.weight) + j0 * E;
+    if constexpr (kHeld)
+        if (a.weight) ld_places<DT, K, W>(weight, left, w);
     const int64_t x_row = a.x_stride * E, y_row = a.y_stride * E, stride = (int64_t)gridDim.x * kGroups * RB;
     for (int64_t r0 = ((int64_t)blockIdx.x * kGroups + group) * RB; r0 < a.rows; r0 += stride) {
         const int64_t x_at = r0 * x_row + j0 * E, y_at = r0 * y_row + j0 * E;
-        float n[RB][K], g[RB][K], r[RB][K], rstd[RB], c[RB];
+        float n[RB][K], g[RB][K], r[kHeld ? RB : 1][kHeld ? K : 1], rstd[RB], c[RB];
 #pragma unroll
         for (int b = 0; b < RB; b++) {                // rows past the end: none of their places is there
             const bool there = RB == 1 || r0 + b < a.rows;
             const int here = there ? left : 0;
             ld_places<DT, K, W>(static_cast<const char*>(a.x) + x_at + b * x_row, here, n[b]);
             ld_places<DT, K, W>(static_cast<const char*>(a.dy) + y_at + b * y_row, here, g[b]);
-            if (a.r) ld_places<DT, K, W>(static_cast<const char*>(a.r) + x_at + b * x_row, here, r[b]);
+            if constexpr (kHeld)
+                if (a.r) ld_places<DT, K, W>(static_cast<const char*>(a.r) + x_at + b * x_row, here, r[b]);
             rstd[b] = there ? a.rstd_in[r0 + b] : 0.0f;
         }
 #pragma unroll
@@ -654,7 +659,8 @@ __global__ void __launch_bounds__(T, kAnyResident / T) k_rms_backward_any(const 
             for (int k = 0; k < K; k++) {
                 n[b][k] *= rstd[b];                   // xhat; 0 past the end
                 dw[k] = fmaf(g[b][k], n[b][k], dw[k]);
-                g[b][k] *= w[k];
+                if constexpr (kHeld) g[b][k] *= w[k];
+                else if (a.weight && place<W>(k) < left) g[b][k] *= ld1<DT>(weight, place<W>(k));
                 c[b] = fmaf(g[b][k], n[b][k], c[b]);
             }
         }
@@ -665,7 +671,12 @@ __global__ void __launch_bounds__(T, kAnyResident / T) k_rms_backward_any(const 
 #pragma unroll
             for (int k = 0; k < K; k++) {
                 g[b][k] = fmaf(n[b][k], c[b], g[b][k]);
-                g[b][k] = a.r ? fmaf(g[b][k], rstd[b], r[b][k]) : g[b][k] * rstd[b];
+                if constexpr (kHeld) {
+                    g[b][k] = a.r ? fmaf(g[b][k], rstd[b], r[b][k]) : g[b][k] * rstd[b];
+                } else {
+                    const float d = a.r && place<W>(k) < left ? ld1<DT>(static_cast<const char*>(a.r) + x_at, place<W>(k)) : 0.0f;
+                    g[b][k] = a.r ? fmaf(g[b][k], rstd[b], d) : g[b][k] * rstd[b];
+                }
             }
             st_places<DT, K, W>(static_cast<char*>(a.dx) + x_at + b * x_row, RB == 1 || r0 + b < a.rows ? left : 0, g[b]);
         }
@@ -693,11 +704,15 @@ __global__ void __launch_bounds__(T, kAnyResident / T) k_rms_backward_any(const 
 
 // ---- long rows -------------------------------------------------------------------------
 // More than a block's registers hold (over 4096 vectors, or 16384 values off their
-// boundaries; backward 2048 and 8192): a block per row, values read again for every
-// use (from cache), so the accesses bound it: 512 x 40000 bfloat16 70 us forward, 2.3
-// TB/s, 162 backward.  Warps take blocks of 128 values in turn, so a thread reads of h
-// what it wrote.
+// boundaries; backward 2048 and 16384): a block per row, values read again for every
+// use (from cache), bound by the latency of one access a value: 512 x 40000 bfloat16
+// 55 us forward, backward 120, 43 of them for the weight (with one value of a thread
+// on its way at a time 70 and 162).  Warps take blocks of 128 values in turn, K / 4
+// of them before any use, so a thread reads of h what it wrote.  K = 8 for few rows
+// (200 x 200000 132 us forward, 205 with 4), 4 for many (8192 x 16385 261 and
+// backward 562, 297 and 687 with 8).
 constexpr int kLongThreads = 512;
+constexpr int64_t kLongRows = 2 * kSms;               // up to so many rows: half as many blocks an SM, twice the loads of a thread on their way
 
 __device__ __forceinline__ float long_sum(float v, float* sh)
 {
@@ -711,69 +726,105 @@ __device__ __forceinline__ float long_sum(float v, float* sh)
     return t;
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kLongThreads) k_rms_forward_long(const __grid_constant__ RmsArgs a)
+template <int DT, int K>
+__global__ void __launch_bounds__(kLongThreads, 16 / K) k_rms_forward_long(const __grid_constant__ RmsArgs a)
 {
-    __shared__ float sh[kLongThreads / 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int E = DT == kF32 ? 4 : 2, W = kLongThreads / 32;
+    __shared__ float sh[W];
+    const int lane = threadIdx.x & 31, j0 = (int)(threadIdx.x >> 5) * 128 + lane;
     const float inv = 1.0f / (float)a.dim;
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const int64_t xo = r * a.x_stride, yo = r * a.y_stride;
+        const char* x = static_cast<const char*>(a.x) + xo * E;
+        const char* res = static_cast<const char*>(a.r) + xo * E;
+        char* h = static_cast<char*>(a.h) + xo * E;
         float ss = 0.0f;
-        for (int64_t j0 = warp * 128; j0 < a.dim; j0 += kLongThreads * 4)
+        for (int j = j0; j < a.dim; j += K * kLongThreads) {
+            const int left = (int)a.dim - j;
+            float f[K], g[K];
+            ld_places<DT, K, W>(x + j * E, left, f);
+            if (a.r) {
+                ld_places<DT, K, W>(res + j * E, left, g);
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
-                const int64_t j = j0 + 32 * k + lane;
-                if (j >= a.dim) continue;
-                float f = ld1<DT>(a.x, xo + j);
-                if (a.r) f = to_f32<DT>(from_f32<DT>(f + ld1<DT>(a.r, xo + j)));
-                if (a.h) st1<DT>(a.h, xo + j, f);
-                ss = fmaf(f, f, ss);
+                for (int k = 0; k < K; k++)
+                    f[k] = to_f32<DT>(from_f32<DT>(f[k] + g[k]));
             }
+            if (a.h) st_places<DT, K, W>(h + j * E, left, f);
+#pragma unroll
+            for (int k = 0; k < K; k++)
+                ss = fmaf(f[k], f[k], ss);
+        }
         const float rstd = inverse_root(fmaf(long_sum(ss, sh), inv, a.eps));
-        const void* h = a.h ? a.h : a.x;
-        for (int64_t j0 = warp * 128; j0 < a.dim; j0 += kLongThreads * 4) {
-            float f[4];
+        if (a.h) x = h;
+        for (int j = j0; j - lane < a.dim; j += K * kLongThreads) {            // whole warps: codes_out's maxima
+            const int left = (int)a.dim - j;
+            float f[K], w[K];
+            ld_places<DT, K, W>(x + j * E, left, f);
+            if (a.weight) ld_places<DT, K, W>(static_cast<const char*>(a.weight) + j * E, left, w);
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
-                const int64_t j = j0 + 32 * k + lane;
-                if (j >= a.dim) {
-                    f[k] = 0.0f;
-                    continue;
-                }
-                f[k] = ld1<DT>(h, xo + j) * rstd * (a.weight ? ld1<DT>(a.weight, j) : 1.0f);
-                if (a.y) st1<DT>(a.y, yo + j, f[k]);
-            }
-            if (a.q) {
-                const int left = (int)(a.dim - j0) - lane;
-                uint8_t* q = a.q + yo + j0 + lane;
-                if (a.block == 128) codes_out<128>(q, a.q_scale + r * a.scale_cols + j0 / 128, left, lane, f);
-                else codes_out<32>(q, a.q_scale + r * a.scale_cols + j0 / 32, left, lane, f);
+            for (int k = 0; k < K; k++)
+                f[k] = f[k] * rstd * (a.weight ? w[k] : 1.0f);
+            if (a.y) st_places<DT, K, W>(static_cast<char*>(a.y) + (yo + j) * E, left, f);
+            if (!a.q) continue;
+            uint8_t* q = a.q + yo + j;
+            uint8_t* q_scale = a.q_scale + r * a.scale_cols;
+#pragma unroll
+            for (int k = 0; k < K; k += 4) {
+                const int at = j - lane + place<W>(k);
+                if (at >= a.dim) break;
+                if (a.block == 128) codes_out<128>(q + place<W>(k), q_scale + at / 128, left - place<W>(k), lane, f + k);
+                else codes_out<32>(q + place<W>(k), q_scale + at / 32, left - place<W>(k), lane, f + k);
             }
         }
         if (threadIdx.x == 0 && a.rstd) a.rstd[r] = rstd;
     }
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kLongThreads) k_rms_dx_long(const __grid_constant__ RmsArgs a)
+template <int DT, int K>
+__global__ void __launch_bounds__(kLongThreads, 16 / K) k_rms_dx_long(const __grid_constant__ RmsArgs a)
 {
-    __shared__ float sh[kLongThreads / 32];
+    constexpr int E = DT == kF32 ? 4 : 2, W = kLongThreads / 32;
+    __shared__ float sh[W];
+    const int j0 = (int)(threadIdx.x >> 5) * 128 + (threadIdx.x & 31);
     const float inv = 1.0f / (float)a.dim;
+    const char* weight = static_cast<const char*>(a.weight);
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const int64_t xo = r * a.x_stride, yo = r * a.y_stride;
+        const int64_t xo = r * a.x_stride;
+        const char* x = static_cast<const char*>(a.x) + xo * E;
+        const char* res = static_cast<const char*>(a.r) + xo * E;
+        const char* dy = static_cast<const char*>(a.dy) + r * a.y_stride * E;
         const float rstd = a.rstd_in[r];
+        float n[K], g[K], w[K];
+        auto load = [&](int j) {                      // xhat and dy weight
+            const int left = (int)a.dim - j;
+            ld_places<DT, K, W>(x + j * E, left, n);
+            ld_places<DT, K, W>(dy + j * E, left, g);
+            if (weight) ld_places<DT, K, W>(weight + j * E, left, w);
+#pragma unroll
+            for (int k = 0; k < K; k++) {
+                n[k] *= rstd;
+                if (weight) g[k] *= w[k];
+            }
+        };
         float s = 0.0f;
-        for (int64_t j = threadIdx.x; j < a.dim; j += kLongThreads) {
-            const float g = ld1<DT>(a.dy, yo + j) * (a.weight ? ld1<DT>(a.weight, j) : 1.0f);
-            s = fmaf(g, ld1<DT>(a.x, xo + j) * rstd, s);
+        for (int j = j0; j < a.dim; j += K * kLongThreads) {
+            load(j);
+#pragma unroll
+            for (int k = 0; k < K; k++)
+                s = fmaf(g[k], n[k], s);
         }
         const float c = long_sum(s, sh) * -inv;
-        for (int64_t j = threadIdx.x; j < a.dim; j += kLongThreads) {
-            const float g = ld1<DT>(a.dy, yo + j) * (a.weight ? ld1<DT>(a.weight, j) : 1.0f);
-            float d = fmaf(ld1<DT>(a.x, xo + j) * rstd, c, g) * rstd;
-            if (a.r) d += ld1<DT>(a.r, xo + j);
-            st1<DT>(a.dx, xo + j, d);
+        for (int j = j0; j < a.dim; j += K * kLongThreads) {
+            const int left = (int)a.dim - j;
+            float d[K];
+            if (a.r) ld_places<DT, K, W>(res + j * E, left, d);
+            load(j);
+#pragma unroll
+            for (int k = 0; k < K; k++) {
+                g[k] = fmaf(n[k], c, g[k]) * rstd;
+                if (a.r) g[k] += d[k];
+            }
+            st_places<DT, K, W>(static_cast<char*>(a.dx) + (xo + j) * E, left, g);
         }
     }
 }
@@ -786,10 +837,20 @@ __global__ void __launch_bounds__(kRowThreads) k_rms_dw_part(const __grid_consta
     if (j >= a.dim) return;
     const int64_t G = gridDim.y, per = (a.rows + G - 1) / G;
     const int64_t lo = min(blockIdx.y * per, a.rows), hi = min(lo + per, a.rows);
+    constexpr int U = 8;
     float dw = 0.0f;
-#pragma unroll 4
-    for (int64_t r = lo; r < hi; r++)
-        dw = fmaf(ld1<DT>(a.dy, r * a.y_stride + j), ld1<DT>(a.x, r * a.x_stride + j) * a.rstd_in[r], dw);
+    for (int64_t r0 = lo; r0 < hi; r0 += U) {
+        float g[U], n[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {                 // past the end: 0
+            const int64_t r = r0 + u;
+            g[u] = r < hi ? ld1<DT>(a.dy, r * a.y_stride + j) : 0.0f;
+            n[u] = r < hi ? ld1<DT>(a.x, r * a.x_stride + j) * a.rstd_in[r] : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++)
+            dw = fmaf(g[u], n[u], dw);
+    }
     a.part[(int64_t)blockIdx.y * a.dim + j] = dw;
 }
 
@@ -1009,7 +1070,8 @@ cudaError_t forward(const RmsArgs& a, bool aligned, cudaStream_t s)
         if (a.dim <= 8192) return forward_any<DT, 16, 16, 1, 2 * T>(a, s);
         if (a.dim <= 16384) return forward_any<DT, 32, 16, 1, 2 * T>(a, s);
     }
-    return launch_rms(k_rms_forward_long<DT>, a, a.rows < kSms * 4 ? a.rows : kSms * 4, kLongThreads, 0, s);
+    if (a.rows <= kLongRows) return launch_rms(k_rms_forward_long<DT, 8>, a, a.rows, kLongThreads, 0, s);
+    return launch_rms(k_rms_forward_long<DT, 4>, a, std::min<int64_t>(a.rows, kSms * 4), kLongThreads, 0, s);
 }
 
 // How the backward pass deals out a row: lanes of a group, vectors of a lane,
@@ -1053,10 +1115,12 @@ int64_t backward_blocks(int64_t rows, int64_t vecs, int L)
     return blocks_for(rows, (int64_t)h.groups * rows_of_batch(rows, h.groups, most, b.rows), most);
 }
 
-// Warps to a row in the kernel for other rows, of 8 values a lane up to 8192; threads of
+// Warps to a row in the kernel for other rows, of 8 values a lane, 16 above 8192; threads of
 // its blocks, and the blocks: as many as are resident, and no more than have rows.
 // (Two rows of a group at a time, with half of the warps: 8192 x 4095 123 us for 86;
-// short rows are two at a time, 65536 x 67 24 us for 32.)
+// short rows are two at a time, 65536 x 67 24 us for 32.  2048 x 16383 98 us, as a
+// long row's kernels 191.)
+constexpr int64_t kAnyBackward = 16384;
 constexpr int64_t any_warps(int64_t dim) { return dim <= 256 ? 1 : dim <= 512 ? 2 : dim <= 1024 ? 4 : dim <= 2048 ? 8 : dim <= 4096 ? 16 : 32; }
 constexpr int64_t any_threads(int64_t W) { return W <= 8 ? 256 : 32 * W; }
 
@@ -1072,6 +1136,14 @@ cudaError_t backward_any(const RmsArgs& a, int64_t& blocks, cudaStream_t s)
     constexpr int T = (int)any_threads(W);
     blocks = any_blocks(a.rows, a.dim);
     return launch_rms(k_rms_backward_any<DT, K, W, RB, T>, a, blocks, T, 0, s);
+}
+
+// Row groups of a long row's column sums: what fills the SMs once, or groups of 256
+// rows (as many as the plan allows, of three rows each: 512 x 40000 74 us for 43).
+int64_t dw_groups(int64_t rows, int64_t cols)
+{
+    const int64_t fill = kSms * (2048 / kRowThreads) / cols, most = (rows + 255) / 256;
+    return std::min(rows, std::max<int64_t>(1, std::max(fill, most)));
 }
 
 template <int DT>
@@ -1091,19 +1163,23 @@ cudaError_t backward(RmsArgs a, bool aligned, int64_t most, void* dw, cudaStream
         else if (vecs <= 512) e = backward_rows<DT, 32, 1, 4, 2 * T, 1>(a, vecs, blocks, s);
         else if (vecs <= 1024) e = backward_rows<DT, 32, 2, 2, 2 * T, 1>(a, vecs, blocks, s);
         else e = backward_rows<DT, 32, 4, 1, 2 * T, 1>(a, vecs, blocks, s);
-    } else if (a.rows && !aligned && a.dim <= 8192) {
+    } else if (a.rows && !aligned && a.dim <= kAnyBackward) {
         if (a.dim <= 128) e = backward_any<DT, 4, 1, 2>(a, blocks, s);
         else if (a.dim <= 256) e = backward_any<DT, 8, 1>(a, blocks, s);
         else if (a.dim <= 512) e = backward_any<DT, 8, 2>(a, blocks, s);
         else if (a.dim <= 1024) e = backward_any<DT, 8, 4>(a, blocks, s);
         else if (a.dim <= 2048) e = backward_any<DT, 8, 8>(a, blocks, s);
         else if (a.dim <= 4096) e = backward_any<DT, 8, 16>(a, blocks, s);
-        else e = backward_any<DT, 8, 32>(a, blocks, s);
+        else if (a.dim <= 8192) e = backward_any<DT, 8, 32>(a, blocks, s);
+        else e = backward_any<DT, 16, 32>(a, blocks, s);
     } else {
-        if (a.dx && a.rows) e = launch_rms(k_rms_dx_long<DT>, a, a.rows < kSms * 4 ? a.rows : kSms * 4, kLongThreads, 0, s);
+        if (a.dx && a.rows)
+            e = a.rows <= kLongRows ? launch_rms(k_rms_dx_long<DT, 8>, a, a.rows, kLongThreads, 0, s)
+                                    : launch_rms(k_rms_dx_long<DT, 4>, a, std::min<int64_t>(a.rows, kSms * 4), kLongThreads, 0, s);
         if (e == cudaSuccess && dw && blocks) {
-            const unsigned cols = (unsigned)((a.dim + kRowThreads - 1) / kRowThreads);
-            k_rms_dw_part<DT><<<dim3(cols, (unsigned)blocks), kRowThreads, 0, s>>>(a);
+            const int64_t cols = (a.dim + kRowThreads - 1) / kRowThreads;
+            blocks = std::min(most, dw_groups(a.rows, cols));
+            k_rms_dw_part<DT><<<dim3((unsigned)cols, (unsigned)blocks), kRowThreads, 0, s>>>(a);
             e = cudaGetLastError();
         }
     }
@@ -1167,7 +1243,7 @@ zero_status_t zero_rms_plan(int64_t rows, int64_t dim, int32_t dtype, int64_t x_
     // each adds up its rows' weight gradients; the most of any alignment of the pointers
     const int64_t vecs = (dim * e + 15) / 16;
     const int64_t by_vec = backward_blocks(rows, vecs, 32), by_some = backward_blocks(rows, vecs, backward_shape(vecs, dim * e % 16 == 0).L);
-    const int64_t by_one = dim <= 8192 ? any_blocks(rows, dim) : 0, more = by_vec > by_some ? by_vec : by_some;
+    const int64_t by_one = dim <= kAnyBackward ? any_blocks(rows, dim) : 0, more = by_vec > by_some ? by_vec : by_some;
     out->blocks = (int32_t)(more > by_one ? more : by_one);
     out->workspace_bytes = 16 + (int64_t)out->blocks * dim * 4;
     out->hbm_bytes_forward = rows * (3 * dim * e + 4 + (block ? dim + out->scale_cols : dim * e)) + dim * e;
