@@ -127,6 +127,71 @@ def test_captured_whole():
         assert torch.equal(p.top_index, q.top_index) and torch.equal(p.norm, q.norm)
 
 
+def test_captured_behind_copies_and_another_stream():
+    """Inputs that a copy and another stream's kernel write just before, in a graph and in a row of calls: each call sees
+    its own, and what is read out just after is its result."""
+    n, d, v = 300, 512, 1000
+    g = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=g)  # noqa: E731
+    rounds = [(r(n, d).bfloat16(), r(n, d).bfloat16(), r(n)) for _ in range(3)]
+    x, res, dl = (torch.zeros_like(t) for t in rounds[0])
+    w, weight = r(v, d).bfloat16() / 16, (1 + r(d) / 8).bfloat16()
+    t = torch.randint(0, v, (n,), device="cuda", generator=g)
+    e = lambda *s: torch.empty(*s, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    h, y, vals, dx, dw, dxn, dwn = e(n, d), e(n, d), e(n, d), e(n, d), e(v, d), e(n, d), e(d)
+    q, qs, rstd = torch.empty(n, d, dtype=torch.uint8, device="cuda"), torch.empty(n, d // 32, dtype=torch.uint8, device="cuda"), torch.empty(n, device="cuda")
+    logp, lse, ent, tl, ti = torch.empty(n, device="cuda"), torch.empty(n, device="cuda"), torch.empty(n, device="cuda"), torch.empty(n, 4, device="cuda"), torch.empty(n, 4, dtype=torch.int64, device="cuda")
+    rp, lp = zg.zero_rms_plan(n, d, zg.ZERO_BF16, block=32), zg.zero_lp_plan(n, v, d, zg.ZERO_BF16, top=4)
+    rw, lw = (torch.empty(p.workspace_bytes, dtype=torch.uint8, device="cuda") for p in (rp, lp))
+    out = [torch.empty_like(o) for o in (vals, logp, ent, tl, ti, dxn, dwn, dw)]
+    side = torch.cuda.Stream()
+
+    def step(k):
+        s = torch.cuda.current_stream()
+        side.wait_stream(s)
+        with torch.cuda.stream(side):
+            torch.mul(rounds[k][0], 1, out=x)
+        res.copy_(rounds[k][1])
+        dl.copy_(rounds[k][2])
+        s.wait_stream(side)
+        zg.zero_rms_forward(rp, x, res, weight, 1e-5, h, y, q, qs, rstd, s)
+        zg.zero_rms_values(rp, q, qs, vals, s)
+        zg.zero_lp_forward(lp, y, w, t, 1.0, logp, lse, ent, tl, ti, lw, s)
+        zg.zero_lp_backward(lp, y, w, t, 1.0, lse, ent, dl, dl, 1.0, dx, dw, lw, s)
+        zg.zero_rms_backward(rp, dx, None, h, weight, rstd, dxn, dwn, rw, s)
+        for o, f in zip(out, (vals, logp, ent, tl, ti, dxn, dwn, dw)):
+            o.copy_(f)
+        for f in (x, res, dl, vals, logp, ent, tl, ti, dxn, dwn, dw):
+            f.zero_()
+
+    want = []
+    for k in range(3):
+        step(k)
+        torch.cuda.synchronize()
+        want.append([o.clone() for o in out])
+    hs = (rounds[0][0].float() + rounds[0][1].float()).bfloat16().double()
+    y64 = hs * torch.rsqrt((hs * hs).mean(1, keepdim=True) + 1e-5) * weight.double()
+    z = y64.bfloat16().double() @ w.double().t()
+    assert (want[0][1].double() - torch.log_softmax(z, 1).gather(1, t[:, None])[:, 0]).abs().max() < 0.05     # a y next to a border rounds either way
+    for turn in range(20):                            # one behind the other, no wait between
+        step(turn % 3)
+        got = [o.clone() for o in out]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want[19 % 3]))
+    graph, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        with torch.cuda.graph(graph, stream=st):
+            step(2)
+            step(1)
+    for o in out:
+        o.zero_()
+    torch.cuda.synchronize()
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want[1]))
+
+
 @pytest.mark.parametrize("block", [32, 128])
 def test_projection_of_8bit_results(block):
     """The norm into 8 bits, read out as values, scored: what a product with 8-bit operands would see.  Each value is off by 2^-4 of itself

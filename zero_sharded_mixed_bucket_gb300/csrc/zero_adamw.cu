@@ -212,6 +212,7 @@ template <int DT>
 __global__ void __launch_bounds__(kAd32Threads) k_adamw32(const AdTable tab, const __grid_constant__ AdHP hp,
                                                         const uint32_t* skip, const float* norm)
 {
+    wait_prev_grid();
     if (skip && *skip) return;
     const float gs = norm ? __fmul_rn(norm[1], hp.gs) : hp.gs;
     constexpr int V = 4;
@@ -258,6 +259,7 @@ template <int DT>
 __global__ void __launch_bounds__(kAd8Threads, 32) k_adamw8(const AdTable tab, const __grid_constant__ AdHP hp,
                                                            const uint32_t* skip, const float* norm)
 {
+    wait_prev_grid();
     if (skip && *skip) return;
     const float gs = norm ? __fmul_rn(norm[1], hp.gs) : hp.gs;
     constexpr int V = 8;
@@ -493,6 +495,7 @@ __global__ void __launch_bounds__(T, T < 1024 ? 2048 / T : 1) k_adamw_norm(const
                                                             const __grid_constant__ NormOut out)
 {
     constexpr int V = kVecOf<DT>, U = kNormUnroll, kBatch = G * V;
+    wait_prev_grid();
     allow_next_grid();
     double sum = 0.0;
     uint64_t bad = 0;
@@ -590,6 +593,7 @@ __global__ void __launch_bounds__(kNormThreads) k_adamw_norm_join(int parts, con
 template <int DT>
 __global__ void __launch_bounds__(kAd32Threads) k_adamw_clip(const AdTable tab, const float* norm)
 {
+    wait_prev_grid();
     const float factor = norm[1];
     if (factor == 1.0f) return;
     constexpr int V = kVecOf<DT>;
@@ -682,10 +686,10 @@ zero_status_t check_adamw_plan(const zero_adamw_plan_t* p, const void* table)
 }
 
 template <int DT>
-void launch_norm(const AdTable& tab, int64_t n_chunks, const NormOut& o, unsigned grid, cudaStream_t s)
+cudaError_t launch_norm(const AdTable& tab, int64_t n_chunks, const NormOut& o, unsigned grid, cudaStream_t s)
 {
-    if (grid == 1) k_adamw_norm<DT, 32, 32 * kNormAlone><<<1, 32 * kNormAlone, 0, s>>>(tab, n_chunks, o);
-    else k_adamw_norm<DT, kNormThreads, kNormThreads><<<grid, kNormThreads, 0, s>>>(tab, n_chunks, o);
+    return grid == 1 ? launch_after(k_adamw_norm<DT, 32, 32 * kNormAlone>, dim3(1), 32 * kNormAlone, 0, s, tab, n_chunks, o)
+                     : launch_after(k_adamw_norm<DT, kNormThreads, kNormThreads>, dim3(grid), kNormThreads, 0, s, tab, n_chunks, o);
 }
 
 // Blocks of the norm's kernel, a function of the list alone.
@@ -728,10 +732,10 @@ zero_status_t adamw_step(const zero_adamw_plan_t* plan, const void* table, const
     const AdTable tab = table_of(table, plan->n_tensors);
     const unsigned grid = (unsigned)plan->n_chunks;
     const int dt = plan->dtype;
+    cudaError_t err;
     if (plan->state_bits == 32) {
-        if (dt == ZERO_FP32) k_adamw32<kF32><<<grid, kAd32Threads, 0, s>>>(tab, h, skip, norm);
-        else if (dt == ZERO_BF16) k_adamw32<kBF16><<<grid, kAd32Threads, 0, s>>>(tab, h, skip, norm);
-        else k_adamw32<kF16><<<grid, kAd32Threads, 0, s>>>(tab, h, skip, norm);
+        const auto kernel = dt == ZERO_FP32 ? k_adamw32<kF32> : dt == ZERO_BF16 ? k_adamw32<kBF16> : k_adamw32<kF16>;
+        err = launch_after(kernel, dim3(grid), kAd32Threads, 0, s, tab, h, skip, norm);
     } else {
         // a chunk's 16 blocks go to one warp, or in a short list to as many as fill
         // the 152 x 32 warps resident at once (148 tensors of up to 8894 values, step
@@ -739,11 +743,9 @@ zero_status_t adamw_step(const zero_adamw_plan_t* plan, const void* table, const
         unsigned share = 1;
         while (share < kChunk / kQBlock && grid * share < 152u * 32u) share *= 2;
         const dim3 grid8(grid, share);
-        if (dt == ZERO_FP32) k_adamw8<kF32><<<grid8, kAd8Threads, 0, s>>>(tab, h, skip, norm);
-        else if (dt == ZERO_BF16) k_adamw8<kBF16><<<grid8, kAd8Threads, 0, s>>>(tab, h, skip, norm);
-        else k_adamw8<kF16><<<grid8, kAd8Threads, 0, s>>>(tab, h, skip, norm);
+        const auto kernel = dt == ZERO_FP32 ? k_adamw8<kF32> : dt == ZERO_BF16 ? k_adamw8<kBF16> : k_adamw8<kF16>;
+        err = launch_after(kernel, grid8, kAd8Threads, 0, s, tab, h, skip, norm);
     }
-    const cudaError_t err = cudaGetLastError();
     return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_adamw_step");
 }
 
@@ -891,11 +893,10 @@ zero_status_t zero_adamw_norm(const zero_adamw_plan_t* plan, const void* table, 
     const NormOut o{static_cast<NormPart*>(workspace), norm, flag, std::fabs((double)grad_scale),
                     max_norm > 0.0f ? (double)max_norm : 0.0};
     const unsigned grid = (unsigned)norm_blocks(*plan);
-    if (plan->dtype == ZERO_FP32) launch_norm<kF32>(tab, plan->n_chunks, o, grid, s);
-    else if (plan->dtype == ZERO_BF16) launch_norm<kBF16>(tab, plan->n_chunks, o, grid, s);
-    else launch_norm<kF16>(tab, plan->n_chunks, o, grid, s);
-    cudaError_t err = cudaGetLastError();
-    if (err == cudaSuccess && grid > 1) err = launch_kernel(k_adamw_norm_join, 1, kNormThreads, s, true, (int)grid, o);
+    cudaError_t err = plan->dtype == ZERO_FP32   ? launch_norm<kF32>(tab, plan->n_chunks, o, grid, s)
+                      : plan->dtype == ZERO_BF16 ? launch_norm<kBF16>(tab, plan->n_chunks, o, grid, s)
+                                                 : launch_norm<kF16>(tab, plan->n_chunks, o, grid, s);
+    if (err == cudaSuccess && grid > 1) err = launch_after(k_adamw_norm_join, dim3(1), kNormThreads, 0, s, (int)grid, o);
     return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_adamw_norm");
 }
 
@@ -909,11 +910,11 @@ zero_status_t zero_adamw_clip(const zero_adamw_plan_t* plan, const void* table, 
     if (plan->n_chunks == 0) return ZERO_OK;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const AdTable tab = table_of(table, plan->n_tensors);
-    const unsigned grid = (unsigned)plan->n_chunks;
-    if (plan->dtype == ZERO_FP32) k_adamw_clip<kF32><<<grid, kAd32Threads, 0, s>>>(tab, norm);
-    else if (plan->dtype == ZERO_BF16) k_adamw_clip<kBF16><<<grid, kAd32Threads, 0, s>>>(tab, norm);
-    else k_adamw_clip<kF16><<<grid, kAd32Threads, 0, s>>>(tab, norm);
-    const cudaError_t err = cudaGetLastError();
+    const dim3 grid((unsigned)plan->n_chunks);
+    const auto kernel = plan->dtype == ZERO_FP32   ? k_adamw_clip<kF32>
+                        : plan->dtype == ZERO_BF16 ? k_adamw_clip<kBF16>
+                                                   : k_adamw_clip<kF16>;
+    const cudaError_t err = launch_after(kernel, grid, kAd32Threads, 0, s, tab, norm);
     return err == cudaSuccess ? ZERO_OK : cuda_failed(err, "zero_adamw_clip");
 }
 

@@ -579,6 +579,7 @@ __global__ void __launch_bounds__(1024) k_lp_factors(CeHead* head, const int64_t
                                                      float* coef, float* coef_h)
 {
     allow_next_grid();
+    wait_prev_grid();
     __shared__ float sm[32];
     auto factor = [&](int64_t i, float& b) {
         const int64_t t = targets[i];
@@ -821,8 +822,7 @@ zero_status_t zero_lp_forward(const zero_lp_plan_t* plan, const void* x, const v
         return set_error(ZERO_EALIGN, "zero_lp_forward: x, w and workspace must be 16-byte aligned, the others to their type");
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
-    k_lp_clear<<<1, 1, 0, s>>>(reinterpret_cast<CeHead*>(ws));
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_after(k_lp_clear, dim3(1), 1, 0, s, reinterpret_cast<CeHead*>(ws));
     const bool few = few_tokens(c);
     const LpLayout l = lp_layout(p, few);
     for (int64_t r0 = 0; r0 < p.tokens && e == cudaSuccess; r0 += p.rows) {
@@ -894,8 +894,8 @@ zero_status_t zero_lp_backward(const zero_lp_plan_t* plan, const void* x, const 
     float* coef = reinterpret_cast<float*>(ws + l.coef);
     float* coef_h = reinterpret_cast<float*>(ws + l.target_logit);   // free in a backward pass
     const float up = p.dtype == ZERO_FP16 ? 16384.0f : 1.0f;
-    k_lp_factors<<<1, 1024, 0, s>>>(head, targets, p.tokens, p.vocab, dlogp, dentropy, grad_scale * scale, up, coef, coef_h);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_after(k_lp_factors, dim3(1), 1024, 0, s, head, targets, p.tokens, p.vocab, dlogp, dentropy,
+                                 grad_scale * scale, up, coef, coef_h);
     GemmArgs base;
     std::memset(&base, 0, sizeof base);
     base.head = head;
