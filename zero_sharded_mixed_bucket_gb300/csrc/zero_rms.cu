@@ -162,7 +162,7 @@ __device__ __forceinline__ Vals<DT> weight_held(const void* p, int64_t i, int cn
 // backward sees), then kept in registers; its slot is free for the next copy
 // before the group has its sum.  Q: values to a scale of 8-bit results, 0: none; a
 // block of them is Q / VE neighbouring lanes of a warp, or a whole shorter row.
-// Bound by memory: 8192 x 4096 bfloat16 with a residual 47.5 us, 5.6 TB/s (a device
+// Bound by memory: 8192 x 4096 bfloat16 with a residual 45.7 us, 5.9 TB/s (a device
 // copy of the same bytes takes 43.3), issuing in 42 % of the cycles, 16
 // instructions a value; into 8 bits 41.5, 22 instructions a value in 55 %.  The
 // lane's weights stay in registers (read for every batch they are what a warp
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(T, BLOCKS) k_rms_forward_rows(const __grid_con
 // Backward: the stream's gradient of the rows, and the column sums of dy * xhat
 // over all the rows of a lane in registers, so h and dy are read once for both.
 // A block writes one partial sum per column (its groups joined in group order).
-// Bound by memory: 32768 x 1600 binary16 69.9 us with the sums' join, 6.0 TB/s; 26
+// Bound by memory: 32768 x 1600 binary16 68.2 us with the sums' join, 6.2 TB/s; 26
 // instructions a value in 58 % of the cycles.  Weights read for every batch: 80.6;
 // as packed pairs of binary32 operations no less (70.9); two rows a batch instead of
 // four 85, one 107.
@@ -497,8 +497,8 @@ __global__ void __launch_bounds__(T, BLOCKS) k_rms_backward_rows(const __grid_co
 // are distances from one address), each with blocks of 128 neighbouring values, four
 // of a block to a lane, 32 apart: neighbouring lanes neighbouring values, and a
 // block's largest magnitude stays inside the warp.  Bound by the accesses, 4 a value,
-// and the instructions around them: 8192 x 4095 bfloat16 66 us, into 8 bits 71,
-// backward 88, 2048 x 16383 98 (with the warps' number unknown to the compiler 114, 196 and 188).
+// and the instructions around them: 8192 x 4095 bfloat16 65 us, into 8 bits 70,
+// backward 86, 2048 x 16383 96 (with the warps' number unknown to the compiler 114, 196 and 188).
 // 16-bit rows on 4-byte boundaries gain nothing by copies of two values (8192 x
 // 4094: 68 and 92 us, here 66 and 86).
 template <int W>
@@ -718,7 +718,7 @@ __global__ void __launch_bounds__(T, kAnyResident / T) k_rms_backward_any(const 
 // More than a block's registers hold (over 4096 vectors, or 16384 values off their
 // boundaries; backward 2048 and 16384): a block per row, values read again for every
 // use (from cache), bound by the latency of one access a value: 512 x 40000 bfloat16
-// 55 us forward, backward 120, 43 of them for the weight (with one value of a thread
+// 53 us forward, backward 114, 42 of them for the weight (with one value of a thread
 // on its way at a time 70 and 162).  Warps take blocks of 128 values in turn, K / 4
 // of them before any use, so a thread reads of h what it wrote.  K = 8 for few rows
 // (200 x 200000 132 us forward, 205 with 4), 4 for many (8192 x 16385 261 and
@@ -871,7 +871,7 @@ __global__ void __launch_bounds__(kRowThreads) k_rms_dw_part(const __grid_consta
 
 // The blocks' partial sums: 32 columns a block, its 32 warps a part of the
 // partial sums each, joined in warp order.  Bound by its own latency, 4.4 us of the
-// 69.9 above.
+// 68.2 above.
 template <int DT>
 __global__ void __launch_bounds__(1024) k_rms_dw_sum(const float* part, int blocks, int64_t dim, void* dw)
 {
@@ -895,9 +895,9 @@ __global__ void __launch_bounds__(1024) k_rms_dw_sum(const float* part, int bloc
 // ---- read-out --------------------------------------------------------------------------
 // 8-bit results as bfloat16 values.  Rows that start and end on 16 codes: 16 to a
 // thread at once; blockDim.x threads along a row, blockDim.y rows, and each thread
-// kValuesRows of them, all read before any is written.  8192 x 4096: 20.8 us, 4.9
+// kValuesRows of them, all read before any is written.  8192 x 4096: 19.4 us, 5.2
 // TB/s, a third of the issue slots used; more warps an SM with fewer loads each on
-// their way were slower (24.9 with 48 of them).  Other rows 46 us.
+// their way were slower (24.9 with 48 of them).  Other rows 44 us.
 constexpr int kValuesRows = 4;
 
 // Other rows: a warp 256 values of one, a code a lane at a time.
@@ -1311,7 +1311,7 @@ zero_status_t zero_rms_values(const zero_rms_plan_t* plan, const void* q, const 
     cudaError_t err;
     const bool wide = aligned_to(q, 16) && aligned_to(values, 16) && plan->y_stride % 16 == 0 && plan->dim % 16 == 0;
     if (wide) {
-        unsigned along = 32;
+        unsigned along = 1;                           // short rows share a warp
         while (along < 256 && along < plan->dim / 16) along *= 2;
         const int64_t high = (plan->rows + 256 / along * kValuesRows - 1) / (256 / along * kValuesRows);
         const dim3 block(along, 256 / along);
