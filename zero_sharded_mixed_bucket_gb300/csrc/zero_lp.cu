@@ -37,11 +37,12 @@ struct LpArgs {
     int64_t* top_index;
 };
 
-// The head cleared, before a forward pass.
+// The head cleared, before a forward pass.  The caller's kernels have ended before the
+// next may start: a product takes its tensor memory before it waits.
 __global__ void k_lp_clear(CeHead* head)
 {
-    allow_next_grid();
     wait_prev_grid();
+    allow_next_grid();
     head->err = 0;
     head->joined = 0;
 }
@@ -578,8 +579,8 @@ __global__ void __launch_bounds__(1024) k_lp_factors(CeHead* head, const int64_t
                                                      const float* dlogp, const float* dentropy, float scale, float up,
                                                      float* coef, float* coef_h)
 {
-    allow_next_grid();
     wait_prev_grid();
+    allow_next_grid();                                // as in k_lp_clear
     __shared__ float sm[32];
     auto factor = [&](int64_t i, float& b) {
         const int64_t t = targets[i];
