@@ -287,6 +287,32 @@ def test_logits_of_the_lowest_value(n):
     assert (j.logp < -3e38).all()
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+def test_gradients_lose_no_more_than_G_rounded_once(dtype):
+    """G scaled and rounded to the operands' type, all else in 64 bits: the kernels are next to that.
+
+    What is left is binary32's: a G_iv is relatively off by some 2^-18 (a logit's sum, exp2), so about one in 2^-18 / (2 u) of them, and
+    of the results, falls on the other side of a border and is a whole step 2 u off: sqrt(2^-18 * 2 u) of the norm, 1.7e-4 in bfloat16
+    and 6.1e-5 in binary16, under a quarter of what the two roundings (some u / 2 each) take."""
+    n, v, d = 300, 5000, 256
+    j = Job(n, v, d, dtype, scale=1.25)
+    dl, de = torch.randn(n, device="cuda", generator=j.g) / n, torch.full((n,), 0.01 / n, device="cuda")
+    j.forward()
+    j.backward(dl, de, 1024.0)
+    j.define()
+    a = torch.where(j.counted, dl.double() * 1024 * j.s32, 0.0)[:, None]
+    b = de.double()[:, None] * 1024 * j.s32
+    onehot = torch.zeros_like(j.z).scatter_(1, j.at, 1.0) * j.counted[:, None]
+    G = a * (onehot - j.p) - b * j.p * (j.lp + j.want_ent[:, None])
+    unit = float((a.abs() + 4 * b.abs()).max()) / (2.0 ** 14 if dtype == "fp16" else 1.0)
+    R = (G / unit).float().to(j.dt).double() * unit
+    for got, exact, near in ((j.dx, G @ j.w.double(), R @ j.w.double()), (j.dw, G.t() @ j.x.double(), R.t() @ j.x.double())):
+        near = near.to(j.dt).double()
+        lost = (near - exact).norm()
+        assert (got.double() - near).norm() <= lost / 4
+        assert lost <= 1.5 * j.u * exact.norm()       # two roundings, half a step each at most: u each
+
+
 def test_tokens_without_a_target_and_factors_of_zero():
     j = Job(300, 700, 64, "bf16", ignore=1.0)
     j.t.fill_(-100)
