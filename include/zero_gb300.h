@@ -846,10 +846,11 @@ zero_status_t zero_adamw_step(const zero_adamw_plan_t* plan, const void* table, 
                               const uint32_t* skip, void* stream);
 /* The global norm of the list's gradients, norm = |grad_scale| sqrt(sum g^2),
  * and the factor that clips them, as in the sharded step: min(1, max_norm /
- * (norm + 1e-6)), 1 where max_norm <= 0.  norm: device memory, {norm, factor}.
+ * (norm + 1e-6)); where max_norm <= 0 or infinite nothing is clipped and the
+ * factor is 1, whatever the norm.  norm: device memory, {norm, factor}.
  * flag (may be NULL): what zero_adamw_check gives, in the same pass.  An infinite
- * gradient makes norm +inf and the factor 0, a NaN both NaN: pass flag to the
- * step.  Squares are summed in binary32 32 (binary32 gradients: 16) at a time,
+ * gradient makes norm +inf and a factor that clips 0, a NaN makes both NaN (with
+ * grad_scale 0 either does): pass flag to the step.  Squares are summed in binary32 32 (binary32 gradients: 16) at a time,
  * those sums in binary64; where binary32 overflows or underflows, all in
  * binary64.  Equal lists give equal bits.  workspace: zero_adamw_norm_workspace
  * bytes of device memory, 16-byte aligned, contents scratch.  Asynchronous.

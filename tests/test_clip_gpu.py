@@ -95,6 +95,24 @@ def test_norm_of_gradients_that_are_not_finite(bad, shift, dtype):
         assert N.of(T, 1.0, 1.0)[2] == 0
 
 
+@pytest.mark.parametrize("n", [9001, 500_001])        # one block alone, and two kernels
+@pytest.mark.parametrize("most", [0.0, -1.0, float("inf"), float("-inf")])
+def test_no_clipping_whatever_the_gradients(most, n):
+    """A max_norm <= 0 or infinite: the factor is 1, also of gradients that are not finite; norm and flag say what they are."""
+    T = _filled("fp32", n)
+    N = Norm(T.plan)
+    for bad in (None, float("inf"), float("-inf"), float("nan")):
+        if bad is not None:
+            T.view[3]["grad"][4097] = bad
+        norm, factor, flag = N.of(T, 1.0, most)
+        assert factor == 1.0 and flag == (bad is not None)
+        assert np.isnan(norm) if bad != bad else norm == np.inf if bad else np.isfinite(norm)
+        norm, factor, flag = N.of(T, 0.0, most)       # 0 times an infinity is NaN, as the formula has it
+        assert factor == 1.0 and flag == (bad is not None) and (np.isnan(norm) if bad else norm == 0)
+    norm, factor, flag = N.of(T, 0.0, 1.0)
+    assert np.isnan(norm) and np.isnan(factor) and flag == 1
+
+
 def test_norm_of_zeros():
     T = _filled("bf16", 9001)
     for k in (0, 1, 3):

@@ -891,7 +891,7 @@ zero_status_t zero_adamw_norm(const zero_adamw_plan_t* plan, const void* table, 
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const AdTable tab = table_of(table, plan->n_tensors);
     const NormOut o{static_cast<NormPart*>(workspace), norm, flag, std::fabs((double)grad_scale),
-                    max_norm > 0.0f ? (double)max_norm : 0.0};
+                    max_norm > 0.0f && std::isfinite(max_norm) ? (double)max_norm : 0.0};
     const unsigned grid = (unsigned)norm_blocks(*plan);
     cudaError_t err = plan->dtype == ZERO_FP32   ? launch_norm<kF32>(tab, plan->n_chunks, o, grid, s)
                       : plan->dtype == ZERO_BF16 ? launch_norm<kBF16>(tab, plan->n_chunks, o, grid, s)
