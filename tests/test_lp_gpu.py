@@ -418,6 +418,27 @@ def test_bounded_wait_is_reported(top, n, v):
     assert j.dx.isnan().all() and j.dw.isnan().all()
 
 
+def test_status_of_a_backward_pass_without_outputs():
+    """Nothing is computed, so nothing has run out: neither a workspace of any contents nor an earlier call's error is reported."""
+    j = Job(130, 600, 64, "bf16")
+    one = torch.ones(130, device="cuda")
+    none = lambda: zg.zero_lp_backward(j.plan, j.x, j.w, j.t, 1.0, j.lse, j.ent, one, one, 1.0, None, None, j.ws,  # noqa: E731
+                                       torch.cuda.current_stream())
+    none()                                            # the workspace is 0xFF everywhere
+    zg.zero_lp_status(j.plan, j.ws)
+    os.environ["ZERO_TEST_WITHHOLD_TILE"] = "1"
+    try:
+        j.forward()
+    finally:
+        del os.environ["ZERO_TEST_WITHHOLD_TILE"]
+    with pytest.raises(zg.ZeroError):
+        zg.zero_lp_status(j.plan, j.ws)
+    none()
+    zg.zero_lp_status(j.plan, j.ws)
+    j.forward()
+    j.check_forward()
+
+
 @pytest.mark.parametrize("n", [2, 70])
 def test_offsets_past_32_bits(n):
     """A weight whose rows lie past 2^32 values."""
