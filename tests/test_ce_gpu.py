@@ -497,6 +497,25 @@ def test_bounded_wait_of_the_gradients_is_seen(hook, n, v, d, with_dx):
     assert j.dx.isfinite().all() and j.dw.isfinite().all()
 
 
+def test_status_of_a_backward_pass_without_outputs():
+    """Nothing is computed, so nothing has run out: neither a workspace of any contents nor an earlier call's error is reported."""
+    j = Job(130, 600, 64, "bf16")
+    none = lambda: zg.zero_ce_backward(j.plan, j.x, j.w, j.t, j.lse, None, 1.0, None, None, j.ws, torch.cuda.current_stream())  # noqa: E731
+    none()                                            # the workspace is 0xFF everywhere
+    zg.zero_ce_status(j.plan, j.ws)
+    os.environ["ZERO_TEST_WITHHOLD_TILE"] = "1"
+    try:
+        j.forward()
+    finally:
+        del os.environ["ZERO_TEST_WITHHOLD_TILE"]
+    with pytest.raises(zg.ZeroError):
+        zg.zero_ce_status(j.plan, j.ws)
+    none()
+    zg.zero_ce_status(j.plan, j.ws)
+    j.forward()
+    j.check_forward()
+
+
 @pytest.mark.parametrize("dtype", list(DT))
 def test_tiny_upstream_gradients_against_the_definition(dtype):
     """dloss far below 1, as it is (bfloat16) and scaled up (binary16)."""

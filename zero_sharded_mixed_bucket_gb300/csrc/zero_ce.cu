@@ -538,13 +538,12 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
         !aligned_to(workspace, 16) || !aligned_to(targets, 8) || !aligned_to(lse, 4) || !aligned_to(dloss, 4))
         return set_error(ZERO_EALIGN, "zero_ce_backward: x, w, dx, dw and workspace must be 16-byte aligned, the others to their type");
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (!p.tokens) {
+    if (!p.tokens || (!dx && !dw)) {                  // no products; the workspace has no error of this call
         if (dw) k_ce_zero<<<1024, 256, 0, s>>>(static_cast<uint16_t*>(dw), p.vocab, p.hidden, p.w_stride);
         cudaError_t e = cudaGetLastError();
         if (e == cudaSuccess) e = cudaMemsetAsync(workspace, 0, sizeof(CeHead), s);
         return e == cudaSuccess ? ZERO_OK : cuda_failed(e, "zero_ce_backward");
     }
-    if (!dx && !dw) return ZERO_OK;
     if (!encode_fn()) return set_error(ZERO_ECUDA, "zero_ce_backward: the driver has no cuTensorMapEncodeTiled");
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     const CeLayout l = layout_of(p);
