@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import zero_sharded_mixed_bucket_gb300 as zg
+from tests.launches import launches
 
 pytestmark = pytest.mark.gpu
 
@@ -119,6 +120,28 @@ def test_forward_and_backward(n, d, pad, shift, dtype):
     plain64 = rstd * (gw - xhat * m)
     tol = plain64.abs() * _half(dt) * 1.001 + _least(dt) + U * (rstd * (8 * gw.abs() + xhat.abs() * (_chain(d) + 8) * mag) + 2 * plain64.abs())
     assert bool(((plain.v.double() - plain64).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("n,d", [(1, 8196), (5, 8193), (160, 9001), (3, 12288), (310, 10_000), (320, 16384)])
+def test_long_binary32_rows_backward_wherever_they_start(n, d):
+    """Rows of 8193 to 16384 values on 16-byte boundaries take the kernel that the same rows off them take: one pass and a join, equal bits."""
+    stride = (d + 3) // 4 * 4
+    p = zg.zero_rms_plan(n, d, zg.ZERO_FP32, stride, stride)
+    g = torch.Generator(device="cuda").manual_seed(d)
+    value = [torch.randn(n, d, device="cuda", generator=g) for _ in range(3)]
+    w, rstd = torch.randn(d, device="cuda", generator=g), torch.rand(n, device="cuda", generator=g) + 0.5
+    ws = torch.empty(p.workspace_bytes, dtype=torch.uint8, device="cuda")
+    out = []
+    for shift in (0, 1):
+        h, dy, dh = (Rows(n, d, stride, shift, torch.float32, v) for v in value)
+        dx, dw = Rows(n, d, stride, shift, torch.float32), torch.full((d,), GUARD, device="cuda")
+        assert (h.v.data_ptr() % 16 == 0) == (shift == 0)
+        call = lambda s: zg.zero_rms_backward(p, dy.v, dh.v, h.v, w, rstd, dx.v, dw, ws, s)  # noqa: E731
+        assert launches(call) == 2
+        call(torch.cuda.current_stream())
+        assert dx.kept()
+        out.append((dx.v.clone(), dw))
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
 
 
 def _codes(y64, block):

@@ -716,7 +716,7 @@ __global__ void __launch_bounds__(T, kAnyResident / T) k_rms_backward_any(const 
 
 // ---- long rows -------------------------------------------------------------------------
 // More than a block's registers hold (over 4096 vectors, or 16384 values off their
-// boundaries; backward 2048 and 16384): a block per row, values read again for every
+// boundaries; backward over 16384 values): a block per row, values read again for every
 // use (from cache), bound by the latency of one access a value: 512 x 40000 bfloat16
 // 53 us forward, backward 114, 42 of them for the weight (with one value of a thread
 // on its way at a time 70 and 162).  Warps take blocks of 128 values in turn, K / 4
@@ -1135,7 +1135,11 @@ int64_t backward_blocks(int64_t rows, int64_t vecs, int L)
 // its blocks, and the blocks: as many as are resident, and no more than have rows.
 // (Two rows of a group at a time, with half of the warps: 8192 x 4095 123 us for 86;
 // short rows are two at a time, 65536 x 67 24 us for 32.  2048 x 16383 98 us, as a
-// long row's kernels 191.)
+// long row's kernels 191.  Binary32 rows of 8193 to 16384 values on 16-byte
+// boundaries: 2048 x 8196 70, 12288 85 and 16384 109 us, as a long row's kernels 97,
+// 133 and 187, 64 x 12288 10 and 13.  The long rows' is ahead only where dx alone is
+// asked for of many rows below some 10000 values, 8192 x 8196 203 us for 246; that the
+// two calls' dx have the same bits counts more.)
 constexpr int64_t kAnyBackward = 16384;
 constexpr int64_t any_warps(int64_t dim) { return dim <= 256 ? 1 : dim <= 512 ? 2 : dim <= 1024 ? 4 : dim <= 2048 ? 8 : dim <= 4096 ? 16 : 32; }
 constexpr int64_t any_threads(int64_t W) { return W <= 8 ? 256 : 32 * W; }
@@ -1179,7 +1183,7 @@ cudaError_t backward(RmsArgs a, bool aligned, int64_t most, void* dw, cudaStream
         else if (vecs <= 512) e = backward_rows<DT, 32, 1, 4, 2 * T, 1>(a, vecs, blocks, s);
         else if (vecs <= 1024) e = backward_rows<DT, 32, 2, 2, 2 * T, 1>(a, vecs, blocks, s);
         else e = backward_rows<DT, 32, 4, 1, 2 * T, 1>(a, vecs, blocks, s);
-    } else if (a.rows && !aligned && a.dim <= kAnyBackward) {
+    } else if (a.rows && a.dim <= kAnyBackward) {     // binary32 on 16-byte boundaries above 8192 values too
         if (a.dim <= 128) e = backward_any<DT, 4, 1, 2>(a, blocks, s);
         else if (a.dim <= 256) e = backward_any<DT, 8, 1>(a, blocks, s);
         else if (a.dim <= 512) e = backward_any<DT, 8, 2>(a, blocks, s);
