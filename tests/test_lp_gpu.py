@@ -12,6 +12,7 @@ import pytest
 import torch
 
 import zero_sharded_mixed_bucket_gb300 as zg
+from tests.launches import launches
 from tests.test_ce_gpu import DT, GUARD, _e, _guards_kept, _rows
 
 pytestmark = pytest.mark.gpu
@@ -179,6 +180,36 @@ def test_alternatives_of_sorted_logits(n, what):
     assert torch.equal(j.ti, _order(j))
     j.define()
     assert ((j.lse.double() - j.want_lse).abs() <= j.elog).all() and ((j.ent.double() - j.want_ent).abs() <= j.eent).all()
+
+
+@pytest.mark.parametrize("n,v,d,top,sample", [
+    (800, 50257, 16, 8, False), (1400, 50257, 16, 8, True), (1300, 50257, 16, 16, False), (1400, 50257, 16, 16, True),
+    (1600, 50257, 16, 20, False), (2048, 50257, 16, 20, True), (2048, 50257, 16, 32, False), (2670, 50257, 16, 32, False),
+    (2700, 50257, 16, 32, True), (2048, 50257, 1024, 1, False), (4000, 50257, 1024, 8, False), (4100, 50257, 1024, 8, True),
+    (20_000, 10_240, 16, 8, False), (20_000, 10_241, 16, 8, True), (2, 50257, 16, 8, None)])
+def test_which_logits_are_kept(n, v, d, top, sample):
+    """All, up to a number of them that goes by the alternatives and the hidden size, or a sample's: two kernels more."""
+    j = Job(n, v, d, "bf16", top=top)
+    assert launches(j.forward) == (2 if sample is None else 6 if sample else 4)
+    assert n * v <= 1 << 29                           # one pass over the rows
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("n,v,top", [(1700, 50257, 20), (2800, 50001, 32)])
+def test_order_of_alternatives_by_sample(n, v, top, dtype):
+    """The order of a stable sort, ties included, where only a sample's logits are kept."""
+    j = Job(n, v, 48, dtype, top=top, grid=True, scale=1.25)
+    j.w[v // 2:v // 2 + 300] = j.w[:300]
+    j.w[5:7] = j.w[3:5]
+    assert launches(j.forward) == 6
+    j.forward()
+    assert torch.equal(j.ti, _order(j))
+
+
+@pytest.mark.parametrize("what", ["rising", "falling", "equal", "rising in strips"])
+def test_alternatives_of_sorted_logits_by_sample(what):
+    test_alternatives_of_sorted_logits(1800, what)
+    assert launches(Job(1800, 50_000, 16, "bf16", top=20).forward) == 6
 
 
 def test_gradients_against_differences():

@@ -634,15 +634,25 @@ zero_status_t cuda_failed(cudaError_t e, const char* what)
 
 int64_t strips_of(int64_t vocab) { return ceil_div(vocab, kBN) * 2; }
 
-// Whether all logits are kept in memory for the alternatives: up to 256 MB, or where
-// a sample would be most of them; else those of a sample, which gives every row a
-// bound, and of the strips that reach it.  Hidden 768, bfloat16, 8 and 32 alternatives:
-// 2048 rows of 50257 with all 173 and 189 us, with a sample of 8192 entries 152 and
-// 204 (4096: 152 and 247; 2048: 166 and 291; no alternatives: 103); 1023 rows 99 and
-// 114, with a sample of 4096 107 and 158; 8192 rows 520 and 680 (4096: 515 and 855).
-bool all_kept(int64_t tokens, int64_t vocab)
+// Whether all logits are kept in memory for the alternatives, or where a sample would
+// be most of them; else those of a sample, which gives every row a bound, and of the
+// strips that reach it.  Kept logits cost their writes; a sample costs a product and a
+// search of its own and, the more alternatives, the more strips that reach the bound.
+// us, bfloat16, kept / by sample:
+//   hidden 768:  700 x 50257 with 8 76 / 82;  1023 with 8 98 / 93, 16 101 / 102, 32 112 / 132;
+//     1400 with 8 131 / 123, 20 137 / 140, 32 145 / 164;  2048 with 8 171 / 150, 20 177 / 172,
+//     32 186 / 202;  2670 with 32 248 / 253;  4096 with 20 342 / 309, 32 362 / 362;
+//     4096 x 32000 with 16 227 / 211, 32 248 / 265;  1000 x 128000 with 8 222 / 177, 32 235 / 233
+//   hidden 1024: 1400 x 50257 with 1 126 / 131, 32 143 / 181;  4096 with 1 311 / 326, 32 357 / 417
+//   hidden 1600: 1023 with 20 139 / 153;  4096 with 1 468 / 468, 32 502 / 558;  8192 with 8 967 / 936
+//   hidden 4096: 2048 with 8 518 / 557;  2670 with 8 762 / 751, 32 731 / 785;  8192 with 8 2186 / 2149
+// So from 1024 hidden values on, where the writes hide behind the product, up to 3 x 2^26
+// logits; below it 2^22 logits for each alternative, ten at least.  (A sample of 4096
+// entries, 2048 x 768 with 32: 247, of 2048 entries 291.)
+bool all_kept(const zero_lp_plan_t& p)
 {
-    return vocab <= kSample + kSample / 4 || tokens * vocab <= (int64_t(1) << 26);
+    const int64_t most = p.hidden >= 1024 ? int64_t(3) << 26 : int64_t(p.top > 10 ? p.top : 10) << 22;
+    return p.vocab <= kSample + kSample / 4 || p.tokens * p.vocab <= most;
 }
 
 int64_t logit_stride(int64_t vocab) { return ceil_div(vocab, kStrip) * kStrip; }
@@ -851,7 +861,7 @@ zero_status_t zero_lp_forward(const zero_lp_plan_t* plan, const void* x, const v
         a.logits = reinterpret_cast<const float*>(ws + l.logits);
         a.logit_stride = logit_stride(p.vocab);
         a.cand = reinterpret_cast<uint64_t*>(ws + l.cand);
-        a.least = p.top && !all_kept(p.tokens, p.vocab) ? reinterpret_cast<float*>(ws + l.least) : nullptr;
+        a.least = p.top && !all_kept(p) ? reinterpret_cast<float*>(ws + l.least) : nullptr;
         a.top_logp = top_logp + r0 * p.top;
         a.top_index = top_index + r0 * p.top;
         if (few) {
