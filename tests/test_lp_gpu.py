@@ -489,3 +489,70 @@ def test_offsets_past_32_bits(n):
     dx = torch.empty_strided(j.dx.shape, j.dx.stride(), dtype=j.dt, device="cuda")
     zg.zero_lp_backward(p, j.x, w, j.t, 1.0, j.lse, j.ent, dl, dl, 1.0, dx, None, ws, torch.cuda.current_stream())
     assert torch.equal(dx, j.dx)
+
+
+@pytest.mark.parametrize("n,d", [(70, 64), (70, 61), (1100, 64)])
+def test_gradient_of_a_weight_past_32_bits(n, d):
+    """dw with rows past 2^32 values, by tiled copies, one by one (rows that do not end on 16 bytes) and summed over parts of the
+    tokens: the bits of the same rows side by side, and nothing beside them."""
+    v, stride = 300, 1 << 24
+    j = Job(n, v, d, "bf16")
+    w, dw = (torch.empty(v * stride, dtype=torch.bfloat16, device="cuda").view(v, stride) for _ in range(2))
+    w[:, :d].copy_(j.w)
+    dw[:, :d + 64].fill_(GUARD)
+    p = zg.zero_lp_plan(n, v, d, zg.ZERO_BF16, j.plan.x_stride, stride)
+    ws = torch.empty(p.workspace_bytes, dtype=torch.uint8, device="cuda")
+    dl = torch.randn(n, device="cuda", generator=j.g)
+    j.forward()
+    j.backward(dl, dl)
+    dx = torch.empty_strided(j.dx.shape, j.dx.stride(), dtype=j.dt, device="cuda")
+    zg.zero_lp_backward(p, j.x, w, j.t, 1.0, j.lse, j.ent, dl, dl, 1.0, dx, dw, ws, torch.cuda.current_stream())
+    assert torch.equal(dx, j.dx) and torch.equal(dw[:, :d], j.dw) and (dw[:, d:d + 64] == GUARD).all()
+    j.define()
+    j.check_backward(dl.double(), dl.double())
+    # no tokens, and a pass whose wait ran out
+    zg.zero_lp_backward(zg.zero_lp_plan(0, v, d, zg.ZERO_BF16, j.plan.x_stride, stride), None, None, None, 1.0, None, None, None, None, 1.0,
+                        None, dw, ws, torch.cuda.current_stream())
+    assert (dw[:, :d] == 0).all() and (dw[:, d:d + 64] == GUARD).all()
+    os.environ["ZERO_TEST_WITHHOLD_TILE"] = "1"
+    try:
+        zg.zero_lp_backward(p, j.x, w, j.t, 1.0, j.lse, j.ent, dl, dl, 1.0, None, dw, ws, torch.cuda.current_stream())
+    finally:
+        del os.environ["ZERO_TEST_WITHHOLD_TILE"]
+    with pytest.raises(zg.ZeroError):
+        zg.zero_lp_status(p, ws)
+    assert dw[:, :d].isnan().all() and (dw[:, d:d + 64] == GUARD).all()
+
+
+@pytest.mark.parametrize("n", [1, 3, 20, 600, 1400])
+def test_infinite_logits_are_the_first_alternatives(n):
+    """+infinity is a number: the lowest such indices come first, with NaN as their log probability; other rows' NaN are none."""
+    j = Job(n, 50257, 16, "bf16", top=5, grid=True, ignore=0.0)
+    j.x[:, 0] = 0
+    j.x[0, 0] = 1
+    j.w[100:103, 0] = float("inf")
+    j.w[40_000:40_200, 0] = float("inf")
+    j.forward()
+    assert j.ti[0].tolist() == [100, 101, 102, 40_000, 40_001] and j.tl[0].isnan().all()
+    assert j.logp[0].isnan() and j.lse[0].isnan() and j.ent[0].isnan()
+    if n > 1:                                         # 0 times infinity
+        rest = j.x[1:, 1:].double() @ j.w[:, 1:].double().t()
+        rest[:, 100:103] = rest[:, 40_000:40_200] = -float("inf")
+        assert torch.equal(j.ti[1:], torch.sort(rest, dim=1, descending=True, stable=True).indices[:, :5])
+
+
+@pytest.mark.parametrize("top,n,v", [(0, 300, 600), (3, 1400, 50257)])
+def test_results_after_a_wait_that_ran_out(top, n, v):
+    """NaN, but for what says nothing of the logits: logp of tokens without a target is 0, the alternatives' indices are -1."""
+    j = Job(n, v, 128, "bf16", top=top, ignore=0.4)
+    os.environ["ZERO_TEST_WITHHOLD_TILE"] = "1"
+    try:
+        j.forward()
+    finally:
+        del os.environ["ZERO_TEST_WITHHOLD_TILE"]
+    counted = (j.t >= 0) & (j.t < v)
+    assert 0 < int(counted.sum()) < n
+    assert j.logp[counted].isnan().all() and (j.logp[~counted] == 0).all()
+    assert j.lse.isnan().all() and j.ent.isnan().all() and (not top or (j.tl.isnan().all() and (j.ti == -1).all()))
+    with pytest.raises(zg.ZeroError):
+        zg.zero_lp_status(j.plan, j.ws)

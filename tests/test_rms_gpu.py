@@ -388,3 +388,61 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         results.append([t.clone() for s, _, out, _, _ in jobs for t in (s["y"].v, *out)])
     assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("d", [16, 31, 64, 120, 128, 136, 300, 771, 1024, 2040, 4096, 4100, 8192, 8200, 12_289, 16_384, 16_392, 33_000, 40_001])
+def test_same_bits_wherever_rows_start(d, dtype):
+    """Small multiples of powers of two, whose sums are exact in every order: rows on 16-byte boundaries, and the same rows off them, come out
+    with equal bits.  Squares: multiples of 1/4 up to 16, 40001 of them below 2^24 / 4; dy w xhat: multiples of 1/8 up to 3/2."""
+    n, stride = 37, (d + 15) // 16 * 16
+    code, dt = DT[dtype]
+    g = torch.Generator(device="cuda").manual_seed(d)
+    k = lambda lo, hi, unit, *size: (torch.randint(lo, hi + 1, size, device="cuda", generator=g) * unit).to(dt)  # noqa: E731
+    x, r, dy, dh, w = k(-4, 4, 0.5, n, d), k(-4, 4, 0.5, n, d), k(-1, 1, 1.0, n, d), k(-8, 8, 0.25, n, d), k(1, 3, 0.5, d)
+    given = torch.exp2(torch.randint(-1, 1, (n,), device="cuda", generator=g).float())
+    out = []
+    for shift in (0, 1):
+        p = zg.zero_rms_plan(n, d, code, stride, stride, 32)
+        a, b, gy, gh = (Rows(n, d, stride, shift, dt, v) for v in (x, r, dy, dh))
+        h, y, dx, plain = (Rows(n, d, stride, shift, dt) for _ in range(4))
+        q, vals = Rows(n, d, stride, shift, torch.uint8, guard=0xA5), Rows(n, d, stride, shift, torch.bfloat16)
+        sc = torch.empty(n, p.scale_cols, dtype=torch.uint8, device="cuda")
+        rstd, dw = torch.empty(n, device="cuda"), torch.empty(d, dtype=dt, device="cuda")
+        ws = torch.empty(p.workspace_bytes, dtype=torch.uint8, device="cuda")
+        assert (a.v.data_ptr() % 16 == 0) == (shift == 0)
+        zg.zero_rms_forward(p, a.v, b.v, w, EPS, h.v, y.v, q.v, sc, rstd)
+        zg.zero_rms_values(p, q.v, sc, vals.v)
+        zg.zero_rms_backward(p, gy.v, gh.v, h.v, w, given, dx.v, dw, ws)
+        zg.zero_rms_backward(p, gy.v, None, h.v, w, given, plain.v, None, None)
+        assert all(t.kept() for t in (h, y, q, vals, dx, plain))
+        out.append([t.v.clone() for t in (h, y, q, vals, dx, plain)] + [sc, rstd, dw])
+    for name, a, b in zip(("h", "y", "q", "values", "dx", "dx without dh", "scales", "rstd", "dw"), *out):
+        assert torch.equal(a, b), name
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("odd", [0, 1])
+@pytest.mark.parametrize("d", [1000, 9000, 20_000])
+def test_gradients_of_rows_past_32_bits(d, odd, dtype):
+    """h, dy, dh and dx with rows 2^31 values apart: dx and dw have the bits of the same rows side by side."""
+    code, dt = DT[dtype]
+    far, near = (1 << 31) + (16 if dtype == "bf16" else 4) + odd, (d + 15) // 16 * 16 + odd
+    g = torch.Generator(device="cuda").manual_seed(d)
+    value = [torch.randn(3, d, device="cuda", generator=g).to(dt) for _ in range(3)]
+    w, rstd = torch.randn(d, device="cuda", generator=g).to(dt), torch.rand(3, device="cuda", generator=g) + 0.5
+    out = []
+    for stride in (near, far):
+        p = zg.zero_rms_plan(3, d, code, stride, stride)
+        h, dy, dx = (torch.empty(2 * stride + d, dtype=dt, device="cuda").as_strided((3, d), (stride, 1)) for _ in range(3))
+        h.copy_(value[0])
+        dy.copy_(value[1])
+        dx.copy_(value[2])                            # dh is written over
+        dw = torch.empty(d, dtype=dt, device="cuda")
+        zg.zero_rms_backward(p, dy, dx, h, w, rstd, dx, dw, torch.empty(p.workspace_bytes, dtype=torch.uint8, device="cuda"))
+        out.append((dx.clone(memory_format=torch.contiguous_format), dw))
+        del h, dy, dx
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+    dw64 = (value[1].double() * value[0].double() * rstd.double()[:, None]).sum(0)
+    mag = (value[1].double() * value[0].double() * rstd.double()[:, None]).abs().sum(0)
+    assert bool(((out[1][1].double() - dw64).abs() <= dw64.abs() * _half(dt) * 1.001 + U * mag * 70).all())
