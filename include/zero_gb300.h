@@ -578,7 +578,8 @@ zero_status_t zero_ln_backward(const zero_ln_plan_t* plan, const void* dy, const
  * have the plan's dtype; rstd is binary32, one per row.  Sums are binary32 in
  * an order fixed by the plan and the pointers' alignment; each output is rounded
  * once.  Squares are summed as they are: a row with values over 2^63 or so in
- * bfloat16 or binary32 has an infinite sum, and y 0.
+ * bfloat16 or binary32 has an infinite sum, and y 0; with eps 0 one whose values are
+ * all under 2^-75 or so has a sum of 0, and y as h * infinity.
  * y may also be (or be as well) q, one byte per value with a scale byte for every
  * `block` (32 or 128) values of a row, the last block of a row maybe shorter:
  *   q = e4m3 (1 sign, 4 exponent, 3 fraction bits, 448 the largest) of
@@ -589,8 +590,10 @@ zero_status_t zero_ln_backward(const zero_ln_plan_t* plan, const void* dy, const
  * residual, h, dh and dx; y_stride: of y, dy, q and values); what is between them is
  * neither read nor written.  q_scale rows are scale_cols bytes apart.  Pointers need
  * the alignment of their type only: rows that all start on 16-byte boundaries (the
- * weight too) take 16-byte accesses, others single-value ones (1.4 to 1.7 times
- * slower).  Outputs must not overlap inputs, but h may be x or residual itself and
+ * weight too) take 16-byte accesses, up to 65536 bytes a row forward and 32768 backward;
+ * others single-value ones, up to 2.2 times slower.  zero_rms_values takes 16 codes at
+ * once where q, values and their rows start on 16 bytes and dim is a multiple of 16,
+ * else one (up to 3 times slower).  Outputs must not overlap inputs, but h may be x or residual itself and
  * dx may be dh itself.  88 bytes. */
 typedef struct zero_rms_plan {
     int64_t rows, dim;
@@ -688,14 +691,15 @@ zero_status_t zero_ce_backward(const zero_ce_plan_t* plan, const void* x, const 
                                const float* lse, const float* dloss, float grad_scale, void* dx, void* dw,
                                void* workspace, void* stream);
 /* Synchronises `stream`; ZERO_ETIMEOUT if a bounded wait inside the last
- * forward or backward call with this workspace ran out.  Losses, dx and dw
- * are then NaN, so zero_adamw_check sees them too. */
+ * forward or backward call with this workspace ran out (a call that computes
+ * nothing has none).  Losses of tokens that have one, dx and dw are then NaN, so
+ * zero_adamw_check sees them too. */
 zero_status_t zero_ce_status(const zero_ce_plan_t* plan, const void* workspace, void* stream);
 
 /* ---- log probabilities over a large vocabulary ---------------------------------
  * What a policy's update and a scored answer need of the last hidden states x
  * [tokens, hidden] against a weight w [vocab, hidden], without the logits in
- * memory (the products are cross entropy's):
+ * memory unless alternatives are asked for (the products are cross entropy's):
  *   z = x w^T * scale (scale: the inverse temperature);  lse_i = log sum_v exp z_iv
  *   logp_i = z_i,t(i) - lse_i;  p = exp(z - lse);  entropy_i = -sum_v p_iv log p_iv
  *   the `top` most likely entries, in falling order of their logits, the lower
@@ -712,8 +716,9 @@ zero_status_t zero_ce_status(const zero_ce_plan_t* plan, const void* workspace, 
  * logits as computed: those closer than their binary32 sums' rounding may
  * change places.  A row with a logit that is NaN or +infinity, or with none above
  * -infinity, has NaN logp and entropy; a -infinity beside others adds nothing to
- * either.  With alternatives the workspace holds logits of `rows` tokens at a time
- * while they are sought (binary32, 2 GiB at most unless 256 rows need more).
+ * either.  With alternatives the workspace has room for the logits of `rows` tokens
+ * at a time while they are sought (binary32, 2 GiB at most unless 256 rows need more),
+ * of which large batches write a part only.
  * Results do not depend on timing: equal calls give equal bits.  104 bytes. */
 typedef struct zero_lp_plan {
     int64_t tokens, vocab, hidden;
@@ -749,7 +754,8 @@ zero_status_t zero_lp_backward(const zero_lp_plan_t* plan, const void* x, const 
                                const float* lse, const float* entropy, const float* dlogp, const float* dentropy,
                                float grad_scale, void* dx, void* dw, void* workspace, void* stream);
 /* As zero_ce_status; after ZERO_ETIMEOUT the forward pass' results and the
- * gradients are NaN. */
+ * gradients are NaN, but logp of tokens without a target, which is 0, and
+ * top_index, which is -1. */
 zero_status_t zero_lp_status(const zero_lp_plan_t* plan, const void* workspace, void* stream);
 
 /* ---- AdamW over a list of tensors -------------------------------------------
