@@ -571,6 +571,101 @@ static __global__ void __launch_bounds__(256) k_ce_zero(uint16_t* p, int64_t row
         p[e / cols * stride + e % cols] = 0;
 }
 
+// Logits of up to kFewTokens tokens, by multiply-adds: the tokens lie in shared memory
+// (xs: T rows of hidden, rounded up to 8), a warp takes a row of w at a time (3
+// tokens: two, which share the unpacked tokens), neighbouring warps neighbouring rows,
+// U 16-byte loads of a lane on their way.  each(v, z): the tokens' logits of entry v, in all
+// lanes, entry after entry of the warp's; target_logit [T]: those of the targets.
+template <int DT, int T, typename EACH>
+__device__ __forceinline__ void few_logits(const uint16_t* x, int64_t x_stride, const uint16_t* w, int64_t w_stride,
+                                           int64_t hidden, int64_t vocab, const int64_t* targets, uint16_t* xs,
+                                           float* target_logit, EACH each)
+{
+    constexpr int R = T <= 2 ? 1 : 2, U = 8 / R;      // rows at a time, loads in flight per row
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wide = (int)((hidden + 7) / 8 * 8);
+#pragma unroll
+    for (int t = 0; t < T; t++)
+        for (int j = threadIdx.x * 8; j < wide; j += kFewThreads * 8) {
+            const uint16_t* p = x + t * x_stride + j;
+            if (j + 8 <= hidden) {
+                *reinterpret_cast<uint4*>(xs + t * wide + j) = *reinterpret_cast<const uint4*>(p);
+            } else {
+                for (int k = 0; k < 8; k++)
+                    xs[t * wide + j + k] = j + k < hidden ? p[k] : (uint16_t)0;
+            }
+        }
+    __syncthreads();
+    const int64_t warps = (int64_t)gridDim.x * (kFewThreads / 32), me = (int64_t)blockIdx.x * (kFewThreads / 32) + warp;
+    for (int64_t v = me * R; v < vocab; v += warps * R) {
+        const uint16_t* row[R];
+        float acc[R][T];
+#pragma unroll
+        for (int q = 0; q < R; q++) {
+            row[q] = w + min(v + q, vocab - 1) * w_stride;
+#pragma unroll
+            for (int t = 0; t < T; t++)
+                acc[q][t] = 0.0f;
+        }
+        auto add = [&](const uint4 r[R], int j) {
+            float wv[R][8];
+#pragma unroll
+            for (int q = 0; q < R; q++)
+                unpack8<DT>(r[q], wv[q]);
+#pragma unroll
+            for (int t = 0; t < T; t++) {
+                float xv[8];
+                unpack8<DT>(*reinterpret_cast<const uint4*>(xs + t * wide + j), xv);
+#pragma unroll
+                for (int q = 0; q < R; q++)
+#pragma unroll
+                    for (int k = 0; k < 8; k++)
+                        acc[q][t] = fmaf(wv[q][k], xv[k], acc[q][t]);
+            }
+        };
+        int j = lane * 8;
+        for (; j + 8 <= hidden; j += 256 * U) {
+            uint4 r[U][R];                            // all loads before any use; 0 past the row's end
+#pragma unroll
+            for (int u = 0; u < U; u++)
+#pragma unroll
+                for (int q = 0; q < R; q++)
+                    r[u][q] = j + 256 * u + 8 <= hidden ? __ldcs(reinterpret_cast<const uint4*>(row[q] + j + 256 * u))
+                                                        : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int u = 0; u < U; u++)
+                if (j + 256 * u + 8 <= hidden) add(r[u], j + 256 * u);
+        }
+        if (lane == (hidden / 8) % 32 && hidden % 8) {    // the rows' ragged end
+            const int e = (int)(hidden / 8 * 8);
+            uint4 r[R];
+#pragma unroll
+            for (int q = 0; q < R; q++) {
+                uint32_t u[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int k = 0; k < 8; k++)
+                    if (e + k < hidden) u[k >> 1] |= (uint32_t)row[q][e + k] << ((k & 1) * 16);
+                r[q] = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+            add(r, e);
+        }
+#pragma unroll
+        for (int q = 0; q < R; q++) {
+            if (v + q >= vocab) break;
+            float z[T];
+#pragma unroll
+            for (int t = 0; t < T; t++) {
+                z[t] = acc[q][t];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    z[t] += __shfl_xor_sync(0xffffffffu, z[t], o);
+                if (lane == 0 && v + q == targets[t]) target_logit[t] = z[t];
+            }
+            each(v + q, z);
+        }
+    }
+}
+
 // ---- host -------------------------------------------------------------------------
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t up256(int64_t a) { return (a + 255) / 256 * 256; }

@@ -150,25 +150,11 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_ce_few(const uint16_t* x, in
                                                            int64_t w_stride, int64_t hidden, float2* part,
                                                            float* target_logit, const __grid_constant__ JoinArgs a)
 {
-    constexpr int R = T <= 2 ? 1 : 2, U = 8 / R;      // rows at a time, loads in flight per row
     wait_prev_grid();
     extern __shared__ __align__(16) uint16_t xs[];    // [T][wide]
     __shared__ float2 sh[kFewThreads / 32][T];
     __shared__ uint32_t last;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int wide = (int)((hidden + 7) / 8 * 8);
-#pragma unroll
-    for (int t = 0; t < T; t++)
-        for (int j = threadIdx.x * 8; j < wide; j += kFewThreads * 8) {
-            const uint16_t* p = x + t * x_stride + j;
-            if (j + 8 <= hidden) {
-                *reinterpret_cast<uint4*>(xs + t * wide + j) = *reinterpret_cast<const uint4*>(p);
-            } else {
-                for (int k = 0; k < 8; k++)
-                    xs[t * wide + j + k] = j + k < hidden ? p[k] : (uint16_t)0;
-            }
-        }
-    __syncthreads();
     float mx[T], sum[T], held[T];                     // held: the logit of row `lane` of the 32 under way
 #pragma unroll
     for (int t = 0; t < T; t++) {
@@ -193,78 +179,16 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_ce_few(const uint16_t* x, in
             held[t] = -INFINITY;
         }
     };
-    const int64_t warps = (int64_t)gridDim.x * (kFewThreads / 32), me = (int64_t)blockIdx.x * (kFewThreads / 32) + warp;
     int have = 0;
-    for (int64_t v = me * R; v < a.vocab; v += warps * R) {
-        const uint16_t* row[R];
-        float acc[R][T];
+    few_logits<DT, T>(x, x_stride, w, w_stride, hidden, a.vocab, a.targets, xs, target_logit, [&](int64_t, const float (&z)[T]) {
 #pragma unroll
-        for (int q = 0; q < R; q++) {
-            row[q] = w + min(v + q, a.vocab - 1) * w_stride;
-#pragma unroll
-            for (int t = 0; t < T; t++)
-                acc[q][t] = 0.0f;
+        for (int t = 0; t < T; t++)
+            if (lane == have) held[t] = z[t];
+        if (++have == 32) {
+            flush();
+            have = 0;
         }
-        auto add = [&](const uint4 r[R], int j) {
-            float wv[R][8];
-#pragma unroll
-            for (int q = 0; q < R; q++)
-                unpack8<DT>(r[q], wv[q]);
-#pragma unroll
-            for (int t = 0; t < T; t++) {
-                float xv[8];
-                unpack8<DT>(*reinterpret_cast<const uint4*>(xs + t * wide + j), xv);
-#pragma unroll
-                for (int q = 0; q < R; q++)
-#pragma unroll
-                    for (int k = 0; k < 8; k++)
-                        acc[q][t] = fmaf(wv[q][k], xv[k], acc[q][t]);
-            }
-        };
-        int j = lane * 8;
-        for (; j + 8 <= hidden; j += 256 * U) {
-            uint4 r[U][R];                            // all loads before any use; 0 past the row's end
-#pragma unroll
-            for (int u = 0; u < U; u++)
-#pragma unroll
-                for (int q = 0; q < R; q++)
-                    r[u][q] = j + 256 * u + 8 <= hidden ? __ldcs(reinterpret_cast<const uint4*>(row[q] + j + 256 * u))
-                                                        : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int u = 0; u < U; u++)
-                if (j + 256 * u + 8 <= hidden) add(r[u], j + 256 * u);
-        }
-        if (lane == (hidden / 8) % 32 && hidden % 8) {    // the rows' ragged end
-            const int e = (int)(hidden / 8 * 8);
-            uint4 r[R];
-#pragma unroll
-            for (int q = 0; q < R; q++) {
-                uint32_t u[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int k = 0; k < 8; k++)
-                    if (e + k < hidden) u[k >> 1] |= (uint32_t)row[q][e + k] << ((k & 1) * 16);
-                r[q] = make_uint4(u[0], u[1], u[2], u[3]);
-            }
-            add(r, e);
-        }
-#pragma unroll
-        for (int q = 0; q < R; q++) {
-            if (v + q >= a.vocab) break;
-#pragma unroll
-            for (int t = 0; t < T; t++) {
-                float z = acc[q][t];
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1)
-                    z += __shfl_xor_sync(0xffffffffu, z, o);
-                if (lane == have) held[t] = z;
-                if (lane == 0 && v + q == a.targets[t]) target_logit[t] = z;
-            }
-            if (++have == 32) {
-                flush();
-                have = 0;
-            }
-        }
-    }
+    });
     if (have) flush();
     if (lane == 0)
 #pragma unroll
