@@ -593,8 +593,8 @@ zero_status_t zero_ln_backward(const zero_ln_plan_t* plan, const void* dy, const
  * weight too) take 16-byte accesses, up to 65536 bytes a row forward and 32768 backward;
  * others single-value ones, up to 2.2 times slower.  zero_rms_values takes 16 codes at
  * once where q, values and their rows start on 16 bytes and dim is a multiple of 16,
- * else one (up to 3 times slower).  Outputs must not overlap inputs, but h may be x or residual itself and
- * dx may be dh itself.  88 bytes. */
+ * else one (up to 3 times slower).  Outputs must not overlap inputs, but h may be x or
+ * residual itself and dx may be dh itself.  88 bytes. */
 typedef struct zero_rms_plan {
     int64_t rows, dim;
     int64_t x_stride, y_stride;
@@ -855,11 +855,12 @@ zero_status_t zero_adamw_step(const zero_adamw_plan_t* plan, const void* table, 
  * (norm + 1e-6)); where max_norm <= 0 or infinite nothing is clipped and the
  * factor is 1, whatever the norm.  norm: device memory, {norm, factor}.
  * flag (may be NULL): what zero_adamw_check gives, in the same pass.  An infinite
- * gradient makes norm +inf and a factor that clips 0, a NaN makes both NaN (with
- * grad_scale 0 either does): pass flag to the step.  Squares are summed in binary32 32 (binary32 gradients: 16) at a time,
- * those sums in binary64; where binary32 overflows or underflows, all in
- * binary64.  Equal lists give equal bits.  workspace: zero_adamw_norm_workspace
- * bytes of device memory, 16-byte aligned, contents scratch.  Asynchronous.
+ * gradient makes norm +inf and the factor, where it clips, 0; a NaN makes both NaN
+ * (with grad_scale 0 either does): pass flag to the step.  Squares are summed in
+ * binary32 32 (binary32 gradients: 16) at a time, those sums in binary64; where
+ * binary32 overflows or underflows, all in binary64.  Equal lists give equal bits.
+ * workspace: zero_adamw_norm_workspace bytes of device memory, 16-byte aligned,
+ * contents scratch.  Asynchronous.
  * Errors: ZERO_EINVAL (grad_scale not finite, max_norm NaN), ZERO_ENOMEM,
  * ZERO_EALIGN, ZERO_ECUDA. */
 zero_status_t zero_adamw_norm(const zero_adamw_plan_t* plan, const void* table, float grad_scale, float max_norm,
